@@ -283,6 +283,175 @@ pkv_status pkv_rope_shift_k(void* k_pool, const int32_t* block_ids, const int32_
                             double rope_base, int32_t* err_flag, void* stream);
 
 /*
+ * Rotary positions of new tokens.
+ *
+ * rope_init — the angle table of a rotary embedding (host).  Channel pair j < rotary_dim / 2
+ * turns by pos * inv_j, inv_j = base^(-2j / rotary_dim) before scaling; channels from
+ * rotary_dim on are copied.  Pairs are (j, j + rotary_dim / 2), or (2j, 2j + 1) with
+ * interleaved != 0.  Scalings for contexts `factor` times the trained length:
+ *   PKV_ROPE_NONE    inv_j as it is (factor ignored)
+ *   PKV_ROPE_LINEAR  inv_j / factor
+ *   PKV_ROPE_NTK     base * factor^(r / (r - 2)) in place of base, r = rotary_dim
+ *   PKV_ROPE_PARTS   w inv_j + (1 - w) inv_j / factor, w = (turns - low) / (high - low) clamped
+ *                    to [0, 1], turns = original_len * inv_j / (2 pi): the turns that the pair
+ *                    makes over the trained length
+ *   PKV_ROPE_YARN    the same blend with w falling linearly with j, from 1 at pair
+ *                    floor(c(high)) to 0 at pair ceil(c(low)), c(t) = r ln(original_len /
+ *                    (2 pi t)) / (2 ln base), both clamped to [0, r - 1]; cos and sin are
+ *                    multiplied by 0.1 ln(factor) + 1
+ * amplitude > 0 replaces that multiplier (1 for the other scalings).
+ * The table holds turns per position as 64-bit fractions, so pos * inv_j modulo one turn is
+ * exact for every int32 position, also negative ones; it is plain data (copy it freely).
+ * PKV_EINVAL: head_dim not 64 or 128, rotary_dim not a multiple of 16 in [16, head_dim], base
+ * <= 1, factor < 1, and for the last two scalings original_len <= 0 or not 0 < low < high.
+ */
+#define PKV_ROPE_NONE   0
+#define PKV_ROPE_LINEAR 1
+#define PKV_ROPE_NTK    2
+#define PKV_ROPE_PARTS  3
+#define PKV_ROPE_YARN   4
+typedef struct {
+  int32_t head_dim, rotary_dim, interleaved, scaling;
+  double base, factor, original_len, low, high, amplitude;
+} pkv_rope_config;
+typedef struct {
+  int32_t head_dim, rotary_dim, interleaved;
+  float amplitude;
+  uint64_t turns[64];
+} pkv_rope_table;
+pkv_status pkv_rope_init(const pkv_rope_config* config, pkv_rope_table* table);
+
+/*
+ * rope_append — rotate a step's queries and keys by their positions and append the keys and
+ * values to the bf16 cache, in one pass (pkv_kv_append with the rotation in front of it).
+ *   q, k, v       bf16 [n_tok][heads][head_dim] with q_stride / k_stride / v_stride elements
+ *                 between tokens (multiples of 8, at least heads * head_dim): parts of one
+ *                 fused projection output are taken as they lie
+ *   positions     int32 [n_tok]
+ *   slot_mapping  int64 [n_tok], as for pkv_kv_append.  A negative slot is padding: nothing of
+ *                 the token is written, its q_out row neither.
+ *   q_out         bf16, q_out_stride elements between tokens; may be q itself (with its stride)
+ *   k_pool,v_pool as for pkv_kv_append
+ * The rotation runs in fp32 and rounds once, to nearest even; copied channels and V are
+ * bit-exact.  A slot >= num_blocks * block_size sets PKV_DEV_BAD_SLOT and skips the token.
+ */
+pkv_status pkv_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping, int n_tok,
+                           const pkv_rope_table* table, void* q_out, int64_t q_out_stride, void* k_pool,
+                           void* v_pool, int num_blocks, int block_size, int n_h, int n_kv, int head_dim,
+                           int32_t* err_flag, void* stream);
+
+/*
+ * rope_qk — the rotation alone (ahead of a quantizing append): q_out and k_out get the rotated
+ * heads, with strides as above; each may be its input.
+ */
+pkv_status pkv_rope_qk(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const int32_t* positions,
+                       int n_tok, const pkv_rope_table* table, void* q_out, int64_t q_out_stride, void* k_out,
+                       int64_t k_out_stride, int n_h, int n_kv, int head_dim, void* stream);
+
+/*
+ * The 8-bit cache: codes of 8 bits with one fp32 scale per (block, kv head) for K and one for V.
+ *
+ * kv_quant_append_q8 — quantize-on-append.  Exact op sequence, in fp32, per (block, kv head) and
+ * for K and V apart, over the rows that the block holds after the call:
+ *   big = max |x|;  scale = big / M and inv = M / big (nearest), M = 448 (PKV_Q8_E4M3) or 127
+ *   (PKV_Q8_INT8); both are 0 when big < 2^-110
+ *   code = e4m3(x * inv), nearest even, saturating; or rint(x * inv) clamped to +-127
+ * and the value held is code * scale.  A block's codes depend on its rows alone, not on the calls
+ * that brought them: the bf16 rows of a sequence's unfinished block are kept in k_tail / v_tail,
+ * and each append writes the record anew from them and its own tokens.
+ *   k, v          bf16 [n_tok][n_kv][head_dim], k_stride / v_stride elements between tokens
+ *                 (multiples of 8)
+ *   slot_mapping  int64 [n_tok] (negative = padding); tail_seq int32 [n_tok]: the tail row of
+ *                 each token's sequence, in [0, tail_rows)
+ *   cache         uint8 [num_blocks][n_kv][R], R = pkv_q8_record_bytes(block_size, head_dim) =
+ *                 2 bs d + 16: K codes [bs * d], V codes [bs * d], K scale, V scale (fp32), 8
+ *                 bytes of zeros.  Codes are stored per 16-token tile in the order in which a
+ *                 warp's lanes hold the operands of mma.m16n8k16: lane 4 i + j of a group of 32
+ *                 channels has 16 bytes; byte 8 a + 4 b + 2 c + e of it is
+ *                   K: token 8 b + i, channel 16 a + 8 c + 2 j + e
+ *                   V: token 8 c + 2 j + e, channel 16 a + 8 b + i
+ *                 with the groups of a tile and the tiles of a block one after another.  Rows
+ *                 not yet appended have codes 0.
+ *   k_tail,v_tail bf16 [tail_rows][n_kv][block_size][head_dim], read and written
+ * Caller contract: as for pkv_kv_quant_append_int4 (slots distinct; within a call the tokens of a
+ * sequence are consecutive entries in logical order with one tail_seq; a sequence starts at row 0
+ * of its first block); values finite (a NaN is lost in INT8 and stays NaN in E4M3, an infinity
+ * spoils its block).  A slot or tail row out of range sets PKV_DEV_BAD_SLOT and is skipped.
+ */
+#define PKV_Q8_E4M3 0
+#define PKV_Q8_INT8 1
+size_t pkv_q8_record_bytes(int block_size, int head_dim);
+pkv_status pkv_kv_quant_append_q8(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                  const int64_t* slot_mapping, const int32_t* tail_seq, int n_tok, int format,
+                                  uint8_t* cache, void* k_tail, void* v_tail, int tail_rows, int num_blocks,
+                                  int block_size, int n_kv, int head_dim, int32_t* err_flag, void* stream);
+
+/*
+ * paged_decode_attn_q8 — decode attention over the records written by pkv_kv_quant_append_q8,
+ * equal to the attention over the values held (code * scale) up to fp32 accumulation: the scales
+ * are taken out of the products, the codes enter the tensor cores exactly (as fp16), q exactly up
+ * to 2^-39 of its head's largest value, p as a high + low fp16 pair (22 bits, down to 2^-31).
+ * window as for pkv_paged_decode_attn_window (0: the whole context).  Other arguments, output and
+ * errors as for pkv_paged_decode_attn; workspace of pkv_q8_workspace_bytes (0: invalid shape).
+ * The tails are not read.
+ */
+size_t pkv_q8_workspace_bytes(int batch, int n_h, int n_kv, int head_dim, int block_size, int format);
+pkv_status pkv_paged_decode_attn_q8(const void* q, const uint8_t* cache, int format, const int32_t* block_tables,
+                                    int max_blocks, const int32_t* context_lens, float scale, int window, int batch,
+                                    int n_h, int n_kv, int head_dim, int block_size, int num_blocks, void* out,
+                                    int out_dtype, void* workspace, size_t workspace_bytes, int32_t* err_flag,
+                                    void* stream);
+
+/*
+ * paged_decode_attn_mass — pkv_paged_decode_attn that also adds, for each token t of sequence s
+ * and kv head g, the attention weights it got from the group's query heads to an account:
+ *   mass[(s * n_kv + g) * mass_stride + t] += sum over h in g of p[s][h][t],  t < context_lens[s]
+ * in fp32 and in a fixed order (the same bits on every call).  Entries at or behind the context
+ * are left as they were.  The accounts are per sequence, also where sequences share blocks.
+ *   mass          fp32, mass_stride >= max_blocks * block_size
+ *   workspace     pkv_mass_workspace_bytes bytes (it holds the step's scores: 4 n_h bytes per
+ *                 token of max_blocks * block_size; 0: invalid shape), 256-byte aligned
+ * Tokens of a bad block weigh nothing.  Other arguments and errors as for pkv_paged_decode_attn.
+ */
+size_t pkv_mass_workspace_bytes(int batch, int n_h, int n_kv, int head_dim, int block_size, int max_blocks);
+pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_pool, const void* v_pool,
+                                      const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
+                                      float scale, int batch, int n_h, int n_kv, int head_dim, int block_size,
+                                      int num_blocks, void* out, int out_dtype, float* mass, int64_t mass_stride,
+                                      void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream);
+
+/*
+ * kv_evict — cut sequences of the bf16 cache to a budget of rows by the accounts above.
+ * For each sequence s with n = context_lens[s] > K = max(0, keep[s]), and each kv head g apart,
+ * K rows stay: those that hold one of the sequence's last min(recent, K) tokens, then those with
+ * the largest mass (equal mass: lowest row first; NaN above +inf, -0 below +0).  Kept rows below K stay in place; the kept rows
+ * at or behind K are moved, in ascending order, into the other rows below K, in ascending order
+ * (attention does not depend on the order of rows; a limited attention window does, so it has no
+ * meaning on a sequence after an eviction).  Sequences with n <= K are left as they are.
+ * State, per sequence and kv head (rows of `stride` >= max_blocks * block_size entries):
+ *   mass       fp32: moved with the rows; rows [K, n) become 0, so later tokens start at 0
+ *   positions  int32: the token each row r < kept[s] holds (counting from the sequence's start);
+ *              row r >= kept[s] holds token dropped[s] + r
+ *   kept       int32 [batch]: rows that the last eviction left (0 at the start)
+ *   dropped    int32 [batch]: tokens evicted so far (0 at the start)
+ * The new state goes to the _out pointers: all four equal to the inputs (in place), or none.
+ * Entries of mass_out behind n, and of positions_out behind the new kept, are left as they were.
+ *   new_lens   int32 [batch]: min(n, K); not the same array as context_lens or keep
+ *   workspace  pkv_evict_workspace_bytes bytes, 256-byte aligned
+ * The blocks that hold the first K rows are rewritten: they must belong to the sequence alone
+ * (see pkv_bm_evict).  Moves from or to a block id outside the pool set PKV_DEV_BAD_BLOCK and are
+ * skipped; context lengths out of range are clamped with PKV_DEV_BAD_CTX.
+ */
+size_t pkv_evict_workspace_bytes(int batch, int n_kv, int block_size, int max_blocks);
+pkv_status pkv_kv_evict(void* k_pool, void* v_pool, const int32_t* block_tables, int max_blocks,
+                        const int32_t* context_lens, const int32_t* keep, int recent, const float* mass,
+                        const int32_t* positions, const int32_t* kept, const int32_t* dropped, float* mass_out,
+                        int32_t* positions_out, int32_t* kept_out, int32_t* dropped_out, int64_t stride,
+                        int32_t* new_lens, int batch, int n_kv, int head_dim, int block_size, int num_blocks,
+                        void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream);
+
+/*
  * CacheBlend's model-free steps ("Research Paper Review : CACHE BLEND ...", sections
  * "Methods" and "System Design"): the KV deviation of candidate tokens, the selection of
  * the tokens with the largest deviation under the recompute ratio, and the fuse of their

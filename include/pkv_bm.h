@@ -105,6 +105,16 @@ int pkv_bm_release(pkv_block_manager* bm, int64_t seq_id);
  * into the tree.  Returns the index of the first block the sequence still holds. */
 int pkv_bm_slide_window(pkv_block_manager* bm, int64_t seq_id, int window);
 
+/* Cut a sequence's cache to its first `keep` rows (1 <= keep <= its length), for pkv_kv_evict
+ * called with the sequence's table from before and that budget: the blocks behind them are
+ * released, later tokens are appended from row `keep` on, and pkv_bm_tables reports `keep` as the
+ * context length.  The remaining blocks no longer hold the prompt's tokens in order: they leave
+ * the tree, with their subtrees, and none of the sequence's blocks is registered again.
+ * Returns the number of blocks left, or PKV_EINVAL (also when a remaining block is shared with
+ * another running sequence, or the sequence has slid its window), changing nothing.
+ * keep equal to the length changes nothing. */
+int pkv_bm_evict(pkv_block_manager* bm, int64_t seq_id, int keep);
+
 /* Block tables and context lengths of n running sequences for one attention call:
  * tables is [n][max_blocks] (int32, entries past a sequence's blocks and of blocks it
  * released by sliding its window are -1), context_lens [n].  PKV_ERANGE if a sequence has

@@ -36,15 +36,18 @@ from .paged_attention import (kv_append, gather_sequence, paged_decode_attention
 from .kv_sizes import kv_bytes, kv_bytes_gqa, kv_bytes_per_token
 from .int4 import (quantize_group, quantize_groups, pack_codes, unpack_codes, Int4Cache,
                    paged_decode_attention_int4)
-from .rope import rope_shift_k, rotate
+from .rope import rope_shift_k, rotate, rope_frequencies, rope_tokens
+from .q8 import Q8Cache, quantize_rows, round_e4m3
 from .brute import attention_loops
 from .block_manager import BlockManager, OutOfBlocks, apply_copies
 from . import cacheblend
+from . import evict
 
 __all__ = [
     "round_bf16", "round_fp16_from_f32", "kv_append", "gather_sequence",
     "paged_decode_attention", "attention_weights", "kv_bytes", "kv_bytes_gqa",
     "kv_bytes_per_token", "quantize_group", "quantize_groups", "pack_codes", "unpack_codes", "Int4Cache",
     "paged_decode_attention_int4", "rope_shift_k", "rotate", "attention_loops", "window_start",
+    "rope_frequencies", "rope_tokens", "Q8Cache", "quantize_rows", "round_e4m3", "evict",
     "layer_windows", "BlockManager", "OutOfBlocks", "apply_copies", "cacheblend",
 ]

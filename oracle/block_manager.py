@@ -279,6 +279,29 @@ class BlockManager:
         seq["first"] = max(seq["first"], first)
         return seq["first"]
 
+    def evict(self, seq_id, keep):
+        """Cut a sequence's cache to its first `keep` rows: the blocks behind are released; the
+        remaining ones no longer hold the prompt in order, so they leave the tree and the sequence
+        registers nothing again.  Returns the blocks left; ValueError changes nothing."""
+        seq = self.seqs[seq_id]
+        n = len(seq["tokens"])
+        nb = -(-keep // self.bs)
+        if not 1 <= keep <= n or seq["first"] > 0:
+            raise ValueError("keep out of range, or the window has slid")
+        if keep == n:
+            return nb
+        if any(self.gpu_ref[b] > 1 for b in seq["blocks"][:nb]):
+            raise ValueError("a remaining block is shared")
+        self.clock += 1
+        for b in seq["blocks"][:nb]:
+            if self.gpu_node[b] is not None:
+                self._drop(self.gpu_node[b])
+        for b in seq["blocks"][nb:]:
+            self._release_block(b)
+        seq["tokens"], seq["blocks"], seq["prios"] = seq["tokens"][:keep], seq["blocks"][:nb], seq["prios"][:nb]
+        seq["chain"] = None
+        return nb
+
     def table(self, seq_id):
         seq = self.seqs[seq_id]
         return list(seq["blocks"]), len(seq["tokens"])

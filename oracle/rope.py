@@ -38,3 +38,49 @@ def rope_shift_k(k_pool, block_ids, deltas, base=10000.0):
     for b, dl in zip(np.asarray(block_ids).tolist(), np.asarray(deltas).tolist()):
         kp[int(b)] = round_bf16(rotate(kp[int(b)], dl, base))
     return kp
+
+
+def rope_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, original_len=0.0, low=1.0, high=32.0):
+    """(angle per position of each channel pair, multiplier of cos and sin) after a scaling for
+    contexts `factor` times the trained length, float64.
+
+    none; linear: every angle divided by factor; ntk: base * factor^(r / (r - 2)); parts: pairs
+    that make at least `high` turns over the trained length keep their angle, those with at most
+    `low` turns are divided by factor, between them the share is linear in the turns; yarn: the
+    share is linear in the pair's index, between the (rounded) indices whose turns are high and
+    low, and cos and sin are multiplied by 0.1 ln(factor) + 1.
+    """
+    r = rotary_dim
+    out, amp = [], 1.0
+    b = base * factor ** (r / (r - 2.0)) if scaling == "ntk" else base
+    if scaling == "yarn":
+        index = [r * np.log(original_len / (2 * np.pi * t)) / (2 * np.log(b)) for t in (high, low)]
+        i0, i1 = max(np.floor(index[0]), 0), min(np.ceil(index[1]), r - 1)
+        amp = 0.1 * np.log(factor) + 1.0
+    for j in range(r // 2):
+        w = 1.0 / b ** (2.0 * j / r)
+        keep = 1.0
+        if scaling == "linear":
+            keep = 0.0
+        elif scaling == "parts":
+            keep = (original_len * w / (2 * np.pi) - low) / (high - low)
+        elif scaling == "yarn":
+            keep = 1.0 - (j - i0) / max(i1 - i0, 0.001)
+        keep = min(max(keep, 0.0), 1.0)
+        out.append(keep * w + (1.0 - keep) * w / factor)
+    return np.array(out), amp
+
+
+def rope_tokens(x, positions, freqs, amp=1.0, interleaved=False):
+    """Rotate the first 2 len(freqs) channels of x [n_tok][heads][d] by the tokens' positions (float64,
+    no rounding): pairs (j, j + r/2), or (2j, 2j + 1) when interleaved; the other channels are copied."""
+    x = np.array(x, dtype=np.float64, copy=True)
+    h = len(freqs)
+    for t, pos in enumerate(np.asarray(positions).tolist()):
+        for j in range(h):
+            i0, i1 = (2 * j, 2 * j + 1) if interleaved else (j, j + h)
+            a = np.fmod(pos * freqs[j], 2 * np.pi)
+            c, s = amp * np.cos(a), amp * np.sin(a)
+            u, v = x[t, :, i0].copy(), x[t, :, i1].copy()
+            x[t, :, i0], x[t, :, i1] = u * c - v * s, u * s + v * c
+    return x

@@ -10,12 +10,16 @@ Functions (same names as the C entry points without the ``pkv_`` prefix):
 ``paged_decode_attn_noalloc``, ``kv_quant_append_int4``, ``paged_decode_attn_int4``,
 ``paged_decode_attn_int4_window``, ``rope_shift_k``, ``copy_blocks``, ``kv_deviation``,
 ``select_top``, ``kv_fuse``, ``recompute_ratio``, ``select_count``, ``probe_read``,
-``probe_copy``, ``layer_window`` (as ``layer_windows``), plus
-``decode_workspace_bytes``, ``alloc_int4_cache`` and ``BlockManager`` (the ``pkv_bm_*`` calls of include/pkv_bm.h).
+``probe_copy``, ``layer_window`` (as ``layer_windows``), ``rope_append``, ``rope_qk``,
+``kv_quant_append_q8``, ``paged_decode_attn_q8``, ``paged_decode_attn_mass``, ``kv_evict``, plus
+``rope_table`` (``pkv_rope_init``), ``decode_workspace_bytes`` and the other ``*_workspace_bytes``,
+``alloc_int4_cache``, ``alloc_q8_cache``, ``alloc_evict_state`` and ``BlockManager`` (the ``pkv_bm_*`` calls of
+include/pkv_bm.h).
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -31,6 +35,7 @@ _lib = None
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 _SIGS = {
     "pkv_status_str": (ctypes.c_char_p, [_I]),
     "pkv_last_cuda_error": (_I, []),
@@ -49,6 +54,21 @@ _SIGS = {
                                           _P, _I, _P, ctypes.c_size_t, _P, _P]),
     "pkv_paged_decode_attn_int4_window": (_I, [_P, _P, _P, _P, _I, _P, ctypes.c_float, _I, _I, _I, _I, _I, _I,
                                                _I, _P, _I, _P, ctypes.c_size_t, _P, _P]),
+    # rotary positions, the 8-bit cache, accounted attention and eviction
+    "pkv_rope_init": (_I, [_P, _P]),
+    "pkv_rope_append": (_I, [_P, _L, _P, _L, _P, _L, _P, _P, _I, _P, _P, _L, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "pkv_rope_qk": (_I, [_P, _L, _P, _L, _P, _I, _P, _P, _L, _P, _L, _I, _I, _I, _P]),
+    "pkv_q8_record_bytes": (ctypes.c_size_t, [_I, _I]),
+    "pkv_kv_quant_append_q8": (_I, [_P, _L, _P, _L, _P, _P, _I, _I, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "pkv_q8_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I]),
+    "pkv_paged_decode_attn_q8": (_I, [_P, _P, _I, _P, _I, _P, ctypes.c_float, _I, _I, _I, _I, _I, _I, _I,
+                                      _P, _I, _P, ctypes.c_size_t, _P, _P]),
+    "pkv_mass_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I]),
+    "pkv_paged_decode_attn_mass": (_I, [_P, _P, _P, _P, _I, _P, ctypes.c_float, _I, _I, _I, _I, _I, _I,
+                                        _P, _I, _P, _L, _P, ctypes.c_size_t, _P, _P]),
+    "pkv_evict_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
+    "pkv_kv_evict": (_I, [_P, _P, _P, _I, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _L, _P, _I, _I, _I, _I, _I,
+                          _P, ctypes.c_size_t, _P, _P]),
     # block manager (host) and its copy executor
     "pkv_bm_create": (_P, [_I, _I, _I, _I, _I]),
     "pkv_bm_destroy": (None, [_P]),
@@ -56,6 +76,7 @@ _SIGS = {
     "pkv_bm_append_tokens": (_I, [_P, _P, _P, _I, _P, _P]),
     "pkv_bm_release": (_I, [_P, ctypes.c_int64]),
     "pkv_bm_slide_window": (_I, [_P, ctypes.c_int64, _I]),
+    "pkv_bm_evict": (_I, [_P, ctypes.c_int64, _I]),
     "pkv_bm_tables": (_I, [_P, _P, _I, _P, _I, _P]),
     "pkv_bm_take_copies": (_I, [_P, _P, _I]),
     "pkv_bm_pending_copies": (_I, [_P]),
@@ -321,6 +342,379 @@ def rope_shift_k(k_pool, block_ids, deltas, rope_base=10000.0, err=None, stream=
 
 
 # ---------------------------------------------------------------------------------------------
+# Rotary positions, the 8-bit cache, accounted attention and eviction (pkv.h).
+ROPE_SCALINGS = ("none", "linear", "ntk", "parts", "yarn")
+Q8_FORMATS = ("e4m3", "int8")
+
+
+class _RopeConfig(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("amplitude", ctypes.c_double)]
+
+
+class RopeTable(ctypes.Structure):
+    """Angle table of a rotary embedding (rope_table); plain data, not to be changed."""
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("amplitude", ctypes.c_float), ("turns", ctypes.c_uint64 * 64)]
+
+
+@functools.lru_cache(maxsize=64)
+def rope_table(head_dim, rotary_dim=None, base=10000.0, interleaved=False, scaling="none", factor=1.0,
+               original_len=0.0, low=1.0, high=32.0, amplitude=0.0) -> RopeTable:
+    """The angle table for rope_append / rope_qk: rotary_dim channels of head_dim (all by default) in
+    half or interleaved pairs, with a scaling for contexts `factor` times original_len (pkv_rope_init)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {ROPE_SCALINGS}")
+    c = _RopeConfig(int(head_dim), int(head_dim if rotary_dim is None else rotary_dim), 1 if interleaved else 0,
+                    ROPE_SCALINGS.index(scaling), float(base), float(factor), float(original_len), float(low),
+                    float(high), float(amplitude))
+    t = RopeTable()
+    _check("rope_init", lib().pkv_rope_init(ctypes.byref(c), ctypes.byref(t)))
+    return t
+
+
+def _on_current(*ts):
+    """All tensors (None is skipped) on the current CUDA device; returns its index."""
+    if not ts[0].is_cuda:
+        raise PkvError("tensors must be CUDA tensors")
+    d = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and t.get_device() != d:             # -1 for a CPU tensor
+            raise PkvError("tensors must be on the current CUDA device")
+    return d
+
+
+def _dense(*ts):
+    for t in ts:
+        if t is not None and not t.is_contiguous():
+            raise PkvError("tensors must be contiguous")
+
+
+def _typed(dtype, *ts):
+    for t in ts:
+        if t is not None and t.dtype != dtype:
+            raise PkvError(f"expected {dtype}, got {t.dtype}")
+
+
+def _shaped(what, t, *shape):
+    if t is not None and tuple(t.shape) != shape:
+        raise PkvError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _heads(t):
+    """Token stride of a [n_tok][heads][head_dim] tensor whose heads are dense."""
+    if t.dim() != 3:
+        raise PkvError("expected a [tokens][heads][head_dim] tensor")
+    n, h, d = t.shape
+    if n and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
+        raise PkvError("the heads of a token must be contiguous")
+    return t.stride(0) if n > 1 else h * d
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, device):
+    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
+
+
+def _scratch(workspace, nbytes, device, stream):
+    """The caller's workspace, or one of nbytes() that stays alive for the work on `stream`."""
+    if workspace is not None:
+        _dense(workspace)
+        return workspace
+    n = nbytes()
+    if n == 0:
+        raise PkvError("unsupported shape or no device")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
+def _result(like, out, out_dtype, stream):
+    if out is None:
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise PkvError("out_dtype must be bfloat16 or float32")
+        out = torch.empty(like.shape, dtype=out_dtype, device=like.device)
+        if stream is not None:
+            out.record_stream(stream)
+    elif out.shape != like.shape or out.dtype not in (torch.bfloat16, torch.float32) or not out.is_contiguous():
+        raise PkvError("out must be a contiguous bfloat16 or float32 tensor of q's shape")
+    return out, (PKV_OUT_F32 if out.dtype == torch.float32 else PKV_OUT_BF16)
+
+
+def rope_append(q, k, v, positions, slot_mapping, table: RopeTable, k_pool, v_pool, q_out=None, err=None, stream=None):
+    """Rotate q and k [n_tok][heads][d] by positions (int32) and append k and v to the bf16 cache;
+    returns the rotated q.  Tokens may be strided (parts of one fused projection); q_out may be q."""
+    dev = _on_current(q, k, v, positions, slot_mapping, k_pool, v_pool, q_out, err)
+    _typed(torch.bfloat16, q, k, v, k_pool, v_pool, q_out)
+    _typed(torch.int32, positions, err)
+    _typed(torch.int64, slot_mapping)
+    _dense(positions, slot_mapping, k_pool, v_pool)
+    n, n_h, d = q.shape
+    num_blocks, n_kv, bs, _ = k_pool.shape
+    _shaped("k", k, n, n_kv, d)
+    _shaped("v", v, n, n_kv, d)
+    _shaped("positions", positions, n)
+    _shaped("slot_mapping", slot_mapping, n)
+    _shaped("k_pool", k_pool, num_blocks, n_kv, bs, d)
+    _shaped("v_pool", v_pool, num_blocks, n_kv, bs, d)
+    if q_out is None:
+        q_out = torch.empty((n, n_h, d), dtype=q.dtype, device=q.device)
+        if stream is not None:
+            q_out.record_stream(stream)
+    _shaped("q_out", q_out, n, n_h, d)
+    _check("rope_append", lib().pkv_rope_append(
+        q.data_ptr(), _heads(q), k.data_ptr(), _heads(k), v.data_ptr(), _heads(v), positions.data_ptr(),
+        slot_mapping.data_ptr(), n, ctypes.addressof(table), q_out.data_ptr(), _heads(q_out), k_pool.data_ptr(),
+        v_pool.data_ptr(), num_blocks, bs, n_h, n_kv, d, _addr(err), _raw_stream(stream, dev)))
+    return q_out
+
+
+def rope_qk(q, k, positions, table: RopeTable, q_out=None, k_out=None, stream=None):
+    """Rotate q and k [n_tok][heads][d] by positions (int32); returns (q_out, k_out), which may be
+    given as q and k themselves."""
+    dev = _on_current(q, k, positions, q_out, k_out)
+    _typed(torch.bfloat16, q, k, q_out, k_out)
+    _typed(torch.int32, positions)
+    _dense(positions)
+    n, n_h, d = q.shape
+    n_kv = k.shape[1]
+    _shaped("k", k, n, n_kv, d)
+    _shaped("positions", positions, n)
+    if q_out is None:
+        q_out = torch.empty((n, n_h, d), dtype=q.dtype, device=q.device)
+        if stream is not None:
+            q_out.record_stream(stream)
+    if k_out is None:
+        k_out = torch.empty((n, n_kv, d), dtype=k.dtype, device=k.device)
+        if stream is not None:
+            k_out.record_stream(stream)
+    _shaped("q_out", q_out, n, n_h, d)
+    _shaped("k_out", k_out, n, n_kv, d)
+    _check("rope_qk", lib().pkv_rope_qk(
+        q.data_ptr(), _heads(q), k.data_ptr(), _heads(k), positions.data_ptr(), n, ctypes.addressof(table),
+        q_out.data_ptr(), _heads(q_out), k_out.data_ptr(), _heads(k_out), n_h, n_kv, d, _raw_stream(stream, dev)))
+    return q_out, k_out
+
+
+def q8_record_bytes(block_size, head_dim) -> int:
+    """Bytes of one (block, kv head) record of the 8-bit cache (0 for an unsupported shape)."""
+    return int(lib().pkv_q8_record_bytes(int(block_size), int(head_dim)))
+
+
+@dataclass
+class Q8CacheTensors:
+    """8-bit paged cache: one record per (block, kv head) -- K codes, V codes in the order of pkv.h,
+    K and V scale -- and the bf16 rows of each sequence's unfinished block."""
+    records: torch.Tensor     # uint8 [num_blocks][n_kv][q8_record_bytes(bs, d)]
+    k_tail: torch.Tensor      # bf16  [tail_rows][n_kv][bs][d]
+    v_tail: torch.Tensor
+    fmt: str = "e4m3"         # or "int8"
+
+    @property
+    def shape(self):
+        _, n_kv, bs, d = self.k_tail.shape
+        return self.records.shape[0], n_kv, bs, d
+
+    @property
+    def scales(self):         # fp32 [num_blocks][n_kv][2]: K, V (a view)
+        _, _, bs, d = self.shape
+        return self.records[:, :, 2 * bs * d:2 * bs * d + 8].view(torch.float32)
+
+    def _codes(self, keys):
+        nb, n_kv, bs, d = self.shape
+        x = self.records[:, :, (0 if keys else bs * d):(bs * d if keys else 2 * bs * d)]
+        # 16-token tile, group of 32 channels, lane (i, j), bytes (a, b, c, e) of pkv.h
+        x = x.reshape(nb, n_kv, bs // 16, d // 32, 8, 4, 2, 2, 2, 2)
+        order = (0, 1, 2, 7, 4, 3, 6, 8, 5, 9) if keys else (0, 1, 2, 8, 5, 9, 3, 6, 7, 4)
+        return x.permute(order).reshape(nb, n_kv, bs, d).view(torch.float8_e4m3fn if self.fmt == "e4m3" else torch.int8)
+
+    @property
+    def k_codes(self):        # [num_blocks][n_kv][bs][d], token by token (a copy)
+        return self._codes(True)
+
+    @property
+    def v_codes(self):
+        return self._codes(False)
+
+
+def alloc_q8_cache(num_blocks, n_kv, block_size, head_dim, tail_rows, fmt="e4m3", device="cuda") -> Q8CacheTensors:
+    rec = q8_record_bytes(block_size, head_dim)
+    if rec == 0 or fmt not in Q8_FORMATS:
+        raise ValueError(f"8-bit cache: unsupported block_size {block_size} / head_dim {head_dim} / format {fmt}")
+    tail = lambda: torch.zeros(tail_rows, n_kv, block_size, head_dim, dtype=torch.bfloat16, device=device)
+    return Q8CacheTensors(torch.zeros(num_blocks, n_kv, rec, dtype=torch.uint8, device=device), tail(), tail(), fmt)
+
+
+def _q8_parts(cache):
+    if cache.fmt not in Q8_FORMATS:
+        raise PkvError(f"format must be one of {Q8_FORMATS}")
+    tail_rows, n_kv, bs, d = cache.k_tail.shape
+    _typed(torch.uint8, cache.records)
+    _typed(torch.bfloat16, cache.k_tail, cache.v_tail)
+    _dense(cache.records, cache.k_tail, cache.v_tail)
+    _shaped("v_tail", cache.v_tail, tail_rows, n_kv, bs, d)
+    nb = cache.records.shape[0]
+    _shaped("records", cache.records, nb, n_kv, 2 * bs * d + 16)
+    return nb, n_kv, bs, d, Q8_FORMATS.index(cache.fmt)
+
+
+def kv_quant_append_q8(k, v, slot_mapping, tail_seq, cache: Q8CacheTensors, err=None, stream=None):
+    """Quantize-on-append of k, v [n_tok][n_kv][d] (tokens may be strided) into the 8-bit cache."""
+    dev = _on_current(k, v, slot_mapping, tail_seq, cache.records, cache.k_tail, cache.v_tail, err)
+    nb, n_kv, bs, d, fmt = _q8_parts(cache)
+    _typed(torch.bfloat16, k, v)
+    _typed(torch.int64, slot_mapping)
+    _typed(torch.int32, tail_seq, err)
+    _dense(slot_mapping, tail_seq)
+    n = k.shape[0]
+    _shaped("k", k, n, n_kv, d)
+    _shaped("v", v, n, n_kv, d)
+    _shaped("slot_mapping", slot_mapping, n)
+    _shaped("tail_seq", tail_seq, n)
+    _check("kv_quant_append_q8", lib().pkv_kv_quant_append_q8(
+        k.data_ptr(), _heads(k), v.data_ptr(), _heads(v), slot_mapping.data_ptr(), tail_seq.data_ptr(), n, fmt,
+        cache.records.data_ptr(), cache.k_tail.data_ptr(), cache.v_tail.data_ptr(), cache.k_tail.shape[0], nb, bs,
+        n_kv, d, _addr(err), _raw_stream(stream, dev)))
+
+
+def q8_workspace_bytes(batch, n_h, n_kv, head_dim, block_size, fmt="e4m3") -> int:
+    """Bytes of workspace paged_decode_attn_q8 needs for this shape on the current device."""
+    n = lib().pkv_q8_workspace_bytes(batch, n_h, n_kv, head_dim, block_size, Q8_FORMATS.index(fmt))
+    if n == 0:
+        raise PkvError("q8_workspace_bytes: invalid shape or no device")
+    return n
+
+
+def paged_decode_attn_q8(q, cache: Q8CacheTensors, block_tables, context_lens, scale, window=0, out=None,
+                         out_dtype=torch.bfloat16, workspace=None, err=None, stream=None):
+    """Decode attention over the 8-bit cache (the last `window` tokens of each context; 0: all)."""
+    dev = _on_current(q, cache.records, block_tables, context_lens, out, workspace, err)
+    nb, n_kv, bs, d, fmt = _q8_parts(cache)
+    _typed(torch.bfloat16, q)
+    _typed(torch.int32, block_tables, context_lens, err)
+    _dense(q, block_tables, context_lens)
+    B, n_h, _ = q.shape
+    _shaped("q", q, B, n_h, d)
+    _shaped("block_tables", block_tables, B, block_tables.shape[-1])
+    _shaped("context_lens", context_lens, B)
+    out, od = _result(q, out, out_dtype, stream)
+    ws = _scratch(workspace, lambda: lib().pkv_q8_workspace_bytes(B, n_h, n_kv, d, bs, fmt), q.device, stream)
+    _check("paged_decode_attn_q8", lib().pkv_paged_decode_attn_q8(
+        q.data_ptr(), cache.records.data_ptr(), fmt, block_tables.data_ptr(), block_tables.shape[1],
+        context_lens.data_ptr(), scale, int(window), B, n_h, n_kv, d, bs, nb, out.data_ptr(), od, ws.data_ptr(),
+        ws.numel() * ws.element_size(), _addr(err), _raw_stream(stream, dev)))
+    return out
+
+
+def mass_workspace_bytes(batch, n_h, n_kv, head_dim, block_size, max_blocks) -> int:
+    """Bytes of workspace paged_decode_attn_mass needs for this shape on the current device."""
+    n = lib().pkv_mass_workspace_bytes(batch, n_h, n_kv, head_dim, block_size, max_blocks)
+    if n == 0:
+        raise PkvError("mass_workspace_bytes: invalid shape or no device")
+    return n
+
+
+def paged_decode_attn_mass(q, k_pool, v_pool, block_tables, context_lens, scale, mass, out=None,
+                           out_dtype=torch.bfloat16, workspace=None, err=None, stream=None):
+    """paged_decode_attn that also adds each cached token's attention weight, summed over the query
+    heads of its group, to mass (fp32 [B][n_kv][at least max_blocks * block_size])."""
+    dev = _on_current(q, k_pool, v_pool, block_tables, context_lens, mass, out, workspace, err)
+    _typed(torch.bfloat16, q, k_pool, v_pool)
+    _typed(torch.int32, block_tables, context_lens, err)
+    _typed(torch.float32, mass)
+    _dense(q, k_pool, v_pool, block_tables, context_lens, mass)
+    B, n_h, d = q.shape
+    nb, n_kv, bs, _ = k_pool.shape
+    _shaped("k_pool", k_pool, nb, n_kv, bs, d)
+    _shaped("v_pool", v_pool, nb, n_kv, bs, d)
+    _shaped("block_tables", block_tables, B, block_tables.shape[-1])
+    _shaped("context_lens", context_lens, B)
+    _shaped("mass", mass, B, n_kv, mass.shape[-1])
+    out, od = _result(q, out, out_dtype, stream)
+    mb = block_tables.shape[1]
+    ws = _scratch(workspace, lambda: lib().pkv_mass_workspace_bytes(B, n_h, n_kv, d, bs, mb), q.device, stream)
+    _check("paged_decode_attn_mass", lib().pkv_paged_decode_attn_mass(
+        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), mb, context_lens.data_ptr(), scale,
+        B, n_h, n_kv, d, bs, nb, out.data_ptr(), od, mass.data_ptr(), mass.shape[2], ws.data_ptr(),
+        ws.numel() * ws.element_size(), _addr(err), _raw_stream(stream, dev)))
+    return out
+
+
+@dataclass
+class EvictState:
+    """What kv_evict keeps of each sequence (pkv.h): accounts, recorded positions, counts."""
+    mass: torch.Tensor        # fp32  [B][n_kv][T]
+    positions: torch.Tensor   # int32 [B][n_kv][T]
+    kept: torch.Tensor        # int32 [B]
+    dropped: torch.Tensor     # int32 [B]
+
+    def reset(self, s):
+        """Make row s ready for a new sequence."""
+        self.mass[s].zero_()
+        self.kept[s] = 0
+        self.dropped[s] = 0
+
+
+def alloc_evict_state(batch, n_kv, max_tokens, device="cuda") -> EvictState:
+    """State for sequences of up to max_tokens rows (a multiple of the block size)."""
+    z = lambda *shape, dtype=torch.int32: torch.zeros(*shape, dtype=dtype, device=device)
+    return EvictState(z(batch, n_kv, max_tokens, dtype=torch.float32), z(batch, n_kv, max_tokens), z(batch), z(batch))
+
+
+def evict_workspace_bytes(batch, n_kv, block_size, max_blocks) -> int:
+    n = lib().pkv_evict_workspace_bytes(batch, n_kv, block_size, max_blocks)
+    if n == 0:
+        raise PkvError("evict_workspace_bytes: invalid shape")
+    return n
+
+
+def kv_evict(k_pool, v_pool, block_tables, context_lens, keep, recent, state: EvictState, out: EvictState | None = None,
+             new_lens=None, workspace=None, err=None, stream=None):
+    """Cut each sequence of the bf16 cache to keep[s] rows (int32 [B]): the `recent` newest and those
+    with the largest accounts.  Updates `state` in place, or writes the new state to `out`; returns
+    the new context lengths (a tensor of its own)."""
+    dst = state if out is None else out
+    dev = _on_current(k_pool, v_pool, block_tables, context_lens, keep, state.mass, state.positions, state.kept,
+                      state.dropped, dst.mass, dst.positions, dst.kept, dst.dropped, new_lens, workspace, err)
+    _typed(torch.bfloat16, k_pool, v_pool)
+    _typed(torch.int32, block_tables, context_lens, keep, state.positions, state.kept, state.dropped, dst.positions,
+           dst.kept, dst.dropped, new_lens, err)
+    _typed(torch.float32, state.mass, dst.mass)
+    _dense(k_pool, v_pool, block_tables, context_lens, keep, state.mass, state.positions, state.kept, state.dropped,
+           dst.mass, dst.positions, dst.kept, dst.dropped, new_lens)
+    nb, n_kv, bs, d = k_pool.shape
+    B, mb = block_tables.shape
+    T = state.mass.shape[-1]
+    _shaped("v_pool", v_pool, nb, n_kv, bs, d)
+    for st in (state, dst):
+        _shaped("mass", st.mass, B, n_kv, T)
+        _shaped("positions", st.positions, B, n_kv, T)
+        _shaped("kept", st.kept, B)
+        _shaped("dropped", st.dropped, B)
+    _shaped("context_lens", context_lens, B)
+    _shaped("keep", keep, B)
+    if new_lens is None:
+        new_lens = torch.empty_like(context_lens)
+        if stream is not None:
+            new_lens.record_stream(stream)
+    _shaped("new_lens", new_lens, B)
+    ws = _scratch(workspace, lambda: lib().pkv_evict_workspace_bytes(B, n_kv, bs, mb), k_pool.device, stream)
+    _check("kv_evict", lib().pkv_kv_evict(
+        k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), mb, context_lens.data_ptr(), keep.data_ptr(),
+        int(recent), state.mass.data_ptr(), state.positions.data_ptr(), state.kept.data_ptr(), state.dropped.data_ptr(),
+        dst.mass.data_ptr(), dst.positions.data_ptr(), dst.kept.data_ptr(), dst.dropped.data_ptr(), T,
+        new_lens.data_ptr(), B, n_kv, d, bs, nb, ws.data_ptr(), ws.numel() * ws.element_size(), _addr(err),
+        _raw_stream(stream, dev)))
+    return new_lens
+
+
+# ---------------------------------------------------------------------------------------------
 # Block manager (host, include/pkv_bm.h) and the GPU copies it records.
 COPY_OFFLOAD, COPY_ONLOAD = 0, 1
 BM_COUNTS = ("free", "active", "cached", "host", "reused_tokens", "evictions", "offloads", "onloads", "drops")
@@ -383,6 +777,13 @@ class BlockManager:
         r = lib().pkv_bm_slide_window(self._h, int(seq_id), int(window))
         if r < 0:
             _check("bm_slide_window", r)
+        return r
+
+    def evict(self, seq_id, keep):
+        """Cut a sequence to its first `keep` cache rows (after kv_evict); returns the blocks left."""
+        r = lib().pkv_bm_evict(self._h, int(seq_id), int(keep))
+        if r < 0:
+            _check("bm_evict", r)
         return r
 
     def tables(self, seq_ids, max_blocks):

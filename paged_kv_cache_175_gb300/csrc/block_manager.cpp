@@ -441,6 +441,34 @@ int pkv_bm_slide_window(pkv_block_manager* bm, int64_t seq_id, int window) {
   return s.first;
 }
 
+int pkv_bm_evict(pkv_block_manager* bm, int64_t seq_id, int keep) {
+  if (!bm || keep < 1) return PKV_EINVAL;
+  auto it = bm->seqs.find(seq_id);
+  if (it == bm->seqs.end()) return PKV_EINVAL;
+  Seq& s = it->second;
+  const int n = (int)s.tokens.size();
+  if (keep > n || s.first > 0) return PKV_EINVAL;
+  const int nb = (int)(((int64_t)keep + bm->bs - 1) / bm->bs);
+  if (keep == n) return nb;
+  for (int i = 0; i < nb; ++i)
+    if (bm->gpu_ref[s.blocks[i]] > 1) return PKV_EINVAL;
+  ++bm->clock;
+  try {
+    for (int i = 0; i < nb; ++i) {
+      const int id = bm->gpu_node[s.blocks[i]];
+      if (id >= 0) bm->drop(id);
+    }
+    for (int i = nb; i < (int)s.blocks.size(); ++i) bm->release_block(s.blocks[i]);
+  } catch (...) {
+    return PKV_ENOSPC;                         // out of host memory
+  }
+  s.tokens.resize(keep);
+  s.blocks.resize(nb);
+  s.prios.resize(nb);
+  s.chain.broken = true;
+  return nb;
+}
+
 int pkv_bm_tables(pkv_block_manager* bm, const int64_t* seq_ids, int n, int32_t* tables, int max_blocks,
                   int32_t* context_lens) {
   if (!bm || n < 0 || max_blocks < 0 || (n && (!seq_ids || !tables || !context_lens))) return PKV_EINVAL;

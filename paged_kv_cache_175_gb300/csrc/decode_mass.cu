@@ -1,0 +1,478 @@
+// Paged decode attention over the bf16 cache that also adds each cached token's attention
+// weight, summed over the query heads of its kv group, to a per-sequence account:
+//   out[s][h] = sum_t p[h][t] v_t,   mass[s][g][t] += sum_{h in g} p[h][t],   p = softmax(scale q k).
+//
+// Mathematics: a token's weight needs the final softmax state (M, L) of its row, which is known
+// only after the whole context was read.  Reading K a second time would add half of the
+// attention's traffic; the scores themselves are 4 G bytes per token and kv head against the
+// 4 d bytes of its K and V.  So the attention kernel stores the scaled scores (base-2 units,
+// fp32, as they entered the softmax) in the workspace, each row's (M, 1 / L) is stored by
+// whoever finishes the row, and a second kernel adds sum_h 2^(x_h - M_h) / L_h to the account.
+// Every token's sum is taken by one thread group in a fixed order: no atomics, the same bits on
+// every call.
+//
+// What bounds it: HBM for K and V; the scores of a step mostly stay in L2 between the two
+// kernels.  Structure of the attention kernel: as decode_q8.cu, with the K and V tiles of a
+// block brought by TMA in 128-byte swizzled boxes and read by ldmatrix.
+#include <cmath>
+#include <cstdlib>
+#include <mutex>
+
+#include "decode_mass.cuh"
+#include "nvtx_range.h"
+#include "piece_producer.cuh"
+
+namespace pkv {
+
+struct MassArgs {
+  float* scores;                 // workspace: [batch][n_kv][max_ctx][G], base-2 units
+  float2* fin;                   // workspace: [batch][n_h] (offset, 1 / sum)
+};
+
+__host__ __device__ constexpr size_t mass_smem_bytes(int stages, int stage_bytes) {
+  return 1024 + (size_t)stages * (stage_bytes + 16 + 16);
+}
+
+// Keep the halves of a pair of rows (t, t + 1) below ntok; zero the others.
+__device__ __forceinline__ uint32_t keep_rows(uint32_t b, int t, int ntok) {
+  return b & ((t < ntok ? 0x0000ffffu : 0u) | (t + 1 < ntok ? 0xffff0000u : 0u));
+}
+
+template <int D, int TT, int NH, int MT>
+__global__ void __launch_bounds__((MT + 1) * 32)
+    decode_mass_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                       const DecodeArgs a, const MassArgs ms, const int bs16l) {
+  constexpr int KS = D / 16, MD = D / 16, HW = 8 * NH, NBOX = D / 64;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int S = a.stages, BS = 16 << bs16l, TPB = 1 << bs16l, NB = TT >> bs16l;
+  const int BOX = BS * 128, TILE = BS * D * 2, STAGE = TT * 16 * D * 4;
+  int4* meta = reinterpret_cast<int4*>(smem + (size_t)S * STAGE);
+  uint64_t* full = reinterpret_cast<uint64_t*>(meta + S);
+  uint64_t* empty = full + S;
+  __shared__ volatile int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tig = lane & 3, gid = lane >> 2;
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], MT);
+    }
+    fence_barrier_init();
+    prefetch_tensormap(&tmk);
+    prefetch_tensormap(&tmv);
+  }
+  __syncthreads();
+  if (!a.inline_plan) grid_dep_wait();   // the plan kernel's cum / ctx_eff / cursors
+  grid_dep_launch();
+
+  Cursor cur;
+  PieceInfo pi;
+  piece_setup(a, blockIdx.x, gridDim.x, warp == MT, cur, pi);
+  const int p = blockIdx.x;
+  const int len = p < pi.P ? (int)(pi.pend - pi.pstart) : 0;
+  // Every thread waits for the kernel before this one (the append), also those without work,
+  // so that no later launch on the stream can pass it.
+  if (len > 0 && warp == MT && lane == 0) prefetch_l2(a.bt + (size_t)cur.s * a.max_blocks + cur.b0 + cur.blk);
+  if (a.inline_plan) grid_dep_wait();
+  if (len <= 0) return;
+
+  if (warp == MT) {
+    const uint64_t pol = policy_evict_first();
+    produce_piece(a, cur, pi, len, bs16l, NB, S, (uint32_t)(2 * TILE), 2 * D, meta, full, empty, &abort_flag,
+                  [&](int slot, int k, int phys, int kvh) {
+                    uint8_t* st = smem + (size_t)slot * STAGE + k * 2 * TILE;
+#pragma unroll
+                    for (int b = 0; b < NBOX; ++b) {
+                      tma_load_3d(st + b * BOX, &tmk, b * 64, kvh * BS, phys, &full[slot], pol);
+                      tma_load_3d(st + TILE + b * BOX, &tmv, b * 64, kvh * BS, phys, &full[slot], pol);
+                    }
+                  });
+    return;
+  }
+
+  // ---------------- consumer warp: local heads [warp * HW, warp * HW + HW) ----------------
+  uint32_t qb[KS][NH][2];
+  float o[MD][NH][4];
+  float m[NH][2], l[NH][2];
+  const int hw0 = warp * HW;
+  const bool even = (a.G & 1) == 0;
+  int slot = 0;
+  uint32_t phase = 0;
+  for (;;) {
+    if (!mbar_wait(&full[slot], phase) || abort_flag) {
+      set_err(a.err, PKV_DEV_TIMEOUT);
+      abort_flag = 1;
+      break;
+    }
+    const int4 mt = meta[slot];
+    const int s = mt.x, g = mt.y, ntok = mt.w & 255, flags = (mt.w >> 8) & 255;
+    const size_t qrow0 = (size_t)s * a.n_h + (size_t)g * a.G;
+    // this thread's score of token t of the stage and its head column n: at sp[t * G + n]
+    float* sp = ms.scores + (((size_t)s * a.n_kv + g) * a.max_ctx + (size_t)mt.z * BS) * a.G + hw0 + 2 * tig;
+
+    if (flags & F_FIRST) {
+#pragma unroll
+      for (int nh = 0; nh < NH; ++nh) {
+        const int hl = hw0 + nh * 8 + gid;                     // B-fragment column n = gid
+        const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q) + (qrow0 + hl) * (D / 2);
+        const bool ok = hl < a.G;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          qb[ks][nh][0] = ok ? __ldg(qp + ks * 8 + tig) : 0u;
+          qb[ks][nh][1] = ok ? __ldg(qp + ks * 8 + 4 + tig) : 0u;
+        }
+        m[nh][0] = m[nh][1] = -INFINITY;
+        l[nh][0] = l[nh][1] = 0.f;
+#pragma unroll
+        for (int md = 0; md < MD; ++md) o[md][nh][0] = o[md][nh][1] = o[md][nh][2] = o[md][nh][3] = 0.f;
+      }
+    }
+
+    if (flags & F_VALID) {
+      const uint32_t st = smem_u32(smem + (size_t)slot * STAGE);
+      const int tiles = (ntok + 15) >> 4, mi = lane >> 3;
+      // ---- S^T = K Q^T ----
+      float sc[TT][NH][4];
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[t][nh][i] = 0.f;
+        if (t >= tiles) continue;
+        const uint32_t kb = st + (uint32_t)((t >> bs16l) * 2 * TILE);
+        const int tok = (t & (TPB - 1)) * 16 + ((mi & 1) << 3) + (lane & 7);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const int ch = 2 * ks + (mi >> 1);
+          uint32_t ka[4];
+          ldsm_x4(ka[0], ka[1], ka[2], ka[3], kb + (ch >> 3) * BOX + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh) mma_bf16(sc[t][nh], ka, qb[ks][nh][0], qb[ks][nh][1]);
+        }
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            sc[t][nh][2 * r] *= a.scale_log2;
+            sc[t][nh][2 * r + 1] *= a.scale_log2;
+            const int tk = t * 16 + gid + 8 * r, n = hw0 + nh * 8 + 2 * tig;
+            if (tk < ntok && n < a.G) {
+              float* d = sp + (size_t)tk * a.G + nh * 8;
+              if (even) {
+                *reinterpret_cast<float2*>(d) = make_float2(sc[t][nh][2 * r], sc[t][nh][2 * r + 1]);
+              } else {
+                d[0] = sc[t][nh][2 * r];
+                if (n + 1 < a.G) d[1] = sc[t][nh][2 * r + 1];
+              }
+            }
+          }
+      }
+      softmax_tile<TT, NH, MD>(sc, m, l, o, gid, ntok, 0, 1.f);
+      // ---- O^T += V^T P^T, P as bf16 high + low ----
+      const bool partial = ntok < TT * 16;
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        if (t >= tiles) continue;
+        const uint32_t vb = st + (uint32_t)((t >> bs16l) * 2 * TILE + TILE);
+        const int tok = (t & (TPB - 1)) * 16 + ((mi >> 1) << 3) + (lane & 7);
+        uint32_t bh[NH][2], bl[NH][2];
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float x = sc[t][nh][2 * r], y = sc[t][nh][2 * r + 1];
+            const uint32_t hi = pack_bf16(x, y);
+            const uint32_t lo = pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi));
+            bh[nh][r] = movmatrix_t(hi);
+            bl[nh][r] = movmatrix_t(lo);
+          }
+        const int t0 = t * 16 + 2 * tig;
+#pragma unroll
+        for (int md = 0; md < MD; ++md) {
+          const int ch = 2 * md + (mi & 1);
+          uint32_t va[4];
+          ldsm_x4_t(va[0], va[1], va[2], va[3], vb + (ch >> 3) * BOX + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
+          if (partial) {
+            va[0] = keep_rows(va[0], t0, ntok);
+            va[1] = keep_rows(va[1], t0, ntok);
+            va[2] = keep_rows(va[2], t0 + 8, ntok);
+            va[3] = keep_rows(va[3], t0 + 8, ntok);
+          }
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh) {
+            mma_bf16(o[md][nh], va, bh[nh][0], bh[nh][1]);
+            mma_bf16(o[md][nh], va, bl[nh][0], bl[nh][1]);
+          }
+        }
+      }
+    } else {
+      // a block outside the pool: its tokens weigh nothing
+      for (int t = gid; t < ntok; t += 8)
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (hw0 + nh * 8 + 2 * tig + e < a.G) sp[(size_t)t * a.G + nh * 8 + e] = -INFINITY;
+    }
+
+    if (flags & F_LAST) {
+      const bool whole = flags & F_WHOLE;
+      const long long part = (long long)s * a.n_kv + g + p;
+#pragma unroll
+      for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float L = l[nh][e];
+          L += __shfl_xor_sync(FULL_MASK, L, 4);
+          L += __shfl_xor_sync(FULL_MASK, L, 8);
+          L += __shfl_xor_sync(FULL_MASK, L, 16);
+          const int hl = hw0 + nh * 8 + 2 * tig + e;           // this thread's head columns
+          if (hl >= a.G) continue;
+          if (whole) {
+            const float inv = L > 0.f ? 1.f / L : 0.f;
+            const size_t base = (qrow0 + hl) * D;
+            if (gid == 0) ms.fin[qrow0 + hl] = make_float2(m[nh][e] == -INFINITY ? 0.f : m[nh][e], inv);
+            if (a.out_f32) {
+              float* out = reinterpret_cast<float*>(a.out) + base;
+#pragma unroll
+              for (int md = 0; md < MD; ++md) {
+                out[md * 16 + gid] = o[md][nh][e] * inv;
+                out[md * 16 + gid + 8] = o[md][nh][2 + e] * inv;
+              }
+            } else {
+              __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + base;
+#pragma unroll
+              for (int md = 0; md < MD; ++md) {
+                out[md * 16 + gid] = __float2bfloat16_rn(o[md][nh][e] * inv);
+                out[md * 16 + gid + 8] = __float2bfloat16_rn(o[md][nh][2 + e] * inv);
+              }
+            }
+          } else {
+            float* wo = a.ws_o + ((size_t)part * a.G + hl) * D;
+#pragma unroll
+            for (int md = 0; md < MD; ++md) {
+              wo[md * 16 + gid] = o[md][nh][e];
+              wo[md * 16 + gid + 8] = o[md][nh][2 + e];
+            }
+            if (gid == 0)
+              *reinterpret_cast<float2*>(a.ws_ml + ((size_t)part * a.G + hl) * 2) = make_float2(m[nh][e], L);
+          }
+        }
+    }
+
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[slot]);
+    if (++slot == S) {
+      slot = 0;
+      phase ^= 1u;
+    }
+    if (flags & F_END) break;
+  }
+}
+
+// mass[s][g][t] += sum over the group's heads of 2^(x - M) / L.  CTA (c, s, g): kMassTokens
+// tokens; LT lanes share a token's G scores (vectors of four where G allows), so a warp reads
+// whole lines, and add their parts by a fixed tree.
+constexpr int kMassTokens = 512;
+
+template <int LT, bool V4>
+__global__ void __launch_bounds__(256) mass_add_kernel(const float* __restrict__ scores, const float2* __restrict__ fin,
+                                                       const int32_t* __restrict__ ctx, int max_ctx, int n_kv, int G,
+                                                       float* __restrict__ mass, long long mass_stride, int chunks) {
+  __shared__ float2 f[64];
+  const int chunk = blockIdx.x % chunks, sg = blockIdx.x / chunks, s = sg / n_kv, g = sg % n_kv;
+  grid_dep_wait();                                            // every thread: see decode_plan.cu's reduce
+  const int n = clamp_ctx(ctx[s], max_ctx), t1 = min(n, (chunk + 1) * kMassTokens);
+  if (chunk * kMassTokens >= n) return;
+  if (threadIdx.x < G) f[threadIdx.x] = fin[((size_t)s * n_kv + g) * G + threadIdx.x];
+  __syncthreads();
+  const int sub = threadIdx.x % LT;
+  const float* x = scores + ((size_t)sg * max_ctx) * G;
+  float* mrow = mass + (size_t)sg * mass_stride;
+  for (int t0 = chunk * kMassTokens; t0 < t1; t0 += 256 / LT) {
+    const int t = t0 + threadIdx.x / LT;
+    float w = 0.f;
+    if (t < t1) {
+      if constexpr (V4) {
+        for (int i = sub; i < G / 4; i += LT) {
+          const float4 v = *(reinterpret_cast<const float4*>(x + (size_t)t * G) + i);
+          w += ex2(v.x - f[4 * i].x) * f[4 * i].y + ex2(v.y - f[4 * i + 1].x) * f[4 * i + 1].y +
+               ex2(v.z - f[4 * i + 2].x) * f[4 * i + 2].y + ex2(v.w - f[4 * i + 3].x) * f[4 * i + 3].y;
+        }
+      } else {
+        for (int i = sub; i < G; i += LT) w += ex2(x[(size_t)t * G + i] - f[i].x) * f[i].y;
+      }
+    }
+#pragma unroll
+    for (int o = LT / 2; o; o >>= 1) w += __shfl_xor_sync(FULL_MASK, w, o);
+    if (sub == 0 && t < t1) mrow[t] += w;
+  }
+}
+
+static const void* mass_add_fn(int G) {
+  if (G % 4) return G >= 8 ? (const void*)mass_add_kernel<4, false> : (const void*)mass_add_kernel<1, false>;
+  return G >= 32 ? (const void*)mass_add_kernel<8, true>
+                 : (G >= 16 ? (const void*)mass_add_kernel<4, true>
+                            : (G >= 8 ? (const void*)mass_add_kernel<2, true> : (const void*)mass_add_kernel<1, true>));
+}
+
+// ---------------------------------------------------------------------------------------------
+struct MassVariant {
+  const void* fn;
+  int stages, warps, P, tiles;
+  size_t smem;
+};
+
+template <int D, int TT>
+static const void* mass_fn(int tiling) {
+  return tiling == 0 ? (const void*)decode_mass_kernel<D, TT, 1, 1>
+                     : (tiling == 1 ? (const void*)decode_mass_kernel<D, TT, 1, 2>
+                                    : (tiling == 2 ? (const void*)decode_mass_kernel<D, TT, 2, 2>
+                                                   : (const void*)decode_mass_kernel<D, TT, 2, 4>));
+}
+
+static MassVariant* lookup_mass(int D, int BS, int tiling) {
+  // One table per process; the library drives one device per process.
+  static std::mutex mu;
+  static MassVariant table[2][3][4];
+  static bool ready[2][3][4] = {};
+  const int di = D == 128 ? 1 : 0, bi = BS == 16 ? 0 : (BS == 32 ? 1 : 2);
+  std::lock_guard<std::mutex> lock(mu);
+  MassVariant& v = table[di][bi][tiling];
+  if (!ready[di][bi][tiling]) {
+    v.tiles = BS == 64 ? 4 : 2;                               // a stage holds whole blocks
+    v.fn = D == 128 ? (v.tiles == 4 ? mass_fn<128, 4>(tiling) : mass_fn<128, 2>(tiling))
+                    : (v.tiles == 4 ? mass_fn<64, 4>(tiling) : mass_fn<64, 2>(tiling));
+    v.warps = (tiling == 0 ? 1 : (tiling == 3 ? 4 : 2)) + 1;
+    const int stage = v.tiles * 16 * D * 4;
+    v.stages = ring_stages(stage, 32768, "PKV_STAGES_MASS");
+    v.smem = mass_smem_bytes(v.stages, stage);
+    if (cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)v.smem) != cudaSuccess) return nullptr;
+    int occ = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, v.fn, v.warps * 32, v.smem) != cudaSuccess || occ < 1)
+      return nullptr;
+    v.P = device_sm_count() * occ;
+    ready[di][bi][tiling] = true;
+  }
+  return &v;
+}
+
+static bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+static bool valid_shape(int n_h, int n_kv, int head_dim, int block_size) {
+  if (head_dim != 64 && head_dim != 128) return false;
+  if (block_size != 16 && block_size != 32 && block_size != 64) return false;
+  if (n_kv <= 0 || n_h <= 0 || n_h % n_kv) return false;
+  return n_h / n_kv <= 64;
+}
+
+struct MassLayout {
+  WorkspaceLayout w;
+  size_t fin, scores, total;
+};
+static MassLayout mass_layout(int B, int n_h, int n_kv, int D, long long max_ctx, int P) {
+  MassLayout x;
+  x.w = workspace_layout(B, n_kv, n_h / n_kv, D, P);
+  x.fin = x.w.total;
+  x.scores = align_up(x.fin + sizeof(float2) * (size_t)B * n_h, 256);
+  x.total = align_up(x.scores + sizeof(float) * (size_t)B * n_h * (size_t)max_ctx, 256);
+  return x;
+}
+
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" size_t pkv_mass_workspace_bytes(int batch, int n_h, int n_kv, int head_dim, int block_size, int max_blocks) {
+  if (batch < 0 || max_blocks < 0 || !valid_shape(n_h, n_kv, head_dim, block_size)) return 0;
+  if ((long long)max_blocks * block_size > 0x7fffffffLL) return 0;
+  MassVariant* v = lookup_mass(head_dim, block_size, head_tiling(n_h / n_kv));
+  return v ? mass_layout(batch, n_h, n_kv, head_dim, (long long)max_blocks * block_size, v->P).total : 0;
+}
+
+extern "C" pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_pool, const void* v_pool,
+                                                 const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
+                                                 float scale, int batch, int n_h, int n_kv, int head_dim, int block_size,
+                                                 int num_blocks, void* out, int out_dtype, float* mass, int64_t mass_stride,
+                                                 void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream) {
+  PKV_NVTX("pkv_paged_decode_attn_mass");
+  if (batch < 0 || !valid_shape(n_h, n_kv, head_dim, block_size) || max_blocks < 0 || num_blocks < 0) return PKV_EINVAL;
+  if (out_dtype != PKV_OUT_BF16 && out_dtype != PKV_OUT_F32) return PKV_EINVAL;
+  if (batch == 0) return PKV_OK;
+  if (!q || !k_pool || !v_pool || !block_tables || !context_lens || !out || !mass || !workspace) return PKV_EINVAL;
+  if (!al16(q) || !al16(k_pool) || !al16(v_pool) || !al16(out) || (reinterpret_cast<uintptr_t>(mass) & 3u) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return PKV_EINVAL;
+  const long long max_ctx = (long long)max_blocks * block_size;
+  if (max_ctx > 0x7fffffffLL) return PKV_ERANGE;
+  if (mass_stride < max_ctx) return PKV_EINVAL;
+  const int G = n_h / n_kv;
+  const long long chunks = (max_ctx + kMassTokens - 1) / kMassTokens;
+  if (chunks * batch * n_kv > 0x7fffffffLL) return PKV_ERANGE;
+  MassVariant* v = lookup_mass(head_dim, block_size, head_tiling(G));
+  if (!v) {
+    record_cuda_error(cudaGetLastError());
+    return PKV_ECUDA;
+  }
+  const MassLayout ml = mass_layout(batch, n_h, n_kv, head_dim, max_ctx, v->P);
+  if (workspace_bytes < ml.total) return PKV_ENOSPC;
+
+  CUtensorMap tmk, tmv;
+  const uint64_t rows = (uint64_t)n_kv * block_size;
+  const uint64_t row_bytes = (uint64_t)head_dim * 2, block_bytes = rows * row_bytes;
+  const uint64_t nblk = num_blocks > 0 ? (uint64_t)num_blocks : 1;
+  if (encode_tensor_map_3d(&tmk, k_pool, head_dim, rows, nblk, row_bytes, block_bytes, 64, block_size) ||
+      encode_tensor_map_3d(&tmv, v_pool, head_dim, rows, nblk, row_bytes, block_bytes, 64, block_size))
+    return PKV_ECUDA;
+
+  char* ws = static_cast<char*>(workspace);
+  DecodeArgs a = {};
+  a.q = q;
+  a.bt = block_tables;
+  a.max_blocks = max_blocks;
+  a.cum = reinterpret_cast<int32_t*>(ws + ml.w.cum);
+  a.ctx_eff = reinterpret_cast<int32_t*>(ws + ml.w.ctx);
+  a.ctx_raw = context_lens;
+  a.max_ctx = (int)max_ctx;
+  a.block_size = block_size;
+  a.inline_plan = batch <= kInlinePlanSeqs;
+  a.pieces = reinterpret_cast<int4*>(ws + ml.w.pieces);
+  a.P_launch = v->P;
+  a.batch = batch;
+  a.n_h = n_h;
+  a.n_kv = n_kv;
+  a.G = G;
+  a.num_blocks = num_blocks;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.out = out;
+  a.out_f32 = out_dtype == PKV_OUT_F32;
+  a.ws_ml = reinterpret_cast<float*>(ws + ml.w.ml);
+  a.ws_o = reinterpret_cast<float*>(ws + ml.w.o);
+  a.err = err_flag;
+  a.stages = v->stages;
+  MassArgs ma = {reinterpret_cast<float*>(ws + ml.scores), reinterpret_cast<float2*>(ws + ml.fin)};
+  int bs16l = block_size == 16 ? 0 : (block_size == 32 ? 1 : 2);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = a.inline_plan ? cudaSuccess : launch_plan(context_lens, batch, (int)max_ctx, block_size, a, v->P, st);
+  if (e == cudaSuccess) {
+    void* kargs[] = {&tmk, &tmv, &a, &ma, &bs16l};
+    e = launch_pdl(v->fn, dim3(v->P), dim3(v->warps * 32), v->smem, st, kargs);
+  }
+  if (e == cudaSuccess) e = launch_reduce_fin(head_dim, a, v->P, ma.fin, st);
+  if (e == cudaSuccess && chunks > 0) {
+    const float* scores = ma.scores;
+    const float2* fin = ma.fin;
+    int mc = (int)max_ctx, nk = n_kv, gg = G, nc = (int)chunks;
+    long long stride = mass_stride;
+    void* kargs[] = {&scores, &fin, (void*)&context_lens, &mc, &nk, &gg, &mass, &stride, &nc};
+    e = launch_pdl(mass_add_fn(G), dim3((unsigned)(chunks * batch * n_kv)), dim3(256), 0, st, kargs);
+  }
+  if (e != cudaSuccess) {
+    record_cuda_error(e);
+    return PKV_ECUDA;
+  }
+  return PKV_OK;
+}

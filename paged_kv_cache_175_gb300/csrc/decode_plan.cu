@@ -8,7 +8,7 @@
 #include <cstdlib>
 #include <mutex>
 
-#include "decode_common.cuh"
+#include "decode_mass.cuh"
 
 namespace pkv {
 
@@ -180,6 +180,7 @@ cudaError_t launch_plan(const int32_t* context_lens, int batch, int max_ctx, int
 // CTA per row whose eight warps take interleaved chunks of its pieces and combine their
 // eight states through shared memory, for few long sequences, where a segment spans a large
 // share of the grid's pieces and one warp would take one memory round trip per eight of them.
+// fin (may be NULL): final softmax state of every row merged here.
 
 // Partial states a warp loads at a time in merge_pieces (LPR = 32 lanes per row: 8 per
 // row; LPR = 16: 4 per row, two rows per warp).
@@ -230,14 +231,16 @@ __device__ __forceinline__ void merge_pieces(const DecodeArgs& a, long long seg,
     float Mc = M;
 #pragma unroll
     for (int i = 0; i < CH; ++i) Mc = fmaxf(Mc, mv[i]);
-    const float r = ex2(M - Mc);                              // rescale what was merged so far
+    // pieces whose blocks were all bad hold -inf: any finite base gives them weight zero
+    const float base = Mc == -INFINITY ? 0.f : Mc;
+    const float r = ex2(M - base);                            // rescale what was merged so far
     L *= r;
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] *= r;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       if (!use[i]) continue;
-      const float w = ex2(mv[i] - Mc);
+      const float w = ex2(mv[i] - base);
       L += w * lv[i];
 #pragma unroll
       for (int k = 0; k < V; ++k) acc[k] += w * ov[i][k];
@@ -250,7 +253,7 @@ __device__ __forceinline__ void merge_pieces(const DecodeArgs& a, long long seg,
 constexpr int kWideReducePieces = 16;
 
 template <int D, bool WIDE, int LPR>
-__global__ void __launch_bounds__(256, LPR == 16 ? 4 : 0) reduce_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(256, LPR == 16 ? 4 : 0) reduce_kernel(const DecodeArgs a, float2* fin) {
   constexpr int V = D / LPR;                                  // channels per lane
   constexpr int RPC = 256 / LPR;                              // rows per CTA (narrow)
   static_assert(kInlinePlanSeqs == 8 * 32, "one sequence per thread of the CTA");
@@ -331,11 +334,12 @@ __global__ void __launch_bounds__(256, LPR == 16 ? 4 : 0) reduce_kernel(const De
     // largest exponent is finite and warps without pieces weigh zero
     const int t = threadIdx.x;
     if (t >= D / 2) return;
-    float o0 = 0.f, o1 = 0.f;
+    float o0 = 0.f, o1 = 0.f, Mt = 0.f, inv = 0.f;
     if (nb > 0) {
-      float Mt = sM[0];
+      Mt = sM[0];
 #pragma unroll
       for (int w = 1; w < 8; ++w) Mt = fmaxf(Mt, sM[w]);
+      if (Mt == -INFINITY) Mt = 0.f;                          // every block of the row was bad
       float Lt = 0.f;
 #pragma unroll
       for (int w = 0; w < 8; ++w) {
@@ -344,10 +348,11 @@ __global__ void __launch_bounds__(256, LPR == 16 ? 4 : 0) reduce_kernel(const De
         o0 += f * sacc[w][2 * t];
         o1 += f * sacc[w][2 * t + 1];
       }
-      const float inv = Lt > 0.f ? 1.f / Lt : 0.f;
+      inv = Lt > 0.f ? 1.f / Lt : 0.f;
       o0 *= inv;
       o1 *= inv;
     }
+    if (fin && t == 0) fin[row] = make_float2(Mt, inv);
     const size_t o = (size_t)row * D + 2 * t;
     if (a.out_f32) {
       *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + o) = make_float2(o0, o1);
@@ -359,6 +364,7 @@ __global__ void __launch_bounds__(256, LPR == 16 ? 4 : 0) reduce_kernel(const De
       constexpr int CH = kMergeChunk * LPR / 32;
       merge_pieces<D, LPR>(a, seg, hl, sub, p0, p1, CH, M, L, acc);
       const float inv = L > 0.f ? 1.f / L : 0.f;
+      if (fin && sub == 0) fin[row] = make_float2(M == -INFINITY ? 0.f : M, inv);
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] *= inv;
     }
@@ -386,6 +392,10 @@ static int reduce_wave() {
 }
 
 cudaError_t launch_reduce(int head_dim, const DecodeArgs& a, int P, cudaStream_t stream) {
+  return launch_reduce_fin(head_dim, a, P, nullptr, stream);
+}
+
+cudaError_t launch_reduce_fin(int head_dim, const DecodeArgs& a, int P, float2* fin, cudaStream_t stream) {
   const int rows = a.batch * a.n_h;
   if (rows == 0) return cudaSuccess;
   // the grid's pieces over the segments: about the average a segment spans
@@ -397,7 +407,7 @@ cudaError_t launch_reduce(int head_dim, const DecodeArgs& a, int P, cudaStream_t
   const bool half = !wide && wave > 0 && (rows + 7) / 8 > wave;
   dim3 grid(wide ? rows : (half ? (rows + 15) / 16 : (rows + 7) / 8)), block(256);
   DecodeArgs args = a;
-  void* kargs[] = {&args};
+  void* kargs[] = {&args, &fin};
   const void* fn;
   if (head_dim == 128)
     fn = wide ? (const void*)reduce_kernel<128, true, 32>
