@@ -12,15 +12,18 @@
 // every call.
 //
 // What bounds it: HBM for K and V; the scores of a step mostly stay in L2 between the two
-// kernels.  Structure of the attention kernel: as decode_q8.cu, with the K and V tiles of a
-// block brought by TMA in 128-byte swizzled boxes and read by ldmatrix.
+// kernels.  Structure of the attention kernel: the persistent grid of decode_common.cuh with the
+// streams of piece_streams.cuh, in units of 16 tokens whatever the block size: a TMA box of 16 rows
+// starts inside a larger block as well.  K and V land in 128-byte swizzled boxes and are read by
+// ldmatrix.
 #include <cmath>
 #include <cstdlib>
 #include <mutex>
 
+
 #include "decode_mass.cuh"
 #include "nvtx_range.h"
-#include "piece_producer.cuh"
+#include "piece_streams.cuh"
 
 namespace pkv {
 
@@ -29,8 +32,8 @@ struct MassArgs {
   float2* fin;                   // workspace: [batch][n_h] (offset, 1 / sum)
 };
 
-__host__ __device__ constexpr size_t mass_smem_bytes(int stages, int stage_bytes) {
-  return 1024 + (size_t)stages * (stage_bytes + 16 + 16);
+__host__ __device__ constexpr size_t mass_smem_bytes(int streams, int stages, int stage_bytes) {
+  return 1024 + (size_t)streams * stages * (stage_bytes + 16 + 16);
 }
 
 // Keep the halves of a pair of rows (t, t + 1) below ntok; zero the others.
@@ -38,24 +41,27 @@ __device__ __forceinline__ uint32_t keep_rows(uint32_t b, int t, int ntok) {
   return b & ((t < ntok ? 0x0000ffffu : 0u) | (t + 1 < ntok ? 0xffff0000u : 0u));
 }
 
-template <int D, int TT, int NH, int MT>
-__global__ void __launch_bounds__((MT + 1) * 32)
+// TT: 16-token units per stage; NH n-tiles of 8 heads per consumer warp, MT consumer warps per
+// stream, NW streams.  sub: log2 of the units per table block.
+template <int D, int TT, int NH, int MT, int NW>
+__global__ void __launch_bounds__((NW * MT + 1) * 32)
     decode_mass_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                       const DecodeArgs a, const MassArgs ms, const int bs16l) {
+                       const DecodeArgs a, const MassArgs ms, const int sub) {
   constexpr int KS = D / 16, MD = D / 16, HW = 8 * NH, NBOX = D / 64;
+  constexpr int BS = 16, BOX = BS * 128, TILE = BS * D * 2, STAGE = TT * 2 * TILE;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const int S = a.stages, BS = 16 << bs16l, TPB = 1 << bs16l, NB = TT >> bs16l;
-  const int BOX = BS * 128, TILE = BS * D * 2, STAGE = TT * 16 * D * 4;
-  int4* meta = reinterpret_cast<int4*>(smem + (size_t)S * STAGE);
-  uint64_t* full = reinterpret_cast<uint64_t*>(meta + S);
-  uint64_t* empty = full + S;
+  const int S = a.stages;
+  int4* meta = reinterpret_cast<int4*>(smem + (size_t)NW * S * STAGE);
+  uint64_t* full = reinterpret_cast<uint64_t*>(meta + NW * S);
+  uint64_t* empty = full + NW * S;
   __shared__ volatile int abort_flag;
+  __shared__ StreamStart starts[NW];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tig = lane & 3, gid = lane >> 2;
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    for (int i = 0; i < S; ++i) {
+    for (int i = 0; i < NW * S; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], MT);
     }
@@ -63,40 +69,42 @@ __global__ void __launch_bounds__((MT + 1) * 32)
     prefetch_tensormap(&tmk);
     prefetch_tensormap(&tmv);
   }
-  __syncthreads();
   if (!a.inline_plan) grid_dep_wait();   // the plan kernel's cum / ctx_eff / cursors
   grid_dep_launch();
-
-  Cursor cur;
-  PieceInfo pi;
-  piece_setup(a, blockIdx.x, gridDim.x, warp == MT, cur, pi);
-  const int p = blockIdx.x;
-  const int len = p < pi.P ? (int)(pi.pend - pi.pstart) : 0;
+  if (warp < NW * MT && warp % MT == 0)
+    stream_setup(a, blockIdx.x * NW + warp / MT, gridDim.x * NW, &starts[warp / MT]);
+  __syncthreads();
   // Every thread waits for the kernel before this one (the append), also those without work,
   // so that no later launch on the stream can pass it.
-  if (len > 0 && warp == MT && lane == 0) prefetch_l2(a.bt + (size_t)cur.s * a.max_blocks + cur.b0 + cur.blk);
   if (a.inline_plan) grid_dep_wait();
-  if (len <= 0) return;
 
-  if (warp == MT) {
+  if (warp == NW * MT) {
     const uint64_t pol = policy_evict_first();
-    produce_piece(a, cur, pi, len, bs16l, NB, S, (uint32_t)(2 * TILE), 2 * D, meta, full, empty, &abort_flag,
-                  [&](int slot, int k, int phys, int kvh) {
-                    uint8_t* st = smem + (size_t)slot * STAGE + k * 2 * TILE;
+    produce_streams(a, starts, NW, S, TT, sub, (uint32_t)(2 * TILE), 2 * D, meta, full, empty, &abort_flag,
+                    [&](int w, int slot, int k, int phys, int u, int kvh) {
+                      uint8_t* st = smem + (size_t)(w * S + slot) * STAGE + k * 2 * TILE;
+                      const int row = (kvh << sub | (u & ((1 << sub) - 1))) * BS;
 #pragma unroll
-                    for (int b = 0; b < NBOX; ++b) {
-                      tma_load_3d(st + b * BOX, &tmk, b * 64, kvh * BS, phys, &full[slot], pol);
-                      tma_load_3d(st + TILE + b * BOX, &tmv, b * 64, kvh * BS, phys, &full[slot], pol);
-                    }
-                  });
+                      for (int b = 0; b < NBOX; ++b) {
+                        tma_load_3d(st + b * BOX, &tmk, b * 64, row, phys, &full[w * S + slot], pol);
+                        tma_load_3d(st + TILE + b * BOX, &tmv, b * 64, row, phys, &full[w * S + slot], pol);
+                      }
+                    });
     return;
   }
 
-  // ---------------- consumer warp: local heads [warp * HW, warp * HW + HW) ----------------
+  // ---------------- consumer warp: local heads [warp % MT * HW, + HW) of its stream ----------------
+  const int w = warp / MT;
+  if (starts[w].len <= 0) return;
+  const int p = blockIdx.x * NW + w;
+  smem += (size_t)w * S * STAGE;
+  meta += w * S;
+  full += w * S;
+  empty += w * S;
   uint32_t qb[KS][NH][2];
   float o[MD][NH][4];
   float m[NH][2], l[NH][2];
-  const int hw0 = warp * HW;
+  const int hw0 = warp % MT * HW;
   const bool even = (a.G & 1) == 0;
   int slot = 0;
   uint32_t phase = 0;
@@ -142,8 +150,8 @@ __global__ void __launch_bounds__((MT + 1) * 32)
 #pragma unroll
           for (int i = 0; i < 4; ++i) sc[t][nh][i] = 0.f;
         if (t >= tiles) continue;
-        const uint32_t kb = st + (uint32_t)((t >> bs16l) * 2 * TILE);
-        const int tok = (t & (TPB - 1)) * 16 + ((mi & 1) << 3) + (lane & 7);
+        const uint32_t kb = st + (uint32_t)(t * 2 * TILE);
+        const int tok = ((mi & 1) << 3) + (lane & 7);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           const int ch = 2 * ks + (mi >> 1);
@@ -176,8 +184,8 @@ __global__ void __launch_bounds__((MT + 1) * 32)
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
         if (t >= tiles) continue;
-        const uint32_t vb = st + (uint32_t)((t >> bs16l) * 2 * TILE + TILE);
-        const int tok = (t & (TPB - 1)) * 16 + ((mi >> 1) << 3) + (lane & 7);
+        const uint32_t vb = st + (uint32_t)(t * 2 * TILE + TILE);
+        const int tok = ((mi >> 1) << 3) + (lane & 7);
         uint32_t bh[NH][2], bl[NH][2];
 #pragma unroll
         for (int nh = 0; nh < NH; ++nh)
@@ -322,40 +330,44 @@ static const void* mass_add_fn(int G) {
 // ---------------------------------------------------------------------------------------------
 struct MassVariant {
   const void* fn;
-  int stages, warps, P, tiles;
+  int stages, warps, streams, P;
   size_t smem;
 };
 
 template <int D, int TT>
-static const void* mass_fn(int tiling) {
-  return tiling == 0 ? (const void*)decode_mass_kernel<D, TT, 1, 1>
-                     : (tiling == 1 ? (const void*)decode_mass_kernel<D, TT, 1, 2>
-                                    : (tiling == 2 ? (const void*)decode_mass_kernel<D, TT, 2, 2>
-                                                   : (const void*)decode_mass_kernel<D, TT, 2, 4>));
+static void mass_pick(int tiling, MassVariant& v) {
+  auto set = [&](const void* fn, int mt, int nw) {
+    v.fn = fn;
+    v.streams = nw;
+    v.warps = nw * mt + 1;
+  };
+  if (tiling == 0) set((const void*)decode_mass_kernel<D, TT, 1, 1, 3>, 1, 3);
+  else if (tiling == 1) set((const void*)decode_mass_kernel<D, TT, 1, 2, 3>, 2, 3);
+  else if (tiling == 2) set((const void*)decode_mass_kernel<D, TT, 2, 2, 2>, 2, 2);
+  else set((const void*)decode_mass_kernel<D, TT, 2, 4, 1>, 4, 1);
 }
 
-static MassVariant* lookup_mass(int D, int BS, int tiling) {
+static MassVariant* lookup_mass(int D, int tiling) {
   // One table per process; the library drives one device per process.
   static std::mutex mu;
-  static MassVariant table[2][3][4];
-  static bool ready[2][3][4] = {};
-  const int di = D == 128 ? 1 : 0, bi = BS == 16 ? 0 : (BS == 32 ? 1 : 2);
+  static MassVariant table[2][4];
+  static bool ready[2][4] = {};
+  const int di = D == 128 ? 1 : 0;
   std::lock_guard<std::mutex> lock(mu);
-  MassVariant& v = table[di][bi][tiling];
-  if (!ready[di][bi][tiling]) {
-    v.tiles = BS == 64 ? 4 : 2;                               // a stage holds whole blocks
-    v.fn = D == 128 ? (v.tiles == 4 ? mass_fn<128, 4>(tiling) : mass_fn<128, 2>(tiling))
-                    : (v.tiles == 4 ? mass_fn<64, 4>(tiling) : mass_fn<64, 2>(tiling));
-    v.warps = (tiling == 0 ? 1 : (tiling == 3 ? 4 : 2)) + 1;
-    const int stage = v.tiles * 16 * D * 4;
-    v.stages = ring_stages(stage, 32768, "PKV_STAGES_MASS");
-    v.smem = mass_smem_bytes(v.stages, stage);
+  MassVariant& v = table[di][tiling];
+  if (!ready[di][tiling]) {
+    // 8 KB per stage at either head size
+    const int stage = 8192;
+    if (D == 128) mass_pick<128, 1>(tiling, v);
+    else mass_pick<64, 2>(tiling, v);
+    v.stages = ring_stages(stage, 2 * stage, "PKV_STAGES_MASS");
+    v.smem = mass_smem_bytes(v.streams, v.stages, stage);
     if (cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)v.smem) != cudaSuccess) return nullptr;
     int occ = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, v.fn, v.warps * 32, v.smem) != cudaSuccess || occ < 1)
       return nullptr;
-    v.P = device_sm_count() * occ;
-    ready[di][bi][tiling] = true;
+    v.P = device_sm_count() * occ * v.streams;
+    ready[di][tiling] = true;
   }
   return &v;
 }
@@ -389,7 +401,7 @@ using namespace pkv;
 extern "C" size_t pkv_mass_workspace_bytes(int batch, int n_h, int n_kv, int head_dim, int block_size, int max_blocks) {
   if (batch < 0 || max_blocks < 0 || !valid_shape(n_h, n_kv, head_dim, block_size)) return 0;
   if ((long long)max_blocks * block_size > 0x7fffffffLL) return 0;
-  MassVariant* v = lookup_mass(head_dim, block_size, head_tiling(n_h / n_kv));
+  MassVariant* v = lookup_mass(head_dim, head_tiling(n_h / n_kv));
   return v ? mass_layout(batch, n_h, n_kv, head_dim, (long long)max_blocks * block_size, v->P).total : 0;
 }
 
@@ -412,7 +424,7 @@ extern "C" pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_po
   const int G = n_h / n_kv;
   const long long chunks = (max_ctx + kMassTokens - 1) / kMassTokens;
   if (chunks * batch * n_kv > 0x7fffffffLL) return PKV_ERANGE;
-  MassVariant* v = lookup_mass(head_dim, block_size, head_tiling(G));
+  MassVariant* v = lookup_mass(head_dim, head_tiling(G));
   if (!v) {
     record_cuda_error(cudaGetLastError());
     return PKV_ECUDA;
@@ -424,8 +436,8 @@ extern "C" pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_po
   const uint64_t rows = (uint64_t)n_kv * block_size;
   const uint64_t row_bytes = (uint64_t)head_dim * 2, block_bytes = rows * row_bytes;
   const uint64_t nblk = num_blocks > 0 ? (uint64_t)num_blocks : 1;
-  if (encode_tensor_map_3d(&tmk, k_pool, head_dim, rows, nblk, row_bytes, block_bytes, 64, block_size) ||
-      encode_tensor_map_3d(&tmv, v_pool, head_dim, rows, nblk, row_bytes, block_bytes, 64, block_size))
+  if (encode_tensor_map_3d(&tmk, k_pool, head_dim, rows, nblk, row_bytes, block_bytes, 64, 16) ||
+      encode_tensor_map_3d(&tmv, v_pool, head_dim, rows, nblk, row_bytes, block_bytes, 64, 16))
     return PKV_ECUDA;
 
   char* ws = static_cast<char*>(workspace);
@@ -437,7 +449,7 @@ extern "C" pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_po
   a.ctx_eff = reinterpret_cast<int32_t*>(ws + ml.w.ctx);
   a.ctx_raw = context_lens;
   a.max_ctx = (int)max_ctx;
-  a.block_size = block_size;
+  a.block_size = 16;                                          // the line is in units of 16 tokens
   a.inline_plan = batch <= kInlinePlanSeqs;
   a.pieces = reinterpret_cast<int4*>(ws + ml.w.pieces);
   a.P_launch = v->P;
@@ -454,12 +466,12 @@ extern "C" pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_po
   a.err = err_flag;
   a.stages = v->stages;
   MassArgs ma = {reinterpret_cast<float*>(ws + ml.scores), reinterpret_cast<float2*>(ws + ml.fin)};
-  int bs16l = block_size == 16 ? 0 : (block_size == 32 ? 1 : 2);
+  int sub = block_size == 16 ? 0 : (block_size == 32 ? 1 : 2);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = a.inline_plan ? cudaSuccess : launch_plan(context_lens, batch, (int)max_ctx, block_size, a, v->P, st);
+  cudaError_t e = a.inline_plan ? cudaSuccess : launch_plan(context_lens, batch, (int)max_ctx, 16, a, v->P, st);
   if (e == cudaSuccess) {
-    void* kargs[] = {&tmk, &tmv, &a, &ma, &bs16l};
-    e = launch_pdl(v->fn, dim3(v->P), dim3(v->warps * 32), v->smem, st, kargs);
+    void* kargs[] = {&tmk, &tmv, &a, &ma, &sub};
+    e = launch_pdl(v->fn, dim3(v->P / v->streams), dim3(v->warps * 32), v->smem, st, kargs);
   }
   if (e == cudaSuccess) e = launch_reduce_fin(head_dim, a, v->P, ma.fin, st);
   if (e == cudaSuccess && chunks > 0) {

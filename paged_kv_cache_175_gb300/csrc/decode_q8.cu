@@ -10,18 +10,18 @@
 // by the lazy offset, so 2^15 at most, and the smallest step is 2^-31 of p = 1), which carries
 // 22 bits.  Softmax, sums and outputs are fp32.
 //
-// Structure: the persistent grid and the line of blocks of decode_common.cuh.  A producer warp
-// walks the CTA's piece and brings the records of up to TT / (bs / 16) consecutive blocks per
-// stage into a ring, one contiguous bulk copy per record, issued by one lane each; consumer
-// warps take 8 or 16 heads each.  Per 16-token tile, S^T = C_k Q^T and O^T += C_v^T P^T with
-// mma.m16n8k16; the A fragments of both are one 16-byte load per lane and 32 channels, since the
-// records hold the codes in fragment order.
+// Structure: the persistent grid and the line of blocks of decode_common.cuh, NW streams per CTA
+// (piece_streams.cuh).  A stage is 32 tokens: two records of 16 tokens, one of 32, or half of a
+// 64-token record (its K half, V half and scales as three copies that land in the layout of a
+// 32-token record), so one kernel serves every block size.  Per 16-token tile, S^T = C_k Q^T and
+// O^T += C_v^T P^T with mma.m16n8k16; the A fragments of both are one 16-byte load per lane and 32
+// channels, since the records hold the codes in fragment order.
 #include <cmath>
 #include <cstdlib>
 #include <mutex>
 
 #include "nvtx_range.h"
-#include "piece_producer.cuh"
+#include "piece_streams.cuh"
 #include "q8_common.cuh"
 
 namespace pkv {
@@ -57,9 +57,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ float lds_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+__device__ __forceinline__ float2 lds_f32x2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
   return v;
 }
 __device__ __forceinline__ float h2_lo(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w & 0xffffu))); }
@@ -69,66 +69,83 @@ __device__ __forceinline__ uint32_t keep_pair(uint32_t b, int t, int lead, int n
   return b & ((t < ntok && t >= lead ? 0x0000ffffu : 0u) | (t + 1 < ntok && t + 1 >= lead ? 0xffff0000u : 0u));
 }
 
-constexpr float kPScale = 128.f;      // p enters the products times this
+// p enters the products times 2^7: the exponent is taken against the running offset minus 7.
+constexpr float kPBits = 7.f;
+constexpr int kQ8Rows = 32;           // tokens per stage
 
-__host__ __device__ constexpr size_t q8_smem_bytes(int stages, int stage_bytes) {
-  return 128 + (size_t)stages * (stage_bytes + 16 + 16);
+__host__ __device__ constexpr size_t q8_smem_bytes(int streams, int stages, int stage_bytes) {
+  return 128 + (size_t)streams * stages * (stage_bytes + 16 + 16);
 }
 
-// BSL: log2 of the block size is a runtime value (bs16l = log2(bs / 16)); TT: 16-token tiles per
-// stage; NH n-tiles of 8 heads per consumer warp, MT consumer warps.
-template <int D, int TT, int NH, int MT, bool E4M3>
-__global__ void __launch_bounds__((MT + 1) * 32) decode_q8_kernel(const DecodeArgs a, const int bs16l) {
-  constexpr int KS = D / 16, MD = D / 16, HW = 8 * NH;
+// NH n-tiles of 8 heads per consumer warp, MT consumer warps per stream, NW streams.
+// COMB (groups of up to 4 heads): column n of the n-tile holds head n % 4; columns 0-3 carry the
+// high parts of p and columns 4-7 the low parts, so the pair costs one product.
+template <int D, int NH, int MT, int NW, bool E4M3, bool COMB>
+__global__ void __launch_bounds__((NW * MT + 1) * 32) decode_q8_kernel(const DecodeArgs a, const int sub) {
+  constexpr int KS = D / 16, MD = D / 16, HW = 8 * NH, TT = kQ8Rows / 16;
+  static_assert(!COMB || (NH == 1 && MT == 1), "one n-tile holds the whole group");
   extern __shared__ uint8_t smem_raw[];
-  const uint32_t ring = (smem_u32(smem_raw) + 127u) & ~127u;
-  const int S = a.stages, BS = 16 << bs16l, TPB = 1 << bs16l, NB = TT >> bs16l;
+  const uint32_t ring0 = (smem_u32(smem_raw) + 127u) & ~127u;
+  const int S = a.stages, BS = a.block_size, NB = kQ8Rows / BS;   // BS: 16 or 32 (units of the line)
   const int REC = q8_record_bytes(BS, D), STAGE = NB * REC;
-  uint8_t* smem = smem_raw + (ring - smem_u32(smem_raw));
-  int4* meta = reinterpret_cast<int4*>(smem + (size_t)S * STAGE);
-  uint64_t* full = reinterpret_cast<uint64_t*>(meta + S);
-  uint64_t* empty = full + S;
+  uint8_t* smem = smem_raw + (ring0 - smem_u32(smem_raw));
+  int4* meta = reinterpret_cast<int4*>(smem + (size_t)NW * S * STAGE);
+  uint64_t* full = reinterpret_cast<uint64_t*>(meta + NW * S);
+  uint64_t* empty = full + NW * S;
   __shared__ volatile int abort_flag;
+  __shared__ StreamStart starts[NW];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tig = lane & 3, gid = lane >> 2;
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    for (int i = 0; i < S; ++i) {
+    for (int i = 0; i < NW * S; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], MT);
     }
     fence_barrier_init();
   }
-  __syncthreads();
   if (!a.inline_plan) grid_dep_wait();   // the plan kernel's cum / ctx_eff / cursors
   grid_dep_launch();
-
-  Cursor cur;
-  PieceInfo pi;
-  piece_setup(a, blockIdx.x, gridDim.x, warp == MT, cur, pi);
-  const int p = blockIdx.x;
-  const int len = p < pi.P ? (int)(pi.pend - pi.pstart) : 0;
+  if (warp < NW * MT && warp % MT == 0)
+    stream_setup(a, blockIdx.x * NW + warp / MT, gridDim.x * NW, &starts[warp / MT]);
+  __syncthreads();
   // Every thread waits for the kernel before this one (the append), also those without work,
   // so that no later launch on the stream can pass it.
-  if (len > 0 && warp == MT && lane == 0) prefetch_l2(a.bt + (size_t)cur.s * a.max_blocks + cur.b0 + cur.blk);
   if (a.inline_plan) grid_dep_wait();
-  if (len <= 0) return;
 
-  if (warp == MT) {
+  if (warp == NW * MT) {
     const uint64_t pol = policy_evict_first();
-    produce_piece(a, cur, pi, len, bs16l, NB, S, (uint32_t)REC, 2 * D, meta, full, empty, &abort_flag,
-                  [&](int slot, int k, int phys, int kvh) {
-                    bulk_g2s_u32(ring + (uint32_t)(slot * STAGE + k * REC),
-                                 a.cache + ((size_t)phys * a.n_kv + kvh) * REC, REC, smem_u32(&full[slot]), pol);
-                  });
+    const int big = q8_record_bytes(BS << sub, D);             // bytes of a record of the cache
+    produce_streams(a, starts, NW, S, NB, sub, (uint32_t)REC, 2 * D, meta, full, empty, &abort_flag,
+                    [&](int w, int slot, int k, int phys, int u, int kvh) {
+                      const uint32_t dst = ring0 + (uint32_t)((w * S + slot) * STAGE + k * REC);
+                      const uint32_t bar = smem_u32(&full[w * S + slot]);
+                      const uint8_t* src = a.cache + ((size_t)phys * a.n_kv + kvh) * big;
+                      if (sub == 0) {
+                        bulk_g2s_u32(dst, src, REC, bar, pol);
+                      } else {
+                        const uint32_t half = (uint32_t)(BS * D);
+                        src += (u & 1) * half;
+                        bulk_g2s_u32(dst, src, half, bar, pol);
+                        bulk_g2s_u32(dst + half, src + 2 * half, half, bar, pol);
+                        bulk_g2s_u32(dst + 2 * half, src + (4 - (u & 1)) * half, 16, bar, pol);
+                      }
+                    });
     return;
   }
 
-  // ---------------- consumer warp: local heads [warp * HW, warp * HW + HW) ----------------
+  // ---------------- consumer warp: local heads [warp % MT * HW, + HW) of its stream ----------------
+  const int w = warp / MT;
+  if (starts[w].len <= 0) return;
+  const int p = blockIdx.x * NW + w;
+  const uint32_t ring = ring0 + (uint32_t)(w * S * STAGE);
+  meta += w * S;
+  full += w * S;
+  empty += w * S;
   uint32_t qb[KS][NH][2];
   float o[MD][NH][4];
-  float m[NH][2], l[NH][2], qs[NH][2];          // qs: what a head's scores are multiplied by
-  const int hw0 = warp * HW;
+  float m[NH][2], l[NH][2], qs[NH][2];          // m: running offset - 7; qs: what a head's scores are multiplied by
+  const int hw0 = warp % MT * HW;
   int slot = 0;
   uint32_t phase = 0;
   for (;;) {
@@ -144,16 +161,16 @@ __global__ void __launch_bounds__((MT + 1) * 32) decode_q8_kernel(const DecodeAr
     if (flags & F_FIRST) {
 #pragma unroll
       for (int nh = 0; nh < NH; ++nh) {
-        const int hl = hw0 + nh * 8 + gid;                     // B-fragment column n = gid
+        const int hl = COMB ? gid & 3 : hw0 + nh * 8 + gid;    // B-fragment column n = gid
         const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q) + (qrow0 + hl) * (D / 2);
         float big = 0.f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const uint32_t w = hl < a.G ? __ldg(qp + ks * 8 + 4 * r + tig) : 0u;
-            qb[ks][nh][r] = w;
-            big = fmaxf(big, fmaxf(fabsf(bf16_lo(w)), fabsf(bf16_hi(w))));
+            const uint32_t x = hl < a.G ? __ldg(qp + ks * 8 + 4 * r + tig) : 0u;
+            qb[ks][nh][r] = x;
+            big = fmaxf(big, fmaxf(fabsf(bf16_lo(x)), fabsf(bf16_hi(x))));
           }
         big = fmaxf(big, __shfl_xor_sync(FULL_MASK, big, 1));
         big = fmaxf(big, __shfl_xor_sync(FULL_MASK, big, 2));
@@ -176,69 +193,138 @@ __global__ void __launch_bounds__((MT + 1) * 32) decode_q8_kernel(const DecodeAr
 
     if (flags & F_VALID) {
       const uint32_t st = ring + (uint32_t)(slot * STAGE);
-      const int tiles = (ntok + 15) >> 4;
+      // tile t: in one record of 32 tokens, or the first tile of the t-th of two
+      const uint32_t rec1 = st + (uint32_t)((NB - 1) * REC);
+      const uint32_t kb1 = NB == 2 ? rec1 : st + 16 * D;
+      const bool partial = ntok < kQ8Rows || lead > 0;         // rows [lead, ntok) count
       // ---- S^T = C_k Q^T ----
       float sc[TT][NH][4];
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
+        const uint32_t kb = (t ? kb1 : st) + lane * 16;
 #pragma unroll
         for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
           for (int i = 0; i < 4; ++i) sc[t][nh][i] = 0.f;
-        if (t >= tiles) continue;
-        const uint32_t rec = st + (uint32_t)((t >> bs16l) * REC);
-        const uint32_t kb = rec + (uint32_t)((t & (TPB - 1)) * 16 * D) + lane * 16;
+        if (t && ntok <= 16) continue;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
-          const uint4 w = lds128(kb + j * 512);
+          const uint4 x = lds128(kb + j * 512);
           uint32_t ka[4];
-          codes_f16<E4M3>(w.x, ka[0], ka[2]);
-          codes_f16<E4M3>(w.y, ka[1], ka[3]);
+          codes_f16<E4M3>(x.x, ka[0], ka[2]);
+          codes_f16<E4M3>(x.y, ka[1], ka[3]);
 #pragma unroll
           for (int nh = 0; nh < NH; ++nh) mma_f16(sc[t][nh], ka, qb[2 * j][nh][0], qb[2 * j][nh][1]);
-          codes_f16<E4M3>(w.z, ka[0], ka[2]);
-          codes_f16<E4M3>(w.w, ka[1], ka[3]);
+          codes_f16<E4M3>(x.z, ka[0], ka[2]);
+          codes_f16<E4M3>(x.w, ka[1], ka[3]);
 #pragma unroll
           for (int nh = 0; nh < NH; ++nh) mma_f16(sc[t][nh], ka, qb[2 * j + 1][nh][0], qb[2 * j + 1][nh][1]);
         }
-        const float sk = lds_f32(rec + 2 * BS * D);
-#pragma unroll
-        for (int nh = 0; nh < NH; ++nh) {
-          sc[t][nh][0] *= sk * qs[nh][0];
-          sc[t][nh][1] *= sk * qs[nh][1];
-          sc[t][nh][2] *= sk * qs[nh][0];
-          sc[t][nh][3] *= sk * qs[nh][1];
-        }
       }
-      softmax_tile<TT, NH, MD>(sc, m, l, o, gid, ntok, lead, 1.f);
-      // ---- O^T += s_v C_v^T P^T ----
-      const bool partial = ntok < TT * 16 || lead > 0;
+      float sv[TT];
+      {
+        const float2 s0 = lds_f32x2(st + 2 * BS * D), s1 = lds_f32x2(rec1 + 2 * BS * D);
+        sv[0] = s0.y;
+        sv[1] = s1.y;
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        if (t >= tiles) continue;
-        const uint32_t rec = st + (uint32_t)((t >> bs16l) * REC);
-        const uint32_t vb = rec + (uint32_t)(BS * D + (t & (TPB - 1)) * 16 * D) + lane * 16;
-        const float sv = lds_f32(rec + 2 * BS * D + 4);
-        uint32_t bh[NH][2], bl[NH][2];
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sc[0][nh][i] *= s0.x * qs[nh][i & 1];
+            sc[1][nh][i] *= s1.x * qs[nh][i & 1];
+          }
+      }
+      if (partial) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int tok = t * 16 + gid + 8 * r;
+            if (tok >= ntok || tok < lead)
+#pragma unroll
+              for (int nh = 0; nh < NH; ++nh) sc[t][nh][2 * r] = sc[t][nh][2 * r + 1] = -INFINITY;
+          }
+      }
+      // ---- online softmax over tokens: the offset is raised (to the exact running maximum) only
+      // when a score exceeds it by more than kLazyMax, so p <= 2^8 ----
+      {
+        bool over = false;
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(fmaxf(sc[0][nh][e], sc[0][nh][2 + e]), fmaxf(sc[1][nh][e], sc[1][nh][2 + e]));
+            over |= mx > m[nh][e] + (kLazyMax + kPBits);
+          }
+        if (__any_sync(FULL_MASK, over)) {
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh) {
+            float al[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mx = fmaxf(fmaxf(sc[0][nh][e], sc[0][nh][2 + e]), fmaxf(sc[1][nh][e], sc[1][nh][2 + e]));
+              mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 16));
+              const float mn = fmaxf(m[nh][e], mx - kPBits);
+              al[e] = ex2(m[nh][e] - mn);
+              m[nh][e] = mn;
+              l[nh][e] *= al[e];
+            }
+#pragma unroll
+            for (int md = 0; md < MD; ++md) {
+              o[md][nh][0] *= al[0]; o[md][nh][1] *= al[1];
+              o[md][nh][2] *= al[0]; o[md][nh][3] *= al[1];
+            }
+          }
+        }
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float rs = 0.f;
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const float pv = ex2(sc[t][nh][2 * r + e] - m[nh][e]);
+                sc[t][nh][2 * r + e] = pv;
+                rs += pv;
+              }
+            l[nh][e] += rs;
+          }
+      }
+      // ---- O^T += s_v C_v^T P^T ----
+      uint32_t bh[TT][NH][2], bl[COMB ? 1 : TT][NH][2];
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
 #pragma unroll
         for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float x = sc[t][nh][2 * r] * kPScale, y = sc[t][nh][2 * r + 1] * kPScale;
+            const float x = sc[t][nh][2 * r], y = sc[t][nh][2 * r + 1];
             const uint32_t hi = pack_f16(x, y);
             const uint32_t lo = pack_f16(x - h2_lo(hi), y - h2_hi(hi));
-            bh[nh][r] = movmatrix_t(hi);
-            bl[nh][r] = movmatrix_t(lo);
+            if constexpr (COMB) {
+              bh[t][nh][r] = movmatrix_t(tig < 2 ? hi : lo);
+            } else {
+              bh[t][nh][r] = movmatrix_t(hi);
+              bl[t][nh][r] = movmatrix_t(lo);
+            }
           }
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        if (t && ntok <= 16) continue;
+        const uint32_t vb = (t ? kb1 : st) + BS * D + lane * 16;
         const int t0 = t * 16 + 2 * tig;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
-          const uint4 w = lds128(vb + j * 512);
+          const uint4 x = lds128(vb + j * 512);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t va[4];
-            codes_f16<E4M3>(h ? w.z : w.x, va[0], va[2]);
-            codes_f16<E4M3>(h ? w.w : w.y, va[1], va[3]);
+            codes_f16<E4M3>(h ? x.z : x.x, va[0], va[2]);
+            codes_f16<E4M3>(h ? x.w : x.y, va[1], va[3]);
             if (partial) {
               va[0] = keep_pair(va[0], t0, lead, ntok);
               va[1] = keep_pair(va[1], t0, lead, ntok);
@@ -248,10 +334,10 @@ __global__ void __launch_bounds__((MT + 1) * 32) decode_q8_kernel(const DecodeAr
 #pragma unroll
             for (int nh = 0; nh < NH; ++nh) {
               float acc[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_f16(acc, va, bh[nh][0], bh[nh][1]);
-              mma_f16(acc, va, bl[nh][0], bl[nh][1]);
+              mma_f16(acc, va, bh[t][nh][0], bh[t][nh][1]);
+              if constexpr (!COMB) mma_f16(acc, va, bl[t][nh][0], bl[t][nh][1]);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) o[2 * j + h][nh][i] = fmaf(sv, acc[i], o[2 * j + h][nh][i]);
+              for (int i = 0; i < 4; ++i) o[2 * j + h][nh][i] = fmaf(sv[t], acc[i], o[2 * j + h][nh][i]);
             }
           }
         }
@@ -262,7 +348,13 @@ __global__ void __launch_bounds__((MT + 1) * 32) decode_q8_kernel(const DecodeAr
       const bool whole = flags & F_WHOLE;
       const long long part = (long long)s * a.n_kv + g + p;
 #pragma unroll
-      for (int nh = 0; nh < NH; ++nh)
+      for (int nh = 0; nh < NH; ++nh) {
+        if constexpr (COMB) {                                  // the low parts' columns lie two lanes on
+#pragma unroll
+          for (int md = 0; md < MD; ++md)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[md][nh][i] += __shfl_down_sync(FULL_MASK, o[md][nh][i], 2, 4);
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float L = l[nh][e];
@@ -271,8 +363,8 @@ __global__ void __launch_bounds__((MT + 1) * 32) decode_q8_kernel(const DecodeAr
           L += __shfl_xor_sync(FULL_MASK, L, 16);
           const int hl = hw0 + nh * 8 + 2 * tig + e;           // this thread's head columns
           if (hl >= a.G) continue;
-          const float inv = (whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f) * (1.f / kPScale);
           if (whole) {
+            const float inv = L > 0.f ? 1.f / L : 0.f;
             const size_t base = (qrow0 + hl) * D;
             if (a.out_f32) {
               float* out = reinterpret_cast<float*>(a.out) + base;
@@ -293,13 +385,14 @@ __global__ void __launch_bounds__((MT + 1) * 32) decode_q8_kernel(const DecodeAr
             float* wo = a.ws_o + ((size_t)part * a.G + hl) * D;
 #pragma unroll
             for (int md = 0; md < MD; ++md) {
-              wo[md * 16 + gid] = o[md][nh][e] * inv;
-              wo[md * 16 + gid + 8] = o[md][nh][2 + e] * inv;
+              wo[md * 16 + gid] = o[md][nh][e];
+              wo[md * 16 + gid + 8] = o[md][nh][2 + e];
             }
             if (gid == 0)
               *reinterpret_cast<float2*>(a.ws_ml + ((size_t)part * a.G + hl) * 2) = make_float2(m[nh][e], L);
           }
         }
+      }
     }
 
     __syncwarp();
@@ -315,47 +408,55 @@ __global__ void __launch_bounds__((MT + 1) * 32) decode_q8_kernel(const DecodeAr
 // ---------------------------------------------------------------------------------------------
 struct Q8Variant {
   const void* fn;
-  int stages, warps, P;
+  int stages, warps, streams, P;
   size_t smem;
 };
 
-constexpr int kQ8Tiles = 4;           // 64 tokens per stage, whatever the block size
-
 constexpr size_t kQ8MaxSmem = 200 * 1024;
 
-template <int D, int NH, int MT, bool E4M3>
-static const void* q8_fn() {
-  return (const void*)decode_q8_kernel<D, kQ8Tiles, NH, MT, E4M3>;
+// Three streams and their producer warp fill an SM's registers at four CTAs of 128 registers: 12
+// consumer warps.  32/8 heads of 128, 64 sequences of 512-4096 tokens in e4m3 / 32 of 8-32K in int8:
+// 55.1 / 205 us (81% / 96% of the measured copy rate), with four streams 55.3 / 208, with six 56.4 /
+// 218; a producer warp per consumer warp and 64-token stages (six consumers per SM) took 72.7 / 324.
+// A third stage costs consumers their shared memory: 55.7 / 212.
+template <int D, bool E4M3>
+static void q8_pick(int G, Q8Variant& v) {
+  auto set = [&](const void* fn, int mt, int nw) {
+    v.fn = fn;
+    v.streams = nw;
+    v.warps = nw * mt + 1;
+  };
+  if (G <= 4) set((const void*)decode_q8_kernel<D, 1, 1, 3, E4M3, true>, 1, 3);
+  else if (G <= 8) set((const void*)decode_q8_kernel<D, 1, 1, 3, E4M3, false>, 1, 3);
+  else if (G <= 16) set((const void*)decode_q8_kernel<D, 1, 2, 3, E4M3, false>, 2, 3);
+  else if (G <= 32) set((const void*)decode_q8_kernel<D, 2, 2, 2, E4M3, false>, 2, 2);
+  else set((const void*)decode_q8_kernel<D, 2, 4, 1, E4M3, false>, 4, 1);
 }
+static int q8_variant_index(int G) { return G <= 4 ? 0 : head_tiling(G) + 1; }
 
-static Q8Variant* lookup_q8(int D, int BS, int tiling, bool e4m3) {
+static Q8Variant* lookup_q8(int D, int BS, int G, bool e4m3) {
   // One table per process; the library drives one device per process.
   static std::mutex mu;
-  static Q8Variant table[2][3][4][2];
-  static bool ready[2][3][4][2] = {};
-  const int di = D == 128 ? 1 : 0, bi = BS == 16 ? 0 : (BS == 32 ? 1 : 2), fi = e4m3 ? 1 : 0;
+  static Q8Variant table[2][2][5][2];
+  static bool ready[2][2][5][2] = {};
+  const int di = D == 128 ? 1 : 0, bi = BS == 16 ? 0 : 1, vi = q8_variant_index(G), fi = e4m3 ? 1 : 0;
   std::lock_guard<std::mutex> lock(mu);
-  Q8Variant& v = table[di][bi][tiling][fi];
-  if (!ready[di][bi][tiling][fi]) {
-#define PKV_V(d, f)                                                                                        \
-  if (D == d && e4m3 == f)                                                                                 \
-    v.fn = tiling == 0 ? q8_fn<d, 1, 1, f>()                                                               \
-                       : (tiling == 1 ? q8_fn<d, 1, 2, f>() : (tiling == 2 ? q8_fn<d, 2, 2, f>() : q8_fn<d, 2, 4, f>()));
-    PKV_V(64, true) PKV_V(64, false) PKV_V(128, true) PKV_V(128, false)
-#undef PKV_V
-    v.warps = (tiling == 0 ? 1 : (tiling == 3 ? 4 : 2)) + 1;
-    const int stage = (kQ8Tiles * 16 / BS) * q8_record_bytes(BS, D);
-    v.stages = ring_stages(stage, 32768, "PKV_STAGES_Q8");
-    v.smem = q8_smem_bytes(v.stages, stage);
-    // one function serves several block sizes, whose rings differ a little: one limit for all
+  Q8Variant& v = table[di][bi][vi][fi];
+  if (!ready[di][bi][vi][fi]) {
+    if (D == 128) e4m3 ? q8_pick<128, true>(G, v) : q8_pick<128, false>(G, v);
+    else e4m3 ? q8_pick<64, true>(G, v) : q8_pick<64, false>(G, v);
+    const int unit = BS == 16 ? 16 : 32, stage = kQ8Rows / unit * q8_record_bytes(unit, D);
+    v.stages = ring_stages(stage, 2 * stage, "PKV_STAGES_Q8");
+    v.smem = q8_smem_bytes(v.streams, v.stages, stage);
+    // one function serves all block sizes, whose rings differ a little: one limit for all
     if (v.smem > kQ8MaxSmem ||
         cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kQ8MaxSmem) != cudaSuccess)
       return nullptr;
     int occ = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, v.fn, v.warps * 32, v.smem) != cudaSuccess || occ < 1)
       return nullptr;
-    v.P = device_sm_count() * occ;
-    ready[di][bi][tiling][fi] = true;
+    v.P = device_sm_count() * occ * v.streams;
+    ready[di][bi][vi][fi] = true;
   }
   return &v;
 }
@@ -376,7 +477,7 @@ extern "C" size_t pkv_q8_workspace_bytes(int batch, int n_h, int n_kv, int head_
   if (batch < 0 || !valid_shape(n_h, n_kv, head_dim, block_size)) return 0;
   if (format != PKV_Q8_E4M3 && format != PKV_Q8_INT8) return 0;
   const int G = n_h / n_kv;
-  Q8Variant* v = lookup_q8(head_dim, block_size, head_tiling(G), format == PKV_Q8_E4M3);
+  Q8Variant* v = lookup_q8(head_dim, block_size, G, format == PKV_Q8_E4M3);
   return v ? workspace_layout(batch, n_kv, G, head_dim, v->P).total : 0;
 }
 
@@ -395,7 +496,7 @@ extern "C" pkv_status pkv_paged_decode_attn_q8(const void* q, const uint8_t* cac
   if (!al16(q) || !al16(cache) || !al16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PKV_EINVAL;
   if ((long long)max_blocks * block_size > 0x7fffffffLL) return PKV_ERANGE;
   const int G = n_h / n_kv;
-  Q8Variant* v = lookup_q8(head_dim, block_size, head_tiling(G), format == PKV_Q8_E4M3);
+  Q8Variant* v = lookup_q8(head_dim, block_size, G, format == PKV_Q8_E4M3);
   if (!v) {
     record_cuda_error(cudaGetLastError());
     return PKV_ECUDA;
@@ -411,7 +512,8 @@ extern "C" pkv_status pkv_paged_decode_attn_q8(const void* q, const uint8_t* cac
   a.ctx_eff = reinterpret_cast<int32_t*>(ws + wl.ctx);
   a.ctx_raw = context_lens;
   a.max_ctx = max_blocks * block_size;
-  a.block_size = block_size;
+  const int unit = block_size == 16 ? 16 : 32;                // blocks of 64 tokens count as two units of 32
+  a.block_size = unit;
   a.inline_plan = batch <= kInlinePlanSeqs;
   a.pieces = reinterpret_cast<int4*>(ws + wl.pieces);
   a.P_launch = v->P;
@@ -430,12 +532,12 @@ extern "C" pkv_status pkv_paged_decode_attn_q8(const void* q, const uint8_t* cac
   a.window = window;
   a.cache = cache;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int bs16l = block_size == 16 ? 0 : (block_size == 32 ? 1 : 2);
+  int sub = block_size == 64 ? 1 : 0;
   cudaError_t e = a.inline_plan ? cudaSuccess
-                                : launch_plan(context_lens, batch, max_blocks * block_size, block_size, a, v->P, st);
+                                : launch_plan(context_lens, batch, max_blocks * block_size, unit, a, v->P, st);
   if (e == cudaSuccess) {
-    void* kargs[] = {&a, &bs16l};
-    e = launch_pdl(v->fn, dim3(v->P), dim3(v->warps * 32), v->smem, st, kargs);
+    void* kargs[] = {&a, &sub};
+    e = launch_pdl(v->fn, dim3(v->P / v->streams), dim3(v->warps * 32), v->smem, st, kargs);
   }
   if (e == cudaSuccess) e = launch_reduce(head_dim, a, v->P, st);
   if (e != cudaSuccess) {
