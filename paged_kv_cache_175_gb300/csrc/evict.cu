@@ -8,16 +8,18 @@
 // in parallel, sources being at or behind K and destinations below it.  What is newest is known
 // from the positions: rows below `kept` have theirs recorded, later rows follow `dropped`.
 //
-// Select kernel: a cluster of CTAs per (sequence, kv head), each holding the keys of an equal
-// run of rows in shared memory (recent rows: the largest key; else the account's bits in an
-// order-keeping form), so the accounts are read once.  Three rounds over 11, 11 and 10 bits of
-// the key build histograms in shared memory, sum them over the cluster through distributed
-// shared memory and narrow the K-th largest key; two ordered scans then give every hole and
-// every mover its place.  Runs longer than the shared memory are read again from L2 per round.
+// Select kernel: a cluster of CTAs per (sequence, kv head), each thread holding the keys of R
+// consecutive rows in registers (recent rows: the largest key; else the account's bits in an
+// order-keeping form), so the accounts are read once, all loads of a thread in flight together.
+// Three rounds over 11, 11 and 10 bits of the key build histograms in shared memory, sum them over
+// the cluster through distributed shared memory and narrow the K-th largest key; one ordered scan
+// then gives every hole and every mover its place in the list (two, when rows with the K-th key
+// have to be told apart).  Rows too many for a cluster's registers (over 131072) are read again in
+// every round.
 // Move kernel: the listed rows of K and V, 16 bytes a lane, spread over the whole GPU.
 //
-// What bounds it: the select kernel, latency (three histogram rounds with cluster barriers over
-// a few KB to MB of accounts); the move kernel, HBM (4 d bytes read and written per moved row).
+// What bounds it: the select kernel, latency (three histogram rounds over a few KB to MB of
+// accounts); the move kernel, HBM (4 d bytes read and written per moved row).
 #include <cooperative_groups.h>
 
 #include <cmath>
@@ -45,13 +47,11 @@ struct EvictArgs {
   int max_moves;
   uint4 *k_pool, *v_pool;
   int32_t* err;
-  int staged;                    // keys a CTA holds in shared memory (0: none)
-  int in_place;
+  int in_place, vec;
 };
 
-constexpr int kEvThreads = 1024;
 constexpr int kEvBins = 2048;
-constexpr int kEvWarps = kEvThreads / 32;
+constexpr int kEvRows = 16;                                   // rows per thread
 
 // Order-keeping bits of an account: -0 below +0, NaN above everything but the recent rows.
 __device__ __forceinline__ uint32_t order_bits(float x) {
@@ -61,36 +61,48 @@ __device__ __forceinline__ uint32_t order_bits(float x) {
 }
 
 // Exclusive prefix sum of x over the CTA's threads, in thread order; total gets the sum.
-__device__ __forceinline__ int cta_scan(int x, int* warp_s, int& total) {
+template <int NT, class T>
+__device__ __forceinline__ T cta_scan(T x, T* warp_s, T& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = x;
+  T incl = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(FULL_MASK, incl, o);
+    const T y = __shfl_up_sync(FULL_MASK, incl, o);
     if (lane >= o) incl += y;
   }
   __syncthreads();                                            // warp_s may still be read from the last scan
   if (lane == 31) warp_s[warp] = incl;
   __syncthreads();
-  int before = 0, all = 0;
+  // lane w holds warp w's sum; the warps before this one add up by a masked reduction
+  const T v = lane < NT / 32 ? warp_s[lane] : 0;
+  T before = lane < warp ? v : 0, all = v;
 #pragma unroll
-  for (int w = 0; w < kEvWarps; ++w) {
-    const int v = warp_s[w];
-    if (w < warp) before += v;
-    all += v;
+  for (int o = 16; o; o >>= 1) {                              // over the whole warp: every lane gets the sums
+    before += __shfl_xor_sync(FULL_MASK, before, o);
+    all += __shfl_xor_sync(FULL_MASK, all, o);
   }
   total = all;
   return before + incl - x;
 }
 
-__global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const EvictArgs a) {
+template <bool SMALL> struct PairOf { using type = uint32_t; };
+template <> struct PairOf<false> { using type = unsigned long long; };
+
+// NT threads of R rows, R a multiple of 4 (0: any number, keys read again whenever they are used).
+template <int NT, int R>
+__global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) evict_select_kernel(const EvictArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-  extern __shared__ uint32_t keys[];
-  __shared__ int hist[kEvBins];
-  __shared__ int warp_s[kEvWarps];
-  __shared__ int share[4];                                    // this CTA's counts, read by the cluster
-  __shared__ int pick[2];
+  // with R > 0 a bin counts at most 16384 rows of the CTA: two bins to a word
+  constexpr int kPack = R > 0 ? 1 : 0;
+  __shared__ __align__(16) uint32_t hist[2][kEvBins >> kPack];
+  // holes and movers travel together, a half of a word each: rows of a CTA fit 15 bits with R > 0
+  using Pair = typename PairOf<(R > 0)>::type;
+  constexpr int kHalf = 4 * sizeof(Pair);
+  __shared__ Pair warp_s[NT / 32];
+  __shared__ int sums_s[NT / 32];
+  __shared__ Pair share[2];                                   // this CTA's counts, read by the cluster
+  __shared__ int pick[3];
   const int sg = blockIdx.x / ranks, s = sg / a.n_kv;
   const int raw = a.ctx[s], n = clamp_ctx(raw, a.max_ctx);
   const int K = max(0, min(a.keep[s], n));
@@ -99,134 +111,258 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const EvictArg
   const int32_t* posn = a.positions + (size_t)sg * a.stride;
   float* mass_out = a.mass_out + (size_t)sg * a.stride;
   int32_t* pos_out = a.positions_out + (size_t)sg * a.stride;
-  const int per = ((n + ranks - 1) / ranks + 3) & ~3;         // rows of a CTA
-  const int r0 = min(n, rank * per), r1 = min(n, r0 + per), rows = r1 - r0;
   if (rank == 0 && sg % a.n_kv == 0 && threadIdx.x == 0) {
     if (raw != n) set_err(a.err, PKV_DEV_BAD_CTX);
     // here and not in the move kernel: an attention call behind this one may read the lengths
     // while the move kernel still runs
     a.new_lens[s] = K;
   }
+  // this thread's rows
+  const int each = R > 0 ? R : (n + ranks * NT - 1) / (ranks * NT);
+  const int r0 = min((long long)n, (long long)(rank * NT + (int)threadIdx.x) * each), r1 = min(n, r0 + each);
 
   if (K == n) {                                               // nothing to evict (uniform in the cluster)
     if (rank == 0 && threadIdx.x == 0) a.counts[sg] = 0;
     if (!a.in_place)
-      for (int r = r0 + threadIdx.x; r < r1; r += kEvThreads) {
+      for (int r = rank * NT + threadIdx.x; r < n; r += ranks * NT) {
         mass_out[r] = mass[r];
         if (r < kept) pos_out[r] = posn[r];
       }
     return;
   }
-  // rows at or behind this position are recent: the newest is dropped + n - 1
+  // rows at or behind this position are recent: the newest token is dropped + n - 1
   const int recent_from = dropped + n - min(a.recent, K);
   auto position = [&](int r) { return r < kept ? posn[r] : dropped + r; };
   auto make_key = [&](int r) { return position(r) >= recent_from ? 0xffffffffu : order_bits(mass[r]); };
-  const bool staged = rows <= a.staged;
-  if (staged)
-    for (int i = threadIdx.x; i < rows; i += kEvThreads) keys[i] = make_key(r0 + i);
-  auto key = [&](int i) { return staged ? keys[i] : make_key(r0 + i); };   // i counts from r0
+  uint32_t keys[R > 0 ? R : 1];
+  if constexpr (R > 0) {
+    const bool vec = a.vec != 0;                              // rows of the state are 16-byte aligned
+    float x[R];
+#pragma unroll
+    for (int i = 0; i < R; i += 4) {
+      if (vec && r0 + i + 4 <= r1) {
+        const float4 v = *reinterpret_cast<const float4*>(mass + r0 + i);
+        x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[i + j] = r0 + i + j < r1 ? mass[r0 + i + j] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < R; i += 4) {
+      int p[4];
+      if (vec && r0 + i + 4 <= min(r1, kept)) {
+        const int4 v = *reinterpret_cast<const int4*>(posn + r0 + i);
+        p[0] = v.x; p[1] = v.y; p[2] = v.z; p[3] = v.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[j] = r0 + i + j < r1 ? position(r0 + i + j) : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) keys[i + j] = p[j] >= recent_from ? 0xffffffffu : order_bits(x[i + j]);
+    }
+  }
+  // f(row, key) for this thread's rows in order
+  auto rows = [&](auto f) {
+    if constexpr (R > 0) {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (r0 + i < r1) f(r0 + i, keys[i]);
+    } else {
+      for (int r = r0; r < r1; ++r) f(r, make_key(r));
+    }
+  };
+  auto meet = [&]() {                                         // barrier of the cluster
+    if (ranks == 1) __syncthreads();
+    else cluster.sync();
+  };
 
   // ---- the K-th largest key: 11 + 11 + 10 bits from the top ----
   uint32_t prefix = 0, mask = 0;
-  int want = K;                                               // rank of the wanted key among those matching prefix
+  int want = K;                                               // of the keys that match prefix, the wanted one's rank
+  bool all_equal = true;                                      // every row with the K-th key is kept
   if (K > 0) {
-#pragma unroll 1
+    for (int b = threadIdx.x; b < 2 * (kEvBins >> kPack); b += NT) hist[0][b] = 0;
+    __syncthreads();
+#pragma unroll
     for (int round = 0; round < 3; ++round) {
-      const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0), bins = round == 2 ? 1024 : 2048;
-      for (int b = threadIdx.x; b < bins; b += kEvThreads) hist[b] = 0;
-      __syncthreads();
-      for (int i0 = 0; i0 < rows; i0 += kEvThreads) {
-        const int i = i0 + threadIdx.x;
-        const uint32_t k = i < rows ? key(i) : 0;
-        if (i < rows && (k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
-      }
-      cluster.sync();
-      // thread t: bins from the top, 2 t and 2 t + 1 (1024 bins: bin t)
-      const int nb = bins / kEvThreads;
-      int c[2] = {0, 0};
-      for (int q = 0; q < ranks; ++q) {
-        const int* h = cluster.map_shared_rank(hist, q);
-        for (int j = 0; j < nb; ++j) c[j] += h[bins - 1 - (threadIdx.x * nb + j)];
-      }
-      int total;
-      const int before = cta_scan(c[0] + c[1], warp_s, total);
-      for (int j = 0, at = before; j < nb; at += c[j], ++j)
-        if (at < want && want <= at + c[j]) {
-          pick[0] = bins - 1 - (threadIdx.x * nb + j);
-          pick[1] = want - at;
+      constexpr int kShift[3] = {21, 10, 0};
+      const int shift = kShift[round], bins = round == 2 ? 1024 : 2048;
+      uint32_t* h = hist[round & 1];
+      rows([&](int, uint32_t k) {
+        const uint32_t b = (k >> shift) & (bins - 1);
+        if ((k & mask) == prefix) atomicAdd(&h[b >> kPack], kPack ? 1u << (16 * (b & 1)) : 1u);
+      });
+      meet();
+      // buffer of the next round but one: its last readers passed the barrier above
+      if (round == 1)
+        for (int b = threadIdx.x; b < (1024 >> kPack); b += NT) hist[0][b] = 0;
+      // warp w takes the w-th run of bins from the top and lane l the l-th run of those; only the
+      // warp that holds the wanted rank looks for its bin
+      constexpr int kRun[3] = {2048 / NT, 2048 / NT, 1024 / NT};
+      const int nb = kRun[round], b0 = bins - nb * ((int)threadIdx.x + 1);
+      int c[kRun[0]] = {};
+      const int w0 = b0 >> kPack, nw = kPack ? (nb + 1) / 2 : nb;   // words of the run
+      auto add = [&](int j, uint32_t v) {
+        if (!kPack) c[j] += (int)v;
+        else if (nb == 1) c[0] += (int)(v >> (16 * (b0 & 1)) & 0xffffu);
+        else {
+          c[2 * j] += (int)(v & 0xffffu);
+          c[2 * j + 1] += (int)(v >> 16);
         }
-      cluster.sync();                                         // all have read the histograms; pick is set
+      };
+      if (ranks == 1) {
+#pragma unroll
+        for (int j = 0; j < nw; ++j) add(j, h[w0 + j]);
+      } else {
+        constexpr int kGroup = NT == 1024 ? 8 : 4;            // CTAs whose loads are in flight together
+        for (int q0 = 0; q0 < ranks; q0 += kGroup) {
+          uint32_t d[kGroup][kRun[0]];
+#pragma unroll
+          for (int q = 0; q < kGroup; ++q) {
+            const uint32_t* hq = cluster.map_shared_rank(h, q0 + q < ranks ? q0 + q : 0);
+#pragma unroll
+            for (int j = 0; j < nw; ++j) d[q][j] = q0 + q < ranks ? hq[w0 + j] : 0u;
+          }
+#pragma unroll
+          for (int q = 0; q < kGroup; ++q)
+#pragma unroll
+            for (int j = 0; j < nw; ++j) add(j, d[q][j]);
+        }
+      }
+      int sum = 0;
+#pragma unroll
+      for (int j = 0; j < nb; ++j) sum += c[j];
+      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+      const int warp_sum = __reduce_add_sync(FULL_MASK, sum);
+      if (lane == 0) sums_s[warp] = warp_sum;
+      __syncthreads();
+      const int ahead = __reduce_add_sync(FULL_MASK, lane < warp ? sums_s[lane] : 0);
+      if (ahead < want && want <= ahead + warp_sum) {
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(FULL_MASK, incl, o);
+          if (lane >= o) incl += y;
+        }
+        int at = ahead + incl - sum;
+#pragma unroll
+        for (int j = nb - 1; j >= 0; --j) {
+          if (at < want && want <= at + c[j]) {
+            pick[0] = b0 + j;
+            pick[1] = want - at;
+            pick[2] = c[j];
+          }
+          at += c[j];
+        }
+      }
+      __syncthreads();
       prefix |= (uint32_t)pick[0] << shift;
       mask |= (uint32_t)(bins - 1) << shift;
       want = pick[1];
+      all_equal = pick[1] == pick[2];
     }
   }
   // prefix is the K-th largest key; of the rows equal to it the `want` lowest are kept
 
-  // ---- ordered scans: thread t takes the rows [t * each, t * each + each) of the CTA ----
-  const int each = (rows + kEvThreads - 1) / kEvThreads | 1;  // odd: threads start in distinct banks
-  const int b0 = min(rows, (int)threadIdx.x * each), b1 = min(rows, b0 + each);
-  auto cluster_before = [&](int slot) {                       // sum of share[slot] over the CTAs before this one
-    int x = 0;
-    for (int q = 0; q < rank; ++q) x += cluster.map_shared_rank(share, q)[slot];
-    return x;
-  };
-  int equal = 0, total;
-  if (K > 0)
-    for (int i = b0; i < b1; ++i) equal += key(i) == prefix;
-  int eq_at = cta_scan(equal, warp_s, total);
-  if (threadIdx.x == 0) share[0] = total;
-  cluster.sync();
-  eq_at += cluster_before(0);
-  int holes = 0, movers = 0;
-  {
-    int e = eq_at;
-    for (int i = b0; i < b1; ++i) {
-      const uint32_t k = key(i);
-      const bool stays = K > 0 && (k > prefix || (k == prefix && e < want));
-      e += K > 0 && k == prefix;
-      if (r0 + i < K) holes += !stays; else movers += stays;
+  // ---- ordered scans ----
+  auto widen = [](Pair v) { return (uint64_t)(v >> kHalf) << 32 | (uint32_t)(v & (((Pair)1 << kHalf) - 1)); };
+  // sums of share[slot] over the CTAs before this one and over all: lane q asks CTA q
+  auto over_cluster = [&](int slot, uint64_t& all) {
+    const int lane = threadIdx.x & 31;
+    const uint64_t v = lane < ranks ? widen(cluster.map_shared_rank(share, lane)[slot]) : 0;
+    uint64_t x = lane < rank ? v : 0;
+    all = v;
+#pragma unroll
+    for (int o = 4; o; o >>= 1) {
+      x += __shfl_xor_sync(FULL_MASK, x, o);
+      all += __shfl_xor_sync(FULL_MASK, all, o);
     }
+    all = __shfl_sync(FULL_MASK, all, 0);
+    return __shfl_sync(FULL_MASK, x, 0);                       // at most eight CTAs: lanes 0-7 hold them
+  };
+  Pair total;
+  int e0 = 0;                                                 // rows with the K-th key before this thread's
+  if (K > 0 && !all_equal) {
+    Pair equal = 0;
+    rows([&](int, uint32_t k) { equal += k == prefix; });
+    e0 = (int)cta_scan<NT, Pair>(equal, warp_s, total);
+    if (threadIdx.x == 0) share[0] = total;
+    meet();
+    uint64_t all;
+    if (ranks > 1) e0 += (int)over_cluster(0, all);
   }
-  int h_at = cta_scan(holes, warp_s, total);
-  if (threadIdx.x == 0) share[1] = total;
-  int m_at = cta_scan(movers, warp_s, total);
-  if (threadIdx.x == 0) share[2] = total;
-  cluster.sync();
-  h_at += cluster_before(1);
-  m_at += cluster_before(2);
-  int n_moves = 0;
-  for (int q = 0; q < ranks; ++q) n_moves += cluster.map_shared_rank(share, q)[2];
-  int2* moves = a.moves + (size_t)sg * a.max_moves;
-  {
-    int e = eq_at;
-    for (int i = b0; i < b1; ++i) {
-      const uint32_t k = key(i);
-      const bool stays = K > 0 && (k > prefix || (k == prefix && e < want));
-      e += K > 0 && k == prefix;
-      if (r0 + i < K) {
-        if (!stays) moves[h_at++].x = r0 + i;
-      } else if (stays) {
-        moves[m_at++].y = r0 + i;
+  int e = e0;
+  auto stays = [&](uint32_t k) {                              // rows asked in order
+    if (K == 0) return false;
+    return k > prefix || (k == prefix && (all_equal || e++ < want));
+  };
+  Pair mine = 0;                                              // holes, and movers in the high half
+  uint32_t hole_bits = 0, mover_bits = 0;                     // of this thread's rows (R > 0)
+  if constexpr (R > 0) {
+    uint32_t st = 0;
+    if (K > 0) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) st |= (keys[i] >= prefix ? 1u : 0u) << i;
+      if (!all_equal) {                                       // of the equal rows only the first `want` of all
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (keys[i] == prefix && r0 + i < r1 && e++ >= want) st &= ~(1u << i);
       }
     }
+    auto low = [](int c) { return c >= R ? (R == 32 ? 0xffffffffu : (1u << R) - 1u) : (c <= 0 ? 0u : (1u << c) - 1u); };
+    const uint32_t valid = low(r1 - r0), below = low(K - r0);
+    hole_bits = valid & below & ~st;
+    mover_bits = valid & ~below & st;
+    mine = (Pair)__popc(hole_bits) | (Pair)__popc(mover_bits) << kHalf;
+  } else {
+    rows([&](int r, uint32_t k) {
+      const bool st = stays(k);
+      mine += r < K ? (Pair)!st : (Pair)st << kHalf;
+    });
   }
-  if (rank == 0 && threadIdx.x == 0) a.counts[sg] = n_moves;
-  // rows below K that stay: their accounts and positions (a hole's come with its mover)
-  for (int r = r0 + threadIdx.x; r < min(r1, K); r += kEvThreads) {
+  const Pair local = cta_scan<NT, Pair>(mine, warp_s, total);
+  uint64_t at = widen(local), moves_all = widen(total);
+  if (ranks > 1) {
+    if (threadIdx.x == 0) share[1] = total;
+    meet();
+    at += over_cluster(1, moves_all);
+  }
+  if (rank == 0 && threadIdx.x == 0) a.counts[sg] = (int)(moves_all >> 32);
+  int2* moves = a.moves + (size_t)sg * a.max_moves;
+  uint32_t h_at = (uint32_t)at, m_at = (uint32_t)(at >> 32);
+  if constexpr (R > 0) {
+    for (; hole_bits; hole_bits &= hole_bits - 1) moves[h_at++].x = r0 + __ffs(hole_bits) - 1;
+    for (; mover_bits; mover_bits &= mover_bits - 1) moves[m_at++].y = r0 + __ffs(mover_bits) - 1;
+  } else {
+    e = e0;
+    rows([&](int r, uint32_t k) {
+      const bool st = stays(k);
+      if (r < K) {
+        if (!st) moves[h_at++].x = r;
+      } else if (st) {
+        moves[m_at++].y = r;
+      }
+    });
+  }
+  // rows below K: accounts and positions (those of the holes are written again below)
+#pragma unroll 4
+  for (int r = (a.in_place ? kept : 0) + rank * NT + threadIdx.x; r < K; r += ranks * NT) {
     if (!a.in_place) mass_out[r] = mass[r];
-    if (!a.in_place || r >= kept) pos_out[r] = position(r);
+    pos_out[r] = position(r);
   }
-  __threadfence();
-  cluster.sync();                                             // the lists are whole, the rows below K written
-  for (int i = rank * kEvThreads + threadIdx.x; i < n_moves; i += ranks * kEvThreads) {
+  meet();                                                     // the list is whole; no shared memory is read from here on
+  const int n_moves = (int)(moves_all >> 32);
+#pragma unroll 4
+  for (int i = rank * NT + threadIdx.x; i < n_moves; i += ranks * NT) {
     const int2 mv = moves[i];
-    mass_out[mv.x] = mass[mv.y];
-    pos_out[mv.x] = position(mv.y);
+    const float x = mass[mv.y];
+    const int p = position(mv.y);
+    mass_out[mv.x] = x;
+    pos_out[mv.x] = p;
   }
-  if (a.in_place) cluster.sync();                             // every mover's account was read
-  for (int r = max(r0, K) + threadIdx.x; r < r1; r += kEvThreads) mass_out[r] = 0.f;
-  cluster.sync();                                             // no CTA leaves while its shared memory is read
+  if (a.in_place) meet();                                     // every mover's account was read
+  for (int r = K + rank * NT + threadIdx.x; r < n; r += ranks * NT) mass_out[r] = 0.f;
 }
 
 // Moves the listed rows.  CTAs [sg * split, sg * split + split) share the list of one
@@ -296,8 +432,6 @@ static EvictLayout evict_layout(int batch, int n_kv, long long max_ctx) {
   return w;
 }
 
-constexpr int kEvStaged = 48 * 1024;                          // keys in shared memory per CTA at most
-
 }  // namespace pkv
 
 using namespace pkv;
@@ -358,32 +492,29 @@ extern "C" pkv_status pkv_kv_evict(void* k_pool, void* v_pool, const int32_t* bl
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int sms = device_sm_count() > 0 ? device_sm_count() : 128;
   const long long pairs = (long long)batch * n_kv;
-  // CTAs per (sequence, kv head): enough for about 4096 rows each, while the grid stays within
-  // two CTAs per SM; longer rows still take a cluster of up to eight
+  a.vec = stride % 4 == 0 && !((reinterpret_cast<uintptr_t>(mass) | reinterpret_cast<uintptr_t>(positions)) & 15u);
+  // CTAs per (sequence, kv head): of 256 threads (4096 rows, four CTAs per SM), as many as it takes
+  // while all of them are resident; else of 1024 threads (16384 rows); at most eight
   int ranks = 1;
-  while (ranks < 8 && max_ctx > 4096LL * ranks && (pairs * ranks * 2 <= 2LL * sms || max_ctx > (long long)kEvStaged * ranks)) ranks *= 2;
-  long long staged = ((max_ctx + ranks - 1) / ranks + 3) & ~3LL;
-  if (staged > kEvStaged) staged = 0;
-  a.staged = (int)staged;
-  const size_t smem = (size_t)staged * sizeof(uint32_t);
-  cudaError_t e = cudaFuncSetAttribute((const void*)evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kEvStaged * (int)sizeof(uint32_t));
-  if (e == cudaSuccess) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(pairs * ranks));
-    cfg.blockDim = dim3(kEvThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ranks;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    void* kargs[] = {&a};
-    e = cudaLaunchKernelExC(&cfg, (const void*)evict_select_kernel, kargs);
-  }
+  while (ranks < 8 && max_ctx > 256LL * kEvRows * ranks && (pairs * ranks * 2 <= 4LL * sms || max_ctx > 1024LL * kEvRows * ranks))
+    ranks *= 2;
+  const bool small = max_ctx <= 256LL * kEvRows * ranks;
+  const void* fn = small ? (const void*)evict_select_kernel<256, kEvRows>
+                         : (max_ctx <= 1024LL * kEvRows * ranks ? (const void*)evict_select_kernel<1024, kEvRows>
+                                                                : (const void*)evict_select_kernel<1024, 0>);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(pairs * ranks));
+  cfg.blockDim = dim3(small ? 256 : 1024);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ranks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* sargs[] = {&a};
+  cudaError_t e = cudaLaunchKernelExC(&cfg, fn, sargs);
   if (e == cudaSuccess) {
     long long split = (16LL * sms + pairs - 1) / pairs;       // about 16 CTAs per SM
     const long long most = (w.max_moves + 31) / 32;
