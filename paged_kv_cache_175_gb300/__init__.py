@@ -375,15 +375,22 @@ def rope_table(head_dim, rotary_dim=None, base=10000.0, interleaved=False, scali
     return t
 
 
+# The calls below check their arguments in one expression first (a call of a few microseconds on the
+# GPU should not wait for its checks); where it is false, the checks that follow name the mistake.
+_bf16, _f32, _i32, _i64, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda d: torch.cuda.current_stream(d).cuda_stream)
+
+
 def _on_current(*ts):
-    """All tensors (None is skipped) on the current CUDA device; returns its index."""
+    """All tensors (None is skipped) on the current CUDA device."""
     if not ts[0].is_cuda:
         raise PkvError("tensors must be CUDA tensors")
     d = torch.cuda.current_device()
     for t in ts:
         if t is not None and t.get_device() != d:             # -1 for a CPU tensor
             raise PkvError("tensors must be on the current CUDA device")
-    return d
 
 
 def _dense(*ts):
@@ -403,102 +410,128 @@ def _shaped(what, t, *shape):
         raise PkvError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
 
 
-def _heads(t):
-    """Token stride of a [n_tok][heads][head_dim] tensor whose heads are dense."""
-    if t.dim() != 3:
-        raise PkvError("expected a [tokens][heads][head_dim] tensor")
-    n, h, d = t.shape
-    if n and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
+def _dims(what, t, n):
+    if t.dim() != n:
+        raise PkvError(f"{what} must have {n} dimensions, got {t.dim()}")
+    return t.shape
+
+
+def _head_dense(t):
+    """The heads of a token of [n_tok][heads][head_dim] are contiguous (tokens may be strided)."""
+    _, h, d = t.shape
+    if t.numel() and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
         raise PkvError("the heads of a token must be contiguous")
-    return t.stride(0) if n > 1 else h * d
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(stream, device):
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
+def _err_ok(err, dev):
+    return err is None or (err.dtype is _i32 and err.get_device() == dev)
 
 
-def _scratch(workspace, nbytes, device, stream):
-    """The caller's workspace, or one of nbytes() that stays alive for the work on `stream`."""
-    if workspace is not None:
-        _dense(workspace)
-        return workspace
-    n = nbytes()
-    if n == 0:
+def _scratch(nbytes, device, stream):
+    """A workspace of nbytes that stays alive for the work on `stream`."""
+    if nbytes == 0:
         raise PkvError("unsupported shape or no device")
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     if stream is not None:
         ws.record_stream(stream)
     return ws
 
 
-def _result(like, out, out_dtype, stream):
-    if out is None:
-        if out_dtype not in (torch.bfloat16, torch.float32):
-            raise PkvError("out_dtype must be bfloat16 or float32")
-        out = torch.empty(like.shape, dtype=out_dtype, device=like.device)
-        if stream is not None:
-            out.record_stream(stream)
-    elif out.shape != like.shape or out.dtype not in (torch.bfloat16, torch.float32) or not out.is_contiguous():
-        raise PkvError("out must be a contiguous bfloat16 or float32 tensor of q's shape")
-    return out, (PKV_OUT_F32 if out.dtype == torch.float32 else PKV_OUT_BF16)
+def _empty(shape, dtype, device, stream):
+    out = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        out.record_stream(stream)
+    return out
+
+
+def _out_type(out_dtype):
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise PkvError("out_dtype must be bfloat16 or float32")
+    return out_dtype
 
 
 def rope_append(q, k, v, positions, slot_mapping, table: RopeTable, k_pool, v_pool, q_out=None, err=None, stream=None):
     """Rotate q and k [n_tok][heads][d] by positions (int32) and append k and v to the bf16 cache;
     returns the rotated q.  Tokens may be strided (parts of one fused projection); q_out may be q."""
-    dev = _on_current(q, k, v, positions, slot_mapping, k_pool, v_pool, q_out, err)
-    _typed(torch.bfloat16, q, k, v, k_pool, v_pool, q_out)
-    _typed(torch.int32, positions, err)
-    _typed(torch.int64, slot_mapping)
-    _dense(positions, slot_mapping, k_pool, v_pool)
-    n, n_h, d = q.shape
-    num_blocks, n_kv, bs, _ = k_pool.shape
-    _shaped("k", k, n, n_kv, d)
-    _shaped("v", v, n, n_kv, d)
-    _shaped("positions", positions, n)
-    _shaped("slot_mapping", slot_mapping, n)
-    _shaped("k_pool", k_pool, num_blocks, n_kv, bs, d)
-    _shaped("v_pool", v_pool, num_blocks, n_kv, bs, d)
+    n, n_h, d = _dims("q", q, 3)
+    num_blocks, n_kv, bs, _ = _dims("k_pool", k_pool, 4)
+    dev = q.get_device()
     if q_out is None:
-        q_out = torch.empty((n, n_h, d), dtype=q.dtype, device=q.device)
-        if stream is not None:
-            q_out.record_stream(stream)
-    _shaped("q_out", q_out, n, n_h, d)
-    _check("rope_append", lib().pkv_rope_append(
-        q.data_ptr(), _heads(q), k.data_ptr(), _heads(k), v.data_ptr(), _heads(v), positions.data_ptr(),
-        slot_mapping.data_ptr(), n, ctypes.addressof(table), q_out.data_ptr(), _heads(q_out), k_pool.data_ptr(),
-        v_pool.data_ptr(), num_blocks, bs, n_h, n_kv, d, _addr(err), _raw_stream(stream, dev)))
+        q_out = _empty((n, n_h, d), q.dtype, q.device, stream)
+    kvs, sq, sk, sv, so = (n, n_kv, d), q.stride(), k.stride(), v.stride(), q_out.stride()
+    if not (dev == k.get_device() == v.get_device() == positions.get_device() == slot_mapping.get_device()
+            == k_pool.get_device() == v_pool.get_device() == q_out.get_device() and dev >= 0 and dev == _device()
+            and q.dtype is _bf16 and k.dtype is _bf16 and v.dtype is _bf16 and k_pool.dtype is _bf16
+            and v_pool.dtype is _bf16 and q_out.dtype is _bf16 and positions.dtype is _i32
+            and slot_mapping.dtype is _i64 and k.shape == kvs and v.shape == kvs and q_out.shape == q.shape
+            and v_pool.shape == k_pool.shape and positions.shape == (n,) and slot_mapping.shape == (n,)
+            and positions.is_contiguous() and slot_mapping.is_contiguous() and k_pool.is_contiguous()
+            and v_pool.is_contiguous() and sq[2] == sk[2] == sv[2] == so[2] == 1
+            and (n_h == 1 or sq[1] == so[1] == d) and (n_kv == 1 or sk[1] == sv[1] == d) and _err_ok(err, dev)):
+        _on_current(q, k, v, positions, slot_mapping, k_pool, v_pool, q_out, err)
+        _typed(_bf16, q, k, v, k_pool, v_pool, q_out)
+        _typed(_i32, positions, err)
+        _typed(_i64, slot_mapping)
+        _shaped("k", k, n, n_kv, d)
+        _shaped("v", v, n, n_kv, d)
+        _shaped("positions", positions, n)
+        _shaped("slot_mapping", slot_mapping, n)
+        _shaped("v_pool", v_pool, num_blocks, n_kv, bs, k_pool.shape[3])
+        _shaped("q_out", q_out, n, n_h, d)
+        _dense(positions, slot_mapping, k_pool, v_pool)
+        for t in (q, k, v, q_out):
+            _head_dense(t)
+    if k_pool.shape[3] != d:
+        raise PkvError("the pools' head_dim differs from q's")
+    many = n > 1                                               # one token has no stride
+    st = lib().pkv_rope_append(
+        q.data_ptr(), sq[0] if many else n_h * d, k.data_ptr(), sk[0] if many else n_kv * d, v.data_ptr(),
+        sv[0] if many else n_kv * d, positions.data_ptr(), slot_mapping.data_ptr(), n, ctypes.addressof(table),
+        q_out.data_ptr(), so[0] if many else n_h * d, k_pool.data_ptr(), v_pool.data_ptr(), num_blocks, bs, n_h, n_kv, d,
+        None if err is None else err.data_ptr(), _raw_current(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _check("rope_append", st)
     return q_out
 
 
 def rope_qk(q, k, positions, table: RopeTable, q_out=None, k_out=None, stream=None):
     """Rotate q and k [n_tok][heads][d] by positions (int32); returns (q_out, k_out), which may be
     given as q and k themselves."""
-    dev = _on_current(q, k, positions, q_out, k_out)
-    _typed(torch.bfloat16, q, k, q_out, k_out)
-    _typed(torch.int32, positions)
-    _dense(positions)
-    n, n_h, d = q.shape
-    n_kv = k.shape[1]
-    _shaped("k", k, n, n_kv, d)
-    _shaped("positions", positions, n)
+    n, n_h, d = _dims("q", q, 3)
+    n_kv = _dims("k", k, 3)[1]
+    dev = q.get_device()
     if q_out is None:
-        q_out = torch.empty((n, n_h, d), dtype=q.dtype, device=q.device)
-        if stream is not None:
-            q_out.record_stream(stream)
+        q_out = _empty((n, n_h, d), q.dtype, q.device, stream)
     if k_out is None:
-        k_out = torch.empty((n, n_kv, d), dtype=k.dtype, device=k.device)
-        if stream is not None:
-            k_out.record_stream(stream)
-    _shaped("q_out", q_out, n, n_h, d)
-    _shaped("k_out", k_out, n, n_kv, d)
-    _check("rope_qk", lib().pkv_rope_qk(
-        q.data_ptr(), _heads(q), k.data_ptr(), _heads(k), positions.data_ptr(), n, ctypes.addressof(table),
-        q_out.data_ptr(), _heads(q_out), k_out.data_ptr(), _heads(k_out), n_h, n_kv, d, _raw_stream(stream, dev)))
+        k_out = _empty((n, n_kv, d), k.dtype, k.device, stream)
+    sq, sk, so, ko = q.stride(), k.stride(), q_out.stride(), k_out.stride()
+    if not (dev == k.get_device() == positions.get_device() == q_out.get_device() == k_out.get_device() and dev >= 0
+            and dev == _device() and q.dtype is _bf16 and k.dtype is _bf16 and q_out.dtype is _bf16
+            and k_out.dtype is _bf16 and positions.dtype is _i32 and k.shape == (n, n_kv, d) and k_out.shape == k.shape
+            and q_out.shape == q.shape and positions.shape == (n,) and positions.is_contiguous()
+            and sq[2] == sk[2] == so[2] == ko[2] == 1 and (n_h == 1 or sq[1] == so[1] == d)
+            and (n_kv == 1 or sk[1] == ko[1] == d)):
+        _on_current(q, k, positions, q_out, k_out)
+        _typed(_bf16, q, k, q_out, k_out)
+        _typed(_i32, positions)
+        _shaped("k", k, n, n_kv, d)
+        _shaped("positions", positions, n)
+        _shaped("q_out", q_out, n, n_h, d)
+        _shaped("k_out", k_out, n, n_kv, d)
+        _dense(positions)
+        for t in (q, k, q_out, k_out):
+            _head_dense(t)
+    many = n > 1
+    st = lib().pkv_rope_qk(
+        q.data_ptr(), sq[0] if many else n_h * d, k.data_ptr(), sk[0] if many else n_kv * d, positions.data_ptr(), n,
+        ctypes.addressof(table), q_out.data_ptr(), so[0] if many else n_h * d, k_out.data_ptr(),
+        ko[0] if many else n_kv * d, n_h, n_kv, d, _raw_current(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _check("rope_qk", st)
     return q_out, k_out
 
 
@@ -551,36 +584,59 @@ def alloc_q8_cache(num_blocks, n_kv, block_size, head_dim, tail_rows, fmt="e4m3"
     return Q8CacheTensors(torch.zeros(num_blocks, n_kv, rec, dtype=torch.uint8, device=device), tail(), tail(), fmt)
 
 
-def _q8_parts(cache):
+def _q8_ok(cache, nb, n_kv, bs, d, dev):
+    r, kt, vt = cache.records, cache.k_tail, cache.v_tail
+    return (r.dtype is _u8 and kt.dtype is _bf16 and vt.dtype is _bf16 and r.is_contiguous() and kt.is_contiguous()
+            and vt.is_contiguous() and vt.shape == kt.shape and r.shape == (nb, n_kv, 2 * bs * d + 16)
+            and dev == r.get_device() == kt.get_device() == vt.get_device())
+
+
+def _q8_refuse(cache, nb, n_kv, bs, d):
+    _typed(_u8, cache.records)
+    _typed(_bf16, cache.k_tail, cache.v_tail)
+    _dense(cache.records, cache.k_tail, cache.v_tail)
+    _shaped("v_tail", cache.v_tail, *cache.k_tail.shape)
+    _shaped("records", cache.records, nb, n_kv, 2 * bs * d + 16)
+
+
+def _q8_format(cache):
     if cache.fmt not in Q8_FORMATS:
         raise PkvError(f"format must be one of {Q8_FORMATS}")
-    tail_rows, n_kv, bs, d = cache.k_tail.shape
-    _typed(torch.uint8, cache.records)
-    _typed(torch.bfloat16, cache.k_tail, cache.v_tail)
-    _dense(cache.records, cache.k_tail, cache.v_tail)
-    _shaped("v_tail", cache.v_tail, tail_rows, n_kv, bs, d)
-    nb = cache.records.shape[0]
-    _shaped("records", cache.records, nb, n_kv, 2 * bs * d + 16)
-    return nb, n_kv, bs, d, Q8_FORMATS.index(cache.fmt)
+    return 0 if cache.fmt == "e4m3" else 1
 
 
 def kv_quant_append_q8(k, v, slot_mapping, tail_seq, cache: Q8CacheTensors, err=None, stream=None):
     """Quantize-on-append of k, v [n_tok][n_kv][d] (tokens may be strided) into the 8-bit cache."""
-    dev = _on_current(k, v, slot_mapping, tail_seq, cache.records, cache.k_tail, cache.v_tail, err)
-    nb, n_kv, bs, d, fmt = _q8_parts(cache)
-    _typed(torch.bfloat16, k, v)
-    _typed(torch.int64, slot_mapping)
-    _typed(torch.int32, tail_seq, err)
-    _dense(slot_mapping, tail_seq)
-    n = k.shape[0]
-    _shaped("k", k, n, n_kv, d)
-    _shaped("v", v, n, n_kv, d)
-    _shaped("slot_mapping", slot_mapping, n)
-    _shaped("tail_seq", tail_seq, n)
-    _check("kv_quant_append_q8", lib().pkv_kv_quant_append_q8(
-        k.data_ptr(), _heads(k), v.data_ptr(), _heads(v), slot_mapping.data_ptr(), tail_seq.data_ptr(), n, fmt,
-        cache.records.data_ptr(), cache.k_tail.data_ptr(), cache.v_tail.data_ptr(), cache.k_tail.shape[0], nb, bs,
-        n_kv, d, _addr(err), _raw_stream(stream, dev)))
+    fmt = _q8_format(cache)
+    rows, n_kv, bs, d = _dims("k_tail", cache.k_tail, 4)
+    nb = cache.records.shape[0]
+    n = _dims("k", k, 3)[0]
+    dev = k.get_device()
+    sk, sv, kvs = k.stride(), v.stride(), (n, n_kv, d)
+    if not (dev == v.get_device() == slot_mapping.get_device() == tail_seq.get_device() and dev >= 0 and dev == _device()
+            and k.dtype is _bf16 and v.dtype is _bf16 and slot_mapping.dtype is _i64 and tail_seq.dtype is _i32
+            and k.shape == kvs and v.shape == kvs and slot_mapping.shape == (n,) and tail_seq.shape == (n,)
+            and slot_mapping.is_contiguous() and tail_seq.is_contiguous() and sk[2] == sv[2] == 1
+            and (n_kv == 1 or sk[1] == sv[1] == d) and _err_ok(err, dev) and _q8_ok(cache, nb, n_kv, bs, d, dev)):
+        _on_current(k, v, slot_mapping, tail_seq, cache.records, cache.k_tail, cache.v_tail, err)
+        _typed(_bf16, k, v)
+        _typed(_i64, slot_mapping)
+        _typed(_i32, tail_seq, err)
+        _shaped("k", k, n, n_kv, d)
+        _shaped("v", v, n, n_kv, d)
+        _shaped("slot_mapping", slot_mapping, n)
+        _shaped("tail_seq", tail_seq, n)
+        _dense(slot_mapping, tail_seq)
+        _q8_refuse(cache, nb, n_kv, bs, d)
+        for t in (k, v):
+            _head_dense(t)
+    many = n > 1
+    st = lib().pkv_kv_quant_append_q8(
+        k.data_ptr(), sk[0] if many else n_kv * d, v.data_ptr(), sv[0] if many else n_kv * d, slot_mapping.data_ptr(),
+        tail_seq.data_ptr(), n, fmt, cache.records.data_ptr(), cache.k_tail.data_ptr(), cache.v_tail.data_ptr(), rows, nb,
+        bs, n_kv, d, _addr(err), _raw_current(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _check("kv_quant_append_q8", st)
 
 
 def q8_workspace_bytes(batch, n_h, n_kv, head_dim, block_size, fmt="e4m3") -> int:
@@ -594,21 +650,40 @@ def q8_workspace_bytes(batch, n_h, n_kv, head_dim, block_size, fmt="e4m3") -> in
 def paged_decode_attn_q8(q, cache: Q8CacheTensors, block_tables, context_lens, scale, window=0, out=None,
                          out_dtype=torch.bfloat16, workspace=None, err=None, stream=None):
     """Decode attention over the 8-bit cache (the last `window` tokens of each context; 0: all)."""
-    dev = _on_current(q, cache.records, block_tables, context_lens, out, workspace, err)
-    nb, n_kv, bs, d, fmt = _q8_parts(cache)
-    _typed(torch.bfloat16, q)
-    _typed(torch.int32, block_tables, context_lens, err)
-    _dense(q, block_tables, context_lens)
-    B, n_h, _ = q.shape
-    _shaped("q", q, B, n_h, d)
-    _shaped("block_tables", block_tables, B, block_tables.shape[-1])
-    _shaped("context_lens", context_lens, B)
-    out, od = _result(q, out, out_dtype, stream)
-    ws = _scratch(workspace, lambda: lib().pkv_q8_workspace_bytes(B, n_h, n_kv, d, bs, fmt), q.device, stream)
-    _check("paged_decode_attn_q8", lib().pkv_paged_decode_attn_q8(
-        q.data_ptr(), cache.records.data_ptr(), fmt, block_tables.data_ptr(), block_tables.shape[1],
-        context_lens.data_ptr(), scale, int(window), B, n_h, n_kv, d, bs, nb, out.data_ptr(), od, ws.data_ptr(),
-        ws.numel() * ws.element_size(), _addr(err), _raw_stream(stream, dev)))
+    fmt = _q8_format(cache)
+    _, n_kv, bs, d = _dims("k_tail", cache.k_tail, 4)
+    nb = cache.records.shape[0]
+    B, n_h, _ = _dims("q", q, 3)
+    mb = _dims("block_tables", block_tables, 2)[1]
+    dev = q.get_device()
+    if out is None:
+        out = _empty(q.shape, _out_type(out_dtype), q.device, stream)
+    if workspace is None and dev >= 0 and B:
+        workspace = _scratch(lib().pkv_q8_workspace_bytes(B, n_h, n_kv, d, bs, fmt), q.device, stream)
+    if not (dev == block_tables.get_device() == context_lens.get_device() == out.get_device() and dev >= 0
+            and dev == _device() and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))
+            and q.dtype is _bf16 and block_tables.dtype is _i32 and context_lens.dtype is _i32
+            and (out.dtype is _bf16 or out.dtype is _f32) and q.shape == (B, n_h, d) and block_tables.shape == (B, mb)
+            and context_lens.shape == (B,) and out.shape == q.shape and q.is_contiguous()
+            and block_tables.is_contiguous() and context_lens.is_contiguous() and out.is_contiguous()
+            and _err_ok(err, dev) and _q8_ok(cache, nb, n_kv, bs, d, dev)):
+        _on_current(q, cache.records, cache.k_tail, cache.v_tail, block_tables, context_lens, out, workspace, err)
+        _typed(_bf16, q)
+        _typed(_i32, block_tables, context_lens, err)
+        _out_type(out.dtype)
+        _shaped("q", q, B, n_h, d)
+        _shaped("block_tables", block_tables, B, mb)
+        _shaped("context_lens", context_lens, B)
+        _shaped("out", out, B, n_h, d)
+        _dense(q, block_tables, context_lens, out, workspace)
+        _q8_refuse(cache, nb, n_kv, bs, d)
+    st = lib().pkv_paged_decode_attn_q8(
+        q.data_ptr(), cache.records.data_ptr(), fmt, block_tables.data_ptr(), mb, context_lens.data_ptr(), scale,
+        int(window), B, n_h, n_kv, d, bs, nb, out.data_ptr(), 1 if out.dtype is _f32 else 0, _addr(workspace),
+        0 if workspace is None else workspace.nbytes, _addr(err),
+        _raw_current(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _check("paged_decode_attn_q8", st)
     return out
 
 
@@ -624,25 +699,43 @@ def paged_decode_attn_mass(q, k_pool, v_pool, block_tables, context_lens, scale,
                            out_dtype=torch.bfloat16, workspace=None, err=None, stream=None):
     """paged_decode_attn that also adds each cached token's attention weight, summed over the query
     heads of its group, to mass (fp32 [B][n_kv][at least max_blocks * block_size])."""
-    dev = _on_current(q, k_pool, v_pool, block_tables, context_lens, mass, out, workspace, err)
-    _typed(torch.bfloat16, q, k_pool, v_pool)
-    _typed(torch.int32, block_tables, context_lens, err)
-    _typed(torch.float32, mass)
-    _dense(q, k_pool, v_pool, block_tables, context_lens, mass)
-    B, n_h, d = q.shape
-    nb, n_kv, bs, _ = k_pool.shape
-    _shaped("k_pool", k_pool, nb, n_kv, bs, d)
-    _shaped("v_pool", v_pool, nb, n_kv, bs, d)
-    _shaped("block_tables", block_tables, B, block_tables.shape[-1])
-    _shaped("context_lens", context_lens, B)
-    _shaped("mass", mass, B, n_kv, mass.shape[-1])
-    out, od = _result(q, out, out_dtype, stream)
-    mb = block_tables.shape[1]
-    ws = _scratch(workspace, lambda: lib().pkv_mass_workspace_bytes(B, n_h, n_kv, d, bs, mb), q.device, stream)
-    _check("paged_decode_attn_mass", lib().pkv_paged_decode_attn_mass(
-        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), mb, context_lens.data_ptr(), scale,
-        B, n_h, n_kv, d, bs, nb, out.data_ptr(), od, mass.data_ptr(), mass.shape[2], ws.data_ptr(),
-        ws.numel() * ws.element_size(), _addr(err), _raw_stream(stream, dev)))
+    B, n_h, d = _dims("q", q, 3)
+    nb, n_kv, bs, _ = _dims("k_pool", k_pool, 4)
+    mb = _dims("block_tables", block_tables, 2)[1]
+    T = _dims("mass", mass, 3)[2]
+    dev = q.get_device()
+    if out is None:
+        out = _empty(q.shape, _out_type(out_dtype), q.device, stream)
+    if workspace is None and dev >= 0 and B:
+        workspace = _scratch(lib().pkv_mass_workspace_bytes(B, n_h, n_kv, d, bs, mb), q.device, stream)
+    if not (dev == k_pool.get_device() == v_pool.get_device() == block_tables.get_device() == context_lens.get_device()
+            == mass.get_device() == out.get_device() and dev >= 0 and dev == _device()
+            and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))
+            and q.dtype is _bf16 and k_pool.dtype is _bf16 and v_pool.dtype is _bf16 and block_tables.dtype is _i32
+            and context_lens.dtype is _i32 and mass.dtype is _f32 and (out.dtype is _bf16 or out.dtype is _f32)
+            and k_pool.shape == (nb, n_kv, bs, d) and v_pool.shape == k_pool.shape and block_tables.shape == (B, mb)
+            and context_lens.shape == (B,) and mass.shape == (B, n_kv, T) and out.shape == q.shape
+            and q.is_contiguous() and k_pool.is_contiguous() and v_pool.is_contiguous() and block_tables.is_contiguous()
+            and context_lens.is_contiguous() and mass.is_contiguous() and out.is_contiguous() and _err_ok(err, dev)):
+        _on_current(q, k_pool, v_pool, block_tables, context_lens, mass, out, workspace, err)
+        _typed(_bf16, q, k_pool, v_pool)
+        _typed(_i32, block_tables, context_lens, err)
+        _typed(_f32, mass)
+        _out_type(out.dtype)
+        _shaped("k_pool", k_pool, nb, n_kv, bs, d)
+        _shaped("v_pool", v_pool, nb, n_kv, bs, d)
+        _shaped("block_tables", block_tables, B, mb)
+        _shaped("context_lens", context_lens, B)
+        _shaped("mass", mass, B, n_kv, T)
+        _shaped("out", out, B, n_h, d)
+        _dense(q, k_pool, v_pool, block_tables, context_lens, mass, out, workspace)
+    st = lib().pkv_paged_decode_attn_mass(
+        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), mb, context_lens.data_ptr(), scale, B,
+        n_h, n_kv, d, bs, nb, out.data_ptr(), 1 if out.dtype is _f32 else 0, mass.data_ptr(), T, _addr(workspace),
+        0 if workspace is None else workspace.nbytes, _addr(err),
+        _raw_current(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _check("paged_decode_attn_mass", st)
     return out
 
 
@@ -674,43 +767,63 @@ def evict_workspace_bytes(batch, n_kv, block_size, max_blocks) -> int:
     return n
 
 
+def _evict_ok(st, B, n_kv, T, dev):
+    m, p, k, x = st.mass, st.positions, st.kept, st.dropped
+    return (m.dtype is _f32 and p.dtype is _i32 and k.dtype is _i32 and x.dtype is _i32 and m.shape == (B, n_kv, T)
+            and p.shape == m.shape and k.shape == (B,) and x.shape == (B,) and m.is_contiguous() and p.is_contiguous()
+            and k.is_contiguous() and x.is_contiguous()
+            and dev == m.get_device() == p.get_device() == k.get_device() == x.get_device())
+
+
 def kv_evict(k_pool, v_pool, block_tables, context_lens, keep, recent, state: EvictState, out: EvictState | None = None,
              new_lens=None, workspace=None, err=None, stream=None):
-    """Cut each sequence of the bf16 cache to keep[s] rows (int32 [B]): the `recent` newest and those
-    with the largest accounts.  Updates `state` in place, or writes the new state to `out`; returns
-    the new context lengths (a tensor of its own)."""
+    """Cut each sequence of the bf16 cache to keep[s] rows (int32 [B]): those of its last `recent`
+    tokens and those with the largest accounts.  Updates `state` in place, or writes the new state to
+    `out`; returns the new context lengths (a tensor of its own)."""
     dst = state if out is None else out
-    dev = _on_current(k_pool, v_pool, block_tables, context_lens, keep, state.mass, state.positions, state.kept,
-                      state.dropped, dst.mass, dst.positions, dst.kept, dst.dropped, new_lens, workspace, err)
-    _typed(torch.bfloat16, k_pool, v_pool)
-    _typed(torch.int32, block_tables, context_lens, keep, state.positions, state.kept, state.dropped, dst.positions,
-           dst.kept, dst.dropped, new_lens, err)
-    _typed(torch.float32, state.mass, dst.mass)
-    _dense(k_pool, v_pool, block_tables, context_lens, keep, state.mass, state.positions, state.kept, state.dropped,
-           dst.mass, dst.positions, dst.kept, dst.dropped, new_lens)
-    nb, n_kv, bs, d = k_pool.shape
-    B, mb = block_tables.shape
-    T = state.mass.shape[-1]
-    _shaped("v_pool", v_pool, nb, n_kv, bs, d)
-    for st in (state, dst):
-        _shaped("mass", st.mass, B, n_kv, T)
-        _shaped("positions", st.positions, B, n_kv, T)
-        _shaped("kept", st.kept, B)
-        _shaped("dropped", st.dropped, B)
-    _shaped("context_lens", context_lens, B)
-    _shaped("keep", keep, B)
+    nb, n_kv, bs, d = _dims("k_pool", k_pool, 4)
+    B, mb = _dims("block_tables", block_tables, 2)
+    T = _dims("mass", state.mass, 3)[2]
+    dev = k_pool.get_device()
     if new_lens is None:
-        new_lens = torch.empty_like(context_lens)
-        if stream is not None:
-            new_lens.record_stream(stream)
-    _shaped("new_lens", new_lens, B)
-    ws = _scratch(workspace, lambda: lib().pkv_evict_workspace_bytes(B, n_kv, bs, mb), k_pool.device, stream)
-    _check("kv_evict", lib().pkv_kv_evict(
+        new_lens = _empty(context_lens.shape, _i32, context_lens.device, stream)
+    if workspace is None and dev >= 0 and B:
+        workspace = _scratch(lib().pkv_evict_workspace_bytes(B, n_kv, bs, mb), k_pool.device, stream)
+    if not (dev == v_pool.get_device() == block_tables.get_device() == context_lens.get_device() == keep.get_device()
+            == new_lens.get_device() and dev >= 0 and dev == _device()
+            and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))
+            and k_pool.dtype is _bf16 and v_pool.dtype is _bf16 and block_tables.dtype is _i32
+            and context_lens.dtype is _i32 and keep.dtype is _i32 and new_lens.dtype is _i32
+            and v_pool.shape == k_pool.shape and context_lens.shape == (B,) and keep.shape == (B,)
+            and new_lens.shape == (B,) and k_pool.is_contiguous() and v_pool.is_contiguous()
+            and block_tables.is_contiguous() and context_lens.is_contiguous() and keep.is_contiguous()
+            and new_lens.is_contiguous() and _err_ok(err, dev) and _evict_ok(state, B, n_kv, T, dev)
+            and (out is None or _evict_ok(out, B, n_kv, T, dev))):
+        _on_current(k_pool, v_pool, block_tables, context_lens, keep, state.mass, state.positions, state.kept,
+                    state.dropped, dst.mass, dst.positions, dst.kept, dst.dropped, new_lens, workspace, err)
+        _typed(_bf16, k_pool, v_pool)
+        _typed(_i32, block_tables, context_lens, keep, state.positions, state.kept, state.dropped, dst.positions,
+               dst.kept, dst.dropped, new_lens, err)
+        _typed(_f32, state.mass, dst.mass)
+        _shaped("v_pool", v_pool, nb, n_kv, bs, d)
+        for st in (state, dst):
+            _shaped("mass", st.mass, B, n_kv, T)
+            _shaped("positions", st.positions, B, n_kv, T)
+            _shaped("kept", st.kept, B)
+            _shaped("dropped", st.dropped, B)
+        _shaped("context_lens", context_lens, B)
+        _shaped("keep", keep, B)
+        _shaped("new_lens", new_lens, B)
+        _dense(k_pool, v_pool, block_tables, context_lens, keep, state.mass, state.positions, state.kept, state.dropped,
+               dst.mass, dst.positions, dst.kept, dst.dropped, new_lens, workspace)
+    st = lib().pkv_kv_evict(
         k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), mb, context_lens.data_ptr(), keep.data_ptr(),
         int(recent), state.mass.data_ptr(), state.positions.data_ptr(), state.kept.data_ptr(), state.dropped.data_ptr(),
         dst.mass.data_ptr(), dst.positions.data_ptr(), dst.kept.data_ptr(), dst.dropped.data_ptr(), T,
-        new_lens.data_ptr(), B, n_kv, d, bs, nb, ws.data_ptr(), ws.numel() * ws.element_size(), _addr(err),
-        _raw_stream(stream, dev)))
+        new_lens.data_ptr(), B, n_kv, d, bs, nb, _addr(workspace), 0 if workspace is None else workspace.nbytes,
+        _addr(err), _raw_current(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _check("kv_evict", st)
     return new_lens
 
 

@@ -281,50 +281,72 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32)
   }
 }
 
-// mass[s][g][t] += sum over the group's heads of 2^(x - M) / L.  CTA (c, s, g): kMassTokens
-// tokens; LT lanes share a token's G scores (vectors of four where G allows), so a warp reads
-// whole lines, and add their parts by a fixed tree.
-constexpr int kMassTokens = 512;
-
-template <int LT, bool V4>
+// mass[s][g][t] += sum over the group's heads of 2^(x - M) / L.  LT lanes share a token's G scores
+// (vectors of four where G allows), so a warp reads whole lines, and add their parts by a fixed
+// tree; a lane has the loads of U tokens in flight (one at a time left the kernel at 2.2 TB/s of
+// scores on 32-head groups).  CTA (c, s, g) takes 256 / LT * U tokens.
+template <int LT, bool V4, int U>
 __global__ void __launch_bounds__(256) mass_add_kernel(const float* __restrict__ scores, const float2* __restrict__ fin,
                                                        const int32_t* __restrict__ ctx, int max_ctx, int n_kv, int G,
                                                        float* __restrict__ mass, long long mass_stride, int chunks) {
+  constexpr int STEP = 256 / LT;
   __shared__ float2 f[64];
-  const int chunk = blockIdx.x % chunks, sg = blockIdx.x / chunks, s = sg / n_kv, g = sg % n_kv;
+  const int chunk = blockIdx.x % chunks, sg = blockIdx.x / chunks, s = sg / n_kv;
   grid_dep_wait();                                            // every thread: see decode_plan.cu's reduce
-  const int n = clamp_ctx(ctx[s], max_ctx), t1 = min(n, (chunk + 1) * kMassTokens);
-  if (chunk * kMassTokens >= n) return;
-  if (threadIdx.x < G) f[threadIdx.x] = fin[((size_t)s * n_kv + g) * G + threadIdx.x];
-  __syncthreads();
-  const int sub = threadIdx.x % LT;
+  const int n = clamp_ctx(ctx[s], max_ctx);
+  if (chunk * STEP * U >= n) return;
+  const int sub = threadIdx.x % LT, t0 = chunk * STEP * U + threadIdx.x / LT;
   const float* x = scores + ((size_t)sg * max_ctx) * G;
   float* mrow = mass + (size_t)sg * mass_stride;
-  for (int t0 = chunk * kMassTokens; t0 < t1; t0 += 256 / LT) {
-    const int t = t0 + threadIdx.x / LT;
-    float w = 0.f;
-    if (t < t1) {
-      if constexpr (V4) {
-        for (int i = sub; i < G / 4; i += LT) {
-          const float4 v = *(reinterpret_cast<const float4*>(x + (size_t)t * G) + i);
-          w += ex2(v.x - f[4 * i].x) * f[4 * i].y + ex2(v.y - f[4 * i + 1].x) * f[4 * i + 1].y +
-               ex2(v.z - f[4 * i + 2].x) * f[4 * i + 2].y + ex2(v.w - f[4 * i + 3].x) * f[4 * i + 3].y;
-        }
-      } else {
-        for (int i = sub; i < G; i += LT) w += ex2(x[(size_t)t * G + i] - f[i].x) * f[i].y;
-      }
-    }
+  float before[U], w[U];
 #pragma unroll
-    for (int o = LT / 2; o; o >>= 1) w += __shfl_xor_sync(FULL_MASK, w, o);
-    if (sub == 0 && t < t1) mrow[t] += w;
+  for (int u = 0; u < U; ++u) {
+    w[u] = 0.f;
+    before[u] = sub == 0 && t0 + u * STEP < n ? mrow[t0 + u * STEP] : 0.f;
+  }
+  if (threadIdx.x < G) f[threadIdx.x] = fin[(size_t)sg * G + threadIdx.x];
+  __syncthreads();
+  if constexpr (V4) {
+    for (int i = sub; i < G / 4; i += LT) {
+      float4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (t0 + u * STEP < n) v[u] = __ldcs(reinterpret_cast<const float4*>(x + (size_t)(t0 + u * STEP) * G) + i);
+        else v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float2 f0 = f[4 * i], f1 = f[4 * i + 1], f2 = f[4 * i + 2], f3 = f[4 * i + 3];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        w[u] += ex2(v[u].x - f0.x) * f0.y + ex2(v[u].y - f1.x) * f1.y + ex2(v[u].z - f2.x) * f2.y + ex2(v[u].w - f3.x) * f3.y;
+    }
+  } else {
+    for (int i = sub; i < G; i += LT) {
+      float v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = t0 + u * STEP < n ? __ldcs(x + (size_t)(t0 + u * STEP) * G + i) : 0.f;
+      const float2 fi = f[i];
+#pragma unroll
+      for (int u = 0; u < U; ++u) w[u] += ex2(v[u] - fi.x) * fi.y;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int o = LT / 2; o; o >>= 1) w[u] += __shfl_xor_sync(FULL_MASK, w[u], o);
+    if (sub == 0 && t0 + u * STEP < n) mrow[t0 + u * STEP] = before[u] + w[u];
   }
 }
 
-static const void* mass_add_fn(int G) {
-  if (G % 4) return G >= 8 ? (const void*)mass_add_kernel<4, false> : (const void*)mass_add_kernel<1, false>;
-  return G >= 32 ? (const void*)mass_add_kernel<8, true>
-                 : (G >= 16 ? (const void*)mass_add_kernel<4, true>
-                            : (G >= 8 ? (const void*)mass_add_kernel<2, true> : (const void*)mass_add_kernel<1, true>));
+struct MassAdd {
+  const void* fn;
+  int tokens;                    // per CTA
+};
+static MassAdd mass_add(int G) {
+  if (G % 4 && G >= 8) return {(const void*)mass_add_kernel<4, false, 8>, 512};
+  if (G % 4) return {(const void*)mass_add_kernel<1, false, 4>, 1024};
+  if (G >= 32) return {(const void*)mass_add_kernel<8, true, 8>, 256};
+  if (G >= 16) return {(const void*)mass_add_kernel<4, true, 8>, 512};
+  if (G >= 8) return {(const void*)mass_add_kernel<2, true, 4>, 512};
+  return {(const void*)mass_add_kernel<1, true, 4>, 1024};
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -356,9 +378,9 @@ static MassVariant* lookup_mass(int D, int tiling) {
   std::lock_guard<std::mutex> lock(mu);
   MassVariant& v = table[di][tiling];
   if (!ready[di][tiling]) {
-    // 8 KB per stage at either head size
-    const int stage = 8192;
-    if (D == 128) mass_pick<128, 1>(tiling, v);
+    const bool wide = D == 128 && tiling >= 2;
+    const int stage = wide ? 16384 : 8192;
+    if (D == 128) wide ? mass_pick<128, 2>(tiling, v) : mass_pick<128, 1>(tiling, v);
     else mass_pick<64, 2>(tiling, v);
     v.stages = ring_stages(stage, 2 * stage, "PKV_STAGES_MASS");
     v.smem = mass_smem_bytes(v.streams, v.stages, stage);
@@ -422,7 +444,8 @@ extern "C" pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_po
   if (max_ctx > 0x7fffffffLL) return PKV_ERANGE;
   if (mass_stride < max_ctx) return PKV_EINVAL;
   const int G = n_h / n_kv;
-  const long long chunks = (max_ctx + kMassTokens - 1) / kMassTokens;
+  const MassAdd add = mass_add(G);
+  const long long chunks = (max_ctx + add.tokens - 1) / add.tokens;
   if (chunks * batch * n_kv > 0x7fffffffLL) return PKV_ERANGE;
   MassVariant* v = lookup_mass(head_dim, head_tiling(G));
   if (!v) {
@@ -480,7 +503,7 @@ extern "C" pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_po
     int mc = (int)max_ctx, nk = n_kv, gg = G, nc = (int)chunks;
     long long stride = mass_stride;
     void* kargs[] = {&scores, &fin, (void*)&context_lens, &mc, &nk, &gg, &mass, &stride, &nc};
-    e = launch_pdl(mass_add_fn(G), dim3((unsigned)(chunks * batch * n_kv)), dim3(256), 0, st, kargs);
+    e = launch_pdl(add.fn, dim3((unsigned)(chunks * batch * n_kv)), dim3(256), 0, st, kargs);
   }
   if (e != cudaSuccess) {
     record_cuda_error(e);

@@ -10,8 +10,8 @@
 // What bounds it: long calls read 4 d bytes and write 2 d per token and kv head (HBM).  A decode
 // step reads the open rows and writes one record per (sequence, kv head): a few hundred KB, so
 // the launch and three dependent round trips (slots, rows, stores).
-// Split: one CTA per kv head and span of tokens takes each run of tokens that lands in one
-// block.  A span is one token for small calls (every run its own CTA, for latency) and
+// Split: one CTA per kv head, K or V, and span of tokens takes each run of tokens that lands in
+// one block.  A span is one token for small calls (every run its own CTA, for latency) and
 // block_size tokens above kSpanTokens (one or two runs per CTA, so that the CTAs whose tokens
 // all continue a run do not cost a launch slot each).
 #include <cuda_fp8.h>
@@ -35,17 +35,22 @@ struct Q8AppendArgs {
   int32_t* err;
 };
 
-constexpr int kQ8Threads = 256;
 constexpr int kSpanTokens = 2048;
 
-__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d, bool e4m3) {
-  if (e4m3) {
+// Four codes.  INT8: |x| <= 127 (1 + 2^-22), so adding 1.5 * 2^23 rounds x to the nearest integer
+// (ties to even) and leaves it in the low byte; no conversion instruction, no clamp.  (The caller's
+// products are __fmul_rn: fused with this addition they would skip the rounding to fp32 between.)
+template <bool E4M3>
+__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d) {
+  if constexpr (E4M3) {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
     return lo | hi << 16;
   }
-  auto one = [](float x) { return (uint32_t)(int)fminf(fmaxf(rintf(x), -127.f), 127.f) & 255u; };
-  return one(a) | one(b) << 8 | one(c) << 16 | one(d) << 24;
+  constexpr float kRound = 12582912.f;
+  const uint32_t x = __byte_perm(__float_as_uint(a + kRound), __float_as_uint(b + kRound), 0x0040);
+  const uint32_t y = __byte_perm(__float_as_uint(c + kRound), __float_as_uint(d + kRound), 0x0040);
+  return __byte_perm(x, y, 0x5410);
 }
 
 // Whether token i belongs to sequence seq (padding belongs to none).
@@ -71,117 +76,167 @@ __device__ int seq_edge(const Q8AppendArgs& a, int i, int seq, int dir) {
 }
 
 template <int D, int BS>
-__global__ void __launch_bounds__(kQ8Threads) q8_append_kernel(const Q8AppendArgs a, const int e4m3) {
-  constexpr int ROW = D + 8;                                  // padded row: the gathers below hit distinct banks
+struct Q8Shape {
+  static constexpr int VECS = BS * D / 8;                     // 16-byte vectors of a block's rows
+  static constexpr int NT = VECS < 256 ? VECS : 256;
+  static constexpr int NV = VECS / NT;
+};
+
+template <int D, int BS, bool E4M3>
+__global__ void __launch_bounds__(Q8Shape<D, BS>::NT) q8_append_kernel(const Q8AppendArgs a) {
+  constexpr int NT = Q8Shape<D, BS>::NT, NV = Q8Shape<D, BS>::NV;
+  constexpr int ROW = D + 8;                                  // padded row: the gathers below spread over the banks
   constexpr int VPR = D / 8;                                  // 16-byte vectors per row
-  constexpr int CHUNKS = BS * D / 16;                         // 16-byte chunks of codes per K (or V)
-  extern __shared__ __align__(16) __nv_bfloat16 rows_s[];    // K rows, then V rows
-  __shared__ float big_s[2][kQ8Threads / 32];
-  __shared__ int run_s, edge_s;
-  const int g = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i1 = min(a.n_tok, ((int)blockIdx.x + 1) * a.span);
-  for (int i = blockIdx.x * a.span; i < i1;) {
-    const int64_t slot = a.slots[i];
-    if (slot < 0) { ++i; continue; }
-    const int seq = a.tail_seq[i];
-    if (slot >= a.n_slots || (unsigned)seq >= (unsigned)a.tail_rows) {
-      if (g == 0 && threadIdx.x == 0) set_err(a.err, PKV_DEV_BAD_SLOT);
-      ++i;
-      continue;
+  constexpr int CHUNKS = BS * D / 16;                         // 16-byte chunks of codes
+  __shared__ __align__(16) __nv_bfloat16 rows_s[BS * ROW];
+  __shared__ float big_s[NT / 32];
+  // the span's tokens and the block_size behind them, which the last run may reach
+  constexpr int WIN = 2 * BS;
+  __shared__ int64_t slot_s[WIN];
+  __shared__ int seq_s[WIN];
+  __shared__ uint32_t lead_s[WIN / 32], cont_s[WIN / 32 + 1];  // bit t: token t starts / continues a run
+  __shared__ int edge_s;
+  const int g = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
+  const bool values = blockIdx.z != 0;                        // this CTA's half of the record: V or K
+  const __nv_bfloat16* x = (values ? a.v : a.k) + (size_t)g * D;
+  const long long stride = values ? a.v_stride : a.k_stride;
+  __nv_bfloat16* tails = values ? a.v_tail : a.k_tail;
+  const int i0 = blockIdx.x * a.span;
+  if (tid < WIN) {
+    const int i = i0 + tid;
+    const bool in = i < a.n_tok && tid < a.span + BS;
+    const int64_t slot = in ? a.slots[i] : -1;
+    const int seq = in ? a.tail_seq[i] : -1;
+    const int64_t slot_before = in && i > 0 ? a.slots[i - 1] : -1;
+    const int seq_before = in && i > 0 ? a.tail_seq[i - 1] : -1;
+    const bool good = slot >= 0 && slot < a.n_slots && (unsigned)seq < (unsigned)a.tail_rows;
+    if (slot >= 0 && !good && tid < a.span && g == 0 && blockIdx.z == 0) set_err(a.err, PKV_DEV_BAD_SLOT);
+    // a run: consecutive rows of one block, of one sequence
+    const bool goes_on = good && (slot & (BS - 1)) != 0 && slot_before == slot - 1 && seq_before == seq;
+    slot_s[tid] = slot;
+    seq_s[tid] = seq;
+    const unsigned c = __ballot_sync(FULL_MASK, goes_on), l = __ballot_sync(FULL_MASK, good && !goes_on && tid < a.span);
+    if (lane == 0) {
+      cont_s[warp] = c;
+      lead_s[warp] = l;
     }
-    const int row0 = (int)(slot % BS);
-    // tokens i, i + 1, ... in consecutive rows of this block
-    if (threadIdx.x == 0) run_s = BS - row0;
-    __syncthreads();
-    if (threadIdx.x < BS - row0) {
-      const int j = i + threadIdx.x;
-      if (j >= a.n_tok || a.slots[j] != slot + (int)threadIdx.x || a.tail_seq[j] != seq) atomicMin(&run_s, (int)threadIdx.x);
+  }
+  if (tid == 0) cont_s[WIN / 32] = 0u;
+  __syncthreads();
+  for (int t = 0;;) {
+    // next run that starts in the span
+    {
+      uint32_t bits = 0;
+      int wd = t >> 5;
+      if (wd < WIN / 32) bits = lead_s[wd] & (0xffffffffu << (t & 31));
+      while (!bits && ++wd < WIN / 32) bits = lead_s[wd];
+      if (!bits) break;
+      t = 32 * wd + __ffs(bits) - 1;
     }
-    __syncthreads();
-    const int m = run_s, end = row0 + m;
-    // a run that began before this span is its predecessor's
-    const bool leads = i == 0 || row0 == 0 || a.slots[i - 1] != slot - 1 || a.tail_seq[i - 1] != seq;
-    if (leads) {
+    const int i = i0 + t, seq = seq_s[t];
+    const int64_t slot = slot_s[t];
+    const int row0 = (int)(slot & (BS - 1));
+    int m = 1;                                                // its length: the tokens that go on from it
+    {
+      int p = t + 1, wd = p >> 5;
+      uint32_t stop = wd < WIN / 32 ? ~cont_s[wd] & (0xffffffffu << (p & 31)) : 0xffffffffu;
+      while (!stop) stop = ~cont_s[++wd];
+      m = 32 * wd + __ffs(stop) - 1 - t;
+      if (wd >= WIN / 32) m = WIN - t;
+    }
+    m = min(m, BS - row0);
+    const int end = row0 + m;
+    {
       const long long phys = slot / BS;
       const size_t tail0 = ((size_t)seq * a.n_kv + g) * BS * D;
-      // rows into shared memory, with the largest magnitudes on the way
-      float big[2] = {0.f, 0.f};
+      // rows into shared memory, with the largest magnitude on the way
+      uint4 w[NV];
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const __nv_bfloat16* x = (kv ? a.v + (long long)i * a.v_stride : a.k + (long long)i * a.k_stride) + (size_t)g * D;
-        const long long stride = kv ? a.v_stride : a.k_stride;
-        const __nv_bfloat16* tail = (kv ? a.v_tail : a.k_tail) + tail0;
-#pragma unroll 4
-        for (int e = threadIdx.x; e < BS * VPR; e += kQ8Threads) {
-          const int r = e / VPR, c = e - r * VPR;
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          if (r < end) w = *(reinterpret_cast<const uint4*>(r < row0 ? tail + (size_t)r * D : x + (r - row0) * stride) + c);
-          *reinterpret_cast<uint4*>(rows_s + (kv * BS + r) * ROW + 8 * c) = w;
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) big[kv] = fmaxf(big[kv], fmaxf(fabsf(bf16_lo(ws[q])), fabsf(bf16_hi(ws[q]))));
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) big[kv] = fmaxf(big[kv], __shfl_xor_sync(FULL_MASK, big[kv], o));
-        if (lane == 0) big_s[kv][warp] = big[kv];
+      for (int u = 0; u < NV; ++u) {
+        const int e = tid + u * NT, r = e / VPR, c = e % VPR;
+        w[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < end)
+          w[u] = *(reinterpret_cast<const uint4*>(r < row0 ? tails + tail0 + (size_t)r * D : x + (long long)(i + r - row0) * stride) + c);
       }
+      __nv_bfloat162 big2 = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        const int e = tid + u * NT, r = e / VPR, c = e % VPR;
+        *reinterpret_cast<uint4*>(rows_s + r * ROW + 8 * c) = w[u];
+        const uint32_t ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) big2 = __hmax2(big2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&ws[q])));
+      }
+      // magnitudes are not negative: their bits order as integers
+      const float mine = fmaxf(__low2float(big2), __high2float(big2));
+      const uint32_t wb = __reduce_max_sync(FULL_MASK, __float_as_uint(mine));
+      if (lane == 0) big_s[warp] = __uint_as_float(wb);
       __syncthreads();
       uint8_t* rec = a.records + ((size_t)phys * a.n_kv + g) * q8_record_bytes(BS, D);
-      const float most = e4m3 ? 448.f : 127.f;
-      float inv[2], scale[2];
+      const float most = E4M3 ? 448.f : 127.f;
+      float big = 0.f;
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        float b = 0.f;
+      for (int k = 0; k < NT / 32; ++k) big = fmaxf(big, big_s[k]);
+      const bool some = big >= kQ8Tiny;
+      const float scale = some ? __fdiv_rn(big, most) : 0.f, inv = some ? __fdiv_rn(most, big) : 0.f;
+      uint8_t* codes = rec + (values ? BS * D : 0);
+      if (!values) {
 #pragma unroll
-        for (int w = 0; w < kQ8Threads / 32; ++w) b = fmaxf(b, big_s[kv][w]);
-        const bool some = b >= kQ8Tiny;
-        scale[kv] = some ? __fdiv_rn(b, most) : 0.f;
-        inv[kv] = some ? __fdiv_rn(most, b) : 0.f;
-      }
-      for (int e = threadIdx.x; e < 2 * CHUNKS; e += kQ8Threads) {
-        const int kv = e / CHUNKS, c = e - kv * CHUNKS;
-        const int ln = c & 31, gid = ln >> 2, tig = ln & 3, j = (c >> 5) % (D / 32), tt = (c >> 5) / (D / 32);
-        uint32_t w[4];
-        if (kv == 0) {
+        for (int e = tid; e < CHUNKS; e += NT) {
+          const int ln = e & 31, gid = ln >> 2, tig = ln & 3, j = (e >> 5) % (D / 32), tt = (e >> 5) / (D / 32);
           const __nv_bfloat16* p = rows_s + (16 * tt + gid) * ROW + 32 * j + 2 * tig;
+          uint32_t o[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {                       // q = 2 ks + hi
             const __nv_bfloat16* s = p + (q & 1) * 8 * ROW + (q >> 1) * 16;
             const uint32_t x0 = *reinterpret_cast<const uint32_t*>(s), x1 = *reinterpret_cast<const uint32_t*>(s + 8);
-            w[q] = code4(bf16_lo(x0) * inv[0], bf16_hi(x0) * inv[0], bf16_lo(x1) * inv[0], bf16_hi(x1) * inv[0], e4m3);
+            o[q] = code4<E4M3>(__fmul_rn(bf16_lo(x0), inv), __fmul_rn(bf16_hi(x0), inv), __fmul_rn(bf16_lo(x1), inv), __fmul_rn(bf16_hi(x1), inv));
           }
-        } else {
-          const __nv_bfloat16* p = rows_s + (BS + 16 * tt + 2 * tig) * ROW + 32 * j + gid;
+          *reinterpret_cast<uint4*>(codes + (size_t)e * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      } else {
+        // the chunks of two neighbouring channels (gid = 2 gp, 2 gp + 1) from one set of loads
+#pragma unroll
+        for (int e = tid; e < CHUNKS / 2; e += NT) {
+          const int ln = e & 15, gp = ln >> 2, tig = ln & 3, j = (e >> 4) % (D / 32), tt = (e >> 4) / (D / 32);
+          const __nv_bfloat16* p = rows_s + (16 * tt + 2 * tig) * ROW + 32 * j + 2 * gp;
+          uint32_t o[2][4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {                       // q = 2 md + hi
             const __nv_bfloat16* s = p + (q >> 1) * 16 + (q & 1) * 8;
-            w[q] = code4(__bfloat162float(s[0]) * inv[1], __bfloat162float(s[ROW]) * inv[1],
-                         __bfloat162float(s[8 * ROW]) * inv[1], __bfloat162float(s[9 * ROW]) * inv[1], e4m3);
+            const uint32_t t0 = *reinterpret_cast<const uint32_t*>(s), t1 = *reinterpret_cast<const uint32_t*>(s + ROW);
+            const uint32_t t2 = *reinterpret_cast<const uint32_t*>(s + 8 * ROW), t3 = *reinterpret_cast<const uint32_t*>(s + 9 * ROW);
+            o[0][q] = code4<E4M3>(__fmul_rn(bf16_lo(t0), inv), __fmul_rn(bf16_lo(t1), inv), __fmul_rn(bf16_lo(t2), inv), __fmul_rn(bf16_lo(t3), inv));
+            o[1][q] = code4<E4M3>(__fmul_rn(bf16_hi(t0), inv), __fmul_rn(bf16_hi(t1), inv), __fmul_rn(bf16_hi(t2), inv), __fmul_rn(bf16_hi(t3), inv));
           }
+          uint8_t* d = codes + (size_t)(((e >> 4) << 5) + 8 * gp + tig) * 16;
+          *reinterpret_cast<uint4*>(d) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
+          *reinterpret_cast<uint4*>(d + 64) = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
         }
-        *reinterpret_cast<uint4*>(rec + (size_t)e * 16) = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      if (threadIdx.x == 0)
-        *reinterpret_cast<uint4*>(rec + 2 * BS * D) = make_uint4(__float_as_uint(scale[0]), __float_as_uint(scale[1]), 0u, 0u);
+      if (tid == 0) {
+        float* sc = reinterpret_cast<float*>(rec + 2 * BS * D);
+        sc[values ? 1 : 0] = scale;
+        sc[values ? 3 : 2] = 0.f;
+      }
 
       // ---- the sequence's tail ----
       // The CTA that read old rows from the tail (a run continuing a block) is the only one
       // that may then overwrite them, also with the rows of a later block of the same call.
       if (end < BS) {
-        bool mine = true;
+        bool own = true;
         if (row0 == 0 && i > 0 && of_seq(a, i - 1, seq)) {    // a later block: did the sequence start inside one?
           if (warp == 0) {
             const int first = seq_edge(a, i, seq, -1) + 1;
             if (lane == 0) edge_s = first;
           }
           __syncthreads();
-          mine = a.slots[edge_s] % BS == 0;
+          own = a.slots[edge_s] % BS == 0;
         }
-        if (mine) {
-          for (int e = threadIdx.x; e < 2 * m * VPR; e += kQ8Threads) {
-            const int kv = e / (m * VPR), f = e - kv * m * VPR, r = row0 + f / VPR, c = f % VPR;
-            *(reinterpret_cast<uint4*>((kv ? a.v_tail : a.k_tail) + tail0 + (size_t)r * D) + c) =
-                *reinterpret_cast<const uint4*>(rows_s + (kv * BS + r) * ROW + 8 * c);
+        if (own) {
+          for (int e = tid; e < m * VPR; e += NT) {
+            const int r = row0 + e / VPR, c = e % VPR;
+            *(reinterpret_cast<uint4*>(tails + tail0 + (size_t)r * D) + c) = *reinterpret_cast<const uint4*>(rows_s + r * ROW + 8 * c);
           }
         }
       } else if (row0 > 0 && i + m < a.n_tok && of_seq(a, i + m, seq)) {
@@ -193,26 +248,26 @@ __global__ void __launch_bounds__(kQ8Threads) q8_append_kernel(const Q8AppendArg
         __syncthreads();
         const int stop = edge_s, n = (int)(a.slots[stop - 1] % BS) + 1;   // rows of the last block
         if (n < BS && n <= stop - i - m) {
-          for (int e = threadIdx.x; e < 2 * n * VPR; e += kQ8Threads) {
-            const int kv = e / (n * VPR), f = e - kv * n * VPR, r = f / VPR, c = f % VPR;
-            const __nv_bfloat16* x = (kv ? a.v + (long long)(stop - n + r) * a.v_stride
-                                         : a.k + (long long)(stop - n + r) * a.k_stride) + (size_t)g * D;
-            *(reinterpret_cast<uint4*>((kv ? a.v_tail : a.k_tail) + tail0 + (size_t)r * D) + c) =
-                *(reinterpret_cast<const uint4*>(x) + c);
+          for (int e = tid; e < n * VPR; e += NT) {
+            const int r = e / VPR, c = e % VPR;
+            *(reinterpret_cast<uint4*>(tails + tail0 + (size_t)r * D) + c) =
+                *(reinterpret_cast<const uint4*>(x + (long long)(stop - n + r) * stride) + c);
           }
         }
       }
-      __syncthreads();                                        // rows_s, big_s and edge_s are reused
     }
-    i += m;
+    t += m;
+    if (t >= a.span) break;
+    __syncthreads();                                          // the shared arrays are reused
   }
 }
 
 template <int D, int BS>
 static cudaError_t launch_q8(const Q8AppendArgs& a, bool e4m3, cudaStream_t st) {
-  const size_t smem = 2 * BS * (D + 8) * sizeof(__nv_bfloat16);
   const unsigned gx = (unsigned)((a.n_tok + a.span - 1) / a.span);
-  q8_append_kernel<D, BS><<<dim3(gx, (unsigned)a.n_kv), kQ8Threads, smem, st>>>(a, e4m3 ? 1 : 0);
+  const dim3 grid(gx, (unsigned)a.n_kv, 2), block(Q8Shape<D, BS>::NT);
+  if (e4m3) q8_append_kernel<D, BS, true><<<grid, block, 0, st>>>(a);
+  else q8_append_kernel<D, BS, false><<<grid, block, 0, st>>>(a);
   return cudaGetLastError();
 }
 
