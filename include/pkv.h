@@ -333,7 +333,8 @@ pkv_status pkv_rope_init(const pkv_rope_config* config, pkv_rope_table* table);
  *   q_out         bf16, q_out_stride elements between tokens; may be q itself (with its stride)
  *   k_pool,v_pool as for pkv_kv_append
  * The rotation runs in fp32 and rounds once, to nearest even; copied channels and V are
- * bit-exact.  A slot >= num_blocks * block_size sets PKV_DEV_BAD_SLOT and skips the token.
+ * bit-exact.  A slot >= num_blocks * block_size sets PKV_DEV_BAD_SLOT and skips the token.  n_h and
+ * n_kv are at most 1024.
  */
 pkv_status pkv_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                            int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping, int n_tok,

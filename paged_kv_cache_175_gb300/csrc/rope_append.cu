@@ -14,7 +14,9 @@
 // channel pairs in the half layout; 16 neighbouring channels in the interleaved one, and for
 // channels that are only copied).  A CTA takes NI * 256 consecutive items of the flat (token,
 // row, vector) order, issues all its loads first and builds the angle table of its tokens
-// (shared by all their heads) while they are in flight.
+// (shared by all their heads) while they are in flight.  What an item needs besides its data is
+// worked out again for the store: held over the barrier it cost the registers of two CTAs per SM
+// (80 us).
 #include <cmath>
 
 #include "decode_common.cuh"
@@ -32,12 +34,14 @@ struct RopeArgs {
   const int64_t* slots;
   long long n_slots;
   int n_tok, n_h, n_kv, bs_log2;
-  int items_per_tok;                             // (n_h + n_kv (+ n_kv)) * d / 16
+  int items_per_tok;                             // (n_h + n_kv (+ n_kv)) * d / 16, at most 24576
+  uint32_t token_magic;                          // ceil(2^32 / items_per_tok): exact for numerators below 2^17
   int32_t* err;
   pkv_rope_table t;
 };
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeItems = 3;              // per thread in long calls
 
 // u c - v s and u s + v c, the contraction spelled out so that every variant of the kernel
 // rounds alike (a token's result does not depend on the size of the call).
@@ -45,9 +49,9 @@ __device__ __forceinline__ float turn_a(float u, float v, float2 c) { return __f
 __device__ __forceinline__ float turn_b(float u, float v, float2 c) { return __fmaf_rn(u, c.y, __fmul_rn(v, c.x)); }
 
 template <int D, int NI, bool APPEND>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 5) rope_append_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int VP = D / 16;                                  // items per row
-  extern __shared__ float2 angles[];                         // [tokens][rotary_dim / 2]: cos, sin
+  extern __shared__ float2 angles[];                         // [tokens][rotary_dim / 2]: cos, sin; then [tokens] slots
   grid_dep_launch();                       // the attention's setup may overlap this kernel
   const int H = a.t.rotary_dim >> 1, RP = a.t.rotary_dim >> 4;
   const bool inter = a.t.interleaved != 0;
@@ -56,61 +60,50 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
   const int tok0 = (int)(i0 / a.items_per_tok);
   const int off0 = (int)(i0 - (long long)tok0 * a.items_per_tok);
   const int n_here = (int)(total - i0 < NI * kRopeThreads ? total - i0 : NI * kRopeThreads);
-  const int tokens = (off0 + n_here - 1) / a.items_per_tok + 1;
+  const int tokens = (int)__umulhi((uint32_t)(off0 + n_here - 1), a.token_magic) + 1;
+  int64_t* slots_s = reinterpret_cast<int64_t*>(angles + tokens * H);
 
+  // item: its token of the CTA, its row (q heads, k heads, v heads) and its vectors within the row
+  struct Item {
+    int tl, row, p, vec, gap;
+    bool turns;
+  };
+  auto item = [&](int idx) {
+    Item it;
+    const int flat = off0 + idx;
+    it.tl = (int)__umulhi((uint32_t)flat, a.token_magic);
+    const int rem = flat - it.tl * a.items_per_tok;
+    it.row = rem / VP;
+    it.p = rem % VP;
+    it.turns = it.row < a.n_h + a.n_kv && it.p < RP;
+    it.vec = it.turns && !inter ? it.p : 2 * it.p;
+    it.gap = it.turns && !inter ? RP : 1;
+    return it;
+  };
   uint4 x[NI], y[NI];
-  __nv_bfloat16* dst[NI];
-  int rot[NI];                             // place of the item's first angle in the table; -1: copied
-  int gap[NI];                             // vectors from the item's first to its second
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int idx = threadIdx.x + i * kRopeThreads;
-    dst[i] = nullptr;
-    rot[i] = -1;
-    gap[i] = 1;
     if (idx >= n_here) continue;
-    const int flat = off0 + idx, tl = flat / a.items_per_tok, rem = flat - tl * a.items_per_tok;
-    const int row = rem / VP, p = rem - row * VP;
-    const int tok = tok0 + tl;
+    const Item it = item(idx);
+    const long long tok = tok0 + it.tl;
     const __nv_bfloat16* src;
-    int vec = 2 * p;                       // first vector of the item within the row
-    if (row < a.n_h + a.n_kv) {
-      if (p < RP) {
-        rot[i] = tl * H + 8 * p;           // eight pairs of the table, both layouts
-        if (!inter) {
-          vec = p;
-          gap[i] = RP;
-        }
-      }
-    }
-    int64_t slot = 0;
-    if (APPEND) {
-      slot = a.slots[tok];
-      if (slot < 0) continue;              // padding: nothing of this token is written
-      if (slot >= a.n_slots) {
-        if (rem == 0) set_err(a.err, PKV_DEV_BAD_SLOT);
-        continue;
-      }
-    }
-    if (row < a.n_h) {
-      src = a.q + (long long)tok * a.q_stride + (long long)row * D;
-      dst[i] = a.q_out + (long long)tok * a.qo_stride + (long long)row * D;
-    } else {
-      const bool is_k = row < a.n_h + a.n_kv;
-      const int g = row - a.n_h - (is_k ? 0 : a.n_kv);
-      src = is_k ? a.k + (long long)tok * a.k_stride + (long long)g * D : a.v + (long long)tok * a.v_stride + (long long)g * D;
-      if (APPEND) {
-        const long long blk = slot >> a.bs_log2, r = slot & ((1 << a.bs_log2) - 1);
-        dst[i] = (is_k ? a.k_pool : a.v_pool) + ((((blk * a.n_kv + g) << a.bs_log2) + r) * D);
-      } else {
-        dst[i] = a.k_out + (long long)tok * a.ko_stride + (long long)g * D;
-      }
-    }
-    dst[i] += 8 * vec;
-    const uint4* s4 = reinterpret_cast<const uint4*>(src + 8 * vec);
+    if (it.row < a.n_h) src = a.q + tok * a.q_stride + it.row * D;
+    else if (it.row < a.n_h + a.n_kv) src = a.k + tok * a.k_stride + (it.row - a.n_h) * D;
+    else src = a.v + tok * a.v_stride + (it.row - a.n_h - a.n_kv) * D;
+    const uint4* s4 = reinterpret_cast<const uint4*>(src) + it.vec;
     x[i] = s4[0];
-    y[i] = s4[gap[i]];
+    y[i] = s4[it.gap];
   }
+  if (APPEND)
+    for (int e = threadIdx.x; e < tokens; e += kRopeThreads) {
+      int64_t slot = a.slots[tok0 + e];
+      if (slot >= a.n_slots) {
+        if (e > 0 || off0 == 0) set_err(a.err, PKV_DEV_BAD_SLOT);   // by the CTA in which the token begins
+        slot = -1;
+      }
+      slots_s[e] = slot;
+    }
   for (int e = threadIdx.x; e < tokens * H; e += kRopeThreads) {
     const int tl = e / H, j = e - tl * H;
     const uint64_t turn = (uint64_t)(int64_t)a.positions[tok0 + tl] * a.t.turns[j];
@@ -121,9 +114,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    if (!dst[i]) continue;
-    if (rot[i] >= 0) {
-      const float2* cs = angles + rot[i];
+    const int idx = threadIdx.x + i * kRopeThreads;
+    if (idx >= n_here) continue;
+    const Item it = item(idx);
+    if (it.turns) {
+      const float2* cs = angles + it.tl * H + 8 * it.p;       // eight pairs of the table, both layouts
       if (inter) {
         auto turn = [&](uint32_t& w, float2 c) {
           const float u = bf16_lo(w), v = bf16_hi(w);
@@ -141,9 +136,26 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
         turn(x[i].z, y[i].z, cs[4], cs[5]); turn(x[i].w, y[i].w, cs[6], cs[7]);
       }
     }
-    uint4* d4 = reinterpret_cast<uint4*>(dst[i]);
+    const long long tok = tok0 + it.tl;
+    const int64_t slot = APPEND ? slots_s[it.tl] : 0;
+    if (slot < 0) continue;                // padding or flagged: nothing of this token is written
+    __nv_bfloat16* dst;
+    if (it.row < a.n_h) {
+      dst = a.q_out + tok * a.qo_stride + it.row * D;
+    } else {
+      const bool is_k = it.row < a.n_h + a.n_kv;
+      const int g = it.row - a.n_h - (is_k ? 0 : a.n_kv);
+      if (APPEND) {
+        const long long blk = slot >> a.bs_log2;
+        const int r = (int)slot & ((1 << a.bs_log2) - 1);
+        dst = (is_k ? a.k_pool : a.v_pool) + (((blk * a.n_kv + g) << a.bs_log2) + r) * D;
+      } else {
+        dst = a.k_out + tok * a.ko_stride + g * D;
+      }
+    }
+    uint4* d4 = reinterpret_cast<uint4*>(dst) + it.vec;
     d4[0] = x[i];
-    d4[gap[i]] = y[i];
+    d4[it.gap] = y[i];
   }
 }
 
@@ -155,7 +167,7 @@ static cudaError_t launch_rope(const RopeArgs& a, int head_dim, cudaStream_t st)
   // a range of NI * 256 items starts inside a token, so it can touch one more than it fills
   int tokens = (NI * kRopeThreads - 1) / a.items_per_tok + 2;
   if (tokens > a.n_tok) tokens = a.n_tok;
-  const size_t smem = (size_t)tokens * (a.t.rotary_dim / 2) * sizeof(float2);
+  const size_t smem = (size_t)tokens * (a.t.rotary_dim / 2 * sizeof(float2) + sizeof(int64_t));
   if (head_dim == 128) rope_append_kernel<128, NI, APPEND><<<(unsigned)grid, kRopeThreads, smem, st>>>(a);
   else rope_append_kernel<64, NI, APPEND><<<(unsigned)grid, kRopeThreads, smem, st>>>(a);
   return cudaGetLastError();
@@ -163,11 +175,13 @@ static cudaError_t launch_rope(const RopeArgs& a, int head_dim, cudaStream_t st)
 
 template <bool APPEND>
 static cudaError_t launch_rope_any(const RopeArgs& a, int head_dim, cudaStream_t st) {
-  // Items per thread: four in flight hide the memory latency of long calls; a call too small
-  // to give every SM two CTAs of those takes one item per thread and four times the CTAs.
+  // Three items per thread, five CTAs of them per SM, hide the memory latency of long calls: 16384
+  // tokens of 32 + 8 + 8 heads of 128 in 63.0 us (6.4 TB/s, 94% of the measured copy rate); two items
+  // 64.5 (six CTAs) and 69.5 (five), four 66.1 (four CTAs).  A call too small to give every SM two
+  // CTAs of those takes one item per thread and three times the CTAs: 64 tokens in 2.5 us.
   const long long total = (long long)a.n_tok * a.items_per_tok;
   const int sms = device_sm_count() > 0 ? device_sm_count() : 128;
-  if (total >= (long long)sms * 2 * 4 * kRopeThreads) return launch_rope<4, APPEND>(a, head_dim, st);
+  if (total >= (long long)sms * 2 * kRopeItems * kRopeThreads) return launch_rope<kRopeItems, APPEND>(a, head_dim, st);
   return launch_rope<1, APPEND>(a, head_dim, st);
 }
 
@@ -234,7 +248,7 @@ extern "C" pkv_status pkv_rope_append(const void* q, int64_t q_stride, const voi
                                       void* k_pool, void* v_pool, int num_blocks, int block_size, int n_h, int n_kv,
                                       int head_dim, int32_t* err_flag, void* stream) {
   PKV_NVTX("pkv_rope_append");
-  if (n_tok < 0 || num_blocks < 0 || n_h <= 0 || n_kv <= 0 || n_h > 65536 || n_kv > 65536) return PKV_EINVAL;
+  if (n_tok < 0 || num_blocks < 0 || n_h <= 0 || n_kv <= 0 || n_h > 1024 || n_kv > 1024) return PKV_EINVAL;
   if (head_dim != 64 && head_dim != 128) return PKV_EINVAL;
   if (block_size != 16 && block_size != 32 && block_size != 64) return PKV_EINVAL;
   if (!valid_table(table, head_dim)) return PKV_EINVAL;
@@ -260,6 +274,7 @@ extern "C" pkv_status pkv_rope_append(const void* q, int64_t q_stride, const voi
   a.n_tok = n_tok; a.n_h = n_h; a.n_kv = n_kv;
   a.bs_log2 = block_size == 16 ? 4 : (block_size == 32 ? 5 : 6);
   a.items_per_tok = (n_h + 2 * n_kv) * (head_dim / 16);
+  a.token_magic = (uint32_t)((0x100000000ull + a.items_per_tok - 1) / a.items_per_tok);
   a.err = err_flag;
   a.t = *table;
   const cudaError_t e = launch_rope_any<true>(a, head_dim, static_cast<cudaStream_t>(stream));
@@ -275,7 +290,7 @@ extern "C" pkv_status pkv_rope_qk(const void* q, int64_t q_stride, const void* k
                                   int64_t q_out_stride, void* k_out, int64_t k_out_stride, int n_h, int n_kv,
                                   int head_dim, void* stream) {
   PKV_NVTX("pkv_rope_qk");
-  if (n_tok < 0 || n_h <= 0 || n_kv <= 0 || n_h > 65536 || n_kv > 65536) return PKV_EINVAL;
+  if (n_tok < 0 || n_h <= 0 || n_kv <= 0 || n_h > 1024 || n_kv > 1024) return PKV_EINVAL;
   if (head_dim != 64 && head_dim != 128) return PKV_EINVAL;
   if (!valid_table(table, head_dim)) return PKV_EINVAL;
   if (n_tok == 0) return PKV_OK;
@@ -295,6 +310,7 @@ extern "C" pkv_status pkv_rope_qk(const void* q, int64_t q_stride, const void* k
   a.positions = positions;
   a.n_tok = n_tok; a.n_h = n_h; a.n_kv = n_kv;
   a.items_per_tok = (n_h + n_kv) * (head_dim / 16);
+  a.token_magic = (uint32_t)((0x100000000ull + a.items_per_tok - 1) / a.items_per_tok);
   a.t = *table;
   const cudaError_t e = launch_rope_any<false>(a, head_dim, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) {
