@@ -43,7 +43,7 @@ struct EvictArgs {
   long long stride;
   int batch, n_kv, max_blocks, max_ctx, bs_log2, recent, num_blocks;
   int* counts;                   // workspace: [batch * n_kv] rows to move
-  int2* moves;                   // workspace: [batch * n_kv][max_ctx / 2 + 1]: x destination, y source
+  int32_t *dst, *src;            // workspace: [batch * n_kv][max_ctx / 2 + 1]: rows of the moves
   int max_moves;
   uint4 *k_pool, *v_pool;
   int32_t* err;
@@ -91,6 +91,7 @@ template <> struct PairOf<false> { using type = unsigned long long; };
 // NT threads of R rows, R a multiple of 4 (0: any number, keys read again whenever they are used).
 template <int NT, int R>
 __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) evict_select_kernel(const EvictArgs a) {
+  grid_dep_launch();                       // the move kernel's launch overlaps; it waits for this grid
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
   // with R > 0 a bin counts at most 16384 rows of the CTA: two bins to a word
@@ -103,6 +104,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) evict_select_kernel(con
   __shared__ int sums_s[NT / 32];
   __shared__ Pair share[2];                                   // this CTA's counts, read by the cluster
   __shared__ int pick[3];
+  __shared__ uint16_t stage[R > 0 ? NT * R : 1];
   const int sg = blockIdx.x / ranks, s = sg / a.n_kv;
   const int raw = a.ctx[s], n = clamp_ctx(raw, a.max_ctx);
   const int K = max(0, min(a.keep[s], n));
@@ -322,26 +324,36 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) evict_select_kernel(con
     });
   }
   const Pair local = cta_scan<NT, Pair>(mine, warp_s, total);
-  uint64_t at = widen(local), moves_all = widen(total);
+  uint64_t first = 0, moves_all = widen(total);               // of the cluster, before this CTA; in all
   if (ranks > 1) {
     if (threadIdx.x == 0) share[1] = total;
     meet();
-    at += over_cluster(1, moves_all);
+    first = over_cluster(1, moves_all);
   }
   if (rank == 0 && threadIdx.x == 0) a.counts[sg] = (int)(moves_all >> 32);
-  int2* moves = a.moves + (size_t)sg * a.max_moves;
-  uint32_t h_at = (uint32_t)at, m_at = (uint32_t)(at >> 32);
+  int32_t* dst = a.dst + (size_t)sg * a.max_moves;
+  int32_t* src = a.src + (size_t)sg * a.max_moves;
   if constexpr (R > 0) {
-    for (; hole_bits; hole_bits &= hole_bits - 1) moves[h_at++].x = r0 + __ffs(hole_bits) - 1;
-    for (; mover_bits; mover_bits &= mover_bits - 1) moves[m_at++].y = r0 + __ffs(mover_bits) - 1;
+    // through shared memory, so that the lists leave in whole lines (each thread's own entries lie
+    // apart from the next lane's: written directly they took 6 us of a 131072-row selection)
+    const int c0 = rank * NT * R, holes = (int)(uint32_t)widen(total), movers = (int)(widen(total) >> 32);
+    int h = (int)(uint32_t)widen(local), mv = holes + (int)(widen(local) >> 32);
+    for (; hole_bits; hole_bits &= hole_bits - 1) stage[h++] = (uint16_t)(r0 - c0 + __ffs(hole_bits) - 1);
+    for (; mover_bits; mover_bits &= mover_bits - 1) stage[mv++] = (uint16_t)(r0 - c0 + __ffs(mover_bits) - 1);
+    __syncthreads();
+    int32_t *d = dst + (uint32_t)first, *q = src + (first >> 32);
+    for (int i = threadIdx.x; i < holes; i += NT) d[i] = c0 + stage[i];
+    for (int i = threadIdx.x; i < movers; i += NT) q[i] = c0 + stage[holes + i];
   } else {
+    const uint64_t at = widen(local) + first;
+    uint32_t h_at = (uint32_t)at, m_at = (uint32_t)(at >> 32);
     e = e0;
     rows([&](int r, uint32_t k) {
       const bool st = stays(k);
       if (r < K) {
-        if (!st) moves[h_at++].x = r;
+        if (!st) dst[h_at++] = r;
       } else if (st) {
-        moves[m_at++].y = r;
+        src[m_at++] = r;
       }
     });
   }
@@ -355,11 +367,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) evict_select_kernel(con
   const int n_moves = (int)(moves_all >> 32);
 #pragma unroll 4
   for (int i = rank * NT + threadIdx.x; i < n_moves; i += ranks * NT) {
-    const int2 mv = moves[i];
-    const float x = mass[mv.y];
-    const int p = position(mv.y);
-    mass_out[mv.x] = x;
-    pos_out[mv.x] = p;
+    const int to = dst[i], from = src[i];
+    const float x = mass[from];
+    const int p = position(from);
+    mass_out[to] = x;
+    pos_out[to] = p;
   }
   if (a.in_place) meet();                                     // every mover's account was read
   for (int r = K + rank * NT + threadIdx.x; r < n; r += ranks * NT) mass_out[r] = 0.f;
@@ -380,7 +392,8 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a, cons
     a.kept_out[s] = K < n ? K : a.kept[s];
   }
   const int count = a.counts[sg];
-  const int2* moves = a.moves + (size_t)sg * a.max_moves;
+  const int32_t* dst = a.dst + (size_t)sg * a.max_moves;
+  const int32_t* src = a.src + (size_t)sg * a.max_moves;
   const int32_t* bt = a.bt + (size_t)s * a.max_blocks;
   const int low = (1 << a.bs_log2) - 1;
   // a row's K takes V lanes and its V row the V lanes behind them; with D = 64 a warp holds two moves
@@ -404,10 +417,9 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a, cons
       const int i = i0 + u * PER + which;
       d[u] = nullptr;
       if (i < count) {
-        const int2 mv = moves[i];
         bool ok = true;
-        uint4* to = row(mv.x, ok);
-        const uint4* from = row(mv.y, ok);
+        uint4* to = row(dst[i], ok);
+        const uint4* from = row(src[i], ok);
         if (ok) {
           d[u] = to;
           x[u] = *from;
@@ -421,14 +433,16 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a, cons
 }
 
 struct EvictLayout {
-  size_t moves, total;
+  size_t dst, src, total;
   int max_moves;
 };
 static EvictLayout evict_layout(int batch, int n_kv, long long max_ctx) {
   EvictLayout w;
   w.max_moves = (int)(max_ctx / 2 + 1);                       // movers and holes lie on both sides of K
-  w.moves = align_up(sizeof(int) * (size_t)batch * n_kv, 256);
-  w.total = align_up(w.moves + sizeof(int2) * (size_t)batch * n_kv * w.max_moves, 256);
+  const size_t list = sizeof(int32_t) * (size_t)batch * n_kv * w.max_moves;
+  w.dst = align_up(sizeof(int) * (size_t)batch * n_kv, 256);
+  w.src = align_up(w.dst + list, 256);
+  w.total = align_up(w.src + list, 256);
   return w;
 }
 
@@ -482,7 +496,8 @@ extern "C" pkv_status pkv_kv_evict(void* k_pool, void* v_pool, const int32_t* bl
   a.bs_log2 = block_size == 16 ? 4 : (block_size == 32 ? 5 : 6);
   a.recent = recent; a.num_blocks = num_blocks;
   a.counts = reinterpret_cast<int*>(ws);
-  a.moves = reinterpret_cast<int2*>(ws + w.moves);
+  a.dst = reinterpret_cast<int32_t*>(ws + w.dst);
+  a.src = reinterpret_cast<int32_t*>(ws + w.src);
   a.max_moves = w.max_moves;
   a.k_pool = static_cast<uint4*>(k_pool);
   a.v_pool = static_cast<uint4*>(v_pool);
