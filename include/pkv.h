@@ -355,8 +355,8 @@ pkv_status pkv_rope_qk(const void* q, int64_t q_stride, const void* k, int64_t k
  *
  * kv_quant_append_q8 — quantize-on-append.  Exact op sequence, in fp32, per (block, kv head) and
  * for K and V apart, over the rows that the block holds after the call:
- *   big = max |x|;  scale = big / M and inv = M / big (nearest), M = 448 (PKV_Q8_E4M3) or 127
- *   (PKV_Q8_INT8); both are 0 when big < 2^-110
+ *   big = max |x|;  scale = big * (1 / M) and inv = (1 / big) * M, each operation rounded to
+ *   nearest, M = 448 (PKV_Q8_E4M3) or 127 (PKV_Q8_INT8); both are 0 when big < 2^-110
  *   code = e4m3(x * inv), nearest even, saturating; or rint(x * inv) clamped to +-127
  * and the value held is code * scale.  A block's codes depend on its rows alone, not on the calls
  * that brought them: the bf16 rows of a sequence's unfinished block are kept in k_tail / v_tail,

@@ -1,8 +1,8 @@
 """8-bit paged cache: one scale per (block, kv head) for K and for V.  Test infrastructure only.
 
 The quantizer follows a stated float32 op sequence, so its codes are bit-exact by construction:
-big = max |x| over the rows the block holds; scale = big / M and inv = M / big in float32 (both 0
-when big < 2^-110); code = x * inv in float32, rounded to the format (nearest even): e4m3 with
+big = max |x| over the rows the block holds; scale = big * (1 / M) and inv = (1 / big) * M, each
+operation in float32 (both 0 when big < 2^-110); code = x * inv in float32, rounded to the format (nearest even): e4m3 with
 saturation (M = 448), or integers in [-127, 127] (M = 127).  The value held is code * scale.
 """
 import numpy as np
@@ -28,7 +28,8 @@ def quantize_rows(x, fmt):
     if not big >= np.float32(2.0 ** -110):
         return np.zeros(x.shape), np.float32(0)
     m = np.float32(MOST[fmt])
-    scale, inv = np.float32(big / m), np.float32(m / big)
+    one = np.float32(1)
+    scale, inv = np.float32(big * np.float32(one / m)), np.float32(np.float32(one / big) * m)
     y = (x * inv).astype(np.float32)
     if fmt == "e4m3":
         return round_e4m3(y), scale

@@ -1,8 +1,8 @@
 // Quantize-on-append into the 8-bit paged cache (record layout: q8_common.cuh).
 //
 // Mathematics, per (block, kv head) and for K and V apart: big = max |x| over the rows that the
-// block holds; scale = big / M, code = round_to_nearest_even(x * (M / big)), M = 448 (e4m3) or
-// 127 (int8), every operation in fp32.  The result is a function of the rows alone, not of how
+// block holds; scale = big * (1 / M), code = round_to_nearest_even(x * ((1 / big) * M)), M = 448
+// (e4m3) or 127 (int8), every operation rounded to fp32.  The result is a function of the rows alone, not of how
 // many calls brought them: the bf16 rows of a sequence's unfinished block are kept in its tail
 // and the record is written anew from them at each append, so the attention reads records only
 // and a finished block was rounded once.
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(Q8Shape<D, BS>::NT) q8_append_kernel(const Q8A
 #pragma unroll
       for (int k = 0; k < NT / 32; ++k) big = fmaxf(big, big_s[k]);
       const bool some = big >= kQ8Tiny;
-      const float scale = some ? __fdiv_rn(big, most) : 0.f, inv = some ? __fdiv_rn(most, big) : 0.f;
+      const float scale = some ? __fmul_rn(big, __fdiv_rn(1.f, most)) : 0.f, inv = some ? __fmul_rn(__fdiv_rn(1.f, big), most) : 0.f;
       uint8_t* codes = rec + (values ? BS * D : 0);
       if (!values) {
 #pragma unroll

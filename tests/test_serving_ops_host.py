@@ -89,9 +89,10 @@ def test_quantize_rows_error_is_half_a_step(fmt):
     big = np.abs(x).max()
     # int8: half a unit of big / 127; e4m3: 2^-4 of the value, or half the subnormal step 2^-9
     step = big / 127 / 2 if fmt == "int8" else np.maximum(np.abs(x) * 2.0 ** -4, 2.0 ** -10 * float(s))
-    # and three float32 roundings of the value: inv = M / big and x * inv move the point that is
-    # rounded by |x| 2^-24 each (in units of the value), scale = big / M the value held by as much
-    tol = step + np.abs(x) * (3 * 2.0 ** -24 * (1 + 1e-6))
+    # and five float32 roundings of the value: 1 / big, its product with M and x * inv move the point
+    # that is rounded by |x| 2^-24 each (in units of the value), 1 / M and its product with big the
+    # value held by as much
+    tol = step + np.abs(x) * (5 * 2.0 ** -24 * (1 + 1e-6))
     assert np.all(np.abs(held - x) <= tol) and np.abs(held).max() >= big * (1 - 1e-6)
     z, s0 = oracle.quantize_rows(np.full((4, 4), 2.0 ** -111), fmt)
     assert s0 == 0 and not z.any()
