@@ -89,11 +89,12 @@ template <bool SMALL> struct PairOf { using type = uint32_t; };
 template <> struct PairOf<false> { using type = unsigned long long; };
 
 // NT threads of R rows, R a multiple of 4 (0: any number, keys read again whenever they are used).
-template <int NT, int R>
-__global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) evict_select_kernel(const EvictArgs a) {
+// CLUSTER: several CTAs may share a (sequence, kv head).
+template <int NT, int R, bool CLUSTER>
+__global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const EvictArgs a) {
   grid_dep_launch();                       // the move kernel's launch overlaps; it waits for this grid
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+  const int rank = CLUSTER ? (int)cluster.block_rank() : 0, ranks = CLUSTER ? (int)cluster.num_blocks() : 1;
   // with R > 0 a bin counts at most 16384 rows of the CTA: two bins to a word
   constexpr int kPack = R > 0 ? 1 : 0;
   __shared__ __align__(16) uint32_t hist[2][kEvBins >> kPack];
@@ -199,70 +200,76 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) evict_select_kernel(con
       // buffer of the next round but one: its last readers passed the barrier above
       if (round == 1)
         for (int b = threadIdx.x; b < (1024 >> kPack); b += NT) hist[0][b] = 0;
-      // warp w takes the w-th run of bins from the top and lane l the l-th run of those; only the
-      // warp that holds the wanted rank looks for its bin
-      constexpr int kRun[3] = {2048 / NT, 2048 / NT, 1024 / NT};
-      const int nb = kRun[round], b0 = bins - nb * ((int)threadIdx.x + 1);
-      int c[kRun[0]] = {};
-      const int w0 = b0 >> kPack, nw = kPack ? (nb + 1) / 2 : nb;   // words of the run
-      auto add = [&](int j, uint32_t v) {
-        if (!kPack) c[j] += (int)v;
-        else if (nb == 1) c[0] += (int)(v >> (16 * (b0 & 1)) & 0xffffu);
-        else {
-          c[2 * j] += (int)(v & 0xffffu);
-          c[2 * j + 1] += (int)(v >> 16);
-        }
-      };
-      if (ranks == 1) {
-#pragma unroll
-        for (int j = 0; j < nw; ++j) add(j, h[w0 + j]);
-      } else {
-        constexpr int kGroup = NT == 1024 ? 8 : 4;            // CTAs whose loads are in flight together
-        for (int q0 = 0; q0 < ranks; q0 += kGroup) {
-          uint32_t d[kGroup][kRun[0]];
-#pragma unroll
-          for (int q = 0; q < kGroup; ++q) {
-            const uint32_t* hq = cluster.map_shared_rank(h, q0 + q < ranks ? q0 + q : 0);
-#pragma unroll
-            for (int j = 0; j < nw; ++j) d[q][j] = q0 + q < ranks ? hq[w0 + j] : 0u;
+      // CTA 0 of the cluster sums the histograms and finds the bin (every CTA reading all of them
+      // took 14 us a round with 64 clusters of eight at work, 70 us in all against 38): warp w takes the w-th run of bins
+      // from the top and lane l the l-th run of those; only the warp that holds the wanted rank looks
+      // for its bin
+      if (rank == 0) {
+        constexpr int kRun[3] = {2048 / NT, 2048 / NT, 1024 / NT};
+        const int nb = kRun[round], b0 = bins - nb * ((int)threadIdx.x + 1);
+        int c[kRun[0]] = {};
+        const int w0 = b0 >> kPack, nw = kPack ? (nb + 1) / 2 : nb;   // words of the run
+        auto add = [&](int j, uint32_t v) {
+          if (!kPack) c[j] += (int)v;
+          else if (nb == 1) c[0] += (int)(v >> (16 * (b0 & 1)) & 0xffffu);
+          else {
+            c[2 * j] += (int)(v & 0xffffu);
+            c[2 * j + 1] += (int)(v >> 16);
           }
+        };
+        if (ranks == 1) {
 #pragma unroll
-          for (int q = 0; q < kGroup; ++q)
+          for (int j = 0; j < nw; ++j) add(j, h[w0 + j]);
+        } else {
+          constexpr int kGroup = NT == 1024 ? 8 : 4;            // CTAs whose loads are in flight together
+          for (int q0 = 0; q0 < ranks; q0 += kGroup) {
+            uint32_t d[kGroup][kRun[0]];
 #pragma unroll
-            for (int j = 0; j < nw; ++j) add(j, d[q][j]);
+            for (int q = 0; q < kGroup; ++q) {
+              const uint32_t* hq = cluster.map_shared_rank(h, q0 + q < ranks ? q0 + q : 0);
+#pragma unroll
+              for (int j = 0; j < nw; ++j) d[q][j] = q0 + q < ranks ? hq[w0 + j] : 0u;
+            }
+#pragma unroll
+            for (int q = 0; q < kGroup; ++q)
+#pragma unroll
+              for (int j = 0; j < nw; ++j) add(j, d[q][j]);
+          }
+        }
+        int sum = 0;
+#pragma unroll
+        for (int j = 0; j < nb; ++j) sum += c[j];
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int warp_sum = __reduce_add_sync(FULL_MASK, sum);
+        if (lane == 0) sums_s[warp] = warp_sum;
+        __syncthreads();
+        const int ahead = __reduce_add_sync(FULL_MASK, lane < warp ? sums_s[lane] : 0);
+        if (ahead < want && want <= ahead + warp_sum) {
+          int incl = sum;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(FULL_MASK, incl, o);
+            if (lane >= o) incl += y;
+          }
+          int at = ahead + incl - sum;
+#pragma unroll
+          for (int j = nb - 1; j >= 0; --j) {
+            if (at < want && want <= at + c[j]) {
+              pick[0] = b0 + j;
+              pick[1] = want - at;
+              pick[2] = c[j];
+            }
+            at += c[j];
+          }
         }
       }
-      int sum = 0;
-#pragma unroll
-      for (int j = 0; j < nb; ++j) sum += c[j];
-      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-      const int warp_sum = __reduce_add_sync(FULL_MASK, sum);
-      if (lane == 0) sums_s[warp] = warp_sum;
-      __syncthreads();
-      const int ahead = __reduce_add_sync(FULL_MASK, lane < warp ? sums_s[lane] : 0);
-      if (ahead < want && want <= ahead + warp_sum) {
-        int incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(FULL_MASK, incl, o);
-          if (lane >= o) incl += y;
-        }
-        int at = ahead + incl - sum;
-#pragma unroll
-        for (int j = nb - 1; j >= 0; --j) {
-          if (at < want && want <= at + c[j]) {
-            pick[0] = b0 + j;
-            pick[1] = want - at;
-            pick[2] = c[j];
-          }
-          at += c[j];
-        }
-      }
-      __syncthreads();
-      prefix |= (uint32_t)pick[0] << shift;
+      meet();
+      const int* found = CLUSTER && ranks > 1 ? cluster.map_shared_rank(pick, 0) : pick;
+      const int bin = found[0], rest = found[1], size = found[2];
+      prefix |= (uint32_t)bin << shift;
       mask |= (uint32_t)(bins - 1) << shift;
-      want = pick[1];
-      all_equal = pick[1] == pick[2];
+      want = rest;
+      all_equal = rest == size;
     }
   }
   // prefix is the K-th largest key; of the rows equal to it the `want` lowest are kept
@@ -508,18 +515,28 @@ extern "C" pkv_status pkv_kv_evict(void* k_pool, void* v_pool, const int32_t* bl
   const int sms = device_sm_count() > 0 ? device_sm_count() : 128;
   const long long pairs = (long long)batch * n_kv;
   a.vec = stride % 4 == 0 && !((reinterpret_cast<uintptr_t>(mass) | reinterpret_cast<uintptr_t>(positions)) & 15u);
-  // CTAs per (sequence, kv head): of 256 threads (4096 rows, four CTAs per SM), as many as it takes
-  // while all of them are resident; else of 1024 threads (16384 rows); at most eight
-  int ranks = 1;
-  while (ranks < 8 && max_ctx > 256LL * kEvRows * ranks && (pairs * ranks * 2 <= 4LL * sms || max_ctx > 1024LL * kEvRows * ranks))
-    ranks *= 2;
-  const bool small = max_ctx <= 256LL * kEvRows * ranks;
-  const void* fn = small ? (const void*)evict_select_kernel<256, kEvRows>
-                         : (max_ctx <= 1024LL * kEvRows * ranks ? (const void*)evict_select_kernel<1024, kEvRows>
-                                                                : (const void*)evict_select_kernel<1024, 0>);
+  // CTAs per (sequence, kv head): one of 256 threads for up to 4096 rows (four per SM), a cluster of
+  // up to eight of them for up to 32768, else eight of 1024 threads (131072 rows; beyond that the keys
+  // are read again in every round).  256 pairs of 9000 rows: two CTAs of 1024 threads (one per SM)
+  // 62 us, four of 256 threads 49; 2048 pairs of 2000 rows: 44 us with 256 as with 128 threads.
+  int threads, ranks = 1;
+  const void* fn;
+  if (max_ctx <= 256LL * kEvRows) {
+    threads = 256;
+    fn = (const void*)evict_select_kernel<256, kEvRows, false>;
+  } else if (max_ctx <= 8 * 256LL * kEvRows) {
+    threads = 256;
+    while (max_ctx > 256LL * kEvRows * ranks) ranks *= 2;
+    fn = (const void*)evict_select_kernel<256, kEvRows, true>;
+  } else {
+    threads = 1024;
+    ranks = 8;
+    fn = max_ctx <= 8 * 1024LL * kEvRows ? (const void*)evict_select_kernel<1024, kEvRows, true>
+                                         : (const void*)evict_select_kernel<1024, 0, true>;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(pairs * ranks));
-  cfg.blockDim = dim3(small ? 256 : 1024);
+  cfg.blockDim = dim3(threads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
