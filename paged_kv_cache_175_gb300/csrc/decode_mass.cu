@@ -21,6 +21,7 @@
 #include <mutex>
 
 
+
 #include "decode_mass.cuh"
 #include "nvtx_range.h"
 #include "piece_streams.cuh"
@@ -44,7 +45,7 @@ __device__ __forceinline__ uint32_t keep_rows(uint32_t b, int t, int ntok) {
 // TT: 16-token units per stage; NH n-tiles of 8 heads per consumer warp, MT consumer warps per
 // stream, NW streams.  sub: log2 of the units per table block.
 template <int D, int TT, int NH, int MT, int NW>
-__global__ void __launch_bounds__((NW * MT + 1) * 32)
+__global__ void __launch_bounds__((NW * MT + 1) * 32, NH == 2 ? 2 : 1)
     decode_mass_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                        const DecodeArgs a, const MassArgs ms, const int sub) {
   constexpr int KS = D / 16, MD = D / 16, HW = 8 * NH, NBOX = D / 64;
@@ -364,7 +365,7 @@ static void mass_pick(int tiling, MassVariant& v) {
     v.warps = nw * mt + 1;
   };
   if (tiling == 0) set((const void*)decode_mass_kernel<D, TT, 1, 1, 3>, 1, 3);
-  else if (tiling == 1) set((const void*)decode_mass_kernel<D, TT, 1, 2, 3>, 2, 3);
+  else if (tiling == 1) set((const void*)decode_mass_kernel<D, TT, 2, 1, 3>, 1, 3);
   else if (tiling == 2) set((const void*)decode_mass_kernel<D, TT, 2, 2, 2>, 2, 2);
   else set((const void*)decode_mass_kernel<D, TT, 2, 4, 1>, 4, 1);
 }
@@ -378,7 +379,7 @@ static MassVariant* lookup_mass(int D, int tiling) {
   std::lock_guard<std::mutex> lock(mu);
   MassVariant& v = table[di][tiling];
   if (!ready[di][tiling]) {
-    const bool wide = D == 128 && tiling >= 2;
+    const bool wide = D == 128 && tiling >= 1;
     const int stage = wide ? 16384 : 8192;
     if (D == 128) wide ? mass_pick<128, 2>(tiling, v) : mass_pick<128, 1>(tiling, v);
     else mass_pick<64, 2>(tiling, v);

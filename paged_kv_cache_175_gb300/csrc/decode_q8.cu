@@ -6,9 +6,12 @@
 // exactly (e4m3 and small integers are fp16 values).  q is bf16; each head's q is multiplied by
 // a power of two that puts its largest value at 2^14, so that every value above 2^-31 of the
 // largest is exact in fp16 (and the rest is off by 2^-39 of the largest at most); the power is
-// taken out of the scores again.  p enters as a high + low pair of fp16 of 128 p (128: p <= 2^8
-// by the lazy offset, so 2^15 at most, and the smallest step is 2^-31 of p = 1), which carries
-// 22 bits.  Softmax, sums and outputs are fp32.
+// taken out of the scores again.  p enters as fp16 of 128 p (128: p <= 2^8 by the lazy offset, so
+// 2^15 at most, and the smallest step is 2^-31 of p = 1): as a high + low pair, 22 bits, for fp32
+// outputs and for groups of up to four heads, where the pair is free; rounded once (2^-12 of p at
+// most, against the 2^-9 of the output's own rounding) for bf16 outputs of larger groups, whose
+// kernels are bound by the products: 32 heads on one kv head 54.8 -> 38.1 us, 64 heads 97.8 -> 62.0
+// (64 x 2-8K tokens).  Softmax, sums and outputs are fp32.
 //
 // Structure: the persistent grid and the line of blocks of decode_common.cuh, NW streams per CTA
 // (piece_streams.cuh).  A stage is 32 tokens: two records of 16 tokens, one of 32, or half of a
@@ -19,6 +22,7 @@
 #include <cmath>
 #include <cstdlib>
 #include <mutex>
+
 
 #include "nvtx_range.h"
 #include "piece_streams.cuh"
@@ -80,8 +84,8 @@ __host__ __device__ constexpr size_t q8_smem_bytes(int streams, int stages, int 
 // NH n-tiles of 8 heads per consumer warp, MT consumer warps per stream, NW streams.
 // COMB (groups of up to 4 heads): column n of the n-tile holds head n % 4; columns 0-3 carry the
 // high parts of p and columns 4-7 the low parts, so the pair costs one product.
-template <int D, int NH, int MT, int NW, bool E4M3, bool COMB>
-__global__ void __launch_bounds__((NW * MT + 1) * 32) decode_q8_kernel(const DecodeArgs a, const int sub) {
+template <int D, int NH, int MT, int NW, bool E4M3, bool COMB, bool PAIR>
+__global__ void __launch_bounds__((NW * MT + 1) * 32, NH == 2 ? 2 : 4) decode_q8_kernel(const DecodeArgs a, const int sub) {
   constexpr int KS = D / 16, MD = D / 16, HW = 8 * NH, TT = kQ8Rows / 16;
   static_assert(!COMB || (NH == 1 && MT == 1), "one n-tile holds the whole group");
   extern __shared__ uint8_t smem_raw[];
@@ -295,7 +299,7 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32) decode_q8_kernel(const Dec
           }
       }
       // ---- O^T += s_v C_v^T P^T ----
-      uint32_t bh[TT][NH][2], bl[COMB ? 1 : TT][NH][2];
+      uint32_t bh[TT][NH][2], bl[PAIR && !COMB ? TT : 1][NH][2];
 #pragma unroll
       for (int t = 0; t < TT; ++t)
 #pragma unroll
@@ -304,13 +308,9 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32) decode_q8_kernel(const Dec
           for (int r = 0; r < 2; ++r) {
             const float x = sc[t][nh][2 * r], y = sc[t][nh][2 * r + 1];
             const uint32_t hi = pack_f16(x, y);
-            const uint32_t lo = pack_f16(x - h2_lo(hi), y - h2_hi(hi));
-            if constexpr (COMB) {
-              bh[t][nh][r] = movmatrix_t(tig < 2 ? hi : lo);
-            } else {
-              bh[t][nh][r] = movmatrix_t(hi);
-              bl[t][nh][r] = movmatrix_t(lo);
-            }
+            const uint32_t lo = PAIR ? pack_f16(x - h2_lo(hi), y - h2_hi(hi)) : 0u;
+            bh[t][nh][r] = movmatrix_t(COMB && tig >= 2 ? lo : hi);
+            if constexpr (PAIR && !COMB) bl[t][nh][r] = movmatrix_t(lo);
           }
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32) decode_q8_kernel(const Dec
             for (int nh = 0; nh < NH; ++nh) {
               float acc[4] = {0.f, 0.f, 0.f, 0.f};
               mma_f16(acc, va, bh[t][nh][0], bh[t][nh][1]);
-              if constexpr (!COMB) mma_f16(acc, va, bl[t][nh][0], bl[t][nh][1]);
+              if constexpr (PAIR && !COMB) mma_f16(acc, va, bl[t][nh][0], bl[t][nh][1]);
 #pragma unroll
               for (int i = 0; i < 4; ++i) o[2 * j + h][nh][i] = fmaf(sv[t], acc[i], o[2 * j + h][nh][i]);
             }
@@ -416,35 +416,43 @@ constexpr size_t kQ8MaxSmem = 200 * 1024;
 
 // Three streams and their producer warp fill an SM's registers at four CTAs of 128 registers: 12
 // consumer warps.  32/8 heads of 128, 64 sequences of 512-4096 tokens in e4m3 / 32 of 8-32K in int8:
-// 55.1 / 205 us (81% / 96% of the measured copy rate), with four streams 55.3 / 208, with six 56.4 /
-// 218; a producer warp per consumer warp and 64-token stages (six consumers per SM) took 72.7 / 324.
-// A third stage costs consumers their shared memory: 55.7 / 212.
-template <int D, bool E4M3>
+// 55 / 205 us (81% / 96% of the measured copy rate), with four streams 55.3 / 208, with six 56.4 /
+// 218, at three CTAs 55 / 215; a producer warp per consumer warp and 64-token stages (six consumers
+// per SM) took 72.7 / 324.  A third ring stage costs consumers their shared memory: 55.7 / 212.
+// Larger groups: 16 heads per consumer warp (two n-tiles share the converted codes), 32/2 heads 26.3
+// us against 32.7 with two warps of 8; two CTAs per SM (three were slower: fewer registers, spills).
+template <int D, bool E4M3, bool PAIR>
 static void q8_pick(int G, Q8Variant& v) {
   auto set = [&](const void* fn, int mt, int nw) {
     v.fn = fn;
     v.streams = nw;
     v.warps = nw * mt + 1;
   };
-  if (G <= 4) set((const void*)decode_q8_kernel<D, 1, 1, 3, E4M3, true>, 1, 3);
-  else if (G <= 8) set((const void*)decode_q8_kernel<D, 1, 1, 3, E4M3, false>, 1, 3);
-  else if (G <= 16) set((const void*)decode_q8_kernel<D, 1, 2, 3, E4M3, false>, 2, 3);
-  else if (G <= 32) set((const void*)decode_q8_kernel<D, 2, 2, 2, E4M3, false>, 2, 2);
-  else set((const void*)decode_q8_kernel<D, 2, 4, 1, E4M3, false>, 4, 1);
+  if (G <= 4) set((const void*)decode_q8_kernel<D, 1, 1, 3, E4M3, true, true>, 1, 3);
+  else if (G <= 8) set((const void*)decode_q8_kernel<D, 1, 1, 3, E4M3, false, PAIR>, 1, 3);
+  else if (G <= 16) set((const void*)decode_q8_kernel<D, 2, 1, 3, E4M3, false, PAIR>, 1, 3);
+  else if (G <= 32) set((const void*)decode_q8_kernel<D, 2, 2, 2, E4M3, false, PAIR>, 2, 2);
+  else set((const void*)decode_q8_kernel<D, 2, 4, 1, E4M3, false, PAIR>, 4, 1);
 }
 static int q8_variant_index(int G) { return G <= 4 ? 0 : head_tiling(G) + 1; }
 
-static Q8Variant* lookup_q8(int D, int BS, int G, bool e4m3) {
+static Q8Variant* lookup_q8(int D, int BS, int G, bool e4m3, bool pair) {
   // One table per process; the library drives one device per process.
   static std::mutex mu;
-  static Q8Variant table[2][2][5][2];
-  static bool ready[2][2][5][2] = {};
+  static Q8Variant table[2][2][5][2][2];
+  static bool ready[2][2][5][2][2] = {};
   const int di = D == 128 ? 1 : 0, bi = BS == 16 ? 0 : 1, vi = q8_variant_index(G), fi = e4m3 ? 1 : 0;
   std::lock_guard<std::mutex> lock(mu);
-  Q8Variant& v = table[di][bi][vi][fi];
-  if (!ready[di][bi][vi][fi]) {
-    if (D == 128) e4m3 ? q8_pick<128, true>(G, v) : q8_pick<128, false>(G, v);
-    else e4m3 ? q8_pick<64, true>(G, v) : q8_pick<64, false>(G, v);
+  const int pi = pair || G <= 4 ? 1 : 0;
+  Q8Variant& v = table[di][bi][vi][fi][pi];
+  if (!ready[di][bi][vi][fi][pi]) {
+    if (D == 128) {
+      if (e4m3) pi ? q8_pick<128, true, true>(G, v) : q8_pick<128, true, false>(G, v);
+      else pi ? q8_pick<128, false, true>(G, v) : q8_pick<128, false, false>(G, v);
+    } else {
+      if (e4m3) pi ? q8_pick<64, true, true>(G, v) : q8_pick<64, true, false>(G, v);
+      else pi ? q8_pick<64, false, true>(G, v) : q8_pick<64, false, false>(G, v);
+    }
     const int unit = BS == 16 ? 16 : 32, stage = kQ8Rows / unit * q8_record_bytes(unit, D);
     v.stages = ring_stages(stage, 2 * stage, "PKV_STAGES_Q8");
     v.smem = q8_smem_bytes(v.streams, v.stages, stage);
@@ -456,7 +464,7 @@ static Q8Variant* lookup_q8(int D, int BS, int G, bool e4m3) {
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, v.fn, v.warps * 32, v.smem) != cudaSuccess || occ < 1)
       return nullptr;
     v.P = device_sm_count() * occ * v.streams;
-    ready[di][bi][vi][fi] = true;
+    ready[di][bi][vi][fi][pi] = true;
   }
   return &v;
 }
@@ -477,8 +485,14 @@ extern "C" size_t pkv_q8_workspace_bytes(int batch, int n_h, int n_kv, int head_
   if (batch < 0 || !valid_shape(n_h, n_kv, head_dim, block_size)) return 0;
   if (format != PKV_Q8_E4M3 && format != PKV_Q8_INT8) return 0;
   const int G = n_h / n_kv;
-  Q8Variant* v = lookup_q8(head_dim, block_size, G, format == PKV_Q8_E4M3);
-  return v ? workspace_layout(batch, n_kv, G, head_dim, v->P).total : 0;
+  size_t most = 0;                                             // for either output type
+  for (int pair = 0; pair < 2; ++pair) {
+    Q8Variant* v = lookup_q8(head_dim, block_size, G, format == PKV_Q8_E4M3, pair != 0);
+    if (!v) return 0;
+    const size_t n = workspace_layout(batch, n_kv, G, head_dim, v->P).total;
+    most = n > most ? n : most;
+  }
+  return most;
 }
 
 extern "C" pkv_status pkv_paged_decode_attn_q8(const void* q, const uint8_t* cache, int format, const int32_t* block_tables,
@@ -496,7 +510,7 @@ extern "C" pkv_status pkv_paged_decode_attn_q8(const void* q, const uint8_t* cac
   if (!al16(q) || !al16(cache) || !al16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PKV_EINVAL;
   if ((long long)max_blocks * block_size > 0x7fffffffLL) return PKV_ERANGE;
   const int G = n_h / n_kv;
-  Q8Variant* v = lookup_q8(head_dim, block_size, G, format == PKV_Q8_E4M3);
+  Q8Variant* v = lookup_q8(head_dim, block_size, G, format == PKV_Q8_E4M3, out_dtype == PKV_OUT_F32);
   if (!v) {
     record_cuda_error(cudaGetLastError());
     return PKV_ECUDA;

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const Evict
   }
   // this thread's rows
   const int each = R > 0 ? R : (n + ranks * NT - 1) / (ranks * NT);
-  const int r0 = min((long long)n, (long long)(rank * NT + (int)threadIdx.x) * each), r1 = min(n, r0 + each);
+  const int r0 = min((long long)n, (long long)(rank * NT + (int)threadIdx.x) * each), r1 = r0 + min(each, n - r0);
 
   if (K == n) {                                               // nothing to evict (uniform in the cluster)
     if (rank == 0 && threadIdx.x == 0) a.counts[sg] = 0;

@@ -181,14 +181,16 @@ def attend(q, cache, bt, ctx, scale, out_dtype=torch.float32, window=0, expect=0
     return out
 
 
-def check_bf16(out, ref):
-    """One rounding (2^-8 of the value at most) of a result within the fp32 bar.  The rel-L2 bar of
+def check_bf16(out, ref, v):
+    """One rounding (2^-8 of the value at most) of a result within the fp32 bar and 2^-11 sum p |v| <=
+    2^-11 max |v|: for a bf16 output and groups of over four heads p is rounded to fp16 once.  The rel-L2 bar of
     the bf16 cache's tests does not apply: it is the rounding of values with evenly spread mantissas
     (2^-8 / sqrt 3 over an octave, 1.7e-3), while a context of one token gives code * scale, whose few
     mantissas can all lie where the rounding costs up to 2^-8 = 3.9e-3."""
     got = f64(out)
     assert np.isfinite(got).all() and out.dtype == torch.bfloat16
-    assert (np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + BAR_F32_MAXABS * (1 + 2.0 ** -8)).all()
+    own = BAR_F32_MAXABS + 2.0 ** -11 * float(np.abs(v).max())
+    assert (np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + own * (1 + 2.0 ** -8)).all()
 
 
 # The bars of the other attention tests hold here too: the codes are exact in fp16, q to 2^-39, p to
@@ -202,7 +204,7 @@ def test_attention_sweep(fmt, d, bs, n_h, n_kv):
     scale = 1 / math.sqrt(d)
     ref = oracle.paged_decode_attention(f64(q), *held, bt, lens, scale, bs)
     check_attention(attend(q, cache, bt, lens, scale), ref, "fp32")
-    check_bf16(attend(q, cache, bt, lens, scale, torch.bfloat16), ref)
+    check_bf16(attend(q, cache, bt, lens, scale, torch.bfloat16), ref, held[1])
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
