@@ -286,6 +286,9 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32, NH == 2 ? 2 : 1)
 // (vectors of four where G allows), so a warp reads whole lines, and add their parts by a fixed
 // tree; a lane has the loads of U tokens in flight (one at a time left the kernel at 2.2 TB/s of
 // scores on 32-head groups).  CTA (c, s, g) takes 256 / LT * U tokens.
+template <bool V4> struct ScoreVec { using type = float4; };
+template <> struct ScoreVec<false> { using type = float; };
+
 template <int LT, bool V4, int U>
 __global__ void __launch_bounds__(256) mass_add_kernel(const float* __restrict__ scores, const float2* __restrict__ fin,
                                                        const int32_t* __restrict__ ctx, int max_ctx, int n_kv, int G,
@@ -299,7 +302,18 @@ __global__ void __launch_bounds__(256) mass_add_kernel(const float* __restrict__
   const int sub = threadIdx.x % LT, t0 = chunk * STEP * U + threadIdx.x / LT;
   const float* x = scores + ((size_t)sg * max_ctx) * G;
   float* mrow = mass + (size_t)sg * mass_stride;
+  // the first scores are asked for together with the states
+  using Vec = typename ScoreVec<V4>::type;
+  const int vecs = V4 ? G / 4 : G;
+  auto score = [&](int u, int i) {
+    Vec v = {};
+    if (t0 + u * STEP < n && i < vecs) v = __ldcs(reinterpret_cast<const Vec*>(x + (size_t)(t0 + u * STEP) * G) + i);
+    return v;
+  };
   float before[U], w[U];
+  Vec v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) v[u] = score(u, sub);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     w[u] = 0.f;
@@ -307,26 +321,20 @@ __global__ void __launch_bounds__(256) mass_add_kernel(const float* __restrict__
   }
   if (threadIdx.x < G) f[threadIdx.x] = fin[(size_t)sg * G + threadIdx.x];
   __syncthreads();
-  if constexpr (V4) {
-    for (int i = sub; i < G / 4; i += LT) {
-      float4 v[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (t0 + u * STEP < n) v[u] = __ldcs(reinterpret_cast<const float4*>(x + (size_t)(t0 + u * STEP) * G) + i);
-        else v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = sub; i < vecs; i += LT) {
+    if constexpr (V4) {
       const float2 f0 = f[4 * i], f1 = f[4 * i + 1], f2 = f[4 * i + 2], f3 = f[4 * i + 3];
 #pragma unroll
       for (int u = 0; u < U; ++u)
         w[u] += ex2(v[u].x - f0.x) * f0.y + ex2(v[u].y - f1.x) * f1.y + ex2(v[u].z - f2.x) * f2.y + ex2(v[u].w - f3.x) * f3.y;
-    }
-  } else {
-    for (int i = sub; i < G; i += LT) {
-      float v[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = t0 + u * STEP < n ? __ldcs(x + (size_t)(t0 + u * STEP) * G + i) : 0.f;
+    } else {
       const float2 fi = f[i];
 #pragma unroll
       for (int u = 0; u < U; ++u) w[u] += ex2(v[u] - fi.x) * fi.y;
+    }
+    if (i + LT < vecs) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = score(u, i + LT);
     }
   }
 #pragma unroll
