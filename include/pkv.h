@@ -378,7 +378,8 @@ pkv_status pkv_rope_qk(const void* q, int64_t q_stride, const void* k, int64_t k
  * Caller contract: as for pkv_kv_quant_append_int4 (slots distinct; within a call the tokens of a
  * sequence are consecutive entries in logical order with one tail_seq; a sequence starts at row 0
  * of its first block); values finite (a NaN is lost in INT8 and stays NaN in E4M3, an infinity
- * spoils its block).  A slot or tail row out of range sets PKV_DEV_BAD_SLOT and is skipped.
+ * spoils its block).  A sequence may be cut back inside its unfinished block (the tail still holds
+ * the rows that remain), not into a finished one.  A slot or tail row out of range sets PKV_DEV_BAD_SLOT and is skipped.
  */
 #define PKV_Q8_E4M3 0
 #define PKV_Q8_INT8 1
@@ -438,7 +439,7 @@ pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_pool, const v
  *   dropped    int32 [batch]: tokens evicted so far (0 at the start)
  * The new state goes to the _out pointers: all four equal to the inputs (in place), or none.
  * Entries of mass_out behind n, and of positions_out behind the new kept, are left as they were.
- *   new_lens   int32 [batch]: min(n, K); not the same array as context_lens or keep
+ *   new_lens   int32 [batch]: min(n, K); must not overlap context_lens, keep, kept or dropped
  *   workspace  pkv_evict_workspace_bytes bytes, 256-byte aligned
  * The blocks that hold the first K rows are rewritten: they must belong to the sequence alone
  * (see pkv_bm_evict).  Moves from or to a block id outside the pool set PKV_DEV_BAD_BLOCK and are

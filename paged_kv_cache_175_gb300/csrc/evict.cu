@@ -483,7 +483,9 @@ extern "C" pkv_status pkv_kv_evict(void* k_pool, void* v_pool, const int32_t* bl
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PKV_EINVAL;
   // the state is replaced as a whole or written to another one as a whole
   const bool in_place = mass_out == mass;
-  if (new_lens == context_lens || new_lens == keep) return PKV_EINVAL;   // both are still read
+  // the lengths are written while these are still read
+  for (const int32_t* p : {context_lens, keep, kept, dropped})
+    if (new_lens < p + batch && p < new_lens + batch) return PKV_EINVAL;
   if (in_place != (positions_out == positions) || in_place != (kept_out == kept) || in_place != (dropped_out == dropped))
     return PKV_EINVAL;
   const long long max_ctx = (long long)max_blocks * block_size;

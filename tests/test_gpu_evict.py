@@ -269,7 +269,8 @@ def test_refusals():
                 lambda: pkv.paged_decode_attn_mass(q, kp, kp, bt, ctx, 1.0, st.mass[:1]), lambda: pkv.paged_decode_attn_mass(q, kp, kp, bt.long(), ctx, 1.0, st.mass),
                 lambda: pkv.paged_decode_attn_mass(q, kp, kp, bt, ctx, 1.0, st.mass, workspace=torch.empty(512, dtype=torch.uint8, device=DEV)),
                 lambda: pkv.mass_workspace_bytes(1, 8, 3, 64, 16, 1),
-                lambda: pkv.kv_evict(kp, kp, bt, ctx, ctx, 0, short), lambda: pkv.kv_evict(kp, kp, bt, ctx, ctx, 0, st, new_lens=ctx),
+                lambda: pkv.kv_evict(kp, kp, bt, ctx, ctx, 0, short), lambda: pkv.kv_evict(kp, kp, bt, ctx, ctx.clone(), 0, st, new_lens=ctx),
+                lambda: pkv.kv_evict(kp, kp, bt, ctx, ctx.clone(), 0, st, new_lens=st.kept),
                 lambda: pkv.kv_evict(kp, kp, bt, ctx, ctx.clone(), -1, st), lambda: pkv.kv_evict(kp, kp, bt, ctx, ctx.clone(), 0, st, out=mixed),
                 lambda: pkv.kv_evict(kp, kp, bt, ctx, ctx.long(), 0, st), lambda: pkv.kv_evict(kp.half(), kp, bt, ctx, ctx.clone(), 0, st)):
         with pytest.raises(pkv.PkvError):

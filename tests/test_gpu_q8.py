@@ -125,6 +125,19 @@ def test_append_long_call_uses_spans(fmt):
     assert_cache(caches[0], want, bt[2, :-(-lens[2] // bs)])
 
 
+def test_append_after_a_cut_inside_the_open_block():
+    # rows taken back from the unfinished block are overwritten: the record is that of the rows that remain
+    d, bs, n_kv = 64, 16, 2
+    k, v = (torch.randn(30, n_kv, d, generator=torch.Generator().manual_seed(i)).to(torch.bfloat16) for i in (1, 2))
+    caches = [pkv.alloc_q8_cache(3, n_kv, bs, d, 1, "e4m3", DEV) for _ in range(2)]
+    seq = lambda n: torch.zeros(n, dtype=torch.int32, device=DEV)
+    put = lambda c, x, y, lo: pkv.kv_quant_append_q8(x.to(DEV), y.to(DEV), torch.arange(lo, lo + len(x), device=DEV), seq(len(x)), c)
+    put(caches[0], k[:27], v[:27], 0)
+    put(caches[0], k[27:], v[27:], 20)                          # rows 20..26 taken back
+    put(caches[1], torch.cat([k[:20], k[27:]]), torch.cat([v[:20], v[27:]]), 0)
+    assert torch.equal(caches[0].records, caches[1].records)
+
+
 def test_append_strided_padding_bad_slots_and_extremes():
     d, bs, n_kv = 64, 16, 2
     cache = pkv.alloc_q8_cache(6, n_kv, bs, d, 2, "e4m3", DEV)
