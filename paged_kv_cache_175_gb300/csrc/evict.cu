@@ -139,38 +139,48 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const Evict
   auto make_key = [&](int r) { return position(r) >= recent_from ? 0xffffffffu : order_bits(mass[r]); };
   uint32_t keys[R > 0 ? R : 1];
   if constexpr (R > 0) {
-    const bool vec = a.vec != 0;                              // rows of the state are 16-byte aligned
-    float x[R];
+    if (r0 < r1) {                                            // warps behind the rows skip theirs throughout
+      const bool vec = a.vec != 0;                            // rows of the state are 16-byte aligned
+      float x[R];
 #pragma unroll
-    for (int i = 0; i < R; i += 4) {
-      if (vec && r0 + i + 4 <= r1) {
-        const float4 v = *reinterpret_cast<const float4*>(mass + r0 + i);
-        x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
-      } else {
+      for (int i = 0; i < R; i += 4) {
+        if (vec && r0 + i + 4 <= r1) {
+          const float4 v = *reinterpret_cast<const float4*>(mass + r0 + i);
+          x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[i + j] = r0 + i + j < r1 ? mass[r0 + i + j] : 0.f;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < R; i += 4) {
-      int p[4];
-      if (vec && r0 + i + 4 <= min(r1, kept)) {
-        const int4 v = *reinterpret_cast<const int4*>(posn + r0 + i);
-        p[0] = v.x; p[1] = v.y; p[2] = v.z; p[3] = v.w;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = r0 + i + j < r1 ? position(r0 + i + j) : 0;
+          for (int j = 0; j < 4; ++j) x[i + j] = r0 + i + j < r1 ? mass[r0 + i + j] : 0.f;
+        }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) keys[i + j] = p[j] >= recent_from ? 0xffffffffu : order_bits(x[i + j]);
+      for (int i = 0; i < R; i += 4) {
+        int p[4];
+        if (r0 + i >= kept) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) p[j] = dropped + r0 + i + j;
+        } else if (vec && r0 + i + 4 <= min(r1, kept)) {
+          const int4 v = *reinterpret_cast<const int4*>(posn + r0 + i);
+          p[0] = v.x; p[1] = v.y; p[2] = v.z; p[3] = v.w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) p[j] = r0 + i + j < r1 ? position(r0 + i + j) : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) keys[i + j] = p[j] >= recent_from ? 0xffffffffu : order_bits(x[i + j]);
+      }
     }
   }
   // f(row, key) for this thread's rows in order
   auto rows = [&](auto f) {
     if constexpr (R > 0) {
+      if (r1 - r0 == R) {
 #pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (r0 + i < r1) f(r0 + i, keys[i]);
+        for (int i = 0; i < R; ++i) f(r0 + i, keys[i]);
+      } else if (r0 < r1) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (r0 + i < r1) f(r0 + i, keys[i]);
+      }
     } else {
       for (int r = r0; r < r1; ++r) f(r, make_key(r));
     }
@@ -310,7 +320,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const Evict
   uint32_t hole_bits = 0, mover_bits = 0;                     // of this thread's rows (R > 0)
   if constexpr (R > 0) {
     uint32_t st = 0;
-    if (K > 0) {
+    if (K > 0 && r0 < r1) {
 #pragma unroll
       for (int i = 0; i < R; ++i) st |= (keys[i] >= prefix ? 1u : 0u) << i;
       if (!all_equal) {                                       // of the equal rows only the first `want` of all
