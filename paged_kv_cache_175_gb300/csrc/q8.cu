@@ -11,9 +11,14 @@
 // step reads the open rows and writes one record per (sequence, kv head): a few hundred KB, so
 // the launch and three dependent round trips (slots, rows, stores).
 // Split: one CTA per kv head, K or V, and span of tokens takes each run of tokens that lands in
-// one block.  A span is one token for small calls (every run its own CTA, for latency) and
-// block_size tokens above kSpanTokens (one or two runs per CTA, so that the CTAs whose tokens
-// all continue a run do not cost a launch slot each).
+// one block, 64 / block_size runs side by side (64 rows in shared memory at a time).  A span is 64
+// tokens in long calls and as many tokens as there are places for runs in short ones, where every
+// token tends to be a run.  The runs of a span are found in one round trip; the search for a
+// sequence's end, which few runs need, goes on while the rows arrive.
+// Measured (8 kv heads of 128): 8000 tokens of one prompt in blocks of 16 in 16.6 us (2.9 TB/s), one
+// run at a time 21.7; 23 ragged prompts of 234-701 tokens in blocks of 64 in 24.7 us (2.9 TB/s; the
+// CTAs with two or three runs end last; asking for the next run's rows ahead cost the registers of a
+// CTA per SM and was level); 64 single tokens in 3.1 us.
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -75,121 +80,161 @@ __device__ int seq_edge(const Q8AppendArgs& a, int i, int seq, int dir) {
   return i + dir * hi;
 }
 
+constexpr int kQ8Rows = 64;              // rows that a CTA quantizes at a time: 64 / BS runs
+
 template <int D, int BS>
 struct Q8Shape {
-  static constexpr int VECS = BS * D / 8;                     // 16-byte vectors of a block's rows
-  static constexpr int NT = VECS < 256 ? VECS : 256;
-  static constexpr int NV = VECS / NT;
+  static constexpr int NT = 256, GROUPS = kQ8Rows / BS, GT = NT / GROUPS;   // threads per run
+  static constexpr int NV = BS * D / 8 / GT;                  // 16-byte vectors of a run per thread
+  static constexpr int WIN = kQ8Rows + BS;                    // tokens of a span, and behind it
 };
 
 template <int D, int BS, bool E4M3>
-__global__ void __launch_bounds__(Q8Shape<D, BS>::NT) q8_append_kernel(const Q8AppendArgs a) {
-  constexpr int NT = Q8Shape<D, BS>::NT, NV = Q8Shape<D, BS>::NV;
+__global__ void __launch_bounds__(256) q8_append_kernel(const Q8AppendArgs a) {
+  using S = Q8Shape<D, BS>;
+  constexpr int NT = S::NT, GROUPS = S::GROUPS, GT = S::GT, NV = S::NV, WIN = S::WIN, WORDS = (WIN + 31) / 32;
   constexpr int ROW = D + 8;                                  // padded row: the gathers below spread over the banks
   constexpr int VPR = D / 8;                                  // 16-byte vectors per row
-  constexpr int CHUNKS = BS * D / 16;                         // 16-byte chunks of codes
-  __shared__ __align__(16) __nv_bfloat16 rows_s[BS * ROW];
+  __shared__ __align__(16) __nv_bfloat16 rows_s[kQ8Rows * ROW];
   __shared__ float big_s[NT / 32];
   // the span's tokens and the block_size behind them, which the last run may reach
-  constexpr int WIN = 2 * BS;
   __shared__ int64_t slot_s[WIN];
   __shared__ int seq_s[WIN];
-  __shared__ uint32_t lead_s[WIN / 32], cont_s[WIN / 32 + 1];  // bit t: token t starts / continues a run
-  __shared__ int edge_s;
+  __shared__ uint32_t lead_s[WORDS], cont_s[WORDS + 1];       // bit t: token t starts / continues a run
+  __shared__ int tail_from_s[GROUPS], tail_rows_s[GROUPS];    // see below
   const int g = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
-  const bool values = blockIdx.z != 0;                        // this CTA's half of the record: V or K
+  const int group = tid / GT, gtid = tid % GT;
+  const bool values = blockIdx.z != 0;                        // this CTA's half of the records: V or K
   const __nv_bfloat16* x = (values ? a.v : a.k) + (size_t)g * D;
   const long long stride = values ? a.v_stride : a.k_stride;
   __nv_bfloat16* tails = values ? a.v_tail : a.k_tail;
+  __nv_bfloat16* rows = rows_s + group * BS * ROW;
   const int i0 = blockIdx.x * a.span;
-  if (tid < WIN) {
+  if (tid < WORDS * 32) {
     const int i = i0 + tid;
-    const bool in = i < a.n_tok && tid < a.span + BS;
+    const bool in = i < a.n_tok && tid < a.span + BS && tid < WIN;
     const int64_t slot = in ? a.slots[i] : -1;
     const int seq = in ? a.tail_seq[i] : -1;
     const int64_t slot_before = in && i > 0 ? a.slots[i - 1] : -1;
     const int seq_before = in && i > 0 ? a.tail_seq[i - 1] : -1;
     const bool good = slot >= 0 && slot < a.n_slots && (unsigned)seq < (unsigned)a.tail_rows;
-    if (slot >= 0 && !good && tid < a.span && g == 0 && blockIdx.z == 0) set_err(a.err, PKV_DEV_BAD_SLOT);
+    if (slot >= 0 && !good && tid < a.span && g == 0 && !values) set_err(a.err, PKV_DEV_BAD_SLOT);
     // a run: consecutive rows of one block, of one sequence
     const bool goes_on = good && (slot & (BS - 1)) != 0 && slot_before == slot - 1 && seq_before == seq;
-    slot_s[tid] = slot;
-    seq_s[tid] = seq;
+    if (tid < WIN) {
+      slot_s[tid] = slot;
+      seq_s[tid] = seq;
+    }
     const unsigned c = __ballot_sync(FULL_MASK, goes_on), l = __ballot_sync(FULL_MASK, good && !goes_on && tid < a.span);
     if (lane == 0) {
       cont_s[warp] = c;
       lead_s[warp] = l;
     }
   }
-  if (tid == 0) cont_s[WIN / 32] = 0u;
+  if (tid == 0) cont_s[WORDS] = 0u;
   __syncthreads();
-  for (int t = 0;;) {
-    // next run that starts in the span
-    {
-      uint32_t bits = 0;
-      int wd = t >> 5;
-      if (wd < WIN / 32) bits = lead_s[wd] & (0xffffffffu << (t & 31));
-      while (!bits && ++wd < WIN / 32) bits = lead_s[wd];
-      if (!bits) break;
-      t = 32 * wd + __ffs(bits) - 1;
+  int n_runs = 0;
+#pragma unroll
+  for (int w = 0; w < WORDS; ++w) n_runs += __popc(lead_s[w]);
+  struct Run {
+    int t, m, seq, row0, end;              // first token of the span, tokens, sequence, rows [row0, end) of the block
+    int64_t slot;
+  };
+  // the k-th run that starts in the span (end = 0: there is none)
+  auto find = [&](int k) {
+    Run r = {0, 0, 0, 0, 0, 0};
+    if (k >= n_runs) return r;
+    int left = k, wd = 0;
+    while (left >= __popc(lead_s[wd])) left -= __popc(lead_s[wd++]);
+    uint32_t bits = lead_s[wd];
+    for (; left > 0; --left) bits &= bits - 1;
+    r.t = 32 * wd + __ffs(bits) - 1;
+    r.slot = slot_s[r.t];
+    r.seq = seq_s[r.t];
+    r.row0 = (int)(r.slot & (BS - 1));
+    const int p = r.t + 1;                                    // its length: the tokens that go on from it
+    wd = p >> 5;
+    uint32_t stop = wd < WORDS ? ~cont_s[wd] & (0xffffffffu << (p & 31)) : 0xffffffffu;
+    while (!stop) stop = ~cont_s[++wd];
+    r.m = min(32 * wd + __ffs(stop) - 1 - r.t, BS - r.row0);
+    r.end = r.row0 + r.m;
+    return r;
+  };
+  uint4 w[NV];
+  auto load = [&](const Run& r) {
+    const __nv_bfloat16* old = tails + ((size_t)r.seq * a.n_kv + g) * BS * D;
+    const __nv_bfloat16* now = x + (long long)(i0 + r.t - r.row0) * stride;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int e = gtid + u * GT, row = e / VPR, c = e % VPR;
+      w[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < r.end) w[u] = *(reinterpret_cast<const uint4*>(row < r.row0 ? old + (size_t)row * D : now + row * stride) + c);
     }
-    const int i = i0 + t, seq = seq_s[t];
-    const int64_t slot = slot_s[t];
-    const int row0 = (int)(slot & (BS - 1));
-    int m = 1;                                                // its length: the tokens that go on from it
-    {
-      int p = t + 1, wd = p >> 5;
-      uint32_t stop = wd < WIN / 32 ? ~cont_s[wd] & (0xffffffffu << (p & 31)) : 0xffffffffu;
-      while (!stop) stop = ~cont_s[++wd];
-      m = 32 * wd + __ffs(stop) - 1 - t;
-      if (wd >= WIN / 32) m = WIN - t;
+  };
+  for (int first = 0; first < n_runs; first += GROUPS) {
+    const Run run = find(first + group);
+    load(run);
+    const bool busy = run.end > 0;
+    const int m = run.m, seq = run.seq, row0 = run.row0, end = run.end, i = i0 + run.t;
+    const size_t tail0 = ((size_t)seq * a.n_kv + g) * BS * D;
+    // The sequence's tail, while the rows arrive.  Rows of an unfinished block go to the tail; but the
+    // CTA that read old rows from it (a run continuing a block) is the only one that may then
+    // overwrite them, also with the rows of a later block of the same call.
+    //   tail_from < 0: the run's own m rows;  >= 0: rows 0 .. tail_rows of the tokens from there on
+    if (busy && gtid < 32) {
+      int from = -1, count = 0;
+      if (end < BS) {
+        count = m;
+        if (row0 == 0 && i > 0 && of_seq(a, i - 1, seq)) {    // a later block: did the sequence start inside one?
+          const int begin = seq_edge(a, i, seq, -1) + 1;
+          if ((a.slots[begin] & (BS - 1)) != 0) count = 0;
+        }
+      } else if (row0 > 0 && i + m < a.n_tok && of_seq(a, i + m, seq)) {
+        // the block is full and the sequence goes on: the open rows behind it are this CTA's
+        const int stop = seq_edge(a, i, seq, 1), n = (int)(a.slots[stop - 1] & (BS - 1)) + 1;
+        if (n < BS && n <= stop - i - m) {
+          from = stop - n;
+          count = n;
+        }
+      }
+      if (lane == 0) {
+        tail_from_s[group] = from;
+        tail_rows_s[group] = count;
+      }
     }
-    m = min(m, BS - row0);
-    const int end = row0 + m;
-    {
-      const long long phys = slot / BS;
-      const size_t tail0 = ((size_t)seq * a.n_kv + g) * BS * D;
-      // rows into shared memory, with the largest magnitude on the way
-      uint4 w[NV];
+    __nv_bfloat162 big2 = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
-      for (int u = 0; u < NV; ++u) {
-        const int e = tid + u * NT, r = e / VPR, c = e % VPR;
-        w[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < end)
-          w[u] = *(reinterpret_cast<const uint4*>(r < row0 ? tails + tail0 + (size_t)r * D : x + (long long)(i + r - row0) * stride) + c);
-      }
-      __nv_bfloat162 big2 = __floats2bfloat162_rn(0.f, 0.f);
+    for (int u = 0; u < NV; ++u) {
+      const int e = gtid + u * GT, r = e / VPR, c = e % VPR;
+      *reinterpret_cast<uint4*>(rows + r * ROW + 8 * c) = w[u];
+      const uint32_t ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
 #pragma unroll
-      for (int u = 0; u < NV; ++u) {
-        const int e = tid + u * NT, r = e / VPR, c = e % VPR;
-        *reinterpret_cast<uint4*>(rows_s + r * ROW + 8 * c) = w[u];
-        const uint32_t ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) big2 = __hmax2(big2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&ws[q])));
-      }
-      // magnitudes are not negative: their bits order as integers
-      const float mine = fmaxf(__low2float(big2), __high2float(big2));
-      const uint32_t wb = __reduce_max_sync(FULL_MASK, __float_as_uint(mine));
-      if (lane == 0) big_s[warp] = __uint_as_float(wb);
-      __syncthreads();
-      uint8_t* rec = a.records + ((size_t)phys * a.n_kv + g) * q8_record_bytes(BS, D);
+      for (int q = 0; q < 4; ++q) big2 = __hmax2(big2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&ws[q])));
+    }
+    // magnitudes are not negative: their bits order as integers
+    const float mine = fmaxf(__low2float(big2), __high2float(big2));
+    const uint32_t wb = __reduce_max_sync(FULL_MASK, __float_as_uint(mine));
+    if (lane == 0) big_s[warp] = __uint_as_float(wb);
+    __syncthreads();
+    if (busy) {
+      uint8_t* rec = a.records + ((size_t)(run.slot / BS) * a.n_kv + g) * q8_record_bytes(BS, D);
       const float most = E4M3 ? 448.f : 127.f;
       float big = 0.f;
 #pragma unroll
-      for (int k = 0; k < NT / 32; ++k) big = fmaxf(big, big_s[k]);
+      for (int k = 0; k < GT / 32; ++k) big = fmaxf(big, big_s[group * (GT / 32) + k]);
       const bool some = big >= kQ8Tiny;
       const float scale = some ? __fmul_rn(big, __fdiv_rn(1.f, most)) : 0.f, inv = some ? __fmul_rn(__fdiv_rn(1.f, big), most) : 0.f;
       uint8_t* codes = rec + (values ? BS * D : 0);
       if (!values) {
 #pragma unroll
-        for (int e = tid; e < CHUNKS; e += NT) {
+        for (int e = gtid; e < BS * D / 16; e += GT) {        // 16-byte chunks of codes
           const int ln = e & 31, gid = ln >> 2, tig = ln & 3, j = (e >> 5) % (D / 32), tt = (e >> 5) / (D / 32);
-          const __nv_bfloat16* p = rows_s + (16 * tt + gid) * ROW + 32 * j + 2 * tig;
+          const __nv_bfloat16* p = rows + (16 * tt + gid) * ROW + 32 * j + 2 * tig;
           uint32_t o[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {                       // q = 2 ks + hi
-            const __nv_bfloat16* s = p + (q & 1) * 8 * ROW + (q >> 1) * 16;
-            const uint32_t x0 = *reinterpret_cast<const uint32_t*>(s), x1 = *reinterpret_cast<const uint32_t*>(s + 8);
+            const __nv_bfloat16* sp = p + (q & 1) * 8 * ROW + (q >> 1) * 16;
+            const uint32_t x0 = *reinterpret_cast<const uint32_t*>(sp), x1 = *reinterpret_cast<const uint32_t*>(sp + 8);
             o[q] = code4<E4M3>(__fmul_rn(bf16_lo(x0), inv), __fmul_rn(bf16_hi(x0), inv), __fmul_rn(bf16_lo(x1), inv), __fmul_rn(bf16_hi(x1), inv));
           }
           *reinterpret_cast<uint4*>(codes + (size_t)e * 16) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -197,15 +242,15 @@ __global__ void __launch_bounds__(Q8Shape<D, BS>::NT) q8_append_kernel(const Q8A
       } else {
         // the chunks of two neighbouring channels (gid = 2 gp, 2 gp + 1) from one set of loads
 #pragma unroll
-        for (int e = tid; e < CHUNKS / 2; e += NT) {
+        for (int e = gtid; e < BS * D / 32; e += GT) {
           const int ln = e & 15, gp = ln >> 2, tig = ln & 3, j = (e >> 4) % (D / 32), tt = (e >> 4) / (D / 32);
-          const __nv_bfloat16* p = rows_s + (16 * tt + 2 * tig) * ROW + 32 * j + 2 * gp;
+          const __nv_bfloat16* p = rows + (16 * tt + 2 * tig) * ROW + 32 * j + 2 * gp;
           uint32_t o[2][4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {                       // q = 2 md + hi
-            const __nv_bfloat16* s = p + (q >> 1) * 16 + (q & 1) * 8;
-            const uint32_t t0 = *reinterpret_cast<const uint32_t*>(s), t1 = *reinterpret_cast<const uint32_t*>(s + ROW);
-            const uint32_t t2 = *reinterpret_cast<const uint32_t*>(s + 8 * ROW), t3 = *reinterpret_cast<const uint32_t*>(s + 9 * ROW);
+            const __nv_bfloat16* sp = p + (q >> 1) * 16 + (q & 1) * 8;
+            const uint32_t t0 = *reinterpret_cast<const uint32_t*>(sp), t1 = *reinterpret_cast<const uint32_t*>(sp + ROW);
+            const uint32_t t2 = *reinterpret_cast<const uint32_t*>(sp + 8 * ROW), t3 = *reinterpret_cast<const uint32_t*>(sp + 9 * ROW);
             o[0][q] = code4<E4M3>(__fmul_rn(bf16_lo(t0), inv), __fmul_rn(bf16_lo(t1), inv), __fmul_rn(bf16_lo(t2), inv), __fmul_rn(bf16_lo(t3), inv));
             o[1][q] = code4<E4M3>(__fmul_rn(bf16_hi(t0), inv), __fmul_rn(bf16_hi(t1), inv), __fmul_rn(bf16_hi(t2), inv), __fmul_rn(bf16_hi(t3), inv));
           }
@@ -214,50 +259,19 @@ __global__ void __launch_bounds__(Q8Shape<D, BS>::NT) q8_append_kernel(const Q8A
           *reinterpret_cast<uint4*>(d + 64) = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
         }
       }
-      if (tid == 0) {
+      if (gtid == 0) {
         float* sc = reinterpret_cast<float*>(rec + 2 * BS * D);
         sc[values ? 1 : 0] = scale;
         sc[values ? 3 : 2] = 0.f;
       }
-
-      // ---- the sequence's tail ----
-      // The CTA that read old rows from the tail (a run continuing a block) is the only one
-      // that may then overwrite them, also with the rows of a later block of the same call.
-      if (end < BS) {
-        bool own = true;
-        if (row0 == 0 && i > 0 && of_seq(a, i - 1, seq)) {    // a later block: did the sequence start inside one?
-          if (warp == 0) {
-            const int first = seq_edge(a, i, seq, -1) + 1;
-            if (lane == 0) edge_s = first;
-          }
-          __syncthreads();
-          own = a.slots[edge_s] % BS == 0;
-        }
-        if (own) {
-          for (int e = tid; e < m * VPR; e += NT) {
-            const int r = row0 + e / VPR, c = e % VPR;
-            *(reinterpret_cast<uint4*>(tails + tail0 + (size_t)r * D) + c) = *reinterpret_cast<const uint4*>(rows_s + r * ROW + 8 * c);
-          }
-        }
-      } else if (row0 > 0 && i + m < a.n_tok && of_seq(a, i + m, seq)) {
-        // the block is full and the sequence goes on: the open rows behind it are this CTA's
-        if (warp == 0) {
-          const int last = seq_edge(a, i, seq, 1);
-          if (lane == 0) edge_s = last;
-        }
-        __syncthreads();
-        const int stop = edge_s, n = (int)(a.slots[stop - 1] % BS) + 1;   // rows of the last block
-        if (n < BS && n <= stop - i - m) {
-          for (int e = tid; e < n * VPR; e += NT) {
-            const int r = e / VPR, c = e % VPR;
-            *(reinterpret_cast<uint4*>(tails + tail0 + (size_t)r * D) + c) =
-                *(reinterpret_cast<const uint4*>(x + (long long)(stop - n + r) * stride) + c);
-          }
-        }
+      const int from = tail_from_s[group], count = tail_rows_s[group];
+      for (int e = gtid; e < count * VPR; e += GT) {
+        const int k = e / VPR, c = e % VPR, r = from < 0 ? row0 + k : k;
+        *(reinterpret_cast<uint4*>(tails + tail0 + (size_t)r * D) + c) =
+            from < 0 ? *reinterpret_cast<const uint4*>(rows + r * ROW + 8 * c)
+                     : *(reinterpret_cast<const uint4*>(x + (long long)(from + k) * stride) + c);
       }
     }
-    t += m;
-    if (t >= a.span) break;
     __syncthreads();                                          // the shared arrays are reused
   }
 }
@@ -265,7 +279,7 @@ __global__ void __launch_bounds__(Q8Shape<D, BS>::NT) q8_append_kernel(const Q8A
 template <int D, int BS>
 static cudaError_t launch_q8(const Q8AppendArgs& a, bool e4m3, cudaStream_t st) {
   const unsigned gx = (unsigned)((a.n_tok + a.span - 1) / a.span);
-  const dim3 grid(gx, (unsigned)a.n_kv, 2), block(Q8Shape<D, BS>::NT);
+  const dim3 grid(gx, (unsigned)a.n_kv, 2), block(256);
   if (e4m3) q8_append_kernel<D, BS, true><<<grid, block, 0, st>>>(a);
   else q8_append_kernel<D, BS, false><<<grid, block, 0, st>>>(a);
   return cudaGetLastError();
@@ -306,7 +320,8 @@ extern "C" pkv_status pkv_kv_quant_append_q8(const void* k, int64_t k_stride, co
   a.v_tail = static_cast<__nv_bfloat16*>(v_tail);
   a.n_slots = (long long)num_blocks * block_size;
   a.n_tok = n_tok; a.n_kv = n_kv; a.tail_rows = tail_rows;
-  a.span = n_tok <= kSpanTokens ? 1 : block_size;
+  // long calls: 64 tokens; short ones (decode steps): as many tokens as the CTA has places for runs
+  a.span = n_tok <= kSpanTokens ? kQ8Rows / block_size : kQ8Rows;
   a.err = err_flag;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool f = format == PKV_Q8_E4M3;
