@@ -20,12 +20,13 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib
 import os
 from dataclasses import dataclass
 
 import torch
 
-from ._build import LIB as LIB_PATH, build_library
+from ._build import CALLS as CALLS_PATH, LIB as LIB_PATH, build_library
 
 PKV_OUT_BF16 = 0
 PKV_OUT_F32 = 1
@@ -375,12 +376,29 @@ def rope_table(head_dim, rotary_dim=None, base=10000.0, interleaved=False, scali
     return t
 
 
-# The calls below check their arguments in one expression first (a call of a few microseconds on the
-# GPU should not wait for its checks); where it is false, the checks that follow name the mistake.
+# The tensors of the calls below are checked and passed on by a small extension (csrc/calls.cpp): a call
+# of a few microseconds on the GPU should not wait for its checks.  Where the extension answers
+# _NOT_TAKEN it called nothing, and the checks after it name the mistake.
 _bf16, _f32, _i32, _i64, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
-_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
-_raw_current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda d: torch.cuda.current_stream(d).cuda_stream)
+_NOT_TAKEN = 1
+_calls = None
+
+
+def _native():
+    """The extension (fails loudly if it has not been built)."""
+    global _calls
+    if _calls is None:
+        lib()
+        if not os.path.exists(CALLS_PATH):
+            raise PkvError(f"{CALLS_PATH} is missing: build it with paged_kv_cache_175_gb300._build.build_library()")
+        _calls = importlib.import_module("._calls", __name__)
+    return _calls
+
+
+def _failed(name, status):
+    if status == _NOT_TAKEN:
+        raise PkvError(f"{name}: unsupported arguments")
+    _check(name, status)
 
 
 def _on_current(*ts):
@@ -423,14 +441,6 @@ def _head_dense(t):
         raise PkvError("the heads of a token must be contiguous")
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _err_ok(err, dev):
-    return err is None or (err.dtype is _i32 and err.get_device() == dev)
-
-
 def _scratch(nbytes, device, stream):
     """A workspace of nbytes that stays alive for the work on `stream`."""
     if nbytes == 0:
@@ -459,19 +469,11 @@ def rope_append(q, k, v, positions, slot_mapping, table: RopeTable, k_pool, v_po
     returns the rotated q.  Tokens may be strided (parts of one fused projection); q_out may be q."""
     n, n_h, d = _dims("q", q, 3)
     num_blocks, n_kv, bs, _ = _dims("k_pool", k_pool, 4)
-    dev = q.get_device()
     if q_out is None:
         q_out = _empty((n, n_h, d), q.dtype, q.device, stream)
-    kvs, sq, sk, sv, so = (n, n_kv, d), q.stride(), k.stride(), v.stride(), q_out.stride()
-    if not (dev == k.get_device() == v.get_device() == positions.get_device() == slot_mapping.get_device()
-            == k_pool.get_device() == v_pool.get_device() == q_out.get_device() and dev >= 0 and dev == _device()
-            and q.dtype is _bf16 and k.dtype is _bf16 and v.dtype is _bf16 and k_pool.dtype is _bf16
-            and v_pool.dtype is _bf16 and q_out.dtype is _bf16 and positions.dtype is _i32
-            and slot_mapping.dtype is _i64 and k.shape == kvs and v.shape == kvs and q_out.shape == q.shape
-            and v_pool.shape == k_pool.shape and positions.shape == (n,) and slot_mapping.shape == (n,)
-            and positions.is_contiguous() and slot_mapping.is_contiguous() and k_pool.is_contiguous()
-            and v_pool.is_contiguous() and sq[2] == sk[2] == sv[2] == so[2] == 1
-            and (n_h == 1 or sq[1] == so[1] == d) and (n_kv == 1 or sk[1] == sv[1] == d) and _err_ok(err, dev)):
+    st = (_calls or _native()).rope_append(q, k, v, positions, slot_mapping, ctypes.addressof(table), k_pool, v_pool, q_out,
+                                           err, None if stream is None else stream.cuda_stream)
+    if st == _NOT_TAKEN:
         _on_current(q, k, v, positions, slot_mapping, k_pool, v_pool, q_out, err)
         _typed(_bf16, q, k, v, k_pool, v_pool, q_out)
         _typed(_i32, positions, err)
@@ -480,21 +482,14 @@ def rope_append(q, k, v, positions, slot_mapping, table: RopeTable, k_pool, v_po
         _shaped("v", v, n, n_kv, d)
         _shaped("positions", positions, n)
         _shaped("slot_mapping", slot_mapping, n)
-        _shaped("v_pool", v_pool, num_blocks, n_kv, bs, k_pool.shape[3])
+        _shaped("k_pool", k_pool, num_blocks, n_kv, bs, d)
+        _shaped("v_pool", v_pool, num_blocks, n_kv, bs, d)
         _shaped("q_out", q_out, n, n_h, d)
         _dense(positions, slot_mapping, k_pool, v_pool)
         for t in (q, k, v, q_out):
             _head_dense(t)
-    if k_pool.shape[3] != d:
-        raise PkvError("the pools' head_dim differs from q's")
-    many = n > 1                                               # one token has no stride
-    st = lib().pkv_rope_append(
-        q.data_ptr(), sq[0] if many else n_h * d, k.data_ptr(), sk[0] if many else n_kv * d, v.data_ptr(),
-        sv[0] if many else n_kv * d, positions.data_ptr(), slot_mapping.data_ptr(), n, ctypes.addressof(table),
-        q_out.data_ptr(), so[0] if many else n_h * d, k_pool.data_ptr(), v_pool.data_ptr(), num_blocks, bs, n_h, n_kv, d,
-        None if err is None else err.data_ptr(), _raw_current(dev) if stream is None else stream.cuda_stream)
     if st:
-        _check("rope_append", st)
+        _failed("rope_append", st)
     return q_out
 
 
@@ -503,18 +498,13 @@ def rope_qk(q, k, positions, table: RopeTable, q_out=None, k_out=None, stream=No
     given as q and k themselves."""
     n, n_h, d = _dims("q", q, 3)
     n_kv = _dims("k", k, 3)[1]
-    dev = q.get_device()
     if q_out is None:
         q_out = _empty((n, n_h, d), q.dtype, q.device, stream)
     if k_out is None:
         k_out = _empty((n, n_kv, d), k.dtype, k.device, stream)
-    sq, sk, so, ko = q.stride(), k.stride(), q_out.stride(), k_out.stride()
-    if not (dev == k.get_device() == positions.get_device() == q_out.get_device() == k_out.get_device() and dev >= 0
-            and dev == _device() and q.dtype is _bf16 and k.dtype is _bf16 and q_out.dtype is _bf16
-            and k_out.dtype is _bf16 and positions.dtype is _i32 and k.shape == (n, n_kv, d) and k_out.shape == k.shape
-            and q_out.shape == q.shape and positions.shape == (n,) and positions.is_contiguous()
-            and sq[2] == sk[2] == so[2] == ko[2] == 1 and (n_h == 1 or sq[1] == so[1] == d)
-            and (n_kv == 1 or sk[1] == ko[1] == d)):
+    st = (_calls or _native()).rope_qk(q, k, positions, ctypes.addressof(table), q_out, k_out,
+                                       None if stream is None else stream.cuda_stream)
+    if st == _NOT_TAKEN:
         _on_current(q, k, positions, q_out, k_out)
         _typed(_bf16, q, k, q_out, k_out)
         _typed(_i32, positions)
@@ -525,13 +515,8 @@ def rope_qk(q, k, positions, table: RopeTable, q_out=None, k_out=None, stream=No
         _dense(positions)
         for t in (q, k, q_out, k_out):
             _head_dense(t)
-    many = n > 1
-    st = lib().pkv_rope_qk(
-        q.data_ptr(), sq[0] if many else n_h * d, k.data_ptr(), sk[0] if many else n_kv * d, positions.data_ptr(), n,
-        ctypes.addressof(table), q_out.data_ptr(), so[0] if many else n_h * d, k_out.data_ptr(),
-        ko[0] if many else n_kv * d, n_h, n_kv, d, _raw_current(dev) if stream is None else stream.cuda_stream)
     if st:
-        _check("rope_qk", st)
+        _failed("rope_qk", st)
     return q_out, k_out
 
 
@@ -584,14 +569,8 @@ def alloc_q8_cache(num_blocks, n_kv, block_size, head_dim, tail_rows, fmt="e4m3"
     return Q8CacheTensors(torch.zeros(num_blocks, n_kv, rec, dtype=torch.uint8, device=device), tail(), tail(), fmt)
 
 
-def _q8_ok(cache, nb, n_kv, bs, d, dev):
-    r, kt, vt = cache.records, cache.k_tail, cache.v_tail
-    return (r.dtype is _u8 and kt.dtype is _bf16 and vt.dtype is _bf16 and r.is_contiguous() and kt.is_contiguous()
-            and vt.is_contiguous() and vt.shape == kt.shape and r.shape == (nb, n_kv, 2 * bs * d + 16)
-            and dev == r.get_device() == kt.get_device() == vt.get_device())
-
-
-def _q8_refuse(cache, nb, n_kv, bs, d):
+def _q8_refuse(cache):
+    nb, n_kv, bs, d = cache.shape
     _typed(_u8, cache.records)
     _typed(_bf16, cache.k_tail, cache.v_tail)
     _dense(cache.records, cache.k_tail, cache.v_tail)
@@ -608,16 +587,11 @@ def _q8_format(cache):
 def kv_quant_append_q8(k, v, slot_mapping, tail_seq, cache: Q8CacheTensors, err=None, stream=None):
     """Quantize-on-append of k, v [n_tok][n_kv][d] (tokens may be strided) into the 8-bit cache."""
     fmt = _q8_format(cache)
-    rows, n_kv, bs, d = _dims("k_tail", cache.k_tail, 4)
-    nb = cache.records.shape[0]
-    n = _dims("k", k, 3)[0]
-    dev = k.get_device()
-    sk, sv, kvs = k.stride(), v.stride(), (n, n_kv, d)
-    if not (dev == v.get_device() == slot_mapping.get_device() == tail_seq.get_device() and dev >= 0 and dev == _device()
-            and k.dtype is _bf16 and v.dtype is _bf16 and slot_mapping.dtype is _i64 and tail_seq.dtype is _i32
-            and k.shape == kvs and v.shape == kvs and slot_mapping.shape == (n,) and tail_seq.shape == (n,)
-            and slot_mapping.is_contiguous() and tail_seq.is_contiguous() and sk[2] == sv[2] == 1
-            and (n_kv == 1 or sk[1] == sv[1] == d) and _err_ok(err, dev) and _q8_ok(cache, nb, n_kv, bs, d, dev)):
+    st = (_calls or _native()).kv_quant_append_q8(k, v, slot_mapping, tail_seq, cache.records, cache.k_tail, cache.v_tail, fmt,
+                                                  err, None if stream is None else stream.cuda_stream)
+    if st == _NOT_TAKEN:
+        n = _dims("k", k, 3)[0]
+        _, n_kv, bs, d = _dims("k_tail", cache.k_tail, 4)
         _on_current(k, v, slot_mapping, tail_seq, cache.records, cache.k_tail, cache.v_tail, err)
         _typed(_bf16, k, v)
         _typed(_i64, slot_mapping)
@@ -627,16 +601,11 @@ def kv_quant_append_q8(k, v, slot_mapping, tail_seq, cache: Q8CacheTensors, err=
         _shaped("slot_mapping", slot_mapping, n)
         _shaped("tail_seq", tail_seq, n)
         _dense(slot_mapping, tail_seq)
-        _q8_refuse(cache, nb, n_kv, bs, d)
+        _q8_refuse(cache)
         for t in (k, v):
             _head_dense(t)
-    many = n > 1
-    st = lib().pkv_kv_quant_append_q8(
-        k.data_ptr(), sk[0] if many else n_kv * d, v.data_ptr(), sv[0] if many else n_kv * d, slot_mapping.data_ptr(),
-        tail_seq.data_ptr(), n, fmt, cache.records.data_ptr(), cache.k_tail.data_ptr(), cache.v_tail.data_ptr(), rows, nb,
-        bs, n_kv, d, _addr(err), _raw_current(dev) if stream is None else stream.cuda_stream)
     if st:
-        _check("kv_quant_append_q8", st)
+        _failed("kv_quant_append_q8", st)
 
 
 def q8_workspace_bytes(batch, n_h, n_kv, head_dim, block_size, fmt="e4m3") -> int:
@@ -651,39 +620,31 @@ def paged_decode_attn_q8(q, cache: Q8CacheTensors, block_tables, context_lens, s
                          out_dtype=torch.bfloat16, workspace=None, err=None, stream=None):
     """Decode attention over the 8-bit cache (the last `window` tokens of each context; 0: all)."""
     fmt = _q8_format(cache)
-    _, n_kv, bs, d = _dims("k_tail", cache.k_tail, 4)
-    nb = cache.records.shape[0]
-    B, n_h, _ = _dims("q", q, 3)
-    mb = _dims("block_tables", block_tables, 2)[1]
-    dev = q.get_device()
     if out is None:
         out = _empty(q.shape, _out_type(out_dtype), q.device, stream)
-    if workspace is None and dev >= 0 and B:
+    if workspace is None and q.is_cuda and q.shape[0]:
+        _, n_kv, bs, d = _dims("k_tail", cache.k_tail, 4)
+        B, n_h, _ = _dims("q", q, 3)
         workspace = _scratch(lib().pkv_q8_workspace_bytes(B, n_h, n_kv, d, bs, fmt), q.device, stream)
-    if not (dev == block_tables.get_device() == context_lens.get_device() == out.get_device() and dev >= 0
-            and dev == _device() and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))
-            and q.dtype is _bf16 and block_tables.dtype is _i32 and context_lens.dtype is _i32
-            and (out.dtype is _bf16 or out.dtype is _f32) and q.shape == (B, n_h, d) and block_tables.shape == (B, mb)
-            and context_lens.shape == (B,) and out.shape == q.shape and q.is_contiguous()
-            and block_tables.is_contiguous() and context_lens.is_contiguous() and out.is_contiguous()
-            and _err_ok(err, dev) and _q8_ok(cache, nb, n_kv, bs, d, dev)):
+    st = (_calls or _native()).paged_decode_attn_q8(q, cache.records, cache.k_tail, cache.v_tail, fmt, block_tables,
+                                                    context_lens, scale, int(window), out, workspace, err,
+                                                    None if stream is None else stream.cuda_stream)
+    if st == _NOT_TAKEN:
+        d = _dims("k_tail", cache.k_tail, 4)[3]
+        B, n_h, _ = _dims("q", q, 3)
+        _dims("block_tables", block_tables, 2)
         _on_current(q, cache.records, cache.k_tail, cache.v_tail, block_tables, context_lens, out, workspace, err)
         _typed(_bf16, q)
         _typed(_i32, block_tables, context_lens, err)
         _out_type(out.dtype)
         _shaped("q", q, B, n_h, d)
-        _shaped("block_tables", block_tables, B, mb)
+        _shaped("block_tables", block_tables, B, block_tables.shape[1])
         _shaped("context_lens", context_lens, B)
         _shaped("out", out, B, n_h, d)
         _dense(q, block_tables, context_lens, out, workspace)
-        _q8_refuse(cache, nb, n_kv, bs, d)
-    st = lib().pkv_paged_decode_attn_q8(
-        q.data_ptr(), cache.records.data_ptr(), fmt, block_tables.data_ptr(), mb, context_lens.data_ptr(), scale,
-        int(window), B, n_h, n_kv, d, bs, nb, out.data_ptr(), 1 if out.dtype is _f32 else 0, _addr(workspace),
-        0 if workspace is None else workspace.nbytes, _addr(err),
-        _raw_current(dev) if stream is None else stream.cuda_stream)
+        _q8_refuse(cache)
     if st:
-        _check("paged_decode_attn_q8", st)
+        _failed("paged_decode_attn_q8", st)
     return out
 
 
@@ -699,24 +660,20 @@ def paged_decode_attn_mass(q, k_pool, v_pool, block_tables, context_lens, scale,
                            out_dtype=torch.bfloat16, workspace=None, err=None, stream=None):
     """paged_decode_attn that also adds each cached token's attention weight, summed over the query
     heads of its group, to mass (fp32 [B][n_kv][at least max_blocks * block_size])."""
-    B, n_h, d = _dims("q", q, 3)
-    nb, n_kv, bs, _ = _dims("k_pool", k_pool, 4)
-    mb = _dims("block_tables", block_tables, 2)[1]
-    T = _dims("mass", mass, 3)[2]
-    dev = q.get_device()
     if out is None:
         out = _empty(q.shape, _out_type(out_dtype), q.device, stream)
-    if workspace is None and dev >= 0 and B:
+    if workspace is None and q.is_cuda and q.shape[0]:
+        B, n_h, d = _dims("q", q, 3)
+        _, n_kv, bs, _ = _dims("k_pool", k_pool, 4)
+        mb = _dims("block_tables", block_tables, 2)[1]
         workspace = _scratch(lib().pkv_mass_workspace_bytes(B, n_h, n_kv, d, bs, mb), q.device, stream)
-    if not (dev == k_pool.get_device() == v_pool.get_device() == block_tables.get_device() == context_lens.get_device()
-            == mass.get_device() == out.get_device() and dev >= 0 and dev == _device()
-            and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))
-            and q.dtype is _bf16 and k_pool.dtype is _bf16 and v_pool.dtype is _bf16 and block_tables.dtype is _i32
-            and context_lens.dtype is _i32 and mass.dtype is _f32 and (out.dtype is _bf16 or out.dtype is _f32)
-            and k_pool.shape == (nb, n_kv, bs, d) and v_pool.shape == k_pool.shape and block_tables.shape == (B, mb)
-            and context_lens.shape == (B,) and mass.shape == (B, n_kv, T) and out.shape == q.shape
-            and q.is_contiguous() and k_pool.is_contiguous() and v_pool.is_contiguous() and block_tables.is_contiguous()
-            and context_lens.is_contiguous() and mass.is_contiguous() and out.is_contiguous() and _err_ok(err, dev)):
+    st = (_calls or _native()).paged_decode_attn_mass(q, k_pool, v_pool, block_tables, context_lens, scale, mass, out, workspace,
+                                                      err, None if stream is None else stream.cuda_stream)
+    if st == _NOT_TAKEN:
+        B, n_h, d = _dims("q", q, 3)
+        nb, n_kv, bs, _ = _dims("k_pool", k_pool, 4)
+        mb = _dims("block_tables", block_tables, 2)[1]
+        T = _dims("mass", mass, 3)[2]
         _on_current(q, k_pool, v_pool, block_tables, context_lens, mass, out, workspace, err)
         _typed(_bf16, q, k_pool, v_pool)
         _typed(_i32, block_tables, context_lens, err)
@@ -729,13 +686,8 @@ def paged_decode_attn_mass(q, k_pool, v_pool, block_tables, context_lens, scale,
         _shaped("mass", mass, B, n_kv, T)
         _shaped("out", out, B, n_h, d)
         _dense(q, k_pool, v_pool, block_tables, context_lens, mass, out, workspace)
-    st = lib().pkv_paged_decode_attn_mass(
-        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), mb, context_lens.data_ptr(), scale, B,
-        n_h, n_kv, d, bs, nb, out.data_ptr(), 1 if out.dtype is _f32 else 0, mass.data_ptr(), T, _addr(workspace),
-        0 if workspace is None else workspace.nbytes, _addr(err),
-        _raw_current(dev) if stream is None else stream.cuda_stream)
     if st:
-        _check("paged_decode_attn_mass", st)
+        _failed("paged_decode_attn_mass", st)
     return out
 
 
@@ -767,38 +719,26 @@ def evict_workspace_bytes(batch, n_kv, block_size, max_blocks) -> int:
     return n
 
 
-def _evict_ok(st, B, n_kv, T, dev):
-    m, p, k, x = st.mass, st.positions, st.kept, st.dropped
-    return (m.dtype is _f32 and p.dtype is _i32 and k.dtype is _i32 and x.dtype is _i32 and m.shape == (B, n_kv, T)
-            and p.shape == m.shape and k.shape == (B,) and x.shape == (B,) and m.is_contiguous() and p.is_contiguous()
-            and k.is_contiguous() and x.is_contiguous()
-            and dev == m.get_device() == p.get_device() == k.get_device() == x.get_device())
-
-
 def kv_evict(k_pool, v_pool, block_tables, context_lens, keep, recent, state: EvictState, out: EvictState | None = None,
              new_lens=None, workspace=None, err=None, stream=None):
     """Cut each sequence of the bf16 cache to keep[s] rows (int32 [B]): those of its last `recent`
     tokens and those with the largest accounts.  Updates `state` in place, or writes the new state to
     `out`; returns the new context lengths (a tensor of its own)."""
     dst = state if out is None else out
-    nb, n_kv, bs, d = _dims("k_pool", k_pool, 4)
-    B, mb = _dims("block_tables", block_tables, 2)
-    T = _dims("mass", state.mass, 3)[2]
-    dev = k_pool.get_device()
     if new_lens is None:
         new_lens = _empty(context_lens.shape, _i32, context_lens.device, stream)
-    if workspace is None and dev >= 0 and B:
+    if workspace is None and k_pool.is_cuda and block_tables.shape[0]:
+        B, mb = _dims("block_tables", block_tables, 2)
+        _, n_kv, bs, _ = _dims("k_pool", k_pool, 4)
         workspace = _scratch(lib().pkv_evict_workspace_bytes(B, n_kv, bs, mb), k_pool.device, stream)
-    if not (dev == v_pool.get_device() == block_tables.get_device() == context_lens.get_device() == keep.get_device()
-            == new_lens.get_device() and dev >= 0 and dev == _device()
-            and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))
-            and k_pool.dtype is _bf16 and v_pool.dtype is _bf16 and block_tables.dtype is _i32
-            and context_lens.dtype is _i32 and keep.dtype is _i32 and new_lens.dtype is _i32
-            and v_pool.shape == k_pool.shape and context_lens.shape == (B,) and keep.shape == (B,)
-            and new_lens.shape == (B,) and k_pool.is_contiguous() and v_pool.is_contiguous()
-            and block_tables.is_contiguous() and context_lens.is_contiguous() and keep.is_contiguous()
-            and new_lens.is_contiguous() and _err_ok(err, dev) and _evict_ok(state, B, n_kv, T, dev)
-            and (out is None or _evict_ok(out, B, n_kv, T, dev))):
+    st = (_calls or _native()).kv_evict(k_pool, v_pool, block_tables, context_lens, keep, int(recent), state.mass,
+                                        state.positions, state.kept, state.dropped, dst.mass, dst.positions, dst.kept,
+                                        dst.dropped, new_lens, workspace, err,
+                                        None if stream is None else stream.cuda_stream)
+    if st == _NOT_TAKEN:
+        nb, n_kv, bs, d = _dims("k_pool", k_pool, 4)
+        B, mb = _dims("block_tables", block_tables, 2)
+        T = _dims("mass", state.mass, 3)[2]
         _on_current(k_pool, v_pool, block_tables, context_lens, keep, state.mass, state.positions, state.kept,
                     state.dropped, dst.mass, dst.positions, dst.kept, dst.dropped, new_lens, workspace, err)
         _typed(_bf16, k_pool, v_pool)
@@ -806,24 +746,18 @@ def kv_evict(k_pool, v_pool, block_tables, context_lens, keep, recent, state: Ev
                dst.kept, dst.dropped, new_lens, err)
         _typed(_f32, state.mass, dst.mass)
         _shaped("v_pool", v_pool, nb, n_kv, bs, d)
-        for st in (state, dst):
-            _shaped("mass", st.mass, B, n_kv, T)
-            _shaped("positions", st.positions, B, n_kv, T)
-            _shaped("kept", st.kept, B)
-            _shaped("dropped", st.dropped, B)
+        for es in (state, dst):
+            _shaped("mass", es.mass, B, n_kv, T)
+            _shaped("positions", es.positions, B, n_kv, T)
+            _shaped("kept", es.kept, B)
+            _shaped("dropped", es.dropped, B)
         _shaped("context_lens", context_lens, B)
         _shaped("keep", keep, B)
         _shaped("new_lens", new_lens, B)
         _dense(k_pool, v_pool, block_tables, context_lens, keep, state.mass, state.positions, state.kept, state.dropped,
                dst.mass, dst.positions, dst.kept, dst.dropped, new_lens, workspace)
-    st = lib().pkv_kv_evict(
-        k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), mb, context_lens.data_ptr(), keep.data_ptr(),
-        int(recent), state.mass.data_ptr(), state.positions.data_ptr(), state.kept.data_ptr(), state.dropped.data_ptr(),
-        dst.mass.data_ptr(), dst.positions.data_ptr(), dst.kept.data_ptr(), dst.dropped.data_ptr(), T,
-        new_lens.data_ptr(), B, n_kv, d, bs, nb, _addr(workspace), 0 if workspace is None else workspace.nbytes,
-        _addr(err), _raw_current(dev) if stream is None else stream.cuda_stream)
     if st:
-        _check("kv_evict", st)
+        _failed("kv_evict", st)
     return new_lens
 
 
