@@ -378,7 +378,7 @@ pkv_status pkv_rope_qk(const void* q, int64_t q_stride, const void* k, int64_t k
  * Caller contract: as for pkv_kv_quant_append_int4 (slots distinct; within a call the tokens of a
  * sequence are consecutive entries in logical order with one tail_seq; a sequence starts at row 0
  * of its first block); values finite (a NaN is lost in INT8 and stays NaN in E4M3, an infinity
- * spoils its block).  A sequence may be cut back inside its unfinished block (the tail still holds
+ * spoils its block); n_tok <= 0x7fff0000.  A sequence may be cut back inside its unfinished block (the tail still holds
  * the rows that remain), not into a finished one.  A slot or tail row out of range sets PKV_DEV_BAD_SLOT and is skipped.
  */
 #define PKV_Q8_E4M3 0
@@ -393,7 +393,9 @@ pkv_status pkv_kv_quant_append_q8(const void* k, int64_t k_stride, const void* v
  * paged_decode_attn_q8 — decode attention over the records written by pkv_kv_quant_append_q8,
  * equal to the attention over the values held (code * scale) up to fp32 accumulation: the scales
  * are taken out of the products, the codes enter the tensor cores exactly (as fp16), q exactly up
- * to 2^-39 of its head's largest value, p as a high + low fp16 pair (22 bits, down to 2^-31).
+ * to 2^-39 of its head's largest value, p as a high + low fp16 pair (22 bits, down to 2^-31); for a
+ * bf16 output and groups of over four query heads p is rounded to fp16 once (an error of at most
+ * 2^-11 sum p |v|, under the output's own rounding wherever its terms do not cancel).
  * window as for pkv_paged_decode_attn_window (0: the whole context).  Other arguments, output and
  * errors as for pkv_paged_decode_attn; workspace of pkv_q8_workspace_bytes (0: invalid shape).
  * The tails are not read.

@@ -458,6 +458,12 @@ def _empty(shape, dtype, device, stream):
     return out
 
 
+def _table(table):
+    if type(table) is not RopeTable:
+        raise PkvError("the table must come from rope_table")
+    return ctypes.addressof(table)
+
+
 def _out_type(out_dtype):
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise PkvError("out_dtype must be bfloat16 or float32")
@@ -471,8 +477,8 @@ def rope_append(q, k, v, positions, slot_mapping, table: RopeTable, k_pool, v_po
     num_blocks, n_kv, bs, _ = _dims("k_pool", k_pool, 4)
     if q_out is None:
         q_out = _empty((n, n_h, d), q.dtype, q.device, stream)
-    st = (_calls or _native()).rope_append(q, k, v, positions, slot_mapping, ctypes.addressof(table), k_pool, v_pool, q_out,
-                                           err, None if stream is None else stream.cuda_stream)
+    st = (_calls or _native()).rope_append(q, k, v, positions, slot_mapping, _table(table), k_pool, v_pool, q_out, err,
+                                           None if stream is None else stream.cuda_stream)
     if st == _NOT_TAKEN:
         _on_current(q, k, v, positions, slot_mapping, k_pool, v_pool, q_out, err)
         _typed(_bf16, q, k, v, k_pool, v_pool, q_out)
@@ -502,7 +508,7 @@ def rope_qk(q, k, positions, table: RopeTable, q_out=None, k_out=None, stream=No
         q_out = _empty((n, n_h, d), q.dtype, q.device, stream)
     if k_out is None:
         k_out = _empty((n, n_kv, d), k.dtype, k.device, stream)
-    st = (_calls or _native()).rope_qk(q, k, positions, ctypes.addressof(table), q_out, k_out,
+    st = (_calls or _native()).rope_qk(q, k, positions, _table(table), q_out, k_out,
                                        None if stream is None else stream.cuda_stream)
     if st == _NOT_TAKEN:
         _on_current(q, k, positions, q_out, k_out)

@@ -107,6 +107,22 @@ struct Args {
 };
 
 PyObject* result(long status) { return PyLong_FromLong(status); }
+
+// The C call without the interpreter's lock: a launch may wait for room in the stream's queue.
+struct NoLock {
+  PyThreadState* state = PyEval_SaveThread();
+  ~NoLock() { PyEval_RestoreThread(state); }
+};
+template <class F>
+PyObject* unlocked(F call) {
+  pkv_status st;
+  {
+    const NoLock none;
+    st = call();
+  }
+  return result(st);
+}
+
 int32_t* ints(const at::Tensor& t) { return t.data_ptr<int32_t>(); }
 
 // a workspace of any type and shape, or none
@@ -134,9 +150,11 @@ PyObject* rope_append(PyObject* const* a, Py_ssize_t n_args) {
   void* stream = x.stream(10);
   x.sizes(n, n_h, nb, n_kv, bs, d);
   if (!x.ok) return result(kNotTaken);
-  return result(pkv_rope_append(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, ints(pos), slots.data_ptr<int64_t>(), (int)n,
-                                table, out.data_ptr(), so, kp.data_ptr(), vp.data_ptr(), (int)nb, (int)bs, (int)n_h, (int)n_kv,
-                                (int)d, err, stream));
+  return unlocked([&] {
+    return pkv_rope_append(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, ints(pos), slots.data_ptr<int64_t>(), (int)n,
+                           table, out.data_ptr(), so, kp.data_ptr(), vp.data_ptr(), (int)nb, (int)bs, (int)n_h, (int)n_kv,
+                           (int)d, err, stream);
+  });
 }
 
 // q, k, positions, table address, q_out, k_out, stream
@@ -154,8 +172,10 @@ PyObject* rope_qk(PyObject* const* a, Py_ssize_t n_args) {
   void* stream = x.stream(6);
   x.sizes(n, n_h, n_kv, d);
   if (!x.ok) return result(kNotTaken);
-  return result(pkv_rope_qk(q.data_ptr(), sq, k.data_ptr(), sk, ints(pos), (int)n, table, qo.data_ptr(), so, kout.data_ptr(), ko,
-                            (int)n_h, (int)n_kv, (int)d, stream));
+  return unlocked([&] {
+    return pkv_rope_qk(q.data_ptr(), sq, k.data_ptr(), sk, ints(pos), (int)n, table, qo.data_ptr(), so, kout.data_ptr(), ko,
+                       (int)n_h, (int)n_kv, (int)d, stream);
+  });
 }
 
 // An 8-bit cache's records, k_tail and v_tail at a[i .. i + 2].
@@ -188,9 +208,11 @@ PyObject* kv_quant_append_q8(PyObject* const* a, Py_ssize_t n_args) {
   void* stream = x.stream(9);
   x.sizes(n);
   if (!x.ok) return result(kNotTaken);
-  return result(pkv_kv_quant_append_q8(k.data_ptr(), sk, v.data_ptr(), sv, slots.data_ptr<int64_t>(), ints(seq), (int)n, format,
-                                       c.records.data_ptr<uint8_t>(), c.k_tail.data_ptr(), c.v_tail->data_ptr(), (int)c.rows,
-                                       (int)c.nb, (int)c.bs, (int)c.n_kv, (int)c.d, err, stream));
+  return unlocked([&] {
+    return pkv_kv_quant_append_q8(k.data_ptr(), sk, v.data_ptr(), sv, slots.data_ptr<int64_t>(), ints(seq), (int)n, format,
+                                  c.records.data_ptr<uint8_t>(), c.k_tail.data_ptr(), c.v_tail->data_ptr(), (int)c.rows,
+                                  (int)c.nb, (int)c.bs, (int)c.n_kv, (int)c.d, err, stream);
+  });
 }
 
 // What the attention calls share: q, block tables, context lengths, output and workspace (None for none).
@@ -229,9 +251,11 @@ PyObject* paged_decode_attn_q8(PyObject* const* a, Py_ssize_t n_args) {
   int32_t* err = x.err(11);
   void* stream = x.stream(12);
   if (!x.ok) return result(kNotTaken);
-  return result(pkv_paged_decode_attn_q8(t.q.data_ptr(), c.records.data_ptr<uint8_t>(), format, ints(*t.bt), (int)t.mb, ints(*t.ctx),
-                                         scale, window, (int)t.B, (int)t.n_h, (int)c.n_kv, (int)c.d, (int)c.bs, (int)c.nb,
-                                         t.out->data_ptr(), t.out_type, t.ws, t.ws_bytes, err, stream));
+  return unlocked([&] {
+    return pkv_paged_decode_attn_q8(t.q.data_ptr(), c.records.data_ptr<uint8_t>(), format, ints(*t.bt), (int)t.mb, ints(*t.ctx),
+                                    scale, window, (int)t.B, (int)t.n_h, (int)c.n_kv, (int)c.d, (int)c.bs, (int)c.nb,
+                                    t.out->data_ptr(), t.out_type, t.ws, t.ws_bytes, err, stream);
+  });
 }
 
 // q, k_pool, v_pool, block_tables, context_lens, scale, mass, out, workspace, err, stream
@@ -249,9 +273,11 @@ PyObject* paged_decode_attn_mass(PyObject* const* a, Py_ssize_t n_args) {
   void* stream = x.stream(10);
   x.sizes(nb, n_kv, bs, d);
   if (!x.ok) return result(kNotTaken);
-  return result(pkv_paged_decode_attn_mass(t.q.data_ptr(), kp.data_ptr(), vp.data_ptr(), ints(*t.bt), (int)t.mb, ints(*t.ctx), scale,
-                                           (int)t.B, (int)t.n_h, (int)n_kv, (int)d, (int)bs, (int)nb, t.out->data_ptr(), t.out_type,
-                                           mass.data_ptr<float>(), T, t.ws, t.ws_bytes, err, stream));
+  return unlocked([&] {
+    return pkv_paged_decode_attn_mass(t.q.data_ptr(), kp.data_ptr(), vp.data_ptr(), ints(*t.bt), (int)t.mb, ints(*t.ctx), scale,
+                                      (int)t.B, (int)t.n_h, (int)n_kv, (int)d, (int)bs, (int)nb, t.out->data_ptr(), t.out_type,
+                                      mass.data_ptr<float>(), T, t.ws, t.ws_bytes, err, stream);
+  });
 }
 
 // One state of an eviction, mass, positions, kept and dropped at a[i .. i + 3].
@@ -284,9 +310,11 @@ PyObject* kv_evict(PyObject* const* a, Py_ssize_t n_args) {
   void* stream = x.stream(17);
   x.sizes(nb, n_kv, bs, d, B, mb);
   if (!x.ok) return result(kNotTaken);
-  return result(pkv_kv_evict(kp.data_ptr(), vp.data_ptr(), ints(bt), (int)mb, ints(ctx), ints(keep), recent, from.mass, from.positions,
-                             from.kept, from.dropped, to.mass, to.positions, to.kept, to.dropped, T, ints(new_lens), (int)B, (int)n_kv,
-                             (int)d, (int)bs, (int)nb, ws, ws_bytes, err, stream));
+  return unlocked([&] {
+    return pkv_kv_evict(kp.data_ptr(), vp.data_ptr(), ints(bt), (int)mb, ints(ctx), ints(keep), recent, from.mass, from.positions,
+                        from.kept, from.dropped, to.mass, to.positions, to.kept, to.dropped, T, ints(new_lens), (int)B, (int)n_kv,
+                        (int)d, (int)bs, (int)nb, ws, ws_bytes, err, stream);
+  });
 }
 
 // No C++ exception leaves a call: one inside, before the C call, counts as "not taken".

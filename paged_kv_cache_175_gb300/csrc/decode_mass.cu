@@ -20,8 +20,6 @@
 #include <cstdlib>
 #include <mutex>
 
-
-
 #include "decode_mass.cuh"
 #include "nvtx_range.h"
 #include "piece_streams.cuh"

@@ -305,6 +305,7 @@ extern "C" pkv_status pkv_kv_quant_append_q8(const void* k, int64_t k_stride, co
   if (pkv_q8_record_bytes(block_size, head_dim) == 0) return PKV_EINVAL;
   if (format != PKV_Q8_E4M3 && format != PKV_Q8_INT8) return PKV_EINVAL;
   if (n_tok == 0) return PKV_OK;
+  if (n_tok > 0x7fff0000) return PKV_ERANGE;                  // token numbers of a span stay in 32 bits
   if (!k || !v || !slot_mapping || !tail_seq || !cache || !k_tail || !v_tail) return PKV_EINVAL;
   if (!al16(k) || !al16(v) || !al16(cache) || !al16(k_tail) || !al16(v_tail)) return PKV_EINVAL;
   const long long row = (long long)n_kv * head_dim;

@@ -219,6 +219,11 @@ def test_bindings_refuse_cpu_tensors():
                  lambda: pkv.kv_evict(pool, pool, i32[None], i32, i32, 0, st)):
         with pytest.raises(pkv.PkvError):
             call()
+    for table in (None, 0, ctypes.create_string_buffer(64)):            # not a table: never read as one
+        with pytest.raises(pkv.PkvError):
+            pkv.rope_append(z, z, z, i32, i64, table, pool, pool)
+        with pytest.raises(pkv.PkvError):
+            pkv.rope_qk(z, z, i32, table)
     with pytest.raises(ValueError):
         pkv.alloc_q8_cache(1, 1, 16, 96, 1, device="cpu")
 
@@ -240,7 +245,7 @@ def test_c_entries_refuse_bad_arguments():
     q8 = lambda **k: L.pkv_kv_quant_append_q8(*[{**dict(k=p, ks=128, v=p, vs=128, slot=p, ts=p, n=1, f=0, c=p, kt=p, vt=p, tr=1, nb=4,
                                                         bs=16, nkv=2, d=64, e=None, s=None), **k}[x] for x in
                                                  "k ks v vs slot ts n f c kt vt tr nb bs nkv d e s".split()])
-    assert q8(n=0) == 0
+    assert q8(n=0) == 0 and q8(n=0x7fff0001) == -2
     for bad in (dict(n=-1), dict(f=2), dict(bs=128), dict(d=80), dict(ks=64), dict(vs=132), dict(c=p + 8), dict(vt=None), dict(tr=-1)):
         assert q8(**bad) == -1, bad
     ev_ = lambda **k: L.pkv_kv_evict(*[{**dict(kp=p, vp=p, bt=p, mb=2, ctx=p, keep=p, rec=0, m=p, pos=p, kd=p, dr=p, mo=p, po=p, ko=p,
