@@ -43,7 +43,7 @@ __device__ __forceinline__ uint32_t keep_rows(uint32_t b, int t, int ntok) {
 // TT: 16-token units per stage; NH n-tiles of 8 heads per consumer warp, MT consumer warps per
 // stream, NW streams.  sub: log2 of the units per table block.
 template <int D, int TT, int NH, int MT, int NW>
-__global__ void __launch_bounds__((NW * MT + 1) * 32, NH == 2 ? 2 : 1)
+__global__ void __launch_bounds__((NW * MT + 1) * 32, MT == 4 && NH == 1 ? 3 : (NH == 2 ? 2 : 1))
     decode_mass_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                        const DecodeArgs a, const MassArgs ms, const int sub) {
   constexpr int KS = D / 16, MD = D / 16, HW = 8 * NH, NBOX = D / 64;
@@ -363,6 +363,9 @@ struct MassVariant {
   size_t smem;
 };
 
+// Streams, consumer warps and heads per warp by group.  One kv head, 17-32 heads, d = 128: four warps
+// of 8 heads, three CTAs per SM, 42.4 us for 8 x 20-40K tokens (64 x 2-8K: 54.6) against 43.8 (55.8)
+// with two warps of 16; at d = 64, 43.2 against 42.0 the other way.
 template <int D, int TT>
 static void mass_pick(int tiling, MassVariant& v) {
   auto set = [&](const void* fn, int mt, int nw) {
@@ -372,6 +375,7 @@ static void mass_pick(int tiling, MassVariant& v) {
   };
   if (tiling == 0) set((const void*)decode_mass_kernel<D, TT, 1, 1, 3>, 1, 3);
   else if (tiling == 1) set((const void*)decode_mass_kernel<D, TT, 2, 1, 3>, 1, 3);
+  else if (tiling == 2 && D == 128) set((const void*)decode_mass_kernel<D, TT, 1, 4, 1>, 4, 1);
   else if (tiling == 2) set((const void*)decode_mass_kernel<D, TT, 2, 2, 2>, 2, 2);
   else set((const void*)decode_mass_kernel<D, TT, 2, 4, 1>, 4, 1);
 }
@@ -389,7 +393,10 @@ static MassVariant* lookup_mass(int D, int tiling) {
     const int stage = wide ? 16384 : 8192;
     if (D == 128) wide ? mass_pick<128, 2>(tiling, v) : mass_pick<128, 1>(tiling, v);
     else mass_pick<64, 2>(tiling, v);
-    v.stages = ring_stages(stage, 2 * stage, "PKV_STAGES_MASS");
+    // Stages of a ring: groups of up to eight heads stream with two (three: 110.8 -> 114.9 us for 64 x
+    // 0.5-4K tokens, 32 heads on 8); larger groups, whose stages take longer to consume, with three
+    // (16 heads 47.7 -> 44.2 us, 32 heads at d = 64 45.0 -> 42.0).
+    v.stages = ring_stages(stage, (tiling == 0 ? 2 : 3) * stage, "PKV_STAGES_MASS");
     v.smem = mass_smem_bytes(v.streams, v.stages, stage);
     if (cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)v.smem) != cudaSuccess) return nullptr;
     int occ = 0;
