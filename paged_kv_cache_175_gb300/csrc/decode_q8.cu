@@ -8,8 +8,8 @@
 // largest is exact in fp16 (and the rest is off by 2^-39 of the largest at most); the power is
 // taken out of the scores again.  p enters as fp16 of 128 p (128: p <= 2^8 by the lazy offset, so
 // 2^15 at most, and the smallest step is 2^-31 of p = 1): as a high + low pair, 22 bits, for fp32
-// outputs and for groups of up to four heads, where the pair is free; rounded once (2^-12 of p at
-// most, against the 2^-9 of the output's own rounding) for bf16 outputs of larger groups, whose
+// outputs and for groups of up to four heads, where the pair is free; rounded once (2^-11 of p at
+// most, against the 2^-8 of the output's own rounding) for bf16 outputs of larger groups, whose
 // kernels are bound by the products: 32 heads on one kv head 54.8 -> 38.1 us, 64 heads 97.8 -> 62.0
 // (64 x 2-8K tokens).  Softmax, sums and outputs are fp32.
 //
@@ -454,7 +454,10 @@ static Q8Variant* lookup_q8(int D, int BS, int G, bool e4m3, bool pair) {
       else pi ? q8_pick<64, false, true>(G, v) : q8_pick<64, false, false>(G, v);
     }
     const int unit = BS == 16 ? 16 : 32, stage = kQ8Rows / unit * q8_record_bytes(unit, D);
-    v.stages = ring_stages(stage, 2 * stage, "PKV_STAGES_Q8");
+    // Stages of a ring: two for groups of up to eight heads at d = 128 (four heads, 64 x 0.5-4K tokens:
+    // 55.0 us, three 56.6; 205 against 212 on long contexts); three where a stage is half as long
+    // (d = 64: 36.3 -> 33.5 us) or takes longer to consume (16 heads: 68.7 -> 64.5 us).
+    v.stages = ring_stages(stage, (D == 128 && G <= 8 ? 2 : 3) * stage, "PKV_STAGES_Q8");
     v.smem = q8_smem_bytes(v.streams, v.stages, stage);
     // one function serves all block sizes, whose rings differ a little: one limit for all
     if (v.smem > kQ8MaxSmem ||

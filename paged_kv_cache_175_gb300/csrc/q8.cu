@@ -15,10 +15,10 @@
 // tokens in long calls and as many tokens as there are places for runs in short ones, where every
 // token tends to be a run.  The runs of a span are found in one round trip; the search for a
 // sequence's end, which few runs need, goes on while the rows arrive.
-// Measured (8 kv heads of 128): 8000 tokens of one prompt in blocks of 16 in 16.6 us (2.9 TB/s), one
-// run at a time 21.7; 23 ragged prompts of 234-701 tokens in blocks of 64 in 24.7 us (2.9 TB/s; the
-// CTAs with two or three runs end last; asking for the next run's rows ahead cost the registers of a
-// CTA per SM and was level); 64 single tokens in 3.1 us.
+// Measured (8 kv heads of 128): 8000 tokens of one prompt in blocks of 16 in 15.1 us (3.3 TB/s), one
+// run at a time 21.7, four CTAs per SM instead of six 17.3; 23 ragged prompts of 234-701 tokens in
+// blocks of 64 in 23.8 us (3.1 TB/s; the CTAs with two or three runs end last; asking for the next
+// run's rows ahead cost the registers of a CTA per SM and was level); 64 single tokens in 3.1 us.
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -90,7 +90,7 @@ struct Q8Shape {
 };
 
 template <int D, int BS, bool E4M3>
-__global__ void __launch_bounds__(256) q8_append_kernel(const Q8AppendArgs a) {
+__global__ void __launch_bounds__(256, 6) q8_append_kernel(const Q8AppendArgs a) {
   using S = Q8Shape<D, BS>;
   constexpr int NT = S::NT, GROUPS = S::GROUPS, GT = S::GT, NV = S::NV, WIN = S::WIN, WORDS = (WIN + 31) / 32;
   constexpr int ROW = D + 8;                                  // padded row: the gathers below spread over the banks
