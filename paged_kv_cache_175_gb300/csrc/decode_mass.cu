@@ -20,9 +20,9 @@
 #include <cstdlib>
 #include <mutex>
 
-#include "decode_mass.cuh"
 #include "nvtx_range.h"
 #include "piece_streams.cuh"
+#include "stream_plan.cuh"
 
 namespace pkv {
 
@@ -505,12 +505,12 @@ extern "C" pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_po
   MassArgs ma = {reinterpret_cast<float*>(ws + ml.scores), reinterpret_cast<float2*>(ws + ml.fin)};
   int sub = block_size == 16 ? 0 : (block_size == 32 ? 1 : 2);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = a.inline_plan ? cudaSuccess : launch_plan(context_lens, batch, (int)max_ctx, 16, a, v->P, st);
+  cudaError_t e = a.inline_plan ? cudaSuccess : launch_plan_streams(context_lens, batch, (int)max_ctx, 16, a, v->P, st);
   if (e == cudaSuccess) {
     void* kargs[] = {&tmk, &tmv, &a, &ma, &sub};
     e = launch_pdl(v->fn, dim3(v->P / v->streams), dim3(v->warps * 32), v->smem, st, kargs);
   }
-  if (e == cudaSuccess) e = launch_reduce_fin(head_dim, a, v->P, ma.fin, st);
+  if (e == cudaSuccess) e = launch_reduce_streams(head_dim, a, v->P, ma.fin, st);
   if (e == cudaSuccess && chunks > 0) {
     const float* scores = ma.scores;
     const float2* fin = ma.fin;

@@ -8,7 +8,7 @@
 #include <cstdlib>
 #include <mutex>
 
-#include "decode_mass.cuh"
+#include "stream_plan.cuh"
 
 namespace pkv {
 
@@ -84,7 +84,7 @@ cudaError_t launch_pdl(const void* func, dim3 grid, dim3 block, size_t smem, cud
 constexpr int kPlanSeqs = 8192;
 
 __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ ctx, int batch, int max_ctx,
-                                                    int block_size, int window, int n_kv, int P,
+                                                    int block_size, int window, int n_kv, int P, bool streams,
                                                     int32_t* __restrict__ cum,
                                                     int32_t* __restrict__ ctx_eff, int4* __restrict__ pieces,
                                                     int32_t* err) {
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
   __syncthreads();
   const int* cu = in_smem ? scum : cum;
   const long long W = (long long)n_kv * carry;
-  const int Pe = effective_pieces(W, P);
+  const int Pe = pieces_of(W, (long long)batch * n_kv, P, streams);
   for (int p = threadIdx.x; p < Pe; p += blockDim.x) {
     const long long pstart = W * p / Pe;
     if (pstart >= W) continue;                                // W == 0: nothing to start
@@ -157,12 +157,20 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
   }
 }
 
-cudaError_t launch_plan(const int32_t* context_lens, int batch, int max_ctx, int block_size,
-                        const DecodeArgs& a, int P, cudaStream_t stream) {
-  plan_kernel<<<1, 1024, 0, stream>>>(context_lens, batch, max_ctx, block_size, a.window, a.n_kv, P,
+static cudaError_t plan(const int32_t* context_lens, int batch, int max_ctx, int block_size, const DecodeArgs& a, int P,
+                        bool streams, cudaStream_t stream) {
+  plan_kernel<<<1, 1024, 0, stream>>>(context_lens, batch, max_ctx, block_size, a.window, a.n_kv, P, streams,
                                       const_cast<int32_t*>(a.cum), const_cast<int32_t*>(a.ctx_eff),
                                       const_cast<int4*>(a.pieces), a.err);
   return cudaGetLastError();
+}
+cudaError_t launch_plan(const int32_t* context_lens, int batch, int max_ctx, int block_size,
+                        const DecodeArgs& a, int P, cudaStream_t stream) {
+  return plan(context_lens, batch, max_ctx, block_size, a, P, false, stream);
+}
+cudaError_t launch_plan_streams(const int32_t* context_lens, int batch, int max_ctx, int block_size, const DecodeArgs& a,
+                                int P, cudaStream_t stream) {
+  return plan(context_lens, batch, max_ctx, block_size, a, P, true, stream);
 }
 
 // ---- reduce: merge the partial softmax states of segments split across pieces ----------------
@@ -253,7 +261,7 @@ __device__ __forceinline__ void merge_pieces(const DecodeArgs& a, long long seg,
 constexpr int kWideReducePieces = 16;
 
 template <int D, bool WIDE, int LPR>
-__global__ void __launch_bounds__(256, LPR == 16 ? 4 : 0) reduce_kernel(const DecodeArgs a, float2* fin) {
+__global__ void __launch_bounds__(256, LPR == 16 ? 4 : 0) reduce_kernel(const DecodeArgs a, float2* fin, const bool streams) {
   constexpr int V = D / LPR;                                  // channels per lane
   constexpr int RPC = 256 / LPR;                              // rows per CTA (narrow)
   static_assert(kInlinePlanSeqs == 8 * 32, "one sequence per thread of the CTA");
@@ -304,15 +312,15 @@ __global__ void __launch_bounds__(256, LPR == 16 ? 4 : 0) reduce_kernel(const De
   int p0 = 0, p1 = 0;
   if (nb > 0) {
     const long long W = (long long)a.n_kv * total;
-    const int P = effective_pieces(W, a.P_launch);
+    const int P = pieces_of(W, (long long)a.batch * a.n_kv, a.P_launch, streams);
     const long long start = (long long)a.n_kv * before + (long long)g * nb;
     p0 = piece_of(start, W, P);
     p1 = piece_of(start + nb - 1, W, P);
   }
   grid_dep_wait();
   if (nb > 0 && p0 == p1) return;                             // finished by the attention kernel
-  // Every piece from p0 to p1 holds part of the segment (pieces hold at least 8 positions,
-  // so none is empty) and wrote a state.
+  // Every piece from p0 to p1 holds part of the segment (pieces hold at least one
+  // position, so none is empty) and wrote a state.
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
@@ -391,11 +399,7 @@ static int reduce_wave() {
   return occ * device_sm_count();
 }
 
-cudaError_t launch_reduce(int head_dim, const DecodeArgs& a, int P, cudaStream_t stream) {
-  return launch_reduce_fin(head_dim, a, P, nullptr, stream);
-}
-
-cudaError_t launch_reduce_fin(int head_dim, const DecodeArgs& a, int P, float2* fin, cudaStream_t stream) {
+static cudaError_t reduce(int head_dim, const DecodeArgs& a, int P, float2* fin, bool streams, cudaStream_t stream) {
   const int rows = a.batch * a.n_h;
   if (rows == 0) return cudaSuccess;
   // the grid's pieces over the segments: about the average a segment spans
@@ -407,7 +411,7 @@ cudaError_t launch_reduce_fin(int head_dim, const DecodeArgs& a, int P, float2* 
   const bool half = !wide && wave > 0 && (rows + 7) / 8 > wave;
   dim3 grid(wide ? rows : (half ? (rows + 15) / 16 : (rows + 7) / 8)), block(256);
   DecodeArgs args = a;
-  void* kargs[] = {&args, &fin};
+  void* kargs[] = {&args, &fin, &streams};
   const void* fn;
   if (head_dim == 128)
     fn = wide ? (const void*)reduce_kernel<128, true, 32>
@@ -416,6 +420,13 @@ cudaError_t launch_reduce_fin(int head_dim, const DecodeArgs& a, int P, float2* 
     fn = wide ? (const void*)reduce_kernel<64, true, 32>
               : (half ? (const void*)reduce_kernel<64, false, 16> : (const void*)reduce_kernel<64, false, 32>);
   return launch_pdl(fn, grid, block, 0, stream, kargs);
+}
+
+cudaError_t launch_reduce(int head_dim, const DecodeArgs& a, int P, cudaStream_t stream) {
+  return reduce(head_dim, a, P, nullptr, false, stream);
+}
+cudaError_t launch_reduce_streams(int head_dim, const DecodeArgs& a, int P, float2* fin, cudaStream_t stream) {
+  return reduce(head_dim, a, P, fin, true, stream);
 }
 
 // Self-test of the bounded wait every ring uses: one thread initialises an mbarrier for

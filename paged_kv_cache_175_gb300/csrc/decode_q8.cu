@@ -27,6 +27,7 @@
 #include "nvtx_range.h"
 #include "piece_streams.cuh"
 #include "q8_common.cuh"
+#include "stream_plan.cuh"
 
 namespace pkv {
 
@@ -551,12 +552,12 @@ extern "C" pkv_status pkv_paged_decode_attn_q8(const void* q, const uint8_t* cac
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int sub = block_size == 64 ? 1 : 0;
   cudaError_t e = a.inline_plan ? cudaSuccess
-                                : launch_plan(context_lens, batch, max_blocks * block_size, unit, a, v->P, st);
+                                : launch_plan_streams(context_lens, batch, max_blocks * block_size, unit, a, v->P, st);
   if (e == cudaSuccess) {
     void* kargs[] = {&a, &sub};
     e = launch_pdl(v->fn, dim3(v->P / v->streams), dim3(v->warps * 32), v->smem, st, kargs);
   }
-  if (e == cudaSuccess) e = launch_reduce(head_dim, a, v->P, st);
+  if (e == cudaSuccess) e = launch_reduce_streams(head_dim, a, v->P, nullptr, st);
   if (e != cudaSuccess) {
     record_cuda_error(e);
     return PKV_ECUDA;

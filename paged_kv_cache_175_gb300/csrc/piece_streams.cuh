@@ -13,6 +13,7 @@
 #pragma once
 
 #include "decode_common.cuh"
+#include "stream_plan.cuh"
 
 namespace pkv {
 
@@ -36,16 +37,70 @@ struct StreamStart {
   int len;                       // units of the stream's piece (0: none)
 };
 
-// Called by one whole warp per stream.
+// The piece of one stream and its first cursor, called by one whole warp per stream: from the plan
+// kernel's tables, or (up to kInlinePlanSeqs sequences) from the context lengths, 32 at a time with all
+// loads issued before any is used.
 __device__ __forceinline__ void stream_setup(const DecodeArgs& a, int piece, int pieces, StreamStart* out) {
+  constexpr int MAXC = kInlinePlanSeqs / 32;
+  const int lane = threadIdx.x & 31, chunks = a.inline_plan ? (a.batch + 31) / 32 : 0;
+  int ctx[MAXC], incl[MAXC];                                   // units of a chunk's sequences, prefix sums
+#pragma unroll
+  for (int c = 0; c < MAXC; ++c) {
+    const int s = c * 32 + lane;
+    ctx[c] = c < chunks && s < a.batch ? a.ctx_raw[s] : 0;
+  }
+  bool bad = false;
+  long long units = 0;
+#pragma unroll
+  for (int c = 0; c < MAXC; ++c) {
+    if (c >= chunks) continue;
+    bad |= ctx[c] < 0 || ctx[c] > a.max_ctx;
+    ctx[c] = clamp_ctx(ctx[c], a.max_ctx);
+    incl[c] = span_blocks(ctx[c], a.window, a.block_size);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(FULL_MASK, incl[c], o);
+      if (lane >= o) incl[c] += y;
+    }
+    units += __shfl_sync(FULL_MASK, incl[c], 31);
+  }
+  if (__any_sync(FULL_MASK, bad) && lane == 0 && blockIdx.x == 0 && threadIdx.x == 0) set_err(a.err, PKV_DEV_BAD_CTX);
+  const long long W = (long long)a.n_kv * (a.inline_plan ? units : a.cum[a.batch]);
+  const int P = stream_pieces(W, (long long)a.batch * a.n_kv, pieces);
   Cursor cur = {};
-  PieceInfo pi = {};
-  piece_setup(a, piece, pieces, true, cur, pi);
-  const int len = piece < pi.P ? (int)(pi.pend - pi.pstart) : 0;
-  if ((threadIdx.x & 31) == 0) {
+  const long long pstart = W * piece / P, pend = W * (piece + 1) / P;
+  const int len = piece < P ? (int)(pend - pstart) : 0;
+  if (len > 0 && !a.inline_plan) {
+    cursor_from_table(cur, piece, pstart, a);
+  } else if (len > 0) {
+    long long before = 0;                                      // units of earlier chunks
+    bool found = false;
+#pragma unroll
+    for (int c = 0; c < MAXC; ++c) {
+      if (c >= chunks || found) continue;
+      const int nb = span_blocks(ctx[c], a.window, a.block_size);
+      const long long lo = (long long)a.n_kv * (before + incl[c] - nb);
+      const unsigned hit = __ballot_sync(FULL_MASK, lo <= pstart && pstart < lo + (long long)a.n_kv * nb);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        cur.s = c * 32 + src;
+        cur.nb = __shfl_sync(FULL_MASK, nb, src);
+        cur.ctx = __shfl_sync(FULL_MASK, ctx[c], src);
+        cur.b0 = window_first_block(cur.ctx, a.window, a.block_size);
+        const long long off = pstart - __shfl_sync(FULL_MASK, lo, src);
+        cur.g = (int)(off / cur.nb);
+        cur.blk = (int)(off % cur.nb);
+        cur.seg_start = pstart - cur.blk;
+        found = true;
+        continue;
+      }
+      before += __shfl_sync(FULL_MASK, incl[c], 31);
+    }
+  }
+  if (lane == 0) {
     out->cur = cur;
-    out->pstart = pi.pstart;
-    out->pend = pi.pend;
+    out->pstart = pstart;
+    out->pend = pend;
     out->len = len;
   }
 }

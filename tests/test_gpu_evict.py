@@ -87,6 +87,21 @@ def test_mass_long_and_many(n_h, n_kv, lens):
     check_mass(f64(masses[0]), ev.attention_mass(f64(q), f64(kp), bt, lens, scale, 32, T), np.zeros(masses[0].shape), q, kp, scale, lens)
 
 
+# as many units of 16 tokens per segment as change the least length of a piece; and more sequences than
+# one CTA plans for
+@pytest.mark.parametrize("lens", [[1008, 1024], [2032, 2048], [4080, 4096, 4096], [(7 * i) % 41 for i in range(300)]],
+                         ids=["64", "128", "256", "300 sequences"])
+def test_mass_piece_lengths(lens):
+    kp, vp, bt, g = pools(lens, 2, 64, 16, seed=len(lens))
+    q = torch.randn(len(lens), 8, 64, generator=g).to(torch.bfloat16)
+    T = bt.shape[1] * 16
+    mass = torch.rand(len(lens), 2, T, generator=g)
+    dm, dq, dk, dv = mass.to(DEV), q.to(DEV), kp.to(DEV), vp.to(DEV)
+    out = run_mass(dq, dk, dv, bt, lens, 0.125, dm)
+    check_attention(out, oracle.paged_decode_attention(f64(q), f64(kp), f64(vp), bt, lens, 0.125, 16), "mass fp32")
+    check_mass(f64(dm), ev.attention_mass(f64(q), f64(kp), bt, lens, 0.125, 16, T), f64(mass), q, kp, 0.125, lens)
+
+
 def test_mass_stale_rows_bad_blocks_and_lengths():
     lens = [100, 64, 30, 50]
     kp, vp, bt, g = pools(lens, 2, 64, 16, seed=4)

@@ -300,6 +300,24 @@ def test_long_and_many(n_h, n_kv, lens):
     assert torch.equal(a, attend(q, cache, bt, lens, scale))
 
 
+# contexts around 64, 128 and 256 units (of 16 or 32 tokens) per segment, where the least length of a
+# piece changes, and more sequences than one CTA plans for
+@pytest.mark.parametrize("bs,unit", [(16, 16), (32, 32), (64, 32)])
+@pytest.mark.parametrize("units", [63, 64, 127, 128, 255, 256])
+def test_piece_lengths(bs, unit, units):
+    lens = [units * unit, units * unit - unit + 1]
+    cache, held, bt, q = build(lens, 4, 2, 64, bs, "e4m3", seed=units + bs)
+    ref = oracle.paged_decode_attention(f64(q), *held, bt, lens, 0.125, bs)
+    check_attention(attend(q, cache, bt, lens, 0.125), ref, "fp32")
+
+
+def test_more_sequences_than_one_cta_plans():
+    lens = [(7 * i) % 41 for i in range(300)]
+    cache, held, bt, q = build(lens, 4, 2, 64, 16, "int8", seed=300)
+    ref = oracle.paged_decode_attention(f64(q), *held, bt, lens, 0.125, 16)
+    check_attention(attend(q, cache, bt, lens, 0.125), ref, "fp32")
+
+
 def test_append_and_attend_in_a_graph_and_on_a_side_stream():
     lens = [33, 100, 5, 64]
     cache, _, bt, q = build(lens, 8, 2, 64, 16, "e4m3", seed=12)
