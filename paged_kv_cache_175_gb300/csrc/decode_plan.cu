@@ -260,8 +260,10 @@ __device__ __forceinline__ void merge_pieces(const DecodeArgs& a, long long seg,
 // Wide reduce when the grid's pieces per segment reach this many (two chunks of the CTA).
 constexpr int kWideReducePieces = 16;
 
-template <int D, bool WIDE, int LPR>
-__global__ void __launch_bounds__(256, LPR == 16 ? 4 : 0) reduce_kernel(const DecodeArgs a, float2* fin, const bool streams) {
+// STREAMS: behind the attention kernels with streams (their pieces; fin, see stream_plan.cuh), a variant of
+// its own so that the others keep their code.
+template <int D, bool WIDE, int LPR, bool STREAMS>
+__global__ void __launch_bounds__(256, LPR == 16 ? 4 : 0) reduce_kernel(const DecodeArgs a, float2* fin) {
   constexpr int V = D / LPR;                                  // channels per lane
   constexpr int RPC = 256 / LPR;                              // rows per CTA (narrow)
   static_assert(kInlinePlanSeqs == 8 * 32, "one sequence per thread of the CTA");
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(256, LPR == 16 ? 4 : 0) reduce_kernel(const De
   int p0 = 0, p1 = 0;
   if (nb > 0) {
     const long long W = (long long)a.n_kv * total;
-    const int P = pieces_of(W, (long long)a.batch * a.n_kv, a.P_launch, streams);
+    const int P = pieces_of(W, (long long)a.batch * a.n_kv, a.P_launch, STREAMS);
     const long long start = (long long)a.n_kv * before + (long long)g * nb;
     p0 = piece_of(start, W, P);
     p1 = piece_of(start + nb - 1, W, P);
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(256, LPR == 16 ? 4 : 0) reduce_kernel(const De
       o0 *= inv;
       o1 *= inv;
     }
-    if (fin && t == 0) fin[row] = make_float2(Mt, inv);
+    if (STREAMS && fin && t == 0) fin[row] = make_float2(Mt, inv);
     const size_t o = (size_t)row * D + 2 * t;
     if (a.out_f32) {
       *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + o) = make_float2(o0, o1);
@@ -372,7 +374,7 @@ __global__ void __launch_bounds__(256, LPR == 16 ? 4 : 0) reduce_kernel(const De
       constexpr int CH = kMergeChunk * LPR / 32;
       merge_pieces<D, LPR>(a, seg, hl, sub, p0, p1, CH, M, L, acc);
       const float inv = L > 0.f ? 1.f / L : 0.f;
-      if (fin && sub == 0) fin[row] = make_float2(M == -INFINITY ? 0.f : M, inv);
+      if (STREAMS && fin && sub == 0) fin[row] = make_float2(M == -INFINITY ? 0.f : M, inv);
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] *= inv;
     }
@@ -392,11 +394,17 @@ __global__ void __launch_bounds__(256, LPR == 16 ? 4 : 0) reduce_kernel(const De
 // CTAs of the warp-per-row reduce resident at once on the device (0 if the query failed).
 static int reduce_wave() {
   int occ = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, reduce_kernel<128, false, 32>, 256, 0) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, reduce_kernel<128, false, 32, false>, 256, 0) != cudaSuccess) {
     (void)cudaGetLastError();
     return 0;
   }
   return occ * device_sm_count();
+}
+
+template <int D, bool STREAMS>
+static const void* reduce_fn(bool wide, bool half) {
+  return wide ? (const void*)reduce_kernel<D, true, 32, STREAMS>
+              : (half ? (const void*)reduce_kernel<D, false, 16, STREAMS> : (const void*)reduce_kernel<D, false, 32, STREAMS>);
 }
 
 static cudaError_t reduce(int head_dim, const DecodeArgs& a, int P, float2* fin, bool streams, cudaStream_t stream) {
@@ -411,14 +419,10 @@ static cudaError_t reduce(int head_dim, const DecodeArgs& a, int P, float2* fin,
   const bool half = !wide && wave > 0 && (rows + 7) / 8 > wave;
   dim3 grid(wide ? rows : (half ? (rows + 15) / 16 : (rows + 7) / 8)), block(256);
   DecodeArgs args = a;
-  void* kargs[] = {&args, &fin, &streams};
+  void* kargs[] = {&args, &fin};
   const void* fn;
-  if (head_dim == 128)
-    fn = wide ? (const void*)reduce_kernel<128, true, 32>
-              : (half ? (const void*)reduce_kernel<128, false, 16> : (const void*)reduce_kernel<128, false, 32>);
-  else
-    fn = wide ? (const void*)reduce_kernel<64, true, 32>
-              : (half ? (const void*)reduce_kernel<64, false, 16> : (const void*)reduce_kernel<64, false, 32>);
+  if (head_dim == 128) fn = streams ? reduce_fn<128, true>(wide, half) : reduce_fn<128, false>(wide, half);
+  else fn = streams ? reduce_fn<64, true>(wide, half) : reduce_fn<64, false>(wide, half);
   return launch_pdl(fn, grid, block, 0, stream, kargs);
 }
 
