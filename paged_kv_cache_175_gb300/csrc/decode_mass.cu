@@ -107,6 +107,20 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32, MT == 4 && NH == 1 ? 3 : (
   const bool even = (a.G & 1) == 0;
   int slot = 0;
   uint32_t phase = 0;
+  auto load_q = [&](size_t qrow0) {
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+      const int hl = hw0 + nh * 8 + gid;                       // B-fragment column n = gid
+      const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q) + (qrow0 + hl) * (D / 2);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) qb[ks][nh][r] = hl < a.G ? __ldg(qp + ks * 8 + 4 * r + tig) : 0u;
+    }
+  };
+  // the first segment's queries, while its first stage is on the way
+  bool have_q = true;
+  load_q((size_t)starts[w].cur.s * a.n_h + (size_t)starts[w].cur.g * a.G);
   for (;;) {
     if (!mbar_wait(&full[slot], phase) || abort_flag) {
       set_err(a.err, PKV_DEV_TIMEOUT);
@@ -120,16 +134,10 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32, MT == 4 && NH == 1 ? 3 : (
     float* sp = ms.scores + (((size_t)s * a.n_kv + g) * a.max_ctx + (size_t)mt.z * BS) * a.G + hw0 + 2 * tig;
 
     if (flags & F_FIRST) {
+      if (!have_q) load_q(qrow0);
+      have_q = false;
 #pragma unroll
       for (int nh = 0; nh < NH; ++nh) {
-        const int hl = hw0 + nh * 8 + gid;                     // B-fragment column n = gid
-        const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q) + (qrow0 + hl) * (D / 2);
-        const bool ok = hl < a.G;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          qb[ks][nh][0] = ok ? __ldg(qp + ks * 8 + tig) : 0u;
-          qb[ks][nh][1] = ok ? __ldg(qp + ks * 8 + 4 + tig) : 0u;
-        }
         m[nh][0] = m[nh][1] = -INFINITY;
         l[nh][0] = l[nh][1] = 0.f;
 #pragma unroll

@@ -153,6 +153,20 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32, NH == 2 ? 2 : 4) decode_q8
   const int hw0 = warp % MT * HW;
   int slot = 0;
   uint32_t phase = 0;
+  auto load_q = [&](size_t qrow0) {
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+      const int hl = COMB ? gid & 3 : hw0 + nh * 8 + gid;      // B-fragment column n = gid
+      const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q) + (qrow0 + hl) * (D / 2);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) qb[ks][nh][r] = hl < a.G ? __ldg(qp + ks * 8 + 4 * r + tig) : 0u;
+    }
+  };
+  // the first segment's queries, while its first stage is on the way
+  bool have_q = true;
+  load_q((size_t)starts[w].cur.s * a.n_h + (size_t)starts[w].cur.g * a.G);
   for (;;) {
     if (!mbar_wait(&full[slot], phase) || abort_flag) {
       set_err(a.err, PKV_DEV_TIMEOUT);
@@ -164,17 +178,16 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32, NH == 2 ? 2 : 4) decode_q8
     const size_t qrow0 = (size_t)s * a.n_h + (size_t)g * a.G;
 
     if (flags & F_FIRST) {
+      if (!have_q) load_q(qrow0);
+      have_q = false;
 #pragma unroll
       for (int nh = 0; nh < NH; ++nh) {
-        const int hl = COMB ? gid & 3 : hw0 + nh * 8 + gid;    // B-fragment column n = gid
-        const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q) + (qrow0 + hl) * (D / 2);
         float big = 0.f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const uint32_t x = hl < a.G ? __ldg(qp + ks * 8 + 4 * r + tig) : 0u;
-            qb[ks][nh][r] = x;
+            const uint32_t x = qb[ks][nh][r];
             big = fmaxf(big, fmaxf(fabsf(bf16_lo(x)), fabsf(bf16_hi(x))));
           }
         big = fmaxf(big, __shfl_xor_sync(FULL_MASK, big, 1));
