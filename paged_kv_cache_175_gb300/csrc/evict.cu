@@ -280,9 +280,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const Evict
       mask |= (uint32_t)(bins - 1) << shift;
       want = rest;
       all_equal = rest == size;
+      // the bin is kept as a whole: its lowest key, the prefix, divides the rows as the K-th would
+      // (among a few thousand accounts 22 bits nearly always suffice)
+      if (all_equal) break;
     }
   }
-  // prefix is the K-th largest key; of the rows equal to it the `want` lowest are kept
+  // prefix is the K-th largest key, of the rows equal to it the `want` lowest are kept; or (all_equal)
+  // exactly the rows with keys from prefix on are
 
   // ---- ordered scans ----
   auto widen = [](Pair v) { return (uint64_t)(v >> kHalf) << 32 | (uint32_t)(v & (((Pair)1 << kHalf) - 1)); };
