@@ -92,6 +92,7 @@ template <> struct PairOf<false> { using type = unsigned long long; };
 // CLUSTER: several CTAs may share a (sequence, kv head).
 template <int NT, int R, bool CLUSTER>
 __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const EvictArgs a) {
+  grid_dep_wait();                         // launched while the kernel before may still run
   grid_dep_launch();                       // the move kernel's launch overlaps; it waits for this grid
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = CLUSTER ? (int)cluster.block_rank() : 0, ranks = CLUSTER ? (int)cluster.num_blocks() : 1;
@@ -554,13 +555,15 @@ extern "C" pkv_status pkv_kv_evict(void* k_pool, void* v_pool, const int32_t* bl
   cfg.gridDim = dim3((unsigned)(pairs * ranks));
   cfg.blockDim = dim3(threads);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ranks;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   void* sargs[] = {&a};
   cudaError_t e = cudaLaunchKernelExC(&cfg, fn, sargs);
   if (e == cudaSuccess) {

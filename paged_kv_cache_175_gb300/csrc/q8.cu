@@ -110,6 +110,8 @@ __global__ void __launch_bounds__(256, 6) q8_append_kernel(const Q8AppendArgs a)
   __nv_bfloat16* tails = values ? a.v_tail : a.k_tail;
   __nv_bfloat16* rows = rows_s + group * BS * ROW;
   const int i0 = blockIdx.x * a.span;
+  grid_dep_wait();                         // launched while the kernel before may still run
+  grid_dep_launch();
   if (tid < WORDS * 32) {
     const int i = i0 + tid;
     const bool in = i < a.n_tok && tid < a.span + BS && tid < WIN;
@@ -280,9 +282,9 @@ template <int D, int BS>
 static cudaError_t launch_q8(const Q8AppendArgs& a, bool e4m3, cudaStream_t st) {
   const unsigned gx = (unsigned)((a.n_tok + a.span - 1) / a.span);
   const dim3 grid(gx, (unsigned)a.n_kv, 2), block(256);
-  if (e4m3) q8_append_kernel<D, BS, true><<<grid, block, 0, st>>>(a);
-  else q8_append_kernel<D, BS, false><<<grid, block, 0, st>>>(a);
-  return cudaGetLastError();
+  void* kargs[] = {const_cast<Q8AppendArgs*>(&a)};
+  return launch_pdl(e4m3 ? (const void*)q8_append_kernel<D, BS, true> : (const void*)q8_append_kernel<D, BS, false>, grid, block, 0, st,
+                    kargs);
 }
 
 static bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -52,6 +52,9 @@ template <int D, int NI, bool APPEND>
 __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int VP = D / 16;                                  // items per row
   extern __shared__ float2 angles[];                         // [tokens][rotary_dim / 2]: cos, sin; then [tokens] slots
+  // Launched while the kernel before may still run; nothing is read or written before the wait, and the
+  // next kernel is let in only behind it (so its setup, too, finds that kernel's results).
+  grid_dep_wait();
   grid_dep_launch();                       // the attention's setup may overlap this kernel
   const int H = a.t.rotary_dim >> 1, RP = a.t.rotary_dim >> 4;
   const bool inter = a.t.interleaved != 0;
@@ -168,9 +171,9 @@ static cudaError_t launch_rope(const RopeArgs& a, int head_dim, cudaStream_t st)
   int tokens = (NI * kRopeThreads - 1) / a.items_per_tok + 2;
   if (tokens > a.n_tok) tokens = a.n_tok;
   const size_t smem = (size_t)tokens * (a.t.rotary_dim / 2 * sizeof(float2) + sizeof(int64_t));
-  if (head_dim == 128) rope_append_kernel<128, NI, APPEND><<<(unsigned)grid, kRopeThreads, smem, st>>>(a);
-  else rope_append_kernel<64, NI, APPEND><<<(unsigned)grid, kRopeThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  void* kargs[] = {const_cast<RopeArgs*>(&a)};
+  return launch_pdl(head_dim == 128 ? (const void*)rope_append_kernel<128, NI, APPEND> : (const void*)rope_append_kernel<64, NI, APPEND>,
+                    dim3((unsigned)grid), dim3(kRopeThreads), smem, st, kargs);
 }
 
 template <bool APPEND>
