@@ -443,6 +443,7 @@ pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_pool, const v
  * Entries of mass_out behind n, and of positions_out behind the new kept, are left as they were.
  *   new_lens   int32 [batch]: min(n, K); must not overlap context_lens, keep, kept or dropped
  *   workspace  pkv_evict_workspace_bytes bytes, 256-byte aligned
+ * max_blocks * block_size is at most 0x7fff0000 (PKV_ERANGE).
  * The blocks that hold the first K rows are rewritten: they must belong to the sequence alone
  * (see pkv_bm_evict).  Moves from or to a block id outside the pool set PKV_DEV_BAD_BLOCK and are
  * skipped; context lengths out of range are clamped with PKV_DEV_BAD_CTX.

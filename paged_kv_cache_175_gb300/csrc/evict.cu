@@ -52,6 +52,7 @@ struct EvictArgs {
 
 constexpr int kEvBins = 2048;
 constexpr int kEvRows = 16;                                   // rows per thread
+constexpr long long kEvMaxRows = 0x7fff0000;                  // row numbers plus a grid's threads stay in 32 bits
 
 // Order-keeping bits of an account: -0 below +0, NaN above everything but the recent rows.
 __device__ __forceinline__ uint32_t order_bits(float x) {
@@ -474,7 +475,7 @@ using namespace pkv;
 
 extern "C" size_t pkv_evict_workspace_bytes(int batch, int n_kv, int block_size, int max_blocks) {
   if (batch < 0 || n_kv <= 0 || max_blocks < 0 || (block_size != 16 && block_size != 32 && block_size != 64)) return 0;
-  if ((long long)max_blocks * block_size > 0x7fffffffLL) return 0;
+  if ((long long)max_blocks * block_size > kEvMaxRows) return 0;
   const size_t n = evict_layout(batch, n_kv, (long long)max_blocks * block_size).total;
   return n ? n : 256;
 }
@@ -504,7 +505,7 @@ extern "C" pkv_status pkv_kv_evict(void* k_pool, void* v_pool, const int32_t* bl
   if (in_place != (positions_out == positions) || in_place != (kept_out == kept) || in_place != (dropped_out == dropped))
     return PKV_EINVAL;
   const long long max_ctx = (long long)max_blocks * block_size;
-  if (max_ctx > 0x7fffffffLL) return PKV_ERANGE;
+  if (max_ctx > kEvMaxRows) return PKV_ERANGE;
   if (stride < max_ctx) return PKV_EINVAL;
   if ((long long)batch * n_kv > 0x7fffffffLL / 64) return PKV_ERANGE;
   const EvictLayout w = evict_layout(batch, n_kv, max_ctx);

@@ -256,5 +256,6 @@ def test_c_entries_refuse_bad_arguments():
     for bad in (dict(nl=p), dict(mo=p + 512), dict(st=31), dict(rec=-1), dict(d=32), dict(bs=48), dict(ws=p + 16), dict(nl=None)):
         assert ev_(**bad) == -1, bad
     assert ev_(wb=16) == -4
+    assert ev_(mb=0x7fff001, st=0x7fff0010) == -2 and L.pkv_evict_workspace_bytes(1, 1, 16, 0x7fff001) == 0
     assert L.pkv_evict_workspace_bytes(2, 3, 16, 10) > 0 and L.pkv_evict_workspace_bytes(2, 3, 24, 10) == 0
     assert L.pkv_q8_workspace_bytes(1, 6, 4, 64, 16, 0) == 0 and L.pkv_mass_workspace_bytes(1, 65, 1, 64, 16, 4) == 0
