@@ -398,7 +398,7 @@ pkv_status pkv_kv_quant_append_q8(const void* k, int64_t k_stride, const void* v
  * 2^-11 sum p |v|, under the output's own rounding wherever its terms do not cancel).
  * window as for pkv_paged_decode_attn_window (0: the whole context).  Other arguments, output and
  * errors as for pkv_paged_decode_attn; workspace of pkv_q8_workspace_bytes (0: invalid shape).
- * The tails are not read.
+ * The tails are not read; max_blocks * block_size is at most 0x7fff0000 (PKV_ERANGE).
  */
 size_t pkv_q8_workspace_bytes(int batch, int n_h, int n_kv, int head_dim, int block_size, int format);
 pkv_status pkv_paged_decode_attn_q8(const void* q, const uint8_t* cache, int format, const int32_t* block_tables,
@@ -416,7 +416,8 @@ pkv_status pkv_paged_decode_attn_q8(const void* q, const uint8_t* cache, int for
  *   mass          fp32, mass_stride >= max_blocks * block_size
  *   workspace     pkv_mass_workspace_bytes bytes (it holds the step's scores: 4 n_h bytes per
  *                 token of max_blocks * block_size; 0: invalid shape), 256-byte aligned
- * Tokens of a bad block weigh nothing.  Other arguments and errors as for pkv_paged_decode_attn.
+ * Tokens of a bad block weigh nothing; max_blocks * block_size is at most 0x7fff0000 (PKV_ERANGE).
+ * Other arguments and errors as for pkv_paged_decode_attn.
  */
 size_t pkv_mass_workspace_bytes(int batch, int n_h, int n_kv, int head_dim, int block_size, int max_blocks);
 pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_pool, const void* v_pool,

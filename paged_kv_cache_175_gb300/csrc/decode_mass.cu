@@ -444,7 +444,7 @@ using namespace pkv;
 
 extern "C" size_t pkv_mass_workspace_bytes(int batch, int n_h, int n_kv, int head_dim, int block_size, int max_blocks) {
   if (batch < 0 || max_blocks < 0 || !valid_shape(n_h, n_kv, head_dim, block_size)) return 0;
-  if ((long long)max_blocks * block_size > 0x7fffffffLL) return 0;
+  if ((long long)max_blocks * block_size > kStreamMaxCtx) return 0;
   MassVariant* v = lookup_mass(head_dim, head_tiling(n_h / n_kv));
   return v ? mass_layout(batch, n_h, n_kv, head_dim, (long long)max_blocks * block_size, v->P).total : 0;
 }
@@ -463,7 +463,7 @@ extern "C" pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_po
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return PKV_EINVAL;
   const long long max_ctx = (long long)max_blocks * block_size;
-  if (max_ctx > 0x7fffffffLL) return PKV_ERANGE;
+  if (max_ctx > kStreamMaxCtx) return PKV_ERANGE;
   if (mass_stride < max_ctx) return PKV_EINVAL;
   const int G = n_h / n_kv;
   const MassAdd add = mass_add(G);

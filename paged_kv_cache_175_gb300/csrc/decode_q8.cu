@@ -525,7 +525,7 @@ extern "C" pkv_status pkv_paged_decode_attn_q8(const void* q, const uint8_t* cac
   if (batch == 0) return PKV_OK;
   if (!q || !cache || !block_tables || !context_lens || !out || !workspace) return PKV_EINVAL;
   if (!al16(q) || !al16(cache) || !al16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PKV_EINVAL;
-  if ((long long)max_blocks * block_size > 0x7fffffffLL) return PKV_ERANGE;
+  if ((long long)max_blocks * block_size > kStreamMaxCtx) return PKV_ERANGE;
   const int G = n_h / n_kv;
   Q8Variant* v = lookup_q8(head_dim, block_size, G, format == PKV_Q8_E4M3, out_dtype == PKV_OUT_F32);
   if (!v) {

@@ -17,6 +17,8 @@
 
 namespace pkv {
 
+constexpr long long kStreamMaxCtx = 0x7fff0000;               // tokens of a table: token numbers stay in 32 bits
+
 // Whether the barrier's phase of this parity is over; does not suspend the thread, so a lane whose
 // ring is full does not hold up the others.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {

@@ -257,5 +257,16 @@ def test_c_entries_refuse_bad_arguments():
         assert ev_(**bad) == -1, bad
     assert ev_(wb=16) == -4
     assert ev_(mb=0x7fff001, st=0x7fff0010) == -2 and L.pkv_evict_workspace_bytes(1, 1, 16, 0x7fff001) == 0
+    att = lambda **k: L.pkv_paged_decode_attn_q8(*[{**dict(q=p, c=p, f=0, bt=p, mb=2, ctx=p, sc=1.0, w=0, b=1, nh=2, nkv=1, d=64, bs=16, nb=4,
+                                                           o=p, ot=0, ws=p, wb=0, e=None, s=None), **k}[x] for x in
+                                                    "q c f bt mb ctx sc w b nh nkv d bs nb o ot ws wb e s".split()])
+    mas = lambda **k: L.pkv_paged_decode_attn_mass(*[{**dict(q=p, k=p, v=p, bt=p, mb=2, ctx=p, sc=1.0, b=1, nh=2, nkv=1, d=64, bs=16, nb=4,
+                                                             o=p, ot=0, m=p, st=32, ws=p, wb=0, e=None, s=None), **k}[x] for x in
+                                                      "q k v bt mb ctx sc b nh nkv d bs nb o ot m st ws wb e s".split()])
+    assert att(b=0) == mas(b=0) == 0
+    assert att(mb=0x7fff001) == mas(mb=0x7fff001, st=0x7fff0010) == -2 and L.pkv_mass_workspace_bytes(1, 1, 1, 64, 16, 0x7fff001) == 0
+    for bad in (dict(d=96), dict(bs=8), dict(nh=65), dict(q=None), dict(o=p + 2), dict(ot=2), dict(ctx=None)):
+        assert att(**bad) == mas(**bad) == -1, bad
+    assert att(w=-1) == att(f=2) == mas(st=31) == -1
     assert L.pkv_evict_workspace_bytes(2, 3, 16, 10) > 0 and L.pkv_evict_workspace_bytes(2, 3, 24, 10) == 0
     assert L.pkv_q8_workspace_bytes(1, 6, 4, 64, 16, 0) == 0 and L.pkv_mass_workspace_bytes(1, 65, 1, 64, 16, 4) == 0
