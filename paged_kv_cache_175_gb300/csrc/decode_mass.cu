@@ -16,6 +16,9 @@
 // streams of piece_streams.cuh, in units of 16 tokens whatever the block size: a TMA box of 16 rows
 // starts inside a larger block as well.  K and V land in 128-byte swizzled boxes and are read by
 // ldmatrix.
+// Measured: 64 x 0.5-4K tokens, 32 heads on 8 of 128, 109 us (83% of the copy rate; the attention 96,
+// merge and addition in series behind it); 8 x 20-40K tokens, 32 heads on one, 42.2 us (30 the
+// attention, bound by each consumer warp's chain of products and softmax); small calls 8-11 us.
 #include <cmath>
 #include <cstdlib>
 #include <mutex>

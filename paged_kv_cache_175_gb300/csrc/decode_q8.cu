@@ -430,7 +430,7 @@ constexpr size_t kQ8MaxSmem = 200 * 1024;
 
 // Three streams and their producer warp fill an SM's registers at four CTAs of 128 registers: 12
 // consumer warps.  32/8 heads of 128, 64 sequences of 512-4096 tokens in e4m3 / 32 of 8-32K in int8:
-// 55 / 205 us (81% / 96% of the measured copy rate), with four streams 55.3 / 208, with six 56.4 /
+// 54 / 203 us (83% / 97% of the measured copy rate), with four streams 55.3 / 208, with six 56.4 /
 // 218, at three CTAs 55 / 215; a producer warp per consumer warp and 64-token stages (six consumers
 // per SM) took 72.7 / 324.  A third ring stage costs consumers their shared memory: 55.7 / 212.
 // Larger groups: 16 heads per consumer warp (two n-tiles share the converted codes), 32/2 heads 26.3

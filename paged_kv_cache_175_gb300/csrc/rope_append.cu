@@ -181,7 +181,7 @@ static cudaError_t launch_rope_any(const RopeArgs& a, int head_dim, cudaStream_t
   // Three items per thread, five CTAs of them per SM, hide the memory latency of long calls: 16384
   // tokens of 32 + 8 + 8 heads of 128 in 63.0 us (6.4 TB/s, 94% of the measured copy rate); two items
   // 64.5 (six CTAs) and 69.5 (five), four 66.1 (four CTAs).  A call too small to give every SM two
-  // CTAs of those takes one item per thread and three times the CTAs: 64 tokens in 2.5 us.
+  // CTAs of those takes one item per thread and three times the CTAs: 64 tokens in 2.3 us.
   const long long total = (long long)a.n_tok * a.items_per_tok;
   const int sms = device_sm_count() > 0 ? device_sm_count() : 128;
   if (total >= (long long)sms * 2 * kRopeItems * kRopeThreads) return launch_rope<kRopeItems, APPEND>(a, head_dim, st);
