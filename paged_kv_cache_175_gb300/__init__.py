@@ -458,10 +458,9 @@ def _empty(shape, dtype, device, stream):
     return out
 
 
-def _table(table):
+def _table_type(table):
     if type(table) is not RopeTable:
         raise PkvError("the table must come from rope_table")
-    return ctypes.addressof(table)
 
 
 def _out_type(out_dtype):
@@ -473,13 +472,14 @@ def _out_type(out_dtype):
 def rope_append(q, k, v, positions, slot_mapping, table: RopeTable, k_pool, v_pool, q_out=None, err=None, stream=None):
     """Rotate q and k [n_tok][heads][d] by positions (int32) and append k and v to the bf16 cache;
     returns the rotated q.  Tokens may be strided (parts of one fused projection); q_out may be q."""
-    n, n_h, d = _dims("q", q, 3)
-    num_blocks, n_kv, bs, _ = _dims("k_pool", k_pool, 4)
     if q_out is None:
-        q_out = _empty((n, n_h, d), q.dtype, q.device, stream)
-    st = (_calls or _native()).rope_append(q, k, v, positions, slot_mapping, _table(table), k_pool, v_pool, q_out, err,
+        q_out = _empty(q.shape, q.dtype, q.device, stream)
+    st = (_calls or _native()).rope_append(q, k, v, positions, slot_mapping, table, k_pool, v_pool, q_out, err,
                                            None if stream is None else stream.cuda_stream)
     if st == _NOT_TAKEN:
+        _table_type(table)
+        n, n_h, d = _dims("q", q, 3)
+        num_blocks, n_kv, bs, _ = _dims("k_pool", k_pool, 4)
         _on_current(q, k, v, positions, slot_mapping, k_pool, v_pool, q_out, err)
         _typed(_bf16, q, k, v, k_pool, v_pool, q_out)
         _typed(_i32, positions, err)
@@ -502,15 +502,16 @@ def rope_append(q, k, v, positions, slot_mapping, table: RopeTable, k_pool, v_po
 def rope_qk(q, k, positions, table: RopeTable, q_out=None, k_out=None, stream=None):
     """Rotate q and k [n_tok][heads][d] by positions (int32); returns (q_out, k_out), which may be
     given as q and k themselves."""
-    n, n_h, d = _dims("q", q, 3)
-    n_kv = _dims("k", k, 3)[1]
     if q_out is None:
-        q_out = _empty((n, n_h, d), q.dtype, q.device, stream)
+        q_out = _empty(q.shape, q.dtype, q.device, stream)
     if k_out is None:
-        k_out = _empty((n, n_kv, d), k.dtype, k.device, stream)
-    st = (_calls or _native()).rope_qk(q, k, positions, _table(table), q_out, k_out,
+        k_out = _empty(k.shape, k.dtype, k.device, stream)
+    st = (_calls or _native()).rope_qk(q, k, positions, table, q_out, k_out,
                                        None if stream is None else stream.cuda_stream)
     if st == _NOT_TAKEN:
+        _table_type(table)
+        n, n_h, d = _dims("q", q, 3)
+        n_kv = _dims("k", k, 3)[1]
         _on_current(q, k, positions, q_out, k_out)
         _typed(_bf16, q, k, q_out, k_out)
         _typed(_i32, positions)
