@@ -20,9 +20,9 @@
 //
 // What bounds it: the select kernel, latency (two or three histogram rounds over a few KB to MB of
 // accounts); the move kernel, HBM (4 d bytes read and written per moved row).
-// Measured: 64 x 2.1-4K rows cut to 2048, 8 kv heads of 128, 84.3 us (17 of them the selection, the
-// moves at 93% of the copy rate); one sequence of 128K rows cut to 32K 58.4 us (24); small calls 9.5.
-// Having the move kernel write the movers' accounts and positions, too, from lists took 86.2 and 60.5.
+// Measured: 64 x 2.1-4K rows cut to 2048, 8 kv heads of 128, 82.7 us (15 of them the selection, the
+// moves at 93% of the copy rate); one sequence of 128K rows cut to 32K 58.4 us (24); small calls 8.
+// Having the move kernel write the movers' accounts and positions, too, from lists took 2 us more in both.
 #include <cooperative_groups.h>
 
 #include <cmath>
@@ -54,7 +54,6 @@ struct EvictArgs {
 };
 
 constexpr int kEvBins = 2048;
-constexpr int kEvRows = 16;                                   // rows per thread
 constexpr long long kEvMaxRows = 0x7fff0000;                  // row numbers plus a grid's threads stay in 32 bits
 
 // Order-keeping bits of an account: -0 below +0, NaN above everything but the recent rows.
@@ -536,25 +535,34 @@ extern "C" pkv_status pkv_kv_evict(void* k_pool, void* v_pool, const int32_t* bl
   const int sms = device_sm_count() > 0 ? device_sm_count() : 128;
   const long long pairs = (long long)batch * n_kv;
   a.vec = stride % 4 == 0 && !((reinterpret_cast<uintptr_t>(mass) | reinterpret_cast<uintptr_t>(positions)) & 15u);
-  // CTAs per (sequence, kv head): one of 256 threads for up to 4096 rows (four per SM), a cluster of
-  // up to eight of them for up to 32768, else eight of 1024 threads (131072 rows; beyond that the keys
-  // are read again in every round).  256 pairs of 9000 rows: two CTAs of 1024 threads (one per SM)
-  // measured 62 us and four of 256 threads 49 (39 since the last round of the histograms is skipped
-  // where it decides nothing); 2048 pairs of 2000 rows: level with 256 and 128 threads.
+  // A CTA's threads times their rows hold a (sequence, kv head) of up to 4096 rows: few rows per thread,
+  // since a thread takes its own in series, in no more threads than stay busy (1000 rows: four rows 8.4
+  // us, 16 rows 10.4; 32 pairs of 2000 rows: 512 threads 9.5, 256 threads 11.6, 2048 pairs of them 40.6
+  // and 36.7; 512 pairs of up to 4096 rows: 512 x 8 rows 82.8, 256 x 16 rows 84.4, 1024 x 4 rows 89.7).
+  // Beyond that a cluster of up to eight CTAs of 512 x 8 rows (8 pairs of 15000: 19.4 us, 256 x 16 24.1;
+  // 256 pairs of 9000, where that was better: 41.4 and 39.1), of 1024 x 8 (64 pairs of 60000: 222, 1024 x
+  // 16 241) or 1024 x 16 rows; more than 131072 rows are read again in every round.
+  const bool few = pairs <= 4LL * sms;
   int threads, ranks = 1;
   const void* fn;
-  if (max_ctx <= 256LL * kEvRows) {
+  if (max_ctx <= 1024) {
     threads = 256;
-    fn = (const void*)evict_select_kernel<256, kEvRows, false>;
-  } else if (max_ctx <= 8 * 256LL * kEvRows) {
-    threads = 256;
-    while (max_ctx > 256LL * kEvRows * ranks) ranks *= 2;
-    fn = (const void*)evict_select_kernel<256, kEvRows, true>;
+    fn = (const void*)evict_select_kernel<256, 4, false>;
+  } else if (max_ctx <= 2048) {
+    threads = few ? 512 : 256;
+    fn = few ? (const void*)evict_select_kernel<512, 4, false> : (const void*)evict_select_kernel<256, 8, false>;
+  } else if (max_ctx <= 4096) {
+    threads = 512;
+    fn = (const void*)evict_select_kernel<512, 8, false>;
+  } else if (max_ctx <= 8 * 4096) {
+    threads = 512;
+    while (max_ctx > 4096LL * ranks) ranks *= 2;
+    fn = (const void*)evict_select_kernel<512, 8, true>;
   } else {
     threads = 1024;
     ranks = 8;
-    fn = max_ctx <= 8 * 1024LL * kEvRows ? (const void*)evict_select_kernel<1024, kEvRows, true>
-                                         : (const void*)evict_select_kernel<1024, 0, true>;
+    fn = max_ctx <= 8 * 8192 ? (const void*)evict_select_kernel<1024, 8, true>
+         : max_ctx <= 8 * 16384 ? (const void*)evict_select_kernel<1024, 16, true> : (const void*)evict_select_kernel<1024, 0, true>;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(pairs * ranks));

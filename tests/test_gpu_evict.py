@@ -220,6 +220,18 @@ def test_evict_long_clusters_and_many(batch, n_kv, n, keep, recent):
     check_evict(kp, vp, bt, lens, [keep] * batch, recent, st, bs, True)
 
 
+# every shape of the selection: threads and rows per thread, one CTA or a cluster
+@pytest.mark.parametrize("batch,n_kv,n,keep", [(1, 2, 1024, 700), (3, 2, 1500, 40), (2, 2, 2048, 2047), (330, 2, 1100, 1000), (3, 2, 3000, 1700),
+                                               (2, 1, 4096, 2048), (1, 2, 20000, 7000), (1, 2, 70000, 69000)])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_evict_selection_shapes(batch, n_kv, n, keep, in_place):
+    bs = 16
+    lens = [max(1, n - 3 * s) for s in range(batch)]
+    kp, vp, bt, _ = pools(lens, n_kv, 64, bs, seed=n)
+    st = state_of(batch, n_kv, bt.shape[1] * bs, lens, [n // 3] * batch, np.random.default_rng(n), ties=n % 3 == 0)
+    check_evict(kp, vp, bt, lens, [keep] * batch, 33, st, bs, in_place)
+
+
 def test_evict_special_accounts():
     # NaN above infinity, both zeros, negatives, equal accounts over CTA boundaries
     bs, n = 16, 9000
