@@ -411,8 +411,10 @@ pkv_status pkv_paged_decode_attn_q8(const void* q, const uint8_t* cache, int for
  * paged_decode_attn_mass — pkv_paged_decode_attn that also adds, for each token t of sequence s
  * and kv head g, the attention weights it got from the group's query heads to an account:
  *   mass[(s * n_kv + g) * mass_stride + t] += sum over h in g of p[s][h][t],  t < context_lens[s]
- * in fp32 and in a fixed order (the same bits on every call).  Entries at or behind the context
- * are left as they were.  The accounts are per sequence, also where sequences share blocks.
+ * in fp32 and in a fixed order (the same bits on every call).  p is carried with all of its 24 bits
+ * as three bf16 parts; for a bf16 output and groups of over eight query heads as a high + low pair
+ * (16 bits: an error of at most 2^-17 sum p |v| of the output; the accounts always get all bits).
+ * Entries at or behind the context are left as they were.  The accounts are per sequence, also where sequences share blocks.
  *   mass          fp32, mass_stride >= max_blocks * block_size
  *   workspace     pkv_mass_workspace_bytes bytes (it holds the step's scores: 4 n_h bytes per
  *                 token of max_blocks * block_size; 0: invalid shape), 256-byte aligned

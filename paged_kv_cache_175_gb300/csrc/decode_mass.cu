@@ -22,6 +22,7 @@
 #include <cmath>
 #include <cstdlib>
 #include <mutex>
+#include <type_traits>
 
 #include "nvtx_range.h"
 #include "piece_streams.cuh"
@@ -44,13 +45,17 @@ __device__ __forceinline__ uint32_t keep_rows(uint32_t b, int t, int ntok) {
 }
 
 // TT: 16-token units per stage; NH n-tiles of 8 heads per consumer warp, MT consumer warps per
-// stream, NW streams.  sub: log2 of the units per table block.
-template <int D, int TT, int NH, int MT, int NW>
+// stream, NW streams.  sub: log2 of the units per table block.  PARTS: bf16 parts of p (8 bits each).
+// COMB (groups of up to 4 heads): column n of the n-tile holds head n % 4, so that two products carry
+// three parts.
+template <int D, int TT, int NH, int MT, int NW, int PARTS, bool COMB>
 __global__ void __launch_bounds__((NW * MT + 1) * 32, MT == 4 && NH == 1 ? 3 : (NH == 2 ? 2 : 1))
     decode_mass_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                        const DecodeArgs a, const MassArgs ms, const int sub) {
   constexpr int KS = D / 16, MD = D / 16, HW = 8 * NH, NBOX = D / 64;
+  constexpr int PROD = COMB ? 2 : PARTS;
   constexpr int BS = 16, BOX = BS * 128, TILE = BS * D * 2, STAGE = TT * 2 * TILE;
+  static_assert(!COMB || (NH == 1 && MT == 1 && PARTS == 3), "one n-tile holds the whole group");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int S = a.stages;
@@ -113,7 +118,7 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32, MT == 4 && NH == 1 ? 3 : (
   auto load_q = [&](size_t qrow0) {
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
-      const int hl = hw0 + nh * 8 + gid;                       // B-fragment column n = gid
+      const int hl = COMB ? gid & 3 : hw0 + nh * 8 + gid;      // B-fragment column n = gid
       const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q) + (qrow0 + hl) * (D / 2);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
@@ -189,23 +194,27 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32, MT == 4 && NH == 1 ? 3 : (
           }
       }
       softmax_tile<TT, NH, MD>(sc, m, l, o, gid, ntok, 0, 1.f);
-      // ---- O^T += V^T P^T, P as bf16 high + low ----
+      // ---- O^T += V^T P^T, a product per part of P; COMB: the high parts in columns 0-3 with the middle
+      // ones in columns 4-7, then the low parts ----
       const bool partial = ntok < TT * 16;
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
         if (t >= tiles) continue;
         const uint32_t vb = st + (uint32_t)(t * 2 * TILE + TILE);
         const int tok = ((mi >> 1) << 3) + (lane & 7);
-        uint32_t bh[NH][2], bl[NH][2];
+        uint32_t bp[PROD][NH][2];
 #pragma unroll
         for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const float x = sc[t][nh][2 * r], y = sc[t][nh][2 * r + 1];
             const uint32_t hi = pack_bf16(x, y);
-            const uint32_t lo = pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi));
-            bh[nh][r] = movmatrix_t(hi);
-            bl[nh][r] = movmatrix_t(lo);
+            const float x1 = x - bf16_lo(hi), y1 = y - bf16_hi(hi);
+            const uint32_t mid = pack_bf16(x1, y1);
+            const uint32_t lo = pack_bf16(x1 - bf16_lo(mid), y1 - bf16_hi(mid));
+            bp[0][nh][r] = movmatrix_t(COMB && tig >= 2 ? mid : hi);
+            bp[1][nh][r] = movmatrix_t(COMB ? (tig >= 2 ? 0u : lo) : mid);
+            if constexpr (PROD == 3) bp[2][nh][r] = movmatrix_t(lo);
           }
         const int t0 = t * 16 + 2 * tig;
 #pragma unroll
@@ -220,10 +229,9 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32, MT == 4 && NH == 1 ? 3 : (
             va[3] = keep_rows(va[3], t0 + 8, ntok);
           }
 #pragma unroll
-          for (int nh = 0; nh < NH; ++nh) {
-            mma_bf16(o[md][nh], va, bh[nh][0], bh[nh][1]);
-            mma_bf16(o[md][nh], va, bl[nh][0], bl[nh][1]);
-          }
+          for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+            for (int i = 0; i < PROD; ++i) mma_bf16(o[md][nh], va, bp[i][nh][0], bp[i][nh][1]);
         }
       }
     } else {
@@ -240,7 +248,13 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32, MT == 4 && NH == 1 ? 3 : (
       const bool whole = flags & F_WHOLE;
       const long long part = (long long)s * a.n_kv + g + p;
 #pragma unroll
-      for (int nh = 0; nh < NH; ++nh)
+      for (int nh = 0; nh < NH; ++nh) {
+        if constexpr (COMB) {                                  // the middle parts' columns lie two lanes on
+#pragma unroll
+          for (int md = 0; md < MD; ++md)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[md][nh][i] += __shfl_down_sync(FULL_MASK, o[md][nh][i], 2, 4);
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float L = l[nh][e];
@@ -279,6 +293,7 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32, MT == 4 && NH == 1 ? 3 : (
               *reinterpret_cast<float2*>(a.ws_ml + ((size_t)part * a.G + hl) * 2) = make_float2(m[nh][e], L);
           }
         }
+      }
     }
 
     __syncwarp();
@@ -377,33 +392,44 @@ struct MassVariant {
 // Streams, consumer warps and heads per warp by group.  One kv head, 17-32 heads, d = 128: four warps
 // of 8 heads, three CTAs per SM, 42.4 us for 8 x 20-40K tokens (64 x 2-8K: 54.6) against 43.8 (55.8)
 // with two warps of 16; at d = 64, 43.2 against 42.0 the other way.
-template <int D, int TT>
-static void mass_pick(int tiling, MassVariant& v) {
+// Parts of p: three, all of its 24 bits, for groups of up to eight heads, where they cost nothing (64 x
+// 0.5-4K tokens, four heads: 101.7 us with two and with three; 32 x 2-8K, eight heads: 122.6 and 122.1),
+// and for fp32 outputs.  For bf16 outputs of larger groups two, 16 bits: an error of at most 2^-17 sum p |v|
+// ahead of the output's own rounding of 2^-8 (64 x 2-8K tokens, 16 / 32 / 64 heads on one: 43.1 / 53.7 /
+// 85.7 us; with three parts 45.3 / 57.9 / 95.9).
+template <int D>
+static void mass_pick(int tiling, int G, bool all_bits, MassVariant& v) {
+  constexpr int T1 = D == 128 ? 1 : 2;                         // stages of 8 KB
   auto set = [&](const void* fn, int mt, int nw) {
     v.fn = fn;
     v.streams = nw;
     v.warps = nw * mt + 1;
   };
-  if (tiling == 0) set((const void*)decode_mass_kernel<D, TT, 1, 1, 3>, 1, 3);
-  else if (tiling == 1) set((const void*)decode_mass_kernel<D, TT, 2, 1, 3>, 1, 3);
-  else if (tiling == 2 && D == 128) set((const void*)decode_mass_kernel<D, TT, 1, 4, 1>, 4, 1);
-  else if (tiling == 2) set((const void*)decode_mass_kernel<D, TT, 2, 2, 2>, 2, 2);
-  else set((const void*)decode_mass_kernel<D, TT, 2, 4, 1>, 4, 1);
+  auto pick = [&](auto parts) {
+    constexpr int N = decltype(parts)::value;
+    if (tiling == 1) set((const void*)decode_mass_kernel<D, 2, 2, 1, 3, N, false>, 1, 3);
+    else if (tiling == 3) set((const void*)decode_mass_kernel<D, 2, 2, 4, 1, N, false>, 4, 1);
+    else if constexpr (D == 128) set((const void*)decode_mass_kernel<D, 2, 1, 4, 1, N, false>, 4, 1);
+    else set((const void*)decode_mass_kernel<D, 2, 2, 2, 2, N, false>, 2, 2);
+  };
+  if (G <= 4) set((const void*)decode_mass_kernel<D, T1, 1, 1, 3, 3, true>, 1, 3);
+  else if (tiling == 0) set((const void*)decode_mass_kernel<D, T1, 1, 1, 3, 3, false>, 1, 3);
+  else if (all_bits) pick(std::integral_constant<int, 3>{});
+  else pick(std::integral_constant<int, 2>{});
 }
 
-static MassVariant* lookup_mass(int D, int tiling) {
+static MassVariant* lookup_mass(int D, int G, bool all_bits) {
   // One table per process; the library drives one device per process.
   static std::mutex mu;
-  static MassVariant table[2][4];
-  static bool ready[2][4] = {};
-  const int di = D == 128 ? 1 : 0;
+  static MassVariant table[2][5][2];
+  static bool ready[2][5][2] = {};
+  const int di = D == 128 ? 1 : 0, tiling = head_tiling(G), vi = G <= 4 ? 0 : tiling + 1, pi = all_bits || G <= 8 ? 1 : 0;
   std::lock_guard<std::mutex> lock(mu);
-  MassVariant& v = table[di][tiling];
-  if (!ready[di][tiling]) {
-    const bool wide = D == 128 && tiling >= 1;
-    const int stage = wide ? 16384 : 8192;
-    if (D == 128) wide ? mass_pick<128, 2>(tiling, v) : mass_pick<128, 1>(tiling, v);
-    else mass_pick<64, 2>(tiling, v);
+  MassVariant& v = table[di][vi][pi];
+  if (!ready[di][vi][pi]) {
+    const int stage = D == 128 && tiling >= 1 ? 16384 : 8192;
+    if (D == 128) mass_pick<128>(tiling, G, all_bits, v);
+    else mass_pick<64>(tiling, G, all_bits, v);
     // Stages of a ring: groups of up to eight heads stream with two (three: 110.8 -> 114.9 us for 64 x
     // 0.5-4K tokens, 32 heads on 8); larger groups, whose stages take longer to consume, with three
     // (16 heads 47.7 -> 44.2 us, 32 heads at d = 64 45.0 -> 42.0).
@@ -414,7 +440,7 @@ static MassVariant* lookup_mass(int D, int tiling) {
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, v.fn, v.warps * 32, v.smem) != cudaSuccess || occ < 1)
       return nullptr;
     v.P = device_sm_count() * occ * v.streams;
-    ready[di][tiling] = true;
+    ready[di][vi][pi] = true;
   }
   return &v;
 }
@@ -448,8 +474,14 @@ using namespace pkv;
 extern "C" size_t pkv_mass_workspace_bytes(int batch, int n_h, int n_kv, int head_dim, int block_size, int max_blocks) {
   if (batch < 0 || max_blocks < 0 || !valid_shape(n_h, n_kv, head_dim, block_size)) return 0;
   if ((long long)max_blocks * block_size > kStreamMaxCtx) return 0;
-  MassVariant* v = lookup_mass(head_dim, head_tiling(n_h / n_kv));
-  return v ? mass_layout(batch, n_h, n_kv, head_dim, (long long)max_blocks * block_size, v->P).total : 0;
+  size_t most = 0;                                             // for either output type
+  for (int all_bits = 0; all_bits < 2; ++all_bits) {
+    MassVariant* v = lookup_mass(head_dim, n_h / n_kv, all_bits != 0);
+    if (!v) return 0;
+    const size_t n = mass_layout(batch, n_h, n_kv, head_dim, (long long)max_blocks * block_size, v->P).total;
+    most = n > most ? n : most;
+  }
+  return most;
 }
 
 extern "C" pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_pool, const void* v_pool,
@@ -472,7 +504,7 @@ extern "C" pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_po
   const MassAdd add = mass_add(G);
   const long long chunks = (max_ctx + add.tokens - 1) / add.tokens;
   if (chunks * batch * n_kv > 0x7fffffffLL) return PKV_ERANGE;
-  MassVariant* v = lookup_mass(head_dim, head_tiling(G));
+  MassVariant* v = lookup_mass(head_dim, G, out_dtype == PKV_OUT_F32);
   if (!v) {
     record_cuda_error(cudaGetLastError());
     return PKV_ECUDA;
