@@ -214,7 +214,7 @@ __device__ __forceinline__ int cta_exclusive_scan(int x, int* warp_tot, int* tot
 }
 
 __global__ void __launch_bounds__(kSelThreads)
-    select_top_kernel(const float* __restrict__ dev, const int32_t* __restrict__ seg_offsets,
+    select_top_kernel(const float* dev, const int32_t* __restrict__ seg_offsets,   // dev: written while this grid is resident
                       const int32_t* __restrict__ counts, int n_seg, int32_t* __restrict__ out) {
   __shared__ int hist[256];
   __shared__ int warp_tot[32];
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kSelThreads)
 // ---- fuse: recomputed rows of the selected tokens into the pools ----------------------------
 __global__ void __launch_bounds__(256) kv_fuse_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
                                                       const int64_t* __restrict__ row_slots,
-                                                      const int32_t* __restrict__ rows, long long total,
+                                                      const int32_t* rows, long long total,   // written while this grid is resident
                                                       int vec_per_row, int n_kv, int block_size, long long n_slots,
                                                       long long n_rows, uint4* __restrict__ k_pool,
                                                       uint4* __restrict__ v_pool, int32_t* err) {

@@ -247,10 +247,11 @@ __global__ void __launch_bounds__((MT + (PW ? 1 : 0)) * 32,
         const int hl = hw0 + nh * 8 + gid;                       // B-fragment column n = gid
         const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q) + (qrow0 + hl) * (D / 2);
         const bool ok = hl < a.G;
+        // plain loads: the kernel before may write q while this grid is already resident
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          qb[ks][nh][0] = ok ? __ldg(qp + ks * 8 + tig) : 0u;
-          qb[ks][nh][1] = ok ? __ldg(qp + ks * 8 + 4 + tig) : 0u;
+          qb[ks][nh][0] = ok ? qp[ks * 8 + tig] : 0u;
+          qb[ks][nh][1] = ok ? qp[ks * 8 + 4 + tig] : 0u;
         }
         m[nh][0] = m[nh][1] = -INFINITY;
         l[nh][0] = l[nh][1] = 0.f;

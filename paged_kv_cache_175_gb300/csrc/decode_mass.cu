@@ -115,6 +115,7 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32, MT == 4 && NH == 1 ? 3 : (
   const bool even = (a.G & 1) == 0;
   int slot = 0;
   uint32_t phase = 0;
+  // plain loads: the kernel before (a rotary append) may write q while this grid is already resident
   auto load_q = [&](size_t qrow0) {
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32, MT == 4 && NH == 1 ? 3 : (
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) qb[ks][nh][r] = hl < a.G ? __ldg(qp + ks * 8 + 4 * r + tig) : 0u;
+        for (int r = 0; r < 2; ++r) qb[ks][nh][r] = hl < a.G ? qp[ks * 8 + 4 * r + tig] : 0u;
     }
   };
   // the first segment's queries, while its first stage is on the way
@@ -314,9 +315,8 @@ template <bool V4> struct ScoreVec { using type = float4; };
 template <> struct ScoreVec<false> { using type = float; };
 
 template <int LT, bool V4, int U>
-__global__ void __launch_bounds__(256) mass_add_kernel(const float* __restrict__ scores, const float2* __restrict__ fin,
-                                                       const int32_t* __restrict__ ctx, int max_ctx, int n_kv, int G,
-                                                       float* __restrict__ mass, long long mass_stride, int chunks) {
+__global__ void __launch_bounds__(256) mass_add_kernel(const float* scores, const float2* fin, const int32_t* ctx, int max_ctx,
+                                                       int n_kv, int G, float* mass, long long mass_stride, int chunks) {
   constexpr int STEP = 256 / LT;
   __shared__ float2 f[64];
   const int chunk = blockIdx.x % chunks, sg = blockIdx.x / chunks, s = sg / n_kv;

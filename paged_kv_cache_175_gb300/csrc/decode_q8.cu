@@ -153,6 +153,7 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32, NH == 2 ? 2 : 4) decode_q8
   const int hw0 = warp % MT * HW;
   int slot = 0;
   uint32_t phase = 0;
+  // plain loads: the kernel before (a rotary append) may write q while this grid is already resident
   auto load_q = [&](size_t qrow0) {
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32, NH == 2 ? 2 : 4) decode_q8
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) qb[ks][nh][r] = hl < a.G ? __ldg(qp + ks * 8 + 4 * r + tig) : 0u;
+        for (int r = 0; r < 2; ++r) qb[ks][nh][r] = hl < a.G ? qp[ks * 8 + 4 * r + tig] : 0u;
     }
   };
   // the first segment's queries, while its first stage is on the way

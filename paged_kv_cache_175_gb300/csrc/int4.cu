@@ -625,8 +625,8 @@ __global__ void __launch_bounds__(MT * 32, TB == 2 || (BS == 64 && MT == 1) ? 12
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           const int w = (cb >> 1) + 4 * (ks >> 1) + 2 * (ks & 1);   // channel pair cb + 2*pr
-          qb[ks][nh][0] = ok ? bf2_to_h2(__ldg(qp + w)) : 0u;
-          qb[ks][nh][1] = ok ? bf2_to_h2(__ldg(qp + w + 1)) : 0u;
+          qb[ks][nh][0] = ok ? bf2_to_h2(qp[w]) : 0u;
+          qb[ks][nh][1] = ok ? bf2_to_h2(qp[w + 1]) : 0u;
         }
         m[nh][0] = m[nh][1] = -INFINITY;
         l[nh][0] = l[nh][1] = 0.f;
@@ -745,7 +745,8 @@ __global__ void __launch_bounds__(MT * 32, TB == 2 || (BS == 64 && MT == 1) ? 12
           }
         } else {
           // unfinished block: K rows from the bf16 tail in global memory (prefetched to L2),
-          // converted to fp16 (exact in range), against q itself
+          // converted to fp16 (exact in range), against q itself; plain loads, like those of q: the kernel
+          // before may write both while this grid is already resident
           const uint4* tl = reinterpret_cast<const uint4*>(a.k_tail + ((size_t)s * a.n_kv + g) * BS * D);
 #pragma unroll
           for (int tt = 0; tt < TPB; ++tt) {
@@ -755,7 +756,7 @@ __global__ void __launch_bounds__(MT * 32, TB == 2 || (BS == 64 && MT == 1) ? 12
             const uint4* q1 = q0 + D;                             // 8 rows further (D / 8 uint4 per row)
 #pragma unroll
             for (int k4 = 0; k4 < CB / 8; ++k4) {
-              const uint4 x = __ldg(q0 + k4), y = __ldg(q1 + k4);
+              const uint4 x = q0[k4], y = q1[k4];
               w0[4 * k4] = x.x; w0[4 * k4 + 1] = x.y; w0[4 * k4 + 2] = x.z; w0[4 * k4 + 3] = x.w;
               w1[4 * k4] = y.x; w1[4 * k4 + 1] = y.y; w1[4 * k4 + 2] = y.z; w1[4 * k4 + 3] = y.w;
             }

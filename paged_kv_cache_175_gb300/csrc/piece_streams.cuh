@@ -128,8 +128,8 @@ __device__ __forceinline__ void produce_streams(const DecodeArgs& a, const Strea
   auto entries = [&]() {                                       // of the next stage, used a round later
     const int32_t* row = a.bt + (size_t)cur.s * a.max_blocks;
     const int u = cur.b0 + cur.blk;
-    e0 = __ldg(row + (u >> sub));
-    e1 = nb > 1 && cur.blk + 1 < cur.nb ? __ldg(row + ((u + 1) >> sub)) : -1;
+    e0 = row[u >> sub];
+    e1 = nb > 1 && cur.blk + 1 < cur.nb ? row[(u + 1) >> sub] : -1;
   };
   if (st.len > 0) entries();
   uint32_t spins = 0;
