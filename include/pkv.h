@@ -24,6 +24,13 @@
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream).  Every call
  *     only enqueues work on `stream` and returns; the caller orders calls (e.g.
  *     append before attend) by issuing them on one stream.
+ *     Kernels are launched ahead of the end of the kernel before them (programmatic dependent
+ *     launch) and wait for it on the device.  Rotary calls, the 8-bit and the accounted attention,
+ *     the 8-bit append and the eviction read nothing before that wait: whatever earlier work on
+ *     the stream wrote, also the kernel directly ahead, is there.  pkv_paged_decode_attn and
+ *     pkv_paged_decode_attn_int4 (with their window and noalloc forms) read context_lens, and only
+ *     those, before it when batch <= 256: write the lengths ahead of the step's append, or of any
+ *     other kernel, not in the kernel directly ahead of these calls.
  *   - Argument errors are returned synchronously as a negative pkv_status and
  *     nothing is enqueued.  Errors only the GPU can see (a block-table entry or
  *     slot out of range, a context length out of range, a bounded wait that gave

@@ -179,7 +179,8 @@ cudaError_t launch_plan_streams(const int32_t* context_lens, int batch, int max_
 // the rows of segments that one piece holds (finished by the attention kernel itself) leave
 // right after it.  Empty sequences get a zero row here.  Without a plan kernel the CTA first
 // lays out the blocks of every sequence and their prefix sums in shared memory (one sequence
-// per thread); the context lengths are inputs of the call, and the plan kernel's prefix sums
+// per thread); the context lengths are inputs of the call (the kernels with streams let this one launch
+// behind their own wait, so whatever wrote the lengths has finished), and the plan kernel's prefix sums
 // finished before the attention kernel let this one launch.
 //
 // Two shapes.  Narrow, for batches whose segments span few pieces: LPR lanes per (sequence,

@@ -109,14 +109,14 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32, NH == 2 ? 2 : 4) decode_q8
     }
     fence_barrier_init();
   }
-  if (!a.inline_plan) grid_dep_wait();   // the plan kernel's cum / ctx_eff / cursors
+  // Every thread waits for the kernel before this one (the append, or whatever wrote the context lengths)
+  // ahead of its first read and, also without work, so that no later launch on the stream can pass it.  The
+  // merge is let in behind the wait: its setup reads the lengths, too.
+  grid_dep_wait();
   grid_dep_launch();
   if (warp < NW * MT && warp % MT == 0)
     stream_setup(a, blockIdx.x * NW + warp / MT, gridDim.x * NW, &starts[warp / MT]);
   __syncthreads();
-  // Every thread waits for the kernel before this one (the append), also those without work,
-  // so that no later launch on the stream can pass it.
-  if (a.inline_plan) grid_dep_wait();
 
   if (warp == NW * MT) {
     const uint64_t pol = policy_evict_first();
