@@ -30,7 +30,8 @@
  *     the stream wrote, also the kernel directly ahead, is there.  pkv_paged_decode_attn and
  *     pkv_paged_decode_attn_int4 (with their window and noalloc forms) read context_lens, and only
  *     those, before it when batch <= 256: write the lengths ahead of the step's append, or of any
- *     other kernel, not in the kernel directly ahead of these calls.
+ *     other kernel, not in the kernel directly ahead of these calls; later lengths may be read as
+ *     they were before (a wrong result or PKV_DEV_TIMEOUT, never an access out of bounds).
  *   - Argument errors are returned synchronously as a negative pkv_status and
  *     nothing is enqueued.  Errors only the GPU can see (a block-table entry or
  *     slot out of range, a context length out of range, a bounded wait that gave

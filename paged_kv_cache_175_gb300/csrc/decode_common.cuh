@@ -202,7 +202,8 @@ __device__ __forceinline__ void piece_setup(const DecodeArgs& a, int p, int P_la
 }
 
 // Advance by one position; only called while positions remain, so a non-empty
-// sequence lies ahead when the kv heads of the current one are exhausted.
+// sequence lies ahead when the kv heads of the current one are exhausted (and where lengths
+// changed during the call there may be none: the walk stays on the last sequence).
 __device__ __forceinline__ void cursor_next(Cursor& c, const DecodeArgs& a) {
   if (++c.blk < c.nb) return;
   c.seg_start += c.nb;
@@ -211,13 +212,13 @@ __device__ __forceinline__ void cursor_next(Cursor& c, const DecodeArgs& a) {
   c.g = 0;
   if (a.inline_plan) {
     do {
-      ++c.s;
+      c.s = min(c.s + 1, a.batch - 1);
       c.ctx = clamp_ctx(a.ctx_raw[c.s], a.max_ctx);
       c.nb = span_blocks(c.ctx, a.window, a.block_size);
     } while (c.nb == 0 && c.s < a.batch - 1);
   } else {
     do {
-      ++c.s;
+      c.s = min(c.s + 1, a.batch - 1);
       c.nb = a.cum[c.s + 1] - a.cum[c.s];
     } while (c.nb == 0 && c.s < a.batch - 1);
     c.ctx = a.ctx_eff[c.s];

@@ -26,3 +26,10 @@ def test_serving_kernels_wait_before_they_read(name, kernel, reads):
         assert r in body and body.index(r) > wait, r
     if "grid_dep_launch();" in body:                                          # what it lets in finds what it found
         assert body.index("grid_dep_launch();") > wait
+
+
+def test_a_walk_behind_the_last_sequence_stays_on_it():
+    text = source("decode_common.cuh")
+    walk = text[text.index("void cursor_next("):]
+    walk = walk[:walk.index("template")]
+    assert walk.count("min(c.s + 1, a.batch - 1)") == 2 and "++c.s" not in walk
