@@ -441,20 +441,26 @@ def _head_dense(t):
         raise PkvError("the heads of a token must be contiguous")
 
 
+# Buffers that a call makes itself come from the pool of the stream it runs on: a block just freed on another
+# stream may still be in use by work queued there, which nothing makes this stream wait for.
 def _scratch(nbytes, device, stream):
-    """A workspace of nbytes that stays alive for the work on `stream`."""
+    """A workspace of nbytes for a call on `stream`, which alone uses it."""
     if nbytes == 0:
         raise PkvError("unsupported shape or no device")
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def _empty(shape, dtype, device, stream):
-    out = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        out.record_stream(stream)
+    """An output of a call on `stream`; it may be used on the current stream, too (once that waits)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    if out.is_cuda:
+        out.record_stream(torch.cuda.current_stream(out.device))
     return out
 
 
