@@ -157,13 +157,32 @@ def decode_workspace_bytes(batch, n_h, n_kv, head_dim, block_size, int4=False) -
     return n
 
 
-def _workspace(nbytes, device):
-    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+# Buffers that a call makes itself come from the pool of the stream it runs on: a block just freed on another
+# stream may still be in use by work queued there, which nothing makes this stream wait for.
+def _scratch(nbytes, device, stream):
+    """A workspace of nbytes for a call on `stream`, which alone uses it."""
+    if nbytes == 0:
+        raise PkvError("unsupported shape or no device")
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _out(q, out, out_dtype):
+def _empty(shape, dtype, device, stream):
+    """An output of a call on `stream`; it may be used on the current stream, too (once that waits)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    if out.is_cuda:
+        out.record_stream(torch.cuda.current_stream(out.device))
+    return out
+
+
+def _out(q, out, out_dtype, stream):
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        out = _empty(q.shape, out_dtype, q.device, stream)
     assert out.shape == q.shape and out.dtype in (torch.bfloat16, torch.float32)
     return out, (PKV_OUT_F32 if out.dtype == torch.float32 else PKV_OUT_BF16)
 
@@ -201,10 +220,10 @@ def _decode_bf16(q, k_pool, v_pool, block_tables, context_lens, scale, window, o
     B, n_h, d = q.shape
     num_blocks, n_kv, bs, d2 = k_pool.shape
     assert d2 == d and v_pool.shape == k_pool.shape
-    out, od = _out(q, out, out_dtype)
+    out, od = _out(q, out, out_dtype, stream)
     need = decode_workspace_bytes(B, n_h, n_kv, d, bs)
     if workspace is None:
-        workspace = _workspace(need, q.device)
+        workspace = _scratch(max(need, 256), q.device, stream)
     if window == 0:
         _check("paged_decode_attn", lib().pkv_paged_decode_attn(
             _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
@@ -229,7 +248,7 @@ def paged_decode_attn_noalloc(q, k_pool, v_pool, block_tables, context_lens, sca
     num_blocks, n_kv, bs, d2 = k_pool.shape
     assert d2 == d and v_pool.shape == k_pool.shape
     assert block_tables.dim() == 2 and block_tables.shape[0] == B and context_lens.shape == (B,)
-    out, od = _out(q, out, out_dtype)
+    out, od = _out(q, out, out_dtype, stream)
     _check("paged_decode_attn_noalloc", lib().pkv_paged_decode_attn_noalloc(
         _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
         float(scale), B, n_h, n_kv, d, bs, num_blocks, _ptr(out), od, _ptr(err), _stream(stream)))
@@ -316,10 +335,10 @@ def _decode_int4(q, cache, block_tables, context_lens, scale, window, out, out_d
     B, n_h, d = q.shape
     nb, n_kv, bs, d2 = cache.shape
     assert d2 == d and cache.k_tail.shape[0] >= B
-    out, od = _out(q, out, out_dtype)
+    out, od = _out(q, out, out_dtype, stream)
     need = decode_workspace_bytes(B, n_h, n_kv, d, bs, int4=True)
     if workspace is None:
-        workspace = _workspace(need, q.device)
+        workspace = _scratch(max(need, 256), q.device, stream)
     if window == 0:
         _check("paged_decode_attn_int4", lib().pkv_paged_decode_attn_int4(
             _ptr(q), _ptr(cache.records), _ptr(cache.k_tail), _ptr(block_tables), block_tables.shape[1],
@@ -439,29 +458,6 @@ def _head_dense(t):
     _, h, d = t.shape
     if t.numel() and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
         raise PkvError("the heads of a token must be contiguous")
-
-
-# Buffers that a call makes itself come from the pool of the stream it runs on: a block just freed on another
-# stream may still be in use by work queued there, which nothing makes this stream wait for.
-def _scratch(nbytes, device, stream):
-    """A workspace of nbytes for a call on `stream`, which alone uses it."""
-    if nbytes == 0:
-        raise PkvError("unsupported shape or no device")
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-
-
-def _empty(shape, dtype, device, stream):
-    """An output of a call on `stream`; it may be used on the current stream, too (once that waits)."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        out = torch.empty(shape, dtype=dtype, device=device)
-    if out.is_cuda:
-        out.record_stream(torch.cuda.current_stream(out.device))
-    return out
 
 
 def _table_type(table):
@@ -898,7 +894,7 @@ def kv_deviation(k_pool, v_pool, slots, k_new, v_new, out=None, err=None, stream
     num_blocks, n_kv, bs, d = k_pool.shape
     n = slots.numel()
     assert k_new.shape == v_new.shape == (n, n_kv, d)
-    dev = torch.empty(n, dtype=torch.float32, device=k_pool.device) if out is None else out
+    dev = _empty((n,), torch.float32, k_pool.device, stream) if out is None else out
     assert dev.dtype == torch.float32 and dev.numel() == n
     _check("kv_deviation", lib().pkv_kv_deviation(_ptr(k_pool), _ptr(v_pool), _ptr(slots), _ptr(k_new), _ptr(v_new),
                                                   n, num_blocks, bs, n_kv, d, _ptr(dev), _ptr(err), _stream(stream)))
@@ -917,9 +913,10 @@ def select_top(dev, seg_offsets, counts, out=None, stream=None):
         cnt = np.ascontiguousarray(counts, dtype=np.int32)
         assert len(offs) == len(cnt) + 1
         total = int(np.minimum(np.maximum(cnt, 0), np.maximum(np.diff(offs), 0)).sum())
-        out = torch.empty(max(total, 1), dtype=torch.int32, device=dev.device)[:total]
-        seg_offsets = torch.as_tensor(offs, device=dev.device)
-        counts = torch.as_tensor(cnt, device=dev.device)
+        out = _empty((max(total, 1),), torch.int32, dev.device, stream)[:total]
+        with torch.cuda.stream(stream):                        # None: the current stream
+            seg_offsets = torch.as_tensor(offs, device=dev.device)
+            counts = torch.as_tensor(cnt, device=dev.device)
     _cuda(seg_offsets, counts)
     assert seg_offsets.dtype == counts.dtype == out.dtype == torch.int32
     _check("select_top", lib().pkv_select_top(_ptr(dev), _ptr(seg_offsets), _ptr(counts), counts.numel(), _ptr(out),

@@ -103,3 +103,47 @@ def test_buffers_made_for_a_stream_are_not_given_away_early(name):
         taken = torch.full_like(want, 3)
     torch.cuda.synchronize()
     assert torch.equal(read, want) and all(bool((x == 77).all()) for x in grabbed) and bool((taken == 3).all())
+
+
+class OlderCalls(Calls):
+    """The bf16 and INT4 attention, the deviation and the selection."""
+
+    def run(self, name, stream, **kw):
+        if name == "bf16":
+            return pkv.paged_decode_attn(self.q, self.kp, self.vp, self.bt, self.ctx, 0.125, stream=stream, **kw)
+        if name == "noalloc":
+            return pkv.paged_decode_attn_noalloc(self.q, self.kp, self.vp, self.bt, self.ctx, 0.125, stream=stream, **kw)
+        if name == "int4":
+            return pkv.paged_decode_attn_int4(self.q, self.c4, self.bt, self.ctx, 0.125, stream=stream, **kw)
+        if name == "deviation":
+            return pkv.kv_deviation(self.kp, self.vp, self.slots, self.k, self.v, stream=stream, **kw)
+        return pkv.select_top(self.k.float().view(-1), [0, 1000, 5000], [100, 900], stream=stream, **kw)
+
+    def buffers(self, name):
+        nbytes = {"deviation": 4 * B, "select": 4 * 1000}.get(name, self.q.nbytes)
+        return ("out", nbytes, None), self.ws.get(name)
+
+
+OLDER = ["bf16", "noalloc", "int4", "deviation", "select"]
+
+
+@pytest.mark.parametrize("name", OLDER)
+def test_older_outputs_do_not_take_memory_still_in_use(name):
+    c, st = OlderCalls(), torch.cuda.Stream()
+    (_, nbytes, _), ws = c.buffers(name)
+    kw = {} if ws is None else {"workspace": torch.empty(ws, dtype=torch.uint8, device=DEV)}
+    want_out = c.run(name, None, **kw)
+    copy, want = freed_under_way(nbytes)
+    out = c.run(name, st, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want) and torch.equal(out, want_out) and out.nbytes == nbytes
+
+
+@pytest.mark.parametrize("name", ["bf16", "int4"])
+def test_older_workspaces_do_not_take_memory_still_in_use(name):
+    c, st = OlderCalls(), torch.cuda.Stream()
+    out = c.run(name, None)
+    copy, want = freed_under_way(c.ws[name])
+    c.run(name, st, out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want)
