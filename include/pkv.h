@@ -455,8 +455,8 @@ pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_pool, const v
  *   new_lens   int32 [batch]: min(n, K); must not overlap context_lens, keep, kept or dropped
  *   workspace  pkv_evict_workspace_bytes bytes, 256-byte aligned
  * max_blocks * block_size is at most 0x7fff0000 (PKV_ERANGE).
- * The blocks that hold the first K rows are rewritten: they must belong to the sequence alone
- * (see pkv_bm_evict).  Moves from or to a block id outside the pool set PKV_DEV_BAD_BLOCK and are
+ * The blocks that hold the first K rows are rewritten: they must belong to the sequence alone.
+ * Nothing here can tell; pkv_bm_evict does, and is called before this (see there).  Moves from or to a block id outside the pool set PKV_DEV_BAD_BLOCK and are
  * skipped; context lengths out of range are clamped with PKV_DEV_BAD_CTX.
  */
 size_t pkv_evict_workspace_bytes(int batch, int n_kv, int block_size, int max_blocks);

@@ -105,8 +105,11 @@ int pkv_bm_release(pkv_block_manager* bm, int64_t seq_id);
  * into the tree.  Returns the index of the first block the sequence still holds. */
 int pkv_bm_slide_window(pkv_block_manager* bm, int64_t seq_id, int window);
 
-/* Cut a sequence's cache to its first `keep` rows (1 <= keep <= its length), for pkv_kv_evict
- * called with the sequence's table from before and that budget: the blocks behind them are
+/* Cut a sequence's cache to its first `keep` rows (1 <= keep <= its length), ahead of
+ * pkv_kv_evict: take the tables, make this call, and where it succeeds launch pkv_kv_evict with the
+ * table and length from before and that budget, ahead of the manager's next call and of any work
+ * that writes the released blocks.  Where it refuses, the sequence's rows must not be moved (give
+ * pkv_kv_evict a budget of at least its length).  The blocks behind the rows are
  * released, later tokens are appended from row `keep` on, and pkv_bm_tables reports `keep` as the
  * context length.  The remaining blocks no longer hold the prompt's tokens in order: they leave
  * the tree, with their subtrees, and none of the sequence's blocks is registered again.

@@ -836,11 +836,31 @@ class BlockManager:
         return r
 
     def evict(self, seq_id, keep):
-        """Cut a sequence to its first `keep` cache rows (after kv_evict); returns the blocks left."""
+        """Cut a sequence to its first `keep` cache rows; returns the blocks left.  Called before kv_evict, with
+        the table from before it: where this refuses (a block that stays is shared), the rows must not move."""
         r = lib().pkv_bm_evict(self._h, int(seq_id), int(keep))
         if r < 0:
             _check("bm_evict", r)
         return r
+
+    def cut_to(self, seq_ids, lens, budget):
+        """Cut sequences of context lengths `lens` (from tables()) to at most `budget` rows; returns `keep` for
+        kv_evict, which follows before the manager's next call, with the tables and lengths from before this one.
+        Sequences no longer than the budget, or whose blocks may not be rewritten (one that stays is shared with
+        another sequence, or some were released by slide_window), keep all their rows."""
+        ids, lens, budget = [int(s) for s in seq_ids], [int(n) for n in lens], int(budget)
+        if budget < 1 or len(lens) != len(ids) or len(set(ids)) != len(ids):
+            raise PkvError("cut_to: a budget of at least one row, and distinct sequences with a length each")
+        keep = list(lens)
+        for i, s in enumerate(ids):
+            if lens[i] <= budget:
+                continue
+            r = lib().pkv_bm_evict(self._h, s, budget)
+            if r >= 0:
+                keep[i] = budget
+            elif r != -1:                                      # anything but a refusal
+                _check("bm_evict", r)
+        return keep
 
     def tables(self, seq_ids, max_blocks):
         """(block tables int32 [n][max_blocks], context lengths int32 [n]) for an attention call."""
