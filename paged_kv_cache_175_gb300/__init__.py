@@ -474,12 +474,12 @@ def _out_type(out_dtype):
 def rope_append(q, k, v, positions, slot_mapping, table: RopeTable, k_pool, v_pool, q_out=None, err=None, stream=None):
     """Rotate q and k [n_tok][heads][d] by positions (int32) and append k and v to the bf16 cache;
     returns the rotated q.  Tokens may be strided (parts of one fused projection); q_out may be q."""
+    _table_type(table)
     if q_out is None:
         q_out = _empty(q.shape, q.dtype, q.device, stream)
     st = (_calls or _native()).rope_append(q, k, v, positions, slot_mapping, table, k_pool, v_pool, q_out, err,
                                            None if stream is None else stream.cuda_stream)
     if st == _NOT_TAKEN:
-        _table_type(table)
         n, n_h, d = _dims("q", q, 3)
         num_blocks, n_kv, bs, _ = _dims("k_pool", k_pool, 4)
         _on_current(q, k, v, positions, slot_mapping, k_pool, v_pool, q_out, err)
@@ -504,6 +504,7 @@ def rope_append(q, k, v, positions, slot_mapping, table: RopeTable, k_pool, v_po
 def rope_qk(q, k, positions, table: RopeTable, q_out=None, k_out=None, stream=None):
     """Rotate q and k [n_tok][heads][d] by positions (int32); returns (q_out, k_out), which may be
     given as q and k themselves."""
+    _table_type(table)
     if q_out is None:
         q_out = _empty(q.shape, q.dtype, q.device, stream)
     if k_out is None:
@@ -511,7 +512,6 @@ def rope_qk(q, k, positions, table: RopeTable, q_out=None, k_out=None, stream=No
     st = (_calls or _native()).rope_qk(q, k, positions, table, q_out, k_out,
                                        None if stream is None else stream.cuda_stream)
     if st == _NOT_TAKEN:
-        _table_type(table)
         n, n_h, d = _dims("q", q, 3)
         n_kv = _dims("k", k, 3)[1]
         _on_current(q, k, positions, q_out, k_out)
