@@ -26,7 +26,7 @@ from dataclasses import dataclass
 
 import torch
 
-from ._build import CALLS as CALLS_PATH, LIB as LIB_PATH, build_library
+from ._build import CALLS as CALLS_PATH, LIB as LIB_PATH, build_library, calls_current
 
 PKV_OUT_BF16 = 0
 PKV_OUT_F32 = 1
@@ -408,8 +408,9 @@ def _native():
     global _calls
     if _calls is None:
         lib()
-        if not os.path.exists(CALLS_PATH):
-            raise PkvError(f"{CALLS_PATH} is missing: build it with paged_kv_cache_175_gb300._build.build_library()")
+        if not calls_current():
+            raise PkvError(f"{CALLS_PATH} is missing, or was built for another torch or Python: build it with "
+                           "paged_kv_cache_175_gb300._build.build_library()")
         _calls = importlib.import_module("._calls", __name__)
     return _calls
 
