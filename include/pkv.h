@@ -450,9 +450,11 @@ pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_pool, const v
  *              row r >= kept[s] holds token dropped[s] + r
  *   kept       int32 [batch]: rows that the last eviction left (0 at the start)
  *   dropped    int32 [batch]: tokens evicted so far (0 at the start)
- * The new state goes to the _out pointers: all four equal to the inputs (in place), or none.
+ * The new state goes to the _out pointers: all four equal to the inputs (in place), or none, and then
+ * without overlap with them, the lengths or the budgets (PKV_EINVAL).
  * Entries of mass_out behind n, and of positions_out behind the new kept, are left as they were.
- *   new_lens   int32 [batch]: min(n, K); must not overlap context_lens, keep, kept or dropped
+ *   new_lens   int32 [batch]: min(n, K); must not overlap context_lens, keep or the old or new kept and
+ *              dropped
  *   workspace  pkv_evict_workspace_bytes bytes, 256-byte aligned
  * max_blocks * block_size is at most 0x7fff0000 (PKV_ERANGE).
  * The blocks that hold the first K rows are rewritten: they must belong to the sequence alone.

@@ -457,6 +457,11 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a, cons
   }
 }
 
+static bool overlap(const void* a, const void* b, size_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + bytes && y < x + bytes;
+}
+
 struct EvictLayout {
   size_t dst, src, total;
   int max_moves;
@@ -512,6 +517,18 @@ extern "C" pkv_status pkv_kv_evict(void* k_pool, void* v_pool, const int32_t* bl
   if ((long long)batch * n_kv > 0x7fffffffLL / 64) return PKV_ERANGE;
   const EvictLayout w = evict_layout(batch, n_kv, max_ctx);
   if (workspace_bytes < w.total) return PKV_ENOSPC;
+  // no output lies over another, nor a new state over what is still read of the old one
+  const size_t lens = sizeof(int32_t) * (size_t)batch;
+  const size_t rows = sizeof(float) * ((size_t)((long long)batch * n_kv - 1) * (size_t)stride + (size_t)max_ctx);
+  if (overlap(new_lens, kept_out, lens) || overlap(new_lens, dropped_out, lens) || overlap(kept_out, dropped_out, lens) ||
+      overlap(mass_out, positions_out, rows))
+    return PKV_EINVAL;
+  if (!in_place) {
+    for (const int32_t* p : {context_lens, keep, kept, dropped})
+      if (overlap(kept_out, p, lens) || overlap(dropped_out, p, lens)) return PKV_EINVAL;
+    for (const void* p : {(const void*)mass, (const void*)positions})
+      if (overlap(mass_out, p, rows) || overlap(positions_out, p, rows)) return PKV_EINVAL;
+  }
   char* ws = static_cast<char*>(workspace);
   EvictArgs a = {};
   a.mass = mass; a.positions = positions; a.kept = kept; a.dropped = dropped;
