@@ -425,7 +425,8 @@ pkv_status pkv_paged_decode_attn_q8(const void* q, const uint8_t* cache, int for
  * Entries at or behind the context are left as they were.  The accounts are per sequence, also where sequences share blocks.
  *   mass          fp32, mass_stride >= max_blocks * block_size
  *   workspace     pkv_mass_workspace_bytes bytes (it holds the step's scores: 4 n_h bytes per
- *                 token of max_blocks * block_size; 0: invalid shape), 256-byte aligned
+ *                 token of max_blocks * block_size, so a table no wider than needed is better; 0:
+ *                 invalid shape), 256-byte aligned
  * Tokens of a bad block weigh nothing; max_blocks * block_size is at most 0x7fff0000 (PKV_ERANGE).
  * Other arguments and errors as for pkv_paged_decode_attn.
  */
@@ -456,7 +457,8 @@ pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_pool, const v
  *   new_lens   int32 [batch]: min(n, K); must not overlap context_lens, keep or the old or new kept and
  *              dropped
  *   workspace  pkv_evict_workspace_bytes bytes, 256-byte aligned
- * max_blocks * block_size is at most 0x7fff0000 (PKV_ERANGE).
+ * max_blocks * block_size is at most 0x7fff0000 (PKV_ERANGE); the work is laid out for that many
+ * rows, so give a table no wider than the longest sequence needs.
  * The blocks that hold the first K rows are rewritten: they must belong to the sequence alone.
  * Nothing here can tell; pkv_bm_evict does, and is called before this (see there).  Moves from or to a block id outside the pool set PKV_DEV_BAD_BLOCK and are
  * skipped; context lengths out of range are clamped with PKV_DEV_BAD_CTX.

@@ -628,7 +628,9 @@ def q8_workspace_bytes(batch, n_h, n_kv, head_dim, block_size, fmt="e4m3") -> in
 
 def paged_decode_attn_q8(q, cache: Q8CacheTensors, block_tables, context_lens, scale, window=0, out=None,
                          out_dtype=torch.bfloat16, workspace=None, err=None, stream=None):
-    """Decode attention over the 8-bit cache (the last `window` tokens of each context; 0: all)."""
+    """Decode attention over the 8-bit cache (the last `window` tokens of each context; 0: all).  A bfloat16
+    output of groups of over four query heads takes the softmax weights rounded to fp16 once (2^-11); a float32
+    output takes 22 bits of them."""
     fmt = _q8_format(cache)
     if out is None:
         out = _empty(q.shape, _out_type(out_dtype), q.device, stream)
@@ -669,7 +671,8 @@ def mass_workspace_bytes(batch, n_h, n_kv, head_dim, block_size, max_blocks) -> 
 def paged_decode_attn_mass(q, k_pool, v_pool, block_tables, context_lens, scale, mass, out=None,
                            out_dtype=torch.bfloat16, workspace=None, err=None, stream=None):
     """paged_decode_attn that also adds each cached token's attention weight, summed over the query
-    heads of its group, to mass (fp32 [B][n_kv][at least max_blocks * block_size])."""
+    heads of its group, to mass (fp32 [B][n_kv][at least max_blocks * block_size]).  The softmax weights
+    reach the output with all their bits (a bfloat16 output of groups of over eight heads: 16 of them)."""
     if out is None:
         out = _empty(q.shape, _out_type(out_dtype), q.device, stream)
     if workspace is None and q.is_cuda and q.shape[0]:
@@ -732,7 +735,8 @@ def evict_workspace_bytes(batch, n_kv, block_size, max_blocks) -> int:
 def kv_evict(k_pool, v_pool, block_tables, context_lens, keep, recent, state: EvictState, out: EvictState | None = None,
              new_lens=None, workspace=None, err=None, stream=None):
     """Cut each sequence of the bf16 cache to keep[s] rows (int32 [B]): those of its last `recent`
-    tokens and those with the largest accounts.  Updates `state` in place, or writes the new state to
+    tokens and those with the largest accounts.  With a BlockManager, `keep` comes from its cut_to, which goes
+    first and knows whose rows may move.  Updates `state` in place, or writes the new state to
     `out`; returns the new context lengths (a tensor of its own)."""
     dst = state if out is None else out
     if new_lens is None:

@@ -16,7 +16,7 @@
 // streams of piece_streams.cuh, in units of 16 tokens whatever the block size: a TMA box of 16 rows
 // starts inside a larger block as well.  K and V land in 128-byte swizzled boxes and are read by
 // ldmatrix.
-// Measured: 64 x 0.5-4K tokens, 32 heads on 8 of 128, 109 us (83% of the copy rate; the attention 96,
+// Measured: 64 x 0.5-4K tokens, 32 heads on 8 of 128, 110 us (83% of the copy rate; the attention 97,
 // merge and addition in series behind it); 8 x 20-40K tokens, 32 heads on one, 42.2 us (30 the
 // attention, bound by each consumer warp's chain of products and softmax); small calls 8-11 us.
 #include <cmath>
@@ -310,7 +310,9 @@ __global__ void __launch_bounds__((NW * MT + 1) * 32, MT == 4 && NH == 1 ? 3 : (
 // mass[s][g][t] += sum over the group's heads of 2^(x - M) / L.  LT lanes share a token's G scores
 // (vectors of four where G allows), so a warp reads whole lines, and add their parts by a fixed
 // tree; a lane has the loads of U tokens in flight (one at a time left the kernel at 2.2 TB/s of
-// scores on 32-head groups).  CTA (c, s, g) takes 256 / LT * U tokens.
+// scores on 32-head groups).  CTA (c, s, g) takes 256 / LT * U tokens of the table's width; those behind
+// the context leave at once, which a table far wider than the contexts still feels (64 x 0.5-4K tokens,
+// 8 kv heads: 100 us with a table of 4096 tokens, 111 with 32768, 145 with 131072).
 template <bool V4> struct ScoreVec { using type = float4; };
 template <> struct ScoreVec<false> { using type = float; };
 

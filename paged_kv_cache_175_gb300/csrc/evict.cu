@@ -20,8 +20,9 @@
 //
 // What bounds it: the select kernel, latency (two or three histogram rounds over a few KB to MB of
 // accounts); the move kernel, HBM (4 d bytes read and written per moved row).
-// Measured: 64 x 2.1-4K rows cut to 2048, 8 kv heads of 128, 82.7 us (15 of them the selection, the
-// moves at 93% of the copy rate); one sequence of 128K rows cut to 32K 58.4 us (24); small calls 8.
+// Measured: 64 x 2.1-4K rows cut to 2048, 8 kv heads of 128, 82.6 us (16.7 of them the selection; the
+// moves, 367 MB, at 82% of the copy rate); one sequence of 128K rows cut to 32K 58.4 us (23.8; 203 MB at 87%);
+// small calls 8.
 // Having the move kernel write the movers' accounts and positions, too, from lists took 2 us more in both.
 #include <cooperative_groups.h>
 
@@ -559,6 +560,9 @@ extern "C" pkv_status pkv_kv_evict(void* k_pool, void* v_pool, const int32_t* bl
   // Beyond that a cluster of up to eight CTAs of 512 x 8 rows (8 pairs of 15000: 19.4 us, 256 x 16 24.1;
   // 256 pairs of 9000, where that was better: 41.4 and 39.1), of 1024 x 8 (64 pairs of 60000: 222, 1024 x
   // 16 241) or 1024 x 16 rows; more than 131072 rows are read again in every round.
+  // All of this goes by the table's width, the host knowing no lengths: with a table wider than any sequence
+  // the clusters hold mostly idle threads (64 x 2.1-4K rows, 8 heads: 83 us with a table of 4096 rows, 109
+  // with 8192, 238 with 32768, 457 with 131072).
   const bool few = pairs <= 4LL * sms;
   int threads, ranks = 1;
   const void* fn;

@@ -2,8 +2,10 @@
 //
 // Mathematics, per (block, kv head) and for K and V apart: big = max |x| over the rows that the
 // block holds; scale = big * (1 / M), code = round_to_nearest_even(x * ((1 / big) * M)), M = 448
-// (e4m3) or 127 (int8), every operation rounded to fp32.  The result is a function of the rows alone, not of how
-// many calls brought them: the bf16 rows of a sequence's unfinished block are kept in its tail
+// (e4m3) or 127 (int8), every operation rounded to fp32.  (Products with reciprocals are how elementary
+// torch operations on the GPU divide a tensor by a number and a number by a tensor, so the codes equal
+// theirs; divisions rounded once would be as repeatable and differ in a last place now and then.)
+// The result is a function of the rows alone, not of how many calls brought them: the bf16 rows of a sequence's unfinished block are kept in its tail
 // and the record is written anew from them at each append, so the attention reads records only
 // and a finished block was rounded once.
 //
@@ -13,12 +15,12 @@
 // Split: one CTA per kv head, K or V, and span of tokens takes each run of tokens that lands in
 // one block, 64 / block_size runs side by side (64 rows in shared memory at a time).  A span is 64
 // tokens in long calls and as many tokens as there are places for runs in short ones, where every
-// token tends to be a run.  The runs of a span are found in one round trip; the search for a
+// token of a decode step is a run (kSpanTokens says what that costs a prompt chunk).  The runs of a span are found in one round trip; the search for a
 // sequence's end, which few runs need, goes on while the rows arrive.
 // Measured (8 kv heads of 128): 8000 tokens of one prompt in blocks of 16 in 15.1 us (3.3 TB/s), one
 // run at a time 21.7, four CTAs per SM instead of six 17.3; 23 ragged prompts of 234-701 tokens in
 // blocks of 64 in 23.8 us (3.1 TB/s; the CTAs with two or three runs end last; asking for the next
-// run's rows ahead cost the registers of a CTA per SM and was level); 64 single tokens in 3.1 us.
+// run's rows ahead cost the registers of a CTA per SM and was level); 64 single tokens in 3.0 us.
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -40,6 +42,12 @@ struct Q8AppendArgs {
   int32_t* err;
 };
 
+// Calls of up to this many tokens are taken for decode steps.  Single tokens of as many sequences, 8 kv heads
+// of 128, spans of 64 / block_size tokens against spans of 64: 64 tokens 3.3 us against 26 (blocks of 64: 6.0
+// and 86), 2048 tokens 37 against 64 (128 and 224).  One prompt is the other way round from 100-500 tokens on, since
+// only one token in block_size starts a run and the other CTAs find nothing to do: 256 tokens in blocks of 16
+// 4.4 against 5.2, 2048 13 against 7.6; in blocks of 64 256 tokens 7.0 against 5.2, 2048 36 against 7.6, with 32
+// kv heads 135 against 13.  A rule that knows the runs would serve both.
 constexpr int kSpanTokens = 2048;
 
 // Four codes.  INT8: |x| <= 127 (1 + 2^-22), so adding 1.5 * 2^23 rounds x to the nearest integer

@@ -16,7 +16,7 @@
 // row, vector) order, issues all its loads first and builds the angle table of its tokens
 // (shared by all their heads) while they are in flight.  What an item needs besides its data is
 // worked out again for the store: held over the barrier it cost the registers of two CTAs per SM
-// (80 us).
+// (16384 tokens of 32 + 8 + 8 heads of 128: 80 us instead of 63).
 #include <cmath>
 
 #include "decode_common.cuh"
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_kernel(const __gr
   // Launched while the kernel before may still run; nothing is read or written before the wait, and the
   // next kernel is let in only behind it (so its setup, too, finds that kernel's results).
   grid_dep_wait();
-  grid_dep_launch();                       // the attention's setup may overlap this kernel
+  grid_dep_launch();                       // the attention's launch may overlap this kernel
   const int H = a.t.rotary_dim >> 1, RP = a.t.rotary_dim >> 4;
   const bool inter = a.t.interleaved != 0;
   const long long total = (long long)a.n_tok * a.items_per_tok;
