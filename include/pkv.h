@@ -422,7 +422,8 @@ pkv_status pkv_paged_decode_attn_q8(const void* q, const uint8_t* cache, int for
  * in fp32 and in a fixed order (the same bits on every call).  p is carried with all of its 24 bits
  * as three bf16 parts; for a bf16 output and groups of over eight query heads as a high + low pair
  * (16 bits: an error of at most 2^-17 sum p |v| of the output; the accounts always get all bits).
- * Entries at or behind the context are left as they were.  The accounts are per sequence, also where sequences share blocks.
+ * Entries at or behind the context are left as they were.  The accounts are per sequence, also where
+ * sequences share blocks.
  *   mass          fp32, mass_stride >= max_blocks * block_size
  *   workspace     pkv_mass_workspace_bytes bytes (it holds the step's scores: 4 n_h bytes per
  *                 token of max_blocks * block_size, so a table no wider than needed is better; 0:
@@ -460,8 +461,8 @@ pkv_status pkv_paged_decode_attn_mass(const void* q, const void* k_pool, const v
  * max_blocks * block_size is at most 0x7fff0000 (PKV_ERANGE); the work is laid out for that many
  * rows, so give a table no wider than the longest sequence needs.
  * The blocks that hold the first K rows are rewritten: they must belong to the sequence alone.
- * Nothing here can tell; pkv_bm_evict does, and is called before this (see there).  Moves from or to a block id outside the pool set PKV_DEV_BAD_BLOCK and are
- * skipped; context lengths out of range are clamped with PKV_DEV_BAD_CTX.
+ * Nothing here can tell; pkv_bm_evict does, and is called before this (see there).  Moves from or to a
+ * block id outside the pool set PKV_DEV_BAD_BLOCK and are skipped; context lengths out of range are clamped with PKV_DEV_BAD_CTX.
  */
 size_t pkv_evict_workspace_bytes(int batch, int n_kv, int block_size, int max_blocks);
 pkv_status pkv_kv_evict(void* k_pool, void* v_pool, const int32_t* block_tables, int max_blocks,

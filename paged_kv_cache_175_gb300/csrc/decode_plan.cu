@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(256, LPR == 16 ? 4 : 0) reduce_kernel(const De
   if (a.inline_plan) {
     // blocks of every sequence and their exclusive prefix: thread t takes sequence t
     const int sq = threadIdx.x;
-    const int n = sq < a.batch ? span_blocks(clamp_ctx(a.ctx_raw[sq], a.max_ctx), a.window, a.block_size) : 0;
+    // from L2: ahead of the wait a line that L1 kept from an earlier kernel may be old
+    const int n = sq < a.batch ? span_blocks(clamp_ctx(__ldcg(a.ctx_raw + sq), a.max_ctx), a.window, a.block_size) : 0;
     int incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

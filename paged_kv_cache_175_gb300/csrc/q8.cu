@@ -5,9 +5,9 @@
 // (e4m3) or 127 (int8), every operation rounded to fp32.  (Products with reciprocals are how elementary
 // torch operations on the GPU divide a tensor by a number and a number by a tensor, so the codes equal
 // theirs; divisions rounded once would be as repeatable and differ in a last place now and then.)
-// The result is a function of the rows alone, not of how many calls brought them: the bf16 rows of a sequence's unfinished block are kept in its tail
-// and the record is written anew from them at each append, so the attention reads records only
-// and a finished block was rounded once.
+// The result is a function of the rows alone, not of how many calls brought them: the bf16 rows of a
+// sequence's unfinished block are kept in its tail and the record is written anew from them at each
+// append, so the attention reads records only and a finished block was rounded once.
 //
 // What bounds it: long calls read 4 d bytes and write 2 d per token and kv head (HBM).  A decode
 // step reads the open rows and writes one record per (sequence, kv head): a few hundred KB, so
@@ -15,8 +15,9 @@
 // Split: one CTA per kv head, K or V, and span of tokens takes each run of tokens that lands in
 // one block, 64 / block_size runs side by side (64 rows in shared memory at a time).  A span is 64
 // tokens in long calls and as many tokens as there are places for runs in short ones, where every
-// token of a decode step is a run (kSpanTokens says what that costs a prompt chunk).  The runs of a span are found in one round trip; the search for a
-// sequence's end, which few runs need, goes on while the rows arrive.
+// token of a decode step is a run (kSpanTokens says what that costs a prompt chunk).  The runs of a span
+// are found in one round trip; the search for a sequence's end, which few runs need, goes on while the
+// rows arrive.
 // Measured (8 kv heads of 128): 8000 tokens of one prompt in blocks of 16 in 15.1 us (3.3 TB/s), one
 // run at a time 21.7, four CTAs per SM instead of six 17.3; 23 ragged prompts of 234-701 tokens in
 // blocks of 64 in 23.8 us (3.1 TB/s; the CTAs with two or three runs end last; asking for the next

@@ -33,3 +33,10 @@ def test_a_walk_behind_the_last_sequence_stays_on_it():
     walk = text[text.index("void cursor_next("):]
     walk = walk[:walk.index("template")]
     assert walk.count("min(c.s + 1, a.batch - 1)") == 2 and "++c.s" not in walk
+
+
+def test_the_merge_reads_lengths_ahead_of_its_wait_from_l2():
+    body = [b for n, _, b in kernels(source("decode_plan.cu")) if n == "reduce_kernel"]
+    assert len(body) == 1
+    early = body[0][:body[0].index("grid_dep_wait();")]
+    assert "__ldcg(a.ctx_raw + sq)" in early and "ctx_raw[" not in body[0]
