@@ -67,6 +67,8 @@ typedef enum {
 #define PKV_DEV_BAD_SLOT  2  /* slot >= num_blocks * block_size (or bad tail row): skipped  */
 #define PKV_DEV_BAD_CTX   4  /* context_lens[s] < 0 or > max_blocks * block_size: clamped  */
 #define PKV_DEV_TIMEOUT   8  /* a bounded wait inside a kernel gave up (about 2 s)          */
+#define PKV_DEV_BAD_TREE 16  /* q_start out of order or range, more drafted tokens than cached
+                                rows, or an accepted path that does not ascend over them     */
 
 /* Output element types of the attention calls. */
 #define PKV_OUT_BF16 0
@@ -471,6 +473,109 @@ pkv_status pkv_kv_evict(void* k_pool, void* v_pool, const int32_t* block_tables,
                         int32_t* positions_out, int32_t* kept_out, int32_t* dropped_out, int64_t stride,
                         int32_t* new_lens, int batch, int n_kv, int head_dim, int block_size, int num_blocks,
                         void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream);
+
+/*
+ * Several tokens of a sequence in one step: drafted tokens that form a chain or a tree.
+ *
+ * A step's tokens lie one sequence after another; q_start int32 [batch + 1] gives each sequence's
+ * first token, so sequence s has n = q_start[s + 1] - q_start[s] of them (0 is allowed; tokens in
+ * front of the first sequence or behind the last one belong to none, and their output rows are left
+ * as they were).  q_start NULL: every sequence has n_tok / batch tokens (n_tok a multiple of batch).
+ * Their rows are in the cache before the attention: they are its last n rows, and context_lens[s]
+ * counts them.  Token i attends to all rows before the n, and of the n to
+ *   tree_mask NULL: its own and the earlier ones (a chain)
+ *   else          : those j with bit (j & 63) of tree_mask[token * mask_words + (j >> 6)] set (its
+ *                   ancestors and itself, for a tree); rows past 64 * mask_words are not attended.
+ * A token with nothing to attend to gets a zero output row; so do the tokens of a sequence of
+ * context length 0.  Where 0 < context_lens[s] < n the first n - context_lens[s] tokens' rows are taken
+ * as missing, with PKV_DEV_BAD_TREE.  A range of q_start that is out of order or outside [0, n_tok] gives
+ * its sequence no tokens, with PKV_DEV_BAD_TREE.
+ *
+ * paged_tree_attn — pkv_paged_decode_attn for such tokens.
+ *   q             bf16 [n_tok][n_h][head_dim]
+ *   q_start       int32 [batch + 1] or NULL
+ *   tree_mask     int64 [n_tok][mask_words] or NULL (mask_words is ignored then)
+ *   out           [n_tok][n_h][head_dim]; must not overlap the other arguments
+ *   workspace     pkv_tree_workspace_bytes bytes (0: invalid shape), 256-byte aligned; a call of other
+ *                 n_tok or batch may need another size
+ * Arithmetic as for pkv_paged_decode_attn.  Cached rows that no token of the sequence attends to do not
+ * reach any output, whatever they hold; a row that some of its tokens attend to and others mask has to
+ * hold finite values (0 times an infinity of V is no number).  Pools, tables, lengths, scale, other
+ * errors and the first call of a shape as for pkv_paged_decode_attn; max_blocks * block_size is at most
+ * 0x7fff0000 and n_tok * n_h at most 0x7fffffff (PKV_ERANGE).
+ */
+size_t pkv_tree_workspace_bytes(int batch, int n_tok, int n_h, int n_kv, int head_dim, int block_size);
+pkv_status pkv_paged_tree_attn(const void* q, const void* k_pool, const void* v_pool, const int32_t* block_tables,
+                               int max_blocks, const int32_t* context_lens, const int32_t* q_start,
+                               const int64_t* tree_mask, int mask_words, float scale, int n_tok, int batch, int n_h,
+                               int n_kv, int head_dim, int block_size, int num_blocks, void* out, int out_dtype,
+                               void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream);
+
+/*
+ * kv_tree_accept — keep the accepted path of each sequence's drafted tokens: for i < n_accept[s] the
+ * cache row of drafted token path[s][i] becomes row base + i, base = context_lens[s] - n, in every given
+ * cache; the rows behind are no longer part of the sequence.  (The drafted keys were rotated by their
+ * depth in the tree, which is where an accepted path puts them.)
+ *   caches        HOST array of n_caches device pointers to caches of one shape,
+ *                 [num_blocks][heads][block_size][row_bytes]: the K and V pools of every layer, or the latent
+ *                 caches (heads = 1).  They must not overlap.  row_bytes is a multiple of 16
+ *   q_start, n_tok, batch as above
+ *   path          int32 [batch][path_stride]: drafted tokens in ascending order (a tree lists parents before
+ *                 children), at least n_accept[s] of them
+ *   n_accept      int32 [batch], 0 .. min(n, path_stride)
+ *   new_lens      int32 [batch]: base + n_accept[s]; must not overlap context_lens, n_accept, path or q_start
+ * An entry that is not larger than the one before it, or not below n, ends the path there, with
+ * PKV_DEV_BAD_TREE (so does n_accept out of range, which is clamped); a sequence with more drafted tokens than
+ * rows keeps its length, with the same flag.  The blocks that hold the drafted rows must belong to the sequence alone.  A
+ * move from or to a block id outside the pool sets PKV_DEV_BAD_BLOCK and is skipped.
+ */
+pkv_status pkv_kv_tree_accept(void* const* caches, int n_caches, int row_bytes, int heads, const int32_t* block_tables,
+                              int max_blocks, const int32_t* context_lens, const int32_t* q_start, int n_tok,
+                              const int32_t* path, int path_stride, const int32_t* n_accept, int32_t* new_lens, int batch,
+                              int block_size, int num_blocks, int32_t* err_flag, void* stream);
+
+/*
+ * The latent cache: one vector per token for all heads, bf16 [num_blocks][block_size][latent + rope]: the
+ * latent part, from which a layer's keys and values are linear maps, and a key part with rotary positions
+ * that all heads share.  With the maps taken into the query and the output projection (the absorbed form),
+ * attention runs on the vectors themselves.
+ * latent is 256 or 512, rope 32 or 64.
+ *
+ * latent_append — normalise, rotate and write a step's vectors, and rotate the queries' position part.
+ *   kv            bf16 [n_tok][latent + rope], kv_stride elements between tokens: part of a projection's output
+ *   q             bf16 [n_tok][n_h][rope], q_stride / q_head_stride elements between tokens / heads
+ *   table         of pkv_rope_init with rotary_dim = rope
+ *   weight        bf16 [latent] or NULL: x * weight / sqrt(mean(x^2) + eps) over the latent part, in
+ *                 fp32, rounded once; NULL copies it as it is
+ *   q_out         bf16 [n_tok][n_h][rope] with strides (inside the absorbed queries [n_tok][n_h][latent +
+ *                 rope], say); may be q itself, with its strides
+ *   cache         written at slot_mapping (int64 [n_tok]; negative: padding, nothing of the token is written)
+ * Strides are multiples of 8 elements, pointers 16-byte aligned.  A slot >= num_blocks * block_size sets
+ * PKV_DEV_BAD_SLOT and skips the token.  n_h is at most 1024.
+ */
+pkv_status pkv_latent_append(const void* kv, int64_t kv_stride, const void* q, int64_t q_stride, int64_t q_head_stride,
+                             const int32_t* positions, const int64_t* slot_mapping, int n_tok,
+                             const pkv_rope_table* table, const void* weight, float eps, void* q_out,
+                             int64_t q_out_stride, int64_t q_out_head_stride, void* cache, int num_blocks, int block_size,
+                             int n_h, int latent, int rope, int32_t* err_flag, void* stream);
+
+/*
+ * paged_latent_attn — attention of one or several tokens per sequence over the latent cache:
+ *   out[token][h] = sum over attended rows t of softmax_t(scale * q[token][h] . cache[t]) cache[t][:latent]
+ *   q             bf16 [n_tok][n_h][latent + rope]; n_h at most 1024
+ *   out           [n_tok][n_h][latent]
+ * q_start, tree_mask and everything else as for pkv_paged_tree_attn (one token per sequence: q_start NULL and
+ * n_tok = batch).
+ * p is carried as a bf16 high + low pair; for a bf16 output and more than 32 query rows per sequence on average
+ * (n_tok * n_h / batch) it is rounded to bf16 once (an error of at most 2^-8 sum p |v|, of the size of the output's own
+ * rounding), and the sum that divides it is that of the rounded values.
+ */
+size_t pkv_latent_workspace_bytes(int batch, int n_tok, int n_h, int latent, int rope, int block_size);
+pkv_status pkv_paged_latent_attn(const void* q, const void* cache, const int32_t* block_tables, int max_blocks,
+                                 const int32_t* context_lens, const int32_t* q_start, const int64_t* tree_mask,
+                                 int mask_words, float scale, int n_tok, int batch, int n_h, int latent, int rope,
+                                 int block_size, int num_blocks, void* out, int out_dtype, void* workspace,
+                                 size_t workspace_bytes, int32_t* err_flag, void* stream);
 
 /*
  * CacheBlend's model-free steps ("Research Paper Review : CACHE BLEND ...", sections

@@ -11,7 +11,8 @@ Functions (same names as the C entry points without the ``pkv_`` prefix):
 ``paged_decode_attn_int4_window``, ``rope_shift_k``, ``copy_blocks``, ``kv_deviation``,
 ``select_top``, ``kv_fuse``, ``recompute_ratio``, ``select_count``, ``probe_read``,
 ``probe_copy``, ``layer_window`` (as ``layer_windows``), ``rope_append``, ``rope_qk``,
-``kv_quant_append_q8``, ``paged_decode_attn_q8``, ``paged_decode_attn_mass``, ``kv_evict``, plus
+``kv_quant_append_q8``, ``paged_decode_attn_q8``, ``paged_decode_attn_mass``, ``kv_evict``,
+``paged_tree_attn``, ``kv_tree_accept``, ``latent_append``, ``paged_latent_attn``, plus
 ``rope_table`` (``pkv_rope_init``), ``decode_workspace_bytes`` and the other ``*_workspace_bytes``,
 ``alloc_int4_cache``, ``alloc_q8_cache``, ``alloc_evict_state`` and ``BlockManager`` (the ``pkv_bm_*`` calls of
 include/pkv_bm.h).
@@ -30,7 +31,7 @@ from ._build import CALLS as CALLS_PATH, LIB as LIB_PATH, build_library, calls_c
 
 PKV_OUT_BF16 = 0
 PKV_OUT_F32 = 1
-DEV_BAD_BLOCK, DEV_BAD_SLOT, DEV_BAD_CTX, DEV_TIMEOUT = 1, 2, 4, 8
+DEV_BAD_BLOCK, DEV_BAD_SLOT, DEV_BAD_CTX, DEV_TIMEOUT, DEV_BAD_TREE = 1, 2, 4, 8, 16
 
 _lib = None
 
@@ -70,6 +71,16 @@ _SIGS = {
     "pkv_evict_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
     "pkv_kv_evict": (_I, [_P, _P, _P, _I, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _L, _P, _I, _I, _I, _I, _I,
                           _P, ctypes.c_size_t, _P, _P]),
+    # drafted tokens and the latent cache
+    "pkv_tree_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I]),
+    "pkv_paged_tree_attn": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _I, ctypes.c_float, _I, _I, _I, _I, _I, _I, _I,
+                                 _P, _I, _P, ctypes.c_size_t, _P, _P]),
+    "pkv_kv_tree_accept": (_I, [_P, _I, _I, _I, _P, _I, _P, _P, _I, _P, _I, _P, _P, _I, _I, _I, _P, _P]),
+    "pkv_latent_append": (_I, [_P, _L, _P, _L, _L, _P, _P, _I, _P, _P, ctypes.c_float, _P, _L, _L, _P, _I, _I, _I, _I, _I,
+                               _P, _P]),
+    "pkv_latent_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I]),
+    "pkv_paged_latent_attn": (_I, [_P, _P, _P, _I, _P, _P, _P, _I, ctypes.c_float, _I, _I, _I, _I, _I, _I, _I,
+                                   _P, _I, _P, ctypes.c_size_t, _P, _P]),
     # block manager (host) and its copy executor
     "pkv_bm_create": (_P, [_I, _I, _I, _I, _I]),
     "pkv_bm_destroy": (None, [_P]),
@@ -772,6 +783,167 @@ def kv_evict(k_pool, v_pool, block_tables, context_lens, keep, recent, state: Ev
                dst.mass, dst.positions, dst.kept, dst.dropped, new_lens, workspace)
     if st:
         _failed("kv_evict", st)
+    return new_lens
+
+
+# ---------------------------------------------------------------------------------------------
+# Drafted tokens (several per sequence and step) and the latent cache (pkv.h).
+def _step_refuse(q, block_tables, context_lens, q_start, tree_mask, out, workspace, err, w, v):
+    T, n_h, _ = _dims("q", q, 3)
+    B, _ = _dims("block_tables", block_tables, 2)
+    _on_current(q, block_tables, context_lens, q_start, tree_mask, out, workspace, err)
+    _typed(_bf16, q)
+    _typed(_i32, block_tables, context_lens, err)
+    _out_type(out.dtype)
+    _shaped("q", q, T, n_h, w)
+    _shaped("context_lens", context_lens, B)
+    _shaped("out", out, T, n_h, v)
+    if q_start is not None:
+        _typed(_i32, q_start)
+        _shaped("q_start", q_start, B + 1)
+    elif B and T % B:
+        raise PkvError(f"without q_start the {T} tokens must be a multiple of the {B} sequences")
+    if tree_mask is not None:
+        _typed(_i64, tree_mask)
+        _shaped("tree_mask", tree_mask, T, _dims("tree_mask", tree_mask, 2)[1])
+    _dense(q, block_tables, context_lens, q_start, tree_mask, out, workspace)
+
+
+def tree_workspace_bytes(batch, n_tok, n_h, n_kv, head_dim, block_size) -> int:
+    """Bytes of workspace paged_tree_attn needs for this shape on the current device."""
+    n = lib().pkv_tree_workspace_bytes(batch, n_tok, n_h, n_kv, head_dim, block_size)
+    if n == 0:
+        raise PkvError("tree_workspace_bytes: invalid shape or no device")
+    return n
+
+
+def paged_tree_attn(q, k_pool, v_pool, block_tables, context_lens, scale, q_start=None, tree_mask=None, out=None,
+                    out_dtype=torch.bfloat16, workspace=None, err=None, stream=None):
+    """Attention of several (drafted) tokens per sequence, q [n_tok][n_h][d], over a paged bf16 cache that holds
+    their rows already, as each sequence's last ones (context_lens counts them).  q_start (int32 [B + 1]): each
+    sequence's first token; None: n_tok / B tokens each.  tree_mask (int64 [n_tok][words]): bit j of a token's
+    words says whether it attends to token j of its sequence; None: to the earlier ones and itself."""
+    if out is None:
+        out = _empty(q.shape, _out_type(out_dtype), q.device, stream)
+    if workspace is None and q.is_cuda and q.shape[0]:
+        T, n_h, d = _dims("q", q, 3)
+        _, n_kv, bs, _ = _dims("k_pool", k_pool, 4)
+        workspace = _scratch(lib().pkv_tree_workspace_bytes(block_tables.shape[0], T, n_h, n_kv, d, bs), q.device, stream)
+    st = (_calls or _native()).paged_tree_attn(q, k_pool, v_pool, block_tables, context_lens, scale, q_start, tree_mask, out,
+                                               workspace, err, None if stream is None else stream.cuda_stream)
+    if st == _NOT_TAKEN:
+        nb, n_kv, bs, d = _dims("k_pool", k_pool, 4)
+        _on_current(q, k_pool, v_pool)
+        _typed(_bf16, k_pool, v_pool)
+        _shaped("v_pool", v_pool, nb, n_kv, bs, d)
+        _dense(k_pool, v_pool)
+        _step_refuse(q, block_tables, context_lens, q_start, tree_mask, out, workspace, err, d, d)
+    if st:
+        _failed("paged_tree_attn", st)
+    return out
+
+
+def latent_workspace_bytes(batch, n_tok, n_h, latent, rope, block_size) -> int:
+    """Bytes of workspace paged_latent_attn needs for this shape on the current device."""
+    n = lib().pkv_latent_workspace_bytes(batch, n_tok, n_h, latent, rope, block_size)
+    if n == 0:
+        raise PkvError("latent_workspace_bytes: invalid shape or no device")
+    return n
+
+
+def paged_latent_attn(q, cache, latent, block_tables, context_lens, scale, q_start=None, tree_mask=None, out=None,
+                      out_dtype=torch.bfloat16, workspace=None, err=None, stream=None):
+    """Attention over the latent cache [num_blocks][block_size][latent + rope] with absorbed queries
+    q [n_tok][n_h][latent + rope]; returns [n_tok][n_h][latent], the weighted sums of the latent parts.  One token
+    per sequence, or several as for paged_tree_attn."""
+    latent = int(latent)
+    if out is None:
+        out = _empty((*q.shape[:2], latent), _out_type(out_dtype), q.device, stream)
+    if workspace is None and q.is_cuda and q.shape[0]:
+        T, n_h, w = _dims("q", q, 3)
+        bs = _dims("cache", cache, 3)[1]
+        workspace = _scratch(lib().pkv_latent_workspace_bytes(block_tables.shape[0], T, n_h, latent, w - latent, bs), q.device, stream)
+    st = (_calls or _native()).paged_latent_attn(q, cache, latent, block_tables, context_lens, scale, q_start, tree_mask, out,
+                                                 workspace, err, None if stream is None else stream.cuda_stream)
+    if st == _NOT_TAKEN:
+        w = _dims("cache", cache, 3)[2]
+        _on_current(q, cache)
+        _typed(_bf16, cache)
+        _dense(cache)
+        _step_refuse(q, block_tables, context_lens, q_start, tree_mask, out, workspace, err, w, latent)
+    if st:
+        _failed("paged_latent_attn", st)
+    return out
+
+
+def _last_dense(t):
+    if t.numel() and t.stride(-1) != 1:
+        raise PkvError("the last dimension must be contiguous")
+
+
+def latent_append(kv, q, positions, slot_mapping, table: RopeTable, cache, q_out=None, weight=None, eps=1e-6, err=None,
+                  stream=None):
+    """Append a step's vectors kv [n_tok][latent + rope] to the latent cache: the latent part normalised by its root
+    mean square and scaled by weight (bf16 [latent]; None: as it is), the key part rotated by positions.  Rotates the
+    position part of the queries, q [n_tok][n_h][rope], too, into q_out (a part of the absorbed queries, say; q
+    itself is allowed), and returns it.  Tokens and heads may be strided.  table: of rope_table with rotary_dim = rope."""
+    _table_type(table)
+    if q_out is None:
+        q_out = _empty(q.shape, q.dtype, q.device, stream)
+    st = (_calls or _native()).latent_append(kv, q, positions, slot_mapping, table, cache, q_out, weight, eps, err,
+                                             None if stream is None else stream.cuda_stream)
+    if st == _NOT_TAKEN:
+        n, n_h, rope = _dims("q", q, 3)
+        w = _dims("cache", cache, 3)[2]
+        _on_current(kv, q, positions, slot_mapping, cache, q_out, weight, err)
+        _typed(_bf16, kv, q, cache, q_out, weight)
+        _typed(_i32, positions, err)
+        _typed(_i64, slot_mapping)
+        _shaped("kv", kv, n, w)
+        _shaped("positions", positions, n)
+        _shaped("slot_mapping", slot_mapping, n)
+        _shaped("q_out", q_out, n, n_h, rope)
+        _shaped("weight", weight, w - rope)
+        _dense(positions, slot_mapping, cache, weight)
+        for t in (kv, q, q_out):
+            _last_dense(t)
+    if st:
+        _failed("latent_append", st)
+    return q_out
+
+
+def kv_tree_accept(caches, block_tables, context_lens, q_start, path, n_accept, n_tok=None, new_lens=None, err=None,
+                   stream=None):
+    """Keep the accepted path of each sequence's drafted tokens, in every cache of the list (the K and V pools of all
+    layers, or their latent caches; one shape): row base + path[s][i] becomes row base + i for i < n_accept[s], base
+    being the rows in front of the drafted ones.  path (int32 [B][P]) ascends.  q_start as for the attention (None:
+    n_tok / B tokens each).  Returns the new context lengths, base + n_accept (a tensor of its own)."""
+    caches = list(caches)
+    if new_lens is None:
+        new_lens = _empty(context_lens.shape, _i32, context_lens.device, stream)
+    if q_start is None and n_tok is None:
+        raise PkvError("without q_start the number of tokens must be given")
+    n = 0x7fffffff if n_tok is None else int(n_tok)              # with q_start: what its entries are checked against
+    st = (_calls or _native()).kv_tree_accept(caches, block_tables, context_lens, q_start, path, n_accept, new_lens, n, err,
+                                              None if stream is None else stream.cuda_stream)
+    if st == _NOT_TAKEN:
+        B, _ = _dims("block_tables", block_tables, 2)
+        P = _dims("path", path, 2)[1]
+        if not caches or caches[0].dim() not in (3, 4):
+            raise PkvError("caches must be tensors [num_blocks][heads][block_size][d] or [num_blocks][block_size][width]")
+        _on_current(block_tables, context_lens, q_start, path, n_accept, new_lens, err, *caches)
+        _typed(_bf16, *caches)
+        _typed(_i32, block_tables, context_lens, q_start, path, n_accept, new_lens, err)
+        for c in caches:
+            _shaped("each cache", c, *caches[0].shape)
+        _shaped("context_lens", context_lens, B)
+        _shaped("n_accept", n_accept, B)
+        _shaped("new_lens", new_lens, B)
+        _shaped("q_start", q_start, B + 1)
+        _shaped("path", path, B, P)
+        _dense(block_tables, context_lens, q_start, path, n_accept, new_lens, *caches)
+    if st:
+        _failed("kv_tree_accept", st)
     return new_lens
 
 

@@ -16,8 +16,9 @@ LIB = os.path.join(PKG, "libpkv.so")
 CALLS = os.path.join(PKG, "_calls.so")
 CALLS_KEY = os.path.join(OBJ, "calls.key")             # what CALLS was built for
 SOURCES = ["decode_plan.cu", "decode_bf16.cu", "decode_tc.cu", "int4.cu", "append_rope.cu", "rope_append.cu",
-           "q8.cu", "decode_q8.cu", "decode_mass.cu", "evict.cu", "offload.cu", "cacheblend.cu", "probe.cu", "block_manager.cpp"]
-HEADERS = ["pkv_device.cuh", "decode_common.cuh", "nvtx_range.h", "umma.cuh", "q8_common.cuh", "piece_streams.cuh", "stream_plan.cuh"]
+           "q8.cu", "decode_q8.cu", "decode_mass.cu", "evict.cu", "decode_rows.cu", "latent_append.cu",
+           "tree_accept.cu", "offload.cu", "cacheblend.cu", "probe.cu", "block_manager.cpp"]
+HEADERS = ["pkv_device.cuh", "decode_common.cuh", "nvtx_range.h", "umma.cuh", "q8_common.cuh", "piece_streams.cuh", "stream_plan.cuh", "drafts.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 

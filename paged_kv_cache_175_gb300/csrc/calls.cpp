@@ -14,6 +14,7 @@
 
 #include <cstring>
 #include <initializer_list>
+#include <vector>
 
 #include "../../include/pkv.h"
 
@@ -325,6 +326,162 @@ PyObject* kv_evict(PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
+// An optional tensor: null for None.
+const at::Tensor* optional(Args& x, int i, at::ScalarType type, std::initializer_list<int64_t> shape) {
+  return x.ok && x.a[i] != Py_None ? &x.dense(i, type, shape) : nullptr;
+}
+
+// What the calls for drafted tokens share: q_start and tree_mask (None for none), tables, lengths, output, workspace.
+struct Rows {
+  const at::Tensor *start = nullptr, *mask = nullptr, *bt = nullptr, *ctx = nullptr, *out = nullptr;
+  int64_t T = 0, n_h = 0, B = 0, mb = 0, words = 0;
+  int out_type = PKV_OUT_BF16;
+  void* ws = nullptr;
+  size_t ws_bytes = 0;
+  Rows(Args& x, const at::Tensor& q, int ibt, int ictx, int istart, int imask, int iout, int64_t w, int64_t v) {
+    if (!x.ok || q.dim() != 3) {
+      x.ok = false;
+      return;
+    }
+    T = q.size(0), n_h = q.size(1);
+    if (x.shaped(q, {T, n_h, w})) x.ok = q.is_contiguous();
+    bt = &x.dense(ibt, I32, 2);
+    if (!x.ok) return;
+    B = bt->size(0), mb = bt->size(1);
+    ctx = &x.dense(ictx, I32, {B});
+    start = optional(x, istart, I32, {B + 1});
+    if (x.ok && x.a[imask] != Py_None) {
+      mask = &x.dense(imask, I64, 2);
+      if (x.ok) words = mask->size(1), x.shaped(*mask, {T, words});
+      if (x.ok) x.ok = words > 0 || T == 0;
+    }
+    out = &x.any(iout, BF16, F32);
+    if (x.shaped(*out, {T, n_h, v})) x.ok = out->is_contiguous();
+    workspace(x, iout + 1, ws, ws_bytes);
+    x.sizes(T, n_h, B, mb, words);
+    if (x.ok && out->scalar_type() == F32) out_type = PKV_OUT_F32;
+  }
+  const int32_t* starts() const { return start ? ints(*start) : nullptr; }
+  const int64_t* bits() const { return mask && words > 0 ? mask->data_ptr<int64_t>() : nullptr; }
+};
+
+// q, k_pool, v_pool, block_tables, context_lens, scale, q_start, tree_mask, out, workspace, err, stream
+PyObject* paged_tree_attn(PyObject* const* a, Py_ssize_t n_args) {
+  if (n_args != 12) return result(kNotTaken);
+  Args x(a);
+  const at::Tensor &q = x.any(0, BF16), &kp = x.dense(1, BF16, 4);
+  if (!x.ok) return result(kNotTaken);
+  const int64_t nb = kp.size(0), n_kv = kp.size(1), bs = kp.size(2), d = kp.size(3);
+  const at::Tensor& vp = x.dense(2, BF16, {nb, n_kv, bs, d});
+  const Rows t(x, q, 3, 4, 6, 7, 8, d, d);
+  const float scale = x.number(5);
+  int32_t* err = x.err(10);
+  void* stream = x.stream(11);
+  x.sizes(nb, n_kv, bs, d);
+  if (!x.ok) return result(kNotTaken);
+  return unlocked([&] {
+    return pkv_paged_tree_attn(q.data_ptr(), kp.data_ptr(), vp.data_ptr(), ints(*t.bt), (int)t.mb, ints(*t.ctx), t.starts(), t.bits(),
+                               (int)t.words, scale, (int)t.T, (int)t.B, (int)t.n_h, (int)n_kv, (int)d, (int)bs, (int)nb,
+                               t.out->data_ptr(), t.out_type, t.ws, t.ws_bytes, err, stream);
+  });
+}
+
+// q, cache, latent, block_tables, context_lens, scale, q_start, tree_mask, out, workspace, err, stream
+PyObject* paged_latent_attn(PyObject* const* a, Py_ssize_t n_args) {
+  if (n_args != 12) return result(kNotTaken);
+  Args x(a);
+  const at::Tensor &q = x.any(0, BF16), &cache = x.dense(1, BF16, 3);
+  const int latent = x.integer(2);
+  if (!x.ok) return result(kNotTaken);
+  const int64_t nb = cache.size(0), bs = cache.size(1), w = cache.size(2);
+  const Rows t(x, q, 3, 4, 6, 7, 8, w, latent);
+  const float scale = x.number(5);
+  int32_t* err = x.err(10);
+  void* stream = x.stream(11);
+  x.sizes(nb, bs, w, w - latent);
+  if (!x.ok) return result(kNotTaken);
+  return unlocked([&] {
+    return pkv_paged_latent_attn(q.data_ptr(), cache.data_ptr(), ints(*t.bt), (int)t.mb, ints(*t.ctx), t.starts(), t.bits(),
+                                 (int)t.words, scale, (int)t.T, (int)t.B, (int)t.n_h, latent, (int)(w - latent), (int)bs, (int)nb,
+                                 t.out->data_ptr(), t.out_type, t.ws, t.ws_bytes, err, stream);
+  });
+}
+
+// [tokens][heads][d] whose last dimension alone is dense
+const at::Tensor& heads_of(Args& x, int i, int64_t n, int64_t heads, int64_t d, int64_t& stride, int64_t& head_stride) {
+  const at::Tensor& t = x.any(i, BF16);
+  if (x.shaped(t, {n, heads, d})) {
+    const auto s = t.strides();
+    x.ok = t.numel() == 0 || s[2] == 1;
+    head_stride = heads > 1 ? s[1] : d;
+    stride = n > 1 ? s[0] : (heads - 1) * head_stride + d;     // one token has no stride
+  }
+  return t;
+}
+
+// kv, q, positions, slot_mapping, table, cache, q_out, weight, eps, err, stream
+PyObject* latent_append(PyObject* const* a, Py_ssize_t n_args) {
+  if (n_args != 11) return result(kNotTaken);
+  Args x(a);
+  const at::Tensor &kv = x.any(0, BF16), &q = x.any(1, BF16), &cache = x.dense(5, BF16, 3);
+  if (!x.ok || kv.dim() != 2 || q.dim() != 3) return result(kNotTaken);
+  const int64_t n = kv.size(0), n_h = q.size(1), rope = q.size(2), nb = cache.size(0), bs = cache.size(1), w = cache.size(2);
+  int64_t sq = 0, sh = 0, so = 0, soh = 0;
+  if (x.shaped(kv, {n, w})) x.ok = kv.numel() == 0 || kv.stride(1) == 1;
+  heads_of(x, 1, n, n_h, rope, sq, sh);
+  const at::Tensor &out = heads_of(x, 6, n, n_h, rope, so, soh), &pos = x.dense(2, I32, {n}), &slots = x.dense(3, I64, {n});
+  const pkv_rope_table table = x.table(4);
+  const at::Tensor* weight = optional(x, 7, BF16, {w - rope});
+  const float eps = x.number(8);
+  int32_t* err = x.err(9);
+  void* stream = x.stream(10);
+  x.sizes(n, n_h, rope, nb, bs, w, w - rope);
+  if (!x.ok) return result(kNotTaken);
+  const int64_t sk = n > 1 ? kv.stride(0) : w;
+  return unlocked([&] {
+    return pkv_latent_append(kv.data_ptr(), sk, q.data_ptr(), sq, sh, ints(pos), slots.data_ptr<int64_t>(), (int)n, &table,
+                             weight ? weight->data_ptr() : nullptr, eps, out.data_ptr(), so, soh, cache.data_ptr(), (int)nb, (int)bs,
+                             (int)n_h, (int)(w - rope), (int)rope, err, stream);
+  });
+}
+
+// caches (a list or tuple), block_tables, context_lens, q_start, path, n_accept, new_lens, n_tok, err, stream
+PyObject* kv_tree_accept(PyObject* const* a, Py_ssize_t n_args) {
+  if (n_args != 10) return result(kNotTaken);
+  if (!PyList_Check(a[0]) && !PyTuple_Check(a[0])) return result(kNotTaken);
+  Args x(a);
+  const at::Tensor& bt = x.dense(1, I32, 2);
+  if (!x.ok) return result(kNotTaken);
+  const int64_t B = bt.size(0), mb = bt.size(1);
+  const at::Tensor &ctx = x.dense(2, I32, {B}), &count = x.dense(5, I32, {B}), &lens = x.dense(6, I32, {B}), &path = x.dense(4, I32, 2);
+  const at::Tensor* start = optional(x, 3, I32, {B + 1});
+  if (!x.ok) return result(kNotTaken);
+  const int64_t stride = path.size(1);
+  x.shaped(path, {B, stride});
+  std::vector<void*> caches;
+  int64_t nb = 0, heads = 0, bs = 0, w = 0;
+  const Py_ssize_t n = PySequence_Fast_GET_SIZE(a[0]);
+  Args each(PySequence_Fast_ITEMS(a[0]));                      // the list's entries as arguments
+  each.dev = x.dev;
+  for (Py_ssize_t i = 0; i < n && x.ok; ++i) {
+    const at::Tensor& t = each.any((int)i, BF16);
+    if (!each.ok || !t.is_contiguous() || t.dim() < 3 || t.dim() > 4) return result(kNotTaken);
+    const int64_t h = t.dim() == 4 ? t.size(1) : 1;
+    if (i == 0) nb = t.size(0), heads = h, bs = t.size(-2), w = t.size(-1);
+    x.ok = nb == t.size(0) && heads == h && bs == t.size(-2) && w == t.size(-1);
+    caches.push_back(t.data_ptr());
+  }
+  const int n_tok = x.integer(7);
+  int32_t* err = x.err(8);
+  void* stream = x.stream(9);
+  x.sizes(B, mb, stride, nb, heads, bs, 2 * w, n);
+  if (!x.ok) return result(kNotTaken);
+  return unlocked([&] {
+    return pkv_kv_tree_accept(caches.data(), (int)n, (int)(2 * w), (int)heads, ints(bt), (int)mb, ints(ctx), start ? ints(*start) : nullptr,
+                              n_tok, ints(path), (int)stride, ints(count), ints(lens), (int)B, (int)bs, (int)nb, err, stream);
+  });
+}
+
 // No C++ exception leaves a call: one inside, before the C call, counts as "not taken".
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -346,6 +503,10 @@ PyMethodDef methods[] = {PKV_CALL(rope_append),
                          PKV_CALL(paged_decode_attn_q8),
                          PKV_CALL(paged_decode_attn_mass),
                          PKV_CALL(kv_evict),
+                         PKV_CALL(paged_tree_attn),
+                         PKV_CALL(paged_latent_attn),
+                         PKV_CALL(latent_append),
+                         PKV_CALL(kv_tree_accept),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
