@@ -322,6 +322,7 @@ bool tc_variant(int block_size, const void** fn, size_t* smem);
 int int4_pieces(int D, int BS, int G);
 void record_cuda_error(cudaError_t e);
 int encode_tensor_map_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
-                         uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0, uint32_t box1);
+                         uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0, uint32_t box1,
+                         uint32_t box2 = 1);
 
 }  // namespace pkv
