@@ -22,6 +22,7 @@
 //   warps 4-11  softmax and epilogue, in two groups of four warps that take half of the R query rows each
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "drafts.cuh"
 #include "nvtx_range.h"
@@ -38,8 +39,11 @@ struct RowsCut {
 struct RowsArgs {
   const int32_t *bt, *ctx, *q_start;
   const int64_t* mask;
-  int max_blocks, max_ctx, mask_words, n_tok, batch, n_h, n_kv, G, num_blocks, n_each;
-  int tile_rows;                 // query rows of a row tile: whole tokens of G heads; R where there is one kv head
+  int max_blocks, max_ctx, mask_words, n_tok, batch, n_h, n_kv, G, num_blocks, n_each, bs_log2;
+  // A row tile: latent cache: R of a sequence's tokens times heads, wherever that cuts a token.  K and V pools: tpt
+  // tokens of gt heads, or where a group has more than R heads one token's heads in hc parts.
+  int gt, tpt, hc;
+  int last_steps;                // 16-channel steps of a latent cache's position chunk
   int C, P;                      // members of a team, teams
   float scale_log2;
   void* out;
@@ -48,42 +52,6 @@ struct RowsArgs {
   RowsCut* cuts;                 // [P]
   float *ws_ml, *ws_o;           // [P * C][2][R][2] and [P * C][2][R][DV]
 };
-
-// KC: 64-channel chunks of a key; VT: M tiles of VM channels of a value; R: query rows; HL: parts of p (high, low)
-template <int BS_, int KC_, int VT_, int VM_, bool SHARED_, int R_, int HL_>
-struct RowsCfg {
-  static constexpr int BS = BS_, KC = KC_, VT = VT_, VM = VM_, R = R_, HL = HL_;
-  static constexpr bool SHARED = SHARED_;
-  static constexpr int TT = SHARED ? 64 : 128;                // cached rows of a tile
-  static constexpr int MT = TT / 64;
-  static constexpr int NBT = TT / BS;
-  static constexpr int DV = VT * VM, VC = DV / 64;
-  static constexpr int CHUNK = TT * 128;
-  static constexpr int KST = KC * CHUNK, VST = SHARED ? 0 : VC * CHUNK;
-  static constexpr int N2 = R * HL;                           // columns of the second product
-  static constexpr int QCH = R * 128, QBUF = KC * QCH;
-  static constexpr int PAT = (N2 + 63) / 64, PBUF = PAT * CHUNK;
-  // stages and buffers, from what 227 KB hold
-  static constexpr int NQ = SHARED && R == 64 ? 1 : 2;
-  static constexpr int NP = SHARED && R >= 32 ? 1 : (SHARED ? 2 : (R == 64 ? 1 : 2));
-  static constexpr int NK = 2 * (SHARED ? (KC <= 5 ? 2 : 1) : (KC == 1 ? 2 : 1));
-  static constexpr int NV = SHARED ? 0 : (KC == 1 ? 6 : (R == 64 ? 3 : 3));
-  static constexpr int NO = VT * N2 * 2 + 2 * R <= 512 ? 2 : 1;
-  static constexpr int NCOL = VT * N2 * NO + 2 * R;
-  static constexpr uint32_t TMEM_COLS = NCOL <= 64 ? 64 : (NCOL <= 128 ? 128 : (NCOL <= 256 ? 256 : 512));
-  static constexpr int S_COL = VT * N2 * NO;                  // S buffers behind the O buffers
-  static constexpr int V_OFF = NK * KST, Q_OFF = V_OFF + NV * VST, P_OFF = Q_OFF + NQ * QBUF, M_OFF = P_OFF + NP * PBUF;
-};
-
-struct RowsMeta {
-  int flags, k;                  // F_ flags; number of the segment in the piece
-  int tile0, ctx, n, q0;         // first cached row of the tile; the sequence
-  int row0, g;                   // first query row of the row tile (of the n * G or n * n_h ones), kv head
-  int invalid, part;             // blocks of the tile with a bad id; partial state of a cut segment
-};
-
-enum : int { RB_KFULL = 0, RB_KEMPTY = 4, RB_VFULL = 8, RB_VEMPTY = 14, RB_QFULL = 20, RB_QEMPTY = 22, RB_SFULL = 24, RB_SEMPTY = 26,
-             RB_PFULL = 28, RB_PEMPTY = 30, RB_OFULL = 32, RB_OEMPTY = 34, RB_DRAIN = 36, RB_DRAIN_PV = 37, RB_COUNT = 38 };
 
 // Where a CTA stands on the line.
 struct RowsCursor {
@@ -94,35 +62,109 @@ struct RowsCursor {
   long long left;                // tiles of the piece from here on (this one included)
 };
 
+// KC: 64-channel chunks of a key; VT: M tiles of VM channels of a value; R: query rows; HL: bf16 parts of p.
+// PP: the two softmax groups take alternate tiles, each with an O accumulator of its own; else both take every tile,
+// half of the query rows each (a latent cache's O leaves no room in tensor memory for a second one).
+template <int KC_, int VT_, int VM_, bool SHARED_, int R_, int HL_>
+struct RowsCfg {
+  static constexpr int KC = KC_, VT = VT_, VM = VM_, R = R_, HL = HL_;
+  static constexpr bool SHARED = SHARED_, PP = !SHARED;
+  static constexpr int TT = SHARED ? 64 : 128;                // cached rows of a tile
+  static constexpr int MT = TT / 64;
+  static constexpr int DV = VT * VM, VC = DV / 64;
+  static constexpr int CHUNK = TT * 128;
+  static constexpr int N2 = R * HL;                           // columns of the second product
+  static constexpr int QCH = R * 128, QBUF = KC * QCH;
+  static constexpr int PAT = (N2 + 63) / 64, PBUF = PAT * CHUNK;
+  // Rings, from what 227 KB hold.  K and V pools: NK stages of a tile's keys and its values.  Latent cache: NK slots of two
+  // chunks, which the second product frees one after another, and NP slots of the position chunk.  The tile's P takes
+  // the place of its keys (of their position chunk), which the first product is the only one to read.
+  static constexpr bool FULL = SHARED && KC == 9 && R == 64;  // 72 KB of query rows
+  static constexpr int KPART = KC * CHUNK > PBUF ? KC * CHUNK : PBUF;
+  static constexpr int KST = SHARED ? 2 * CHUNK : KPART + VC * CHUNK;
+  static constexpr int PST = SHARED ? PBUF : KST;
+  static constexpr int NQ = SHARED && (KC == 9 ? R > 16 : R == 64) ? 1 : 2;
+  static constexpr int NK = SHARED ? (FULL || PAT > 1 ? 8 : 9) : (KC == 1 ? 4 : 3);
+  static constexpr int NP = SHARED ? 3 : NK;                  // tiles whose P there is room for
+  static constexpr int NM = SHARED ? (KC == 9 ? 4 : 8) : NK;  // metadata of tiles: of all that the ring may hold a part of
+  static constexpr int NS = PP ? 4 : 2, NG = PP ? 2 : 1;      // S buffers; accumulators of a segment
+  static constexpr int NO = VT * N2 * NG * 2 + NS * R <= 512 && !(PP && R == 64) ? 2 : 1;
+  static constexpr int S_COL = VT * N2 * NG * NO, NCOL = S_COL + NS * R;
+  static constexpr uint32_t TMEM_COLS = NCOL <= 64 ? 64 : (NCOL <= 128 ? 128 : (NCOL <= 256 ? 256 : 512));
+  static constexpr int P_OFF = SHARED ? NK * KST : 0, Q_OFF = NK * KST + (SHARED ? NP * PST : 0), M_OFF = Q_OFF + NQ * QBUF;
+  static constexpr bool F32 = HL == 3;                        // output type
+};
+
+struct RowsMeta {
+  int flags, k;                  // F_ and G_ flags; number of the segment in the piece
+  int tile0, ctx, n, q0;         // first cached row of the tile; the sequence
+  int t0, h0, g;                 // first token of the row tile and its first head of the group; kv head
+  int invalid, part;             // blocks of the tile with a bad id; partial state of a cut segment
+};
+// Exponents (base 2) up to this are taken against an offset as it is: p is held in bf16 and fp32, whose range is 2^127, and
+// is as exact at 2^32 as at 1; what an offset this far below the maximum takes from the other end, 2^-94, is nothing.
+constexpr float kRowsLazy = 32.f;
+// For a softmax group: its first and its last tile of the segment, the piece's last one for it, and a segment of one tile.
+enum : int { G_FIRST = 64, G_LAST = 128, G_END = 256, G_SOLO = 512 };
+
 template <class X>
 struct RowsShared {
-  static constexpr int R = X::R;
-  RowsMeta kmeta[X::NK], vmeta[X::NV > 0 ? X::NV : 1];
-  uint64_t bar[RB_COUNT];
+  // Slots of keys (stages), of position chunks or values, P by its slot; the products of P by the tile's parity
+  uint64_t kfull[X::NK], kempty[X::NK], vfull[X::NP], pfull[X::NP], pslot[X::NP], pempty[2], qfull[2], qempty[2], sfull[X::NS], sempty[X::NS],
+      ofull[2], oempty[2], joined[2], drain, drain_pv;
+  RowsMeta meta[X::NM];          // of tile i: entry i % NM
   uint32_t tmem;
   int any;
   volatile int abort_flag;
-  RowsCursor cur;
-  union {
-    long long scan[12];                                       // of the setup
-    float red[4 * R];                                         // each warp's part of a query row's maximum or sum
-  };
-  float factor[R];                                            // of each query row: of a rescale, then of the output
-  // Attended rows of a tile, by each query row and by any; at a segment's end, behind the vote of the group whose
-  // query row c is, win[c] holds its final offset and its output row instead.
-  unsigned long long win[X::MT * R], seen[2];
-  __device__ float& offset(int c) { return reinterpret_cast<float*>(win + c)[0]; }
-  __device__ int& row(int c) { return reinterpret_cast<int*>(win + c)[1]; }
+  volatile int bad[2][2];                                     // of each group of waiting warps, by the parity of its barriers
+  RowsCursor cur, first;         // the member's first tile; the piece's
+  long long W;
+  // Of a segment's end, by its O buffer: offset and sum of each query row in a group's tiles, factors of the output (of
+  // either accumulator), and output rows.  (P's slot is given back with the last product.)
+  float2 state[X::NO][X::NG][X::R], factor[X::NO][X::R];
+  int row[X::NO][X::R];
+  long long scan[12];
+};
+// What the warps of a tile share for a moment, in its P buffer while that holds no weights.
+template <class X>
+struct RowsScratch {
+  float red[4][X::R];                                         // each warp's part of a query row's maximum or sum
+  float offset[X::R];
+  float factor[X::R];                                         // of a rescale
+  unsigned long long win[X::MT][X::R], seen[X::MT][4];        // cached rows attended to, by each query row and by any of a warp's
 };
 
-__device__ __forceinline__ int row_tiles(const RowsArgs& a, int n) { return (int)(((long long)n * a.G + a.tile_rows - 1) / a.tile_rows); }
-__device__ __forceinline__ long long line_length(const RowsArgs& a, const Drafts& d, int tt) {
-  const int rt = row_tiles(a, d.n);
+// Quotient of numbers that are hardly ever beyond 32 bits, where a division takes a third of the time.
+__device__ __forceinline__ long long div_pos(long long x, long long y) {
+  return (x | y) >> 32 ? x / y : (long long)((unsigned)x / (unsigned)y);
+}
+// Piece p of a line of W tiles in P pieces starts here: the first W % P pieces are one tile longer.
+struct RowsLine {
+  long long W, each, longer;
+  int P;
+  __device__ __forceinline__ RowsLine(long long w, int most) : W(w), P((int)(w < most ? w : most)) {
+    each = P ? div_pos(W, P) : 0;
+    longer = W - each * P;
+  }
+  __device__ __forceinline__ long long start(int p) const { return p * each + (p < longer ? p : longer); }
+  __device__ __forceinline__ int piece(long long pos) const {
+    const long long head = longer * (each + 1);
+    return (int)(pos < head ? div_pos(pos, each + 1) : longer + div_pos(pos - head, each));
+  }
+};
+template <class X>
+__device__ __forceinline__ int row_tiles(const RowsArgs& a, int n) {
+  return X::SHARED ? (int)(((long long)n * a.G + X::R - 1) / X::R) : (n + a.tpt - 1) / a.tpt * a.hc;
+}
+template <class X>
+__device__ __forceinline__ long long line_length(const RowsArgs& a, const Drafts& d) {
+  constexpr int tt = X::TT;
+  const int rt = row_tiles<X>(a, d.n);
   return (long long)a.n_kv * ((rt + a.C - 1) / a.C) * ((d.ctx + tt - 1) / tt);
 }
 
 // Moves to the next tile of this member (false: the piece has none left).  Row tiles past the last one are passed over.
-template <int TT>
+template <class X>
 __device__ __forceinline__ bool rows_settle(RowsCursor& c, const RowsArgs& a, int member) {
   while (c.left > 0) {
     if (c.t >= c.nt) {
@@ -137,8 +179,8 @@ __device__ __forceinline__ bool rows_settle(RowsCursor& c, const RowsArgs& a, in
           do {
             if (++c.s >= a.batch) return false;
             c.d = drafts_of(a.ctx, a.q_start, a.n_each, a.n_tok, a.max_ctx, c.s, flags);
-            c.nt = (c.d.ctx + TT - 1) / TT;
-            c.rt = row_tiles(a, c.d.n);
+            c.nt = (c.d.ctx + X::TT - 1) / X::TT;
+            c.rt = row_tiles<X>(a, c.d.n);
           } while (c.nt == 0 || c.rt == 0);
         }
       }
@@ -152,11 +194,31 @@ __device__ __forceinline__ bool rows_settle(RowsCursor& c, const RowsArgs& a, in
 
 __device__ __forceinline__ float sum_inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }   // a sum that is no number stays one
 
-// Output row of column c of a row tile (-1: none): rows are tokens times the group's heads.
-__device__ __forceinline__ long long out_row(const RowsArgs& a, int q0, int n, int g, int row0, int c) {
-  const int r = row0 + c;
-  if (c >= a.tile_rows || r >= n * a.G) return -1;
-  return (long long)(q0 + r / a.G) * a.n_h + g * a.G + r % a.G;
+// Token (of its sequence, -1: none) and head of the group of query row c of a row tile.
+template <class X>
+__device__ __forceinline__ int2 query_of(const RowsArgs& a, int n, int t0, int h0, int c) {
+  int t, h;
+  if constexpr (X::SHARED) {
+    const int r = h0 + c;                                     // the tile may begin inside a token
+    t = t0 + r / a.G;
+    h = r % a.G;
+  } else {
+    t = t0 + c / a.gt;
+    h = h0 + c % a.gt;
+    if (c >= a.gt * a.tpt) t = n;
+  }
+  return make_int2(t < n && h < a.G ? t : -1, h);
+}
+template <class X>
+__device__ __forceinline__ void tile_of(const RowsArgs& a, int rt, int& t0, int& h0) {
+  if constexpr (X::SHARED) {
+    const long long r = (long long)rt * X::R;
+    t0 = (int)(r / a.G);
+    h0 = (int)(r - (long long)t0 * a.G);
+  } else {
+    t0 = rt / a.hc * a.tpt;
+    h0 = rt % a.hc * a.gt;
+  }
 }
 __device__ __forceinline__ void store_out(const RowsArgs& a, long long at, float v) {
   if (a.out_f32) reinterpret_cast<float*>(a.out)[at] = v;
@@ -188,13 +250,11 @@ template <class X>
 __global__ void __launch_bounds__(384, 1)
     decode_rows_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                        const __grid_constant__ CUtensorMap tmq, const __grid_constant__ RowsArgs a) {
-  constexpr int TT = X::TT, BS = X::BS, R = X::R, HL = X::HL, N2 = X::N2, KC = X::KC, VT = X::VT, MT = X::MT, DV = X::DV;
-  constexpr int NK = X::NK, NV = X::SHARED ? X::NK : X::NV;
+  constexpr int TT = X::TT, R = X::R, HL = X::HL, N2 = X::N2, KC = X::KC, VT = X::VT, MT = X::MT, DV = X::DV;
+  constexpr int NK = X::NK, NM = X::NM, NP = X::NP, NO = X::NO, NS = X::NS, NG = X::NG, NQ = X::NQ;
+  constexpr bool PP = X::PP;
   extern __shared__ __align__(1024) uint8_t sm[];
   RowsShared<X>& sh = *reinterpret_cast<RowsShared<X>*>(sm + X::M_OFF);
-  RowsMeta* vmeta = X::SHARED ? sh.kmeta : sh.vmeta;
-  uint64_t* bar = sh.bar;
-  constexpr int VFULL = X::SHARED ? RB_KFULL : RB_VFULL, VEMPTY = X::SHARED ? RB_KEMPTY : RB_VEMPTY;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int team = blockIdx.x / a.C, member = blockIdx.x % a.C;
   if (smem_u32(sm) & 1023u) {              // the descriptors and the swizzle count on it, and there is no room to align it here
@@ -205,8 +265,12 @@ __global__ void __launch_bounds__(384, 1)
   if (threadIdx.x == 0) {
     sh.abort_flag = 0;
     sh.any = 0;
-    for (int b = 0; b < RB_COUNT; ++b)
-      mbar_init(&bar[b], (b >= RB_SEMPTY && b < RB_PEMPTY) || b == RB_OEMPTY || b == RB_OEMPTY + 1 ? 8 : 1);   // one arrival per softmax warp
+    for (int j = 0; j < 4; ++j) sh.bad[j >> 1][j & 1] = 0;
+    constexpr int SW = PP ? 4 : 8;         // softmax warps of a tile
+    for (uint64_t* b = sh.kfull; b <= &sh.drain_pv; ++b) {
+      const bool softmax = (b >= sh.sempty && b < sh.sempty + NS) || (b >= sh.pfull && b < sh.pfull + NP);
+      mbar_init(b, softmax ? SW : (b >= sh.oempty && b < sh.oempty + 2 ? 8 : (b >= sh.joined && b < sh.joined + 2 ? 4 : 1)));
+    }
     fence_barrier_init();
     prefetch_tensormap(&tmk);
     if (!X::SHARED) prefetch_tensormap(&tmv);
@@ -224,7 +288,11 @@ __global__ void __launch_bounds__(384, 1)
     const int per = (a.batch + 383) / 384, s0 = threadIdx.x * per, s1 = min(s0 + per, a.batch);
     long long mine = 0;
     int flags = 0;
-    for (int s = s0; s < s1; ++s) mine += line_length(a, drafts_of(a.ctx, a.q_start, a.n_each, a.n_tok, a.max_ctx, s, flags), TT);
+    Drafts d = {};
+    for (int s = s0; s < s1; ++s) {
+      d = drafts_of(a.ctx, a.q_start, a.n_each, a.n_tok, a.max_ctx, s, flags);
+      mine += line_length<X>(a, d);
+    }
     if (flags && blockIdx.x == 0) set_err(a.err, flags);
     long long incl = mine;
 #pragma unroll
@@ -242,225 +310,314 @@ __global__ void __launch_bounds__(384, 1)
       W += y;
     }
     before += incl - mine;
-    const int Pe = (int)(W < a.P ? W : a.P);
-    if (team < Pe) {
-      const long long pstart = W * team / Pe, pend = W * (team + 1) / Pe;
+    const RowsLine line(W, a.P);
+    const long long pstart = line.start(team);
+    if (team < line.P) {
       if (pstart >= before && pstart < before + mine) {
         RowsCursor c;
         long long off = pstart - before;
-        for (c.s = s0;; ++c.s) {
-          c.d = drafts_of(a.ctx, a.q_start, a.n_each, a.n_tok, a.max_ctx, c.s, flags);
-          const long long len = line_length(a, c.d, TT);
-          if (off < len || c.s + 1 >= s1) break;
-          off -= len;
-        }
+        c.s = s0;
+        c.d = d;                             // with a sequence per thread it is the one
+        if (per > 1)
+          for (;; ++c.s) {
+            c.d = drafts_of(a.ctx, a.q_start, a.n_each, a.n_tok, a.max_ctx, c.s, flags);
+            const long long len = line_length<X>(a, c.d);
+            if (off < len || c.s + 1 >= s1) break;
+            off -= len;
+          }
         c.nt = max(1, (c.d.ctx + TT - 1) / TT);
-        c.rt = row_tiles(a, c.d.n);
+        c.rt = row_tiles<X>(a, c.d.n);
         const int groups = max(1, (c.rt + a.C - 1) / a.C);
-        c.t = (int)(off % c.nt);
-        c.rg = (int)(off / c.nt % groups);
-        c.g = (int)(off / c.nt / groups);
+        const long long seg_at = div_pos(off, c.nt);          // segment of the sequence
+        c.t = (int)(off - seg_at * c.nt);
+        c.g = (int)div_pos(seg_at, groups);
+        c.rg = (int)(seg_at - (long long)c.g * groups);
         c.at_start = 1;
         c.whole_from = c.t == 0;
-        c.left = pend - pstart;
-        if (member == 0) {
-          RowsCut cut = {};
-          const long long seg = pstart - c.t, prev = team > 0 ? W * (team - 1) / Pe : 0;
-          if (c.t > 0 && prev <= seg) {
-            const int last = (int)min(((seg + c.nt) * Pe - 1) / W, (long long)Pe - 1);   // the last piece that holds a part
-            cut.parts = last - team + 2;
-            cut.first = prev == seg ? 0 : 1;
-            cut.q0 = c.d.q0; cut.n = c.d.n; cut.g = c.g; cut.rg = c.rg;
-          }
-          a.cuts[team] = cut;
-        }
-        const bool any = rows_settle<TT>(c, a, member);
+        c.left = line.start(team + 1) - pstart;
+        sh.first = c;
+        sh.W = W;
+        const bool any = rows_settle<X>(c, a, member);
         sh.cur = c;
-        sh.any = any;
+        ++c.t;
+        --c.left;
+        sh.any = any ? (rows_settle<X>(c, a, member) ? 2 : 1) : 0;
       }
-    } else if (member == 0 && threadIdx.x == 0) {
-      a.cuts[team] = RowsCut{};
+    } else if (threadIdx.x == 0) {
+      sh.W = 0;
     }
   }
   // query rows past a tile's own hold zeros until the end
   if constexpr (!X::SHARED)
-    for (int i = threadIdx.x; i < X::NQ * X::QBUF / 16; i += 384) reinterpret_cast<uint4*>(sm + X::Q_OFF)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x; i < NQ * X::QBUF / 16; i += 384) reinterpret_cast<uint4*>(sm + X::Q_OFF)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
-  if (sh.any && (warp == 0 || (warp == 3 && !X::SHARED))) {
-    // ------------------------------- producers -------------------------------
-    const bool kside = warp == 0;
-    const int depth = kside ? NK : NV, NC = kside ? KC : X::VC;
+  if (warp == 3 && lane == 0 && member == 0) {
+    // whether the piece's start cuts a segment for the first time, for the kernel that joins the parts
+    RowsCut cut = {};
+    if (sh.W > 0) {
+      const RowsLine line(sh.W, a.P);
+      const RowsCursor& c = sh.first;
+      const long long pstart = line.start(team), seg = pstart - c.t, prev = team > 0 ? line.start(team - 1) : 0;
+      if (c.t > 0 && prev <= seg) {
+        const int last = min(line.piece(min(seg + c.nt, line.W) - 1), line.P - 1);   // the last piece that holds a part
+        cut.parts = last - team + 2;
+        cut.first = prev == seg ? 0 : 1;
+        cut.q0 = c.d.q0; cut.n = c.d.n; cut.g = c.g; cut.rg = c.rg;
+      }
+    }
+    a.cuts[team] = cut;
+  }
+  __syncwarp();
+  if (sh.any && warp == 0) {
+    // ------------------------------- producer --------------------------------
+    const int bsz = 1 << a.bs_log2, nbt = TT >> a.bs_log2;    // rows of a block, blocks of a tile
     const uint64_t pol = policy_evict_first();
     RowsCursor c = sh.cur;
-    int k = -1, kq = -1, i = 0;
+    int k = -1, kq = -1, i = 0, slots = 0;                    // slots: of a latent cache's ring, issued so far
     struct Tile {
       RowsMeta m;
-      int nblk, phys, first;
+      int nblk, phys, idx;                                    // idx: number of the tile in its segment, within the piece
     };
     // the tile at the cursor, which then moves on; false when it was the last one
-    auto describe = [&](Tile& t) {
+    auto describe = [&](Tile& t, int prev_idx) {
       const bool first = k < 0 || c.t == 0;
       if (first) ++k;
-      t.first = first;
+      t.idx = first ? 0 : prev_idx + 1;
       t.m.k = k;
       t.m.tile0 = c.t * TT;
       t.m.ctx = c.d.ctx; t.m.n = c.d.n; t.m.q0 = c.d.q0;
-      t.m.row0 = (c.rg * a.C + member) * a.tile_rows;
+      tile_of<X>(a, c.rg * a.C + member, t.m.t0, t.m.h0);
       t.m.g = c.g;
       t.m.part = blockIdx.x * 2 + (c.at_start ? 0 : 1);
-      const int blk0 = c.t * X::NBT, nb = (c.d.ctx + BS - 1) / BS;
-      t.nblk = min(nb - blk0, X::NBT);
+      const int blk0 = c.t * nbt, nb = (c.d.ctx + bsz - 1) >> a.bs_log2;
+      t.nblk = min(nb - blk0, nbt);
       const int32_t* row = a.bt + (size_t)c.s * a.max_blocks + blk0;
       t.phys = lane < t.nblk ? row[lane] : -1;
       const bool seg_end = c.t + 1 == c.nt;
       t.m.flags = (first ? F_FIRST : 0) | (seg_end || c.left == 1 ? F_LAST : 0) | (seg_end && c.whole_from ? F_WHOLE : 0);
       ++c.t;
       --c.left;
-      const bool more = rows_settle<TT>(c, a, member);
+      const bool more = rows_settle<X>(c, a, member);
       if (!more) t.m.flags |= F_END;
       return more;
     };
     Tile t, tn;
-    bool more = describe(t);
+    bool more = describe(t, 0), ok = true;
+    auto waited = [&](uint64_t* bar, int round) {             // of the whole warp: for a slot's use number `round` to be over
+      bool w = !sh.abort_flag;
+      if (w && round >= 0 && lane == 0) w = mbar_wait(bar, round & 1);
+      return __shfl_sync(FULL_MASK, w, 0) != 0;
+    };
     for (;; ++i) {
       bool more2 = false;
-      if (more) more2 = describe(tn);                         // its block ids in flight
-      const int slot = i % depth, qb = t.m.k % X::NQ;
-      uint64_t* fullb = &bar[(kside ? RB_KFULL : VFULL) + slot];
-      bool ok = !sh.abort_flag;
-      if (ok && i >= depth && lane == 0) ok = mbar_wait(&bar[(kside ? RB_KEMPTY : VEMPTY) + slot], (i / depth - 1) & 1);
-      if (ok && kside && t.first && t.m.k >= X::NQ && lane == 0) ok = mbar_wait(&bar[RB_QEMPTY + qb], (t.m.k / X::NQ - 1) & 1);
-      ok = __shfl_sync(FULL_MASK, ok, 0);
-      if (!ok) {
-        if (lane == 0) {
-          set_err(a.err, PKV_DEV_TIMEOUT);
-          sh.abort_flag = 1;
-        }
-        break;
-      }
+      if (more) more2 = describe(tn, t.idx);                  // its block ids in flight
+      // what the tile is to its softmax group
+      int flags = t.m.flags;
+      const bool next_last = more && tn.m.k == t.m.k && (tn.m.flags & F_LAST);
+      if (t.idx < (PP ? 2 : 1)) flags |= G_FIRST;
+      if ((flags & F_LAST) || (PP && next_last)) flags |= G_LAST;
+      if (PP && next_last) flags |= tn.m.flags & F_WHOLE;
+      if ((flags & F_END) || (PP && more && (tn.m.flags & F_END))) flags |= G_END;
+      if (t.idx == 0 && (flags & F_LAST)) flags |= G_SOLO;
+      t.m.flags = flags;
       const bool okb = lane < t.nblk && (unsigned)t.phys < (unsigned)a.num_blocks;
       const unsigned invalid = __ballot_sync(FULL_MASK, lane < t.nblk && !okb), valid = __ballot_sync(FULL_MASK, okb);
-      uint8_t* st = sm + (kside ? slot * X::KST : X::V_OFF + slot * X::VST);
-      if (lane == 0) {
-        if (invalid && kside) set_err(a.err, PKV_DEV_BAD_BLOCK);
-        t.m.invalid = (int)invalid;
-        (kside ? sh.kmeta : vmeta)[slot] = t.m;
-        if (kside && t.first) {
-          uint8_t* qd = sm + X::Q_OFF + qb * X::QBUF;
-          mbar_arrive_expect_tx(&bar[RB_QFULL + qb], (uint32_t)KC * 128u * (uint32_t)a.tile_rows);
+      t.m.invalid = (int)invalid;
+      if (lane == 0 && invalid) set_err(a.err, PKV_DEV_BAD_BLOCK);
+      // The segment's query rows.  With one buffer for them they come behind the tile, which need not wait for the
+      // last segment's products.
+      auto queries = [&] {
+        const int qb = t.m.k % NQ;
+        ok = waited(&sh.qempty[qb], t.m.k / NQ - 1);
+        if (!ok) return;
+        if (lane == 0) {
+          const uint32_t rows = X::SHARED ? R : a.gt * a.tpt;
+          mbar_arrive_expect_tx(&sh.qfull[qb], (uint32_t)KC * 128u * rows);
           for (int ch = 0; ch < KC; ++ch) {
-            if constexpr (X::SHARED) tma_load_3d(qd + ch * X::QCH, &tmq, ch * 64, t.m.q0 * a.n_h + t.m.row0, 0, &bar[RB_QFULL + qb], pol);
-            else tma_load_3d(qd + ch * X::QCH, &tmq, ch * 64, t.m.g * a.G, t.m.q0 + t.m.row0 / a.G, &bar[RB_QFULL + qb], pol);
+            uint8_t* qd = sm + X::Q_OFF + qb * X::QBUF + ch * X::QCH;
+            if constexpr (X::SHARED) tma_load_3d(qd, &tmq, ch * 64, (t.m.q0 + t.m.t0) * a.n_h + t.m.h0, 0, &sh.qfull[qb], pol);
+            else tma_load_3d(qd, &tmq, ch * 64, t.m.g * a.G + t.m.h0, t.m.q0 + t.m.t0, &sh.qfull[qb], pol);
           }
-          kq = t.m.k;
         }
-        mbar_arrive_expect_tx(fullb, (uint32_t)__popc(valid) * (uint32_t)NC * BS * 128u);
-      }
-      __syncwarp();
-      for (int j0 = 0; j0 < X::NBT * NC; j0 += 32) {          // lane: one box of 64 channels of one block
-        const int j = j0 + lane, b = j / NC, ch = j - b * NC;
+        kq = t.m.k;
+      };
+      const bool asks = flags & F_FIRST;
+      if (NQ > 1 && asks) queries();
+      if (!ok) break;
+      // One fill of a slot: `nc` chunks from channel c0 on, of each block; lane: one box of 64 channels of one block.
+      auto fill = [&](uint8_t* dst, uint64_t* full, const CUtensorMap* tm, int c0, int nc) {
+        if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)__popc(valid) * (uint32_t)(nc * 128) << a.bs_log2);
+        __syncwarp();
+        const int b = lane / nc, ch = lane - b * nc;
         const int pb = __shfl_sync(FULL_MASK, t.phys, b & 31);
         if (b < t.nblk && ((valid >> b) & 1))
-          tma_load_3d(st + ch * X::CHUNK + b * BS * 128, kside ? &tmk : &tmv, ch * 64, t.m.g * BS, pb, fullb, pol);
+          tma_load_3d(dst + ch * X::CHUNK + (b << a.bs_log2) * 128, tm, c0 + ch * 64, t.m.g << a.bs_log2, pb, full, pol);
+      };
+      if constexpr (X::SHARED) {
+        for (int vt = 0; vt < VT && ok; ++vt, ++slots) {
+          const int slot = slots % NK;
+          ok = waited(&sh.kempty[slot], slots / NK - 1);
+          if (!ok) break;
+          if (vt == 0 && lane == 0) sh.meta[i % NM] = t.m;
+          fill(sm + slot * X::KST, &sh.kfull[slot], &tmk, vt * 128, 2);
+        }
+        if (ok) ok = waited(&sh.pslot[i % NP], i / NP - 1);
+        if (!ok) break;
+        fill(sm + X::P_OFF + (i % NP) * X::PST, &sh.vfull[i % NP], &tmk, VT * 128, 1);
+      } else {
+        ok = waited(&sh.kempty[i % NK], i / NK - 1);
+        if (!ok) break;
+        if (lane == 0) sh.meta[i % NM] = t.m;
+        fill(sm + (i % NK) * X::KST, &sh.kfull[i % NK], &tmk, 0, KC);
+        fill(sm + (i % NK) * X::KST + X::KPART, &sh.vfull[i % NK], &tmv, 0, X::VC);
       }
-      if (!more) {
-        ++i;
-        break;
-      }
+      if (NQ == 1 && asks) queries();
+      if (!ok || !more) break;
       t = tn;
       more = more2;
+    }
+    if (!ok && lane == 0) {
+      set_err(a.err, PKV_DEV_TIMEOUT);
+      sh.abort_flag = 1;
     }
     // After a timeout: let the loads already issued land before the CTA leaves (bounded).
     if (sh.abort_flag && lane == 0) {
       bool live = true;
-      for (int j = i - depth < 0 ? 0 : i - depth; j < i && live; ++j)
-        live = mbar_wait(&bar[(kside ? RB_KFULL : VFULL) + j % depth], (j / depth) & 1);
-      if (live && kside && kq >= 0) mbar_wait(&bar[RB_QFULL + kq % X::NQ], (kq / X::NQ) & 1);
+      const int nk = X::SHARED ? slots : i + 1;
+      for (int j = max(0, nk - NK - 1); j < nk && live; ++j) live = mbar_wait(&sh.kfull[j % NK], (j / NK) & 1, 20000000ull);
+      for (int j = max(0, i - NP); j <= i && live; ++j) live = mbar_wait(&sh.vfull[j % NP], (j / NP) & 1, 20000000ull);
+      if (kq >= 0) mbar_wait(&sh.qfull[kq % NQ], (kq / NQ) & 1, 20000000ull);
     }
     __syncwarp();
   } else if (sh.any && warp == 1) {
     // ------------------------- first-product issuer -------------------------
-    if (lane == 0) {
-      constexpr uint32_t IQK = umma_idesc_bf16(TT, R, 0, 0);
-      const uint32_t sbase = smem_u32(sm);
-      bool ok = true;
-      for (int i = 0;; ++i) {
-        const int slot = i % NK, sb = i & 1;
-        if (sh.abort_flag || !mbar_wait(&bar[RB_KFULL + slot], (i / NK) & 1)) {
-          ok = false;
-          break;
-        }
-        const int flags = sh.kmeta[slot].flags, k = sh.kmeta[slot].k, qb = k % X::NQ;
-        if (((flags & F_FIRST) && !mbar_wait(&bar[RB_QFULL + qb], (k / X::NQ) & 1)) ||
-            (i >= 2 && !mbar_wait(&bar[RB_SEMPTY + sb], ((i >> 1) - 1) & 1))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t kb = sbase + slot * X::KST, qa = sbase + X::Q_OFF + qb * X::QBUF;
-#pragma unroll 4
-        for (int ks = 0; ks < KC * 4; ++ks) {
-          const uint64_t ad = umma_desc(kb + (ks >> 2) * X::CHUNK + (ks & 3) * 32, 16, 1024, kLayoutSw128);
-          const uint64_t bd = umma_desc(qa + (ks >> 2) * X::QCH + (ks & 3) * 32, 16, 1024, kLayoutSw128);
-          umma_bf16(tmem + X::S_COL + R * sb, ad, bd, IQK, ks > 0 ? 1u : 0u);
-        }
-        umma_commit(&bar[RB_SFULL + sb]);
-        if (!X::SHARED) umma_commit(&bar[RB_KEMPTY + slot]);
-        if (flags & F_LAST) umma_commit(&bar[RB_QEMPTY + qb]);
-        if (flags & F_END) break;
+    // The whole warp runs the loop and one lane issues (elect_one).
+    constexpr uint32_t IQK = umma_idesc_bf16(TT, R, 0, 0);
+    constexpr uint32_t HI = (uint32_t)(umma_desc_k(16, 1024) >> 32);
+    const uint32_t sbase = (uint32_t)umma_desc_k(16, 1024) + (smem_u32(sm) >> 4);
+    const uint32_t tm = __shfl_sync(FULL_MASK, tmem, 0);
+    const bool leader = elect_one();
+    bool ok = true;
+    for (int i = 0;; ++i) {
+      const int k0 = X::SHARED ? i * VT : i, sb = i % NS;     // first slot of the tile's keys
+      if (sh.abort_flag || !mbar_wait(&sh.kfull[k0 % NK], (k0 / NK) & 1)) {
+        ok = false;
+        break;
       }
+      const RowsMeta& mt = sh.meta[i % NM];
+      const int flags = __shfl_sync(FULL_MASK, mt.flags, 0), k = __shfl_sync(FULL_MASK, mt.k, 0), qb = k % NQ;
+      if (((flags & F_FIRST) && !mbar_wait(&sh.qfull[qb], (k / NQ) & 1)) || (i >= NS && !mbar_wait(&sh.sempty[sb], (i / NS - 1) & 1))) {
+        ok = false;
+        break;
+      }
+      const uint32_t qa = sbase + ((X::Q_OFF + qb * X::QBUF) >> 4), d = tm + X::S_COL + R * sb;
+      // chunks [ch0, ch0 + nc) of the keys, at ka: four steps of 16 channels each
+      auto chunks = [&](uint32_t ka, int ch0, int nc, int steps) {
+        tc_fence_after();
+        __syncwarp();
+        if (leader) {
+          uint32_t qc = qa + ch0 * (X::QCH >> 4);
+#pragma unroll 1
+          for (int ch = 0; ch < nc; ++ch, ka += X::CHUNK >> 4, qc += X::QCH >> 4)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              if (ks < steps) umma_bf16_lo(d, ka + ks * 2, HI, qc + ks * 2, HI, IQK, ks > 0 || ch > 0 || ch0 > 0 ? 1u : 0u);
+        }
+        __syncwarp();
+      };
+      if constexpr (X::SHARED) {
+        for (int vt = 0; vt < VT && ok; ++vt) {
+          const int slot = (k0 + vt) % NK;
+          if (vt > 0) ok = mbar_wait(&sh.kfull[slot], ((k0 + vt) / NK) & 1);
+          if (ok) chunks(sbase + (slot * X::KST >> 4), 2 * vt, 2, 4);
+        }
+        ok = ok && mbar_wait(&sh.vfull[i % NP], (i / NP) & 1);
+        if (!ok) break;
+        chunks(sbase + ((X::P_OFF + (i % NP) * X::PST) >> 4), KC - 1, 1, a.last_steps);
+      } else {
+        chunks(sbase + ((i % NK) * X::KST >> 4), 0, KC, 4);
+      }
+      if (leader) {
+        umma_commit(&sh.sfull[sb]);
+        if (flags & F_LAST) umma_commit(&sh.qempty[qb]);
+      }
+      __syncwarp();
+      if (flags & F_END) break;
+    }
+    ok = __all_sync(FULL_MASK, ok);
+    if (leader) {
       if (!ok) {
         set_err(a.err, PKV_DEV_TIMEOUT);
         sh.abort_flag = 1;
       }
       // every product issued has completed before the tensor memory is released
-      umma_commit(&bar[RB_DRAIN]);
-      mbar_wait(&bar[RB_DRAIN], 0);
+      umma_commit(&sh.drain);
+      mbar_wait(&sh.drain, 0);
     }
     __syncwarp();
   } else if (sh.any && warp == 2) {
     // ------------------------- second-product issuer ------------------------
-    if (lane == 0) {
-      constexpr uint32_t IPV = umma_idesc_bf16(X::VM, N2, 1, 1);
-      const uint32_t sbase = smem_u32(sm);
-      bool ok = true;
-      for (int i = 0;; ++i) {
-        const int slot = i % NV, pb = i % X::NP;
-        if (sh.abort_flag || !mbar_wait(&bar[VFULL + slot], (i / NV) & 1) || !mbar_wait(&bar[RB_PFULL + pb], (i / X::NP) & 1)) {
-          ok = false;
-          break;
-        }
-        const RowsMeta& mt = vmeta[slot];
-        const int flags = mt.flags, k = mt.k, ob = k % X::NO, nks = (min(TT, mt.ctx - mt.tile0) + 15) >> 4;
-        if ((flags & F_FIRST) && k >= X::NO && !mbar_wait(&bar[RB_OEMPTY + ob], (k / X::NO - 1) & 1)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t vb = sbase + (X::SHARED ? slot * X::KST : X::V_OFF + slot * X::VST), pa = sbase + X::P_OFF + pb * X::PBUF;
-#pragma unroll
-        for (int vt = 0; vt < VT; ++vt) {
-          for (int kk = 0; kk < nks; ++kk) {
-            const uint64_t ad = umma_desc(vb + vt * (X::VM / 64) * X::CHUNK + kk * 2048, X::CHUNK, 1024, kLayoutSw128);
-            const uint64_t bd = umma_desc(pa + kk * 2048, X::CHUNK, 1024, kLayoutSw128);
-            umma_bf16(tmem + (ob * VT + vt) * N2, ad, bd, IPV, (flags & F_FIRST) && kk == 0 ? 0u : 1u);
-          }
-        }
-        umma_commit(&bar[VEMPTY + slot]);
-        umma_commit(&bar[RB_PEMPTY + pb]);
-        if (flags & F_LAST) umma_commit(&bar[RB_OFULL + ob]);
-        if (flags & F_END) break;
+    constexpr uint32_t IPV = umma_idesc_bf16(X::VM, N2, 1, 1);
+    constexpr uint32_t HI = (uint32_t)(umma_desc_k(X::CHUNK, 1024) >> 32);
+    const uint32_t sbase = (uint32_t)umma_desc_k(X::CHUNK, 1024) + (smem_u32(sm) >> 4);
+    const uint32_t tm = __shfl_sync(FULL_MASK, tmem, 0);
+    const bool leader = elect_one();
+    bool ok = true;
+    for (int i = 0;; ++i) {
+      const int pb = i % NP, k0 = i * VT;
+      if (sh.abort_flag || !mbar_wait(X::SHARED ? &sh.kfull[k0 % NK] : &sh.vfull[pb], (X::SHARED ? k0 / NK : i / NP) & 1) ||
+          !mbar_wait(&sh.pfull[pb], (i / NP) & 1)) {
+        ok = false;
+        break;
       }
+      const RowsMeta& mt = sh.meta[i % NM];
+      const int flags = __shfl_sync(FULL_MASK, mt.flags, 0), k = __shfl_sync(FULL_MASK, mt.k, 0), ob = k % NO;
+      const int nks = __shfl_sync(FULL_MASK, (min(TT, mt.ctx - mt.tile0) + 15) >> 4, 0);
+      if ((flags & F_FIRST) && k >= NO && !mbar_wait(&sh.oempty[ob], (k / NO - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      __syncwarp();
+      const uint32_t pa = sbase + ((X::P_OFF + pb * X::PST) >> 4), d = tm + (ob * NG + (PP ? i & 1 : 0)) * VT * N2;
+      const uint32_t acc0 = flags & G_FIRST ? 0u : 1u;
+#pragma unroll 1
+      for (int vt = 0; vt < VT; ++vt) {
+        const int slot = X::SHARED ? (k0 + vt) % NK : i % NK;
+        if (X::SHARED && vt > 0) ok = ok && mbar_wait(&sh.kfull[slot], ((k0 + vt) / NK) & 1);   // it landed before the first product
+        const uint32_t vb = sbase + ((slot * X::KST + (X::SHARED ? 0 : X::KPART)) >> 4);
+        if (leader && ok) {
+#pragma unroll
+          for (int kk = 0; kk < TT / 16; ++kk)
+            if (kk < nks) umma_bf16_lo(d + vt * N2, vb + kk * 128, HI, pa + kk * 128, HI, IPV, kk ? 1u : acc0);
+          umma_commit(&sh.kempty[slot]);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (leader) {
+        if (X::SHARED) umma_commit(&sh.pslot[pb]);
+        umma_commit(&sh.pempty[i & 1]);
+        if (flags & F_LAST) {              // for the groups that had tiles of the segment
+          if (!PP || (i & 1) == 0 || !(flags & G_SOLO)) umma_commit(&sh.ofull[0]);
+          if (PP && ((i & 1) == 1 || !(flags & G_SOLO))) umma_commit(&sh.ofull[1]);
+        }
+      }
+      __syncwarp();
+      if (flags & F_END) break;
+    }
+    ok = __all_sync(FULL_MASK, ok);
+    if (leader) {
       if (!ok) {
         set_err(a.err, PKV_DEV_TIMEOUT);
         sh.abort_flag = 1;
       }
-      umma_commit(&bar[RB_DRAIN_PV]);
-      mbar_wait(&bar[RB_DRAIN_PV], 0);
+      umma_commit(&sh.drain_pv);
+      mbar_wait(&sh.drain_pv, 0);
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -473,231 +630,375 @@ __global__ void __launch_bounds__(384, 1)
       for (long long e = threadIdx.x - 128; e < len; e += 256) store_out(a, at + e, 0.f);
     }
     // -------------------------- softmax and epilogue ------------------------
-    // Group gi takes query rows [hb, hb + R / 2).  Warp w reaches the tensor-memory lanes of quarter w % 4: in
-    // S^T the cached rows 16 MT wq + ..., in fragments of 16 rows x 8 query rows, in O^T the channels 32 wq + lane.
-    constexpr int RG = R / 2, KB = RG / 8;                    // query rows of a group, fragments
-    const int wq = warp & 3, gi = (warp - 4) >> 2, hb = RG * gi;
+    // Warp w reaches the tensor-memory lanes of quarter w % 4: in S^T the cached rows 16 MT wq + ..., in fragments of
+    // 16 rows x 8 query rows, in O^T the channels 32 wq + lane.
+    constexpr int RC = PP ? R : R / 2;     // query rows of a group in a tile
+    constexpr int NC = RC / 4;             // of a thread: 2 (lane % 4) + {0, 1} of every eight
+    constexpr int CB = RC >= 16 ? 2 : 1;   // fragments at a time
+    constexpr int NW = PP ? 128 : 256;     // threads that share a tile
+    const int wq = warp & 3, gi = (warp - 4) >> 2, hb = PP ? 0 : RC * gi;
+    const int wg = PP ? gi : 0, tid = (threadIdx.x - 128) & (NW - 1);
     const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
-    float m[2 * KB], l[2 * KB];                               // offsets and this thread's rows' share of the sums, of its query rows
-    // A failed (timed-out) wait makes `bad` true for the whole warp; both groups learn of it at the vote that
-    // opens each tile and leave together, so no thread is left at a named barrier.
-    bool bad = false;
-    int i = 0;
-    for (; sh.any;) {
-      const int slot = i % NV, sb = i & 1, pb = i % X::NP;
-      bool okw = !bad && !sh.abort_flag && mbar_wait(&bar[VFULL + slot], (i / NV) & 1) && mbar_wait(&bar[RB_SFULL + sb], (i >> 1) & 1);
-      okw = __all_sync(FULL_MASK, okw);
-      if (named_bar_or(1, 256, !okw)) {
-        bad = true;
+    const int r0 = 16 * MT * wq + (lane >> 2), c0 = hb + 2 * (lane & 3);   // this thread's first cached row and query row
+    auto col = [&](int q) { return c0 + 8 * (q >> 1) + (q & 1); };
+    // Offsets and this thread's rows' share of the sums, of its query rows.
+    float m[NC], l[NC];
+    bool was_special = false;
+    // Barriers among the threads of a tile.  A failed (timed-out) wait makes `bad` true for its warp, which raises a flag ahead
+    // of the next barrier; behind that all of them see it and leave together, so no thread is left at a barrier.  The
+    // flag goes by the barrier's parity, since a warp may be one barrier ahead of another.
+    bool bad = false, gone = false;
+    int turn = 0, joins = 0, ends = 0;     // barriers, exchanges and segments so far
+    auto sync = [&](bool pred) {
+      if (bad && lane == 0) sh.bad[wg][turn & 1] = 1;
+      __syncwarp();
+      const bool any = named_bar_or(1 + wg, NW, pred || bad);
+      if (any && sh.bad[wg][turn & 1]) gone = true;
+      ++turn;
+      return any;
+    };
+    auto wait = [&](uint64_t* bar, int round) { bad |= !__all_sync(FULL_MASK, !bad && !sh.abort_flag && mbar_wait(bar, round & 1)); };
+
+    for (int i = PP ? gi : 0; sh.any > (PP ? gi : 0); i += PP ? 2 : 1) {
+      const int pb = i % NP, sb = i % NS, k0 = X::SHARED ? i * VT : i;
+      // A barrier tells a phase from the one before it only by parity, and this group may not have waited for that.  It is
+      // over, though: behind the group's last tile the keys of the tiles before it had landed, and behind this one's
+      // scores the tile whose slot they took was done with.
+      wait(&sh.kfull[k0 % NK], k0 / NK);                      // the metadata, which stay until P is there
+      wait(&sh.sfull[sb], i / NS);                            // the scores, and room for P in place of the keys
+      if (bad) {
+        sync(true);
         break;
       }
-      const RowsMeta mt = vmeta[slot];
-      const int flags = mt.flags, ob = mt.k % X::NO, nrows = min(TT, mt.ctx - mt.tile0);
+      const RowsMeta mt = sh.meta[i % NM];
+      const int flags = mt.flags, ob = mt.k % NO, acc = (ob * NG + (PP ? gi : 0)) * VT * N2;
       const bool special = mt.tile0 + TT > mt.ctx - mt.n || mt.invalid;
+      uint8_t* pbuf = sm + X::P_OFF + pb * X::PST;
+      RowsScratch<X>& scr = *reinterpret_cast<RowsScratch<X>*>(pbuf);
       tc_fence_after();
-      float x[MT][KB][4];
-      {
-        uint32_t sr[MT][4 * KB];
+      if (flags & G_FIRST) {
 #pragma unroll
-        for (int j = 0; j < MT; ++j) tmem_ld_frag(tmem + lane_off + ((uint32_t)(16 * j) << 16) + X::S_COL + R * sb + hb, sr[j]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-#pragma unroll
-          for (int b = 0; b < KB; ++b)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[j][b][e] = __uint_as_float(sr[j][4 * b + e]) * a.scale_log2;
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[RB_SEMPTY + sb]);       // S buffer sb may be rewritten
-      if (flags & F_FIRST) {
-#pragma unroll
-        for (int b = 0; b < 2 * KB; ++b) {
-          m[b] = -INFINITY;
-          l[b] = 0.f;
+        for (int q = 0; q < NC; ++q) {
+          m[q] = -INFINITY;
+          l[q] = 0.f;
         }
       }
-      const int r0 = 16 * MT * wq + (lane >> 2), c0 = hb + 2 * (lane & 3);   // this thread's first cached row and query row
-      if (special) {
-        // what each query row attends to in this tile, and what any of them does
-        const int tid = threadIdx.x - 128;
-        if (tid < 2) sh.seen[tid] = 0;
-        named_bar(6, 256);
-        if (tid < R * MT) {
-          const int c = tid % R, w = tid / R, r = mt.row0 + c;
-          unsigned long long win = 0;
-          if (c < a.tile_rows && r < mt.n * a.G) win = attended(a, mt, r / a.G, mt.tile0 + 64 * w);
-          for (int b = 0; b < 64 / BS; ++b)
-            if ((mt.invalid >> (w * (64 / BS) + b)) & 1) win &= ~(ones_below(BS) << (b * BS));
-          sh.win[w * R + c] = win;
-          atomicOr(&sh.seen[w], win);
-        }
-        named_bar(6, 256);
+      const uint32_t st = tmem + lane_off + X::S_COL + R * sb + hb;
+      uint32_t bits[(NC * 2 * MT + 31) / 32];                 // of a special tile: which of this thread's scores count
+      float ts[NC];                                           // the tile's part of l
+      // One pass over the tile: weights against the offsets, into P as bf16 parts, and their sums.  Returns the largest
+      // exponent.  Row t of the B operand: 128 bytes per 64 columns (first parts of the query rows, then the next parts),
+      // 16-byte chunk c stored at chunk c ^ (t % 8) (128-byte swizzle).
+      auto emit = [&](auto masked) {
+        constexpr bool MASKED = decltype(masked)::value;
+        float top = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < MT; ++j)
+        for (int ch = 0; ch < RC / (8 * CB); ++ch) {
+          uint32_t sr[MT][4 * CB];
 #pragma unroll
-          for (int b = 0; b < KB; ++b)
+          for (int j = 0; j < MT; ++j) tmem_ld_frag(st + ((uint32_t)(16 * j) << 16) + ch * 8 * CB, sr[j]);
+          tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int row = r0 + 16 * j + 8 * (e >> 1), c = c0 + 8 * b + (e & 1);
-              if (!((sh.win[(row >> 6) * R + c] >> (row & 63)) & 1)) x[j][b][e] = -INFINITY;
+          for (int b = 0; b < CB; ++b) {
+            const int q = 2 * (ch * CB + b);
+            const float o0 = MASKED && m[q] == -INFINITY ? 0.f : m[q], o1 = MASKED && m[q + 1] == -INFINITY ? 0.f : m[q + 1];
+            float t0 = 0.f, t1 = 0.f;
+#pragma unroll
+            for (int jh = 0; jh < 2 * MT; ++jh) {
+              const int j = jh >> 1, h = jh & 1, row = r0 + 16 * j + 8 * h;
+              float y0 = fmaf(__uint_as_float(sr[j][4 * b + 2 * h]), a.scale_log2, -o0);
+              float y1 = fmaf(__uint_as_float(sr[j][4 * b + 2 * h + 1]), a.scale_log2, -o1);
+              if constexpr (MASKED) {
+                const int z = q * 2 * MT + jh, z1 = z + 2 * MT;
+                if (!((bits[z >> 5] >> (z & 31)) & 1)) y0 = -INFINITY;
+                if (!((bits[z1 >> 5] >> (z1 & 31)) & 1)) y1 = -INFINITY;
+              }
+              top = fmaxf(top, fmaxf(y0, y1));
+              float p0 = ex2(y0), p1 = ex2(y1);
+              const uint32_t hi = pack_bf16(p0, p1);
+              uint8_t* prow = pbuf + row * 128 + 4 * (lane & 3);
+              auto put = [&](int part, uint32_t v) {
+                const int cc = (part * R + hb) / 8 + (q >> 1);
+                *reinterpret_cast<uint32_t*>(prow + (cc >> 3) * X::CHUNK + (((cc & 7) ^ (row & 7)) << 4)) = v;
+              };
+              put(0, hi);
+              if constexpr (HL == 1) {                        // the sums take the rounded weights, which the products take
+                p0 = bf16_lo(hi);
+                p1 = bf16_hi(hi);
+              } else {
+                const float u0 = p0 - bf16_lo(hi), u1 = p1 - bf16_hi(hi);
+                const uint32_t lo = pack_bf16(u0, u1);
+                put(1, lo);
+                if constexpr (HL == 3) put(2, pack_bf16(u0 - bf16_lo(lo), u1 - bf16_hi(lo)));
+              }
+              t0 += p0;
+              t1 += p1;
             }
-      }
-      bool over = false;
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-#pragma unroll
-        for (int b = 0; b < KB; ++b)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) over |= x[j][b][e] > m[2 * b + (e & 1)] + kLazyMax;
-      if (named_bar_or(2 + gi, 128, over)) {
-        // raise the group's offsets to the running max
-#pragma unroll
-        for (int b = 0; b < 2 * KB; ++b) {
-          float v = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < MT; ++j) v = fmaxf(v, fmaxf(x[j][b >> 1][b & 1], x[j][b >> 1][2 + (b & 1)]));
-#pragma unroll
-          for (int o = 4; o <= 16; o <<= 1) v = fmaxf(v, __shfl_xor_sync(FULL_MASK, v, o));
-          if (lane < 4) sh.red[wq * R + c0 + 8 * (b >> 1) + (b & 1)] = v;
+            ts[q] = t0;
+            ts[q + 1] = t1;
+          }
         }
-        named_bar(4 + gi, 128);
+        return top;
+      };
+      // A tile's weights are taken against the running offsets first; only where an exponent exceeds them by more than
+      // kRowsLazy the offsets are raised and the pass is made again.  A query row has no offset yet in its segment's first tile,
+      // and may have none behind tiles of which it attended to nothing: there the offsets are raised first.
+      bool raise = (flags & G_FIRST) || special || was_special;
+      was_special = special;
+      bool retry = false;
+      for (;;) {
+        if (raise) {
+          if (special) {
+            // what each query row attends to in this tile, and what any of them does
+            constexpr int EN = R * MT < NW ? R * MT : NW;     // of whole warps, or of one part of a warp
+            for (int w0 = 0; w0 < MT; w0 += EN / R) {
+              unsigned long long win = 0;
+              const int c = tid % R, w = w0 + tid / R;
+              if (tid < EN) {
+                const int tok = query_of<X>(a, mt.n, mt.t0, mt.h0, c).x;
+                if (tok >= 0) win = attended(a, mt, tok, mt.tile0 + 64 * w);
+                for (int b = 0; b < 64 >> a.bs_log2; ++b)
+                  if ((mt.invalid >> ((w * 64 >> a.bs_log2) + b)) & 1) win &= ~(ones_below(1 << a.bs_log2) << (b << a.bs_log2));
+                scr.win[w][c] = win;
+              }
+              // a warp's lanes hold one or two words' columns: an OR of each word's
+              const unsigned group = R >= 32 ? FULL_MASK : (0xffffu << (lane & 16));
+              const uint32_t lo = __reduce_or_sync(group, (uint32_t)win), hi = __reduce_or_sync(group, (uint32_t)(win >> 32));
+              if (tid < EN && lane % (R >= 32 ? 32 : 16) == 0) scr.seen[w][R > 32 ? (c >> 5) : 0] = (unsigned long long)hi << 32 | lo;
+            }
+            wait(&sh.vfull[pb], i / NP);                      // the values, of which some are about to be overwritten
+            if (sync(false), gone) break;
+            auto seen = [&](int row) {
+              unsigned long long x = scr.seen[row >> 6][0];
+              if constexpr (R > 32) x |= scr.seen[row >> 6][1];
+              return (x >> (row & 63)) & 1;
+            };
 #pragma unroll
-        for (int b = 0; b < 2 * KB; ++b) {
-          const int c = c0 + 8 * (b >> 1) + (b & 1);
-          const float mx = fmaxf(fmaxf(sh.red[c], sh.red[R + c]), fmaxf(sh.red[2 * R + c], sh.red[3 * R + c]));
-          const float mn = fmaxf(m[b], mx), al = m[b] == -INFINITY ? 0.f : ex2(m[b] - mn);
-          m[b] = mn;
-          l[b] *= al;
-          if (wq == 0 && lane < 4) sh.factor[c] = al;
-        }
-        named_bar(4 + gi, 128);
-        if (!(flags & F_FIRST)) {
-          // O accumulated so far: wait for the previous tile's products, then scale the group's columns in place
-          bad |= !__all_sync(FULL_MASK, mbar_wait(&bar[RB_PEMPTY + (i - 1) % X::NP], ((i - 1) / X::NP) & 1));
-          if (!bad) {
+            for (int z = 0; z < (NC * 2 * MT + 31) / 32; ++z) bits[z] = 0;
+#pragma unroll
+            for (int q = 0; q < NC; ++q)
+#pragma unroll
+              for (int jh = 0; jh < 2 * MT; ++jh) {
+                const int row = r0 + 16 * (jh >> 1) + 8 * (jh & 1), z = q * 2 * MT + jh;
+                bits[z >> 5] |= (uint32_t)((scr.win[row >> 6][col(q)] >> (row & 63)) & 1) << (z & 31);
+              }
+            // V rows that no query row attends to, and that the product reads with p = 0: they may hold anything
+            const int topr = (min(TT, mt.ctx - mt.tile0) + 15) & ~15;
+            for (int row = tid >> 5; row < topr; row += NW / 32)
+              if (!seen(row))
+                for (int v = lane; v < X::VC * 8; v += 32) {
+                  const int ch = v >> 3;
+                  uint8_t* base = X::SHARED ? sm + ((k0 + (ch >> 1)) % NK) * X::KST + (ch & 1) * X::CHUNK
+                                            : sm + (i % NK) * X::KST + X::KPART + ch * X::CHUNK;
+                  *reinterpret_cast<uint4*>(base + row * 128 + (v & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+          }
+          if ((flags & G_FIRST) && !special && !retry) {
+            // A segment's first tile starts from its first row's scores: offsets need not be the maxima, only near them
+            if (wq == 0) {
+#pragma unroll
+              for (int ch = 0; ch < RC / (8 * CB); ++ch) {
+                uint32_t sr[4 * CB];
+                tmem_ld_frag(st + ch * 8 * CB, sr);
+                tmem_wait_ld();
+#pragma unroll
+                for (int qq = 0; qq < 2 * CB; ++qq)
+                  if (lane < 4) scr.offset[col(2 * ch * CB + qq)] = __uint_as_float(sr[4 * (qq >> 1) + (qq & 1)]) * a.scale_log2;
+              }
+            }
+            if (sync(false), gone) break;
+#pragma unroll
+            for (int q = 0; q < NC; ++q) m[q] = scr.offset[col(q)];
+            if (sync(false), gone) break;                     // they are read before P is written over them
+            raise = false;
+            retry = true;
+          } else {
+          // the running maxima of the query rows, this tile's among them
+#pragma unroll
+          for (int ch = 0; ch < RC / (8 * CB); ++ch) {
+            uint32_t sr[MT][4 * CB];
+#pragma unroll
+            for (int j = 0; j < MT; ++j) tmem_ld_frag(st + ((uint32_t)(16 * j) << 16) + ch * 8 * CB, sr[j]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int qq = 0; qq < 2 * CB; ++qq) {
+              const int q = 2 * ch * CB + qq;
+              float v = -INFINITY;
+#pragma unroll
+              for (int jh = 0; jh < 2 * MT; ++jh) {
+                const int z = q * 2 * MT + jh;
+                const float y = __uint_as_float(sr[jh >> 1][4 * (qq >> 1) + 2 * (jh & 1) + (qq & 1)]) * a.scale_log2;
+                if (!special || ((bits[z >> 5] >> (z & 31)) & 1)) v = fmaxf(v, y);
+              }
+#pragma unroll
+              for (int o = 4; o <= 16; o <<= 1) v = fmaxf(v, __shfl_xor_sync(FULL_MASK, v, o));
+              if (lane < 4) scr.red[wq][col(q)] = v;
+            }
+          }
+          if (sync(false), gone) break;
+#pragma unroll
+          for (int q = 0; q < NC; ++q) {
+            const int c = col(q);
+            const float mx = fmaxf(fmaxf(scr.red[0][c], scr.red[1][c]), fmaxf(scr.red[2][c], scr.red[3][c]));
+            const float mn = fmaxf(m[q], mx), al = m[q] == -INFINITY ? 0.f : ex2(m[q] - mn);
+            m[q] = mn;
+            l[q] *= al;
+            if (wq == 0 && lane < 4) scr.factor[c] = al;
+          }
+          if (!(flags & G_FIRST)) {
+            // O accumulated so far, which the products of the tiles before have completed: scaled in place
+            wait(&sh.pempty[PP ? i & 1 : (i - 1) & 1], PP ? i / 2 - 1 : (i - 1) / 2);
+            if (sync(false), gone) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int q = 0; q < VT * HL; ++q) {
+            for (int p = 0; p < VT * HL; ++p) {
 #pragma unroll 1
-              for (int b = 0; b < KB; ++b) {
-                const uint32_t ta = tmem + lane_off + (ob * VT + q / HL) * N2 + (q % HL) * R + hb + 8 * b;
+              for (int b = 0; b < RC / 8; ++b) {
+                const uint32_t ta = tmem + lane_off + acc + (p / HL) * N2 + (p % HL) * R + hb + 8 * b;
                 uint32_t o[8];
                 tmem_ld8(ta, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sh.factor[hb + 8 * b + e]);
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scr.factor[hb + 8 * b + e]);
                 tmem_st8(ta, o);
               }
             }
             tmem_wait_st();
             tc_fence_before();
           }
-        }
-      }
-      // the P buffer is free once the products that read it last have completed
-      if (i >= X::NP) bad |= !__all_sync(FULL_MASK, mbar_wait(&bar[RB_PEMPTY + pb], (i / X::NP - 1) & 1));
-      // Row t of the B operand: 128 bytes per 64 columns (high parts of the query rows, then low parts), 16-byte
-      // chunk c stored at chunk c ^ (t % 8) (128-byte swizzle).
-      uint8_t* pbuf = sm + X::P_OFF + pb * X::PBUF;
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-#pragma unroll
-        for (int b = 0; b < KB; ++b)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int row = r0 + 16 * j + 8 * h;
-            float p[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float off = m[2 * b + e] == -INFINITY ? 0.f : m[2 * b + e];
-              p[e] = ex2(x[j][b][2 * h + e] - off);
-            }
-            const uint32_t hi = pack_bf16(p[0], p[1]);
-            if constexpr (HL == 1) {                          // the sums take the rounded weights, which the products take
-              p[0] = bf16_lo(hi);
-              p[1] = bf16_hi(hi);
-            }
-            l[2 * b] += p[0];
-            l[2 * b + 1] += p[1];
-            if (!bad) {
-              uint8_t* prow = pbuf + row * 128 + 4 * (lane & 3);
-              const int ch = (hb >> 3) + b;
-              *reinterpret_cast<uint32_t*>(prow + ((ch ^ (row & 7)) << 4)) = hi;
-              if constexpr (HL == 2) {
-                const uint32_t lo = pack_bf16(p[0] - bf16_lo(hi), p[1] - bf16_hi(hi));
-                const int cl = R / 8 + ch;
-                *reinterpret_cast<uint32_t*>(prow + (cl >> 3) * X::CHUNK + (((cl & 7) ^ (row & 7)) << 4)) = lo;
-              }
-            }
+          if (sync(false), gone) break;                       // the scratch is read before P is written over it
           }
-      if (special && !bad) {
-        // V rows that no query row attends to, and that the product reads with p = 0: they may hold anything
-        uint8_t* vst = sm + (X::SHARED ? slot * X::KST : X::V_OFF + slot * X::VST);
-        const int top = (nrows + 15) & ~15;
-        for (int row = warp - 4; row < top; row += 8)
-          if (!((sh.seen[row >> 6] >> (row & 63)) & 1))
-            for (int v = lane; v < X::VC * 8; v += 32) *reinterpret_cast<uint4*>(vst + (v >> 3) * X::CHUNK + row * 128 + (v & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        float top = 0.f;
+        if (raise) {
+          if (!special) {
+#pragma unroll
+            for (int z = 0; z < (NC * 2 * MT + 31) / 32; ++z) bits[z] = 0xffffffffu;
+          }
+          emit(std::true_type());
+        } else {
+          top = emit(std::false_type());
+        }
+        if (raise) break;
+        raise = sync(top > kRowsLazy);
+        retry = true;
+        if (gone || !raise) break;
       }
-      fence_proxy_async_smem();          // the rows written above, for the tensor core
+      if (gone) break;
+#pragma unroll
+      for (int q = 0; q < NC; ++q) l[q] += ts[q];
+      tc_fence_before();
+      fence_proxy_async_smem();            // the rows written above, for the tensor core
       __syncwarp();
-      if (lane == 0 && !bad) mbar_arrive(&bar[RB_PFULL + pb]);
+      if (lane == 0 && !bad) {
+        mbar_arrive(&sh.sempty[sb]);
+        mbar_arrive(&sh.pfull[pb]);
+      }
 
-      if (flags & F_LAST) {
-        // the segment's sums over all cached rows, and the output rows of its query rows
+      if (flags & G_LAST) {
+        // The segment's sums over all cached rows, and behind its last product the output rows of its query rows.  With two
+        // accumulators the groups exchange their states, and each puts together half of the query rows.
 #pragma unroll
-        for (int b = 0; b < 2 * KB; ++b) {
-          float v = l[b];
+        for (int q = 0; q < NC; ++q)
 #pragma unroll
-          for (int o = 4; o <= 16; o <<= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
-          if (lane < 4) sh.red[wq * R + c0 + 8 * (b >> 1) + (b & 1)] = v;
-          if (wq == 0 && lane < 4) sh.offset(c0 + 8 * (b >> 1) + (b & 1)) = m[b];
+          for (int o = 4; o <= 16; o <<= 1) l[q] += __shfl_xor_sync(FULL_MASK, l[q], o);
+        wait(&sh.ofull[wg], ends++);
+        // the four warps' sums, in two steps through the place where the first of them then leaves the state
+        float* part = reinterpret_cast<float*>(sh.state[ob][wg]);
+        const bool puts = lane < 4 && !bad;
+        if (wq >= 2 && puts)
+#pragma unroll
+          for (int q = 0; q < NC; ++q) part[(wq - 2) * R + col(q)] = l[q];
+        if (sync(false), gone) break;
+        if (wq < 2 && puts)
+#pragma unroll
+          for (int q = 0; q < NC; ++q) {
+            l[q] += part[wq * R + col(q)];
+            if (wq == 1) part[R + col(q)] = l[q];
+          }
+        if (sync(false), gone) break;
+        if (wq == 0 && puts)
+#pragma unroll
+          for (int q = 0; q < NC; ++q) l[q] += part[R + col(q)];
+        if (sync(false), gone) break;
+        if (wq == 0 && puts)
+#pragma unroll
+          for (int q = 0; q < NC; ++q) sh.state[ob][wg][col(q)] = make_float2(m[q], l[q]);
+        const bool whole = flags & F_WHOLE, pair = PP && !(flags & G_SOLO);
+        if (!pair && (sync(false), gone)) break;
+        if (pair) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.joined[gi]);
+          wait(&sh.joined[0], joins);
+          wait(&sh.joined[1], joins);
+          ++joins;
         }
-        if (wq == 1 && lane < RG) sh.row(hb + lane) = (int)out_row(a, mt.q0, mt.n, mt.g, mt.row0, hb + lane);
-        named_bar(4 + gi, 128);
-        const bool whole = flags & F_WHOLE;
-        if (wq == 0 && lane < RG) {
-          const int c = hb + lane;
-          const float s = (sh.red[c] + sh.red[R + c]) + (sh.red[2 * R + c] + sh.red[3 * R + c]);
-          sh.factor[c] = whole ? sum_inverse(s) : 1.f;
-          if (!whole) *reinterpret_cast<float2*>(a.ws_ml + ((size_t)mt.part * R + c) * 2) = make_float2(sh.offset(c), s);
+        if (tid < R && !bad) {
+          const float2 own = sh.state[ob][wg][tid];
+          float M = own.x, L = own.y;
+          float2 f = make_float2(1.f, 1.f);
+          if (pair) {
+            const float2 x = sh.state[ob][0][tid], y = sh.state[ob][1][tid];
+            M = fmaxf(x.x, y.x);
+            f = make_float2(x.x == -INFINITY ? 0.f : ex2(x.x - M), y.x == -INFINITY ? 0.f : ex2(y.x - M));
+            L = x.y * f.x + y.y * f.y;
+          }
+          const int2 qh = query_of<X>(a, mt.n, mt.t0, mt.h0, tid);
+          sh.row[ob][tid] = qh.x < 0 ? -1 : (mt.q0 + qh.x) * a.n_h + mt.g * a.G + qh.y;
+          if (whole) {
+            const float inv = sum_inverse(L);
+            f.x *= inv;
+            f.y *= inv;
+          } else if (!pair || gi == 0) {
+            *reinterpret_cast<float2*>(a.ws_ml + ((size_t)mt.part * R + tid) * 2) = make_float2(M, L);
+          }
+          if (!pair || tid / (R / 2) == gi) sh.factor[ob][tid] = f;   // a pair's groups each put together half of the query rows
         }
-        named_bar(4 + gi, 128);
-        bad |= !__all_sync(FULL_MASK, !bad && mbar_wait(&bar[RB_OFULL + ob], (mt.k / X::NO) & 1));
-        if (!bad) {
-          tc_fence_after();
+        if (sync(false), gone) break;
+        tc_fence_after();
+        const int cb = PP ? (pair ? gi * (R / 2) : 0) : hb, cn = PP && !pair ? R : R / 2;
+        const uint32_t oa = tmem + lane_off + ob * NG * VT * N2 + (PP && !pair ? gi * VT * N2 : 0);
 #pragma unroll 1
-          for (int vt = 0; vt < VT; ++vt) {
-            const int chn = vt * X::VM + (X::VM == 128 ? 32 * wq + lane : 16 * wq + lane);
-            const bool mine = X::VM == 128 || lane < 16;
+        for (int vt = 0; vt < VT; ++vt) {
+          const int chn = vt * X::VM + (X::VM == 128 ? 32 * wq + lane : 16 * wq + lane);
+          const bool mine = X::VM == 128 || lane < 16;
+#pragma unroll 1
+          for (int b = 0; b < cn; b += 8) {
+            uint32_t t[NG][HL][8];
 #pragma unroll
-            for (int b = 0; b < KB; ++b) {
-              uint32_t t0[8], t1[8];
-              const uint32_t oc = tmem + lane_off + (ob * VT + vt) * N2 + hb + 8 * b;
-              tmem_ld8(oc, t0);
-              if constexpr (HL == 2) tmem_ld8(oc + R, t1);
-              tmem_wait_ld();
+            for (int g = 0; g < NG; ++g)
+              if (g == 0 || pair)
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int c = hb + 8 * b + e, row = sh.row(c);
-                float v = __uint_as_float(t0[e]);
-                if constexpr (HL == 2) v += __uint_as_float(t1[e]);
-                v *= sh.factor[c];
-                if (row < 0 || !mine) continue;
-                if (whole) store_out(a, (long long)row * DV + chn, v);
-                else a.ws_o[((size_t)mt.part * R + c) * DV + chn] = v;
+                for (int p = 0; p < HL; ++p) tmem_ld8(oa + (g * VT + vt) * N2 + p * R + cb + b, t[g][p]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int c = cb + b + e, row = sh.row[ob][c];
+              const float2 f = sh.factor[ob][c];
+              float v = 0.f;
+#pragma unroll
+              for (int p = HL - 1; p >= 0; --p) v += __uint_as_float(t[0][p][e]);
+              v *= f.x;
+              if constexpr (PP) {
+                if (pair) {
+                  float w = 0.f;
+#pragma unroll
+                  for (int p = HL - 1; p >= 0; --p) w += __uint_as_float(t[NG - 1][p][e]);
+                  v = fmaf(w, f.y, v);
+                }
               }
+              if (row < 0 || !mine) continue;
+              if (!whole) a.ws_o[((size_t)mt.part * R + c) * DV + chn] = v;
+              else if constexpr (X::F32) reinterpret_cast<float*>(a.out)[(size_t)row * DV + chn] = v;
+              else reinterpret_cast<__nv_bfloat16*>(a.out)[(size_t)row * DV + chn] = __float2bfloat16_rn(v);
             }
           }
-          tc_fence_before();
         }
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0 && !bad) mbar_arrive(&bar[RB_OEMPTY + ob]);
-        named_bar(4 + gi, 128);            // sums and rows are read before the next segment's
+        if (lane == 0) mbar_arrive_n(&sh.oempty[ob], PP && !pair ? 2 : 1);
       }
-      if (flags & F_END) break;
-      ++i;
+      if (flags & G_END) break;
     }
     if (bad && lane == 0) {
       set_err(a.err, PKV_DEV_TIMEOUT);
@@ -713,17 +1014,20 @@ __global__ void __launch_bounds__(384, 1)
 
 // ---- parts of cut segments ----------------------------------------------------------------------------
 // A CTA per (boundary, member, 8 query rows, 128 channels): a warp per query row joins the parts of its segment.
-template <int R, int DV>
+template <class X>
 __global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ RowsArgs a) {
-  constexpr int CB = DV < 128 ? DV : 128, V = CB / 32;        // channels of a CTA, of a lane
+  constexpr int R = X::R, DV = X::DV, CB = DV < 128 ? DV : 128, V = CB / 32;   // channels of a CTA, of a lane
   grid_dep_wait();
   grid_dep_launch();
   const int team = blockIdx.x / a.C, member = blockIdx.x % a.C, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const RowsCut cut = a.cuts[team];
   if (cut.parts == 0) return;
-  const int c = blockIdx.y * 8 + warp, row0 = (cut.rg * a.C + member) * a.tile_rows;
-  const long long row = out_row(a, cut.q0, cut.n, cut.g, row0, c);
-  if (row < 0) return;
+  const int c = blockIdx.y * 8 + warp;
+  int t0, h0;
+  tile_of<X>(a, cut.rg * a.C + member, t0, h0);
+  const int2 qh = query_of<X>(a, cut.n, t0, h0, c);
+  if (qh.x < 0) return;
+  const long long row = (long long)(cut.q0 + qh.x) * a.n_h + cut.g * a.G + qh.y;
   auto part = [&](int p) { return (size_t)(((team - 1 + p) * a.C + member) * 2 + (p == 0 ? cut.first : 0)) * R + c; };
   float M = -INFINITY;
   for (int p = lane; p < cut.parts; p += 32) M = fmaxf(M, a.ws_ml[2 * part(p)]);
@@ -766,36 +1070,40 @@ static RowsVariant make_variant() {
   constexpr size_t smem = X::M_OFF + sizeof(RowsShared<X>);
   static_assert(smem <= 232448, "shared memory of one CTA");
   static_assert(X::Q_OFF % 1024 == 0 && X::P_OFF % 1024 == 0 && X::NCOL <= 512, "descriptor alignment, tensor memory");
-  return {(const void*)decode_rows_kernel<X>, (const void*)rows_join_kernel<X::R, X::DV>, smem, X::R, X::DV, {}};
+  return {(const void*)decode_rows_kernel<X>, (const void*)rows_join_kernel<X>, smem, X::R, X::DV, {}};
 }
-template <int BS>
-static RowsVariant* kv_variant(int d, int R) {
-  static RowsVariant v[2][3] = {
-      {make_variant<RowsCfg<BS, 1, 1, 64, false, 16, 2>>(), make_variant<RowsCfg<BS, 1, 1, 64, false, 32, 2>>(),
-       make_variant<RowsCfg<BS, 1, 1, 64, false, 64, 2>>()},
-      {make_variant<RowsCfg<BS, 2, 1, 128, false, 16, 2>>(), make_variant<RowsCfg<BS, 2, 1, 128, false, 32, 2>>(),
-       make_variant<RowsCfg<BS, 2, 1, 128, false, 64, 2>>()}};
-  return &v[d == 128][R == 16 ? 0 : (R == 32 ? 1 : 2)];
+// bf16 outputs take p in two bf16 parts (16 bits) up to 32 query rows and in one with 64, fp32 outputs in three (all 24
+// bits), with 32 query rows at most: more columns do not fit the tensor memory beside a latent cache's O.
+static int variant_index(int R, bool f32) { return f32 ? (R == 16 ? 3 : 4) : (R == 16 ? 0 : (R == 32 ? 1 : 2)); }
+static RowsVariant* kv_variant(int d, int R, bool f32) {
+  static RowsVariant v[2][5] = {
+      {make_variant<RowsCfg<1, 1, 64, false, 16, 2>>(), make_variant<RowsCfg<1, 1, 64, false, 32, 2>>(),
+       make_variant<RowsCfg<1, 1, 64, false, 64, 1>>(), make_variant<RowsCfg<1, 1, 64, false, 16, 3>>(),
+       make_variant<RowsCfg<1, 1, 64, false, 32, 3>>()},
+      {make_variant<RowsCfg<2, 1, 128, false, 16, 2>>(), make_variant<RowsCfg<2, 1, 128, false, 32, 2>>(),
+       make_variant<RowsCfg<2, 1, 128, false, 64, 1>>(), make_variant<RowsCfg<2, 1, 128, false, 16, 3>>(),
+       make_variant<RowsCfg<2, 1, 128, false, 32, 3>>()}};
+  return &v[d == 128][variant_index(R, f32)];
 }
-template <int BS>
-static RowsVariant* latent_variant(int latent, int R) {
-  static RowsVariant v[2][3] = {
-      {make_variant<RowsCfg<BS, 5, 2, 128, true, 16, 2>>(), make_variant<RowsCfg<BS, 5, 2, 128, true, 32, 2>>(),
-       make_variant<RowsCfg<BS, 5, 2, 128, true, 64, 1>>()},
-      {make_variant<RowsCfg<BS, 9, 4, 128, true, 16, 2>>(), make_variant<RowsCfg<BS, 9, 4, 128, true, 32, 2>>(),
-       make_variant<RowsCfg<BS, 9, 4, 128, true, 64, 1>>()}};
-  return &v[latent == 512][R == 16 ? 0 : (R == 32 ? 1 : 2)];
+static RowsVariant* latent_variant(int latent, int R, bool f32) {
+  static RowsVariant v[2][5] = {
+      {make_variant<RowsCfg<5, 2, 128, true, 16, 2>>(), make_variant<RowsCfg<5, 2, 128, true, 32, 2>>(),
+       make_variant<RowsCfg<5, 2, 128, true, 64, 1>>(), make_variant<RowsCfg<5, 2, 128, true, 16, 3>>(),
+       make_variant<RowsCfg<5, 2, 128, true, 32, 3>>()},
+      {make_variant<RowsCfg<9, 4, 128, true, 16, 2>>(), make_variant<RowsCfg<9, 4, 128, true, 32, 2>>(),
+       make_variant<RowsCfg<9, 4, 128, true, 64, 1>>(), make_variant<RowsCfg<9, 4, 128, true, 16, 3>>(),
+       make_variant<RowsCfg<9, 4, 128, true, 32, 3>>()}};
+  return &v[latent == 512][variant_index(R, f32)];
 }
 
 // Query rows of a row tile, and members of a team, from the average of the sequences' query rows per kv head.
 struct RowsShape {
   int R, C, P;
 };
-static RowsShape rows_shape(int n_tok, int batch, int G, int most) {
+static RowsShape rows_shape(int n_tok, int batch, int G, bool f32) {
   const long long rows = ((long long)n_tok * G + batch - 1) / batch;
   RowsShape s;
-  s.R = rows <= 16 && G <= 16 ? 16 : (rows <= 32 && G <= 32 ? 32 : 64);
-  if (s.R > most) s.R = most;
+  s.R = rows <= 16 && G <= 16 ? 16 : (rows <= 32 || f32 ? 32 : 64);
   const long long tiles = (rows + s.R - 1) / s.R;
   s.C = tiles <= 1 ? 1 : (tiles <= 2 ? 2 : 4);
   const int sms = device_sm_count();
@@ -812,6 +1120,13 @@ static RowsLayout rows_layout(const RowsShape& s, int DV) {
   l.o = align_up(l.ml + parts * 2 * sizeof(float), 256);
   l.total = align_up(l.o + parts * DV * sizeof(float), 256);
   return l;
+}
+
+// Enough for either output type; 0 without a device.
+static size_t most_layout(const RowsShape& x, const RowsShape& y, int DV) {
+  if (x.P < 1 || y.P < 1) return 0;
+  const size_t a = rows_layout(x, DV).total, b = rows_layout(y, DV).total;
+  return a > b ? a : b;
 }
 
 static bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -866,10 +1181,15 @@ static pkv_status rows_attn(const RowsShape& s, RowsVariant* v, bool latent, con
   a.max_ctx = max_blocks * block_size;
   a.n_tok = n_tok; a.batch = batch; a.n_h = n_h; a.n_kv = n_kv; a.G = n_h / n_kv;
   a.num_blocks = num_blocks;
+  a.bs_log2 = block_size == 16 ? 4 : (block_size == 32 ? 5 : 6);
   a.n_each = q_start ? 0 : n_tok / batch;
-  a.tile_rows = latent ? s.R : s.R / a.G * a.G;
+  a.gt = a.G < s.R ? a.G : s.R;
+  a.tpt = s.R / a.gt;
+  a.hc = (a.G + a.gt - 1) / a.gt;
+  a.last_steps = (w - v->DV) / 16;
   a.C = s.C; a.P = s.P;
   a.scale_log2 = scale * 1.4426950408889634f;
+  if (a.scale_log2 == 0.f) a.scale_log2 = 1.1754944e-38f;      // a masked score times the scale stays an infinity
   a.out = out;
   a.out_f32 = out_dtype == PKV_OUT_F32;
   a.err = err;
@@ -885,7 +1205,7 @@ static pkv_status rows_attn(const RowsShape& s, RowsVariant* v, bool latent, con
     bad |= encode_tensor_map_3d(&tmq, q, w, (uint64_t)n_tok * n_h, 1, row, row, 64, s.R);
   } else {
     bad |= encode_tensor_map_3d(&tmv, vp, w, rows, nblk, row, rows * row, 64, block_size);
-    bad |= encode_tensor_map_3d(&tmq, q, w, n_h, n_tok, row, n_h * row, 64, a.G, s.R / a.G);
+    bad |= encode_tensor_map_3d(&tmq, q, w, n_h, n_tok, row, n_h * row, 64, a.gt, a.tpt);
   }
   if (bad) return PKV_ECUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -907,8 +1227,8 @@ using namespace pkv;
 extern "C" size_t pkv_tree_workspace_bytes(int batch, int n_tok, int n_h, int n_kv, int head_dim, int block_size) {
   if (batch < 0 || n_tok < 0 || !valid_heads(n_h, n_kv, head_dim, block_size)) return 0;
   if (batch == 0 || n_tok == 0) return 256;
-  const RowsShape s = rows_shape(n_tok, batch, n_h / n_kv, 64);
-  return s.P < 1 ? 0 : rows_layout(s, head_dim).total;
+  const RowsShape x = rows_shape(n_tok, batch, n_h / n_kv, false), y = rows_shape(n_tok, batch, n_h / n_kv, true);
+  return most_layout(x, y, head_dim);
 }
 
 extern "C" pkv_status pkv_paged_tree_attn(const void* q, const void* k_pool, const void* v_pool, const int32_t* block_tables,
@@ -922,23 +1242,18 @@ extern "C" pkv_status pkv_paged_tree_attn(const void* q, const void* k_pool, con
       !valid_step(n_tok, batch, q_start, tree_mask, mask_words, out_dtype, max_blocks, num_blocks))
     return PKV_EINVAL;
   if (n_tok == 0 || batch == 0) return PKV_OK;
-  const RowsShape s = rows_shape(n_tok, batch, n_h / n_kv, 64);
-  RowsVariant* v = block_size == 16 ? kv_variant<16>(head_dim, s.R) : (block_size == 32 ? kv_variant<32>(head_dim, s.R) : kv_variant<64>(head_dim, s.R));
+  const bool f32 = out_dtype == PKV_OUT_F32;
+  const RowsShape s = rows_shape(n_tok, batch, n_h / n_kv, f32);
+  RowsVariant* v = kv_variant(head_dim, s.R, f32);
   return rows_attn(s, v, false, q, k_pool, v_pool, block_tables, max_blocks, context_lens, q_start, tree_mask, mask_words, scale,
                    n_tok, batch, n_h, n_kv, head_dim, block_size, num_blocks, out, out_dtype, workspace, workspace_bytes, err_flag,
                    stream);
 }
 
-// fp32 outputs take p in two parts, which for 64 query rows would not fit the tensor memory: 32 at most.
-static RowsShape latent_shape(int n_tok, int batch, int n_h, bool f32) { return rows_shape(n_tok, batch, n_h, f32 ? 32 : 64); }
-
 extern "C" size_t pkv_latent_workspace_bytes(int batch, int n_tok, int n_h, int latent, int rope, int block_size) {
   if (batch < 0 || n_tok < 0 || !valid_latent(n_h, latent, rope, block_size)) return 0;
   if (batch == 0 || n_tok == 0) return 256;
-  const RowsShape a = latent_shape(n_tok, batch, n_h, false), b = latent_shape(n_tok, batch, n_h, true);
-  if (a.P < 1 || b.P < 1) return 0;
-  const size_t x = rows_layout(a, latent).total, y = rows_layout(b, latent).total;
-  return x > y ? x : y;
+  return most_layout(rows_shape(n_tok, batch, n_h, false), rows_shape(n_tok, batch, n_h, true), latent);
 }
 
 extern "C" pkv_status pkv_paged_latent_attn(const void* q, const void* cache, const int32_t* block_tables, int max_blocks,
@@ -951,8 +1266,9 @@ extern "C" pkv_status pkv_paged_latent_attn(const void* q, const void* cache, co
       !valid_step(n_tok, batch, q_start, tree_mask, mask_words, out_dtype, max_blocks, num_blocks))
     return PKV_EINVAL;
   if (n_tok == 0 || batch == 0) return PKV_OK;
-  const RowsShape s = latent_shape(n_tok, batch, n_h, out_dtype == PKV_OUT_F32);
-  RowsVariant* v = block_size == 16 ? latent_variant<16>(latent, s.R) : (block_size == 32 ? latent_variant<32>(latent, s.R) : latent_variant<64>(latent, s.R));
+  const bool f32 = out_dtype == PKV_OUT_F32;
+  const RowsShape s = rows_shape(n_tok, batch, n_h, f32);
+  RowsVariant* v = latent_variant(latent, s.R, f32);
   return rows_attn(s, v, true, q, cache, cache, block_tables, max_blocks, context_lens, q_start, tree_mask, mask_words, scale, n_tok,
                    batch, n_h, 1, latent + rope, block_size, num_blocks, out, out_dtype, workspace, workspace_bytes, err_flag, stream);
 }

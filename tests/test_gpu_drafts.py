@@ -80,8 +80,10 @@ class Case:
         return out
 
     def single(self):
-        """Whether a bf16 output of this case takes the softmax weights rounded to bf16 once."""
-        return self.latent and self.q.shape[0] * self.n_h > 32 * len(self.ctx)
+        """Whether a bf16 output of this case takes the softmax weights rounded to bf16 once: over 32 query rows per kv
+        head and sequence on average (pkv.h)."""
+        group = self.n_h if self.latent else self.n_h // self.kind[0]
+        return self.q.shape[0] * group > 32 * len(self.ctx)
 
     def check(self, out, ref, what):
         ref, size = ref
