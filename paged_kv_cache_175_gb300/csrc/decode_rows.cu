@@ -80,18 +80,18 @@ struct RowsCfg {
   // chunks, which the second product frees one after another, and NP slots of the position chunk.  The tile's P takes
   // the place of its keys (of their position chunk), which the first product is the only one to read.
   static constexpr bool FULL = SHARED && KC == 9 && R == 64;  // 72 KB of query rows
-  static constexpr int KPART = KC * CHUNK > PBUF ? KC * CHUNK : PBUF;
+  static constexpr int KPART = KC * CHUNK > PBUF + 4096 ? KC * CHUNK : PBUF + 4096;   // P and the scratch behind it
   static constexpr int KST = SHARED ? 2 * CHUNK : KPART + VC * CHUNK;
   static constexpr int PST = SHARED ? PBUF : KST;
   static constexpr int NQ = SHARED && (KC == 9 ? R > 16 : R == 64) ? 1 : 2;
   static constexpr int NK = SHARED ? (FULL || PAT > 1 ? 8 : 9) : (KC == 1 ? 4 : 3);
-  static constexpr int NP = SHARED ? 3 : NK;                  // tiles whose P there is room for
+  static constexpr int NP = SHARED ? (FULL ? 2 : 3) : NK;     // tiles whose P there is room for
   static constexpr int NM = SHARED ? (KC == 9 ? 4 : 8) : NK;  // metadata of tiles: of all that the ring may hold a part of
   static constexpr int NS = PP ? 4 : 2, NG = PP ? 2 : 1;      // S buffers; accumulators of a segment
   static constexpr int NO = VT * N2 * NG * 2 + NS * R <= 512 && !(PP && R == 64) ? 2 : 1;
   static constexpr int S_COL = VT * N2 * NG * NO, NCOL = S_COL + NS * R;
   static constexpr uint32_t TMEM_COLS = NCOL <= 64 ? 64 : (NCOL <= 128 ? 128 : (NCOL <= 256 ? 256 : 512));
-  static constexpr int P_OFF = SHARED ? NK * KST : 0, Q_OFF = NK * KST + (SHARED ? NP * PST : 0), M_OFF = Q_OFF + NQ * QBUF;
+  static constexpr int P_OFF = SHARED ? NK * KST : 0, Q_OFF = NK * KST + (SHARED ? NP * PST : 0), W_OFF = Q_OFF + NQ * QBUF, M_OFF = W_OFF + (SHARED ? 32 * R + 128 : 0);   // W: scratch
   static constexpr bool F32 = HL == 3;                        // output type
 };
 
@@ -119,24 +119,25 @@ struct RowsShared {
   volatile int bad[2][2];                                     // of each group of waiting warps, by the parity of its barriers
   RowsCursor cur, first;         // the member's first tile; the piece's
   long long W;
+  float offset[X::NG][X::R];     // of each query row: what its exponents are taken against
   // Of a segment's end, by its O buffer: offset and sum of each query row in a group's tiles, factors of the output (of
-  // either accumulator), and output rows.  (P's slot is given back with the last product.)
-  float2 state[X::NO][X::NG][X::R], factor[X::NO][X::R];
+  // either accumulator), and output rows
+  float2 sum[X::NO][X::NG][X::R], factor[X::NO][X::R];
   int row[X::NO][X::R];
   long long scan[12];
 };
-// What the warps of a tile share for a moment, in its P buffer while that holds no weights.
+// What the warps of a tile share for a moment: behind its P, or in a place of its own.
 template <class X>
 struct RowsScratch {
   float red[4][X::R];                                         // each warp's part of a query row's maximum or sum
-  float offset[X::R];
+  unsigned long long win[X::MT][X::R], seen[X::MT][2];        // cached rows attended to, by each query row and by any of a warp's
   float factor[X::R];                                         // of a rescale
-  unsigned long long win[X::MT][X::R], seen[X::MT][4];        // cached rows attended to, by each query row and by any of a warp's
 };
 
+static __device__ __noinline__ long long div_far(long long x, long long y) { return x / y; }
 // Quotient of numbers that are hardly ever beyond 32 bits, where a division takes a third of the time.
 __device__ __forceinline__ long long div_pos(long long x, long long y) {
-  return (x | y) >> 32 ? x / y : (long long)((unsigned)x / (unsigned)y);
+  return (x | y) >> 32 ? div_far(x, y) : (long long)((unsigned)x / (unsigned)y);
 }
 // Piece p of a line of W tiles in P pieces starts here: the first W % P pieces are one tile longer.
 struct RowsLine {
@@ -165,7 +166,7 @@ __device__ __forceinline__ long long line_length(const RowsArgs& a, const Drafts
 
 // Moves to the next tile of this member (false: the piece has none left).  Row tiles past the last one are passed over.
 template <class X>
-__device__ __forceinline__ bool rows_settle(RowsCursor& c, const RowsArgs& a, int member) {
+__device__ __noinline__ bool rows_settle(RowsCursor& c, const RowsArgs& a, int member) {
   while (c.left > 0) {
     if (c.t >= c.nt) {
       c.t = 0;
@@ -227,23 +228,51 @@ __device__ __forceinline__ void store_out(const RowsArgs& a, long long at, float
 
 __device__ __forceinline__ unsigned long long ones_below(int b) { return b <= 0 ? 0ull : (b >= 64 ? ~0ull : (1ull << b) - 1); }
 
-// Which of the 64 cached rows from `first` on token i of a sequence attends to.
-__device__ __forceinline__ unsigned long long attended(const RowsArgs& a, const RowsMeta& mt, int i, int first) {
+// Which of the 64 cached rows from `first` on, in the tile `mt`, token i of its sequence attends to.
+static __device__ __noinline__ unsigned long long attended(const RowsArgs& a, const RowsMeta& mt, int i, int first) {
   const int o = mt.ctx - mt.n - first;                        // the first drafted token's row, from `first`
-  const unsigned long long cached = ones_below(mt.ctx - first);
-  if (!a.mask) return ones_below(o + i + 1) & cached;
-  unsigned long long w = 0;
-  if (o < 64) {
+  unsigned long long w;
+  if (!a.mask) {
+    w = ones_below(o + i + 1);
+  } else {
+    w = ones_below(o);
     const int64_t* m = a.mask + (size_t)(mt.q0 + i) * a.mask_words;
-    if (o >= 0) {
-      w = (unsigned long long)m[0] << o;
-    } else {
+    if (o < 64 && o >= 0) w |= (unsigned long long)m[0] << o;
+    if (o < 0) {
       const int q = -o >> 6, r = -o & 63;
-      if (q < a.mask_words) w = (unsigned long long)m[q] >> r;
+      if (q < a.mask_words) w |= (unsigned long long)m[q] >> r;
       if (r && q + 1 < a.mask_words) w |= (unsigned long long)m[q + 1] << (64 - r);
     }
   }
-  return (ones_below(o) | w) & cached;
+  w &= ones_below(mt.ctx - first);
+  // rows of blocks with a bad id
+  unsigned bad = (unsigned)mt.invalid >> ((first - mt.tile0) >> a.bs_log2);
+  for (int b = 0; bad && b < 64 >> a.bs_log2; ++b, bad >>= 1)
+    if (bad & 1) w &= ~(ones_below(1 << a.bs_log2) << (b << a.bs_log2));
+  return w;
+}
+
+// A wait whose polling is out of line: the roles' loops have to fit the instruction cache together.
+static __device__ __noinline__ bool rows_poll(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1; it < (1u << 30); ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 255u) == 0 && global_timer_ns() - t0 > limit_ns) return false;
+  }
+  return false;
+}
+// Of a whole warp, whose lanes leave it together: what follows (elect.sync, tensor memory) wants a converged warp.
+__device__ __forceinline__ bool rows_wait(uint64_t* bar, int round) {
+  const bool done = mbar_try_wait(bar, round & 1) || rows_poll(bar, round & 1, 2000000000ull);
+  const bool all = __all_sync(FULL_MASK, done);
+  __syncwarp();
+  return all;
+}
+// The lane that issues copies and products, of a converged warp.  What it runs is a straight line, and loops are the whole
+// warp's: a rolled loop around tcgen05.mma and its commits in one lane alone ended in an illegal instruction.
+__device__ __forceinline__ bool elected() {
+  __syncwarp();
+  return elect_one();
 }
 
 template <class X>
@@ -262,21 +291,28 @@ __global__ void __launch_bounds__(384, 1)
     return;
   }
 
-  if (threadIdx.x == 0) {
-    sh.abort_flag = 0;
-    sh.any = 0;
-    for (int j = 0; j < 4; ++j) sh.bad[j >> 1][j & 1] = 0;
+  if (warp == 1) tmem_alloc(&sh.tmem, X::TMEM_COLS);
+  if (warp == 2) {
     constexpr int SW = PP ? 4 : 8;         // softmax warps of a tile
-    for (uint64_t* b = sh.kfull; b <= &sh.drain_pv; ++b) {
+    for (uint64_t* b = sh.kfull + lane; b <= &sh.drain_pv; b += 32) {
       const bool softmax = (b >= sh.sempty && b < sh.sempty + NS) || (b >= sh.pfull && b < sh.pfull + NP);
       mbar_init(b, softmax ? SW : (b >= sh.oempty && b < sh.oempty + 2 ? 8 : (b >= sh.joined && b < sh.joined + 2 ? 4 : 1)));
     }
     fence_barrier_init();
+  }
+  if (threadIdx.x == 0) {
+    sh.abort_flag = 0;
+    sh.any = 0;
+    sh.W = 0;
+    for (int j = 0; j < 4; ++j) sh.bad[j >> 1][j & 1] = 0;
     prefetch_tensormap(&tmk);
     if (!X::SHARED) prefetch_tensormap(&tmv);
     prefetch_tensormap(&tmq);
   }
-  if (warp == 1) tmem_alloc(&sh.tmem, X::TMEM_COLS);
+  // query rows past a tile's own hold zeros until the end
+  if constexpr (!X::SHARED)
+    for (int i = threadIdx.x; i < NQ * X::QBUF / 16; i += 384) reinterpret_cast<uint4*>(sm + X::Q_OFF)[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
   tc_fence_before();
   grid_dep_wait();
   grid_dep_launch();
@@ -289,6 +325,7 @@ __global__ void __launch_bounds__(384, 1)
     long long mine = 0;
     int flags = 0;
     Drafts d = {};
+#pragma unroll 1
     for (int s = s0; s < s1; ++s) {
       d = drafts_of(a.ctx, a.q_start, a.n_each, a.n_tok, a.max_ctx, s, flags);
       mine += line_length<X>(a, d);
@@ -312,174 +349,169 @@ __global__ void __launch_bounds__(384, 1)
     before += incl - mine;
     const RowsLine line(W, a.P);
     const long long pstart = line.start(team);
-    if (team < line.P) {
-      if (pstart >= before && pstart < before + mine) {
-        RowsCursor c;
-        long long off = pstart - before;
-        c.s = s0;
-        c.d = d;                             // with a sequence per thread it is the one
-        if (per > 1)
-          for (;; ++c.s) {
-            c.d = drafts_of(a.ctx, a.q_start, a.n_each, a.n_tok, a.max_ctx, c.s, flags);
-            const long long len = line_length<X>(a, c.d);
-            if (off < len || c.s + 1 >= s1) break;
-            off -= len;
-          }
-        c.nt = max(1, (c.d.ctx + TT - 1) / TT);
-        c.rt = row_tiles<X>(a, c.d.n);
-        const int groups = max(1, (c.rt + a.C - 1) / a.C);
-        const long long seg_at = div_pos(off, c.nt);          // segment of the sequence
-        c.t = (int)(off - seg_at * c.nt);
-        c.g = (int)div_pos(seg_at, groups);
-        c.rg = (int)(seg_at - (long long)c.g * groups);
-        c.at_start = 1;
-        c.whole_from = c.t == 0;
-        c.left = line.start(team + 1) - pstart;
-        sh.first = c;
-        sh.W = W;
-        const bool any = rows_settle<X>(c, a, member);
-        sh.cur = c;
-        ++c.t;
-        --c.left;
-        sh.any = any ? (rows_settle<X>(c, a, member) ? 2 : 1) : 0;
-      }
-    } else if (threadIdx.x == 0) {
-      sh.W = 0;
+    if (team < line.P && pstart >= before && pstart < before + mine) {
+      RowsCursor c;
+      long long off = pstart - before;
+      c.s = s0;
+      c.d = d;                             // with a sequence per thread it is the one
+      if (per > 1)
+#pragma unroll 1
+        for (;; ++c.s) {
+          c.d = drafts_of(a.ctx, a.q_start, a.n_each, a.n_tok, a.max_ctx, c.s, flags);
+          const long long len = line_length<X>(a, c.d);
+          if (off < len || c.s + 1 >= s1) break;
+          off -= len;
+        }
+      c.nt = max(1, (c.d.ctx + TT - 1) / TT);
+      c.rt = row_tiles<X>(a, c.d.n);
+      const int groups = max(1, (c.rt + a.C - 1) / a.C);
+      const long long seg_at = div_pos(off, c.nt);            // segment of the sequence
+      c.t = (int)(off - seg_at * c.nt);
+      c.g = (int)div_pos(seg_at, groups);
+      c.rg = (int)(seg_at - (long long)c.g * groups);
+      c.at_start = 1;
+      c.whole_from = c.t == 0;
+      c.left = line.start(team + 1) - pstart;
+      sh.first = c;
+      sh.W = W;
+      const bool any = rows_settle<X>(c, a, member);
+      sh.cur = c;
+      ++c.t;
+      --c.left;
+      sh.any = any ? (rows_settle<X>(c, a, member) ? 2 : 1) : 0;
     }
   }
-  // query rows past a tile's own hold zeros until the end
-  if constexpr (!X::SHARED)
-    for (int i = threadIdx.x; i < NQ * X::QBUF / 16; i += 384) reinterpret_cast<uint4*>(sm + X::Q_OFF)[i] = make_uint4(0u, 0u, 0u, 0u);
-  fence_proxy_async_smem();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
-  if (warp == 3 && lane == 0 && member == 0) {
-    // whether the piece's start cuts a segment for the first time, for the kernel that joins the parts
-    RowsCut cut = {};
-    if (sh.W > 0) {
-      const RowsLine line(sh.W, a.P);
-      const RowsCursor& c = sh.first;
-      const long long pstart = line.start(team), seg = pstart - c.t, prev = team > 0 ? line.start(team - 1) : 0;
-      if (c.t > 0 && prev <= seg) {
-        const int last = min(line.piece(min(seg + c.nt, line.W) - 1), line.P - 1);   // the last piece that holds a part
-        cut.parts = last - team + 2;
-        cut.first = prev == seg ? 0 : 1;
-        cut.q0 = c.d.q0; cut.n = c.d.n; cut.g = c.g; cut.rg = c.rg;
-      }
-    }
-    a.cuts[team] = cut;
-  }
-  __syncwarp();
-  if (sh.any && warp == 0) {
-    // ------------------------------- producer --------------------------------
+  if (sh.any && (warp == 0 || warp == 3)) {
+    // ------------------------------- producers -------------------------------
+    // Both walk the piece.  Warp 0 loads the queries, the tile's metadata and its keys, or the first half of a latent
+    // cache's chunks; warp 3 the values, or the other half and the position chunk.  The whole warp runs the loop
+    // and one lane (elect_one) issues the copies in unrolled runs: about 30 clocks each, where a lane per copy
+    // or a loop around one takes 60 to 90, which bounded the kernel with blocks of 16.
+    const bool lead = warp == 0;
     const int bsz = 1 << a.bs_log2, nbt = TT >> a.bs_log2;    // rows of a block, blocks of a tile
     const uint64_t pol = policy_evict_first();
     RowsCursor c = sh.cur;
-    int k = -1, kq = -1, i = 0, slots = 0;                    // slots: of a latent cache's ring, issued so far
-    struct Tile {
-      RowsMeta m;
-      int nblk, phys, idx;                                    // idx: number of the tile in its segment, within the piece
-    };
-    // the tile at the cursor, which then moves on; false when it was the last one
-    auto describe = [&](Tile& t, int prev_idx) {
-      const bool first = k < 0 || c.t == 0;
-      if (first) ++k;
-      t.idx = first ? 0 : prev_idx + 1;
-      t.m.k = k;
-      t.m.tile0 = c.t * TT;
-      t.m.ctx = c.d.ctx; t.m.n = c.d.n; t.m.q0 = c.d.q0;
-      tile_of<X>(a, c.rg * a.C + member, t.m.t0, t.m.h0);
-      t.m.g = c.g;
-      t.m.part = blockIdx.x * 2 + (c.at_start ? 0 : 1);
-      const int blk0 = c.t * nbt, nb = (c.d.ctx + bsz - 1) >> a.bs_log2;
-      t.nblk = min(nb - blk0, nbt);
-      const int32_t* row = a.bt + (size_t)c.s * a.max_blocks + blk0;
-      t.phys = lane < t.nblk ? row[lane] : -1;
-      const bool seg_end = c.t + 1 == c.nt;
-      t.m.flags = (first ? F_FIRST : 0) | (seg_end || c.left == 1 ? F_LAST : 0) | (seg_end && c.whole_from ? F_WHOLE : 0);
-      ++c.t;
-      --c.left;
-      const bool more = rows_settle<X>(c, a, member);
-      if (!more) t.m.flags |= F_END;
-      return more;
-    };
-    Tile t, tn;
-    bool more = describe(t, 0), ok = true;
-    auto waited = [&](uint64_t* bar, int round) {             // of the whole warp: for a slot's use number `round` to be over
-      bool w = !sh.abort_flag;
-      if (w && round >= 0 && lane == 0) w = mbar_wait(bar, round & 1);
-      return __shfl_sync(FULL_MASK, w, 0) != 0;
-    };
+    int k = -1, kq = -1, i = -1;
+    RowsMeta m = {}, mn = {};                                 // the tile to load, and the one behind it
+    int phys = -1, physn = -1, idx = 0, idxn = -1;            // block ids; number of the tile in its segment, within the piece
+    unsigned used = 0, usedn = 0;                             // blocks of the tile
+    bool more = true, ok = true;
+#pragma unroll 1
     for (;; ++i) {
-      bool more2 = false;
-      if (more) more2 = describe(tn, t.idx);                  // its block ids in flight
-      // what the tile is to its softmax group
-      int flags = t.m.flags;
-      const bool next_last = more && tn.m.k == t.m.k && (tn.m.flags & F_LAST);
-      if (t.idx < (PP ? 2 : 1)) flags |= G_FIRST;
-      if ((flags & F_LAST) || (PP && next_last)) flags |= G_LAST;
-      if (PP && next_last) flags |= tn.m.flags & F_WHOLE;
-      if ((flags & F_END) || (PP && more && (tn.m.flags & F_END))) flags |= G_END;
-      if (t.idx == 0 && (flags & F_LAST)) flags |= G_SOLO;
-      t.m.flags = flags;
-      const bool okb = lane < t.nblk && (unsigned)t.phys < (unsigned)a.num_blocks;
-      const unsigned invalid = __ballot_sync(FULL_MASK, lane < t.nblk && !okb), valid = __ballot_sync(FULL_MASK, okb);
-      t.m.invalid = (int)invalid;
-      if (lane == 0 && invalid) set_err(a.err, PKV_DEV_BAD_BLOCK);
-      // The segment's query rows.  With one buffer for them they come behind the tile, which need not wait for the
-      // last segment's products.
-      auto queries = [&] {
-        const int qb = t.m.k % NQ;
-        ok = waited(&sh.qempty[qb], t.m.k / NQ - 1);
-        if (!ok) return;
-        if (lane == 0) {
-          const uint32_t rows = X::SHARED ? R : a.gt * a.tpt;
-          mbar_arrive_expect_tx(&sh.qfull[qb], (uint32_t)KC * 128u * rows);
-          for (int ch = 0; ch < KC; ++ch) {
-            uint8_t* qd = sm + X::Q_OFF + qb * X::QBUF + ch * X::QCH;
-            if constexpr (X::SHARED) tma_load_3d(qd, &tmq, ch * 64, (t.m.q0 + t.m.t0) * a.n_h + t.m.h0, 0, &sh.qfull[qb], pol);
-            else tma_load_3d(qd, &tmq, ch * 64, t.m.g * a.G + t.m.h0, t.m.q0 + t.m.t0, &sh.qfull[qb], pol);
-          }
+      // The tile at the cursor is described a round before it is loaded, with its block ids in flight meanwhile; the first
+      // round only does that.
+      const bool has = more;
+      if (has) {
+        const bool first = k < 0 || c.t == 0;
+        if (first) {
+          ++k;
+          tile_of<X>(a, c.rg * a.C + member, mn.t0, mn.h0);
         }
-        kq = t.m.k;
-      };
-      const bool asks = flags & F_FIRST;
-      if (NQ > 1 && asks) queries();
-      if (!ok) break;
-      // One fill of a slot: `nc` chunks from channel c0 on, of each block; lane: one box of 64 channels of one block.
-      auto fill = [&](uint8_t* dst, uint64_t* full, const CUtensorMap* tm, int c0, int nc) {
-        if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)__popc(valid) * (uint32_t)(nc * 128) << a.bs_log2);
-        __syncwarp();
-        const int b = lane / nc, ch = lane - b * nc;
-        const int pb = __shfl_sync(FULL_MASK, t.phys, b & 31);
-        if (b < t.nblk && ((valid >> b) & 1))
-          tma_load_3d(dst + ch * X::CHUNK + (b << a.bs_log2) * 128, tm, c0 + ch * 64, t.m.g << a.bs_log2, pb, full, pol);
-      };
-      if constexpr (X::SHARED) {
-        for (int vt = 0; vt < VT && ok; ++vt, ++slots) {
-          const int slot = slots % NK;
-          ok = waited(&sh.kempty[slot], slots / NK - 1);
-          if (!ok) break;
-          if (vt == 0 && lane == 0) sh.meta[i % NM] = t.m;
-          fill(sm + slot * X::KST, &sh.kfull[slot], &tmk, vt * 128, 2);
-        }
-        if (ok) ok = waited(&sh.pslot[i % NP], i / NP - 1);
-        if (!ok) break;
-        fill(sm + X::P_OFF + (i % NP) * X::PST, &sh.vfull[i % NP], &tmk, VT * 128, 1);
-      } else {
-        ok = waited(&sh.kempty[i % NK], i / NK - 1);
-        if (!ok) break;
-        if (lane == 0) sh.meta[i % NM] = t.m;
-        fill(sm + (i % NK) * X::KST, &sh.kfull[i % NK], &tmk, 0, KC);
-        fill(sm + (i % NK) * X::KST + X::KPART, &sh.vfull[i % NK], &tmv, 0, X::VC);
+        idxn = first ? 0 : idxn + 1;
+        mn.k = k;
+        mn.tile0 = c.t * TT;
+        mn.ctx = c.d.ctx; mn.n = c.d.n; mn.q0 = c.d.q0;
+        mn.g = c.g;
+        mn.part = blockIdx.x * 2 + (c.at_start ? 0 : 1);
+        const int blk0 = c.t * nbt, nb = (c.d.ctx + bsz - 1) >> a.bs_log2;
+        usedn = (1u << min(nb - blk0, nbt)) - 1;
+        physn = (usedn >> lane) & 1 ? a.bt[(size_t)c.s * a.max_blocks + blk0 + lane] : -1;
+        const bool seg_end = c.t + 1 == c.nt;
+        mn.flags = (first ? F_FIRST : 0) | (seg_end || c.left == 1 ? F_LAST : 0) | (seg_end && c.whole_from ? F_WHOLE : 0);
+        ++c.t;
+        --c.left;
+        more = rows_settle<X>(c, a, member);
+        if (!more) mn.flags |= F_END;
       }
-      if (NQ == 1 && asks) queries();
-      if (!ok || !more) break;
-      t = tn;
-      more = more2;
+      if (i >= 0) {
+        if (sh.abort_flag) break;
+        const unsigned valid = __ballot_sync(FULL_MASK, (unsigned)phys < (unsigned)a.num_blocks);
+        const uint32_t chunk_bytes = (uint32_t)__popc(valid) * 128u << a.bs_log2;
+        if (lead) {
+          // what the tile is to its softmax group
+          const bool next_last = has && mn.k == m.k && (mn.flags & F_LAST);
+          if (idx < (PP ? 2 : 1)) m.flags |= G_FIRST;
+          if (idx == 0 && (m.flags & F_LAST)) m.flags |= G_SOLO;
+          if ((m.flags & F_LAST) || (PP && next_last)) m.flags |= G_LAST;
+          if ((m.flags & F_END) || (PP && has && (mn.flags & F_END))) m.flags |= G_END;
+          if (PP && next_last) m.flags |= mn.flags & F_WHOLE;
+          m.invalid = (int)(used & ~valid);
+          if (lane == 0 && m.invalid) set_err(a.err, PKV_DEV_BAD_BLOCK);
+        }
+        // The segment's query rows.  With one buffer for them they come behind the tile, which need not wait for the
+        // last segment's products.
+        const bool asks = lead && (m.flags & F_FIRST);
+        auto queries = [&] {
+          const int qb = m.k % NQ;
+          ok = m.k < NQ || rows_wait(&sh.qempty[qb], m.k / NQ - 1);
+          if (!ok) return;
+          if (elected()) mbar_arrive_expect_tx(&sh.qfull[qb], (uint32_t)KC * 128u * (uint32_t)(X::SHARED ? R : a.gt * a.tpt));
+#pragma unroll 1
+          for (int ch = 0; ch < KC; ++ch)
+            if (elected())
+              tma_load_3d(sm + X::Q_OFF + qb * X::QBUF + ch * X::QCH, &tmq, ch * 64,
+                          X::SHARED ? (m.q0 + m.t0) * a.n_h + m.h0 : m.g * a.G + m.h0, X::SHARED ? 0 : m.q0 + m.t0, &sh.qfull[qb], pol);
+          kq = m.k;
+          __syncwarp();
+        };
+        if (NQ > 1 && asks) queries();
+        if (!ok) break;
+        // one fill of a slot: NC chunks from channel c0 on, of each block
+        constexpr int MB = TT / 16;
+        int ids[MB];
+#pragma unroll
+        for (int b = 0; b < MB; ++b) ids[b] = __shfl_sync(FULL_MASK, phys, b);
+        const int grow = m.g << a.bs_log2, step = 128 << a.bs_log2;
+        auto fill = [&](uint8_t* dst, uint64_t* full, const CUtensorMap* tm, int c0, auto chunks_of) {
+          constexpr int NC = decltype(chunks_of)::value;
+          if (elected()) {
+            mbar_arrive_expect_tx(full, chunk_bytes * NC);
+#pragma unroll
+            for (int b = 0; b < MB; ++b)
+              if ((valid >> b) & 1) {
+#pragma unroll
+                for (int ch = 0; ch < NC; ++ch) tma_load_3d(dst + ch * X::CHUNK + b * step, tm, c0 + ch * 64, grow, ids[b], full, pol);
+              }
+          }
+          __syncwarp();
+        };
+        if constexpr (X::SHARED) {
+#pragma unroll 1
+          for (int v = 0; v < VT / 2 && ok; ++v) {
+            const int vt = lead ? v : VT / 2 + v, use = i * VT + vt, slot = use % NK;
+            ok = use < NK || rows_wait(&sh.kempty[slot], use / NK - 1);
+            if (!ok) break;
+            if (lead && v == 0 && lane == 0) sh.meta[i % NM] = m;
+            __syncwarp();
+            fill(sm + slot * X::KST, &sh.kfull[slot], &tmk, vt * 128, std::integral_constant<int, 2>());
+          }
+          if (ok && !lead) {
+            ok = i < NP || rows_wait(&sh.pslot[i % NP], i / NP - 1);
+            if (ok) fill(sm + X::P_OFF + (i % NP) * X::PST, &sh.vfull[i % NP], &tmk, VT * 128, std::integral_constant<int, 1>());
+          }
+        } else {
+          const int st = i % NK;
+          ok = i < NK || rows_wait(&sh.kempty[st], i / NK - 1);
+          if (!ok) break;
+          if (lead && lane == 0) sh.meta[i % NM] = m;
+          __syncwarp();
+          fill(sm + st * X::KST + (lead ? 0 : X::KPART), lead ? &sh.kfull[st] : &sh.vfull[st], lead ? &tmk : &tmv, 0,
+               std::integral_constant<int, KC>());
+        }
+        if (!ok) break;
+        if (NQ == 1 && asks) queries();
+        if (!ok || !has) break;
+      }
+      m = mn;
+      phys = physn;
+      used = usedn;
+      idx = idxn;
     }
+    ok = __all_sync(FULL_MASK, ok);
     if (!ok && lane == 0) {
       set_err(a.err, PKV_DEV_TIMEOUT);
       sh.abort_flag = 1;
@@ -487,61 +519,64 @@ __global__ void __launch_bounds__(384, 1)
     // After a timeout: let the loads already issued land before the CTA leaves (bounded).
     if (sh.abort_flag && lane == 0) {
       bool live = true;
-      const int nk = X::SHARED ? slots : i + 1;
-      for (int j = max(0, nk - NK - 1); j < nk && live; ++j) live = mbar_wait(&sh.kfull[j % NK], (j / NK) & 1, 20000000ull);
-      for (int j = max(0, i - NP); j <= i && live; ++j) live = mbar_wait(&sh.vfull[j % NP], (j / NP) & 1, 20000000ull);
-      if (kq >= 0) mbar_wait(&sh.qfull[kq % NQ], (kq / NQ) & 1, 20000000ull);
+      const int nk = X::SHARED ? (i + 1) * VT : i + 1;
+      for (int j = max(0, nk - NK - 1); j < nk && live; ++j) live = rows_poll(&sh.kfull[j % NK], (j / NK) & 1, 20000000ull);
+      live = true;
+      for (int j = max(0, i - NP); j <= i && live; ++j) live = rows_poll(&sh.vfull[j % NP], (j / NP) & 1, 20000000ull);
+      if (kq >= 0) rows_poll(&sh.qfull[kq % NQ], (kq / NQ) & 1, 20000000ull);
     }
     __syncwarp();
   } else if (sh.any && warp == 1) {
     // ------------------------- first-product issuer -------------------------
-    // The whole warp runs the loop and one lane issues (elect_one).
     constexpr uint32_t IQK = umma_idesc_bf16(TT, R, 0, 0);
     constexpr uint32_t HI = (uint32_t)(umma_desc_k(16, 1024) >> 32);
     const uint32_t sbase = (uint32_t)umma_desc_k(16, 1024) + (smem_u32(sm) >> 4);
     const uint32_t tm = __shfl_sync(FULL_MASK, tmem, 0);
-    const bool leader = elect_one();
     bool ok = true;
+#pragma unroll 1
     for (int i = 0;; ++i) {
       const int k0 = X::SHARED ? i * VT : i, sb = i % NS;     // first slot of the tile's keys
-      if (sh.abort_flag || !mbar_wait(&sh.kfull[k0 % NK], (k0 / NK) & 1)) {
-        ok = false;
-        break;
-      }
+      ok = !sh.abort_flag && rows_wait(&sh.kfull[k0 % NK], k0 / NK);
+      if (!ok) break;
       const RowsMeta& mt = sh.meta[i % NM];
       const int flags = __shfl_sync(FULL_MASK, mt.flags, 0), k = __shfl_sync(FULL_MASK, mt.k, 0), qb = k % NQ;
-      if (((flags & F_FIRST) && !mbar_wait(&sh.qfull[qb], (k / NQ) & 1)) || (i >= NS && !mbar_wait(&sh.sempty[sb], (i / NS - 1) & 1))) {
-        ok = false;
-        break;
-      }
+      ok = (!(flags & F_FIRST) || rows_wait(&sh.qfull[qb], k / NQ)) && (i < NS || rows_wait(&sh.sempty[sb], i / NS - 1));
+      if (!ok) break;
       const uint32_t qa = sbase + ((X::Q_OFF + qb * X::QBUF) >> 4), d = tm + X::S_COL + R * sb;
-      // chunks [ch0, ch0 + nc) of the keys, at ka: four steps of 16 channels each
-      auto chunks = [&](uint32_t ka, int ch0, int nc, int steps) {
-        tc_fence_after();
-        __syncwarp();
-        if (leader) {
-          uint32_t qc = qa + ch0 * (X::QCH >> 4);
-#pragma unroll 1
-          for (int ch = 0; ch < nc; ++ch, ka += X::CHUNK >> 4, qc += X::QCH >> 4)
+      tc_fence_after();
+      // Chunks [ch0, ch0 + NC) of the keys, at ka, four steps of 16 channels each.  Loops are the warp's; what the elected
+      // lane runs is a straight line.
+      auto chunks = [&](uint32_t ka, int ch0, int steps, auto chunks_of) {
+        constexpr int NC = decltype(chunks_of)::value;
+        const uint32_t qc = qa + ch0 * (X::QCH >> 4), first = ch0 == 0 ? 0u : 1u;
+        if (elected()) {
+#pragma unroll
+          for (int ch = 0; ch < NC; ++ch)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              if (ks < steps) umma_bf16_lo(d, ka + ks * 2, HI, qc + ks * 2, HI, IQK, ks > 0 || ch > 0 || ch0 > 0 ? 1u : 0u);
+              if (ks < steps)
+                umma_bf16_lo(d, ka + ch * (X::CHUNK >> 4) + ks * 2, HI, qc + ch * (X::QCH >> 4) + ks * 2, HI, IQK, ch + ks ? 1u : first);
         }
         __syncwarp();
       };
       if constexpr (X::SHARED) {
-        for (int vt = 0; vt < VT && ok; ++vt) {
-          const int slot = (k0 + vt) % NK;
-          if (vt > 0) ok = mbar_wait(&sh.kfull[slot], ((k0 + vt) / NK) & 1);
-          if (ok) chunks(sbase + (slot * X::KST >> 4), 2 * vt, 2, 4);
+        // slots as they are loaded, and the position chunk
+#pragma unroll 1
+        for (int u = 0; u < VT && ok; ++u) {
+          const int slot = (k0 + u) % NK;
+          if (u > 0) ok = rows_wait(&sh.kfull[slot], (k0 + u) / NK);
+          if (!ok) break;
+          tc_fence_after();
+          chunks(sbase + (slot * X::KST >> 4), 2 * u, 4, std::integral_constant<int, 2>());
         }
-        ok = ok && mbar_wait(&sh.vfull[i % NP], (i / NP) & 1);
+        ok = ok && rows_wait(&sh.vfull[i % NP], i / NP);
         if (!ok) break;
-        chunks(sbase + ((X::P_OFF + (i % NP) * X::PST) >> 4), KC - 1, 1, a.last_steps);
+        tc_fence_after();
+        chunks(sbase + ((X::P_OFF + (i % NP) * X::PST) >> 4), KC - 1, a.last_steps, std::integral_constant<int, 1>());
       } else {
-        chunks(sbase + ((i % NK) * X::KST >> 4), 0, KC, 4);
+        chunks(sbase + ((i % NK) * X::KST >> 4), 0, 4, std::integral_constant<int, KC>());
       }
-      if (leader) {
+      if (elected()) {
         umma_commit(&sh.sfull[sb]);
         if (flags & F_LAST) umma_commit(&sh.qempty[qb]);
       }
@@ -549,48 +584,42 @@ __global__ void __launch_bounds__(384, 1)
       if (flags & F_END) break;
     }
     ok = __all_sync(FULL_MASK, ok);
-    if (leader) {
+    if (elected()) {
       if (!ok) {
         set_err(a.err, PKV_DEV_TIMEOUT);
         sh.abort_flag = 1;
       }
       // every product issued has completed before the tensor memory is released
       umma_commit(&sh.drain);
-      mbar_wait(&sh.drain, 0);
     }
-    __syncwarp();
+    rows_wait(&sh.drain, 0);
   } else if (sh.any && warp == 2) {
     // ------------------------- second-product issuer ------------------------
     constexpr uint32_t IPV = umma_idesc_bf16(X::VM, N2, 1, 1);
     constexpr uint32_t HI = (uint32_t)(umma_desc_k(X::CHUNK, 1024) >> 32);
     const uint32_t sbase = (uint32_t)umma_desc_k(X::CHUNK, 1024) + (smem_u32(sm) >> 4);
     const uint32_t tm = __shfl_sync(FULL_MASK, tmem, 0);
-    const bool leader = elect_one();
     bool ok = true;
+#pragma unroll 1
     for (int i = 0;; ++i) {
       const int pb = i % NP, k0 = i * VT;
-      if (sh.abort_flag || !mbar_wait(X::SHARED ? &sh.kfull[k0 % NK] : &sh.vfull[pb], (X::SHARED ? k0 / NK : i / NP) & 1) ||
-          !mbar_wait(&sh.pfull[pb], (i / NP) & 1)) {
-        ok = false;
-        break;
-      }
+      ok = !sh.abort_flag && rows_wait(X::SHARED ? &sh.kfull[k0 % NK] : &sh.vfull[pb], X::SHARED ? k0 / NK : i / NP) &&
+           rows_wait(&sh.pfull[pb], i / NP);
+      if (!ok) break;
       const RowsMeta& mt = sh.meta[i % NM];
       const int flags = __shfl_sync(FULL_MASK, mt.flags, 0), k = __shfl_sync(FULL_MASK, mt.k, 0), ob = k % NO;
       const int nks = __shfl_sync(FULL_MASK, (min(TT, mt.ctx - mt.tile0) + 15) >> 4, 0);
-      if ((flags & F_FIRST) && k >= NO && !mbar_wait(&sh.oempty[ob], (k / NO - 1) & 1)) {
-        ok = false;
-        break;
-      }
+      ok = !(flags & F_FIRST) || k < NO || rows_wait(&sh.oempty[ob], k / NO - 1);
+      if (!ok) break;
       tc_fence_after();
       __syncwarp();
-      const uint32_t pa = sbase + ((X::P_OFF + pb * X::PST) >> 4), d = tm + (ob * NG + (PP ? i & 1 : 0)) * VT * N2;
-      const uint32_t acc0 = flags & G_FIRST ? 0u : 1u;
+      const uint32_t pa = sbase + ((X::P_OFF + pb * X::PST) >> 4), acc0 = flags & G_FIRST ? 0u : 1u;
+      const uint32_t d = tm + (ob * NG + (PP ? i & 1 : 0)) * VT * N2;
 #pragma unroll 1
       for (int vt = 0; vt < VT; ++vt) {
         const int slot = X::SHARED ? (k0 + vt) % NK : i % NK;
-        if (X::SHARED && vt > 0) ok = ok && mbar_wait(&sh.kfull[slot], ((k0 + vt) / NK) & 1);   // it landed before the first product
         const uint32_t vb = sbase + ((slot * X::KST + (X::SHARED ? 0 : X::KPART)) >> 4);
-        if (leader && ok) {
+        if (elected()) {
 #pragma unroll
           for (int kk = 0; kk < TT / 16; ++kk)
             if (kk < nks) umma_bf16_lo(d + vt * N2, vb + kk * 128, HI, pa + kk * 128, HI, IPV, kk ? 1u : acc0);
@@ -598,8 +627,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         __syncwarp();
       }
-      if (!ok) break;
-      if (leader) {
+      if (elected()) {
         if (X::SHARED) umma_commit(&sh.pslot[pb]);
         umma_commit(&sh.pempty[i & 1]);
         if (flags & F_LAST) {              // for the groups that had tiles of the segment
@@ -611,24 +639,15 @@ __global__ void __launch_bounds__(384, 1)
       if (flags & F_END) break;
     }
     ok = __all_sync(FULL_MASK, ok);
-    if (leader) {
+    if (elected()) {
       if (!ok) {
         set_err(a.err, PKV_DEV_TIMEOUT);
         sh.abort_flag = 1;
       }
       umma_commit(&sh.drain_pv);
-      mbar_wait(&sh.drain_pv, 0);
     }
-    __syncwarp();
+    rows_wait(&sh.drain_pv, 0);
   } else if (warp >= 4) {
-    // Sequences without cached rows: their tokens' outputs are zeros
-    for (int s = blockIdx.x; s < a.batch; s += gridDim.x) {
-      int flags = 0;
-      const Drafts d = drafts_of(a.ctx, a.q_start, a.n_each, a.n_tok, a.max_ctx, s, flags);
-      if (d.ctx > 0 || d.n == 0) continue;
-      const long long at = (long long)d.q0 * a.n_h * DV, len = (long long)d.n * a.n_h * DV;
-      for (long long e = threadIdx.x - 128; e < len; e += 256) store_out(a, at + e, 0.f);
-    }
     // -------------------------- softmax and epilogue ------------------------
     // Warp w reaches the tensor-memory lanes of quarter w % 4: in S^T the cached rows 16 MT wq + ..., in fragments of
     // 16 rows x 8 query rows, in O^T the channels 32 wq + lane.
@@ -640,9 +659,8 @@ __global__ void __launch_bounds__(384, 1)
     const int wg = PP ? gi : 0, tid = (threadIdx.x - 128) & (NW - 1);
     const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
     const int r0 = 16 * MT * wq + (lane >> 2), c0 = hb + 2 * (lane & 3);   // this thread's first cached row and query row
-    auto col = [&](int q) { return c0 + 8 * (q >> 1) + (q & 1); };
-    // Offsets and this thread's rows' share of the sums, of its query rows.
-    float m[NC], l[NC];
+    float* off = sh.offset[wg];            // offsets of the query rows, minus infinity where there is none yet
+    float l[NC];                           // this thread's rows' share of the sums of its query rows
     bool was_special = false;
     // Barriers among the threads of a tile.  A failed (timed-out) wait makes `bad` true for its warp, which raises a flag ahead
     // of the next barrier; behind that all of them see it and leave together, so no thread is left at a barrier.  The
@@ -650,15 +668,19 @@ __global__ void __launch_bounds__(384, 1)
     bool bad = false, gone = false;
     int turn = 0, joins = 0, ends = 0;     // barriers, exchanges and segments so far
     auto sync = [&](bool pred) {
-      if (bad && lane == 0) sh.bad[wg][turn & 1] = 1;
+      if (bad) sh.bad[wg][turn & 1] = 1;
       __syncwarp();
       const bool any = named_bar_or(1 + wg, NW, pred || bad);
       if (any && sh.bad[wg][turn & 1]) gone = true;
       ++turn;
       return any;
     };
-    auto wait = [&](uint64_t* bar, int round) { bad |= !__all_sync(FULL_MASK, !bad && !sh.abort_flag && mbar_wait(bar, round & 1)); };
+    auto wait = [&](uint64_t* bar, int round) {               // nothing but that a wait failed, or one of another role did, ends it early
+      bad = __any_sync(FULL_MASK, bad || sh.abort_flag);
+      if (!bad) bad = !rows_wait(bar, round);
+    };
 
+#pragma unroll 1
     for (int i = PP ? gi : 0; sh.any > (PP ? gi : 0); i += PP ? 2 : 1) {
       const int pb = i % NP, sb = i % NS, k0 = X::SHARED ? i * VT : i;
       // A barrier tells a phase from the one before it only by parity, and this group may not have waited for that.  It is
@@ -670,27 +692,152 @@ __global__ void __launch_bounds__(384, 1)
         sync(true);
         break;
       }
-      const RowsMeta mt = sh.meta[i % NM];
-      const int flags = mt.flags, ob = mt.k % NO, acc = (ob * NG + (PP ? gi : 0)) * VT * N2;
+      const RowsMeta& mt = sh.meta[i % NM];
+      const int flags = mt.flags, ob = mt.k % NO;
       const bool special = mt.tile0 + TT > mt.ctx - mt.n || mt.invalid;
       uint8_t* pbuf = sm + X::P_OFF + pb * X::PST;
-      RowsScratch<X>& scr = *reinterpret_cast<RowsScratch<X>*>(pbuf);
+      RowsScratch<X>& scr = *reinterpret_cast<RowsScratch<X>*>(X::SHARED ? sm + X::W_OFF : pbuf + X::PBUF);
+      const uint32_t st = tmem + lane_off + X::S_COL + R * sb + hb, acc = tmem + lane_off + (ob * NG + (PP ? gi : 0)) * VT * N2;
       tc_fence_after();
       if (flags & G_FIRST) {
 #pragma unroll
-        for (int q = 0; q < NC; ++q) {
-          m[q] = -INFINITY;
-          l[q] = 0.f;
-        }
+        for (int q = 0; q < NC; ++q) l[q] = 0.f;
       }
-      const uint32_t st = tmem + lane_off + X::S_COL + R * sb + hb;
-      uint32_t bits[(NC * 2 * MT + 31) / 32];                 // of a special tile: which of this thread's scores count
-      float ts[NC];                                           // the tile's part of l
-      // One pass over the tile: weights against the offsets, into P as bf16 parts, and their sums.  Returns the largest
-      // exponent.  Row t of the B operand: 128 bytes per 64 columns (first parts of the query rows, then the next parts),
-      // 16-byte chunk c stored at chunk c ^ (t % 8) (128-byte swizzle).
-      auto emit = [&](auto masked) {
-        constexpr bool MASKED = decltype(masked)::value;
+      if (special) {
+        // What each query row attends to in this tile, and what any of them does.  Scores that do not count become minus
+        // infinities (before the scale) where they lie.
+#pragma unroll 1
+        for (int e = tid; e < (R * MT + 31) / 32 * 32; e += NW) {
+          unsigned long long win = 0;
+          const int c = e % R, w = e / R;
+          if (w < MT) {
+            const int tok = query_of<X>(a, mt.n, mt.t0, mt.h0, c).x;
+            if (tok >= 0) win = attended(a, mt, tok, mt.tile0 + 64 * w);
+            scr.win[w][c] = win;
+          }
+          // a warp's lanes hold query rows of one word, or of two: an OR of each word's
+          const unsigned group = R >= 32 ? FULL_MASK : (0xffffu << (lane & 16));
+          const uint32_t lo = __reduce_or_sync(group, (uint32_t)win), hi = __reduce_or_sync(group, (uint32_t)(win >> 32));
+          if (w < MT && lane % (R >= 32 ? 32 : 16) == 0) scr.seen[w][R > 32 ? (c >> 5) : 0] = (unsigned long long)hi << 32 | lo;
+        }
+        wait(&sh.vfull[pb], i / NP);                          // the values, of which some are about to be overwritten
+        if (sync(false), gone) break;
+        const uint32_t none = a.scale_log2 < 0.f ? 0x7f800000u : 0xff800000u;
+#pragma unroll 1
+        for (int ch = 0; ch < RC / (8 * CB); ++ch) {
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            uint32_t sr[4 * CB];
+            const uint32_t at = st + ((uint32_t)(16 * j) << 16) + ch * 8 * CB;
+            tmem_ld_frag(at, sr);
+            tmem_wait_ld();
+            const int row = (r0 + 16 * j) & 63;
+#pragma unroll
+            for (int b = 0; b < 2 * CB; ++b) {
+              const unsigned long long win = scr.win[(r0 + 16 * j) >> 6][c0 + 8 * (ch * CB + (b >> 1)) + (b & 1)] >> row;
+              if (!(win & 1)) sr[4 * (b >> 1) + (b & 1)] = none;
+              if (!(win & 256)) sr[4 * (b >> 1) + 2 + (b & 1)] = none;
+            }
+            __syncwarp();
+            tmem_st_frag(at, sr);
+          }
+        }
+        tmem_wait_st();
+        // V rows that no query row attends to, and that the product reads with p = 0: they may hold anything
+        const int topr = (min(TT, mt.ctx - mt.tile0) + 15) & ~15;
+#pragma unroll 1
+        for (int row = tid >> 5; row < topr; row += NW / 32) {
+          unsigned long long seen = scr.seen[row >> 6][0];
+          if constexpr (R > 32) seen |= scr.seen[row >> 6][1];
+          if ((seen >> (row & 63)) & 1) continue;
+#pragma unroll 1
+          for (int v = lane; v < X::VC * 8; v += 32) {
+            const int ch = v >> 3;
+            uint8_t* base = X::SHARED ? sm + ((k0 + (ch >> 1)) % NK) * X::KST + (ch & 1) * X::CHUNK
+                                      : sm + (i % NK) * X::KST + X::KPART + ch * X::CHUNK;
+            *reinterpret_cast<uint4*>(base + row * 128 + (v & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        __syncwarp();
+      }
+      // A tile's weights are taken against the running offsets; where an exponent exceeds them by more than kRowsLazy the
+      // offsets are raised and the pass is made again.  A segment's first tile starts from the scores of its first row:
+      // offsets need not be the maxima, only near them.  Where that may not be attended to, and behind such a tile, where a
+      // query row may still have no offset, the maxima are taken first.
+      bool raise = special || (was_special && !(flags & G_FIRST));
+      was_special = special;
+      if ((flags & G_FIRST) && !special) {
+        if (wq == 0) {
+#pragma unroll 1
+          for (int ch = 0; ch < RC / (8 * CB); ++ch) {
+            uint32_t sr[4 * CB];
+            tmem_ld_frag(st + ch * 8 * CB, sr);
+            tmem_wait_ld();
+            if (lane < 4) {
+#pragma unroll
+              for (int b = 0; b < 2 * CB; ++b) off[c0 + 8 * (ch * CB + (b >> 1)) + (b & 1)] = __uint_as_float(sr[4 * (b >> 1) + (b & 1)]) * a.scale_log2;
+            }
+            __syncwarp();
+          }
+        }
+        if (sync(false), gone) break;
+      }
+      float ts[NC];                        // the tile's part of l
+#pragma unroll 1
+      for (;;) {
+        if (raise) {
+          // the running maxima of the query rows, this tile's among them
+#pragma unroll 1
+          for (int ch = 0; ch < RC / (8 * CB); ++ch) {
+            uint32_t sr[MT][4 * CB];
+#pragma unroll
+            for (int j = 0; j < MT; ++j) tmem_ld_frag(st + ((uint32_t)(16 * j) << 16) + ch * 8 * CB, sr[j]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int b = 0; b < 2 * CB; ++b) {
+              float v = -INFINITY;
+#pragma unroll
+              for (int jh = 0; jh < 2 * MT; ++jh) v = fmaxf(v, __uint_as_float(sr[jh >> 1][4 * (b >> 1) + 2 * (jh & 1) + (b & 1)]) * a.scale_log2);
+#pragma unroll
+              for (int o = 4; o <= 16; o <<= 1) v = fmaxf(v, __shfl_xor_sync(FULL_MASK, v, o));
+              if (lane < 4) scr.red[wq][c0 + 8 * (ch * CB + (b >> 1)) + (b & 1)] = v;
+            }
+            __syncwarp();
+          }
+          if (!(flags & G_FIRST)) wait(&sh.pempty[PP ? i & 1 : (i - 1) & 1], PP ? i / 2 - 1 : (i - 1) / 2);   // for the rescale
+          if (sync(false), gone) break;
+          if (tid < R) {
+            const float mx = fmaxf(fmaxf(scr.red[0][tid], scr.red[1][tid]), fmaxf(scr.red[2][tid], scr.red[3][tid]));
+            const float m = flags & G_FIRST ? -INFINITY : off[tid], mn = fmaxf(m, mx);
+            scr.factor[tid] = m == -INFINITY ? 0.f : ex2(m - mn);
+            off[tid] = mn;
+          }
+          if (sync(false), gone) break;
+          if (!(flags & G_FIRST)) {
+            // the sums and O so far, to which the products of the tiles before have been added: scaled in place
+#pragma unroll
+            for (int q = 0; q < NC; ++q) l[q] *= scr.factor[c0 + 8 * (q >> 1) + (q & 1)];
+            tc_fence_after();
+#pragma unroll 1
+            for (int p = 0; p < VT * HL; ++p) {
+#pragma unroll 1
+              for (int b = 0; b < RC; b += 8) {
+                const uint32_t ta = acc + (p / HL) * N2 + (p % HL) * R + hb + b;
+                uint32_t o[8];
+                tmem_ld8(ta, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scr.factor[hb + b + e]);
+                tmem_st8(ta, o);
+              }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+          }
+        }
+        // One pass over the tile: weights against the offsets, into P as bf16 parts, and their sums.  Row t of the B operand:
+        // 128 bytes per 64 columns (first parts of the query rows, then the next parts), 16-byte chunk c stored at chunk
+        // c ^ (t % 8) (128-byte swizzle).
         float top = -INFINITY;
 #pragma unroll
         for (int ch = 0; ch < RC / (8 * CB); ++ch) {
@@ -701,18 +848,14 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int b = 0; b < CB; ++b) {
             const int q = 2 * (ch * CB + b);
-            const float o0 = MASKED && m[q] == -INFINITY ? 0.f : m[q], o1 = MASKED && m[q + 1] == -INFINITY ? 0.f : m[q + 1];
+            const float2 o = *reinterpret_cast<const float2*>(off + c0 + 4 * q);
+            const float o0 = o.x == -INFINITY ? 0.f : o.x, o1 = o.y == -INFINITY ? 0.f : o.y;
             float t0 = 0.f, t1 = 0.f;
 #pragma unroll
             for (int jh = 0; jh < 2 * MT; ++jh) {
               const int j = jh >> 1, h = jh & 1, row = r0 + 16 * j + 8 * h;
-              float y0 = fmaf(__uint_as_float(sr[j][4 * b + 2 * h]), a.scale_log2, -o0);
-              float y1 = fmaf(__uint_as_float(sr[j][4 * b + 2 * h + 1]), a.scale_log2, -o1);
-              if constexpr (MASKED) {
-                const int z = q * 2 * MT + jh, z1 = z + 2 * MT;
-                if (!((bits[z >> 5] >> (z & 31)) & 1)) y0 = -INFINITY;
-                if (!((bits[z1 >> 5] >> (z1 & 31)) & 1)) y1 = -INFINITY;
-              }
+              const float y0 = fmaf(__uint_as_float(sr[j][4 * b + 2 * h]), a.scale_log2, -o0);
+              const float y1 = fmaf(__uint_as_float(sr[j][4 * b + 2 * h + 1]), a.scale_log2, -o1);
               top = fmaxf(top, fmaxf(y0, y1));
               float p0 = ex2(y0), p1 = ex2(y1);
               const uint32_t hi = pack_bf16(p0, p1);
@@ -738,155 +881,27 @@ __global__ void __launch_bounds__(384, 1)
             ts[q + 1] = t1;
           }
         }
-        return top;
-      };
-      // A tile's weights are taken against the running offsets first; only where an exponent exceeds them by more than
-      // kRowsLazy the offsets are raised and the pass is made again.  A query row has no offset yet in its segment's first tile,
-      // and may have none behind tiles of which it attended to nothing: there the offsets are raised first.
-      bool raise = (flags & G_FIRST) || special || was_special;
-      was_special = special;
-      bool retry = false;
-      for (;;) {
-        if (raise) {
-          if (special) {
-            // what each query row attends to in this tile, and what any of them does
-            constexpr int EN = R * MT < NW ? R * MT : NW;     // of whole warps, or of one part of a warp
-            for (int w0 = 0; w0 < MT; w0 += EN / R) {
-              unsigned long long win = 0;
-              const int c = tid % R, w = w0 + tid / R;
-              if (tid < EN) {
-                const int tok = query_of<X>(a, mt.n, mt.t0, mt.h0, c).x;
-                if (tok >= 0) win = attended(a, mt, tok, mt.tile0 + 64 * w);
-                for (int b = 0; b < 64 >> a.bs_log2; ++b)
-                  if ((mt.invalid >> ((w * 64 >> a.bs_log2) + b)) & 1) win &= ~(ones_below(1 << a.bs_log2) << (b << a.bs_log2));
-                scr.win[w][c] = win;
-              }
-              // a warp's lanes hold one or two words' columns: an OR of each word's
-              const unsigned group = R >= 32 ? FULL_MASK : (0xffffu << (lane & 16));
-              const uint32_t lo = __reduce_or_sync(group, (uint32_t)win), hi = __reduce_or_sync(group, (uint32_t)(win >> 32));
-              if (tid < EN && lane % (R >= 32 ? 32 : 16) == 0) scr.seen[w][R > 32 ? (c >> 5) : 0] = (unsigned long long)hi << 32 | lo;
-            }
-            wait(&sh.vfull[pb], i / NP);                      // the values, of which some are about to be overwritten
-            if (sync(false), gone) break;
-            auto seen = [&](int row) {
-              unsigned long long x = scr.seen[row >> 6][0];
-              if constexpr (R > 32) x |= scr.seen[row >> 6][1];
-              return (x >> (row & 63)) & 1;
-            };
-#pragma unroll
-            for (int z = 0; z < (NC * 2 * MT + 31) / 32; ++z) bits[z] = 0;
-#pragma unroll
-            for (int q = 0; q < NC; ++q)
-#pragma unroll
-              for (int jh = 0; jh < 2 * MT; ++jh) {
-                const int row = r0 + 16 * (jh >> 1) + 8 * (jh & 1), z = q * 2 * MT + jh;
-                bits[z >> 5] |= (uint32_t)((scr.win[row >> 6][col(q)] >> (row & 63)) & 1) << (z & 31);
-              }
-            // V rows that no query row attends to, and that the product reads with p = 0: they may hold anything
-            const int topr = (min(TT, mt.ctx - mt.tile0) + 15) & ~15;
-            for (int row = tid >> 5; row < topr; row += NW / 32)
-              if (!seen(row))
-                for (int v = lane; v < X::VC * 8; v += 32) {
-                  const int ch = v >> 3;
-                  uint8_t* base = X::SHARED ? sm + ((k0 + (ch >> 1)) % NK) * X::KST + (ch & 1) * X::CHUNK
-                                            : sm + (i % NK) * X::KST + X::KPART + ch * X::CHUNK;
-                  *reinterpret_cast<uint4*>(base + row * 128 + (v & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                }
-          }
-          if ((flags & G_FIRST) && !special && !retry) {
-            // A segment's first tile starts from its first row's scores: offsets need not be the maxima, only near them
-            if (wq == 0) {
-#pragma unroll
-              for (int ch = 0; ch < RC / (8 * CB); ++ch) {
-                uint32_t sr[4 * CB];
-                tmem_ld_frag(st + ch * 8 * CB, sr);
-                tmem_wait_ld();
-#pragma unroll
-                for (int qq = 0; qq < 2 * CB; ++qq)
-                  if (lane < 4) scr.offset[col(2 * ch * CB + qq)] = __uint_as_float(sr[4 * (qq >> 1) + (qq & 1)]) * a.scale_log2;
-              }
-            }
-            if (sync(false), gone) break;
-#pragma unroll
-            for (int q = 0; q < NC; ++q) m[q] = scr.offset[col(q)];
-            if (sync(false), gone) break;                     // they are read before P is written over them
-            raise = false;
-            retry = true;
-          } else {
-          // the running maxima of the query rows, this tile's among them
-#pragma unroll
-          for (int ch = 0; ch < RC / (8 * CB); ++ch) {
-            uint32_t sr[MT][4 * CB];
-#pragma unroll
-            for (int j = 0; j < MT; ++j) tmem_ld_frag(st + ((uint32_t)(16 * j) << 16) + ch * 8 * CB, sr[j]);
-            tmem_wait_ld();
-#pragma unroll
-            for (int qq = 0; qq < 2 * CB; ++qq) {
-              const int q = 2 * ch * CB + qq;
-              float v = -INFINITY;
-#pragma unroll
-              for (int jh = 0; jh < 2 * MT; ++jh) {
-                const int z = q * 2 * MT + jh;
-                const float y = __uint_as_float(sr[jh >> 1][4 * (qq >> 1) + 2 * (jh & 1) + (qq & 1)]) * a.scale_log2;
-                if (!special || ((bits[z >> 5] >> (z & 31)) & 1)) v = fmaxf(v, y);
-              }
-#pragma unroll
-              for (int o = 4; o <= 16; o <<= 1) v = fmaxf(v, __shfl_xor_sync(FULL_MASK, v, o));
-              if (lane < 4) scr.red[wq][col(q)] = v;
-            }
-          }
-          if (sync(false), gone) break;
-#pragma unroll
-          for (int q = 0; q < NC; ++q) {
-            const int c = col(q);
-            const float mx = fmaxf(fmaxf(scr.red[0][c], scr.red[1][c]), fmaxf(scr.red[2][c], scr.red[3][c]));
-            const float mn = fmaxf(m[q], mx), al = m[q] == -INFINITY ? 0.f : ex2(m[q] - mn);
-            m[q] = mn;
-            l[q] *= al;
-            if (wq == 0 && lane < 4) scr.factor[c] = al;
-          }
-          if (!(flags & G_FIRST)) {
-            // O accumulated so far, which the products of the tiles before have completed: scaled in place
-            wait(&sh.pempty[PP ? i & 1 : (i - 1) & 1], PP ? i / 2 - 1 : (i - 1) / 2);
-            if (sync(false), gone) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int p = 0; p < VT * HL; ++p) {
-#pragma unroll 1
-              for (int b = 0; b < RC / 8; ++b) {
-                const uint32_t ta = tmem + lane_off + acc + (p / HL) * N2 + (p % HL) * R + hb + 8 * b;
-                uint32_t o[8];
-                tmem_ld8(ta, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scr.factor[hb + 8 * b + e]);
-                tmem_st8(ta, o);
-              }
-            }
-            tmem_wait_st();
-            tc_fence_before();
-          }
-          if (sync(false), gone) break;                       // the scratch is read before P is written over it
-          }
-        }
-        float top = 0.f;
-        if (raise) {
-          if (!special) {
-#pragma unroll
-            for (int z = 0; z < (NC * 2 * MT + 31) / 32; ++z) bits[z] = 0xffffffffu;
-          }
-          emit(std::true_type());
-        } else {
-          top = emit(std::false_type());
-        }
         if (raise) break;
         raise = sync(top > kRowsLazy);
-        retry = true;
         if (gone || !raise) break;
       }
       if (gone) break;
 #pragma unroll
       for (int q = 0; q < NC; ++q) l[q] += ts[q];
+      const bool ends_here = flags & G_LAST;
+      if (ends_here) {
+        // the sums over all cached rows of the group's tiles, while the scratch is there
+#pragma unroll
+        for (int q = 0; q < NC; ++q) {
+          float v = l[q];
+#pragma unroll
+          for (int o = 4; o <= 16; o <<= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
+          if (lane < 4) scr.red[wq][c0 + 8 * (q >> 1) + (q & 1)] = v;
+        }
+        if (sync(false), gone) break;
+        if (tid < R) sh.sum[ob][wg][tid] = make_float2(off[tid], (scr.red[0][tid] + scr.red[1][tid]) + (scr.red[2][tid] + scr.red[3][tid]));
+      }
+      const int part = mt.part, q0 = mt.q0, n = mt.n, t0 = mt.t0, h0 = mt.h0, g = mt.g;   // (they may be gone behind P)
       tc_fence_before();
       fence_proxy_async_smem();            // the rows written above, for the tensor core
       __syncwarp();
@@ -895,62 +910,34 @@ __global__ void __launch_bounds__(384, 1)
         mbar_arrive(&sh.pfull[pb]);
       }
 
-      if (flags & G_LAST) {
-        // The segment's sums over all cached rows, and behind its last product the output rows of its query rows.  With two
-        // accumulators the groups exchange their states, and each puts together half of the query rows.
-#pragma unroll
-        for (int q = 0; q < NC; ++q)
-#pragma unroll
-          for (int o = 4; o <= 16; o <<= 1) l[q] += __shfl_xor_sync(FULL_MASK, l[q], o);
-        wait(&sh.ofull[wg], ends++);
-        // the four warps' sums, in two steps through the place where the first of them then leaves the state
-        float* part = reinterpret_cast<float*>(sh.state[ob][wg]);
-        const bool puts = lane < 4 && !bad;
-        if (wq >= 2 && puts)
-#pragma unroll
-          for (int q = 0; q < NC; ++q) part[(wq - 2) * R + col(q)] = l[q];
-        if (sync(false), gone) break;
-        if (wq < 2 && puts)
-#pragma unroll
-          for (int q = 0; q < NC; ++q) {
-            l[q] += part[wq * R + col(q)];
-            if (wq == 1) part[R + col(q)] = l[q];
-          }
-        if (sync(false), gone) break;
-        if (wq == 0 && puts)
-#pragma unroll
-          for (int q = 0; q < NC; ++q) l[q] += part[R + col(q)];
-        if (sync(false), gone) break;
-        if (wq == 0 && puts)
-#pragma unroll
-          for (int q = 0; q < NC; ++q) sh.state[ob][wg][col(q)] = make_float2(m[q], l[q]);
+      if (ends_here) {
+        // Behind the segment's last product, its output rows.  With two accumulators the groups exchange their states, and
+        // each puts together half of the query rows.
         const bool whole = flags & F_WHOLE, pair = PP && !(flags & G_SOLO);
-        if (!pair && (sync(false), gone)) break;
+        wait(&sh.ofull[wg], ends++);
         if (pair) {
-          __syncwarp();
           if (lane == 0) mbar_arrive(&sh.joined[gi]);
           wait(&sh.joined[0], joins);
           wait(&sh.joined[1], joins);
           ++joins;
+        } else if (sync(false), gone) {
+          break;
         }
         if (tid < R && !bad) {
-          const float2 own = sh.state[ob][wg][tid];
-          float M = own.x, L = own.y;
-          float2 f = make_float2(1.f, 1.f);
-          if (pair) {
-            const float2 x = sh.state[ob][0][tid], y = sh.state[ob][1][tid];
-            M = fmaxf(x.x, y.x);
-            f = make_float2(x.x == -INFINITY ? 0.f : ex2(x.x - M), y.x == -INFINITY ? 0.f : ex2(y.x - M));
-            L = x.y * f.x + y.y * f.y;
-          }
-          const int2 qh = query_of<X>(a, mt.n, mt.t0, mt.h0, tid);
-          sh.row[ob][tid] = qh.x < 0 ? -1 : (mt.q0 + qh.x) * a.n_h + mt.g * a.G + qh.y;
+          // an accumulator none of whose rows counted (its sum is 0) has no part in it
+          float2 x = sh.sum[ob][wg][tid], y = make_float2(0.f, 0.f);
+          if (pair) x = sh.sum[ob][0][tid], y = sh.sum[ob][NG - 1][tid];
+          const float M = fmaxf(x.y == 0.f ? -INFINITY : x.x, y.y == 0.f ? -INFINITY : y.x);
+          float2 f = make_float2(x.y == 0.f ? 0.f : ex2(x.x - M), y.y == 0.f ? 0.f : ex2(y.x - M));
+          const float L = x.y * f.x + y.y * f.y;
+          const int2 qh = query_of<X>(a, n, t0, h0, tid);
+          sh.row[ob][tid] = qh.x < 0 ? -1 : (q0 + qh.x) * a.n_h + g * a.G + qh.y;
           if (whole) {
             const float inv = sum_inverse(L);
             f.x *= inv;
             f.y *= inv;
           } else if (!pair || gi == 0) {
-            *reinterpret_cast<float2*>(a.ws_ml + ((size_t)mt.part * R + tid) * 2) = make_float2(M, L);
+            *reinterpret_cast<float2*>(a.ws_ml + ((size_t)part * R + tid) * 2) = make_float2(M, L);
           }
           if (!pair || tid / (R / 2) == gi) sh.factor[ob][tid] = f;   // a pair's groups each put together half of the query rows
         }
@@ -959,39 +946,36 @@ __global__ void __launch_bounds__(384, 1)
         const int cb = PP ? (pair ? gi * (R / 2) : 0) : hb, cn = PP && !pair ? R : R / 2;
         const uint32_t oa = tmem + lane_off + ob * NG * VT * N2 + (PP && !pair ? gi * VT * N2 : 0);
 #pragma unroll 1
-        for (int vt = 0; vt < VT; ++vt) {
+        for (int e0 = 0; e0 < VT * cn; e0 += 8) {
+          const int vt = e0 / cn, cc = cb + e0 - vt * cn;
           const int chn = vt * X::VM + (X::VM == 128 ? 32 * wq + lane : 16 * wq + lane);
-          const bool mine = X::VM == 128 || lane < 16;
-#pragma unroll 1
-          for (int b = 0; b < cn; b += 8) {
-            uint32_t t[NG][HL][8];
+          float v[8];
+          uint32_t t[HL][8];
+          auto load = [&](int g) {
+            __syncwarp();
 #pragma unroll
-            for (int g = 0; g < NG; ++g)
-              if (g == 0 || pair)
-#pragma unroll
-                for (int p = 0; p < HL; ++p) tmem_ld8(oa + (g * VT + vt) * N2 + p * R + cb + b, t[g][p]);
+            for (int p = 0; p < HL; ++p) tmem_ld8(oa + (g * VT + vt) * N2 + p * R + cc, t[p]);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int c = cb + b + e, row = sh.row[ob][c];
-              const float2 f = sh.factor[ob][c];
-              float v = 0.f;
+            for (int e = 0; e < 8; ++e)
 #pragma unroll
-              for (int p = HL - 1; p >= 0; --p) v += __uint_as_float(t[0][p][e]);
-              v *= f.x;
-              if constexpr (PP) {
-                if (pair) {
-                  float w = 0.f;
+              for (int p = HL - 2; p >= 0; --p) t[HL - 1][e] = __float_as_uint(__uint_as_float(t[HL - 1][e]) + __uint_as_float(t[p][e]));
+          };
+          load(0);
 #pragma unroll
-                  for (int p = HL - 1; p >= 0; --p) w += __uint_as_float(t[NG - 1][p][e]);
-                  v = fmaf(w, f.y, v);
-                }
-              }
-              if (row < 0 || !mine) continue;
-              if (!whole) a.ws_o[((size_t)mt.part * R + c) * DV + chn] = v;
-              else if constexpr (X::F32) reinterpret_cast<float*>(a.out)[(size_t)row * DV + chn] = v;
-              else reinterpret_cast<__nv_bfloat16*>(a.out)[(size_t)row * DV + chn] = __float2bfloat16_rn(v);
-            }
+          for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(t[HL - 1][e]) * sh.factor[ob][cc + e].x;
+          if (PP && pair) {
+            load(NG - 1);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = fmaf(__uint_as_float(t[HL - 1][e]), sh.factor[ob][cc + e].y, v[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int row = sh.row[ob][cc + e];
+            if (row < 0 || (X::VM == 64 && lane >= 16)) continue;
+            if (!whole) a.ws_o[((size_t)part * R + cc + e) * DV + chn] = v[e];
+            else if constexpr (X::F32) reinterpret_cast<float*>(a.out)[(size_t)row * DV + chn] = v[e];
+            else reinterpret_cast<__nv_bfloat16*>(a.out)[(size_t)row * DV + chn] = __float2bfloat16_rn(v[e]);
           }
         }
         tc_fence_before();
@@ -1003,6 +987,35 @@ __global__ void __launch_bounds__(384, 1)
     if (bad && lane == 0) {
       set_err(a.err, PKV_DEV_TIMEOUT);
       sh.abort_flag = 1;
+    }
+    if (warp == 11) {
+      if (lane == 0 && member == 0) {
+        // whether the piece's start cuts a segment for the first time, for the kernel that joins the parts
+        RowsCut cut = {};
+        if (sh.W > 0) {
+          const RowsLine line(sh.W, a.P);
+          const RowsCursor& c = sh.first;
+          const long long pstart = line.start(team), seg = pstart - c.t, prev = team > 0 ? line.start(team - 1) : 0;
+          if (c.t > 0 && prev <= seg) {
+            const int last = min(line.piece(min(seg + c.nt, line.W) - 1), line.P - 1);   // the last piece that holds a part
+            cut.parts = last - team + 2;
+            cut.first = prev == seg ? 0 : 1;
+            cut.q0 = c.d.q0; cut.n = c.d.n; cut.g = c.g; cut.rg = c.rg;
+          }
+        }
+        a.cuts[team] = cut;
+      }
+      __syncwarp();
+    }
+    // Sequences without cached rows: their tokens' outputs are zeros
+#pragma unroll 1
+    for (int s = blockIdx.x; s < a.batch; s += gridDim.x) {
+      int flags = 0;
+      const Drafts d = drafts_of(a.ctx, a.q_start, a.n_each, a.n_tok, a.max_ctx, s, flags);
+      if (d.ctx > 0 || d.n == 0) continue;
+      const long long at = (long long)d.q0 * a.n_h * DV, len = (long long)d.n * a.n_h * DV;
+#pragma unroll 1
+      for (long long e = threadIdx.x - 128; e < len; e += 256) store_out(a, at + e, 0.f);
     }
   }
   // the tensor memory is released once every role is done with it (the issuers waited for their last products)
