@@ -109,8 +109,9 @@ enum : int { G_FIRST = 64, G_LAST = 128, G_END = 256, G_SOLO = 512 };
 
 template <class X>
 struct RowsShared {
-  // Slots of keys (stages), of position chunks or values, P by its slot; the products of P by the tile's parity
-  uint64_t kfull[X::NK], kempty[X::NK], vfull[X::NP], pfull[X::NP], pslot[X::NP], pempty[2], qfull[2], qempty[2], sfull[X::NS], sempty[X::NS],
+  // What has landed, by stage (latent cache: all of a tile, by its metadata); slots of keys, or stages; values; P, by its slot;
+  // slots of position chunks; the products of P by the tile's parity
+  uint64_t kfull[X::SHARED ? X::NM : X::NK], kempty[X::NK], vfull[X::NP], pfull[X::NP], pslot[X::NP], pempty[2], qfull[2], qempty[2], sfull[X::NS], sempty[X::NS],
       ofull[2], oempty[2], joined[2], drain, drain_pv;
   RowsMeta meta[X::NM];          // of tile i: entry i % NM
   uint32_t tmem;
@@ -281,6 +282,7 @@ __global__ void __launch_bounds__(384, 1)
                        const __grid_constant__ CUtensorMap tmq, const __grid_constant__ RowsArgs a) {
   constexpr int TT = X::TT, R = X::R, HL = X::HL, N2 = X::N2, KC = X::KC, VT = X::VT, MT = X::MT, DV = X::DV;
   constexpr int NK = X::NK, NM = X::NM, NP = X::NP, NO = X::NO, NS = X::NS, NG = X::NG, NQ = X::NQ;
+  constexpr int NF = X::SHARED ? NM : NK;                     // full barriers
   constexpr bool PP = X::PP;
   extern __shared__ __align__(1024) uint8_t sm[];
   RowsShared<X>& sh = *reinterpret_cast<RowsShared<X>*>(sm + X::M_OFF);
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(384, 1)
     constexpr int SW = PP ? 4 : 8;         // softmax warps of a tile
     for (uint64_t* b = sh.kfull + lane; b <= &sh.drain_pv; b += 32) {
       const bool softmax = (b >= sh.sempty && b < sh.sempty + NS) || (b >= sh.pfull && b < sh.pfull + NP);
-      mbar_init(b, softmax ? SW : (b >= sh.oempty && b < sh.oempty + 2 ? 8 : (b >= sh.joined && b < sh.joined + 2 ? 4 : 1)));
+      mbar_init(b, softmax ? SW : X::SHARED && b >= sh.kfull && b < sh.kfull + NM ? VT + 1 : (b >= sh.oempty && b < sh.oempty + 2 ? 8 : (b >= sh.joined && b < sh.joined + 2 ? 4 : 1)));
     }
     fence_barrier_init();
   }
@@ -397,19 +399,35 @@ __global__ void __launch_bounds__(384, 1)
     RowsCursor c = sh.cur;
     int k = -1, kq = -1, i = -1;
     RowsMeta m = {}, mn = {};                                 // the tile to load, and the one behind it
-    int phys = -1, physn = -1, idx = 0, idxn = -1;            // block ids; number of the tile in its segment, within the piece
-    unsigned used = 0, usedn = 0;                             // blocks of the tile
+    int idx = 0, idxn = -1;                                   // number of the tile in its segment, within the piece
+    // Block ids, one per lane: 32 blocks from `wfrom` on, the 32 behind them, and the first 32 of the segment that comes next.
+    // (A copy of a register that a load is on the way to waits for it, so these are copied long after they are asked for.)
+    int win = -1, win_next = -1, win_first = -1, wfrom = 0;
+    const int32_t *row = a.bt, *rown = a.bt, *rown_m = a.bt;   // block tables of the segment being loaded, and of mn and m
+    auto ids_at = [&](const int32_t* bt, int ctx, int from) { return from + lane < (ctx + bsz - 1) >> a.bs_log2 ? bt[from + lane] : -1; };
     bool more = true, ok = true;
 #pragma unroll 1
     for (;; ++i) {
-      // The tile at the cursor is described a round before it is loaded, with its block ids in flight meanwhile; the first
-      // round only does that.
+      const int blk0 = m.tile0 >> a.bs_log2;
+      if (i >= 0 && (m.flags & F_FIRST)) {
+        win = win_first;
+        wfrom = blk0;
+        row = rown_m;
+        win_next = ids_at(row, m.ctx, blk0 + 32);
+      } else if (i >= 0 && blk0 >= wfrom + 32) {
+        win = win_next;
+        wfrom += 32;
+        win_next = ids_at(row, m.ctx, wfrom + 32);
+      }
+      // The tile at the cursor is described a round before it is loaded; the first round only does that.
       const bool has = more;
       if (has) {
         const bool first = k < 0 || c.t == 0;
         if (first) {
           ++k;
           tile_of<X>(a, c.rg * a.C + member, mn.t0, mn.h0);
+          rown = a.bt + (size_t)c.s * a.max_blocks;
+          win_first = ids_at(rown, c.d.ctx, c.t * nbt);
         }
         idxn = first ? 0 : idxn + 1;
         mn.k = k;
@@ -417,9 +435,6 @@ __global__ void __launch_bounds__(384, 1)
         mn.ctx = c.d.ctx; mn.n = c.d.n; mn.q0 = c.d.q0;
         mn.g = c.g;
         mn.part = blockIdx.x * 2 + (c.at_start ? 0 : 1);
-        const int blk0 = c.t * nbt, nb = (c.d.ctx + bsz - 1) >> a.bs_log2;
-        usedn = (1u << min(nb - blk0, nbt)) - 1;
-        physn = (usedn >> lane) & 1 ? a.bt[(size_t)c.s * a.max_blocks + blk0 + lane] : -1;
         const bool seg_end = c.t + 1 == c.nt;
         mn.flags = (first ? F_FIRST : 0) | (seg_end || c.left == 1 ? F_LAST : 0) | (seg_end && c.whole_from ? F_WHOLE : 0);
         ++c.t;
@@ -429,7 +444,9 @@ __global__ void __launch_bounds__(384, 1)
       }
       if (i >= 0) {
         if (sh.abort_flag) break;
-        const unsigned valid = __ballot_sync(FULL_MASK, (unsigned)phys < (unsigned)a.num_blocks);
+        const unsigned used = (1u << min(((m.ctx + bsz - 1) >> a.bs_log2) - blk0, nbt)) - 1;   // blocks of the tile
+        const int phys = __shfl_sync(FULL_MASK, win, (blk0 - wfrom + lane) & 31);
+        const unsigned valid = __ballot_sync(FULL_MASK, (unsigned)phys < (unsigned)a.num_blocks) & used;
         const uint32_t chunk_bytes = (uint32_t)__popc(valid) * 128u << a.bs_log2;
         if (lead) {
           // what the tile is to its softmax group
@@ -487,11 +504,11 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok) break;
             if (lead && v == 0 && lane == 0) sh.meta[i % NM] = m;
             __syncwarp();
-            fill(sm + slot * X::KST, &sh.kfull[slot], &tmk, vt * 128, std::integral_constant<int, 2>());
+            fill(sm + slot * X::KST, &sh.kfull[i % NM], &tmk, vt * 128, std::integral_constant<int, 2>());
           }
           if (ok && !lead) {
             ok = i < NP || rows_wait(&sh.pslot[i % NP], i / NP - 1);
-            if (ok) fill(sm + X::P_OFF + (i % NP) * X::PST, &sh.vfull[i % NP], &tmk, VT * 128, std::integral_constant<int, 1>());
+            if (ok) fill(sm + X::P_OFF + (i % NP) * X::PST, &sh.kfull[i % NM], &tmk, VT * 128, std::integral_constant<int, 1>());
           }
         } else {
           const int st = i % NK;
@@ -507,8 +524,7 @@ __global__ void __launch_bounds__(384, 1)
         if (!ok || !has) break;
       }
       m = mn;
-      phys = physn;
-      used = usedn;
+      rown_m = rown;
       idx = idxn;
     }
     ok = __all_sync(FULL_MASK, ok);
@@ -519,10 +535,10 @@ __global__ void __launch_bounds__(384, 1)
     // After a timeout: let the loads already issued land before the CTA leaves (bounded).
     if (sh.abort_flag && lane == 0) {
       bool live = true;
-      const int nk = X::SHARED ? (i + 1) * VT : i + 1;
-      for (int j = max(0, nk - NK - 1); j < nk && live; ++j) live = rows_poll(&sh.kfull[j % NK], (j / NK) & 1, 20000000ull);
-      live = true;
-      for (int j = max(0, i - NP); j <= i && live; ++j) live = rows_poll(&sh.vfull[j % NP], (j / NP) & 1, 20000000ull);
+      constexpr int NF = X::SHARED ? NM : NK;
+      for (int j = max(0, i - NF); j <= i && live; ++j) live = rows_poll(&sh.kfull[j % NF], (j / NF) & 1, 20000000ull);
+      live = !X::SHARED;
+      for (int j = max(0, i - NK); j <= i && live; ++j) live = rows_poll(&sh.vfull[j % NP], (j / NP) & 1, 20000000ull);
       if (kq >= 0) rows_poll(&sh.qfull[kq % NQ], (kq / NQ) & 1, 20000000ull);
     }
     __syncwarp();
@@ -536,7 +552,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 1
     for (int i = 0;; ++i) {
       const int k0 = X::SHARED ? i * VT : i, sb = i % NS;     // first slot of the tile's keys
-      ok = !sh.abort_flag && rows_wait(&sh.kfull[k0 % NK], k0 / NK);
+      ok = !sh.abort_flag && rows_wait(&sh.kfull[i % NF], i / NF);
       if (!ok) break;
       const RowsMeta& mt = sh.meta[i % NM];
       const int flags = __shfl_sync(FULL_MASK, mt.flags, 0), k = __shfl_sync(FULL_MASK, mt.k, 0), qb = k % NQ;
@@ -560,18 +576,8 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
       };
       if constexpr (X::SHARED) {
-        // slots as they are loaded, and the position chunk
 #pragma unroll 1
-        for (int u = 0; u < VT && ok; ++u) {
-          const int slot = (k0 + u) % NK;
-          if (u > 0) ok = rows_wait(&sh.kfull[slot], (k0 + u) / NK);
-          if (!ok) break;
-          tc_fence_after();
-          chunks(sbase + (slot * X::KST >> 4), 2 * u, 4, std::integral_constant<int, 2>());
-        }
-        ok = ok && rows_wait(&sh.vfull[i % NP], i / NP);
-        if (!ok) break;
-        tc_fence_after();
+        for (int u = 0; u < VT; ++u) chunks(sbase + ((k0 + u) % NK * X::KST >> 4), 2 * u, 4, std::integral_constant<int, 2>());
         chunks(sbase + ((X::P_OFF + (i % NP) * X::PST) >> 4), KC - 1, a.last_steps, std::integral_constant<int, 1>());
       } else {
         chunks(sbase + ((i % NK) * X::KST >> 4), 0, 4, std::integral_constant<int, KC>());
@@ -603,7 +609,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 1
     for (int i = 0;; ++i) {
       const int pb = i % NP, k0 = i * VT;
-      ok = !sh.abort_flag && rows_wait(X::SHARED ? &sh.kfull[k0 % NK] : &sh.vfull[pb], X::SHARED ? k0 / NK : i / NP) &&
+      ok = !sh.abort_flag && rows_wait(X::SHARED ? &sh.kfull[i % NF] : &sh.vfull[pb], X::SHARED ? i / NF : i / NP) &&
            rows_wait(&sh.pfull[pb], i / NP);
       if (!ok) break;
       const RowsMeta& mt = sh.meta[i % NM];
@@ -661,7 +667,7 @@ __global__ void __launch_bounds__(384, 1)
     const int r0 = 16 * MT * wq + (lane >> 2), c0 = hb + 2 * (lane & 3);   // this thread's first cached row and query row
     float* off = sh.offset[wg];            // offsets of the query rows, minus infinity where there is none yet
     float l[NC];                           // this thread's rows' share of the sums of its query rows
-    bool was_special = false;
+    bool unset = false;                    // a query row may have no offset yet
     // Barriers among the threads of a tile.  A failed (timed-out) wait makes `bad` true for its warp, which raises a flag ahead
     // of the next barrier; behind that all of them see it and leave together, so no thread is left at a barrier.  The
     // flag goes by the barrier's parity, since a warp may be one barrier ahead of another.
@@ -686,7 +692,7 @@ __global__ void __launch_bounds__(384, 1)
       // A barrier tells a phase from the one before it only by parity, and this group may not have waited for that.  It is
       // over, though: behind the group's last tile the keys of the tiles before it had landed, and behind this one's
       // scores the tile whose slot they took was done with.
-      wait(&sh.kfull[k0 % NK], k0 / NK);                      // the metadata, which stay until P is there
+      wait(&sh.kfull[i % NF], i / NF);                        // the metadata, which stay until P is there
       wait(&sh.sfull[sb], i / NS);                            // the scores, and room for P in place of the keys
       if (bad) {
         sync(true);
@@ -702,6 +708,11 @@ __global__ void __launch_bounds__(384, 1)
       if (flags & G_FIRST) {
 #pragma unroll
         for (int q = 0; q < NC; ++q) l[q] = 0.f;
+        if (a.mask && tid < R && !special) {                  // the masks that the segment will end with
+          const int tok = query_of<X>(a, mt.n, mt.t0, mt.h0, tid).x;
+          if (tok >= 0) prefetch_l2(a.mask + (size_t)(mt.q0 + tok) * a.mask_words);
+        }
+        __syncwarp();
       }
       if (special) {
         // What each query row attends to in this tile, and what any of them does.  Scores that do not count become minus
@@ -720,7 +731,7 @@ __global__ void __launch_bounds__(384, 1)
           const uint32_t lo = __reduce_or_sync(group, (uint32_t)win), hi = __reduce_or_sync(group, (uint32_t)(win >> 32));
           if (w < MT && lane % (R >= 32 ? 32 : 16) == 0) scr.seen[w][R > 32 ? (c >> 5) : 0] = (unsigned long long)hi << 32 | lo;
         }
-        wait(&sh.vfull[pb], i / NP);                          // the values, of which some are about to be overwritten
+        if (!X::SHARED) wait(&sh.vfull[pb], i / NP);          // the values, of which some are about to be overwritten
         if (sync(false), gone) break;
         const uint32_t none = a.scale_log2 < 0.f ? 0x7f800000u : 0xff800000u;
 #pragma unroll 1
@@ -731,12 +742,13 @@ __global__ void __launch_bounds__(384, 1)
             const uint32_t at = st + ((uint32_t)(16 * j) << 16) + ch * 8 * CB;
             tmem_ld_frag(at, sr);
             tmem_wait_ld();
-            const int row = (r0 + 16 * j) & 63;
+            const int first = 16 * MT * wq + 16 * j;          // the fragment's first row: 16 bits of a word
 #pragma unroll
             for (int b = 0; b < 2 * CB; ++b) {
-              const unsigned long long win = scr.win[(r0 + 16 * j) >> 6][c0 + 8 * (ch * CB + (b >> 1)) + (b & 1)] >> row;
-              if (!(win & 1)) sr[4 * (b >> 1) + (b & 1)] = none;
-              if (!(win & 256)) sr[4 * (b >> 1) + 2 + (b & 1)] = none;
+              const int c = c0 + 8 * (ch * CB + (b >> 1)) + (b & 1);
+              const uint32_t w = reinterpret_cast<const uint16_t*>(&scr.win[first >> 6][c])[(first & 63) >> 4] >> (lane >> 2);
+              if (!(w & 1)) sr[4 * (b >> 1) + (b & 1)] = none;
+              if (!(w & 256)) sr[4 * (b >> 1) + 2 + (b & 1)] = none;
             }
             __syncwarp();
             tmem_st_frag(at, sr);
@@ -762,10 +774,11 @@ __global__ void __launch_bounds__(384, 1)
       }
       // A tile's weights are taken against the running offsets; where an exponent exceeds them by more than kRowsLazy the
       // offsets are raised and the pass is made again.  A segment's first tile starts from the scores of its first row:
-      // offsets need not be the maxima, only near them.  Where that may not be attended to, and behind such a tile, where a
-      // query row may still have no offset, the maxima are taken first.
-      bool raise = special || (was_special && !(flags & G_FIRST));
-      was_special = special;
+      // offsets need not be the maxima, only near them.  Where that may not be attended to, the maxima are taken first, and so
+      // they are behind such tiles, where a query row may still have no offset, up to one that all of them attend to.
+      if (flags & G_FIRST) unset = special;
+      bool raise = unset;
+      unset = unset && special;
       if ((flags & G_FIRST) && !special) {
         if (wq == 0) {
 #pragma unroll 1
@@ -889,6 +902,8 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
       for (int q = 0; q < NC; ++q) l[q] += ts[q];
       const bool ends_here = flags & G_LAST;
+      float2 own = make_float2(0.f, 0.f);  // of query row tid, at the segment's end
+      int out_row = -1;
       if (ends_here) {
         // the sums over all cached rows of the group's tiles, while the scratch is there
 #pragma unroll
@@ -899,7 +914,7 @@ __global__ void __launch_bounds__(384, 1)
           if (lane < 4) scr.red[wq][c0 + 8 * (q >> 1) + (q & 1)] = v;
         }
         if (sync(false), gone) break;
-        if (tid < R) sh.sum[ob][wg][tid] = make_float2(off[tid], (scr.red[0][tid] + scr.red[1][tid]) + (scr.red[2][tid] + scr.red[3][tid]));
+        if (tid < R) own = make_float2(off[tid], (scr.red[0][tid] + scr.red[1][tid]) + (scr.red[2][tid] + scr.red[3][tid]));
       }
       const int part = mt.part, q0 = mt.q0, n = mt.n, t0 = mt.t0, h0 = mt.h0, g = mt.g;   // (they may be gone behind P)
       tc_fence_before();
@@ -914,24 +929,29 @@ __global__ void __launch_bounds__(384, 1)
         // Behind the segment's last product, its output rows.  With two accumulators the groups exchange their states, and
         // each puts together half of the query rows.
         const bool whole = flags & F_WHOLE, pair = PP && !(flags & G_SOLO);
+        if (tid < R) {
+          const int2 qh = query_of<X>(a, n, t0, h0, tid);
+          if (qh.x >= 0) out_row = (q0 + qh.x) * a.n_h + g * a.G + qh.y;
+        }
+        __syncwarp();
+        // (behind this wait the segment before it in this O buffer is done with, in both groups)
         wait(&sh.ofull[wg], ends++);
+        if (tid < R && !bad) sh.sum[ob][wg][tid] = own;
         if (pair) {
+          __syncwarp();
           if (lane == 0) mbar_arrive(&sh.joined[gi]);
           wait(&sh.joined[0], joins);
           wait(&sh.joined[1], joins);
           ++joins;
-        } else if (sync(false), gone) {
-          break;
         }
         if (tid < R && !bad) {
           // an accumulator none of whose rows counted (its sum is 0) has no part in it
-          float2 x = sh.sum[ob][wg][tid], y = make_float2(0.f, 0.f);
+          float2 x = own, y = make_float2(0.f, 0.f);
           if (pair) x = sh.sum[ob][0][tid], y = sh.sum[ob][NG - 1][tid];
           const float M = fmaxf(x.y == 0.f ? -INFINITY : x.x, y.y == 0.f ? -INFINITY : y.x);
           float2 f = make_float2(x.y == 0.f ? 0.f : ex2(x.x - M), y.y == 0.f ? 0.f : ex2(y.x - M));
           const float L = x.y * f.x + y.y * f.y;
-          const int2 qh = query_of<X>(a, n, t0, h0, tid);
-          sh.row[ob][tid] = qh.x < 0 ? -1 : (q0 + qh.x) * a.n_h + g * a.G + qh.y;
+          sh.row[ob][tid] = out_row;
           if (whole) {
             const float inv = sum_inverse(L);
             f.x *= inv;
