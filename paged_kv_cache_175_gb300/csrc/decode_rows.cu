@@ -85,13 +85,13 @@ struct RowsCfg {
   static constexpr int PST = SHARED ? PBUF : KST;
   static constexpr int NQ = SHARED && (KC == 9 ? R > 16 : R == 64) ? 1 : 2;
   static constexpr int NK = SHARED ? (FULL || PAT > 1 ? 8 : 9) : (KC == 1 ? 4 : 3);
-  static constexpr int NP = SHARED ? (FULL ? 2 : 3) : NK;     // tiles whose P there is room for
-  static constexpr int NM = SHARED ? (KC == 9 ? 4 : 8) : NK;  // metadata of tiles: of all that the ring may hold a part of
+  static constexpr int NP = SHARED ? 3 : NK;                  // tiles whose P there is room for
+  static constexpr int NM = SHARED ? (KC == 9 ? 3 : 8) : NK;  // metadata of tiles: of all that the ring may hold a part of
   static constexpr int NS = PP ? 4 : 2, NG = PP ? 2 : 1;      // S buffers; accumulators of a segment
   static constexpr int NO = VT * N2 * NG * 2 + NS * R <= 512 && !(PP && R == 64) ? 2 : 1;
   static constexpr int S_COL = VT * N2 * NG * NO, NCOL = S_COL + NS * R;
   static constexpr uint32_t TMEM_COLS = NCOL <= 64 ? 64 : (NCOL <= 128 ? 128 : (NCOL <= 256 ? 256 : 512));
-  static constexpr int P_OFF = SHARED ? NK * KST : 0, Q_OFF = NK * KST + (SHARED ? NP * PST : 0), W_OFF = Q_OFF + NQ * QBUF, M_OFF = W_OFF + (SHARED ? 32 * R + 128 : 0);   // W: scratch
+  static constexpr int P_OFF = SHARED ? NK * KST : 0, Q_OFF = NK * KST + (SHARED ? NP * PST : 0), W_OFF = Q_OFF + NQ * QBUF, M_OFF = W_OFF + (SHARED ? 28 * R + 16 : 0);   // W: scratch
   static constexpr bool F32 = HL == 3;                        // output type
 };
 
@@ -111,28 +111,32 @@ template <class X>
 struct RowsShared {
   // What has landed, by stage (latent cache: all of a tile, by its metadata); slots of keys, or stages; values; P, by its slot;
   // slots of position chunks; the products of P by the tile's parity
-  uint64_t kfull[X::SHARED ? X::NM : X::NK], kempty[X::NK], vfull[X::NP], pfull[X::NP], pslot[X::NP], pempty[2], qfull[2], qempty[2], sfull[X::NS], sempty[X::NS],
-      ofull[2], oempty[2], joined[2], drain, drain_pv;
+  uint64_t kfull[X::SHARED ? X::NM : X::NK], kempty[X::NK], vfull[X::SHARED ? 1 : X::NP], pfull[X::NP], pslot[X::SHARED ? X::NP : 1], pempty[2],
+      qfull[X::NQ], qempty[X::NQ], sfull[X::NS], sempty[X::NS], ofull[X::NG], oempty[X::NO], joined[X::NG], drain;
   RowsMeta meta[X::NM];          // of tile i: entry i % NM
   uint32_t tmem;
   int any;
   volatile int abort_flag;
-  volatile int bad[2][2];                                     // of each group of waiting warps, by the parity of its barriers
-  RowsCursor cur, first;         // the member's first tile; the piece's
+  volatile int bad[X::NG][2];                                     // of each group of waiting warps, by the parity of its barriers
+  RowsCursor cur;                // the member's first tile
+  RowsCut first;                 // the piece's first segment; parts: tiles ahead of the piece, first: of the segment
   long long W;
   float offset[X::NG][X::R];     // of each query row: what its exponents are taken against
   // Of a segment's end, by its O buffer: offset and sum of each query row in a group's tiles, factors of the output (of
   // either accumulator), and output rows
-  float2 sum[X::NO][X::NG][X::R], factor[X::NO][X::R];
-  int row[X::NO][X::R];
-  long long scan[12];
+  float2 sum[X::PP ? X::NO : 1][X::NG][X::PP ? X::R : 1];
+  std::conditional_t<X::PP, float2, float> factor[X::NO][X::R];
+  union {
+    int row[X::NO][X::R];
+    long long scan[12];            // of the setup
+  };
 };
 // What the warps of a tile share for a moment: behind its P, or in a place of its own.
 template <class X>
 struct RowsScratch {
   float red[4][X::R];                                         // each warp's part of a query row's maximum or sum
-  unsigned long long win[X::MT][X::R], seen[X::MT][2];        // cached rows attended to, by each query row and by any of a warp's
   float factor[X::R];                                         // of a rescale
+  unsigned long long win[X::MT][X::R], seen[X::MT][2];        // cached rows attended to, by each query row and by any of a warp's
 };
 
 static __device__ __noinline__ long long div_far(long long x, long long y) { return x / y; }
@@ -165,9 +169,10 @@ __device__ __forceinline__ long long line_length(const RowsArgs& a, const Drafts
   return (long long)a.n_kv * ((rt + a.C - 1) / a.C) * ((d.ctx + tt - 1) / tt);
 }
 
-// Moves to the next tile of this member (false: the piece has none left).  Row tiles past the last one are passed over.
+// Behind a segment's last tile, or where the member has no row tile: the next segment in which it has one (left is 0: the
+// piece has none).  By value, so that a cursor stays in registers between segments.
 template <class X>
-__device__ __noinline__ bool rows_settle(RowsCursor& c, const RowsArgs& a, int member) {
+__device__ __noinline__ RowsCursor next_segment(RowsCursor c, const RowsArgs& a, int member) {
   while (c.left > 0) {
     if (c.t >= c.nt) {
       c.t = 0;
@@ -179,7 +184,10 @@ __device__ __noinline__ bool rows_settle(RowsCursor& c, const RowsArgs& a, int m
           c.g = 0;
           int flags = 0;
           do {
-            if (++c.s >= a.batch) return false;
+            if (++c.s >= a.batch) {
+              c.left = 0;
+              return c;
+            }
             c.d = drafts_of(a.ctx, a.q_start, a.n_each, a.n_tok, a.max_ctx, c.s, flags);
             c.nt = (c.d.ctx + X::TT - 1) / X::TT;
             c.rt = row_tiles<X>(a, c.d.n);
@@ -187,11 +195,20 @@ __device__ __noinline__ bool rows_settle(RowsCursor& c, const RowsArgs& a, int m
         }
       }
     }
-    if (c.rg * a.C + member < c.rt) return true;
+    if (c.rg * a.C + member < c.rt) return c;
     c.left -= c.nt - c.t;
     c.t = c.nt;
   }
-  return false;
+  c.left = 0;
+  return c;
+}
+// The next tile; false when the piece has none left.
+template <class X>
+__device__ __forceinline__ bool next_tile(RowsCursor& c, const RowsArgs& a, int member) {
+  ++c.t;
+  --c.left;
+  if (c.left > 0 && c.t >= c.nt) c = next_segment<X>(c, a, member);
+  return c.left > 0;
 }
 
 __device__ __forceinline__ float sum_inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }   // a sum that is no number stays one
@@ -296,9 +313,14 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 1) tmem_alloc(&sh.tmem, X::TMEM_COLS);
   if (warp == 2) {
     constexpr int SW = PP ? 4 : 8;         // softmax warps of a tile
-    for (uint64_t* b = sh.kfull + lane; b <= &sh.drain_pv; b += 32) {
-      const bool softmax = (b >= sh.sempty && b < sh.sempty + NS) || (b >= sh.pfull && b < sh.pfull + NP);
-      mbar_init(b, softmax ? SW : X::SHARED && b >= sh.kfull && b < sh.kfull + NM ? VT + 1 : (b >= sh.oempty && b < sh.oempty + 2 ? 8 : (b >= sh.joined && b < sh.joined + 2 ? 4 : 1)));
+    for (uint64_t* b = sh.kfull + lane; b <= &sh.drain; b += 32) {
+      int count = 1;
+      if (X::SHARED && b < sh.kfull + NF) count = VT + 1;
+      if ((b >= sh.sempty && b < sh.sempty + NS) || (b >= sh.pfull && b < sh.pfull + NP)) count = SW;
+      if (b >= sh.oempty && b < sh.oempty + NO) count = 8;
+      if (PP && b >= sh.joined && b < sh.joined + NG) count = 4;
+      if (b == &sh.drain) count = 2;
+      mbar_init(b, count);
     }
     fence_barrier_init();
   }
@@ -306,7 +328,7 @@ __global__ void __launch_bounds__(384, 1)
     sh.abort_flag = 0;
     sh.any = 0;
     sh.W = 0;
-    for (int j = 0; j < 4; ++j) sh.bad[j >> 1][j & 1] = 0;
+    for (int j = 0; j < 2 * NG; ++j) sh.bad[j >> 1][j & 1] = 0;
     prefetch_tensormap(&tmk);
     if (!X::SHARED) prefetch_tensormap(&tmv);
     prefetch_tensormap(&tmq);
@@ -374,13 +396,14 @@ __global__ void __launch_bounds__(384, 1)
       c.at_start = 1;
       c.whole_from = c.t == 0;
       c.left = line.start(team + 1) - pstart;
-      sh.first = c;
+      sh.first = RowsCut{c.t, c.nt, c.d.q0, c.d.n, c.g, c.rg, 0, 0};
       sh.W = W;
-      const bool any = rows_settle<X>(c, a, member);
+      if (c.rg * a.C + member >= c.rt) c = next_segment<X>(c, a, member);
       sh.cur = c;
-      ++c.t;
-      --c.left;
-      sh.any = any ? (rows_settle<X>(c, a, member) ? 2 : 1) : 0;
+      if (c.left > 0) {
+        prefetch_l2(a.bt + (size_t)c.s * a.max_blocks + ((c.t * TT) >> a.bs_log2));
+        sh.any = next_tile<X>(c, a, member) ? 2 : 1;
+      }
     }
   }
   __syncthreads();
@@ -437,9 +460,7 @@ __global__ void __launch_bounds__(384, 1)
         mn.part = blockIdx.x * 2 + (c.at_start ? 0 : 1);
         const bool seg_end = c.t + 1 == c.nt;
         mn.flags = (first ? F_FIRST : 0) | (seg_end || c.left == 1 ? F_LAST : 0) | (seg_end && c.whole_from ? F_WHOLE : 0);
-        ++c.t;
-        --c.left;
-        more = rows_settle<X>(c, a, member);
+        more = next_tile<X>(c, a, member);
         if (!more) mn.flags |= F_END;
       }
       if (i >= 0) {
@@ -483,10 +504,9 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int b = 0; b < MB; ++b) ids[b] = __shfl_sync(FULL_MASK, phys, b);
         const int grow = m.g << a.bs_log2, step = 128 << a.bs_log2;
-        auto fill = [&](uint8_t* dst, uint64_t* full, const CUtensorMap* tm, int c0, auto chunks_of) {
+        auto fill = [&](uint8_t* dst, uint64_t* full, const CUtensorMap* tm, int c0, bool tells, auto chunks_of) {
           constexpr int NC = decltype(chunks_of)::value;
           if (elected()) {
-            mbar_arrive_expect_tx(full, chunk_bytes * NC);
 #pragma unroll
             for (int b = 0; b < MB; ++b)
               if ((valid >> b) & 1) {
@@ -494,6 +514,10 @@ __global__ void __launch_bounds__(384, 1)
                 for (int ch = 0; ch < NC; ++ch) tma_load_3d(dst + ch * X::CHUNK + b * step, tm, c0 + ch * 64, grow, ids[b], full, pol);
               }
           }
+          // (the copies' bytes are counted behind them: the phase waits for this arrival)
+          if (tells && lane == 0) sh.meta[i % NM] = m;
+          __syncwarp();
+          if (elected()) mbar_arrive_expect_tx(full, chunk_bytes * NC);
           __syncwarp();
         };
         if constexpr (X::SHARED) {
@@ -502,21 +526,17 @@ __global__ void __launch_bounds__(384, 1)
             const int vt = lead ? v : VT / 2 + v, use = i * VT + vt, slot = use % NK;
             ok = use < NK || rows_wait(&sh.kempty[slot], use / NK - 1);
             if (!ok) break;
-            if (lead && v == 0 && lane == 0) sh.meta[i % NM] = m;
-            __syncwarp();
-            fill(sm + slot * X::KST, &sh.kfull[i % NM], &tmk, vt * 128, std::integral_constant<int, 2>());
+            fill(sm + slot * X::KST, &sh.kfull[i % NM], &tmk, vt * 128, lead && v == 0, std::integral_constant<int, 2>());
           }
           if (ok && !lead) {
             ok = i < NP || rows_wait(&sh.pslot[i % NP], i / NP - 1);
-            if (ok) fill(sm + X::P_OFF + (i % NP) * X::PST, &sh.kfull[i % NM], &tmk, VT * 128, std::integral_constant<int, 1>());
+            if (ok) fill(sm + X::P_OFF + (i % NP) * X::PST, &sh.kfull[i % NM], &tmk, VT * 128, false, std::integral_constant<int, 1>());
           }
         } else {
           const int st = i % NK;
           ok = i < NK || rows_wait(&sh.kempty[st], i / NK - 1);
           if (!ok) break;
-          if (lead && lane == 0) sh.meta[i % NM] = m;
-          __syncwarp();
-          fill(sm + st * X::KST + (lead ? 0 : X::KPART), lead ? &sh.kfull[st] : &sh.vfull[st], lead ? &tmk : &tmv, 0,
+          fill(sm + st * X::KST + (lead ? 0 : X::KPART), lead ? &sh.kfull[st] : &sh.vfull[st], lead ? &tmk : &tmv, 0, lead,
                std::integral_constant<int, KC>());
         }
         if (!ok) break;
@@ -538,7 +558,7 @@ __global__ void __launch_bounds__(384, 1)
       constexpr int NF = X::SHARED ? NM : NK;
       for (int j = max(0, i - NF); j <= i && live; ++j) live = rows_poll(&sh.kfull[j % NF], (j / NF) & 1, 20000000ull);
       live = !X::SHARED;
-      for (int j = max(0, i - NK); j <= i && live; ++j) live = rows_poll(&sh.vfull[j % NP], (j / NP) & 1, 20000000ull);
+      for (int j = max(0, i - NK); j <= i && live; ++j) live = rows_poll(&sh.vfull[X::SHARED ? 0 : j % NP], (j / NP) & 1, 20000000ull);
       if (kq >= 0) rows_poll(&sh.qfull[kq % NQ], (kq / NQ) & 1, 20000000ull);
     }
     __syncwarp();
@@ -609,7 +629,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 1
     for (int i = 0;; ++i) {
       const int pb = i % NP, k0 = i * VT;
-      ok = !sh.abort_flag && rows_wait(X::SHARED ? &sh.kfull[i % NF] : &sh.vfull[pb], X::SHARED ? i / NF : i / NP) &&
+      ok = !sh.abort_flag && rows_wait(X::SHARED ? &sh.kfull[i % NF] : &sh.vfull[X::SHARED ? 0 : pb], X::SHARED ? i / NF : i / NP) &&
            rows_wait(&sh.pfull[pb], i / NP);
       if (!ok) break;
       const RowsMeta& mt = sh.meta[i % NM];
@@ -638,7 +658,7 @@ __global__ void __launch_bounds__(384, 1)
         umma_commit(&sh.pempty[i & 1]);
         if (flags & F_LAST) {              // for the groups that had tiles of the segment
           if (!PP || (i & 1) == 0 || !(flags & G_SOLO)) umma_commit(&sh.ofull[0]);
-          if (PP && ((i & 1) == 1 || !(flags & G_SOLO))) umma_commit(&sh.ofull[1]);
+          if (PP && ((i & 1) == 1 || !(flags & G_SOLO))) umma_commit(&sh.ofull[NG - 1]);
         }
       }
       __syncwarp();
@@ -650,9 +670,9 @@ __global__ void __launch_bounds__(384, 1)
         set_err(a.err, PKV_DEV_TIMEOUT);
         sh.abort_flag = 1;
       }
-      umma_commit(&sh.drain_pv);
+      umma_commit(&sh.drain);
     }
-    rows_wait(&sh.drain_pv, 0);
+    rows_wait(&sh.drain, 0);
   } else if (warp >= 4) {
     // -------------------------- softmax and epilogue ------------------------
     // Warp w reaches the tensor-memory lanes of quarter w % 4: in S^T the cached rows 16 MT wq + ..., in fragments of
@@ -693,7 +713,6 @@ __global__ void __launch_bounds__(384, 1)
       // over, though: behind the group's last tile the keys of the tiles before it had landed, and behind this one's
       // scores the tile whose slot they took was done with.
       wait(&sh.kfull[i % NF], i / NF);                        // the metadata, which stay until P is there
-      wait(&sh.sfull[sb], i / NS);                            // the scores, and room for P in place of the keys
       if (bad) {
         sync(true);
         break;
@@ -701,6 +720,26 @@ __global__ void __launch_bounds__(384, 1)
       const RowsMeta& mt = sh.meta[i % NM];
       const int flags = mt.flags, ob = mt.k % NO;
       const bool special = mt.tile0 + TT > mt.ctx - mt.n || mt.invalid;
+      // what query row (tid + e NW) % R attends to in word (tid + e NW) / R of the tile's rows
+      constexpr int WN = (R * MT + NW - 1) / NW;
+      unsigned long long win[WN];
+      if (special) {
+#pragma unroll
+        for (int e = 0; e < WN; ++e) {
+          win[e] = 0;
+          const int c = (tid + e * NW) % R, w = (tid + e * NW) / R;
+          if (w < MT) {
+            const int tok = query_of<X>(a, mt.n, mt.t0, mt.h0, c).x;
+            if (tok >= 0) win[e] = attended(a, mt, tok, mt.tile0 + 64 * w);
+          }
+        }
+        __syncwarp();
+      }
+      wait(&sh.sfull[sb], i / NS);                            // the scores, and room for P in place of the keys
+      if (bad) {
+        sync(true);
+        break;
+      }
       uint8_t* pbuf = sm + X::P_OFF + pb * X::PST;
       RowsScratch<X>& scr = *reinterpret_cast<RowsScratch<X>*>(X::SHARED ? sm + X::W_OFF : pbuf + X::PBUF);
       const uint32_t st = tmem + lane_off + X::S_COL + R * sb + hb, acc = tmem + lane_off + (ob * NG + (PP ? gi : 0)) * VT * N2;
@@ -715,23 +754,18 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
       }
       if (special) {
-        // What each query row attends to in this tile, and what any of them does.  Scores that do not count become minus
-        // infinities (before the scale) where they lie.
-#pragma unroll 1
-        for (int e = tid; e < (R * MT + 31) / 32 * 32; e += NW) {
-          unsigned long long win = 0;
-          const int c = e % R, w = e / R;
-          if (w < MT) {
-            const int tok = query_of<X>(a, mt.n, mt.t0, mt.h0, c).x;
-            if (tok >= 0) win = attended(a, mt, tok, mt.tile0 + 64 * w);
-            scr.win[w][c] = win;
-          }
+        // What each query row attends to, and what any of them does.  Scores that do not count become minus infinities (before
+        // the scale) where they lie.
+#pragma unroll
+        for (int e = 0; e < WN; ++e) {
+          const int c = (tid + e * NW) % R, w = (tid + e * NW) / R;
+          if (w < MT) scr.win[w][c] = win[e];
           // a warp's lanes hold query rows of one word, or of two: an OR of each word's
           const unsigned group = R >= 32 ? FULL_MASK : (0xffffu << (lane & 16));
-          const uint32_t lo = __reduce_or_sync(group, (uint32_t)win), hi = __reduce_or_sync(group, (uint32_t)(win >> 32));
+          const uint32_t lo = __reduce_or_sync(group, (uint32_t)win[e]), hi = __reduce_or_sync(group, (uint32_t)(win[e] >> 32));
           if (w < MT && lane % (R >= 32 ? 32 : 16) == 0) scr.seen[w][R > 32 ? (c >> 5) : 0] = (unsigned long long)hi << 32 | lo;
         }
-        if (!X::SHARED) wait(&sh.vfull[pb], i / NP);          // the values, of which some are about to be overwritten
+        if (!X::SHARED) wait(&sh.vfull[X::SHARED ? 0 : pb], i / NP);          // the values, of which some are about to be overwritten
         if (sync(false), gone) break;
         const uint32_t none = a.scale_log2 < 0.f ? 0x7f800000u : 0xff800000u;
 #pragma unroll 1
@@ -936,18 +970,18 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
         // (behind this wait the segment before it in this O buffer is done with, in both groups)
         wait(&sh.ofull[wg], ends++);
-        if (tid < R && !bad) sh.sum[ob][wg][tid] = own;
         if (pair) {
+          if (tid < R && !bad) sh.sum[PP ? ob : 0][wg][PP ? tid : 0] = own;
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.joined[gi]);
+          if (lane == 0) mbar_arrive(&sh.joined[wg]);
           wait(&sh.joined[0], joins);
-          wait(&sh.joined[1], joins);
+          wait(&sh.joined[NG - 1], joins);
           ++joins;
         }
         if (tid < R && !bad) {
           // an accumulator none of whose rows counted (its sum is 0) has no part in it
           float2 x = own, y = make_float2(0.f, 0.f);
-          if (pair) x = sh.sum[ob][0][tid], y = sh.sum[ob][NG - 1][tid];
+          if (pair) x = sh.sum[PP ? ob : 0][0][PP ? tid : 0], y = sh.sum[PP ? ob : 0][NG - 1][PP ? tid : 0];
           const float M = fmaxf(x.y == 0.f ? -INFINITY : x.x, y.y == 0.f ? -INFINITY : y.x);
           float2 f = make_float2(x.y == 0.f ? 0.f : ex2(x.x - M), y.y == 0.f ? 0.f : ex2(y.x - M));
           const float L = x.y * f.x + y.y * f.y;
@@ -959,7 +993,11 @@ __global__ void __launch_bounds__(384, 1)
           } else if (!pair || gi == 0) {
             *reinterpret_cast<float2*>(a.ws_ml + ((size_t)part * R + tid) * 2) = make_float2(M, L);
           }
-          if (!pair || tid / (R / 2) == gi) sh.factor[ob][tid] = f;   // a pair's groups each put together half of the query rows
+          if constexpr (PP) {
+            if (!pair || tid / (R / 2) == gi) sh.factor[ob][tid] = f;   // a pair's groups each put together half of the query rows
+          } else {
+            sh.factor[ob][tid] = f.x;
+          }
         }
         if (sync(false), gone) break;
         tc_fence_after();
@@ -982,12 +1020,17 @@ __global__ void __launch_bounds__(384, 1)
               for (int p = HL - 2; p >= 0; --p) t[HL - 1][e] = __float_as_uint(__uint_as_float(t[HL - 1][e]) + __uint_as_float(t[p][e]));
           };
           load(0);
+          if constexpr (PP) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(t[HL - 1][e]) * sh.factor[ob][cc + e].x;
-          if (PP && pair) {
-            load(NG - 1);
+            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(t[HL - 1][e]) * sh.factor[ob][cc + e].x;
+            if (pair) {
+              load(NG - 1);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fmaf(__uint_as_float(t[HL - 1][e]), sh.factor[ob][cc + e].y, v[e]);
+              for (int e = 0; e < 8; ++e) v[e] = fmaf(__uint_as_float(t[HL - 1][e]), sh.factor[ob][cc + e].y, v[e]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(t[HL - 1][e]) * sh.factor[ob][cc + e];
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -1014,13 +1057,12 @@ __global__ void __launch_bounds__(384, 1)
         RowsCut cut = {};
         if (sh.W > 0) {
           const RowsLine line(sh.W, a.P);
-          const RowsCursor& c = sh.first;
-          const long long pstart = line.start(team), seg = pstart - c.t, prev = team > 0 ? line.start(team - 1) : 0;
-          if (c.t > 0 && prev <= seg) {
-            const int last = min(line.piece(min(seg + c.nt, line.W) - 1), line.P - 1);   // the last piece that holds a part
-            cut.parts = last - team + 2;
+          const int t = sh.first.parts, nt = sh.first.first;
+          const long long pstart = line.start(team), seg = pstart - t, prev = team > 0 ? line.start(team - 1) : 0;
+          if (t > 0 && prev <= seg) {
+            cut = sh.first;
+            cut.parts = min(line.piece(min(seg + nt, line.W) - 1), line.P - 1) - team + 2;   // up to the last piece that holds a part
             cut.first = prev == seg ? 0 : 1;
-            cut.q0 = c.d.q0; cut.n = c.d.n; cut.g = c.g; cut.rg = c.rg;
           }
         }
         a.cuts[team] = cut;
@@ -1046,53 +1088,123 @@ __global__ void __launch_bounds__(384, 1)
 }
 
 // ---- parts of cut segments ----------------------------------------------------------------------------
-// A CTA per (boundary, member, 8 query rows, 128 channels): a warp per query row joins the parts of its segment.
-template <class X>
+// Joins the parts of a segment that piece boundaries cut, by its first boundary.  Narrow: a warp per query row, all of its
+// channels.  Wide, for few long segments, of which each has many parts: a CTA per query row, whose warps take every eighth
+// part and meet in shared memory.
+template <class X, bool WIDE>
 __global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ RowsArgs a) {
-  constexpr int R = X::R, DV = X::DV, CB = DV < 128 ? DV : 128, V = CB / 32;   // channels of a CTA, of a lane
+  constexpr int R = X::R, DV = X::DV, V = DV < 128 ? 2 : 4, CH = DV / (32 * V);   // channels lane V + 32 V j + ...
   grid_dep_wait();
   grid_dep_launch();
   const int team = blockIdx.x / a.C, member = blockIdx.x % a.C, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const RowsCut cut = a.cuts[team];
   if (cut.parts == 0) return;
-  const int c = blockIdx.y * 8 + warp;
+  const int c = WIDE ? blockIdx.y : blockIdx.y * 8 + warp;
   int t0, h0;
   tile_of<X>(a, cut.rg * a.C + member, t0, h0);
   const int2 qh = query_of<X>(a, cut.n, t0, h0, c);
   if (qh.x < 0) return;
   const long long row = (long long)(cut.q0 + qh.x) * a.n_h + cut.g * a.G + qh.y;
-  auto part = [&](int p) { return (size_t)(((team - 1 + p) * a.C + member) * 2 + (p == 0 ? cut.first : 0)) * R + c; };
-  float M = -INFINITY;
-  for (int p = lane; p < cut.parts; p += 32) M = fmaxf(M, a.ws_ml[2 * part(p)]);
+  float M = -INFINITY, L = 0.f, acc[CH][V];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, o));
-  if (M == -INFINITY) M = 0.f;
-  float L = 0.f, acc[V];
+  for (int j = 0; j < CH; ++j)
 #pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.f;
-  const int ch = blockIdx.z * CB + lane * V;
-#pragma unroll 8
-  for (int p = 0; p < cut.parts; ++p) {
-    const size_t at = part(p);
-    const float2 ml = *reinterpret_cast<const float2*>(a.ws_ml + 2 * at);
-    const float w = ex2(ml.x - M);
-    L += w * ml.y;
-    if constexpr (V == 4) {
-      const float4 o = *reinterpret_cast<const float4*>(a.ws_o + at * DV + ch);
-      acc[0] += w * o.x; acc[1] += w * o.y; acc[2] += w * o.z; acc[3] += w * o.w;
+    for (int v = 0; v < V; ++v) acc[j][v] = 0.f;
+  constexpr int AT = DV > 256 ? 2 : 4;     // parts at a time, with all their loads ahead of the first use
+#pragma unroll 1
+  for (int p0 = WIDE ? warp * AT : 0; p0 < cut.parts; p0 += WIDE ? 8 * AT : AT) {
+    float2 ml[AT];
+    float o[AT][CH][V];
+#pragma unroll
+    for (int i = 0; i < AT; ++i) {
+      const int p = min(p0 + i, cut.parts - 1);
+      const size_t at = (size_t)(((team - 1 + p) * a.C + member) * 2 + (p == 0 ? cut.first : 0)) * R + c;
+      ml[i] = *reinterpret_cast<const float2*>(a.ws_ml + 2 * at);
+      if (p0 + i >= cut.parts) ml[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        const float* src = a.ws_o + at * DV + lane * V + 32 * V * j;
+        if constexpr (V == 4) *reinterpret_cast<float4*>(o[i][j]) = *reinterpret_cast<const float4*>(src);
+        else *reinterpret_cast<float2*>(o[i][j]) = *reinterpret_cast<const float2*>(src);
+      }
+    }
+    float top = M;
+#pragma unroll
+    for (int i = 0; i < AT; ++i) top = fmaxf(top, ml[i].x);
+    const float base = top == -INFINITY ? 0.f : top, keep = ex2(M - base);
+    L *= keep;
+    float w[AT];
+#pragma unroll
+    for (int i = 0; i < AT; ++i) {
+      w[i] = ml[i].x == -INFINITY ? 0.f : ex2(ml[i].x - base);
+      L += w[i] * ml[i].y;
+    }
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        acc[j][v] *= keep;
+#pragma unroll
+        for (int i = 0; i < AT; ++i) acc[j][v] += w[i] * o[i][j][v];
+      }
+    M = top;
+  }
+  auto store = [&](int ch, const float* x) {
+    const size_t at = (size_t)row * DV + ch;
+    if constexpr (X::F32) {
+      if constexpr (V == 4) *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = make_float4(x[0], x[1], x[2], x[3]);
+      else *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + at) = make_float2(x[0], x[1]);
     } else {
-      const float2 o = *reinterpret_cast<const float2*>(a.ws_o + at * DV + ch);
-      acc[0] += w * o.x; acc[1] += w * o.y;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at);
+      if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+      else *dst = pack_bf16(x[0], x[1]);
+    }
+  };
+  if constexpr (WIDE) {
+    __shared__ float2 s_ml[8];
+    __shared__ __align__(16) float s_o[8][DV];
+    if (lane == 0) s_ml[warp] = make_float2(M, L);
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) s_o[warp][lane * V + 32 * V * j + v] = acc[j][v];
+    __syncthreads();
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, s_ml[i].x);
+    if (top == -INFINITY) top = 0.f;
+    float sum = 0.f, f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      f[i] = ex2(s_ml[i].x - top);
+      sum += f[i] * s_ml[i].y;
+    }
+    const float inv = sum_inverse(sum);
+    for (int ch = threadIdx.x * V; ch < DV; ch += 256 * V) {
+      float x[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        x[v] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[v] += f[i] * s_o[i][ch + v];
+        x[v] *= inv;
+      }
+      store(ch, x);
+    }
+  } else {
+    const float inv = sum_inverse(L);
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[j][v] *= inv;
+      store(lane * V + 32 * V * j, acc[j]);
     }
   }
-  const float inv = sum_inverse(L);
-#pragma unroll
-  for (int v = 0; v < V; ++v) store_out(a, row * DV + ch + v, acc[v] * inv);
 }
 
 // ---- variants ----------------------------------------------------------------------------------------
 struct RowsVariant {
-  const void *fn, *join;
+  const void *fn, *join[2];
   size_t smem;
   int R, DV;
   bool ready[64];
@@ -1103,7 +1215,7 @@ static RowsVariant make_variant() {
   constexpr size_t smem = X::M_OFF + sizeof(RowsShared<X>);
   static_assert(smem <= 232448, "shared memory of one CTA");
   static_assert(X::Q_OFF % 1024 == 0 && X::P_OFF % 1024 == 0 && X::NCOL <= 512, "descriptor alignment, tensor memory");
-  return {(const void*)decode_rows_kernel<X>, (const void*)rows_join_kernel<X>, smem, X::R, X::DV, {}};
+  return {(const void*)decode_rows_kernel<X>, {(const void*)rows_join_kernel<X, false>, (const void*)rows_join_kernel<X, true>}, smem, X::R, X::DV, {}};
 }
 // bf16 outputs take p in two bf16 parts (16 bits) up to 32 query rows and in one with 64, fp32 outputs in three (all 24
 // bits), with 32 query rows at most: more columns do not fit the tensor memory beside a latent cache's O.
@@ -1132,6 +1244,7 @@ static RowsVariant* latent_variant(int latent, int R, bool f32) {
 // Query rows of a row tile, and members of a team, from the average of the sequences' query rows per kv head.
 struct RowsShape {
   int R, C, P;
+  long long groups;              // of row tiles, on average
 };
 static RowsShape rows_shape(int n_tok, int batch, int G, bool f32) {
   const long long rows = ((long long)n_tok * G + batch - 1) / batch;
@@ -1141,6 +1254,7 @@ static RowsShape rows_shape(int n_tok, int batch, int G, bool f32) {
   s.C = tiles <= 1 ? 1 : (tiles <= 2 ? 2 : 4);
   const int sms = device_sm_count();
   s.P = sms / s.C;
+  s.groups = (tiles + s.C - 1) / s.C;
   return s;
 }
 struct RowsLayout {
@@ -1245,8 +1359,11 @@ static pkv_status rows_attn(const RowsShape& s, RowsVariant* v, bool latent, con
   void* kargs[] = {&tmk, &tmv, &tmq, &a};
   cudaError_t e = launch_pdl(v->fn, dim3(s.P * s.C), dim3(384), v->smem, st, kargs);
   if (e == cudaSuccess) {
+    // the pieces over the segments: about the parts that each has
+    const long long segments = (long long)batch * n_kv * s.groups;
+    const bool wide = s.P >= 8 * segments;
     void* jargs[] = {&a};
-    e = launch_pdl(v->join, dim3(s.P * s.C, s.R / 8, v->DV < 128 ? 1 : v->DV / 128), dim3(256), 0, st, jargs);
+    e = launch_pdl(v->join[wide], dim3(s.P * s.C, wide ? s.R : s.R / 8), dim3(256), 0, st, jargs);
   }
   if (e == cudaSuccess) return PKV_OK;
   record_cuda_error(e);
