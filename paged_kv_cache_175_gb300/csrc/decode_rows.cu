@@ -104,28 +104,30 @@ struct RowsMeta {
 // Exponents (base 2) up to this are taken against an offset as it is: p is held in bf16 and fp32, whose range is 2^127, and
 // is as exact at 2^32 as at 1; what an offset this far below the maximum takes from the other end, 2^-94, is nothing.
 constexpr float kRowsLazy = 32.f;
-// For a softmax group: its first and its last tile of the segment, the piece's last one for it, and a segment of one tile.
-enum : int { G_FIRST = 64, G_LAST = 128, G_END = 256, G_SOLO = 512 };
+// For a softmax group: its first and its last tile of the segment; a segment of one tile.  (F_END: no tile, but the end.)
+enum : int { G_FIRST = 64, G_LAST = 128, G_SOLO = 256 };
 
 template <class X>
 struct RowsShared {
-  // What has landed, by stage (latent cache: all of a tile, by its metadata); slots of keys, or stages; values; P, by its slot;
+  // What has landed, by stage (latent cache: either half of a tile's chunks, by its metadata); slots of keys, or stages; values; P, by its slot;
   // slots of position chunks; the products of P by the tile's parity
-  uint64_t kfull[X::SHARED ? X::NM : X::NK], kempty[X::NK], vfull[X::SHARED ? 1 : X::NP], pfull[X::NP], pslot[X::SHARED ? X::NP : 1], pempty[2],
+  uint64_t kfull[X::SHARED ? 2 * X::NM : X::NK], kempty[X::NK], vfull[X::SHARED ? 1 : X::NP], pfull[X::NP], pslot[X::SHARED ? X::NP : 1], pempty[2],
       qfull[X::NQ], qempty[X::NQ], sfull[X::NS], sempty[X::NS], ofull[X::NG], oempty[X::NO], joined[X::NG], drain;
   RowsMeta meta[X::NM];          // of tile i: entry i % NM
   uint32_t tmem;
   int any;
   volatile int abort_flag;
   volatile int bad[X::NG][2];                                     // of each group of waiting warps, by the parity of its barriers
-  RowsCursor cur;                // the member's first tile
   RowsCut first;                 // the piece's first segment; parts: tiles ahead of the piece, first: of the segment
   long long W;
   float offset[X::NG][X::R];     // of each query row: what its exponents are taken against
   // Of a segment's end, by its O buffer: offset and sum of each query row in a group's tiles, factors of the output (of
   // either accumulator), and output rows
   float2 sum[X::PP ? X::NO : 1][X::NG][X::PP ? X::R : 1];
-  std::conditional_t<X::PP, float2, float> factor[X::NO][X::R];
+  union {
+    std::conditional_t<X::PP, float2, float> factor[X::NO][X::R];
+    RowsCursor cur;                // of the setup: the member's first tile (both producers have read it before any product)
+  };
   union {
     int row[X::NO][X::R];
     long long scan[12];            // of the setup
@@ -202,15 +204,6 @@ __device__ __noinline__ RowsCursor next_segment(RowsCursor c, const RowsArgs& a,
   c.left = 0;
   return c;
 }
-// The next tile; false when the piece has none left.
-template <class X>
-__device__ __forceinline__ bool next_tile(RowsCursor& c, const RowsArgs& a, int member) {
-  ++c.t;
-  --c.left;
-  if (c.left > 0 && c.t >= c.nt) c = next_segment<X>(c, a, member);
-  return c.left > 0;
-}
-
 __device__ __forceinline__ float sum_inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }   // a sum that is no number stays one
 
 // Token (of its sequence, -1: none) and head of the group of query row c of a row tile.
@@ -315,7 +308,7 @@ __global__ void __launch_bounds__(384, 1)
     constexpr int SW = PP ? 4 : 8;         // softmax warps of a tile
     for (uint64_t* b = sh.kfull + lane; b <= &sh.drain; b += 32) {
       int count = 1;
-      if (X::SHARED && b < sh.kfull + NF) count = VT + 1;
+      if (X::SHARED && b < sh.kempty) count = ((smem_u32(b) - smem_u32(sh.kfull)) & 8u) ? VT / 2 + 1 : VT / 2;
       if ((b >= sh.sempty && b < sh.sempty + NS) || (b >= sh.pfull && b < sh.pfull + NP)) count = SW;
       if (b >= sh.oempty && b < sh.oempty + NO) count = 8;
       if (PP && b >= sh.joined && b < sh.joined + NG) count = 4;
@@ -402,7 +395,7 @@ __global__ void __launch_bounds__(384, 1)
       sh.cur = c;
       if (c.left > 0) {
         prefetch_l2(a.bt + (size_t)c.s * a.max_blocks + ((c.t * TT) >> a.bs_log2));
-        sh.any = next_tile<X>(c, a, member) ? 2 : 1;
+        sh.any = 1;
       }
     }
   }
@@ -420,90 +413,76 @@ __global__ void __launch_bounds__(384, 1)
     const int bsz = 1 << a.bs_log2, nbt = TT >> a.bs_log2;    // rows of a block, blocks of a tile
     const uint64_t pol = policy_evict_first();
     RowsCursor c = sh.cur;
-    int k = -1, kq = -1, i = -1;
-    RowsMeta m = {}, mn = {};                                 // the tile to load, and the one behind it
-    int idx = 0, idxn = -1;                                   // number of the tile in its segment, within the piece
-    // Block ids, one per lane: 32 blocks from `wfrom` on, the 32 behind them, and the first 32 of the segment that comes next.
-    // (A copy of a register that a load is on the way to waits for it, so these are copied long after they are asked for.)
-    int win = -1, win_next = -1, win_first = -1, wfrom = 0;
-    const int32_t *row = a.bt, *rown = a.bt, *rown_m = a.bt;   // block tables of the segment being loaded, and of mn and m
-    auto ids_at = [&](const int32_t* bt, int ctx, int from) { return from + lane < (ctx + bsz - 1) >> a.bs_log2 ? bt[from + lane] : -1; };
-    bool more = true, ok = true;
+    int k = 0, kq = -1, i = 0;
+    bool ok = true;
+    auto ids_at = [&](int s, int ctx, int from) {             // block ids, one per lane
+      return from + lane < (ctx + bsz - 1) >> a.bs_log2 ? a.bt[(size_t)s * a.max_blocks + from + lane] : -1;
+    };
+    int win_first = ids_at(c.s, c.d.ctx, c.t * nbt);          // the first 32 of the segment that comes next
 #pragma unroll 1
-    for (;; ++i) {
-      const int blk0 = m.tile0 >> a.bs_log2;
-      if (i >= 0 && (m.flags & F_FIRST)) {
-        win = win_first;
-        wfrom = blk0;
-        row = rown_m;
-        win_next = ids_at(row, m.ctx, blk0 + 32);
-      } else if (i >= 0 && blk0 >= wfrom + 32) {
-        win = win_next;
-        wfrom += 32;
-        win_next = ids_at(row, m.ctx, wfrom + 32);
-      }
-      // The tile at the cursor is described a round before it is loaded; the first round only does that.
-      const bool has = more;
-      if (has) {
-        const bool first = k < 0 || c.t == 0;
-        if (first) {
-          ++k;
-          tile_of<X>(a, c.rg * a.C + member, mn.t0, mn.h0);
-          rown = a.bt + (size_t)c.s * a.max_blocks;
-          win_first = ids_at(rown, c.d.ctx, c.t * nbt);
+    for (;; ++k) {
+      // A segment: `count` tiles of it from c.t on.  Lane l keeps word l of its metadata (RowsMeta), of which a tile changes few.
+      const int count = c.left < c.nt - c.t ? (int)c.left : c.nt - c.t, all_blocks = (c.d.ctx + bsz - 1) >> a.bs_log2;
+      const int whole = c.whole_from && c.t + count == c.nt ? F_WHOLE : 0, grow = c.g << a.bs_log2, step = 128 << a.bs_log2;
+      int t0, h0;
+      tile_of<X>(a, c.rg * a.C + member, t0, h0);
+      int word = 0;
+      if (lane == 1) word = k;
+      if (lane == 3) word = c.d.ctx;
+      if (lane == 4) word = c.d.n;
+      if (lane == 5) word = c.d.q0;
+      if (lane == 6) word = t0;
+      if (lane == 7) word = h0;
+      if (lane == 8) word = c.g;
+      if (lane == 10) word = blockIdx.x * 2 + (c.at_start ? 0 : 1);
+      int blk0 = c.t * nbt, wfrom = blk0, win = win_first, win_next = ids_at(c.s, c.d.ctx, blk0 + 32);
+      // The segment's query rows.  With one buffer for them they come behind the first tile, which need not wait for the
+      // last segment's products.
+      auto queries = [&] {
+        const int qb = k % NQ;
+        ok = k < NQ || rows_wait(&sh.qempty[qb], k / NQ - 1);
+        if (!ok) return;
+        if (elected()) mbar_arrive_expect_tx(&sh.qfull[qb], (uint32_t)KC * 128u * (uint32_t)(X::SHARED ? R : a.gt * a.tpt));
+#pragma unroll 1
+        for (int ch = 0; ch < KC; ++ch)
+          if (elected())
+            tma_load_3d(sm + X::Q_OFF + qb * X::QBUF + ch * X::QCH, &tmq, ch * 64, X::SHARED ? (c.d.q0 + t0) * a.n_h + h0 : c.g * a.G + h0,
+                        X::SHARED ? 0 : c.d.q0 + t0, &sh.qfull[qb], pol);
+        kq = k;
+        __syncwarp();
+      };
+      if (NQ > 1 && lead) queries();
+      RowsCursor next = c;
+#pragma unroll 1
+      for (int j = 0; j < count && ok; ++j, ++i, blk0 += nbt) {
+        if (sh.abort_flag) {
+          ok = false;
+          break;
         }
-        idxn = first ? 0 : idxn + 1;
-        mn.k = k;
-        mn.tile0 = c.t * TT;
-        mn.ctx = c.d.ctx; mn.n = c.d.n; mn.q0 = c.d.q0;
-        mn.g = c.g;
-        mn.part = blockIdx.x * 2 + (c.at_start ? 0 : 1);
-        const bool seg_end = c.t + 1 == c.nt;
-        mn.flags = (first ? F_FIRST : 0) | (seg_end || c.left == 1 ? F_LAST : 0) | (seg_end && c.whole_from ? F_WHOLE : 0);
-        more = next_tile<X>(c, a, member);
-        if (!more) mn.flags |= F_END;
-      }
-      if (i >= 0) {
-        if (sh.abort_flag) break;
-        const unsigned used = (1u << min(((m.ctx + bsz - 1) >> a.bs_log2) - blk0, nbt)) - 1;   // blocks of the tile
+        if (blk0 >= wfrom + 32) {
+          win = win_next;
+          wfrom += 32;
+          win_next = ids_at(c.s, c.d.ctx, wfrom + 32);
+        }
         const int phys = __shfl_sync(FULL_MASK, win, (blk0 - wfrom + lane) & 31);
+        const unsigned used = (1u << min(all_blocks - blk0, nbt)) - 1;
         const unsigned valid = __ballot_sync(FULL_MASK, (unsigned)phys < (unsigned)a.num_blocks) & used;
         const uint32_t chunk_bytes = (uint32_t)__popc(valid) * 128u << a.bs_log2;
-        if (lead) {
-          // what the tile is to its softmax group
-          const bool next_last = has && mn.k == m.k && (mn.flags & F_LAST);
-          if (idx < (PP ? 2 : 1)) m.flags |= G_FIRST;
-          if (idx == 0 && (m.flags & F_LAST)) m.flags |= G_SOLO;
-          if ((m.flags & F_LAST) || (PP && next_last)) m.flags |= G_LAST;
-          if ((m.flags & F_END) || (PP && has && (mn.flags & F_END))) m.flags |= G_END;
-          if (PP && next_last) m.flags |= mn.flags & F_WHOLE;
-          m.invalid = (int)(used & ~valid);
-          if (lane == 0 && m.invalid) set_err(a.err, PKV_DEV_BAD_BLOCK);
-        }
-        // The segment's query rows.  With one buffer for them they come behind the tile, which need not wait for the
-        // last segment's products.
-        const bool asks = lead && (m.flags & F_FIRST);
-        auto queries = [&] {
-          const int qb = m.k % NQ;
-          ok = m.k < NQ || rows_wait(&sh.qempty[qb], m.k / NQ - 1);
-          if (!ok) return;
-          if (elected()) mbar_arrive_expect_tx(&sh.qfull[qb], (uint32_t)KC * 128u * (uint32_t)(X::SHARED ? R : a.gt * a.tpt));
-#pragma unroll 1
-          for (int ch = 0; ch < KC; ++ch)
-            if (elected())
-              tma_load_3d(sm + X::Q_OFF + qb * X::QBUF + ch * X::QCH, &tmq, ch * 64,
-                          X::SHARED ? (m.q0 + m.t0) * a.n_h + m.h0 : m.g * a.G + m.h0, X::SHARED ? 0 : m.q0 + m.t0, &sh.qfull[qb], pol);
-          kq = m.k;
-          __syncwarp();
-        };
-        if (NQ > 1 && asks) queries();
-        if (!ok) break;
-        // one fill of a slot: NC chunks from channel c0 on, of each block
         constexpr int MB = TT / 16;
         int ids[MB];
 #pragma unroll
         for (int b = 0; b < MB; ++b) ids[b] = __shfl_sync(FULL_MASK, phys, b);
-        const int grow = m.g << a.bs_log2, step = 128 << a.bs_log2;
+        if (lead) {
+          const bool last = j + 1 == count, next_last = PP && j + 2 == count;
+          const int flags = (j == 0 ? F_FIRST : 0) | (last ? F_LAST : 0) | whole | (j < (PP ? 2 : 1) ? G_FIRST : 0) |
+                            (last || next_last ? G_LAST : 0) | (count == 1 ? G_SOLO : 0);
+          if (lane == 0) word = flags;
+          if (lane == 2) word = blk0 << a.bs_log2;
+          if (lane == 9) word = (int)(used & ~valid);
+          if (lane == 9 && word) set_err(a.err, PKV_DEV_BAD_BLOCK);
+        }
+        // One fill of a slot: NC chunks from channel c0 on, of each block.  (The copies' bytes are counted behind them: the
+        // phase waits for this arrival.)
         auto fill = [&](uint8_t* dst, uint64_t* full, const CUtensorMap* tm, int c0, bool tells, auto chunks_of) {
           constexpr int NC = decltype(chunks_of)::value;
           if (elected()) {
@@ -514,38 +493,54 @@ __global__ void __launch_bounds__(384, 1)
                 for (int ch = 0; ch < NC; ++ch) tma_load_3d(dst + ch * X::CHUNK + b * step, tm, c0 + ch * 64, grow, ids[b], full, pol);
               }
           }
-          // (the copies' bytes are counted behind them: the phase waits for this arrival)
-          if (tells && lane == 0) sh.meta[i % NM] = m;
-          __syncwarp();
+          if (tells && lane < (int)(sizeof(RowsMeta) / 4)) reinterpret_cast<int*>(&sh.meta[i % NM])[lane] = word;
           if (elected()) mbar_arrive_expect_tx(full, chunk_bytes * NC);
           __syncwarp();
         };
         if constexpr (X::SHARED) {
+          uint64_t* full = &sh.kfull[2 * (i % NM) + (lead ? 0 : 1)];
 #pragma unroll 1
           for (int v = 0; v < VT / 2 && ok; ++v) {
             const int vt = lead ? v : VT / 2 + v, use = i * VT + vt, slot = use % NK;
             ok = use < NK || rows_wait(&sh.kempty[slot], use / NK - 1);
             if (!ok) break;
-            fill(sm + slot * X::KST, &sh.kfull[i % NM], &tmk, vt * 128, lead && v == 0, std::integral_constant<int, 2>());
+            fill(sm + slot * X::KST, full, &tmk, vt * 128, lead && v == 0, std::integral_constant<int, 2>());
           }
           if (ok && !lead) {
             ok = i < NP || rows_wait(&sh.pslot[i % NP], i / NP - 1);
-            if (ok) fill(sm + X::P_OFF + (i % NP) * X::PST, &sh.kfull[i % NM], &tmk, VT * 128, false, std::integral_constant<int, 1>());
+            if (ok) fill(sm + X::P_OFF + (i % NP) * X::PST, full, &tmk, VT * 128, false, std::integral_constant<int, 1>());
           }
         } else {
           const int st = i % NK;
           ok = i < NK || rows_wait(&sh.kempty[st], i / NK - 1);
-          if (!ok) break;
-          fill(sm + st * X::KST + (lead ? 0 : X::KPART), lead ? &sh.kfull[st] : &sh.vfull[st], lead ? &tmk : &tmv, 0, lead,
-               std::integral_constant<int, KC>());
+          if (ok)
+            fill(sm + st * X::KST + (lead ? 0 : X::KPART), lead ? &sh.kfull[st] : &sh.vfull[st], lead ? &tmk : &tmv, 0, lead,
+                 std::integral_constant<int, KC>());
         }
-        if (!ok) break;
-        if (NQ == 1 && asks) queries();
-        if (!ok || !has) break;
+        if (NQ == 1 && lead && j == 0 && ok) queries();
+        if (j + 1 == count) {              // on to the next segment, with its block ids on the way meanwhile
+          next.t += count;
+          next.left -= count;
+          if (next.left > 0) next = next_segment<X>(next, a, member);
+          if (next.left > 0) win_first = ids_at(next.s, next.d.ctx, next.t * nbt);
+        }
       }
-      m = mn;
-      rown_m = rown;
-      idx = idxn;
+      c = next;
+      if (!ok || c.left <= 0) break;
+    }
+    // Behind the last tile, an end for each softmax group.
+    if (ok && lead) {
+#pragma unroll 1
+      for (int z = 0; z < NG && ok; ++z, ++i) {
+        const int use = X::SHARED ? i * VT : i, slot = use % NK;
+        ok = use < NK || rows_wait(&sh.kempty[slot], use / NK - 1);
+        if (!ok) break;
+        if (lane == 0) {
+          sh.meta[i % NM].flags = F_END;
+          mbar_arrive_n(&sh.kfull[X::SHARED ? 2 * (i % NM) : slot], X::SHARED ? VT / 2 : 1);
+        }
+        __syncwarp();
+      }
     }
     ok = __all_sync(FULL_MASK, ok);
     if (!ok && lane == 0) {
@@ -555,10 +550,10 @@ __global__ void __launch_bounds__(384, 1)
     // After a timeout: let the loads already issued land before the CTA leaves (bounded).
     if (sh.abort_flag && lane == 0) {
       bool live = true;
-      constexpr int NF = X::SHARED ? NM : NK;
-      for (int j = max(0, i - NF); j <= i && live; ++j) live = rows_poll(&sh.kfull[j % NF], (j / NF) & 1, 20000000ull);
-      live = !X::SHARED;
-      for (int j = max(0, i - NK); j <= i && live; ++j) live = rows_poll(&sh.vfull[X::SHARED ? 0 : j % NP], (j / NP) & 1, 20000000ull);
+      for (int j = max(0, i - NF); j <= i && live; ++j) live = rows_poll(&sh.kfull[X::SHARED ? 2 * (j % NF) : j % NF], (j / NF) & 1, 20000000ull);
+      live = true;
+      for (int j = max(0, i - NF); j <= i && live; ++j)
+        live = rows_poll(X::SHARED ? &sh.kfull[2 * (j % NF) + 1] : &sh.vfull[j % NP], (j / NF) & 1, 20000000ull);
       if (kq >= 0) rows_poll(&sh.qfull[kq % NQ], (kq / NQ) & 1, 20000000ull);
     }
     __syncwarp();
@@ -572,10 +567,11 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 1
     for (int i = 0;; ++i) {
       const int k0 = X::SHARED ? i * VT : i, sb = i % NS;     // first slot of the tile's keys
-      ok = !sh.abort_flag && rows_wait(&sh.kfull[i % NF], i / NF);
+      ok = !sh.abort_flag && rows_wait(&sh.kfull[X::SHARED ? 2 * (i % NF) : i % NF], i / NF);
       if (!ok) break;
       const RowsMeta& mt = sh.meta[i % NM];
       const int flags = __shfl_sync(FULL_MASK, mt.flags, 0), k = __shfl_sync(FULL_MASK, mt.k, 0), qb = k % NQ;
+      if (flags & F_END) break;
       ok = (!(flags & F_FIRST) || rows_wait(&sh.qfull[qb], k / NQ)) && (i < NS || rows_wait(&sh.sempty[sb], i / NS - 1));
       if (!ok) break;
       const uint32_t qa = sbase + ((X::Q_OFF + qb * X::QBUF) >> 4), d = tm + X::S_COL + R * sb;
@@ -596,8 +592,14 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
       };
       if constexpr (X::SHARED) {
+        // the halves of its chunks as they land
 #pragma unroll 1
-        for (int u = 0; u < VT; ++u) chunks(sbase + ((k0 + u) % NK * X::KST >> 4), 2 * u, 4, std::integral_constant<int, 2>());
+        for (int u = 0; u < VT / 2; ++u) chunks(sbase + ((k0 + u) % NK * X::KST >> 4), 2 * u, 4, std::integral_constant<int, 2>());
+        ok = rows_wait(&sh.kfull[2 * (i % NF) + 1], i / NF);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int u = VT / 2; u < VT; ++u) chunks(sbase + ((k0 + u) % NK * X::KST >> 4), 2 * u, 4, std::integral_constant<int, 2>());
         chunks(sbase + ((X::P_OFF + (i % NP) * X::PST) >> 4), KC - 1, a.last_steps, std::integral_constant<int, 1>());
       } else {
         chunks(sbase + ((i % NK) * X::KST >> 4), 0, 4, std::integral_constant<int, KC>());
@@ -607,7 +609,6 @@ __global__ void __launch_bounds__(384, 1)
         if (flags & F_LAST) umma_commit(&sh.qempty[qb]);
       }
       __syncwarp();
-      if (flags & F_END) break;
     }
     ok = __all_sync(FULL_MASK, ok);
     if (elected()) {
@@ -629,11 +630,13 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 1
     for (int i = 0;; ++i) {
       const int pb = i % NP, k0 = i * VT;
-      ok = !sh.abort_flag && rows_wait(X::SHARED ? &sh.kfull[i % NF] : &sh.vfull[X::SHARED ? 0 : pb], X::SHARED ? i / NF : i / NP) &&
-           rows_wait(&sh.pfull[pb], i / NP);
+      ok = !sh.abort_flag && rows_wait(&sh.kfull[X::SHARED ? 2 * (i % NF) : i % NF], i / NF);
       if (!ok) break;
       const RowsMeta& mt = sh.meta[i % NM];
       const int flags = __shfl_sync(FULL_MASK, mt.flags, 0), k = __shfl_sync(FULL_MASK, mt.k, 0), ob = k % NO;
+      if (flags & F_END) break;
+      ok = rows_wait(X::SHARED ? &sh.kfull[2 * (i % NF) + 1] : &sh.vfull[X::SHARED ? 0 : pb], i / NF) && rows_wait(&sh.pfull[pb], i / NP);
+      if (!ok) break;
       const int nks = __shfl_sync(FULL_MASK, (min(TT, mt.ctx - mt.tile0) + 15) >> 4, 0);
       ok = !(flags & F_FIRST) || k < NO || rows_wait(&sh.oempty[ob], k / NO - 1);
       if (!ok) break;
@@ -662,7 +665,6 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
       __syncwarp();
-      if (flags & F_END) break;
     }
     ok = __all_sync(FULL_MASK, ok);
     if (elected()) {
@@ -707,18 +709,19 @@ __global__ void __launch_bounds__(384, 1)
     };
 
 #pragma unroll 1
-    for (int i = PP ? gi : 0; sh.any > (PP ? gi : 0); i += PP ? 2 : 1) {
+    for (int i = PP ? gi : 0; sh.any; i += PP ? 2 : 1) {
       const int pb = i % NP, sb = i % NS, k0 = X::SHARED ? i * VT : i;
       // A barrier tells a phase from the one before it only by parity, and this group may not have waited for that.  It is
       // over, though: behind the group's last tile the keys of the tiles before it had landed, and behind this one's
       // scores the tile whose slot they took was done with.
-      wait(&sh.kfull[i % NF], i / NF);                        // the metadata, which stay until P is there
+      wait(&sh.kfull[X::SHARED ? 2 * (i % NF) : i % NF], i / NF);   // the metadata, which stay until P is there
       if (bad) {
         sync(true);
         break;
       }
       const RowsMeta& mt = sh.meta[i % NM];
       const int flags = mt.flags, ob = mt.k % NO;
+      if (flags & F_END) break;
       const bool special = mt.tile0 + TT > mt.ctx - mt.n || mt.invalid;
       // what query row (tid + e NW) % R attends to in word (tid + e NW) / R of the tile's rows
       constexpr int WN = (R * MT + NW - 1) / NW;
@@ -792,16 +795,20 @@ __global__ void __launch_bounds__(384, 1)
         // V rows that no query row attends to, and that the product reads with p = 0: they may hold anything
         const int topr = (min(TT, mt.ctx - mt.tile0) + 15) & ~15;
 #pragma unroll 1
-        for (int row = tid >> 5; row < topr; row += NW / 32) {
-          unsigned long long seen = scr.seen[row >> 6][0];
-          if constexpr (R > 32) seen |= scr.seen[row >> 6][1];
-          if ((seen >> (row & 63)) & 1) continue;
+        for (int w = 0; w < MT; ++w) {
+          unsigned long long rows = ~scr.seen[w][0] & ones_below(topr - 64 * w);
+          if constexpr (R > 32) rows &= ~scr.seen[w][1];
 #pragma unroll 1
-          for (int v = lane; v < X::VC * 8; v += 32) {
-            const int ch = v >> 3;
-            uint8_t* base = X::SHARED ? sm + ((k0 + (ch >> 1)) % NK) * X::KST + (ch & 1) * X::CHUNK
-                                      : sm + (i % NK) * X::KST + X::KPART + ch * X::CHUNK;
-            *reinterpret_cast<uint4*>(base + row * 128 + (v & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          for (; rows; rows &= rows - 1) {
+            const int row = 64 * w + __ffsll(rows) - 1;
+            if (row % (NW / 32) != tid >> 5) continue;
+#pragma unroll 1
+            for (int v = lane; v < X::VC * 8; v += 32) {
+              const int ch = v >> 3;
+              uint8_t* base = X::SHARED ? sm + ((k0 + (ch >> 1)) % NK) * X::KST + (ch & 1) * X::CHUNK
+                                        : sm + (i % NK) * X::KST + X::KPART + ch * X::CHUNK;
+              *reinterpret_cast<uint4*>(base + row * 128 + (v & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
         }
         __syncwarp();
@@ -928,13 +935,13 @@ __global__ void __launch_bounds__(384, 1)
             ts[q + 1] = t1;
           }
         }
+        tc_fence_before();
+        fence_proxy_async_smem();          // the rows written above, for the tensor core
         if (raise) break;
         raise = sync(top > kRowsLazy);
         if (gone || !raise) break;
       }
       if (gone) break;
-#pragma unroll
-      for (int q = 0; q < NC; ++q) l[q] += ts[q];
       const bool ends_here = flags & G_LAST;
       float2 own = make_float2(0.f, 0.f);  // of query row tid, at the segment's end
       int out_row = -1;
@@ -942,7 +949,7 @@ __global__ void __launch_bounds__(384, 1)
         // the sums over all cached rows of the group's tiles, while the scratch is there
 #pragma unroll
         for (int q = 0; q < NC; ++q) {
-          float v = l[q];
+          float v = l[q] + ts[q];
 #pragma unroll
           for (int o = 4; o <= 16; o <<= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
           if (lane < 4) scr.red[wq][c0 + 8 * (q >> 1) + (q & 1)] = v;
@@ -951,13 +958,13 @@ __global__ void __launch_bounds__(384, 1)
         if (tid < R) own = make_float2(off[tid], (scr.red[0][tid] + scr.red[1][tid]) + (scr.red[2][tid] + scr.red[3][tid]));
       }
       const int part = mt.part, q0 = mt.q0, n = mt.n, t0 = mt.t0, h0 = mt.h0, g = mt.g;   // (they may be gone behind P)
-      tc_fence_before();
-      fence_proxy_async_smem();            // the rows written above, for the tensor core
       __syncwarp();
       if (lane == 0 && !bad) {
-        mbar_arrive(&sh.sempty[sb]);
         mbar_arrive(&sh.pfull[pb]);
+        mbar_arrive(&sh.sempty[sb]);
       }
+#pragma unroll
+      for (int q = 0; q < NC; ++q) l[q] += ts[q];
 
       if (ends_here) {
         // Behind the segment's last product, its output rows.  With two accumulators the groups exchange their states, and
@@ -1045,7 +1052,6 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_n(&sh.oempty[ob], PP && !pair ? 2 : 1);
       }
-      if (flags & G_END) break;
     }
     if (bad && lane == 0) {
       set_err(a.err, PKV_DEV_TIMEOUT);
