@@ -76,22 +76,24 @@ struct RowsCfg {
   static constexpr int N2 = R * HL;                           // columns of the second product
   static constexpr int QCH = R * 128, QBUF = KC * QCH;
   static constexpr int PAT = (N2 + 63) / 64, PBUF = PAT * CHUNK;
-  // Rings, from what 227 KB hold.  K and V pools: NK stages of a tile's keys and its values.  Latent cache: NK slots of two
+  // Rings, from what 227 KB hold.  K and V pools: NK stages of a tile's keys and NV of its values, which are held for less of
+  // a tile's way: with 64 query rows of 128 channels, where that way and not the memory sets the pace, 4 and 2 (8 x 8-32K
+  // tokens, 512 rows: 431 us, and 475 with 3 and 3).  Latent cache: NK slots of two
   // chunks, which the second product frees one after another, and NP slots of the position chunk.  The tile's P takes
   // the place of its keys (of their position chunk), which the first product is the only one to read.
   static constexpr bool FULL = SHARED && KC == 9 && R == 64;  // 72 KB of query rows
   static constexpr int KPART = KC * CHUNK > PBUF + 4096 ? KC * CHUNK : PBUF + 4096;   // P and the scratch behind it
-  static constexpr int KST = SHARED ? 2 * CHUNK : KPART + VC * CHUNK;
+  static constexpr int KST = SHARED ? 2 * CHUNK : KPART, VST = VC * CHUNK;
   static constexpr int PST = SHARED ? PBUF : KST;
   static constexpr int NQ = SHARED && (KC == 9 ? R > 16 : R == 64) ? 1 : 2;
-  static constexpr int NK = SHARED ? (FULL || PAT > 1 ? 8 : 9) : (KC == 1 ? 4 : 3);
+  static constexpr int NK = SHARED ? (FULL || PAT > 1 ? 8 : 9) : (KC == 1 || R == 64 ? 4 : 3), NV = SHARED ? 1 : (KC == 1 ? 4 : (R == 64 ? 2 : 3));
   static constexpr int NP = SHARED ? 3 : NK;                  // tiles whose P there is room for
   static constexpr int NM = SHARED ? (KC == 9 ? 3 : 8) : NK;  // metadata of tiles: of all that the ring may hold a part of
   static constexpr int NS = PP ? 4 : 2, NG = PP ? 2 : 1;      // S buffers; accumulators of a segment
   static constexpr int NO = VT * N2 * NG * 2 + NS * R <= 512 && !(PP && R == 64) ? 2 : 1;
   static constexpr int S_COL = VT * N2 * NG * NO, NCOL = S_COL + NS * R;
   static constexpr uint32_t TMEM_COLS = NCOL <= 64 ? 64 : (NCOL <= 128 ? 128 : (NCOL <= 256 ? 256 : 512));
-  static constexpr int P_OFF = SHARED ? NK * KST : 0, Q_OFF = NK * KST + (SHARED ? NP * PST : 0), W_OFF = Q_OFF + NQ * QBUF, M_OFF = W_OFF + (SHARED ? 28 * R + 16 : 0);   // W: scratch
+  static constexpr int P_OFF = SHARED ? NK * KST : 0, V_OFF = NK * KST, Q_OFF = NK * KST + (SHARED ? NP * PST : NV * VST), W_OFF = Q_OFF + NQ * QBUF, M_OFF = W_OFF + (SHARED ? 28 * R + 16 : 0);   // W: scratch
   static constexpr bool F32 = HL == 3;                        // output type
 };
 
@@ -111,7 +113,7 @@ template <class X>
 struct RowsShared {
   // What has landed, by stage (latent cache: either half of a tile's chunks, by its metadata); slots of keys, or stages; values; P, by its slot;
   // slots of position chunks; the products of P by the tile's parity
-  uint64_t kfull[X::SHARED ? 2 * X::NM : X::NK], kempty[X::NK], vfull[X::SHARED ? 1 : X::NP], pfull[X::NP], pslot[X::SHARED ? X::NP : 1], pempty[2],
+  uint64_t kfull[X::SHARED ? 2 * X::NM : X::NK], kempty[X::NK], vfull[X::NV], vempty[X::NV], pfull[X::NP], pslot[X::SHARED ? X::NP : 1], pempty[2],
       qfull[X::NQ], qempty[X::NQ], sfull[X::NS], sempty[X::NS], ofull[X::NG], oempty[X::NO], joined[X::NG], drain;
   RowsMeta meta[X::NM];          // of tile i: entry i % NM
   uint32_t tmem;
@@ -291,7 +293,7 @@ __global__ void __launch_bounds__(384, 1)
     decode_rows_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                        const __grid_constant__ CUtensorMap tmq, const __grid_constant__ RowsArgs a) {
   constexpr int TT = X::TT, R = X::R, HL = X::HL, N2 = X::N2, KC = X::KC, VT = X::VT, MT = X::MT, DV = X::DV;
-  constexpr int NK = X::NK, NM = X::NM, NP = X::NP, NO = X::NO, NS = X::NS, NG = X::NG, NQ = X::NQ;
+  constexpr int NK = X::NK, NV = X::NV, NM = X::NM, NP = X::NP, NO = X::NO, NS = X::NS, NG = X::NG, NQ = X::NQ;
   constexpr int NF = X::SHARED ? NM : NK;                     // full barriers
   constexpr bool PP = X::PP;
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -511,10 +513,10 @@ __global__ void __launch_bounds__(384, 1)
             if (ok) fill(sm + X::P_OFF + (i % NP) * X::PST, full, &tmk, VT * 128, false, std::integral_constant<int, 1>());
           }
         } else {
-          const int st = i % NK;
-          ok = i < NK || rows_wait(&sh.kempty[st], i / NK - 1);
+          const int depth = lead ? NK : NV, st = i % depth;
+          ok = i < depth || rows_wait(lead ? &sh.kempty[st] : &sh.vempty[st], i / depth - 1);
           if (ok)
-            fill(sm + st * X::KST + (lead ? 0 : X::KPART), lead ? &sh.kfull[st] : &sh.vfull[st], lead ? &tmk : &tmv, 0, lead,
+            fill(sm + (lead ? st * X::KST : X::V_OFF + st * X::VST), lead ? &sh.kfull[st] : &sh.vfull[st], lead ? &tmk : &tmv, 0, lead,
                  std::integral_constant<int, KC>());
         }
         if (NQ == 1 && lead && j == 0 && ok) queries();
@@ -552,8 +554,9 @@ __global__ void __launch_bounds__(384, 1)
       bool live = true;
       for (int j = max(0, i - NF); j <= i && live; ++j) live = rows_poll(&sh.kfull[X::SHARED ? 2 * (j % NF) : j % NF], (j / NF) & 1, 20000000ull);
       live = true;
-      for (int j = max(0, i - NF); j <= i && live; ++j)
-        live = rows_poll(X::SHARED ? &sh.kfull[2 * (j % NF) + 1] : &sh.vfull[j % NP], (j / NF) & 1, 20000000ull);
+      constexpr int ND = X::SHARED ? NM : NV;
+      for (int j = max(0, i - ND); j <= i && live; ++j)
+        live = rows_poll(X::SHARED ? &sh.kfull[2 * (j % NF) + 1] : &sh.vfull[j % NV], (j / ND) & 1, 20000000ull);
       if (kq >= 0) rows_poll(&sh.qfull[kq % NQ], (kq / NQ) & 1, 20000000ull);
     }
     __syncwarp();
@@ -635,7 +638,7 @@ __global__ void __launch_bounds__(384, 1)
       const RowsMeta& mt = sh.meta[i % NM];
       const int flags = __shfl_sync(FULL_MASK, mt.flags, 0), k = __shfl_sync(FULL_MASK, mt.k, 0), ob = k % NO;
       if (flags & F_END) break;
-      ok = rows_wait(X::SHARED ? &sh.kfull[2 * (i % NF) + 1] : &sh.vfull[X::SHARED ? 0 : pb], i / NF) && rows_wait(&sh.pfull[pb], i / NP);
+      ok = rows_wait(X::SHARED ? &sh.kfull[2 * (i % NF) + 1] : &sh.vfull[i % NV], X::SHARED ? i / NF : i / NV) && rows_wait(&sh.pfull[pb], i / NP);
       if (!ok) break;
       const int nks = __shfl_sync(FULL_MASK, (min(TT, mt.ctx - mt.tile0) + 15) >> 4, 0);
       ok = !(flags & F_FIRST) || k < NO || rows_wait(&sh.oempty[ob], k / NO - 1);
@@ -646,18 +649,18 @@ __global__ void __launch_bounds__(384, 1)
       const uint32_t d = tm + (ob * NG + (PP ? i & 1 : 0)) * VT * N2;
 #pragma unroll 1
       for (int vt = 0; vt < VT; ++vt) {
-        const int slot = X::SHARED ? (k0 + vt) % NK : i % NK;
-        const uint32_t vb = sbase + ((slot * X::KST + (X::SHARED ? 0 : X::KPART)) >> 4);
+        const int slot = X::SHARED ? (k0 + vt) % NK : i % NV;
+        const uint32_t vb = sbase + ((X::SHARED ? slot * X::KST : X::V_OFF + slot * X::VST) >> 4);
         if (elected()) {
 #pragma unroll
           for (int kk = 0; kk < TT / 16; ++kk)
             if (kk < nks) umma_bf16_lo(d + vt * N2, vb + kk * 128, HI, pa + kk * 128, HI, IPV, kk ? 1u : acc0);
-          umma_commit(&sh.kempty[slot]);
+          umma_commit(X::SHARED ? &sh.kempty[slot] : &sh.vempty[slot]);
         }
         __syncwarp();
       }
       if (elected()) {
-        if (X::SHARED) umma_commit(&sh.pslot[pb]);
+        umma_commit(X::SHARED ? &sh.pslot[pb] : &sh.kempty[pb]);
         umma_commit(&sh.pempty[i & 1]);
         if (flags & F_LAST) {              // for the groups that had tiles of the segment
           if (!PP || (i & 1) == 0 || !(flags & G_SOLO)) umma_commit(&sh.ofull[0]);
@@ -768,7 +771,10 @@ __global__ void __launch_bounds__(384, 1)
           const uint32_t lo = __reduce_or_sync(group, (uint32_t)win[e]), hi = __reduce_or_sync(group, (uint32_t)(win[e] >> 32));
           if (w < MT && lane % (R >= 32 ? 32 : 16) == 0) scr.seen[w][R > 32 ? (c >> 5) : 0] = (unsigned long long)hi << 32 | lo;
         }
-        if (!X::SHARED) wait(&sh.vfull[X::SHARED ? 0 : pb], i / NP);          // the values, of which some are about to be overwritten
+        if (PP) {                          // the values, of which some are about to be overwritten, behind the group's last product
+          if (i >= 2) wait(&sh.pempty[i & 1], i / 2 - 1);
+          wait(&sh.vfull[i % NV], i / NV);
+        }
         if (sync(false), gone) break;
         const uint32_t none = a.scale_log2 < 0.f ? 0x7f800000u : 0xff800000u;
 #pragma unroll 1
@@ -806,7 +812,7 @@ __global__ void __launch_bounds__(384, 1)
             for (int v = lane; v < X::VC * 8; v += 32) {
               const int ch = v >> 3;
               uint8_t* base = X::SHARED ? sm + ((k0 + (ch >> 1)) % NK) * X::KST + (ch & 1) * X::CHUNK
-                                        : sm + (i % NK) * X::KST + X::KPART + ch * X::CHUNK;
+                                        : sm + X::V_OFF + (i % NV) * X::VST + ch * X::CHUNK;
               *reinterpret_cast<uint4*>(base + row * 128 + (v & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
           }
