@@ -324,5 +324,9 @@ void record_cuda_error(cudaError_t e);
 int encode_tensor_map_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                          uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0, uint32_t box1,
                          uint32_t box2 = 1);
+// Rows of `chunks` 64-channel chunks of bf16 (the first of a row of row_bytes), `rows` (a multiple of 8) to a block.  A copy
+// brings box_rows rows of box_chunks chunks: shared memory gets, of every 8 rows in turn, 1024 bytes of each chunk.
+int encode_tensor_map_chunks(CUtensorMap* map, const void* base, int chunks, uint64_t rows, uint64_t blocks, uint64_t row_bytes,
+                             uint32_t box_chunks, uint32_t box_rows);
 
 }  // namespace pkv

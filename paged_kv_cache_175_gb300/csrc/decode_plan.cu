@@ -30,8 +30,8 @@ int device_sm_count() {
   return n;
 }
 
-int encode_tensor_map_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
-                         uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0, uint32_t box1, uint32_t box2) {
+static int encode_tiled(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                        const cuuint32_t* box) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -43,14 +43,25 @@ int encode_tensor_map_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64
       encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
   if (!encode) return -1;
-  const cuuint64_t dims[3] = {d0, d1, d2};
-  const cuuint64_t strides[2] = {stride1_bytes, stride2_bytes};
-  const cuuint32_t box[3] = {box0, box1, box2};
-  const cuuint32_t elem[3] = {1, 1, 1};
-  CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+  const cuuint32_t elem[5] = {1, 1, 1, 1, 1};
+  CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box,
                       elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? 0 : (int)r;
+}
+int encode_tensor_map_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                         uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0, uint32_t box1, uint32_t box2) {
+  const cuuint64_t dims[3] = {d0, d1, d2};
+  const cuuint64_t strides[2] = {stride1_bytes, stride2_bytes};
+  const cuuint32_t box[3] = {box0, box1, box2};
+  return encode_tiled(map, base, 3, dims, strides, box);
+}
+int encode_tensor_map_chunks(CUtensorMap* map, const void* base, int chunks, uint64_t rows, uint64_t blocks, uint64_t row_bytes,
+                             uint32_t box_chunks, uint32_t box_rows) {
+  const cuuint64_t dims[5] = {64, 8, (cuuint64_t)chunks, rows / 8, blocks};
+  const cuuint64_t strides[4] = {row_bytes, 128, 8 * row_bytes, rows * row_bytes};
+  const cuuint32_t box[5] = {64, 8, box_chunks, box_rows / 8, 1};
+  return encode_tiled(map, base, 5, dims, strides, box);
 }
 
 int ring_stages(size_t stage_bytes, size_t ring_bytes, const char* env) {

@@ -73,6 +73,9 @@ struct RowsCfg {
   static constexpr int MT = TT / 64;
   static constexpr int DV = VT * VM, VC = DV / 64;
   static constexpr int CHUNK = TT * 128;
+  // Bytes from 8 rows of a slot to the next 8: a copy brings a block's rows of all of a slot's chunks, 1024 bytes of each
+  // chunk for every 8 rows.
+  static constexpr int GS = SHARED ? 2048 : KC * 1024;
   static constexpr int N2 = R * HL;                           // columns of the second product
   static constexpr int QCH = R * 128, QBUF = KC * QCH;
   static constexpr int PAT = (N2 + 63) / 64, PBUF = PAT * CHUNK;
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(384, 1)
     sh.W = 0;
     for (int j = 0; j < 2 * NG; ++j) sh.bad[j >> 1][j & 1] = 0;
     prefetch_tensormap(&tmk);
-    if (!X::SHARED) prefetch_tensormap(&tmv);
+    prefetch_tensormap(&tmv);
     prefetch_tensormap(&tmq);
   }
   // query rows past a tile's own hold zeros until the end
@@ -425,7 +428,7 @@ __global__ void __launch_bounds__(384, 1)
     for (;; ++k) {
       // A segment: `count` tiles of it from c.t on.  Lane l keeps word l of its metadata (RowsMeta), of which a tile changes few.
       const int count = c.left < c.nt - c.t ? (int)c.left : c.nt - c.t, all_blocks = (c.d.ctx + bsz - 1) >> a.bs_log2;
-      const int whole = c.whole_from && c.t + count == c.nt ? F_WHOLE : 0, grow = c.g << a.bs_log2, step = 128 << a.bs_log2;
+      const int whole = c.whole_from && c.t + count == c.nt ? F_WHOLE : 0;
       int t0, h0;
       tile_of<X>(a, c.rg * a.C + member, t0, h0);
       int word = 0;
@@ -469,7 +472,7 @@ __global__ void __launch_bounds__(384, 1)
         const int phys = __shfl_sync(FULL_MASK, win, (blk0 - wfrom + lane) & 31);
         const unsigned used = (1u << min(all_blocks - blk0, nbt)) - 1;
         const unsigned valid = __ballot_sync(FULL_MASK, (unsigned)phys < (unsigned)a.num_blocks) & used;
-        const uint32_t chunk_bytes = (uint32_t)__popc(valid) * 128u << a.bs_log2;
+        const uint32_t rows_bytes = (uint32_t)__popc(valid) << a.bs_log2;   // rows that are copied
         constexpr int MB = TT / 16;
         int ids[MB];
 #pragma unroll
@@ -483,20 +486,29 @@ __global__ void __launch_bounds__(384, 1)
           if (lane == 9) word = (int)(used & ~valid);
           if (lane == 9 && word) set_err(a.err, PKV_DEV_BAD_BLOCK);
         }
-        // One fill of a slot: NC chunks from channel c0 on, of each block.  (The copies' bytes are counted behind them: the
+        // One fill of a slot: all of its chunks of each block, from chunk c0 on.  (The copies' bytes are counted behind them: the
         // phase waits for this arrival.)
-        auto fill = [&](uint8_t* dst, uint64_t* full, const CUtensorMap* tm, int c0, bool tells, auto chunks_of) {
-          constexpr int NC = decltype(chunks_of)::value;
+        const int step = X::GS / 8 << a.bs_log2, group = c.g << (a.bs_log2 - 3);
+        auto fill = [&](uint8_t* dst, uint64_t* full, const CUtensorMap* tm, int c0, bool tells) {
+          auto box = [&](int b) {
+            if ((valid >> b) & 1) tma_load_5d(dst + b * step, tm, 0, 0, c0, group, ids[b], full, pol);
+          };
           if (elected()) {
+            box(0);
+            if (MB == 8 || nbt > 1) {
+              box(1);
+              if (nbt > 2) {
+                box(2);
+                box(3);
+                if (MB == 8 && nbt > 4) {
 #pragma unroll
-            for (int b = 0; b < MB; ++b)
-              if ((valid >> b) & 1) {
-#pragma unroll
-                for (int ch = 0; ch < NC; ++ch) tma_load_3d(dst + ch * X::CHUNK + b * step, tm, c0 + ch * 64, grow, ids[b], full, pol);
+                  for (int b = 4; b < MB; ++b) box(b);
+                }
               }
+            }
           }
           if (tells && lane < (int)(sizeof(RowsMeta) / 4)) reinterpret_cast<int*>(&sh.meta[i % NM])[lane] = word;
-          if (elected()) mbar_arrive_expect_tx(full, chunk_bytes * NC);
+          if (elected()) mbar_arrive_expect_tx(full, rows_bytes * (X::GS / 8));
           __syncwarp();
         };
         if constexpr (X::SHARED) {
@@ -506,18 +518,34 @@ __global__ void __launch_bounds__(384, 1)
             const int vt = lead ? v : VT / 2 + v, use = i * VT + vt, slot = use % NK;
             ok = use < NK || rows_wait(&sh.kempty[slot], use / NK - 1);
             if (!ok) break;
-            fill(sm + slot * X::KST, full, &tmk, vt * 128, lead && v == 0, std::integral_constant<int, 2>());
+            fill(sm + slot * X::KST, full, &tmk, 2 * vt, lead && v == 0);
           }
           if (ok && !lead) {
             ok = i < NP || rows_wait(&sh.pslot[i % NP], i / NP - 1);
-            if (ok) fill(sm + X::P_OFF + (i % NP) * X::PST, full, &tmk, VT * 128, false, std::integral_constant<int, 1>());
+            if (ok) {                      // the position chunk (tmv: its rows may be narrower than a chunk)
+              uint8_t* dst = sm + X::P_OFF + (i % NP) * X::PST;
+              auto box = [&](int b) {
+                if ((valid >> b) & 1) tma_load_3d(dst + (b * 128 << a.bs_log2), &tmv, VT * 128, group * 8, ids[b], full, pol);
+              };
+              if (elected()) {
+                box(0);
+                if (nbt > 1) {
+                  box(1);
+                  if (nbt > 2) {
+                    box(2);
+                    box(3);
+                  }
+                }
+                mbar_arrive_expect_tx(full, rows_bytes * 128);
+              }
+              __syncwarp();
+            }
           }
         } else {
           const int depth = lead ? NK : NV, st = i % depth;
           ok = i < depth || rows_wait(lead ? &sh.kempty[st] : &sh.vempty[st], i / depth - 1);
           if (ok)
-            fill(sm + (lead ? st * X::KST : X::V_OFF + st * X::VST), lead ? &sh.kfull[st] : &sh.vfull[st], lead ? &tmk : &tmv, 0, lead,
-                 std::integral_constant<int, KC>());
+            fill(sm + (lead ? st * X::KST : X::V_OFF + st * X::VST), lead ? &sh.kfull[st] : &sh.vfull[st], lead ? &tmk : &tmv, 0, lead);
         }
         if (NQ == 1 && lead && j == 0 && ok) queries();
         if (j + 1 == count) {              // on to the next segment, with its block ids on the way meanwhile
@@ -563,7 +591,7 @@ __global__ void __launch_bounds__(384, 1)
   } else if (sh.any && warp == 1) {
     // ------------------------- first-product issuer -------------------------
     constexpr uint32_t IQK = umma_idesc_bf16(TT, R, 0, 0);
-    constexpr uint32_t HI = (uint32_t)(umma_desc_k(16, 1024) >> 32);
+    constexpr uint32_t HI = (uint32_t)(umma_desc_k(16, 1024) >> 32), HIK = (uint32_t)(umma_desc_k(16, X::GS) >> 32);
     const uint32_t sbase = (uint32_t)umma_desc_k(16, 1024) + (smem_u32(sm) >> 4);
     const uint32_t tm = __shfl_sync(FULL_MASK, tmem, 0);
     bool ok = true;
@@ -590,7 +618,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               if (ks < steps)
-                umma_bf16_lo(d, ka + ch * (X::CHUNK >> 4) + ks * 2, HI, qc + ch * (X::QCH >> 4) + ks * 2, HI, IQK, ch + ks ? 1u : first);
+                umma_bf16_lo(d, ka + ch * (1024 >> 4) + ks * 2, X::SHARED && NC == 1 ? HI : HIK, qc + ch * (X::QCH >> 4) + ks * 2, HI, IQK, ch + ks ? 1u : first);
         }
         __syncwarp();
       };
@@ -626,8 +654,9 @@ __global__ void __launch_bounds__(384, 1)
   } else if (sh.any && warp == 2) {
     // ------------------------- second-product issuer ------------------------
     constexpr uint32_t IPV = umma_idesc_bf16(X::VM, N2, 1, 1);
-    constexpr uint32_t HI = (uint32_t)(umma_desc_k(X::CHUNK, 1024) >> 32);
+    constexpr uint32_t HI = (uint32_t)(umma_desc_k(X::CHUNK, 1024) >> 32), HIV = (uint32_t)(umma_desc_k(1024, X::GS) >> 32);
     const uint32_t sbase = (uint32_t)umma_desc_k(X::CHUNK, 1024) + (smem_u32(sm) >> 4);
+    const uint32_t vbase = (uint32_t)umma_desc_k(1024, X::GS) + (smem_u32(sm) >> 4);
     const uint32_t tm = __shfl_sync(FULL_MASK, tmem, 0);
     bool ok = true;
 #pragma unroll 1
@@ -650,11 +679,11 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 1
       for (int vt = 0; vt < VT; ++vt) {
         const int slot = X::SHARED ? (k0 + vt) % NK : i % NV;
-        const uint32_t vb = sbase + ((X::SHARED ? slot * X::KST : X::V_OFF + slot * X::VST) >> 4);
+        const uint32_t vb = vbase + ((X::SHARED ? slot * X::KST : X::V_OFF + slot * X::VST) >> 4);
         if (elected()) {
 #pragma unroll
           for (int kk = 0; kk < TT / 16; ++kk)
-            if (kk < nks) umma_bf16_lo(d + vt * N2, vb + kk * 128, HI, pa + kk * 128, HI, IPV, kk ? 1u : acc0);
+            if (kk < nks) umma_bf16_lo(d + vt * N2, vb + kk * (2 * X::GS >> 4), HIV, pa + kk * 128, HI, IPV, kk ? 1u : acc0);
           umma_commit(X::SHARED ? &sh.kempty[slot] : &sh.vempty[slot]);
         }
         __syncwarp();
@@ -811,9 +840,8 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 1
             for (int v = lane; v < X::VC * 8; v += 32) {
               const int ch = v >> 3;
-              uint8_t* base = X::SHARED ? sm + ((k0 + (ch >> 1)) % NK) * X::KST + (ch & 1) * X::CHUNK
-                                        : sm + X::V_OFF + (i % NV) * X::VST + ch * X::CHUNK;
-              *reinterpret_cast<uint4*>(base + row * 128 + (v & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+              uint8_t* base = X::SHARED ? sm + ((k0 + (ch >> 1)) % NK) * X::KST + (ch & 1) * 1024 : sm + X::V_OFF + (i % NV) * X::VST + ch * 1024;
+              *reinterpret_cast<uint4*>(base + (row >> 3) * X::GS + (row & 7) * 128 + (v & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
           }
         }
@@ -1358,12 +1386,12 @@ static pkv_status rows_attn(const RowsShape& s, RowsVariant* v, bool latent, con
 
   CUtensorMap tmk, tmv, tmq;
   const uint64_t row = (uint64_t)w * 2, rows = (uint64_t)n_kv * block_size, nblk = num_blocks > 0 ? (uint64_t)num_blocks : 1;
-  int bad = encode_tensor_map_3d(&tmk, k, w, rows, nblk, row, rows * row, 64, block_size);
+  int bad = encode_tensor_map_chunks(&tmk, k, v->DV / 64, rows, nblk, row, latent ? 2 : v->DV / 64, block_size);
   if (latent) {
-    tmv = tmk;
+    bad |= encode_tensor_map_3d(&tmv, k, w, rows, nblk, row, rows * row, 64, block_size);   // for the position chunk
     bad |= encode_tensor_map_3d(&tmq, q, w, (uint64_t)n_tok * n_h, 1, row, row, 64, s.R);
   } else {
-    bad |= encode_tensor_map_3d(&tmv, vp, w, rows, nblk, row, rows * row, 64, block_size);
+    bad |= encode_tensor_map_chunks(&tmv, vp, v->DV / 64, rows, nblk, row, v->DV / 64, block_size);
     bad |= encode_tensor_map_3d(&tmq, q, w, n_h, n_tok, row, n_h * row, 64, a.gt, a.tpt);
   }
   if (bad) return PKV_ECUDA;
