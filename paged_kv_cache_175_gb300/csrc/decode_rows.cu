@@ -828,21 +828,15 @@ __global__ void __launch_bounds__(384, 1)
         }
         tmem_wait_st();
         // V rows that no query row attends to, and that the product reads with p = 0: they may hold anything
-        const int topr = (min(TT, mt.ctx - mt.tile0) + 15) & ~15;
+        const int topr = (min(TT, mt.ctx - mt.tile0) + 15) & ~15, row = PP ? tid : tid >> 2;
+        unsigned long long seen = scr.seen[row >> 6][0];
+        if constexpr (R > 32) seen |= scr.seen[row >> 6][1];
+        if (row < topr && !((seen >> (row & 63)) & 1)) {
 #pragma unroll 1
-        for (int w = 0; w < MT; ++w) {
-          unsigned long long rows = ~scr.seen[w][0] & ones_below(topr - 64 * w);
-          if constexpr (R > 32) rows &= ~scr.seen[w][1];
-#pragma unroll 1
-          for (; rows; rows &= rows - 1) {
-            const int row = 64 * w + __ffsll(rows) - 1;
-            if (row % (NW / 32) != tid >> 5) continue;
-#pragma unroll 1
-            for (int v = lane; v < X::VC * 8; v += 32) {
-              const int ch = v >> 3;
-              uint8_t* base = X::SHARED ? sm + ((k0 + (ch >> 1)) % NK) * X::KST + (ch & 1) * 1024 : sm + X::V_OFF + (i % NV) * X::VST + ch * 1024;
-              *reinterpret_cast<uint4*>(base + (row >> 3) * X::GS + (row & 7) * 128 + (v & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
+          for (int v = PP ? 0 : tid & 3; v < X::VC * 8; v += PP ? 1 : 4) {
+            const int ch = v >> 3;
+            uint8_t* base = X::SHARED ? sm + ((k0 + (ch >> 1)) % NK) * X::KST + (ch & 1) * 1024 : sm + X::V_OFF + (i % NV) * X::VST + ch * 1024;
+            *reinterpret_cast<uint4*>(base + (row >> 3) * X::GS + (row & 7) * 128 + (v & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         __syncwarp();
@@ -1073,13 +1067,21 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(t[HL - 1][e]) * sh.factor[ob][cc + e];
           }
+          if (X::VM == 64 && lane >= 16) continue;
+          if (!whole) {                    // (rows that no query has are written too)
+            float* dst = a.ws_o + ((size_t)part * R + cc) * DV + chn;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int row = sh.row[ob][cc + e];
-            if (row < 0 || (X::VM == 64 && lane >= 16)) continue;
-            if (!whole) a.ws_o[((size_t)part * R + cc + e) * DV + chn] = v[e];
-            else if constexpr (X::F32) reinterpret_cast<float*>(a.out)[(size_t)row * DV + chn] = v[e];
-            else reinterpret_cast<__nv_bfloat16*>(a.out)[(size_t)row * DV + chn] = __float2bfloat16_rn(v[e]);
+            for (int e = 0; e < 8; ++e) dst[e * DV] = v[e];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int row = sh.row[ob][cc + e];
+              if constexpr (X::F32) {
+                if (row >= 0) reinterpret_cast<float*>(a.out)[(size_t)row * DV + chn] = v[e];
+              } else {
+                if (row >= 0) reinterpret_cast<__nv_bfloat16*>(a.out)[(size_t)row * DV + chn] = __float2bfloat16_rn(v[e]);
+              }
+            }
           }
         }
         tc_fence_before();
