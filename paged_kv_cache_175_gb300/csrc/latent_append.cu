@@ -4,11 +4,14 @@
 // Mathematics: y = x w / sqrt(mean(x^2) + eps) in fp32 with one rounding; the rotation and its angles as in
 // rope_append.cu (the position times a 64-bit fraction of a turn, exact for every int32 position).
 //
-// What bounds it: every element is read once and written once: HBM for long calls, the launch and two
-// dependent memory round trips (position and slot beside the rows, then the stores) for short ones.
+// What bounds it: every element is read once and written once: HBM for long calls (16001 tokens of 16 heads, 102 MB:
+// 21.4 us, 4.8 TB/s; 4001 of 128 heads, 140 MB: 23.8 us, 5.9 TB/s), the launch and two dependent memory round trips
+// (position and slot beside the rows, then the stores) for short ones (64 tokens of 128 heads: 2.5 us).
 // Split: a warp per (token, part).  Part 0 is the token's vector: 16 or 8 channels of the latent part
 // per lane, whose squares meet in five shuffles, and the key part.  The other parts are runs of
-// 32 * NI items of the token's query heads, an item being two 16-byte vectors (eight channel pairs).
+// 32 * NI items of the token's query heads, an item being two 16-byte vectors (eight channel pairs): one item per lane
+// while that does not fill the GPU, more where it does, so that a warp's fixed work (position, angles) goes round more
+// bytes (16 heads: 26.9 us with one item, 21.4 with two; 128 heads: 25.1 with two, 23.8 with four).
 // A lane computes the angle of pair `lane`; the eight that an item needs come by shuffles, and are the same
 // for all of a lane's items.  All loads are issued before the first use.
 #include <cmath>
@@ -199,13 +202,13 @@ extern "C" pkv_status pkv_latent_append(const void* kv, int64_t kv_stride, const
   a.t = *table;
   const int items = n_h * (rope / 16), sms = device_sm_count() > 0 ? device_sm_count() : 128;
   const bool wide = (long long)n_tok * items >= (long long)sms * 32 * 64;
-  const int ni = wide ? 4 : 1;
+  const int ni = !wide ? 1 : (items <= 64 ? 2 : 4);
   a.parts = 1 + (items + 32 * ni - 1) / (32 * ni);
   const long long grid = ((long long)n_tok * a.parts + kLatentThreads / 32 - 1) / (kLatentThreads / 32);
   if (grid > 0x7fffffffLL) return PKV_ERANGE;
   void* kargs[] = {&a};
-  const cudaError_t e = launch_pdl(wide ? latent_append_fn<4>(latent, rope) : latent_append_fn<1>(latent, rope), dim3((unsigned)grid),
-                                   dim3(kLatentThreads), 0, static_cast<cudaStream_t>(stream), kargs);
+  const void* fn = ni == 1 ? latent_append_fn<1>(latent, rope) : (ni == 2 ? latent_append_fn<2>(latent, rope) : latent_append_fn<4>(latent, rope));
+  const cudaError_t e = launch_pdl(fn, dim3((unsigned)grid), dim3(kLatentThreads), 0, static_cast<cudaStream_t>(stream), kargs);
   if (e != cudaSuccess) {
     record_cuda_error(e);
     return PKV_ECUDA;

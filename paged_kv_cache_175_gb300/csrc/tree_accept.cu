@@ -2,11 +2,13 @@
 // of a call (every layer's pools) at once.
 //
 // A thread owns one 16-byte column of a sequence's drafted rows in one cache and head and moves the path's
-// rows in ascending order, eight loads ahead of eight stores.  path[i] >= i, so a row is written only
+// rows in ascending order, four loads ahead of four stores.  path[i] >= i, so a row is written only
 // once it has been read: the rows still to be read come after path[i], and the thread's column is
 // nobody else's.  Rows that stay where they are are not touched.
 // What bounds it: four dependent memory round trips (lengths and path, block ids, rows, stores); one launch for
-// all layers where a launch per layer would cost that much each.
+// all layers where a launch per layer would cost that much each.  64 sequences, 8 layers of K and V of 8 x 128: 5.6 us;
+// 4 sequences, 40 latent caches: 6.7 us.  Eight loads ahead and CTAs of 256 threads took 7.1 and 7.6: twice the registers,
+// and CTAs in two waves.
 #include "drafts.cuh"
 #include "nvtx_range.h"
 
@@ -22,19 +24,26 @@ struct AcceptArgs {
   uint4* caches[kAcceptCaches];
 };
 
-constexpr int kAcceptBatch = 8;
+constexpr int kAcceptBatch = 4, kAcceptThreads = 128;
 
-__global__ void __launch_bounds__(256) tree_accept_kernel(const __grid_constant__ AcceptArgs a) {
+__global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __grid_constant__ AcceptArgs a) {
   grid_dep_wait();
   grid_dep_launch();
-  const long long col = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long col = (long long)blockIdx.x * kAcceptThreads + threadIdx.x;
   if (col >= a.columns) return;
   const int v = (int)(col % a.vecs), h = (int)(col / a.vecs % a.heads), s = (int)(col / ((long long)a.vecs * a.heads));
   const bool speaks = blockIdx.y == 0 && v == 0 && h == 0;    // one thread per sequence flags and writes its length
   int flags = 0;
+  // the path's first rows are asked for with the lengths: how many of them count is known behind both
+  int at[kAcceptBatch];
+  auto ask = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < kAcceptBatch; ++i) at[i] = i0 + i < a.path_stride ? a.path[(size_t)s * a.path_stride + i0 + i] : -1;
+  };
+  ask(0);
+  int count = a.n_accept[s];
   const Drafts d = drafts_of(a.ctx, a.q_start, a.n_each, a.n_tok, a.max_ctx, s, flags);
   const int base = d.ctx - d.n, most = min(d.n, a.path_stride);
-  int count = a.n_accept[s];
   if (count < 0 || count > most) {
     if (d.ctx > 0) flags |= PKV_DEV_BAD_TREE;
     count = count < 0 ? 0 : most;
@@ -42,40 +51,40 @@ __global__ void __launch_bounds__(256) tree_accept_kernel(const __grid_constant_
   if (base < 0) count = 0;
   uint4* cache = a.caches[blockIdx.y];
   const int32_t* bt = a.bt + (size_t)s * a.max_blocks;
-  auto place = [&](int t) -> long long {                      // of row t's column in the cache, in vectors
-    const int b = bt[t >> a.bs_log2];
-    if ((unsigned)b >= (unsigned)a.num_blocks) {
-      set_err(a.err, PKV_DEV_BAD_BLOCK);
-      return -1;
-    }
-    return (((((long long)b * a.heads + h) << a.bs_log2) + (t & ((1 << a.bs_log2) - 1)))) * a.vecs + v;
-  };
+  const int in = (1 << a.bs_log2) - 1;
   int last = -1, done = 0;
   bool good = true;
   for (int i0 = 0; i0 < count && good; i0 += kAcceptBatch) {
-    long long src[kAcceptBatch], dst[kAcceptBatch];
+    long long src[kAcceptBatch], dst[kAcceptBatch];            // block ids, then columns of rows in the cache, in vectors
     uint4 x[kAcceptBatch];
-    int at[kAcceptBatch];
-#pragma unroll
-    for (int i = 0; i < kAcceptBatch; ++i) at[i] = i0 + i < count ? a.path[(size_t)s * a.path_stride + i0 + i] : -1;
+    if (i0) ask(i0);
 #pragma unroll
     for (int i = 0; i < kAcceptBatch; ++i) {
-      src[i] = dst[i] = -1;
+      src[i] = dst[i] = -1;                                   // nothing to do
       if (i0 + i >= count || !good) continue;
       good = at[i] > last && at[i] < d.n;
       if (!good) continue;
       last = at[i];
       ++done;
       if (at[i] == i0 + i) continue;
-      src[i] = place(base + at[i]);
-      dst[i] = place(base + i0 + i);
+      src[i] = (unsigned)bt[(base + at[i]) >> a.bs_log2];
+      dst[i] = (unsigned)bt[(base + i0 + i) >> a.bs_log2];
     }
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kAcceptBatch; ++i) {
+      const bool both = src[i] >= 0 && src[i] < a.num_blocks && dst[i] < a.num_blocks;
+      bad |= src[i] >= 0 && !both;
+      src[i] = both ? ((((src[i] * a.heads + h) << a.bs_log2) + ((base + at[i]) & in))) * a.vecs + v : -1;
+      dst[i] = ((((dst[i] * a.heads + h) << a.bs_log2) + ((base + i0 + i) & in))) * a.vecs + v;
+    }
+    if (bad) set_err(a.err, PKV_DEV_BAD_BLOCK);
 #pragma unroll
     for (int i = 0; i < kAcceptBatch; ++i)
-      if (src[i] >= 0 && dst[i] >= 0) x[i] = cache[src[i]];
+      if (src[i] >= 0) x[i] = cache[src[i]];
 #pragma unroll
     for (int i = 0; i < kAcceptBatch; ++i)
-      if (src[i] >= 0 && dst[i] >= 0) cache[dst[i]] = x[i];
+      if (src[i] >= 0) cache[dst[i]] = x[i];
   }
   if (!speaks || !a.write_lens) return;
   if (!good) flags |= PKV_DEV_BAD_TREE;
@@ -124,14 +133,14 @@ extern "C" pkv_status pkv_kv_tree_accept(void* const* caches, int n_caches, int 
   a.num_blocks = num_blocks;
   a.err = err_flag;
   a.columns = (long long)batch * heads * a.vecs;
-  const long long grid = (a.columns + 255) / 256;
+  const long long grid = (a.columns + kAcceptThreads - 1) / kAcceptThreads;
   if (grid > 0x7fffffffLL) return PKV_ERANGE;
   for (int c0 = 0; c0 < n_caches; c0 += kAcceptCaches) {
     const int n = n_caches - c0 < kAcceptCaches ? n_caches - c0 : kAcceptCaches;
     for (int i = 0; i < n; ++i) a.caches[i] = static_cast<uint4*>(caches[c0 + i]);
     a.write_lens = c0 == 0;
     void* kargs[] = {&a};
-    const cudaError_t e = launch_pdl((const void*)tree_accept_kernel, dim3((unsigned)grid, n), dim3(256), 0,
+    const cudaError_t e = launch_pdl((const void*)tree_accept_kernel, dim3((unsigned)grid, n), dim3(kAcceptThreads), 0,
                                      static_cast<cudaStream_t>(stream), kargs);
     if (e != cudaSuccess) {
       record_cuda_error(e);
