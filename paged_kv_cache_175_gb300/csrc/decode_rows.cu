@@ -1130,117 +1130,143 @@ __global__ void __launch_bounds__(384, 1)
 }
 
 // ---- parts of cut segments ----------------------------------------------------------------------------
-// Joins the parts of a segment that piece boundaries cut, by its first boundary.  Narrow: a warp per query row, all of its
-// channels.  Wide, for few long segments, of which each has many parts: a CTA per query row, whose warps take every eighth
-// part and meet in shared memory.
+// Joins the parts of a segment that piece boundaries cut, by its first boundary.  Narrow: a warp per query row and boundary,
+// all of its channels.  Wide, for few segments of many parts each: a CTA per query row, whose warps take every eighth
+// part and meet in shared memory; there a CTA looks its boundary up among all of them, since most cut nothing anew
+// and a CTA for each of those, too, cost a short call 2 to 4 us.
 template <class X, bool WIDE>
 __global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ RowsArgs a) {
   constexpr int R = X::R, DV = X::DV, V = DV < 128 ? 2 : 4, CH = DV / (32 * V);   // channels lane V + 32 V j + ...
   grid_dep_wait();
   grid_dep_launch();
-  const int team = blockIdx.x / a.C, member = blockIdx.x % a.C, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const RowsCut cut = a.cuts[team];
-  if (cut.parts == 0) return;
-  const int c = WIDE ? blockIdx.y : blockIdx.y * 8 + warp;
-  int t0, h0;
-  tile_of<X>(a, cut.rg * a.C + member, t0, h0);
-  const int2 qh = query_of<X>(a, cut.n, t0, h0, c);
-  if (qh.x < 0) return;
-  const long long row = (long long)(cut.q0 + qh.x) * a.n_h + cut.g * a.G + qh.y;
-  float M = -INFINITY, L = 0.f, acc[CH][V];
-#pragma unroll
-  for (int j = 0; j < CH; ++j)
-#pragma unroll
-    for (int v = 0; v < V; ++v) acc[j][v] = 0.f;
-  constexpr int AT = DV > 256 ? 2 : 4;     // parts at a time, with all their loads ahead of the first use
+  const int member = blockIdx.x % a.C, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ unsigned some[8];
+  if constexpr (WIDE) {                    // boundaries with something to join (of at most 256)
+    const unsigned mine = __ballot_sync(FULL_MASK, threadIdx.x < a.P && a.cuts[threadIdx.x].parts != 0);
+    if (lane == 0) some[warp] = mine;
+  }
 #pragma unroll 1
-  for (int p0 = WIDE ? warp * AT : 0; p0 < cut.parts; p0 += WIDE ? 8 * AT : AT) {
-    float2 ml[AT];
-    float o[AT][CH][V];
+  for (int turn = blockIdx.x / a.C;; turn += gridDim.x / a.C) {
+    int team = turn;
+    if constexpr (WIDE) {
+      __syncthreads();
+      int left = turn;
+      team = -1;
 #pragma unroll
-    for (int i = 0; i < AT; ++i) {
-      const int p = min(p0 + i, cut.parts - 1);
-      const size_t at = (size_t)(((team - 1 + p) * a.C + member) * 2 + (p == 0 ? cut.first : 0)) * R + c;
-      ml[i] = *reinterpret_cast<const float2*>(a.ws_ml + 2 * at);
-      if (p0 + i >= cut.parts) ml[i] = make_float2(-INFINITY, 0.f);
+      for (int w = 0; w < 8; ++w) {
+        const int n = __popc(some[w]);
+        if (team < 0 && left < n) team = 32 * w + __fns(some[w], 0, left + 1);
+        left -= n;
+      }
+      if (team < 0) return;
+    }
+    const RowsCut cut = a.cuts[team];
+    if (cut.parts == 0) return;
+    const int c = WIDE ? blockIdx.y : blockIdx.y * 8 + warp;
+    int t0, h0;
+    tile_of<X>(a, cut.rg * a.C + member, t0, h0);
+    const int2 qh = query_of<X>(a, cut.n, t0, h0, c);
+    if (qh.x < 0) {                          // (of the whole CTA, where it is wide)
+      if (WIDE) continue;
+      return;
+    }
+    const long long row = (long long)(cut.q0 + qh.x) * a.n_h + cut.g * a.G + qh.y;
+    float M = -INFINITY, L = 0.f, acc[CH][V];
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[j][v] = 0.f;
+    constexpr int AT = DV > 256 ? 2 : 4;     // parts at a time, with all their loads ahead of the first use
+#pragma unroll 1
+    for (int p0 = WIDE ? warp * AT : 0; p0 < cut.parts; p0 += WIDE ? 8 * AT : AT) {
+      float2 ml[AT];
+      float o[AT][CH][V];
+#pragma unroll
+      for (int i = 0; i < AT; ++i) {
+        const int p = min(p0 + i, cut.parts - 1);
+        const size_t at = (size_t)(((team - 1 + p) * a.C + member) * 2 + (p == 0 ? cut.first : 0)) * R + c;
+        ml[i] = *reinterpret_cast<const float2*>(a.ws_ml + 2 * at);
+        if (p0 + i >= cut.parts) ml[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+          const float* src = a.ws_o + at * DV + lane * V + 32 * V * j;
+          if constexpr (V == 4) *reinterpret_cast<float4*>(o[i][j]) = *reinterpret_cast<const float4*>(src);
+          else *reinterpret_cast<float2*>(o[i][j]) = *reinterpret_cast<const float2*>(src);
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int i = 0; i < AT; ++i) top = fmaxf(top, ml[i].x);
+      const float base = top == -INFINITY ? 0.f : top, keep = ex2(M - base);
+      L *= keep;
+      float w[AT];
+#pragma unroll
+      for (int i = 0; i < AT; ++i) {
+        w[i] = ml[i].x == -INFINITY ? 0.f : ex2(ml[i].x - base);
+        L += w[i] * ml[i].y;
+      }
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          acc[j][v] *= keep;
+#pragma unroll
+          for (int i = 0; i < AT; ++i) acc[j][v] += w[i] * o[i][j][v];
+        }
+      M = top;
+    }
+    auto store = [&](int ch, const float* x) {
+      const size_t at = (size_t)row * DV + ch;
+      if constexpr (X::F32) {
+        if constexpr (V == 4) *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = make_float4(x[0], x[1], x[2], x[3]);
+        else *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + at) = make_float2(x[0], x[1]);
+      } else {
+        uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at);
+        if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+        else *dst = pack_bf16(x[0], x[1]);
+      }
+    };
+    if constexpr (WIDE) {
+      __shared__ float2 s_ml[8];
+      __shared__ __align__(16) float s_o[8][DV];
+      if (lane == 0) s_ml[warp] = make_float2(M, L);
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) s_o[warp][lane * V + 32 * V * j + v] = acc[j][v];
+      __syncthreads();
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, s_ml[i].x);
+      if (top == -INFINITY) top = 0.f;
+      float sum = 0.f, f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        f[i] = ex2(s_ml[i].x - top);
+        sum += f[i] * s_ml[i].y;
+      }
+      const float inv = sum_inverse(sum);
+      for (int ch = threadIdx.x * V; ch < DV; ch += 256 * V) {
+        float x[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          x[v] = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[v] += f[i] * s_o[i][ch + v];
+          x[v] *= inv;
+        }
+        store(ch, x);
+      }
+    } else {
+      const float inv = sum_inverse(L);
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
-        const float* src = a.ws_o + at * DV + lane * V + 32 * V * j;
-        if constexpr (V == 4) *reinterpret_cast<float4*>(o[i][j]) = *reinterpret_cast<const float4*>(src);
-        else *reinterpret_cast<float2*>(o[i][j]) = *reinterpret_cast<const float2*>(src);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[j][v] *= inv;
+        store(lane * V + 32 * V * j, acc[j]);
       }
     }
-    float top = M;
-#pragma unroll
-    for (int i = 0; i < AT; ++i) top = fmaxf(top, ml[i].x);
-    const float base = top == -INFINITY ? 0.f : top, keep = ex2(M - base);
-    L *= keep;
-    float w[AT];
-#pragma unroll
-    for (int i = 0; i < AT; ++i) {
-      w[i] = ml[i].x == -INFINITY ? 0.f : ex2(ml[i].x - base);
-      L += w[i] * ml[i].y;
-    }
-#pragma unroll
-    for (int j = 0; j < CH; ++j)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        acc[j][v] *= keep;
-#pragma unroll
-        for (int i = 0; i < AT; ++i) acc[j][v] += w[i] * o[i][j][v];
-      }
-    M = top;
-  }
-  auto store = [&](int ch, const float* x) {
-    const size_t at = (size_t)row * DV + ch;
-    if constexpr (X::F32) {
-      if constexpr (V == 4) *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = make_float4(x[0], x[1], x[2], x[3]);
-      else *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + at) = make_float2(x[0], x[1]);
-    } else {
-      uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at);
-      if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-      else *dst = pack_bf16(x[0], x[1]);
-    }
-  };
-  if constexpr (WIDE) {
-    __shared__ float2 s_ml[8];
-    __shared__ __align__(16) float s_o[8][DV];
-    if (lane == 0) s_ml[warp] = make_float2(M, L);
-#pragma unroll
-    for (int j = 0; j < CH; ++j)
-#pragma unroll
-      for (int v = 0; v < V; ++v) s_o[warp][lane * V + 32 * V * j + v] = acc[j][v];
-    __syncthreads();
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, s_ml[i].x);
-    if (top == -INFINITY) top = 0.f;
-    float sum = 0.f, f[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      f[i] = ex2(s_ml[i].x - top);
-      sum += f[i] * s_ml[i].y;
-    }
-    const float inv = sum_inverse(sum);
-    for (int ch = threadIdx.x * V; ch < DV; ch += 256 * V) {
-      float x[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        x[v] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[v] += f[i] * s_o[i][ch + v];
-        x[v] *= inv;
-      }
-      store(ch, x);
-    }
-  } else {
-    const float inv = sum_inverse(L);
-#pragma unroll
-    for (int j = 0; j < CH; ++j) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[j][v] *= inv;
-      store(lane * V + 32 * V * j, acc[j]);
-    }
+    if (!WIDE) return;
   }
 }
 
@@ -1256,7 +1282,8 @@ template <class X>
 static RowsVariant make_variant() {
   constexpr size_t smem = X::M_OFF + sizeof(RowsShared<X>);
   static_assert(smem <= 232448, "shared memory of one CTA");
-  static_assert(X::Q_OFF % 1024 == 0 && X::P_OFF % 1024 == 0 && X::NCOL <= 512, "descriptor alignment, tensor memory");
+  static_assert(sizeof(RowsScratch<X>) <= (X::SHARED ? X::M_OFF - X::W_OFF : X::KPART - X::PBUF), "scratch of a tile");
+  static_assert(X::Q_OFF % 1024 == 0 && X::V_OFF % 1024 == 0 && X::P_OFF % 1024 == 0 && X::NCOL <= 512, "descriptor alignment, tensor memory");
   return {(const void*)decode_rows_kernel<X>, {(const void*)rows_join_kernel<X, false>, (const void*)rows_join_kernel<X, true>}, smem, X::R, X::DV, {}};
 }
 // bf16 outputs take p in two bf16 parts (16 bits) up to 32 query rows and in one with 64, fp32 outputs in three (all 24
@@ -1293,7 +1320,7 @@ static RowsShape rows_shape(int n_tok, int batch, int G, bool f32) {
   RowsShape s;
   s.R = rows <= 16 && G <= 16 ? 16 : (rows <= 32 || f32 ? 32 : 64);
   const long long tiles = (rows + s.R - 1) / s.R;
-  s.C = tiles <= 1 ? 1 : (tiles <= 2 ? 2 : 4);
+  s.C = tiles <= 1 ? 1 : 2;
   const int sms = device_sm_count();
   s.P = sms / s.C;
   s.groups = (tiles + s.C - 1) / s.C;
@@ -1401,11 +1428,12 @@ static pkv_status rows_attn(const RowsShape& s, RowsVariant* v, bool latent, con
   void* kargs[] = {&tmk, &tmv, &tmq, &a};
   cudaError_t e = launch_pdl(v->fn, dim3(s.P * s.C), dim3(384), v->smem, st, kargs);
   if (e == cudaSuccess) {
-    // the pieces over the segments: about the parts that each has
-    const long long segments = (long long)batch * n_kv * s.groups;
-    const bool wide = s.P >= 8 * segments;
+    // The pieces over the segments: about the parts that each has, if it has so many tiles.  16 heads over 64K latent tokens:
+    // 64 us by a warp per query row, 31 by a CTA; 64 sequences of 16 heads: 41 and 43.
+    const long long segments = (long long)batch * n_kv * s.groups, tiles = a.max_ctx / (latent ? 64 : 128);
+    const bool wide = s.P >= 8 * segments && tiles >= 8 && s.P <= 256;
     void* jargs[] = {&a};
-    e = launch_pdl(v->join[wide], dim3(s.P * s.C, wide ? s.R : s.R / 8), dim3(256), 0, st, jargs);
+    e = launch_pdl(v->join[wide], dim3((wide ? (int)segments : s.P) * s.C, wide ? s.R : s.R / 8), dim3(256), 0, st, jargs);
   }
   if (e == cudaSuccess) return PKV_OK;
   record_cuda_error(e);
