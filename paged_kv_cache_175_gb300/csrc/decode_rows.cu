@@ -5,8 +5,9 @@
 // cached rows on the M side of the tensor core and query rows on its N side: with 16 to 64 query rows N is
 // what may be small, and M = 128 (64) cached rows or channels fills the tensor core's lanes.
 //   S^T[rows of the tile][R]   = K Q^T                 (both K-major, as they lie in memory)
-//   O^T[channels][R or 2 R]   += V^T [P_hi | P_lo]^T   (both MN-major, as they lie in shared memory)
-// K and V of a latent cache are the same rows, which are loaded once: V is the first channels of the K stage.
+//   O^T[channels][HL R]       += V^T [P_1 | P_2 ..]^T  (both MN-major, as they lie in shared memory)
+// K and V of a latent cache are the same rows, which are loaded once: V is the first channels of the K slots.  P is
+// taken as HL bf16 parts, which are columns of one product and are added in the epilogue.
 //
 // Work partition: the line of all (sequence, kv head, group of row tiles, tile of cached rows), in that order, is
 // cut into equal pieces, one for each team of C CTAs; the members of a team take C row tiles of
@@ -15,11 +16,23 @@
 // second kernel joins; a piece holds at most two cut segments, its first and its last.
 //
 // A CTA of 12 warps runs these roles, joined by mbarriers with bounded waits:
-//   warp 0      K (or latent) tiles into a ring of stages by TMA, and each segment's query rows
-//   warp 3      V tiles, in a ring of their own
-//   warp 1      owner of the tensor memory; one thread issues the first product into one of two S buffers
-//   warp 2      one thread issues the second product
-//   warps 4-11  softmax and epilogue, in two groups of four warps that take half of the R query rows each
+//   warps 0, 3  producers: keys and query rows, and values (latent cache: a half of a tile's chunks each), by TMA
+//   warp 1      owner of the tensor memory; issues the first product into one of the S buffers
+//   warp 2      issues the second product
+//   warps 4-11  softmax and epilogue, in two groups of four warps.  K and V pools: the groups take alternate tiles, each
+//               with an O accumulator of its own; latent cache: both take every tile, half of the query rows each
+//
+// What bounds it (GPU time; R query rows per CTA):
+//   64 trees of up to 16 tokens over 0.5-4K rows, 8 kv heads of 4 x 128 (620 MB): 124 us, 5.0 TB/s: HBM, and about 10000 clocks
+//     per segment for its masked tile and its epilogue.  The same of up to 8 tokens: 108 us.
+//   8 trees of up to 64 over 8-32K, 8 x 8 heads (512 rows, 207 TFLOP): 380 us, 544 TFLOP/s: shared memory.  A tile of 128 rows
+//     writes 64 KB there and its products read 96, about 1600 of the 1750 clocks that it takes.  128 rows per CTA,
+//     which would read less, took 489: they leave two S buffers and three key stages.
+//   64 x 0.5-4K latent tokens of 16 heads (173 MB): 41 us, 4.2 TB/s: HBM for 25 of them, then setup, first loads and the join.
+//   32 x 2-16K latent tokens of 128 heads (82 TFLOP): 126 us, 645 TFLOP/s: shared memory again, 72 KB written and 245
+//     read per tile of 64 rows.
+//   One tree of 8 over 333 rows: 10.9 us; one latent token of 16 heads over 301: 12.5: setup 1.4 us, loads 2, masks and softmax 2,
+//     epilogue 1, the join 2, and code that is run once and cold.
 #include <cmath>
 #include <mutex>
 #include <type_traits>
@@ -1310,7 +1323,12 @@ static RowsVariant* latent_variant(int latent, int R, bool f32) {
   return &v[latent == 512][variant_index(R, f32)];
 }
 
-// Query rows of a row tile, and members of a team, from the average of the sequences' query rows per kv head.
+// Query rows of a row tile, and members of a team, from the average of the sequences' query rows per kv head.  Rows that no
+// query has cost products and softmax all the same, row tiles loads: 64 trees of 16 rows took 103 us with R = 16 and 110
+// with 32, of 32 rows 109 with 32 and 124 with 64, of 64 rows 125 with 64 and 167 with 32; 64 latent tokens of 16 heads
+// 41, 43 and 50 with 16, 32 and 64.  Two members read what one CTA loads twice (32 latent tokens of 128 heads 126 us and
+// 136, 8 trees of 512 rows 382 and 418), but where the sequences' rows differ one of them may have no tile (12 trees over the latent
+// cache 53 and 51; with four members 61, and 397 for the 8 trees).
 struct RowsShape {
   int R, C, P;
   long long groups;              // of row tiles, on average
