@@ -25,11 +25,12 @@
 // What bounds it (GPU time; R query rows per CTA):
 //   64 trees of up to 16 tokens over 0.5-4K rows, 8 kv heads of 4 x 128 (620 MB): 124 us, 5.0 TB/s: HBM, and about 10000 clocks
 //     per segment for its masked tile and its epilogue.  The same of up to 8 tokens: 108 us.
-//   8 trees of up to 64 over 8-32K, 8 x 8 heads (512 rows, 207 TFLOP): 380 us, 544 TFLOP/s: shared memory.  A tile of 128 rows
-//     writes 64 KB there and its products read 96, about 1600 of the 1750 clocks that it takes.  128 rows per CTA,
-//     which would read less, took 489: they leave two S buffers and three key stages.
+//   8 trees of up to 64 over 8-32K, 8 x 8 heads (512 rows, 207 GFLOP): 380 us, 544 TFLOP/s: shared memory and HBM.  A tile of 128
+//     rows writes 64 KB to shared memory and its products read 96, about 1600 of the 1750 clocks that it takes; HBM is 72% busy, since
+//     the caches are read 3.2 times over.  128 rows per CTA, which would read less, took 489: they leave two S buffers and three
+//     key stages.  Teams of four read half and took 397: their members lack a row tile more often.
 //   64 x 0.5-4K latent tokens of 16 heads (173 MB): 41 us, 4.2 TB/s: HBM for 25 of them, then setup, first loads and the join.
-//   32 x 2-16K latent tokens of 128 heads (82 TFLOP): 126 us, 645 TFLOP/s: shared memory again, 72 KB written and 245
+//   32 x 2-16K latent tokens of 128 heads (82 GFLOP): 126 us, 645 TFLOP/s: shared memory again, 72 KB written and 245
 //     read per tile of 64 rows.
 //   One tree of 8 over 333 rows: 10.9 us; one latent token of 16 heads over 301: 12.5: setup 1.4 us, loads 2, masks and softmax 2,
 //     epilogue 1, the join 2, and code that is run once and cold.
