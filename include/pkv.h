@@ -503,7 +503,8 @@ pkv_status pkv_kv_evict(void* k_pool, void* v_pool, const int32_t* block_tables,
  * than 32 query rows per kv head and sequence on average (n_tok * n_h / (batch * n_kv)), in one (2^-8 sum p |v|, of the size of
  * the output's own rounding; the sum that divides it is then that of the rounded values).  Cached rows that no token of the sequence attends to do not
  * reach any output, whatever they hold; a row that some of its tokens attend to and others mask has to
- * hold finite values (0 times an infinity of V is no number).  Pools, tables, lengths, scale, other
+ * hold finite values (0 times an infinity of V is no number).  Weights are held as exp(score - c) with a c that may lie
+ * 2^32 in weight below the largest until the end, so values of V beyond 2^90 may overflow.  Pools, tables, lengths, scale, other
  * errors and the first call of a shape as for pkv_paged_decode_attn; max_blocks * block_size is at most
  * 0x7fff0000 and n_tok * n_h at most 0x7fffffff (PKV_ERANGE).
  */
@@ -521,7 +522,7 @@ pkv_status pkv_paged_tree_attn(const void* q, const void* k_pool, const void* v_
  * depth in the tree, which is where an accepted path puts them.)
  *   caches        HOST array of n_caches device pointers to caches of one shape,
  *                 [num_blocks][heads][block_size][row_bytes]: the K and V pools of every layer, or the latent
- *                 caches (heads = 1).  They must not overlap.  row_bytes is a multiple of 16
+ *                 caches (heads = 1).  They must not overlap (PKV_EINVAL).  row_bytes is a multiple of 16
  *   q_start, n_tok, batch as above
  *   path          int32 [batch][path_stride]: drafted tokens in ascending order (a tree lists parents before
  *                 children), at least n_accept[s] of them
@@ -552,7 +553,8 @@ pkv_status pkv_kv_tree_accept(void* const* caches, int n_caches, int row_bytes, 
  *                 fp32, rounded once; NULL copies it as it is
  *   q_out         bf16 [n_tok][n_h][rope] with strides (inside the absorbed queries [n_tok][n_h][latent +
  *                 rope], say); may be q itself, with its strides
- *   cache         written at slot_mapping (int64 [n_tok]; negative: padding, nothing of the token is written)
+ *   cache         written at slot_mapping (int64 [n_tok]; negative: padding, nothing of the token is written;
+ *                 the others must be distinct)
  * Strides are multiples of 8 elements, pointers 16-byte aligned.  A slot >= num_blocks * block_size sets
  * PKV_DEV_BAD_SLOT and skips the token.  n_h is at most 1024.
  */

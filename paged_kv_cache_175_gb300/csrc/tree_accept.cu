@@ -9,6 +9,9 @@
 // all layers where a launch per layer would cost that much each.  64 sequences, 8 layers of K and V of 8 x 128: 5.6 us;
 // 4 sequences, 40 latent caches: 6.7 us.  Eight loads ahead and CTAs of 256 threads took 7.1 and 7.6: twice the registers,
 // and CTAs in two waves.
+#include <algorithm>
+#include <vector>
+
 #include "drafts.cuh"
 #include "nvtx_range.h"
 
@@ -100,6 +103,19 @@ static bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return a && b && x < y + nb && y < x + na;
 }
+// Whether two of n caches of `bytes` each share memory (one given twice, say, whose rows would move twice).
+static bool any_overlap(void* const* caches, int n, uint64_t bytes) noexcept {
+  try {
+    std::vector<uintptr_t> at(n);
+    for (int i = 0; i < n; ++i) at[i] = reinterpret_cast<uintptr_t>(caches[i]);
+    std::sort(at.begin(), at.end());
+    for (int i = 1; i < n; ++i)
+      if (at[i] - at[i - 1] < bytes) return true;
+    return false;
+  } catch (...) {
+    return true;
+  }
+}
 
 extern "C" pkv_status pkv_kv_tree_accept(void* const* caches, int n_caches, int row_bytes, int heads, const int32_t* block_tables,
                                          int max_blocks, const int32_t* context_lens, const int32_t* q_start, int n_tok,
@@ -120,6 +136,7 @@ extern "C" pkv_status pkv_kv_tree_accept(void* const* caches, int n_caches, int 
       overlaps(new_lens, lens, path, lens * path_stride) || overlaps(new_lens, lens, q_start, lens + sizeof(int32_t)))
     return PKV_EINVAL;
   if ((long long)max_blocks * block_size > 0x7fff0000LL) return PKV_ERANGE;
+  if (any_overlap(caches, n_caches, std::max<uint64_t>(1, (uint64_t)num_blocks * heads * block_size * row_bytes))) return PKV_EINVAL;
   AcceptArgs a = {};
   a.bt = block_tables; a.ctx = context_lens; a.q_start = q_start; a.path = path; a.n_accept = n_accept;
   a.new_lens = new_lens;

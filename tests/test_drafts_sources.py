@@ -1,5 +1,6 @@
 """The kernels of drafted tokens and of the latent cache, read from the sources (no GPU): they start while the kernel before
 them still runs, and nothing it may be writing is read before the wait for it, or past the coherent path."""
+import ctypes
 import re
 
 import pytest
@@ -41,3 +42,12 @@ def test_every_wait_ends():
     for m in re.finditer(r"mbar_try_wait\(", text):
         fn = text[:m.start()].rfind("__device__")
         assert re.search(r"rows_(poll|wait)\(", text[fn:m.start()]), text[fn:m.start()][:80]
+
+
+def test_accept_refuses_caches_that_share_memory():
+    """A cache given twice, or two that overlap: rows would move twice.  (Refused before anything is used; no GPU.)"""
+    from test_drafts_host import EINVAL, accept
+    size = 9 * 2 * 16 * 256                                    # of a cache of the host tests' call
+    for ptrs in ((1 << 20, 1 << 20), (1 << 20, (1 << 20) + size - 16), ((1 << 20) + 16, 1 << 20), (1 << 20, 1 << 30, 1 << 20)):
+        assert accept(caches=(ctypes.c_void_p * len(ptrs))(*ptrs), n=len(ptrs)) == EINVAL
+    assert accept(caches=(ctypes.c_void_p * 2)(1 << 20, (1 << 20) + size), B=0) == 0

@@ -76,7 +76,7 @@ def test_caches_of_an_accept_are_checked():
     a, _ = accept()
     good = rnd(NB, NKV, BS, D)
     for bad in ([], [good, good.cpu()], [good, good.half()], [good, rnd(NB, NKV, BS, 2 * D)], [good, rnd(NB, NKV, BS, 2 * D)[..., :D]],
-                [good, good[None]], [good[0, 0]], [good, None]):
+                [good, good[None]], [good[0, 0]], [good, None], [good, rnd(NB, NKV, BS, D), good]):
         with pytest.raises((pkv.PkvError, ValueError, TypeError, AttributeError)):
             pkv.kv_tree_accept(bad, **a)
     for out in (a["context_lens"], a["n_accept"], a["q_start"][1:], a["path"].view(-1)[:B]):

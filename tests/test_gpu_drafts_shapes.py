@@ -12,6 +12,12 @@ pytestmark = pytest.mark.gpu
 DTYPES = (torch.float32, torch.bfloat16)
 
 
+def check_pairs(got, ref, size, what):
+    """bf16 outputs of weights in two bf16 parts (2^-16 of each), fp32 sums (2^-17) and the output's own rounding, 2^-8 of
+    it.  Outputs of one row are the row: at 4 half a step is 2^-6, so a bar of 10^-2 on the error itself does not fit them."""
+    assert (np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -16 + 2.0 ** -17) * size).all(), what
+
+
 @pytest.mark.parametrize("kind,n_h", [pytest.param(k, h, id=f"{k[0]}_{k[1]}_h{h}") for k, h in
                                       [((1, 64), 64), ((1, 128), 50), ((2, 128), 34), ((512, 64), 128), ((512, 64), 33), ((256, 64), 70)]])
 def test_teams_whose_members_lack_a_row_tile(kind, n_h):
@@ -119,9 +125,31 @@ def test_more_sequences_than_threads(kind, n_h):
     rng = np.random.default_rng(5)
     ctx = rng.integers(0, 40, size=1100)
     c = Case(kind, n_h, 16, ctx, np.minimum(ctx, 1), seed=26, mask=None)
-    got, (ref, size) = f64(c.run(torch.bfloat16)), c.oracle()
-    # p in two bf16 parts, 2^-16 of it; fp32 sums, 2^-17; the output's own rounding, 2^-8 of it.  (Outputs of one row are the row:
-    # at 4 half a step is 2^-6, so a bar on the error itself does not fit them.)
-    assert (np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -16 + 2.0 ** -17) * size).all()
+    check_pairs(f64(c.run(torch.bfloat16)), *c.oracle(), "1100 sequences")
 
 
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_steps(seed):
+    """Heads, blocks, lengths, trees and bad blocks at random."""
+    rng = np.random.default_rng(1000 + seed)
+    if seed % 2:
+        kind, n_h = (int(rng.choice([256, 512])), int(rng.choice([32, 64]))), int(rng.choice([1, 3, 8, 16, 31, 64, 128]))
+    else:
+        n_kv = int(rng.choice([1, 2, 3, 8]))
+        kind, n_h = (n_kv, int(rng.choice([64, 128]))), n_kv * int(rng.choice([1, 2, 5, 8, 16, 33, 64]))
+    batch, most = int(rng.integers(1, 12)), int(rng.choice([1, 2, 9, 33]))
+    ns = rng.integers(0, most + 1, size=batch)
+    if ns.sum() == 0:
+        ns[0] = 1
+    ctx = [int(n + 2.0 ** rng.uniform(0, 11)) * int(rng.random() < 0.9) for n in ns]
+    ctx = [max(c, int(n)) if c else 0 for c, n in zip(ctx, ns)]
+    c = Case(kind, n_h, int(rng.choice([16, 32, 64])), ctx, ns, seed=seed, mask="tree" if rng.random() < 0.7 else None)
+    ref = c.oracle()
+    what = f"{kind} {n_h} {ctx} {ns}"
+    c.check(c.run(), ref, what)
+    if c.single():
+        c.check(c.run(torch.bfloat16), ref, what)
+    else:
+        check_pairs(f64(c.run(torch.bfloat16)), *ref, what)
