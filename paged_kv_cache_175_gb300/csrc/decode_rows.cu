@@ -10,9 +10,10 @@
 // taken as HL bf16 parts, which are columns of one product and are added in the epilogue.
 //
 // Work partition: the line of all (sequence, kv head, group of row tiles, tile of cached rows), in that order, is
-// cut into equal pieces, one for each team of C CTAs; the members of a team take C row tiles of
-// the same cached rows at the same time, so those come from HBM once.  A CTA finds its piece from the lengths by a
-// block-wide scan.  A segment (all tiles of one row tile) that a piece boundary cuts leaves partial softmax states, which a
+// cut into equal pieces, one for each team of C CTAs, where a segment (all tiles of one row tile) counts as a few tiles more than
+// it has, for what its end costs; the members of a team take C row tiles of the same cached rows at the same time, so
+// those come from HBM once.  A CTA finds its piece from the lengths by a
+// block-wide scan.  A segment that a piece boundary cuts leaves partial softmax states, which a
 // second kernel joins; a piece holds at most two cut segments, its first and its last.
 //
 // A CTA of 12 warps runs these roles, joined by mbarriers with bounded waits:
@@ -73,7 +74,7 @@ struct RowsCursor {
   int s, g, rg, t, nt, rt;       // sequence, kv head, group of row tiles, tile; tiles of a segment, row tiles
   int at_start;                  // still in the segment that the piece starts in
   int whole_from;                // the segment began in this piece
-  long long left;                // tiles of the piece from here on (this one included)
+  long long left;                // the piece's share of the line from here on (this tile included)
 };
 
 // KC: 64-channel chunks of a key; VT: M tiles of VM channels of a value; R: query rows; HL: bf16 parts of p.
@@ -85,6 +86,10 @@ struct RowsCfg {
   static constexpr bool SHARED = SHARED_, PP = !SHARED;
   static constexpr int TT = SHARED ? 64 : 128;                // cached rows of a tile
   static constexpr int MT = TT / 64;
+  // What a segment's end (its masked tile, its epilogue, the next queries) weighs on the line, in tiles: with 0 a CTA of many short
+  // segments ended last.  64 trees of 16: 126 us with 0, 113 with 2, 108 with 4, 109 with 6; 128 x 16-1K latent tokens of 16 heads:
+  // 29.6 with 0, 26.7 with 1, 28.4 with 3, and of 128 heads 56.3, 51.3, 50.1.
+  static constexpr int END = PP ? (R == 64 ? 4 : 3) : (R == 64 ? 2 : 1);
   static constexpr int DV = VT * VM, VC = DV / 64;
   static constexpr int CHUNK = TT * 128;
   // Bytes from 8 rows of a slot to the next 8: a copy brings a block's rows of all of a slot's chunks, 1024 bytes of each
@@ -187,7 +192,7 @@ template <class X>
 __device__ __forceinline__ long long line_length(const RowsArgs& a, const Drafts& d) {
   constexpr int tt = X::TT;
   const int rt = row_tiles<X>(a, d.n);
-  return (long long)a.n_kv * ((rt + a.C - 1) / a.C) * ((d.ctx + tt - 1) / tt);
+  return d.ctx > 0 ? (long long)a.n_kv * ((rt + a.C - 1) / a.C) * ((d.ctx + tt - 1) / tt + X::END) : 0;
 }
 
 // Behind a segment's last tile, or where the member has no row tile: the next segment in which it has one (left is 0: the
@@ -199,6 +204,8 @@ __device__ __noinline__ RowsCursor next_segment(RowsCursor c, const RowsArgs& a,
       c.t = 0;
       c.at_start = 0;
       c.whole_from = 1;
+      c.left -= X::END;
+      if (c.left <= 0) break;
       if (++c.rg * a.C >= c.rt) {
         c.rg = 0;
         if (++c.g >= a.n_kv) {
@@ -401,16 +408,17 @@ __global__ void __launch_bounds__(384, 1)
       c.nt = max(1, (c.d.ctx + TT - 1) / TT);
       c.rt = row_tiles<X>(a, c.d.n);
       const int groups = max(1, (c.rt + a.C - 1) / a.C);
-      const long long seg_at = div_pos(off, c.nt);            // segment of the sequence
-      c.t = (int)(off - seg_at * c.nt);
+      const long long seg_at = div_pos(off, c.nt + X::END);   // segment of the sequence
+      const int x = (int)(off - seg_at * (c.nt + X::END));    // where in it: behind its tiles, the piece begins with the next one
+      c.t = min(x, c.nt);
       c.g = (int)div_pos(seg_at, groups);
       c.rg = (int)(seg_at - (long long)c.g * groups);
       c.at_start = 1;
-      c.whole_from = c.t == 0;
-      c.left = line.start(team + 1) - pstart;
-      sh.first = RowsCut{c.t, c.nt, c.d.q0, c.d.n, c.g, c.rg, 0, 0};
+      c.whole_from = x == 0;
+      c.left = line.start(team + 1) - pstart + (x - c.t);
+      sh.first = RowsCut{x < c.nt ? x : 0, c.nt, c.d.q0, c.d.n, c.g, c.rg, 0, 0};
       sh.W = W;
-      if (c.rg * a.C + member >= c.rt) c = next_segment<X>(c, a, member);
+      if (c.t >= c.nt || c.rg * a.C + member >= c.rt) c = next_segment<X>(c, a, member);
       sh.cur = c;
       if (c.left > 0) {
         prefetch_l2(a.bt + (size_t)c.s * a.max_blocks + ((c.t * TT) >> a.bs_log2));
