@@ -865,12 +865,13 @@ __global__ void __launch_bounds__(384, 1)
       }
       // A tile's weights are taken against the running offsets; where an exponent exceeds them by more than kRowsLazy the
       // offsets are raised and the pass is made again.  A segment's first tile starts from the scores of its first row:
-      // offsets need not be the maxima, only near them.  Where that may not be attended to, the maxima are taken first, and so
-      // they are behind such tiles, where a query row may still have no offset, up to one that all of them attend to.
-      if (flags & G_FIRST) unset = special;
+      // offsets need not be the maxima, only near them.  Where not all query rows attend to that, the maxima are taken first, and
+      // so they are behind such tiles, where a query row may still have no offset, up to one whose first row all attend to.
+      const bool sure = mt.tile0 < mt.ctx - mt.n && !(mt.invalid & 1);
+      if (flags & G_FIRST) unset = !sure;
       bool raise = unset;
-      unset = unset && special;
-      if ((flags & G_FIRST) && !special) {
+      unset = unset && !sure;
+      if ((flags & G_FIRST) && sure) {
         if (wq == 0) {
 #pragma unroll 1
           for (int ch = 0; ch < RC / (8 * CB); ++ch) {
