@@ -289,18 +289,20 @@ static __device__ __noinline__ unsigned long long attended(const RowsArgs& a, co
   return w;
 }
 
-// A wait whose polling is out of line: the roles' loops have to fit the instruction cache together.
-static __device__ __noinline__ bool rows_poll(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+// A wait whose polling is out of line: the roles' loops have to fit the instruction cache together.  It gives up after its
+// limit, or when another role has (`stop`).
+static __device__ __noinline__ bool rows_poll(uint64_t* bar, uint32_t parity, uint64_t limit_ns, const volatile int* stop) {
   const uint64_t t0 = global_timer_ns();
   for (uint32_t it = 1; it < (1u << 30); ++it) {
     if (mbar_try_wait(bar, parity)) return true;
+    if (stop && *stop) return false;
     if ((it & 255u) == 0 && global_timer_ns() - t0 > limit_ns) return false;
   }
   return false;
 }
 // Of a whole warp, whose lanes leave it together: what follows (elect.sync, tensor memory) wants a converged warp.
-__device__ __forceinline__ bool rows_wait(uint64_t* bar, int round) {
-  const bool done = mbar_try_wait(bar, round & 1) || rows_poll(bar, round & 1, 2000000000ull);
+__device__ __forceinline__ bool rows_wait(uint64_t* bar, int round, const volatile int* stop) {
+  const bool done = mbar_try_wait(bar, round & 1) || rows_poll(bar, round & 1, 2000000000ull, stop);
   const bool all = __all_sync(FULL_MASK, done);
   __syncwarp();
   return all;
@@ -467,7 +469,7 @@ __global__ void __launch_bounds__(384, 1)
       // last segment's products.
       auto queries = [&] {
         const int qb = k % NQ;
-        ok = k < NQ || rows_wait(&sh.qempty[qb], k / NQ - 1);
+        ok = k < NQ || rows_wait(&sh.qempty[qb], k / NQ - 1, &sh.abort_flag);
         if (!ok) return;
         if (elected()) mbar_arrive_expect_tx(&sh.qfull[qb], (uint32_t)KC * 128u * (uint32_t)(X::SHARED ? R : a.gt * a.tpt));
 #pragma unroll 1
@@ -482,10 +484,6 @@ __global__ void __launch_bounds__(384, 1)
       RowsCursor next = c;
 #pragma unroll 1
       for (int j = 0; j < count && ok; ++j, ++i, blk0 += nbt) {
-        if (sh.abort_flag) {
-          ok = false;
-          break;
-        }
         if (blk0 >= wfrom + 32) {
           win = win_next;
           wfrom += 32;
@@ -538,12 +536,12 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 1
           for (int v = 0; v < VT / 2 && ok; ++v) {
             const int vt = lead ? v : VT / 2 + v, use = i * VT + vt, slot = use % NK;
-            ok = use < NK || rows_wait(&sh.kempty[slot], use / NK - 1);
+            ok = use < NK || rows_wait(&sh.kempty[slot], use / NK - 1, &sh.abort_flag);
             if (!ok) break;
             fill(sm + slot * X::KST, full, &tmk, 2 * vt, lead && v == 0);
           }
           if (ok && !lead) {
-            ok = i < NP || rows_wait(&sh.pslot[i % NP], i / NP - 1);
+            ok = i < NP || rows_wait(&sh.pslot[i % NP], i / NP - 1, &sh.abort_flag);
             if (ok) {                      // the position chunk (tmv: its rows may be narrower than a chunk)
               uint8_t* dst = sm + X::P_OFF + (i % NP) * X::PST;
               auto box = [&](int b) {
@@ -565,7 +563,7 @@ __global__ void __launch_bounds__(384, 1)
           }
         } else {
           const int depth = lead ? NK : NV, st = i % depth;
-          ok = i < depth || rows_wait(lead ? &sh.kempty[st] : &sh.vempty[st], i / depth - 1);
+          ok = i < depth || rows_wait(lead ? &sh.kempty[st] : &sh.vempty[st], i / depth - 1, &sh.abort_flag);
           if (ok)
             fill(sm + (lead ? st * X::KST : X::V_OFF + st * X::VST), lead ? &sh.kfull[st] : &sh.vfull[st], lead ? &tmk : &tmv, 0, lead);
         }
@@ -585,7 +583,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 1
       for (int z = 0; z < NG && ok; ++z, ++i) {
         const int use = X::SHARED ? i * VT : i, slot = use % NK;
-        ok = use < NK || rows_wait(&sh.kempty[slot], use / NK - 1);
+        ok = use < NK || rows_wait(&sh.kempty[slot], use / NK - 1, &sh.abort_flag);
         if (!ok) break;
         if (lane == 0) {
           sh.meta[i % NM].flags = F_END;
@@ -602,12 +600,12 @@ __global__ void __launch_bounds__(384, 1)
     // After a timeout: let the loads already issued land before the CTA leaves (bounded).
     if (sh.abort_flag && lane == 0) {
       bool live = true;
-      for (int j = max(0, i - NF); j <= i && live; ++j) live = rows_poll(&sh.kfull[X::SHARED ? 2 * (j % NF) : j % NF], (j / NF) & 1, 20000000ull);
+      for (int j = max(0, i - NF); j <= i && live; ++j) live = rows_poll(&sh.kfull[X::SHARED ? 2 * (j % NF) : j % NF], (j / NF) & 1, 20000000ull, nullptr);
       live = true;
       constexpr int ND = X::SHARED ? NM : NV;
       for (int j = max(0, i - ND); j <= i && live; ++j)
-        live = rows_poll(X::SHARED ? &sh.kfull[2 * (j % NF) + 1] : &sh.vfull[j % NV], (j / ND) & 1, 20000000ull);
-      if (kq >= 0) rows_poll(&sh.qfull[kq % NQ], (kq / NQ) & 1, 20000000ull);
+        live = rows_poll(X::SHARED ? &sh.kfull[2 * (j % NF) + 1] : &sh.vfull[j % NV], (j / ND) & 1, 20000000ull, nullptr);
+      if (kq >= 0) rows_poll(&sh.qfull[kq % NQ], (kq / NQ) & 1, 20000000ull, nullptr);
     }
     __syncwarp();
   } else if (sh.any && warp == 1) {
@@ -620,12 +618,12 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 1
     for (int i = 0;; ++i) {
       const int k0 = X::SHARED ? i * VT : i, sb = i % NS;     // first slot of the tile's keys
-      ok = !sh.abort_flag && rows_wait(&sh.kfull[X::SHARED ? 2 * (i % NF) : i % NF], i / NF);
+      ok = rows_wait(&sh.kfull[X::SHARED ? 2 * (i % NF) : i % NF], i / NF, &sh.abort_flag);
       if (!ok) break;
       const RowsMeta& mt = sh.meta[i % NM];
       const int flags = __shfl_sync(FULL_MASK, mt.flags, 0), k = __shfl_sync(FULL_MASK, mt.k, 0), qb = k % NQ;
       if (flags & F_END) break;
-      ok = (!(flags & F_FIRST) || rows_wait(&sh.qfull[qb], k / NQ)) && (i < NS || rows_wait(&sh.sempty[sb], i / NS - 1));
+      ok = (!(flags & F_FIRST) || rows_wait(&sh.qfull[qb], k / NQ, &sh.abort_flag)) && (i < NS || rows_wait(&sh.sempty[sb], i / NS - 1, &sh.abort_flag));
       if (!ok) break;
       const uint32_t qa = sbase + ((X::Q_OFF + qb * X::QBUF) >> 4), d = tm + X::S_COL + R * sb;
       tc_fence_after();
@@ -648,7 +646,7 @@ __global__ void __launch_bounds__(384, 1)
         // the halves of its chunks as they land
 #pragma unroll 1
         for (int u = 0; u < VT / 2; ++u) chunks(sbase + ((k0 + u) % NK * X::KST >> 4), 2 * u, 4, std::integral_constant<int, 2>());
-        ok = rows_wait(&sh.kfull[2 * (i % NF) + 1], i / NF);
+        ok = rows_wait(&sh.kfull[2 * (i % NF) + 1], i / NF, &sh.abort_flag);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
@@ -672,7 +670,7 @@ __global__ void __launch_bounds__(384, 1)
       // every product issued has completed before the tensor memory is released
       umma_commit(&sh.drain);
     }
-    rows_wait(&sh.drain, 0);
+    rows_wait(&sh.drain, 0, nullptr);
   } else if (sh.any && warp == 2) {
     // ------------------------- second-product issuer ------------------------
     constexpr uint32_t IPV = umma_idesc_bf16(X::VM, N2, 1, 1);
@@ -684,15 +682,15 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 1
     for (int i = 0;; ++i) {
       const int pb = i % NP, k0 = i * VT;
-      ok = !sh.abort_flag && rows_wait(&sh.kfull[X::SHARED ? 2 * (i % NF) : i % NF], i / NF);
+      ok = rows_wait(&sh.kfull[X::SHARED ? 2 * (i % NF) : i % NF], i / NF, &sh.abort_flag);
       if (!ok) break;
       const RowsMeta& mt = sh.meta[i % NM];
       const int flags = __shfl_sync(FULL_MASK, mt.flags, 0), k = __shfl_sync(FULL_MASK, mt.k, 0), ob = k % NO;
       if (flags & F_END) break;
-      ok = rows_wait(X::SHARED ? &sh.kfull[2 * (i % NF) + 1] : &sh.vfull[i % NV], X::SHARED ? i / NF : i / NV) && rows_wait(&sh.pfull[pb], i / NP);
+      ok = rows_wait(X::SHARED ? &sh.kfull[2 * (i % NF) + 1] : &sh.vfull[i % NV], X::SHARED ? i / NF : i / NV, &sh.abort_flag) && rows_wait(&sh.pfull[pb], i / NP, &sh.abort_flag);
       if (!ok) break;
       const int nks = __shfl_sync(FULL_MASK, (min(TT, mt.ctx - mt.tile0) + 15) >> 4, 0);
-      ok = !(flags & F_FIRST) || k < NO || rows_wait(&sh.oempty[ob], k / NO - 1);
+      ok = !(flags & F_FIRST) || k < NO || rows_wait(&sh.oempty[ob], k / NO - 1, &sh.abort_flag);
       if (!ok) break;
       tc_fence_after();
       __syncwarp();
@@ -728,7 +726,7 @@ __global__ void __launch_bounds__(384, 1)
       }
       umma_commit(&sh.drain);
     }
-    rows_wait(&sh.drain, 0);
+    rows_wait(&sh.drain, 0, nullptr);
   } else if (warp >= 4) {
     // -------------------------- softmax and epilogue ------------------------
     // Warp w reaches the tensor-memory lanes of quarter w % 4: in S^T the cached rows 16 MT wq + ..., in fragments of
@@ -758,8 +756,7 @@ __global__ void __launch_bounds__(384, 1)
       return any;
     };
     auto wait = [&](uint64_t* bar, int round) {               // nothing but that a wait failed, or one of another role did, ends it early
-      bad = __any_sync(FULL_MASK, bad || sh.abort_flag);
-      if (!bad) bad = !rows_wait(bar, round);
+      if (!bad) bad = !rows_wait(bar, round, &sh.abort_flag);
     };
 
 #pragma unroll 1

@@ -38,7 +38,7 @@ def test_every_wait_ends():
     for fn in ("rows_poll", "rows_wait"):
         start = text.index(" " + fn + "(")
         body = text[start:text.index("\n}", start)]
-        assert "limit_ns" in body or "rows_poll(bar, round & 1, 2000000000ull)" in body
+        assert "limit_ns" in body or "rows_poll(bar, round & 1, 2000000000ull" in body
     for m in re.finditer(r"mbar_try_wait\(", text):
         fn = text[:m.start()].rfind("__device__")
         assert re.search(r"rows_(poll|wait)\(", text[fn:m.start()]), text[fn:m.start()][:80]
