@@ -232,20 +232,21 @@ __device__ __noinline__ RowsCursor next_segment(RowsCursor c, const RowsArgs& a,
 }
 __device__ __forceinline__ float sum_inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }   // a sum that is no number stays one
 
-// Token (of its sequence, -1: none) and head of the group of query row c of a row tile.
+// Token (of its sequence, -1: none) and head of the group of query row c of a row tile; `in` is row_in(a, c).
 template <class X>
-__device__ __forceinline__ int2 query_of(const RowsArgs& a, int n, int t0, int h0, int c) {
-  int t, h;
+__device__ __forceinline__ int2 row_in(const RowsArgs& a, int c) {
+  if constexpr (X::SHARED) return make_int2(0, c);
+  return make_int2(c < a.gt * a.tpt ? c / a.gt : 1 << 30, c % a.gt);
+}
+template <class X>
+__device__ __forceinline__ int2 query_of(const RowsArgs& a, int n, int t0, int h0, int2 in) {
+  int h = h0 + in.y;                                          // a latent cache's tile may begin inside a token
+  long long t = (long long)t0 + in.x;
   if constexpr (X::SHARED) {
-    const int r = h0 + c;                                     // the tile may begin inside a token
-    t = t0 + r / a.G;
-    h = r % a.G;
-  } else {
-    t = t0 + c / a.gt;
-    h = h0 + c % a.gt;
-    if (c >= a.gt * a.tpt) t = n;
+    t += h / a.G;
+    h %= a.G;
   }
-  return make_int2(t < n && h < a.G ? t : -1, h);
+  return make_int2(t < n && h < a.G ? (int)t : -1, h);
 }
 template <class X>
 __device__ __forceinline__ void tile_of(const RowsArgs& a, int rt, int& t0, int& h0) {
@@ -742,6 +743,8 @@ __global__ void __launch_bounds__(384, 1)
     float* off = sh.offset[wg];            // offsets of the query rows, minus infinity where there is none yet
     float l[NC];                           // this thread's rows' share of the sums of its query rows
     bool unset = false;                    // a query row may have no offset yet
+    static_assert(NW % R == 0, "a thread's query row in every pass");
+    const int2 mine = row_in<X>(a, tid % R);
     // Barriers among the threads of a tile.  A failed (timed-out) wait makes `bad` true for its warp, which raises a flag ahead
     // of the next barrier; behind that all of them see it and leave together, so no thread is left at a barrier.  The
     // flag goes by the barrier's parity, since a warp may be one barrier ahead of another.
@@ -781,9 +784,9 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int e = 0; e < WN; ++e) {
           win[e] = 0;
-          const int c = (tid + e * NW) % R, w = (tid + e * NW) / R;
+          const int w = (tid + e * NW) / R;
           if (w < MT) {
-            const int tok = query_of<X>(a, mt.n, mt.t0, mt.h0, c).x;
+            const int tok = query_of<X>(a, mt.n, mt.t0, mt.h0, mine).x;
             if (tok >= 0) win[e] = attended(a, mt, tok, mt.tile0 + 64 * w);
           }
         }
@@ -802,10 +805,34 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int q = 0; q < NC; ++q) l[q] = 0.f;
         if (a.mask && tid < R && !special) {                  // the masks that the segment will end with
-          const int tok = query_of<X>(a, mt.n, mt.t0, mt.h0, tid).x;
+          const int tok = query_of<X>(a, mt.n, mt.t0, mt.h0, mine).x;
           if (tok >= 0) prefetch_l2(a.mask + (size_t)(mt.q0 + tok) * a.mask_words);
         }
         __syncwarp();
+      }
+      // A tile's weights are taken against the running offsets; where an exponent exceeds them by more than kRowsLazy the
+      // offsets are raised and the pass is made again.  A segment's first tile starts from the scores of its first row:
+      // offsets need not be the maxima, only near them.  Where not all query rows attend to that, the maxima are taken first, and
+      // so they are behind such tiles, where a query row may still have no offset, up to one whose first row all attend to.
+      const bool sure = mt.tile0 < mt.ctx - mt.n && !(mt.invalid & 1);
+      if (flags & G_FIRST) unset = !sure;
+      bool raise = unset;
+      unset = unset && !sure;
+      if ((flags & G_FIRST) && sure) {
+        if (wq == 0) {
+#pragma unroll 1
+          for (int ch = 0; ch < RC / (8 * CB); ++ch) {
+            uint32_t sr[4 * CB];
+            tmem_ld_frag(st + ch * 8 * CB, sr);
+            tmem_wait_ld();
+            if (lane < 4) {
+#pragma unroll
+              for (int b = 0; b < 2 * CB; ++b) off[c0 + 8 * (ch * CB + (b >> 1)) + (b & 1)] = __uint_as_float(sr[4 * (b >> 1) + (b & 1)]) * a.scale_log2;
+            }
+            __syncwarp();
+          }
+        }
+        if (!special && (sync(false), gone)) break;            // (behind a masked tile's barrier otherwise)
       }
       if (special) {
         // What each query row attends to, and what any of them does.  Scores that do not count become minus infinities (before
@@ -859,30 +886,6 @@ __global__ void __launch_bounds__(384, 1)
           }
         }
         __syncwarp();
-      }
-      // A tile's weights are taken against the running offsets; where an exponent exceeds them by more than kRowsLazy the
-      // offsets are raised and the pass is made again.  A segment's first tile starts from the scores of its first row:
-      // offsets need not be the maxima, only near them.  Where not all query rows attend to that, the maxima are taken first, and
-      // so they are behind such tiles, where a query row may still have no offset, up to one whose first row all attend to.
-      const bool sure = mt.tile0 < mt.ctx - mt.n && !(mt.invalid & 1);
-      if (flags & G_FIRST) unset = !sure;
-      bool raise = unset;
-      unset = unset && !sure;
-      if ((flags & G_FIRST) && sure) {
-        if (wq == 0) {
-#pragma unroll 1
-          for (int ch = 0; ch < RC / (8 * CB); ++ch) {
-            uint32_t sr[4 * CB];
-            tmem_ld_frag(st + ch * 8 * CB, sr);
-            tmem_wait_ld();
-            if (lane < 4) {
-#pragma unroll
-              for (int b = 0; b < 2 * CB; ++b) off[c0 + 8 * (ch * CB + (b >> 1)) + (b & 1)] = __uint_as_float(sr[4 * (b >> 1) + (b & 1)]) * a.scale_log2;
-            }
-            __syncwarp();
-          }
-        }
-        if (sync(false), gone) break;
       }
       float ts[NC];                        // the tile's part of l
 #pragma unroll 1
@@ -1019,7 +1022,7 @@ __global__ void __launch_bounds__(384, 1)
         // each puts together half of the query rows.
         const bool whole = flags & F_WHOLE, pair = PP && !(flags & G_SOLO);
         if (tid < R) {
-          const int2 qh = query_of<X>(a, n, t0, h0, tid);
+          const int2 qh = query_of<X>(a, n, t0, h0, mine);
           if (qh.x >= 0) out_row = (q0 + qh.x) * a.n_h + g * a.G + qh.y;
         }
         __syncwarp();
@@ -1185,7 +1188,7 @@ __global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ 
     const int c = WIDE ? blockIdx.y : blockIdx.y * 8 + warp;
     int t0, h0;
     tile_of<X>(a, cut.rg * a.C + member, t0, h0);
-    const int2 qh = query_of<X>(a, cut.n, t0, h0, c);
+    const int2 qh = query_of<X>(a, cut.n, t0, h0, row_in<X>(a, c));
     if (qh.x < 0) {                          // (of the whole CTA, where it is wide)
       if (WIDE) continue;
       return;
