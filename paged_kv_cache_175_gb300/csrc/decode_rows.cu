@@ -1032,9 +1032,7 @@ __global__ void __launch_bounds__(384, 1)
           if (tid < R && !bad) sh.sum[PP ? ob : 0][wg][PP ? tid : 0] = own;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.joined[wg]);
-          wait(&sh.joined[0], joins);
-          wait(&sh.joined[NG - 1], joins);
-          ++joins;
+          wait(&sh.joined[NG - 1 - wg], joins++);             // the other group's (a thread reads no more of its own than it wrote)
         }
         if (tid < R && !bad) {
           // an accumulator none of whose rows counted (its sum is 0) has no part in it
