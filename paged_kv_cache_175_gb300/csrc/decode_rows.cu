@@ -24,16 +24,18 @@
 //               with an O accumulator of its own; latent cache: both take every tile, half of the query rows each
 //
 // What bounds it (GPU time; R query rows per CTA):
-//   64 trees of up to 16 tokens over 0.5-4K rows, 8 kv heads of 4 x 128 (620 MB): 124 us, 5.0 TB/s: HBM, and about 10000 clocks
-//     per segment for its masked tile and its epilogue.  The same of up to 8 tokens: 108 us.
-//   8 trees of up to 64 over 8-32K, 8 x 8 heads (512 rows, 207 GFLOP): 380 us, 544 TFLOP/s: shared memory and HBM.  A tile of 128
-//     rows writes 64 KB to shared memory and its products read 96, about 1600 of the 1750 clocks that it takes; HBM is 72% busy, since
-//     the caches are read 3.2 times over.  128 rows per CTA, which would read less, took 489: they leave two S buffers and three
-//     key stages.  Teams of four read half and took 397: their members lack a row tile more often.
-//   64 x 0.5-4K latent tokens of 16 heads (173 MB): 41 us, 4.2 TB/s: HBM for 25 of them, then setup, first loads and the join.
-//   32 x 2-16K latent tokens of 128 heads (82 GFLOP): 126 us, 645 TFLOP/s: shared memory again, 72 KB written and 245
+//   64 trees of up to 16 tokens over 0.5-4K rows, 8 kv heads of 4 x 128 (620 MB): 106 us, 5.8 TB/s: HBM, then the segments' ends.  The
+//     same of up to 8 tokens: 101 us.
+//   8 trees of up to 64 over 8-32K, 8 x 8 heads (512 rows, 207 GFLOP): 369 us, 558 TFLOP/s: shared memory and HBM.  A tile of 128
+//     rows writes 64 KB to shared memory and its products read 96, about 1600 of the 1700 clocks that it takes; HBM is 72% busy, since
+//     the caches are read 3.2 times over.  (128 query rows per CTA, which read less, took 489 us where 64 took 398: they leave two S
+//     buffers and three key stages.)
+//   64 x 0.5-4K latent tokens of 16 heads (173 MB): 41 us, 4.2 TB/s: HBM for 28 of them, then setup, first loads and the join.
+//   32 x 2-16K latent tokens of 128 heads (82 GFLOP): 123 us, 662 TFLOP/s: shared memory again, 72 KB written and 245
 //     read per tile of 64 rows.
-//   One tree of 8 over 333 rows: 10.9 us; one latent token of 16 heads over 301: 12.5: setup 1.4 us, loads 2, masks and softmax 2,
+//   300 trees of up to 4 over 1-300 rows (2400 segments): 73 us: the ends of 16 segments per CTA, about 8000 clocks each: masks, softmax,
+//     second product and epilogue, in series.
+//   One tree of 8 over 333 rows: 10.9 us; one latent token of 16 heads over 301: 12.5: setup 1.5 us, loads 2, masks and softmax 2,
 //     epilogue 1, the join 2, and code that is run once and cold.
 #include <cmath>
 #include <mutex>
@@ -87,8 +89,8 @@ struct RowsCfg {
   static constexpr int TT = SHARED ? 64 : 128;                // cached rows of a tile
   static constexpr int MT = TT / 64;
   // What a segment's end (its masked tile, its epilogue, the next queries) weighs on the line, in tiles: with 0 a CTA of many short
-  // segments ended last.  64 trees of 16: 126 us with 0, 113 with 2, 108 with 4, 109 with 6; 128 x 16-1K latent tokens of 16 heads:
-  // 29.6 with 0, 26.7 with 1, 28.4 with 3, and of 128 heads 56.3, 51.3, 50.1.
+  // segments ended last.  When it was chosen: 64 trees of 16 126 us with 0, 113 with 2, 108 with 4, 109 with 6; 128 x 16-1K latent
+  // tokens of 16 heads 29.6 with 0, 26.7 with 1, 28.4 with 3, and of 128 heads 56.3, 51.3, 50.1.
   static constexpr int END = PP ? (R == 64 ? 4 : 3) : (R == 64 ? 2 : 1);
   static constexpr int DV = VT * VM, VC = DV / 64;
   static constexpr int CHUNK = TT * 128;
@@ -100,7 +102,7 @@ struct RowsCfg {
   static constexpr int PAT = (N2 + 63) / 64, PBUF = PAT * CHUNK;
   // Rings, from what 227 KB hold.  K and V pools: NK stages of a tile's keys and NV of its values, which are held for less of
   // a tile's way: with 64 query rows of 128 channels, where that way and not the memory sets the pace, 4 and 2 (8 x 8-32K
-  // tokens, 512 rows: 431 us, and 475 with 3 and 3).  Latent cache: NK slots of two
+  // tokens, 512 rows: 369 us, and 426 with 3 and 3).  Latent cache: NK slots of two
   // chunks, which the second product frees one after another, and NP slots of the position chunk.  The tile's P takes
   // the place of its keys (of their position chunk), which the first product is the only one to read.
   static constexpr bool FULL = SHARED && KC == 9 && R == 64;  // 72 KB of query rows
@@ -1332,11 +1334,11 @@ static RowsVariant* latent_variant(int latent, int R, bool f32) {
 }
 
 // Query rows of a row tile, and members of a team, from the average of the sequences' query rows per kv head.  Rows that no
-// query has cost products and softmax all the same, row tiles loads: 64 trees of 16 rows took 103 us with R = 16 and 110
-// with 32, of 32 rows 109 with 32 and 124 with 64, of 64 rows 125 with 64 and 167 with 32; 64 latent tokens of 16 heads
-// 41, 43 and 50 with 16, 32 and 64.  Two members read what one CTA loads twice (32 latent tokens of 128 heads 126 us and
-// 136, 8 trees of 512 rows 382 and 418), but where the sequences' rows differ one of them may have no tile (12 trees over the latent
-// cache 53 and 51; with four members 61, and 397 for the 8 trees).
+// query has cost products and softmax all the same, row tiles loads: 64 trees of 16 rows took 99 us with R = 16, 102
+// with 32 and 105 with 64, of 32 rows 102 with 32 and 106 with 64, of 64 rows 108 with 64 and 154 with 32; 64 latent tokens of 16
+// heads 41, 42 and 49 with 16, 32 and 64.  Two members read what one CTA loads twice (32 latent tokens of 128 heads 124 us and
+// 134, 8 trees of 512 rows 369 and 392), but where the sequences' rows differ one of them may have no tile (12 trees over the latent
+// cache 48 and 48; with four members 58, and 379 for the 8 trees).
 struct RowsShape {
   int R, C, P;
   long long groups;              // of row tiles, on average
@@ -1455,7 +1457,7 @@ static pkv_status rows_attn(const RowsShape& s, RowsVariant* v, bool latent, con
   cudaError_t e = launch_pdl(v->fn, dim3(s.P * s.C), dim3(384), v->smem, st, kargs);
   if (e == cudaSuccess) {
     // The pieces over the segments: about the parts that each has, if it has so many tiles.  16 heads over 64K latent tokens:
-    // 64 us by a warp per query row, 31 by a CTA; 64 sequences of 16 heads: 41 and 43.
+    // 64 us by a warp per query row, 30 by a CTA; 64 trees of 64 rows: 106 and 150.
     const long long segments = (long long)batch * n_kv * s.groups, tiles = a.max_ctx / (latent ? 64 : 128);
     const bool wide = s.P >= 8 * segments && tiles >= 8 && s.P <= 256;
     void* jargs[] = {&a};

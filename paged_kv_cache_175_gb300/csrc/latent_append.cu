@@ -4,9 +4,10 @@
 // Mathematics: y = x w / sqrt(mean(x^2) + eps) in fp32 with one rounding; the rotation and its angles as in
 // rope_append.cu (the position times a 64-bit fraction of a turn, exact for every int32 position).
 //
-// What bounds it: every element is read once and written once: HBM for long calls (16001 tokens of 16 heads, 102 MB:
-// 21.4 us, 4.8 TB/s; 4001 of 128 heads, 140 MB: 23.8 us, 5.9 TB/s), the launch and two dependent memory round trips
-// (position and slot beside the rows, then the stores) for short ones (64 tokens of 128 heads: 2.5 us).
+// What bounds it: every element is read once and written once.  Long calls of many heads are at HBM (4001 tokens of 128 heads,
+// 140 MB: 23.8 us, 5.9 TB/s), of few heads at issue (54% busy: angles, shuffles, conversions) and latency with 32 warps per SM
+// (16001 of 16, 103 MB: 21.4 us, 4.8 TB/s), short ones at the launch and two dependent memory round trips
+// (position and slot beside the rows, then the stores): 64 tokens of 128 heads 2.5 us.
 // Split: a warp per (token, part).  Part 0 is the token's vector: 16 or 8 channels of the latent part
 // per lane, whose squares meet in five shuffles, and the key part.  The other parts are runs of
 // 32 * NI items of the token's query heads, an item being two 16-byte vectors (eight channel pairs): one item per lane
