@@ -51,7 +51,7 @@ static int encode_tiled(CUtensorMap* map, const void* base, int rank, const cuui
   };
   CUresult r = call();
   int dev = 0;
-  // the driver's call wants a current context, which a thread whose first CUDA call this is does not have yet
+  // cuTensorMapEncodeTiled wants a current context, which a thread whose first CUDA call this is does not have yet
   if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = call();
   return r == CUDA_SUCCESS ? 0 : (int)r;
 }

@@ -5,14 +5,14 @@
 // rope_append.cu (the position times a 64-bit fraction of a turn, exact for every int32 position).
 //
 // What bounds it: every element is read once and written once.  Long calls of many heads are at HBM (4001 tokens of 128 heads,
-// 140 MB: 23.8 us, 5.9 TB/s), of few heads at issue (54% busy: angles, shuffles, conversions) and latency with 32 warps per SM
-// (16001 of 16, 103 MB: 21.4 us, 4.8 TB/s), short ones at the launch and two dependent memory round trips
-// (position and slot beside the rows, then the stores): 64 tokens of 128 heads 2.5 us.
+// 140 MB: 24.4 us, 5.8 TB/s), of few heads at issue (54% busy: angles, shuffles, conversions) and latency with 32 warps per SM
+// (16001 of 16, 103 MB: 20.8 us, 4.9 TB/s), short ones at the launch and two dependent memory round trips
+// (position and slot beside the rows, then the stores): 64 tokens of 128 heads 2.3 us.
 // Split: a warp per (token, part).  Part 0 is the token's vector: 16 or 8 channels of the latent part
 // per lane, whose squares meet in five shuffles, and the key part.  The other parts are runs of
 // 32 * NI items of the token's query heads, an item being two 16-byte vectors (eight channel pairs): one item per lane
 // while that does not fill the GPU, more where it does, so that a warp's fixed work (position, angles) goes round more
-// bytes (16 heads: 26.9 us with one item, 21.4 with two; 128 heads: 25.1 with two, 23.8 with four).
+// bytes (16 heads: 24.5 us with one item, 20.8 with two, 21.9 with four; 128 heads: 32.0, 24.8 and 24.4).
 // A lane computes the angle of pair `lane`; the eight that an item needs come by shuffles, and are the same
 // for all of a lane's items.  All loads are issued before the first use.
 #include <cmath>
@@ -29,7 +29,7 @@ struct LatentAppendArgs {
   const int32_t* positions;
   const int64_t* slots;
   long long n_slots;
-  int n_tok, n_h, parts;                         // parts: 1 + runs of query items
+  int n_tok, n_h;
   float eps;
   int32_t* err;
   pkv_rope_table t;
@@ -43,9 +43,9 @@ __global__ void __launch_bounds__(kLatentThreads) latent_append_kernel(const __g
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31;
-  const long long unit = (long long)blockIdx.x * (kLatentThreads / 32) + (threadIdx.x >> 5);
-  if (unit >= (long long)a.n_tok * a.parts) return;
-  const int tok = (int)(unit / a.parts), part = (int)(unit % a.parts);
+  const long long group = (long long)blockIdx.z * gridDim.y + blockIdx.y, t = group * (kLatentThreads / 32) + (threadIdx.x >> 5);
+  if (t >= a.n_tok) return;
+  const int tok = (int)t, part = blockIdx.x;
   const bool inter = a.t.interleaved != 0;
   const int p = lane % IPH;                                   // this lane's group of eight pairs
   const int va = inter ? 2 * p : p, vb = inter ? 2 * p + 1 : p + IPH;   // its two vectors
@@ -204,12 +204,12 @@ extern "C" pkv_status pkv_latent_append(const void* kv, int64_t kv_stride, const
   const int items = n_h * (rope / 16), sms = device_sm_count() > 0 ? device_sm_count() : 128;
   const bool wide = (long long)n_tok * items >= (long long)sms * 32 * 64;
   const int ni = !wide ? 1 : (items <= 64 ? 2 : 4);
-  a.parts = 1 + (items + 32 * ni - 1) / (32 * ni);
-  const long long grid = ((long long)n_tok * a.parts + kLatentThreads / 32 - 1) / (kLatentThreads / 32);
-  if (grid > 0x7fffffffLL) return PKV_ERANGE;
+  // the parts of a few tokens run side by side, near one another in memory (4001 tokens of 128 heads: 26.3 us the other way about)
+  const unsigned groups = (n_tok - 1) / (kLatentThreads / 32) + 1, rows = groups < 32768u ? groups : 32768u;
+  const dim3 grid(1 + (items + 32 * ni - 1) / (32 * ni), rows, (groups + rows - 1) / rows);
   void* kargs[] = {&a};
   const void* fn = ni == 1 ? latent_append_fn<1>(latent, rope) : (ni == 2 ? latent_append_fn<2>(latent, rope) : latent_append_fn<4>(latent, rope));
-  const cudaError_t e = launch_pdl(fn, dim3((unsigned)grid), dim3(kLatentThreads), 0, static_cast<cudaStream_t>(stream), kargs);
+  const cudaError_t e = launch_pdl(fn, grid, dim3(kLatentThreads), 0, static_cast<cudaStream_t>(stream), kargs);
   if (e != cudaSuccess) {
     record_cuda_error(e);
     return PKV_ECUDA;
