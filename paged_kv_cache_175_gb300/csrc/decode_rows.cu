@@ -777,7 +777,10 @@ __global__ void __launch_bounds__(384, 1)
       }
       const RowsMeta& mt = sh.meta[i % NM];
       const int flags = mt.flags, ob = mt.k % NO;
-      if (flags & F_END) break;
+      if (flags & F_END) {
+        sync(false);                       // with a warp whose wait for it has failed
+        break;
+      }
       const bool special = mt.tile0 + TT > mt.ctx - mt.n || mt.invalid;
       // what query row (tid + e NW) % R attends to in word (tid + e NW) / R of the tile's rows
       constexpr int WN = (R * MT + NW - 1) / NW;

@@ -153,3 +153,19 @@ def test_random_steps(seed):
         c.check(c.run(torch.bfloat16), ref, what)
     else:
         check_pairs(f64(c.run(torch.bfloat16)), *ref, what)
+
+
+def test_a_long_append_is_its_parts():
+    # more tokens than one dimension of the grid takes, against calls of a few thousand
+    n, n_h, latent, rope, bs = 140003, 2, 256, 32, 64
+    g = torch.Generator(device=DEV).manual_seed(0)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=DEV).bfloat16()  # noqa: E731
+    kv, q, weight, table = rnd(n, latent + rope), rnd(n, n_h, rope), rnd(latent), pkv.rope_table(64, rope)
+    pos, blocks = torch.arange(n, dtype=torch.int32, device=DEV), -(-n // bs)
+    slots, err = torch.randperm(blocks * bs, generator=g, device=DEV)[:n], err_flag()
+    caches = [torch.zeros(blocks, bs, latent + rope, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    out = pkv.latent_append(kv, q, pos, slots, table, caches[0], weight=weight, err=err)
+    parts = [pkv.latent_append(kv[i:i + 9001], q[i:i + 9001], pos[i:i + 9001], slots[i:i + 9001], table, caches[1], weight=weight, err=err)
+             for i in range(0, n, 9001)]
+    assert torch.equal(out, torch.cat(parts)) and torch.equal(*caches) and int(err.item()) == 0
+    assert bool(caches[0].view(-1, latent + rope)[slots].any(1).all())
