@@ -499,9 +499,8 @@ pkv_status pkv_kv_evict(void* k_pool, void* v_pool, const int32_t* block_tables,
  *   workspace     pkv_tree_workspace_bytes bytes (0: invalid shape), 256-byte aligned; a call of other
  *                 n_tok or batch may need another size
  * Softmax and sums are fp32 and taken in a fixed order (the same bits on every call).  p is carried in bf16 parts: all
- * of its 24 bits in three for an fp32 output; for a bf16 output in two (an error of at most 2^-16 sum p |v|), or, with more
- * than 32 query rows per kv head and sequence on average (n_tok * n_h / (batch * n_kv)), in one (2^-8 sum p |v|, of the size of
- * the output's own rounding; the sum that divides it is then that of the rounded values).  Cached rows that no token of the sequence attends to do not
+ * of its 24 bits in three for an fp32 output, in two for a bf16 output (an error of at most 2^-16 sum p |v|).  Cached rows
+ * that no token of the sequence attends to do not
  * reach any output, whatever they hold; a row that some of its tokens attend to and others mask has to
  * hold finite values (0 times an infinity of V is no number).  Weights are held as exp(score - c) with a c that may lie
  * 2^32 in weight below the largest until the end, so values of V beyond 2^90 may overflow.  Pools, tables, lengths, scale, other
@@ -571,7 +570,6 @@ pkv_status pkv_latent_append(const void* kv, int64_t kv_stride, const void* q, i
  *   out           [n_tok][n_h][latent]
  * q_start, tree_mask and everything else as for pkv_paged_tree_attn (one token per sequence: q_start NULL and
  * n_tok = batch).
- * The query rows that choose p's parts are n_tok * n_h / batch here.
  */
 size_t pkv_latent_workspace_bytes(int batch, int n_tok, int n_h, int latent, int rope, int block_size);
 pkv_status pkv_paged_latent_attn(const void* q, const void* cache, const int32_t* block_tables, int max_blocks,

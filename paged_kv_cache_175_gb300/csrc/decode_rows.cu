@@ -7,7 +7,8 @@
 //   S^T[rows of the tile][R]   = K Q^T                 (both K-major, as they lie in memory)
 //   O^T[channels][HL R]       += V^T [P_1 | P_2 ..]^T  (both MN-major, as they lie in shared memory)
 // K and V of a latent cache are the same rows, which are loaded once: V is the first channels of the K slots.  P is
-// taken as HL bf16 parts, which are columns of one product and are added in the epilogue.
+// taken as HL bf16 parts, which are columns of one product and are added in the epilogue (64 query rows over 512 latent
+// channels: two products into the same columns).
 //
 // Work partition: the line of all (sequence, kv head, group of row tiles, tile of cached rows), in that order, is
 // cut into equal pieces, one for each team of C CTAs, where a segment (all tiles of one row tile) counts as a few tiles more than
@@ -97,27 +98,31 @@ struct RowsCfg {
   // Bytes from 8 rows of a slot to the next 8: a copy brings a block's rows of all of a slot's chunks, 1024 bytes of each
   // chunk for every 8 rows.
   static constexpr int GS = SHARED ? 2048 : KC * 1024;
-  static constexpr int N2 = R * HL;                           // columns of the second product
+  // 64 query rows of 512 latent channels: 72 KB of queries, and an O that leaves tensor memory for one part of p.  The second
+  // part is then a product of its own into the same columns, from one buffer for all tiles.
+  static constexpr bool FULL = SHARED && KC == 9 && R == 64;
+  static constexpr int HO = FULL ? 1 : HL;                    // parts of p that are columns of one product
+  static constexpr int N2 = R * HO;                           // columns of the second product
   static constexpr int QCH = R * 128, QBUF = KC * QCH;
   static constexpr int PAT = (N2 + 63) / 64, PBUF = PAT * CHUNK;
   // Rings, from what 227 KB hold.  K and V pools: NK stages of a tile's keys and NV of its values, which are held for less of
-  // a tile's way: with 64 query rows of 128 channels, where that way and not the memory sets the pace, 4 and 2 (8 x 8-32K
-  // tokens, 512 rows: 369 us, and 426 with 3 and 3).  Latent cache: NK slots of two
+  // a tile's way: with 64 query rows of 128 channels, where that way and not the memory sets the pace, 4 and 2, and one buffer of
+  // query rows (8 x 8-32K tokens, 512 rows: 388 us, and 452 with 3 and 2 and two such buffers).  Latent cache: NK slots of two
   // chunks, which the second product frees one after another, and NP slots of the position chunk.  The tile's P takes
   // the place of its keys (of their position chunk), which the first product is the only one to read.
-  static constexpr bool FULL = SHARED && KC == 9 && R == 64;  // 72 KB of query rows
-  static constexpr int KPART = KC * CHUNK > PBUF + 4096 ? KC * CHUNK : PBUF + 4096;   // P and the scratch behind it
+  static constexpr int KPART = KC * CHUNK > PBUF + 3072 ? KC * CHUNK : PBUF + 3072;   // P and the scratch behind it
   static constexpr int KST = SHARED ? 2 * CHUNK : KPART, VST = VC * CHUNK;
   static constexpr int PST = SHARED ? PBUF : KST;
-  static constexpr int NQ = SHARED && (KC == 9 ? R > 16 : R == 64) ? 1 : 2;
+  static constexpr int NQ = (SHARED && (KC == 9 ? R > 16 : R == 64)) || (KC == 2 && R == 64) ? 1 : 2;
   static constexpr int NK = SHARED ? (FULL || PAT > 1 ? 8 : 9) : (KC == 1 || R == 64 ? 4 : 3), NV = SHARED ? 1 : (KC == 1 ? 4 : (R == 64 ? 2 : 3));
-  static constexpr int NP = SHARED ? 3 : NK;                  // tiles whose P there is room for
+  static constexpr int NP = SHARED ? (FULL ? 2 : 3) : NK;     // tiles whose P there is room for
   static constexpr int NM = SHARED ? (KC == 9 ? 3 : 8) : NK;  // metadata of tiles: of all that the ring may hold a part of
   static constexpr int NS = PP ? 4 : 2, NG = PP ? 2 : 1;      // S buffers; accumulators of a segment
   static constexpr int NO = VT * N2 * NG * 2 + NS * R <= 512 && !(PP && R == 64) ? 2 : 1;
   static constexpr int S_COL = VT * N2 * NG * NO, NCOL = S_COL + NS * R;
   static constexpr uint32_t TMEM_COLS = NCOL <= 64 ? 64 : (NCOL <= 128 ? 128 : (NCOL <= 256 ? 256 : 512));
-  static constexpr int P_OFF = SHARED ? NK * KST : 0, V_OFF = NK * KST, Q_OFF = NK * KST + (SHARED ? NP * PST : NV * VST), W_OFF = Q_OFF + NQ * QBUF, M_OFF = W_OFF + (SHARED ? 28 * R + 16 : 0);   // W: scratch
+  static constexpr int P_OFF = SHARED ? NK * KST : 0, V_OFF = NK * KST, L_OFF = P_OFF + NP * PST,
+                       Q_OFF = NK * KST + (SHARED ? NP * PST + (FULL ? PBUF : 0) : NV * VST), W_OFF = Q_OFF + NQ * QBUF, M_OFF = W_OFF + (SHARED ? 28 * R + 16 : 0);   // W: scratch
   static constexpr bool F32 = HL == 3;                        // output type
 };
 
@@ -321,7 +326,7 @@ template <class X>
 __global__ void __launch_bounds__(384, 1)
     decode_rows_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                        const __grid_constant__ CUtensorMap tmq, const __grid_constant__ RowsArgs a) {
-  constexpr int TT = X::TT, R = X::R, HL = X::HL, N2 = X::N2, KC = X::KC, VT = X::VT, MT = X::MT, DV = X::DV;
+  constexpr int TT = X::TT, R = X::R, HL = X::HL, HO = X::HO, N2 = X::N2, KC = X::KC, VT = X::VT, MT = X::MT, DV = X::DV;
   constexpr int NK = X::NK, NV = X::NV, NM = X::NM, NP = X::NP, NO = X::NO, NS = X::NS, NG = X::NG, NQ = X::NQ;
   constexpr int NF = X::SHARED ? NM : NK;                     // full barriers
   constexpr bool PP = X::PP;
@@ -707,6 +712,11 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int kk = 0; kk < TT / 16; ++kk)
             if (kk < nks) umma_bf16_lo(d + vt * N2, vb + kk * (2 * X::GS >> 4), HIV, pa + kk * 128, HI, IPV, kk ? 1u : acc0);
+          if constexpr (X::FULL) {
+#pragma unroll
+            for (int kk = 0; kk < TT / 16; ++kk)
+              if (kk < nks) umma_bf16_lo(d + vt * N2, vb + kk * (2 * X::GS >> 4), HIV, sbase + (X::L_OFF >> 4) + kk * 128, HI, IPV, 1u);
+          }
           umma_commit(X::SHARED ? &sh.kempty[slot] : &sh.vempty[slot]);
         }
         __syncwarp();
@@ -893,6 +903,7 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
       }
       float ts[NC];                        // the tile's part of l
+      uint32_t second[X::FULL ? NC * MT : 1];                 // second parts of p that wait for their buffer
 #pragma unroll 1
       for (;;) {
         if (raise) {
@@ -929,10 +940,10 @@ __global__ void __launch_bounds__(384, 1)
             for (int q = 0; q < NC; ++q) l[q] *= scr.factor[c0 + 8 * (q >> 1) + (q & 1)];
             tc_fence_after();
 #pragma unroll 1
-            for (int p = 0; p < VT * HL; ++p) {
+            for (int p = 0; p < VT * HO; ++p) {
 #pragma unroll 1
               for (int b = 0; b < RC; b += 8) {
-                const uint32_t ta = acc + (p / HL) * N2 + (p % HL) * R + hb + b;
+                const uint32_t ta = acc + (p / HO) * N2 + (p % HO) * R + hb + b;
                 uint32_t o[8];
                 tmem_ld8(ta, o);
                 tmem_wait_ld();
@@ -967,7 +978,7 @@ __global__ void __launch_bounds__(384, 1)
               const float y0 = fmaf(__uint_as_float(sr[j][4 * b + 2 * h]), a.scale_log2, -o0);
               const float y1 = fmaf(__uint_as_float(sr[j][4 * b + 2 * h + 1]), a.scale_log2, -o1);
               top = fmaxf(top, fmaxf(y0, y1));
-              float p0 = ex2(y0), p1 = ex2(y1);
+              const float p0 = ex2(y0), p1 = ex2(y1);
               const uint32_t hi = pack_bf16(p0, p1);
               uint8_t* prow = pbuf + row * 128 + 4 * (lane & 3);
               auto put = [&](int part, uint32_t v) {
@@ -975,15 +986,11 @@ __global__ void __launch_bounds__(384, 1)
                 *reinterpret_cast<uint32_t*>(prow + (cc >> 3) * X::CHUNK + (((cc & 7) ^ (row & 7)) << 4)) = v;
               };
               put(0, hi);
-              if constexpr (HL == 1) {                        // the sums take the rounded weights, which the products take
-                p0 = bf16_lo(hi);
-                p1 = bf16_hi(hi);
-              } else {
-                const float u0 = p0 - bf16_lo(hi), u1 = p1 - bf16_hi(hi);
-                const uint32_t lo = pack_bf16(u0, u1);
-                put(1, lo);
-                if constexpr (HL == 3) put(2, pack_bf16(u0 - bf16_lo(lo), u1 - bf16_hi(lo)));
-              }
+              const float u0 = p0 - bf16_lo(hi), u1 = p1 - bf16_hi(hi);
+              const uint32_t lo = pack_bf16(u0, u1);
+              if constexpr (X::FULL) second[(q >> 1) * 2 * MT + jh] = lo;
+              else put(1, lo);
+              if constexpr (HL == 3) put(2, pack_bf16(u0 - bf16_lo(lo), u1 - bf16_hi(lo)));
               t0 += p0;
               t1 += p1;
             }
@@ -998,6 +1005,19 @@ __global__ void __launch_bounds__(384, 1)
         if (gone || !raise) break;
       }
       if (gone) break;
+      if constexpr (X::FULL) {
+        // the buffer is free behind the last tile's products; that they are known to be behind the ones before, see the top
+        if (i > 0) wait(&sh.pempty[(i - 1) & 1], (i - 1) / 2);
+        if (!bad) {
+#pragma unroll
+          for (int e = 0; e < NC * MT; ++e) {
+            const int q = e / (2 * MT), row = r0 + 8 * (e % (2 * MT)), cc = hb / 8 + q;
+            *reinterpret_cast<uint32_t*>(sm + X::L_OFF + row * 128 + 4 * (lane & 3) + ((cc ^ (row & 7)) << 4)) = second[e];
+          }
+        }
+        __syncwarp();
+        fence_proxy_async_smem();
+      }
       const bool ends_here = flags & G_LAST;
       float2 own = make_float2(0.f, 0.f);  // of query row tid, at the segment's end
       int out_row = -1;
@@ -1069,29 +1089,29 @@ __global__ void __launch_bounds__(384, 1)
           const int vt = e0 / cn, cc = cb + e0 - vt * cn;
           const int chn = vt * X::VM + (X::VM == 128 ? 32 * wq + lane : 16 * wq + lane);
           float v[8];
-          uint32_t t[HL][8];
+          uint32_t t[HO][8];
           auto load = [&](int g) {
             __syncwarp();
 #pragma unroll
-            for (int p = 0; p < HL; ++p) tmem_ld8(oa + (g * VT + vt) * N2 + p * R + cc, t[p]);
+            for (int p = 0; p < HO; ++p) tmem_ld8(oa + (g * VT + vt) * N2 + p * R + cc, t[p]);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 8; ++e)
 #pragma unroll
-              for (int p = HL - 2; p >= 0; --p) t[HL - 1][e] = __float_as_uint(__uint_as_float(t[HL - 1][e]) + __uint_as_float(t[p][e]));
+              for (int p = HO - 2; p >= 0; --p) t[HO - 1][e] = __float_as_uint(__uint_as_float(t[HO - 1][e]) + __uint_as_float(t[p][e]));
           };
           load(0);
           if constexpr (PP) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(t[HL - 1][e]) * sh.factor[ob][cc + e].x;
+            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(t[HO - 1][e]) * sh.factor[ob][cc + e].x;
             if (pair) {
               load(NG - 1);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = fmaf(__uint_as_float(t[HL - 1][e]), sh.factor[ob][cc + e].y, v[e]);
+              for (int e = 0; e < 8; ++e) v[e] = fmaf(__uint_as_float(t[HO - 1][e]), sh.factor[ob][cc + e].y, v[e]);
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(t[HL - 1][e]) * sh.factor[ob][cc + e];
+            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(t[HO - 1][e]) * sh.factor[ob][cc + e];
           }
           if (X::VM == 64 && lane >= 16) continue;
           if (!whole) {                    // (rows that no query has are written too)
@@ -1312,26 +1332,29 @@ static RowsVariant make_variant() {
   static_assert(X::Q_OFF % 1024 == 0 && X::V_OFF % 1024 == 0 && X::P_OFF % 1024 == 0 && X::NCOL <= 512, "descriptor alignment, tensor memory");
   return {(const void*)decode_rows_kernel<X>, {(const void*)rows_join_kernel<X, false>, (const void*)rows_join_kernel<X, true>}, smem, X::R, X::DV, {}};
 }
-// bf16 outputs take p in two bf16 parts (16 bits) up to 32 query rows and in one with 64, fp32 outputs in three (all 24
-// bits), with 32 query rows at most: more columns do not fit the tensor memory beside a latent cache's O.
+// bf16 outputs take p in two bf16 parts (16 bits), whatever the number of query rows: with one part (8 bits) in the 64-row variants
+// 8 trees of 512 rows took 369 us and not 388, 32 latent tokens of 128 heads 123 and not 143, but the error of a sequence's
+// output went from 1.7e-3 to 2.3e-3 (relative, 1.7e-3 of it the output's own rounding) and depended on which others were in its batch.
+// fp32 outputs take three parts (all 24 bits), with 32 query rows at most: more columns do not fit the tensor memory beside a
+// latent cache's O.
 static int variant_index(int R, bool f32) { return f32 ? (R == 16 ? 3 : 4) : (R == 16 ? 0 : (R == 32 ? 1 : 2)); }
 static RowsVariant* kv_variant(int d, int R, bool f32) {
   static RowsVariant v[2][5] = {
       {make_variant<RowsCfg<1, 1, 64, false, 16, 2>>(), make_variant<RowsCfg<1, 1, 64, false, 32, 2>>(),
-       make_variant<RowsCfg<1, 1, 64, false, 64, 1>>(), make_variant<RowsCfg<1, 1, 64, false, 16, 3>>(),
+       make_variant<RowsCfg<1, 1, 64, false, 64, 2>>(), make_variant<RowsCfg<1, 1, 64, false, 16, 3>>(),
        make_variant<RowsCfg<1, 1, 64, false, 32, 3>>()},
       {make_variant<RowsCfg<2, 1, 128, false, 16, 2>>(), make_variant<RowsCfg<2, 1, 128, false, 32, 2>>(),
-       make_variant<RowsCfg<2, 1, 128, false, 64, 1>>(), make_variant<RowsCfg<2, 1, 128, false, 16, 3>>(),
+       make_variant<RowsCfg<2, 1, 128, false, 64, 2>>(), make_variant<RowsCfg<2, 1, 128, false, 16, 3>>(),
        make_variant<RowsCfg<2, 1, 128, false, 32, 3>>()}};
   return &v[d == 128][variant_index(R, f32)];
 }
 static RowsVariant* latent_variant(int latent, int R, bool f32) {
   static RowsVariant v[2][5] = {
       {make_variant<RowsCfg<5, 2, 128, true, 16, 2>>(), make_variant<RowsCfg<5, 2, 128, true, 32, 2>>(),
-       make_variant<RowsCfg<5, 2, 128, true, 64, 1>>(), make_variant<RowsCfg<5, 2, 128, true, 16, 3>>(),
+       make_variant<RowsCfg<5, 2, 128, true, 64, 2>>(), make_variant<RowsCfg<5, 2, 128, true, 16, 3>>(),
        make_variant<RowsCfg<5, 2, 128, true, 32, 3>>()},
       {make_variant<RowsCfg<9, 4, 128, true, 16, 2>>(), make_variant<RowsCfg<9, 4, 128, true, 32, 2>>(),
-       make_variant<RowsCfg<9, 4, 128, true, 64, 1>>(), make_variant<RowsCfg<9, 4, 128, true, 16, 3>>(),
+       make_variant<RowsCfg<9, 4, 128, true, 64, 2>>(), make_variant<RowsCfg<9, 4, 128, true, 16, 3>>(),
        make_variant<RowsCfg<9, 4, 128, true, 32, 3>>()}};
   return &v[latent == 512][variant_index(R, f32)];
 }
