@@ -502,7 +502,8 @@ pkv_status pkv_kv_evict(void* k_pool, void* v_pool, const int32_t* block_tables,
  * of its 24 bits in three for an fp32 output, in two for a bf16 output (an error of at most 2^-16 sum p |v|).  Cached rows
  * that no token of the sequence attends to do not
  * reach any output, whatever they hold; a row that some of its tokens attend to and others mask has to
- * hold finite values (0 times an infinity of V is no number).  Weights are held as exp(score - c) with a c that may lie
+ * hold finite values (0 times an infinity of V is no number).  A score of minus infinity has weight zero, and a
+ * token that has no other a zero output row.  Weights are held as exp(score - c) with a c that may lie
  * 2^32 in weight below the largest until the end, so values of V beyond 2^90 may overflow.  Pools, tables, lengths, scale, other
  * errors and the first call of a shape as for pkv_paged_decode_attn; max_blocks * block_size is at most
  * 0x7fff0000 and n_tok * n_h at most 0x7fffffff (PKV_ERANGE).

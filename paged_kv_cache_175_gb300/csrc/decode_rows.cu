@@ -135,6 +135,9 @@ struct RowsMeta {
 // Exponents (base 2) up to this are taken against an offset as it is: p is held in bf16 and fp32, whose range is 2^127, and
 // is as exact at 2^32 as at 1; what an offset this far below the maximum takes from the other end, 2^-94, is nothing.
 constexpr float kRowsLazy = 32.f;
+// The lowest offset, of a query row that has seen no score above it: a number, so that what is subtracted is what a state says,
+// and a row whose scores so far were minus infinities (weight 0) goes on from there.  Any other score against it is raised.
+constexpr float kRowsLowest = -3.402823466e38f;
 // For a softmax group: its first and its last tile of the segment; a segment of one tile.  (F_END: no tile, but the end.)
 enum : int { G_FIRST = 64, G_LAST = 128, G_SOLO = 256 };
 
@@ -752,7 +755,7 @@ __global__ void __launch_bounds__(384, 1)
     const int wg = PP ? gi : 0, tid = (threadIdx.x - 128) & (NW - 1);
     const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
     const int r0 = 16 * MT * wq + (lane >> 2), c0 = hb + 2 * (lane & 3);   // this thread's first cached row and query row
-    float* off = sh.offset[wg];            // offsets of the query rows, minus infinity where there is none yet
+    float* off = sh.offset[wg];            // offsets of the query rows, the lowest where there is none yet
     float l[NC];                           // this thread's rows' share of the sums of its query rows
     bool unset = false;                    // a query row may have no offset yet
     static_assert(NW % R == 0, "a thread's query row in every pass");
@@ -842,7 +845,7 @@ __global__ void __launch_bounds__(384, 1)
             tmem_wait_ld();
             if (lane < 4) {
 #pragma unroll
-              for (int b = 0; b < 2 * CB; ++b) off[c0 + 8 * (ch * CB + (b >> 1)) + (b & 1)] = __uint_as_float(sr[4 * (b >> 1) + (b & 1)]) * a.scale_log2;
+              for (int b = 0; b < 2 * CB; ++b) off[c0 + 8 * (ch * CB + (b >> 1)) + (b & 1)] = fmaxf(__uint_as_float(sr[4 * (b >> 1) + (b & 1)]) * a.scale_log2, kRowsLowest);
             }
             __syncwarp();
           }
@@ -929,8 +932,8 @@ __global__ void __launch_bounds__(384, 1)
           if (sync(false), gone) break;
           if (tid < R) {
             const float mx = fmaxf(fmaxf(scr.red[0][tid], scr.red[1][tid]), fmaxf(scr.red[2][tid], scr.red[3][tid]));
-            const float m = flags & G_FIRST ? -INFINITY : off[tid], mn = fmaxf(m, mx);
-            scr.factor[tid] = m == -INFINITY ? 0.f : ex2(m - mn);
+            const float m = flags & G_FIRST ? kRowsLowest : off[tid], mn = fmaxf(m, mx);
+            scr.factor[tid] = ex2(m - mn);
             off[tid] = mn;
           }
           if (sync(false), gone) break;
@@ -970,13 +973,12 @@ __global__ void __launch_bounds__(384, 1)
           for (int b = 0; b < CB; ++b) {
             const int q = 2 * (ch * CB + b);
             const float2 o = *reinterpret_cast<const float2*>(off + c0 + 4 * q);
-            const float o0 = o.x == -INFINITY ? 0.f : o.x, o1 = o.y == -INFINITY ? 0.f : o.y;
             float t0 = 0.f, t1 = 0.f;
 #pragma unroll
             for (int jh = 0; jh < 2 * MT; ++jh) {
               const int j = jh >> 1, h = jh & 1, row = r0 + 16 * j + 8 * h;
-              const float y0 = fmaf(__uint_as_float(sr[j][4 * b + 2 * h]), a.scale_log2, -o0);
-              const float y1 = fmaf(__uint_as_float(sr[j][4 * b + 2 * h + 1]), a.scale_log2, -o1);
+              const float y0 = fmaf(__uint_as_float(sr[j][4 * b + 2 * h]), a.scale_log2, -o.x);
+              const float y1 = fmaf(__uint_as_float(sr[j][4 * b + 2 * h + 1]), a.scale_log2, -o.y);
               top = fmaxf(top, fmaxf(y0, y1));
               const float p0 = ex2(y0), p1 = ex2(y1);
               const uint32_t hi = pack_bf16(p0, p1);
