@@ -138,6 +138,9 @@ constexpr float kRowsLazy = 32.f;
 // The lowest offset, of a query row that has seen no score above it: a number, so that what is subtracted is what a state says,
 // and a row whose scores so far were minus infinities (weight 0) goes on from there.  Any other score against it is raised.
 constexpr float kRowsLowest = -3.402823466e38f;
+// An exponent is a score times the scale less the offset in one operation, where the offset is such a product rounded: half a step
+// of it stays, which is below 1 up to this size.  A segment with a larger offset rounds its other products likewise.
+constexpr float kRowsFar = 16777216.f;
 // For a softmax group: its first and its last tile of the segment; a segment of one tile.  (F_END: no tile, but the end.)
 enum : int { G_FIRST = 64, G_LAST = 128, G_SOLO = 256 };
 
@@ -758,6 +761,7 @@ __global__ void __launch_bounds__(384, 1)
     float* off = sh.offset[wg];            // offsets of the query rows, the lowest where there is none yet
     float l[NC];                           // this thread's rows' share of the sums of its query rows
     bool unset = false;                    // a query row may have no offset yet
+    bool far = false;                      // a query row's offset is beyond kRowsFar
     static_assert(NW % R == 0, "a thread's query row in every pass");
     const int2 mine = row_in<X>(a, tid % R);
     // Barriers among the threads of a tile.  A failed (timed-out) wait makes `bad` true for its warp, which raises a flag ahead
@@ -833,7 +837,7 @@ __global__ void __launch_bounds__(384, 1)
       // offsets need not be the maxima, only near them.  Where not all query rows attend to that, the maxima are taken first, and
       // so they are behind such tiles, where a query row may still have no offset, up to one whose first row all attend to.
       const bool sure = mt.tile0 < mt.ctx - mt.n && !(mt.invalid & 1);
-      if (flags & G_FIRST) unset = !sure;
+      if (flags & G_FIRST) unset = !sure, far = false;
       bool raise = unset;
       unset = unset && !sure;
       if ((flags & G_FIRST) && sure) {
@@ -845,7 +849,10 @@ __global__ void __launch_bounds__(384, 1)
             tmem_wait_ld();
             if (lane < 4) {
 #pragma unroll
-              for (int b = 0; b < 2 * CB; ++b) off[c0 + 8 * (ch * CB + (b >> 1)) + (b & 1)] = fmaxf(__uint_as_float(sr[4 * (b >> 1) + (b & 1)]) * a.scale_log2, kRowsLowest);
+              for (int b = 0; b < 2 * CB; ++b) {
+                const float x = __uint_as_float(sr[4 * (b >> 1) + (b & 1)]) * a.scale_log2;
+                off[c0 + 8 * (ch * CB + (b >> 1)) + (b & 1)] = fabsf(x) < kRowsFar ? x : kRowsLowest;   // (to be raised)
+              }
             }
             __syncwarp();
           }
@@ -906,6 +913,7 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
       }
       float ts[NC];                        // the tile's part of l
+      float mul = a.scale_log2;            // of the scores as they lie
       uint32_t second[X::FULL ? NC * MT : 1];                 // second parts of p that wait for their buffer
 #pragma unroll 1
       for (;;) {
@@ -921,7 +929,7 @@ __global__ void __launch_bounds__(384, 1)
             for (int b = 0; b < 2 * CB; ++b) {
               float v = -INFINITY;
 #pragma unroll
-              for (int jh = 0; jh < 2 * MT; ++jh) v = fmaxf(v, __uint_as_float(sr[jh >> 1][4 * (b >> 1) + 2 * (jh & 1) + (b & 1)]) * a.scale_log2);
+              for (int jh = 0; jh < 2 * MT; ++jh) v = fmaxf(v, __uint_as_float(sr[jh >> 1][4 * (b >> 1) + 2 * (jh & 1) + (b & 1)]) * mul);
 #pragma unroll
               for (int o = 4; o <= 16; o <<= 1) v = fmaxf(v, __shfl_xor_sync(FULL_MASK, v, o));
               if (lane < 4) scr.red[wq][c0 + 8 * (ch * CB + (b >> 1)) + (b & 1)] = v;
@@ -930,13 +938,16 @@ __global__ void __launch_bounds__(384, 1)
           }
           if (!(flags & G_FIRST)) wait(&sh.pempty[PP ? i & 1 : (i - 1) & 1], PP ? i / 2 - 1 : (i - 1) / 2);   // for the rescale
           if (sync(false), gone) break;
+          bool large = false;
           if (tid < R) {
             const float mx = fmaxf(fmaxf(scr.red[0][tid], scr.red[1][tid]), fmaxf(scr.red[2][tid], scr.red[3][tid]));
             const float m = flags & G_FIRST ? kRowsLowest : off[tid], mn = fmaxf(m, mx);
             scr.factor[tid] = ex2(m - mn);
             off[tid] = mn;
+            large = fabsf(mn) >= kRowsFar && mx > -INFINITY;  // (not the lowest offset, of a row without a score)
           }
-          if (sync(false), gone) break;
+          far |= sync(large);
+          if (gone) break;
           if (!(flags & G_FIRST)) {
             // the sums and O so far, to which the products of the tiles before have been added: scaled in place
 #pragma unroll
@@ -959,6 +970,24 @@ __global__ void __launch_bounds__(384, 1)
             tc_fence_before();
           }
         }
+        if (far && mul != 1.f) {
+          // the products, rounded, in place of the scores
+#pragma unroll 1
+          for (int ch = 0; ch < RC / (8 * CB); ++ch) {
+#pragma unroll 1
+            for (int j = 0; j < MT; ++j) {
+              uint32_t sr[4 * CB];
+              const uint32_t at = st + ((uint32_t)(16 * j) << 16) + ch * 8 * CB;
+              tmem_ld_frag(at, sr);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 4 * CB; ++e) sr[e] = __float_as_uint(__uint_as_float(sr[e]) * mul);
+              tmem_st_frag(at, sr);
+            }
+          }
+          tmem_wait_st();
+          mul = 1.f;
+        }
         // One pass over the tile: weights against the offsets, into P as bf16 parts, and their sums.  Row t of the B operand:
         // 128 bytes per 64 columns (first parts of the query rows, then the next parts), 16-byte chunk c stored at chunk
         // c ^ (t % 8) (128-byte swizzle).
@@ -977,8 +1006,8 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
             for (int jh = 0; jh < 2 * MT; ++jh) {
               const int j = jh >> 1, h = jh & 1, row = r0 + 16 * j + 8 * h;
-              const float y0 = fmaf(__uint_as_float(sr[j][4 * b + 2 * h]), a.scale_log2, -o.x);
-              const float y1 = fmaf(__uint_as_float(sr[j][4 * b + 2 * h + 1]), a.scale_log2, -o.y);
+              const float y0 = fmaf(__uint_as_float(sr[j][4 * b + 2 * h]), mul, -o.x);
+              const float y1 = fmaf(__uint_as_float(sr[j][4 * b + 2 * h + 1]), mul, -o.y);
               top = fmaxf(top, fmaxf(y0, y1));
               const float p0 = ex2(y0), p1 = ex2(y1);
               const uint32_t hi = pack_bf16(p0, p1);
