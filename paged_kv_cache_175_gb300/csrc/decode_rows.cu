@@ -131,6 +131,7 @@ struct RowsMeta {
   int tile0, ctx, n, q0;         // first cached row of the tile; the sequence
   int t0, h0, g;                 // first token of the row tile and its first head of the group; kv head
   int invalid, part;             // blocks of the tile with a bad id; partial state of a cut segment
+  int rows;                      // query rows of the row tile: the first ones
 };
 // Exponents (base 2) up to this are taken against an offset as it is: p is held in bf16 and fp32, whose range is 2^127, and
 // is as exact at 2^32 as at 1; what an offset this far below the maximum takes from the other end, 2^-94, is nothing.
@@ -478,6 +479,7 @@ __global__ void __launch_bounds__(384, 1)
       if (lane == 7) word = h0;
       if (lane == 8) word = c.g;
       if (lane == 10) word = blockIdx.x * 2 + (c.at_start ? 0 : 1);
+      if (lane == 11) word = X::SHARED ? (c.d.n - t0) * a.G - h0 : (a.hc > 1 ? a.G - h0 : min(a.tpt, c.d.n - t0) * a.gt);
       int blk0 = c.t * nbt, wfrom = blk0, win = win_first, win_next = ids_at(c.s, c.d.ctx, blk0 + 32);
       // The segment's query rows.  With one buffer for them they come behind the first tile, which need not wait for the
       // last segment's products.
@@ -840,6 +842,8 @@ __global__ void __launch_bounds__(384, 1)
       if (flags & G_FIRST) unset = !sure, far = false;
       bool raise = unset;
       unset = unset && !sure;
+      // Behind the row tile's own query rows lie other sequences' tokens or other groups' heads, or zeros: their offset is plus
+      // infinity, so that their weights are zeros and no offset is raised for them.
       if ((flags & G_FIRST) && sure) {
         if (wq == 0) {
 #pragma unroll 1
@@ -850,8 +854,9 @@ __global__ void __launch_bounds__(384, 1)
             if (lane < 4) {
 #pragma unroll
               for (int b = 0; b < 2 * CB; ++b) {
+                const int c = c0 + 8 * (ch * CB + (b >> 1)) + (b & 1);
                 const float x = __uint_as_float(sr[4 * (b >> 1) + (b & 1)]) * a.scale_log2;
-                off[c0 + 8 * (ch * CB + (b >> 1)) + (b & 1)] = fabsf(x) < kRowsFar ? x : kRowsLowest;   // (to be raised)
+                off[c] = c >= mt.rows ? INFINITY : (fabsf(x) < kRowsFar ? x : kRowsLowest);   // (the lowest: to be raised)
               }
             }
             __syncwarp();
@@ -941,10 +946,11 @@ __global__ void __launch_bounds__(384, 1)
           bool large = false;
           if (tid < R) {
             const float mx = fmaxf(fmaxf(scr.red[0][tid], scr.red[1][tid]), fmaxf(scr.red[2][tid], scr.red[3][tid]));
-            const float m = flags & G_FIRST ? kRowsLowest : off[tid], mn = fmaxf(m, mx);
-            scr.factor[tid] = ex2(m - mn);
+            const bool here = tid < mt.rows;
+            const float m = flags & G_FIRST ? (here ? kRowsLowest : INFINITY) : off[tid], mn = fmaxf(m, mx);
+            scr.factor[tid] = m == mn ? 1.f : ex2(m - mn);
             off[tid] = mn;
-            large = fabsf(mn) >= kRowsFar && mx > -INFINITY;  // (not the lowest offset, of a row without a score)
+            large = here && fabsf(mn) >= kRowsFar && mx > -INFINITY;   // (not the lowest offset, of a row without a score)
           }
           far |= sync(large);
           if (gone) break;
