@@ -1069,6 +1069,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         if (sync(false), gone) break;
         if (tid < R) own = make_float2(off[tid], (scr.red[0][tid] + scr.red[1][tid]) + (scr.red[2][tid] + scr.red[3][tid]));
+        fence_proxy_async_smem();          // of the scratch, which lies in a slot that a copy fills again
       }
       const int part = mt.part, q0 = mt.q0, n = mt.n, t0 = mt.t0, h0 = mt.h0, g = mt.g;   // (they may be gone behind P)
       __syncwarp();
