@@ -98,6 +98,20 @@ int pkv_bm_add_sequence(pkv_block_manager* bm, int64_t seq_id, const int32_t* to
 int pkv_bm_append_tokens(pkv_block_manager* bm, const int64_t* seq_ids, const int32_t* tokens, int n,
                          int64_t* slots, int* n_done);
 
+/* Drafted tokens: rows for n >= 0 of them behind the sequence's tokens, slots[i] the cache slot of the i-th.
+ * Their blocks are the sequence's alone: no draft enters the tree, since the rows of a tree's branches are not
+ * those of its tokens one after another, and pkv_kv_tree_accept moves rows.  (pkv_bm_append_tokens is not for
+ * drafts: it registers a block as soon as it is full, and another request would reuse rows that were rejected
+ * or moved.)  Until pkv_bm_accept_drafts, pkv_bm_tables counts the drafts in the context length, and the
+ * sequence takes no other call but pkv_bm_release, which gives them up (PKV_EINVAL).  PKV_ENOSPC: no room for all of them. */
+int pkv_bm_append_drafts(pkv_block_manager* bm, int64_t seq_id, int n, int64_t* slots);
+
+/* The accepted path: its n tokens (0 .. the drafts), in the path's order, become the sequence's next ones, blocks that are full
+ * with them enter the tree, and the blocks behind are released.  Call it once pkv_kv_tree_accept has been
+ * launched with the tables and lengths from before it and the same number of tokens, ahead of the manager's next call.  Returns
+ * the number of blocks left. */
+int pkv_bm_accept_drafts(pkv_block_manager* bm, int64_t seq_id, const int32_t* tokens, int n);
+
 /* End a request: its registered blocks stay cached in the tree, the others are freed. */
 int pkv_bm_release(pkv_block_manager* bm, int64_t seq_id);
 
@@ -114,7 +128,7 @@ int pkv_bm_slide_window(pkv_block_manager* bm, int64_t seq_id, int window);
  * context length.  The remaining blocks no longer hold the prompt's tokens in order: they leave
  * the tree, with their subtrees, and none of the sequence's blocks is registered again.
  * Returns the number of blocks left, or PKV_EINVAL (also when a remaining block is shared with
- * another running sequence, or the sequence has slid its window), changing nothing.
+ * another running sequence, the sequence has slid its window, or drafts are open), changing nothing.
  * keep equal to the length changes nothing. */
 int pkv_bm_evict(pkv_block_manager* bm, int64_t seq_id, int keep);
 

@@ -185,7 +185,7 @@ class BlockManager:
         n = len(tokens)
         nb = -(-n // self.bs)
         seq = dict(tokens=tokens, blocks=[], prios=[self._priority(ranges, i) for i in range(nb)],
-                   ranges=list(ranges), chain=ROOT, first=0)
+                   ranges=list(ranges), chain=ROOT, first=0, drafts=0)
         self.seqs[seq_id] = seq
         # longest matching chain of full blocks, leaving at least one token to compute
         matched = []
@@ -238,8 +238,10 @@ class BlockManager:
 
     def append_token(self, seq_id, token):
         """Slot of one new token of a running sequence (a new block when the last is full)."""
-        self.clock += 1
         seq = self.seqs[seq_id]
+        if seq["drafts"]:
+            raise ValueError("drafts that have not been decided on")
+        self.clock += 1
         t = len(seq["tokens"])
         i = t // self.bs
         if t % self.bs == 0:                        # a new block (on failure nothing changes)
@@ -252,6 +254,57 @@ class BlockManager:
         if t % self.bs == self.bs - 1:
             self._register(seq, i, b)
         return b * self.bs + t % self.bs
+
+    def append_drafts(self, seq_ids, counts):
+        """Slots of counts[i] drafted tokens behind each sequence.  Their rows are the sequence's alone: nothing of them enters the
+        tree.  On failure nothing changes but evictions already made."""
+        slots, opened = [], []
+        try:
+            for s, n in zip(seq_ids, counts):
+                slots += self._append_drafts(s, int(n))
+                opened.append(s)
+        except (OutOfBlocks, ValueError, KeyError):
+            self.accept_drafts(opened, [[]] * len(opened))
+            raise
+        return slots
+
+    def _append_drafts(self, seq_id, n):
+        seq = self.seqs[seq_id]
+        if n < 0 or seq["drafts"]:
+            raise ValueError("a negative count, or drafts that have not been decided on")
+        self.clock += 1
+        have, size = len(seq["blocks"]), len(seq["tokens"])
+        try:
+            for i in range(have, -(-(size + n) // self.bs)):
+                b = self._alloc()
+                self.gpu_ref[b] = 1
+                seq["blocks"].append(b)
+                seq["prios"].append(self._priority(seq["ranges"], i))
+        except OutOfBlocks:
+            self._cut(seq, have)
+            raise
+        seq["drafts"] = n
+        return [seq["blocks"][t // self.bs] * self.bs + t % self.bs for t in range(size, size + n)]
+
+    def _cut(self, seq, nb):
+        for b in seq["blocks"][nb:]:
+            self._release_block(b)
+        seq["blocks"], seq["prios"] = seq["blocks"][:nb], seq["prios"][:nb]
+
+    def accept_drafts(self, seq_ids, tokens):
+        """The accepted path's tokens become each sequence's next ones, the other drafts' rows are given back."""
+        for s, toks in zip(seq_ids, tokens):
+            seq = self.seqs[s]
+            if len(toks) > seq["drafts"]:
+                raise ValueError("more tokens than drafts")
+            self.clock += 1
+            for x in toks:
+                seq["tokens"].append(int(x))
+                t = len(seq["tokens"])
+                if t % self.bs == 0:
+                    self._register(seq, t // self.bs - 1, seq["blocks"][t // self.bs - 1])
+            seq["drafts"] = 0
+            self._cut(seq, -(-len(seq["tokens"]) // self.bs))
 
     def _release_block(self, b):
         self.gpu_ref[b] -= 1
@@ -270,8 +323,10 @@ class BlockManager:
 
     def slide_window(self, seq_id, window):
         """Release the blocks that end before the last `window` tokens of the sequence."""
-        self.clock += 1
         seq = self.seqs[seq_id]
+        if seq["drafts"]:
+            raise ValueError("drafts that have not been decided on")
+        self.clock += 1
         n = len(seq["tokens"])
         first = max(0, n - window) // self.bs if window > 0 else 0
         for i in range(seq["first"], first):
@@ -286,8 +341,8 @@ class BlockManager:
         seq = self.seqs[seq_id]
         n = len(seq["tokens"])
         nb = -(-keep // self.bs)
-        if not 1 <= keep <= n or seq["first"] > 0:
-            raise ValueError("keep out of range, or the window has slid")
+        if not 1 <= keep <= n or seq["first"] > 0 or seq["drafts"]:
+            raise ValueError("keep out of range, or the window has slid, or drafts are open")
         if keep == n:
             return nb
         if any(self.gpu_ref[b] > 1 for b in seq["blocks"][:nb]):
@@ -304,7 +359,7 @@ class BlockManager:
 
     def table(self, seq_id):
         seq = self.seqs[seq_id]
-        return list(seq["blocks"]), len(seq["tokens"])
+        return list(seq["blocks"]), len(seq["tokens"]) + seq["drafts"]
 
     def take_copies(self):
         c, self.copies = self.copies, []

@@ -86,6 +86,8 @@ _SIGS = {
     "pkv_bm_destroy": (None, [_P]),
     "pkv_bm_add_sequence": (_I, [_P, ctypes.c_int64, _P, _I, _P, _I, _P, _I]),
     "pkv_bm_append_tokens": (_I, [_P, _P, _P, _I, _P, _P]),
+    "pkv_bm_append_drafts": (_I, [_P, ctypes.c_int64, _I, _P]),
+    "pkv_bm_accept_drafts": (_I, [_P, ctypes.c_int64, _P, _I]),
     "pkv_bm_release": (_I, [_P, ctypes.c_int64]),
     "pkv_bm_slide_window": (_I, [_P, ctypes.c_int64, _I]),
     "pkv_bm_evict": (_I, [_P, ctypes.c_int64, _I]),
@@ -1002,6 +1004,39 @@ class BlockManager:
             msg = lib().pkv_status_str(r).decode()
             raise PkvError(f"bm_append_tokens: {msg} after {done.value} of {len(ids)} sequences")
         return slots
+
+    def append_drafts(self, seq_ids, counts):
+        """Rows for counts[i] drafted tokens behind each sequence: their cache slots (int64, one sequence after another).
+        No draft is reused by another request; until accept_drafts, tables() counts them in the context lengths and
+        the sequences take no other call but release.  All sequences get their rows, or none."""
+        np = self._np
+        ids, counts = [int(s) for s in seq_ids], [int(n) for n in counts]
+        if len(ids) != len(counts) or any(not 0 <= n <= 0x7fffffff for n in counts):
+            raise PkvError("append_drafts: a number of drafts for each sequence")
+        if any(n > self.num_blocks * self.block_size for n in counts):
+            raise PkvError("append_drafts: more drafts than rows")
+        slots, at = np.empty(sum(counts), dtype=np.int64), 0
+        for i, (s, n) in enumerate(zip(ids, counts)):
+            r = lib().pkv_bm_append_drafts(self._h, s, n, slots[at:].ctypes.data)
+            if r < 0:
+                for back in ids[:i]:
+                    lib().pkv_bm_accept_drafts(self._h, back, None, 0)
+                _check(f"bm_append_drafts of sequence {s}", r)
+            at += n
+        return slots
+
+    def accept_drafts(self, seq_ids, tokens):
+        """tokens[i], the accepted path's in its order, become the next ones of sequence i; the other drafts' rows are given
+        back.  After kv_tree_accept has been launched with the tables and lengths from before, ahead of the manager's next call.
+        Stops at the first sequence that refuses (more tokens than drafts, or unknown)."""
+        np = self._np
+        ids, tokens = [int(s) for s in seq_ids], [self._a(t, np.int32) for t in tokens]
+        if len(ids) != len(tokens) or len(set(ids)) != len(ids):
+            raise PkvError("accept_drafts: distinct sequences with a list of tokens each")
+        for s, t in zip(ids, tokens):
+            r = lib().pkv_bm_accept_drafts(self._h, s, t.ctypes.data, len(t))
+            if r < 0:
+                _check(f"bm_accept_drafts of sequence {s}", r)
 
     def release(self, seq_id):
         _check("bm_release", lib().pkv_bm_release(self._h, int(seq_id)))

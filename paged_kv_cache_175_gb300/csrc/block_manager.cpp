@@ -61,6 +61,7 @@ struct Seq {
   std::vector<pkv_token_range> ranges;
   ChainRef chain;
   int first = 0;                   // first block still held (after window slides)
+  int drafts = 0;                  // drafted tokens behind `tokens`, of which no path has been accepted yet
 };
 
 }  // namespace
@@ -356,6 +357,48 @@ struct pkv_block_manager {
     *slot = (int64_t)b * bs + t % bs;
     return PKV_OK;
   }
+
+  // Release a sequence's blocks from the nb-th on.
+  void cut(Seq& s, int nb) {
+    for (size_t i = (size_t)nb; i < s.blocks.size(); ++i) release_block(s.blocks[i]);
+    s.blocks.resize(nb);
+    s.prios.resize(nb);
+  }
+
+  int append_drafts(Seq& s, int n, int64_t* slots) {
+    const int size = (int)s.tokens.size(), have = (int)s.blocks.size(), nb = (int)(((int64_t)size + n + bs - 1) / bs);
+    if (nb - have > N) return PKV_ENOSPC;
+    s.blocks.reserve(nb);                      // (nothing below throws with blocks half taken)
+    s.prios.reserve(nb);
+    ++clock;
+    for (int i = have; i < nb; ++i) {
+      const int b = alloc();
+      if (b < 0) {
+        cut(s, have);
+        return PKV_ENOSPC;
+      }
+      take_gpu(b);
+      gpu_ref[b] = 1;
+      s.blocks.push_back(b);
+      s.prios.push_back(priority(s.ranges, i));
+    }
+    s.drafts = n;
+    for (int t = size; t < size + n; ++t) slots[t - size] = (int64_t)s.blocks[t / bs] * bs + t % bs;
+    return PKV_OK;
+  }
+
+  int accept_drafts(Seq& s, const int32_t* tokens, int n) {
+    s.tokens.reserve(s.tokens.size() + n);
+    ++clock;
+    for (int i = 0; i < n; ++i) {
+      s.tokens.push_back(tokens[i]);
+      const int t = (int)s.tokens.size();
+      if (t % bs == 0) register_block(s, t / bs - 1, s.blocks[t / bs - 1]);
+    }
+    s.drafts = 0;
+    cut(s, (int)((s.tokens.size() + bs - 1) / bs));
+    return (int)s.blocks.size();
+  }
 };
 
 extern "C" {
@@ -405,7 +448,7 @@ int pkv_bm_append_tokens(pkv_block_manager* bm, const int64_t* seq_ids, const in
   if (!bm || n < 0 || (n && (!seq_ids || !tokens || !slots))) return PKV_EINVAL;
   for (int i = 0; i < n; ++i) {
     auto it = bm->seqs.find(seq_ids[i]);
-    if (it == bm->seqs.end()) return PKV_EINVAL;
+    if (it == bm->seqs.end() || it->second.drafts) return PKV_EINVAL;
     int st;
     try {
       st = bm->append_token(it->second, tokens[i], &slots[i]);
@@ -416,6 +459,29 @@ int pkv_bm_append_tokens(pkv_block_manager* bm, const int64_t* seq_ids, const in
     if (n_done) *n_done = i + 1;
   }
   return PKV_OK;
+}
+
+int pkv_bm_append_drafts(pkv_block_manager* bm, int64_t seq_id, int n, int64_t* slots) {
+  if (!bm || n < 0 || (n && !slots)) return PKV_EINVAL;
+  auto it = bm->seqs.find(seq_id);
+  if (it == bm->seqs.end() || it->second.drafts) return PKV_EINVAL;
+  if ((int64_t)it->second.tokens.size() + n > INT32_MAX) return PKV_EINVAL;
+  try {
+    return bm->append_drafts(it->second, n, slots);
+  } catch (...) {
+    return PKV_ENOSPC;
+  }
+}
+
+int pkv_bm_accept_drafts(pkv_block_manager* bm, int64_t seq_id, const int32_t* tokens, int n) {
+  if (!bm || n < 0 || (n && !tokens)) return PKV_EINVAL;
+  auto it = bm->seqs.find(seq_id);
+  if (it == bm->seqs.end() || n > it->second.drafts) return PKV_EINVAL;
+  try {
+    return bm->accept_drafts(it->second, tokens, n);
+  } catch (...) {
+    return PKV_ENOSPC;
+  }
 }
 
 int pkv_bm_release(pkv_block_manager* bm, int64_t seq_id) {
@@ -431,7 +497,7 @@ int pkv_bm_release(pkv_block_manager* bm, int64_t seq_id) {
 int pkv_bm_slide_window(pkv_block_manager* bm, int64_t seq_id, int window) {
   if (!bm || window < 1) return PKV_EINVAL;
   auto it = bm->seqs.find(seq_id);
-  if (it == bm->seqs.end()) return PKV_EINVAL;
+  if (it == bm->seqs.end() || it->second.drafts) return PKV_EINVAL;
   ++bm->clock;
   Seq& s = it->second;
   const int n = (int)s.tokens.size();
@@ -447,7 +513,7 @@ int pkv_bm_evict(pkv_block_manager* bm, int64_t seq_id, int keep) {
   if (it == bm->seqs.end()) return PKV_EINVAL;
   Seq& s = it->second;
   const int n = (int)s.tokens.size();
-  if (keep > n || s.first > 0) return PKV_EINVAL;
+  if (keep > n || s.first > 0 || s.drafts) return PKV_EINVAL;
   const int nb = (int)(((int64_t)keep + bm->bs - 1) / bm->bs);
   if (keep == n) return nb;
   for (int i = 0; i < nb; ++i)
@@ -480,7 +546,7 @@ int pkv_bm_tables(pkv_block_manager* bm, const int64_t* seq_ids, int n, int32_t*
     int32_t* row = tables + (size_t)r * max_blocks;
     for (int i = 0; i < max_blocks; ++i)
       row[i] = (i >= s.first && i < (int)s.blocks.size()) ? s.blocks[i] : -1;
-    context_lens[r] = (int32_t)s.tokens.size();
+    context_lens[r] = (int32_t)s.tokens.size() + s.drafts;
   }
   return PKV_OK;
 }
