@@ -495,7 +495,7 @@ pkv_status pkv_kv_evict(void* k_pool, void* v_pool, const int32_t* block_tables,
  *   q             bf16 [n_tok][n_h][head_dim]
  *   q_start       int32 [batch + 1] or NULL
  *   tree_mask     int64 [n_tok][mask_words] or NULL (mask_words is ignored then)
- *   out           [n_tok][n_h][head_dim]; must not overlap the other arguments
+ *   out           [n_tok][n_h][head_dim]; neither it nor the workspace may overlap the other arguments (PKV_EINVAL)
  *   workspace     pkv_tree_workspace_bytes bytes (0: invalid shape), 256-byte aligned; a call of other
  *                 n_tok or batch may need another size
  * Softmax and sums are fp32 and taken in a fixed order (the same bits on every call).  p is carried in bf16 parts: all

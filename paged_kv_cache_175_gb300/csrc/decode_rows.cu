@@ -1479,6 +1479,17 @@ static pkv_status rows_attn(const RowsShape& s, RowsVariant* v, bool latent, con
   if ((long long)max_blocks * block_size > kRowsMaxCtx || (long long)n_tok * n_h > 0x7fffffffLL) return PKV_ERANGE;
   const RowsLayout lay = rows_layout(s, v->DV);
   if (ws_bytes < lay.total) return PKV_ENOSPC;
+  {
+    // the output and the workspace are written while the rest is still read
+    const size_t out_bytes = (size_t)n_tok * n_h * v->DV * (out_dtype == PKV_OUT_F32 ? 4 : 2);
+    const size_t own = lay.total > 256 ? lay.total : 256, pool = (size_t)num_blocks * n_kv * block_size * w * 2;
+    const struct { const void* at; size_t bytes; } read[] = {
+        {q, (size_t)n_tok * n_h * w * 2}, {k, pool}, {vp, latent ? 0 : pool}, {bt, (size_t)batch * max_blocks * 4}, {ctx, (size_t)batch * 4},
+        {q_start, ((size_t)batch + 1) * 4}, {mask, (size_t)n_tok * mask_words * 8}, {err, 4}};
+    for (const auto& r : read)
+      if (r.bytes && (overlaps(out, out_bytes, r.at, r.bytes) || overlaps(ws, own, r.at, r.bytes))) return PKV_EINVAL;
+    if (overlaps(out, out_bytes, ws, own)) return PKV_EINVAL;
+  }
   if (s.P < 1 || !rows_ready(v)) {
     record_cuda_error(cudaGetLastError());
     return PKV_ECUDA;

@@ -29,4 +29,10 @@ __device__ __forceinline__ Drafts drafts_of(const int32_t* ctx, const int32_t* q
   return d;
 }
 
+// Whether two ranges of bytes share any (null: an argument that is not given).
+inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
 }  // namespace pkv

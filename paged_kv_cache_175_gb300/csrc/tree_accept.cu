@@ -99,10 +99,6 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __gri
 
 using namespace pkv;
 
-static bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + nb && y < x + na;
-}
 // Whether two of n caches of `bytes` each share memory (one given twice, say, whose rows would move twice).
 static bool any_overlap(void* const* caches, int n, uint64_t bytes) noexcept {
   try {
