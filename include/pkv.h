@@ -530,7 +530,7 @@ pkv_status pkv_paged_tree_attn(const void* q, const void* k_pool, const void* v_
  *   new_lens      int32 [batch]: base + n_accept[s]; must not overlap context_lens, n_accept, path or q_start
  * An entry that is not larger than the one before it, or not below n, ends the path there, with
  * PKV_DEV_BAD_TREE (so does n_accept out of range, which is clamped); a sequence with more drafted tokens than
- * rows keeps its length, with the same flag.  The blocks that hold the drafted rows must belong to the sequence alone, and
+ * rows keeps its length, with the same flag (but for a padded one: length 0 and n_accept 0).  The blocks that hold the drafted rows must belong to the sequence alone, and
  * stay so until the path is decided on: pkv_bm_append_drafts and pkv_bm_accept_drafts of pkv_bm.h see to it.  A
  * move from or to a block id outside the pool sets PKV_DEV_BAD_BLOCK and is skipped.
  */

@@ -919,7 +919,8 @@ def kv_tree_accept(caches, block_tables, context_lens, q_start, path, n_accept, 
     """Keep the accepted path of each sequence's drafted tokens, in every cache of the list (the K and V pools of all
     layers, or their latent caches; one shape): row base + path[s][i] becomes row base + i for i < n_accept[s], base
     being the rows in front of the drafted ones.  path (int32 [B][P]) ascends.  q_start as for the attention (None:
-    n_tok / B tokens each).  Returns the new context lengths, base + n_accept (a tensor of its own)."""
+    n_tok / B tokens each); n_tok, which may be left out beside it, is what its entries must not exceed.  Returns the new
+    context lengths, base + n_accept (a tensor of its own)."""
     caches = list(caches)
     if new_lens is None:
         new_lens = _empty(context_lens.shape, _i32, context_lens.device, stream)

@@ -47,8 +47,9 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __gri
   int count = a.n_accept[s];
   const Drafts d = drafts_of(a.ctx, a.q_start, a.n_each, a.n_tok, a.max_ctx, s, flags);
   const int base = d.ctx - d.n, most = min(d.n, a.path_stride);
+  if (base < 0 && count != 0) flags |= PKV_DEV_BAD_TREE;      // (drafted tokens of a padded sequence, of length 0, are none's)
   if (count < 0 || count > most) {
-    if (d.ctx > 0) flags |= PKV_DEV_BAD_TREE;
+    flags |= PKV_DEV_BAD_TREE;
     count = count < 0 ? 0 : most;
   }
   if (base < 0) count = 0;
