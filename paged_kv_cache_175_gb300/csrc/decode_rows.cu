@@ -846,6 +846,7 @@ __global__ void __launch_bounds__(384, 1)
       // infinity, so that their weights are zeros and no offset is raised for them.
       if ((flags & G_FIRST) && sure) {
         if (wq == 0) {
+          const int rows = mt.rows;
 #pragma unroll 1
           for (int ch = 0; ch < RC / (8 * CB); ++ch) {
             uint32_t sr[4 * CB];
@@ -856,7 +857,7 @@ __global__ void __launch_bounds__(384, 1)
               for (int b = 0; b < 2 * CB; ++b) {
                 const int c = c0 + 8 * (ch * CB + (b >> 1)) + (b & 1);
                 const float x = __uint_as_float(sr[4 * (b >> 1) + (b & 1)]) * a.scale_log2;
-                off[c] = c >= mt.rows ? INFINITY : (fabsf(x) < kRowsFar ? x : kRowsLowest);   // (the lowest: to be raised)
+                off[c] = (fabsf(x) < kRowsFar ? x : kRowsLowest) + (c < rows ? 0.f : INFINITY);   // (the lowest: to be raised)
               }
             }
             __syncwarp();
