@@ -504,7 +504,7 @@ pkv_status pkv_kv_evict(void* k_pool, void* v_pool, const int32_t* block_tables,
  * reach any output, whatever they hold; a row that some of its tokens attend to and others mask has to
  * hold finite values (0 times an infinity of V is no number).  A score of minus infinity has weight zero, and a
  * token that has no other a zero output row.  Weights are held as exp(score - c) with a c that may lie
- * 2^32 in weight below the largest until the end, so values of V beyond 2^90 may overflow.  Pools, tables, lengths, scale, other
+ * 2^32 in weight below the largest until the end, so values of V beyond 2^95 / context_lens[s] may overflow.  Pools, tables, lengths, scale, other
  * errors and the first call of a shape as for pkv_paged_decode_attn; max_blocks * block_size is at most
  * 0x7fff0000 and n_tok * n_h at most 0x7fffffff (PKV_ERANGE).
  */
@@ -556,7 +556,8 @@ pkv_status pkv_kv_tree_accept(void* const* caches, int n_caches, int row_bytes, 
  *                 rope], say); may be q itself, with its strides
  *   cache         written at slot_mapping (int64 [n_tok]; negative: padding, nothing of the token is written;
  *                 the others must be distinct)
- * Strides are multiples of 8 elements, pointers 16-byte aligned.  A slot >= num_blocks * block_size sets
+ * Strides are multiples of 8 elements, a token's heads lie within its stride (q_stride >= (n_h - 1) * q_head_stride + rope),
+ * pointers are 16-byte aligned; but for q_out = q, what is written must not overlap what is read.  A slot >= num_blocks * block_size sets
  * PKV_DEV_BAD_SLOT and skips the token.  n_h is at most 1024.
  */
 pkv_status pkv_latent_append(const void* kv, int64_t kv_stride, const void* q, int64_t q_stride, int64_t q_head_stride,

@@ -25,18 +25,19 @@
 //               with an O accumulator of its own; latent cache: both take every tile, half of the query rows each
 //
 // What bounds it (GPU time; R query rows per CTA):
-//   64 trees of up to 16 tokens over 0.5-4K rows, 8 kv heads of 4 x 128 (620 MB): 106 us, 5.8 TB/s: HBM, then the segments' ends.  The
+//   64 trees of up to 16 tokens over 0.5-4K rows, 8 kv heads of 4 x 128 (620 MB): 110 us, 5.6 TB/s: HBM, then the segments' ends.  The
 //     same of up to 8 tokens: 101 us.
-//   8 trees of up to 64 over 8-32K, 8 x 8 heads (512 rows, 207 GFLOP): 369 us, 558 TFLOP/s: shared memory and HBM.  A tile of 128
-//     rows writes 64 KB to shared memory and its products read 96, about 1600 of the 1700 clocks that it takes; HBM is 72% busy, since
-//     the caches are read 3.2 times over.  (128 query rows per CTA, which read less, took 489 us where 64 took 398: they leave two S
-//     buffers and three key stages.)
+//   8 trees of up to 64 over 8-32K, 8 x 8 heads (512 rows, 207 GFLOP): 390 us, 530 TFLOP/s: shared memory and HBM.  A tile of 128
+//     rows takes 96 KB written to shared memory (P among them) and 112 read by its products, 1625 clocks at 128 bytes each, of the 2200 that
+//     there are for each tile of a CTA; HBM is 70% busy, since the caches are read 3.2 times over.  (128 query rows per CTA, with one
+//     part of p, took 489 us where 64 took 398: they leave two S buffers and three key stages.)
 //   64 x 0.5-4K latent tokens of 16 heads (173 MB): 41 us, 4.2 TB/s: HBM for 28 of them, then setup, first loads and the join.
-//   32 x 2-16K latent tokens of 128 heads (82 GFLOP): 123 us, 662 TFLOP/s: shared memory again, 72 KB written and 245
-//     read per tile of 64 rows.
-//   300 trees of up to 4 over 1-300 rows (2400 segments): 73 us: the ends of 16 segments per CTA, about 8000 clocks each: masks, softmax,
+//   32 x 2-16K latent tokens of 128 heads (82 GFLOP): 144 us, 567 TFLOP/s: shared memory for three quarters of it, 88 KB written and
+//     341 read per tile of 64 rows, 3430 of the 4640 clocks that there are for each tile of a CTA.  What the others go to was not measured; the
+//     products, the softmax and the copies of a tile wait on one another.
+//   300 trees of up to 4 over 1-300 rows (2400 segments): 77 us: the ends of 16 segments per CTA, about 8000 clocks each: masks, softmax,
 //     second product and epilogue, in series.
-//   One tree of 8 over 333 rows: 10.9 us; one latent token of 16 heads over 301: 12.5: setup 1.5 us, loads 2, masks and softmax 2,
+//   One tree of 8 over 333 rows: 10.8 us; one latent token of 16 heads over 301: 11.7: setup 1.5 us, loads 2, masks and softmax 2,
 //     epilogue 1, the join 2, and code that is run once and cold.
 #include <cmath>
 #include <mutex>
@@ -1400,10 +1401,10 @@ static RowsVariant* latent_variant(int latent, int R, bool f32) {
 
 // Query rows of a row tile, and members of a team, from the average of the sequences' query rows per kv head.  Rows that no
 // query has cost products and softmax all the same, row tiles loads: 64 trees of 16 rows took 99 us with R = 16, 102
-// with 32 and 105 with 64, of 32 rows 102 with 32 and 106 with 64, of 64 rows 108 with 64 and 154 with 32; 64 latent tokens of 16
-// heads 41, 42 and 49 with 16, 32 and 64.  Two members read what one CTA loads twice (32 latent tokens of 128 heads 124 us and
-// 134, 8 trees of 512 rows 369 and 392), but where the sequences' rows differ one of them may have no tile (12 trees over the latent
-// cache 48 and 48; with four members 58, and 379 for the 8 trees).
+// with 32 and 109 with 64, of 32 rows 102 with 32 and 109 with 64, of 64 rows 111 with 64 and 153 with 32; 64 latent tokens of 16
+// heads 41, 43 and 54 with 16, 32 and 64.  Two members read what one CTA loads twice (32 latent tokens of 128 heads 144 us and
+// 151, 8 trees of 512 rows 390 and 404), but where the sequences' rows differ one of them may have no tile (12 trees over the latent
+// cache 54 and 53; with four members 66, and 412 for the 8 trees).
 struct RowsShape {
   int R, C, P;
   long long groups;              // of row tiles, on average
@@ -1533,7 +1534,7 @@ static pkv_status rows_attn(const RowsShape& s, RowsVariant* v, bool latent, con
   cudaError_t e = launch_pdl(v->fn, dim3(s.P * s.C), dim3(384), v->smem, st, kargs);
   if (e == cudaSuccess) {
     // The pieces over the segments: about the parts that each has, if it has so many tiles.  16 heads over 64K latent tokens:
-    // 64 us by a warp per query row, 30 by a CTA; 64 trees of 64 rows: 106 and 150.
+    // 65 us by a warp per query row, 30 by a CTA; 64 trees of 64 rows: 111 and 156.
     const long long segments = (long long)batch * n_kv * s.groups, tiles = a.max_ctx / (latent ? 64 : 128);
     const bool wide = s.P >= 8 * segments && tiles >= 8 && s.P <= 256;
     void* jargs[] = {&a};
