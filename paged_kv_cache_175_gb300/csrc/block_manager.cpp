@@ -368,19 +368,24 @@ struct pkv_block_manager {
   int append_drafts(Seq& s, int n, int64_t* slots) {
     const int size = (int)s.tokens.size(), have = (int)s.blocks.size(), nb = (int)(((int64_t)size + n + bs - 1) / bs);
     if (nb - have > N) return PKV_ENOSPC;
-    s.blocks.reserve(nb);                      // (nothing below throws with blocks half taken)
+    s.blocks.reserve(nb);                      // (a block that is taken has its entry)
     s.prios.reserve(nb);
     ++clock;
-    for (int i = have; i < nb; ++i) {
-      const int b = alloc();
-      if (b < 0) {
-        cut(s, have);
-        return PKV_ENOSPC;
+    try {
+      for (int i = have; i < nb; ++i) {
+        const int b = alloc();
+        if (b < 0) {
+          cut(s, have);
+          return PKV_ENOSPC;
+        }
+        take_gpu(b);
+        gpu_ref[b] = 1;
+        s.blocks.push_back(b);
+        s.prios.push_back(priority(s.ranges, i));
       }
-      take_gpu(b);
-      gpu_ref[b] = 1;
-      s.blocks.push_back(b);
-      s.prios.push_back(priority(s.ranges, i));
+    } catch (...) {                            // out of host memory while making room
+      cut(s, have);
+      throw;
     }
     s.drafts = n;
     for (int t = size; t < size + n; ++t) slots[t - size] = (int64_t)s.blocks[t / bs] * bs + t % bs;
@@ -393,7 +398,11 @@ struct pkv_block_manager {
     for (int i = 0; i < n; ++i) {
       s.tokens.push_back(tokens[i]);
       const int t = (int)s.tokens.size();
-      if (t % bs == 0) register_block(s, t / bs - 1, s.blocks[t / bs - 1]);
+      try {
+        if (t % bs == 0) register_block(s, t / bs - 1, s.blocks[t / bs - 1]);
+      } catch (...) {                          // out of host memory: the block and the later ones stay private
+        s.chain.broken = true;
+      }
     }
     s.drafts = 0;
     cut(s, (int)((s.tokens.size() + bs - 1) / bs));
